@@ -318,6 +318,125 @@ msk_status msk_attention_noalloc(const void* q, const void* kv_layer, int32_t to
                                  int32_t n_kv_heads, int32_t head_dim, int32_t max_seq, int32_t pos0,
                                  int32_t window, void* out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the step, each a call of its own on the caller's buffers:
+ * a KV cache held in 4 bits, products with 4-bit weights, and the log
+ * probabilities that accept or reject the verified tokens.  The pages
+ * describe none of them; they serve the same batch-one verify pass.
+ *
+ * They differ from the step's calls in three ways: they take no model, they
+ * ENQUEUE their work on `stream` and return without waiting for it (no wait
+ * in them can run out, so there is no error word to read), and they may be
+ * captured into a CUDA graph.  They keep nothing between calls.  Where a call
+ * takes a workspace, the caller owns it: calls that may overlap on the GPU
+ * (two streams, two graphs) need one each.  Its contents are of no meaning
+ * before or after a call.
+ * The device must be the current one of the calling thread. */
+typedef enum { MSK_BF16 = 0, MSK_FP16 = 1, MSK_FP32 = 2 } msk_dtype;
+
+/* One layer's KV cache in the step's order, NVFP4:
+ *   codes : [2 (K, V)][n_kv_heads][max_seq][head_dim / 2] E2M1 codes, element
+ *           2i in the low nibble of byte i;
+ *   scales: [2][n_kv_heads][max_seq][head_dim / 16] E4M3 block scales.
+ * Value = e2m1 * e4m3 * k_scale (keys) or v_scale (values); both positive.
+ * Both pointers 16-byte aligned; head_dim 64 or 128. */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  int32_t n_kv_heads, head_dim, max_seq;
+  float k_scale, v_scale;
+} msk_kv4_desc;
+
+/* Quantises `tokens` rows of K and V into cache rows pos0 .. pos0 + tokens - 1.
+ *   k, v: element (t, h, i) at t * token_stride + h * head_stride + i, of type
+ *         dtype (any of the three): rows of a QKV projection and layers of the
+ *         bf16 cache alike.  Rows and strides are multiples of 16 bytes.
+ *   pos0_dev: NULL, or a DEVICE int32 that is read instead of pos0 when the
+ *         kernel runs (for graphs); clamped to [0, max_seq - tokens].
+ * The activation quantiser of the step (see msk_debug_quantize) on
+ * fp32(x / k_scale): block scale E4M3_RN(amax / 6), codes E2M1_RN(x / scale).
+ * A value beyond 2688 * k_scale saturates; an infinity counts as such a
+ * value; a NaN does not count for its block's scale and is stored as 6 times
+ * it.  tokens == 0 does nothing. */
+msk_status msk_kv4_write(const msk_kv4_desc* cache, const void* k, const void* v, int32_t dtype, int32_t tokens,
+                         int64_t token_stride, int64_t head_stride, int32_t pos0, const int32_t* pos0_dev,
+                         void* stream);
+
+/* The reverse: rows pos0 .. pos0 + tokens - 1 of the cache as values of type
+ * dtype (exact in bf16 and fp16 where the tensor's scale is 1, else rounded
+ * once), to k and v laid out as above. */
+msk_status msk_kv4_read(const msk_kv4_desc* cache, int32_t pos0, int32_t tokens, void* k, void* v, int32_t dtype,
+                        int64_t token_stride, int64_t head_stride, void* stream);
+
+/* GQA attention of `tokens` (1..16) queries over a 4-bit cache: what
+ * msk_attention_noalloc computes, and its tree form.
+ *   q      : element (t, h, i) at t * q_stride + h * head_dim + i, bf16 or
+ *            fp16, after RoPE; q_stride a multiple of 8, 16-byte aligned;
+ *   out    : [tokens][n_q_heads * head_dim], the type of q, 16-byte aligned;
+ *   cache_len: S, cached rows; the tokens' own K/V sit at rows S + t, written
+ *            before; S + tokens <= max_seq;
+ *   cache_len_dev: NULL, or a DEVICE int32 that is read instead of cache_len
+ *            when the kernels run (for graphs); clamped to
+ *            [0, max_seq - tokens];
+ *   parents: HOST [tokens] as in msk_decode_step_tree, or NULL for the chain
+ *            (read during the call, so a graph keeps the tree it was captured
+ *            with);
+ *   window : 0 for global attention, else keys [p - window + 1, p];
+ *   softmax_scale: factor of the scores, 0 for 1 / sqrt(head_dim).
+ * n_q_heads a multiple of cache->n_kv_heads, any quotient.  Cache rows that no
+ * query sees are not read, or do not count whatever they hold.
+ * Queries and softmax weights enter the products in fp16 (queries after an
+ * exact scaling of each row by a power of two), keys and values without
+ * rounding, sums are fp32.
+ * workspace: msk_attention_kv4_workspace bytes, 16-byte aligned. */
+size_t msk_attention_kv4_workspace(int32_t tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
+msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_stride, const msk_kv4_desc* cache,
+                             int32_t tokens, int32_t n_q_heads, int32_t cache_len, const int32_t* cache_len_dev,
+                             const int32_t* parents, int32_t window, float softmax_scale, void* out,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* y[t][n] = sum_k x[t][k] w[n][k] for `tokens` (1..16) rows: a projection or
+ * vocabulary head whose weights are NVFP4 and whose activations are not
+ * quantised.
+ *   x: [tokens][cols], bf16 or fp16, x_stride elements between rows (a
+ *      multiple of 8), 16-byte aligned;
+ *   w: rows arbitrary, cols a multiple of 128 up to 32768, codes and scales
+ *      16-byte aligned, read where they are (no repacking);
+ *   y: [tokens][rows] of y_dtype (bf16, fp16 or fp32), y_stride elements
+ *      between rows, aligned to its element.
+ * Weights enter without rounding (the products e2m1 * e4m3), x in fp16 after an
+ * exact scaling by powers of two, sums are fp32.  A NaN block scale makes the
+ * outputs of its row NaN.  tokens == 0 or rows == 0 does nothing.
+ * workspace: msk_linear_fp4_workspace bytes (may be 0), 16-byte aligned. */
+size_t msk_linear_fp4_workspace(int32_t tokens, int64_t rows, int64_t cols);
+msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_stride, const msk_nvfp4_desc* w, int32_t tokens,
+                          void* y, int32_t y_dtype, int64_t y_stride, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* Log probabilities under softmax(logits / temperature), one pass per row:
+ *   logits : [rows][vocab] of dtype (any of the three), ld elements between
+ *            rows (>= vocab, no alignment asked beyond the element's);
+ *   tokens : int32 [rows] given tokens, or NULL (then logprob and rank are
+ *            NULL too).  A token outside [0, vocab) marks a padded row: its
+ *            logprob is 0 and its rank -1;
+ *   temperature: > 0;
+ *   logprob: fp32 [rows], log softmax at the given token;
+ *   rank   : int32 [rows], how many logits are greater than the given one;
+ *   entropy: fp32 [rows], in nats;
+ *   top    : 0..32 alternatives (at most vocab): top_ids int32 [rows][top] and
+ *            top_logprobs fp32 [rows][top], greatest first, of equal logits
+ *            the lowest index first.
+ * Any output may be NULL.  Logits of -inf are barred tokens (probability 0).
+ * A row with a NaN or +inf, or with nothing but -inf, has no distribution: its
+ * logprob, entropy and top_logprobs are NaN, its ids in range.
+ * rows == 0 does nothing.
+ * workspace: msk_token_logprobs_workspace bytes (may be 0), 16-byte aligned. */
+size_t msk_token_logprobs_workspace(int64_t rows, int64_t vocab, int32_t top);
+msk_status msk_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                              const int32_t* tokens, float temperature, int32_t top, float* logprob, int32_t* rank,
+                              float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Number of SMs (= CTAs per launch) the model uses, and bytes of device
  * memory it owns. */
 msk_status msk_get_info(msk_model* m, int32_t* n_ctas, int64_t* device_bytes);

@@ -6,12 +6,16 @@ is no CPU fallback: if the compiled library is missing, every call raises.
 
 The entry points carry the C names (``msk_create``, ``msk_load_layer``,
 ``msk_layer_step``, ``msk_decode_step``, ...); :class:`Model` bundles them for
-weights held in torch tensors.
+weights held in torch tensors.  The operators beside the step
+(``msk_kv4_write``, ``msk_kv4_read``, ``msk_attention_kv4``, ``msk_linear_fp4``,
+``msk_token_logprobs``) take torch tensors, with :class:`Kv4Cache` and
+:class:`Fp4Weight` as the handles of a 4-bit cache and a 4-bit matrix.
 """
 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -67,13 +71,21 @@ class LayerWeightsC(ctypes.Structure):
                 ("w_down", ctypes.POINTER(Nvfp4Desc))]
 
 
+class Kv4Desc(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("max_seq", ctypes.c_int32), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
 #: every symbol include/msk.h declares
 SYMBOLS = ["msk_create", "msk_load_layer", "msk_layer_step", "msk_decode_step", "msk_layer_step_tree",
            "msk_decode_step_tree", "msk_step_graph_capture", "msk_step_graph_launch", "msk_set_timing",
            "msk_get_timeline", "msk_set_launch_timing", "msk_get_launch_ms", "msk_set_wait_budget",
            "msk_set_fault_injection", "msk_debug_scratch", "msk_debug_dequant", "msk_debug_quantize", "msk_debug_convert",
            "msk_debug_fp4_gemm",
-           "msk_attention_noalloc", "msk_get_info", "msk_status_string", "msk_destroy"]
+           "msk_attention_noalloc", "msk_kv4_write", "msk_kv4_read", "msk_attention_kv4_workspace",
+           "msk_attention_kv4", "msk_linear_fp4_workspace", "msk_linear_fp4", "msk_token_logprobs_workspace",
+           "msk_token_logprobs", "msk_get_info", "msk_status_string", "msk_destroy"]
 
 _lib = None
 
@@ -109,13 +121,25 @@ def load_library(path: str = LIB_PATH):
     L.msk_debug_convert.argtypes = [vp, i64, vp, vp, vp]
     L.msk_debug_fp4_gemm.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp]
     L.msk_attention_noalloc.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    f32, size, kv4 = ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(Kv4Desc)
+    L.msk_kv4_write.argtypes = [kv4, vp, vp, i32, i32, i64, i64, i32, vp, vp]
+    L.msk_kv4_read.argtypes = [kv4, i32, i32, vp, vp, i32, i64, i64, vp]
+    L.msk_attention_kv4_workspace.argtypes = [i32, i32, i32, i32]
+    L.msk_attention_kv4.argtypes = [vp, i32, i64, kv4, i32, i32, i32, vp, ctypes.POINTER(i32), i32, f32, vp, vp,
+                                    size, vp]
+    L.msk_linear_fp4_workspace.argtypes = [i32, i64, i64]
+    L.msk_linear_fp4.argtypes = [vp, i32, i64, ctypes.POINTER(Nvfp4Desc), i32, vp, i32, i64, vp, size, vp]
+    L.msk_token_logprobs_workspace.argtypes = [i64, i64, i32]
+    L.msk_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, vp, vp, vp, vp, size, vp]
     L.msk_get_info.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(i64)]
     L.msk_status_string.argtypes = [i32]
     L.msk_status_string.restype = ctypes.c_char_p
     L.msk_destroy.argtypes = [vp]
     L.msk_destroy.restype = None
     for name in SYMBOLS:
-        if name not in ("msk_status_string", "msk_destroy"):
+        if name.endswith("_workspace"):
+            getattr(L, name).restype = size
+        elif name not in ("msk_status_string", "msk_destroy"):
             getattr(L, name).restype = i32
     _lib = L
     return L
@@ -226,6 +250,226 @@ def msk_attention_noalloc(q, kv_layer, pos0, window, out, stream=None):
 
 def msk_destroy(handle):
     load_library().msk_destroy(handle)
+
+
+# ----------------------------------------------------------------------------
+# operators beside the step
+# ----------------------------------------------------------------------------
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _enqueue(stream, *tensors):
+    """The stream handle of a call on these tensors, which all live on the
+    current device."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        d = t.device
+        _need(d.type == "cuda" and d.index == dev,
+              f"every tensor must live on the current CUDA device (cuda:{dev}), got one on {d}")
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _empty(stream, shape, dtype):
+    """A new tensor on the current device for a call on `stream`: taken from
+    that stream's memory pool, so that freeing it is ordered after the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _workspace(given, need, stream):
+    """(tensor kept alive over the call, address, bytes)."""
+    if given is None:
+        if need == 0:
+            return None, None, 0
+        given = _empty(stream, need, torch.uint8)
+    _need(given.is_contiguous(), "workspace must be contiguous")
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+class Kv4Cache:
+    """One layer's KV cache held in 4 bits (see msk_kv4_desc in
+    include/msk.h), over the caller's tensors: codes [2][n_kv_heads][max_seq]
+    [head_dim / 2] and scales [2][n_kv_heads][max_seq][head_dim / 16], uint8."""
+
+    def __init__(self, codes, scales, k_scale=1.0, v_scale=1.0):
+        _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8, "codes and scales are uint8")
+        _need(codes.dim() == 4 and codes.shape[0] == 2 and codes.is_contiguous(),
+              "codes: contiguous [2][n_kv_heads][max_seq][head_dim / 2]")
+        self.n_kv_heads, self.max_seq, self.head_dim = codes.shape[1], codes.shape[2], 2 * codes.shape[3]
+        _need(scales.shape == (2, self.n_kv_heads, self.max_seq, self.head_dim // 16) and scales.is_contiguous(),
+              "scales: contiguous [2][n_kv_heads][max_seq][head_dim / 16]")
+        _need(codes.is_cuda and codes.device == scales.device, "codes and scales live on one CUDA device")
+        self.codes, self.scales = codes, scales
+        self.desc = ctypes.pointer(Kv4Desc(codes.data_ptr(), scales.data_ptr(), self.n_kv_heads, self.head_dim,
+                                           self.max_seq, k_scale, v_scale))
+
+    @classmethod
+    def empty(cls, n_kv_heads, max_seq, head_dim, k_scale=1.0, v_scale=1.0, device="cuda"):
+        """A new cache of zeros."""
+        shape = (2, n_kv_heads, max_seq)
+        return cls(torch.zeros(*shape, head_dim // 2, dtype=torch.uint8, device=device),
+                   torch.zeros(*shape, head_dim // 16, dtype=torch.uint8, device=device), k_scale, v_scale)
+
+
+class Fp4Weight:
+    """A 4-bit matrix [rows][cols] (see msk_nvfp4_desc in include/msk.h) over
+    the caller's tensors: packed [rows][cols / 2] and scales
+    [rows][cols / 16], uint8."""
+
+    def __init__(self, packed, scales, tensor_scale=1.0):
+        _need(packed.dtype == torch.uint8 and scales.dtype == torch.uint8, "packed and scales are uint8")
+        _need(packed.dim() == 2 and packed.is_contiguous(), "packed: contiguous [rows][cols / 2]")
+        self.rows, self.cols = packed.shape[0], 2 * packed.shape[1]
+        _need(scales.shape == (self.rows, self.cols // 16) and scales.is_contiguous(),
+              "scales: contiguous [rows][cols / 16]")
+        _need(packed.is_cuda and packed.device == scales.device, "packed and scales live on one CUDA device")
+        self.packed, self.scales, self.tensor_scale = packed, scales, float(tensor_scale)
+        self.desc = ctypes.pointer(Nvfp4Desc(packed.data_ptr(), scales.data_ptr(), self.tensor_scale, self.rows,
+                                             self.cols))
+
+
+def _step(t, axis):
+    """Elements between neighbours of an axis; 0 where there are none (the
+    stride of an axis of one is arbitrary)."""
+    return t.stride(axis) if t.shape[axis] > 1 else 0
+
+
+def _position(pos):
+    """(host value, device address) of a position given as an int or as a
+    CUDA int32 tensor of one element."""
+    if isinstance(pos, torch.Tensor):
+        _need(pos.dtype == torch.int32 and pos.numel() == 1 and pos.is_cuda,
+              "a position tensor is one int32 on the GPU")
+        return 0, pos.data_ptr()
+    return int(pos), None
+
+
+def _kv_rows(cache, k, v):
+    _need(k.dim() == 3 and k.shape == v.shape and k.dtype == v.dtype and k.dtype in _DTYPES
+          and _step(k, 0) == _step(v, 0) and _step(k, 1) == _step(v, 1) and v.stride(2) == 1,
+          "k and v: [tokens][n_kv_heads][head_dim], one shape, type and layout")
+    _need(k.shape[1] == cache.n_kv_heads and k.shape[2] == cache.head_dim and k.stride(2) == 1,
+          "k and v do not fit the cache's heads")
+
+
+def msk_kv4_write(cache, k, v, pos0, stream=None):
+    """Quantises k and v ([tokens][n_kv_heads][head_dim], any strides of the
+    first two axes) into cache rows pos0, pos0 + 1, ...  pos0: an int, or a
+    CUDA int32 tensor read when the kernel runs."""
+    _kv_rows(cache, k, v)
+    host, dev = _position(pos0)
+    st = _enqueue(stream, k, v, cache.codes)
+    _check(load_library().msk_kv4_write(cache.desc, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.shape[0],
+                                        _step(k, 0), _step(k, 1), host, dev, st), "msk_kv4_write")
+
+
+def msk_kv4_read(cache, pos0, tokens, dtype=torch.bfloat16, out=None, stream=None):
+    """Rows pos0 .. pos0 + tokens - 1 as (k, v), each
+    [tokens][n_kv_heads][head_dim] of `dtype`, or into the pair `out`."""
+    if out is None:
+        _need(tokens >= 0 and dtype in _DTYPES, "tokens >= 0 and a floating type")
+        shape = (tokens, cache.n_kv_heads, cache.head_dim)
+        out = _empty(stream, shape, dtype), _empty(stream, shape, dtype)
+    k, v = out
+    _kv_rows(cache, k, v)
+    _need(k.shape[0] == tokens, "out does not hold `tokens` rows")
+    st = _enqueue(stream, k, v, cache.codes)
+    _check(load_library().msk_kv4_read(cache.desc, int(pos0), tokens, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype],
+                                       _step(k, 0), _step(k, 1), st), "msk_kv4_read")
+    return k, v
+
+
+@functools.lru_cache(maxsize=None)
+def msk_attention_kv4_workspace(tokens, n_q_heads, n_kv_heads, head_dim):
+    """Workspace bytes of msk_attention_kv4 for these sizes."""
+    return load_library().msk_attention_kv4_workspace(tokens, n_q_heads, n_kv_heads, head_dim)
+
+
+def msk_attention_kv4(q, cache, cache_len, window=0, parents=None, softmax_scale=0.0, out=None, workspace=None,
+                      stream=None):
+    """Attention of q ([tokens][n_q_heads][head_dim] bf16 or fp16, any token
+    stride) over a Kv4Cache holding `cache_len` rows and then the tokens' own;
+    returns out [tokens][n_q_heads * head_dim].  cache_len: an int, or a CUDA
+    int32 tensor read when the kernels run.  parents: the candidate tree as in
+    msk_decode_step_tree, None for the chain.  Nothing is waited for."""
+    T, Hq, d = q.shape
+    _need(q.dtype in _DTYPES and d == cache.head_dim and q.stride(2) == 1 and _step(q, 1) in (0, d),
+          "q: [tokens][n_q_heads][head_dim] with contiguous heads")
+    _need(parents is None or len(parents) == T, "parents: one for each token")
+    if out is None:
+        out = _empty(stream, (T, Hq * d), q.dtype)
+    _need(out.dtype == q.dtype and out.numel() == q.numel() and out.is_contiguous(),
+          "out: contiguous [tokens][n_q_heads * head_dim] of q's type")
+    host, dev = _position(cache_len)
+    ws, addr, size = _workspace(workspace, msk_attention_kv4_workspace(T, Hq, cache.n_kv_heads, d), stream)
+    st = _enqueue(stream, q, out, cache.codes) if ws is None else _enqueue(stream, q, out, cache.codes, ws)
+    _check(load_library().msk_attention_kv4(q.data_ptr(), _DTYPES[q.dtype], _step(q, 0), cache.desc, T, Hq, host, dev,
+                                            None if parents is None else _positions(parents), int(window),
+                                            softmax_scale, out.data_ptr(), addr, size, st), "msk_attention_kv4")
+    return out
+
+
+@functools.lru_cache(maxsize=None)
+def msk_linear_fp4_workspace(tokens, rows, cols):
+    """Workspace bytes of msk_linear_fp4 for these sizes."""
+    return load_library().msk_linear_fp4_workspace(tokens, rows, cols)
+
+
+def msk_linear_fp4(x, weight, out_dtype=None, out=None, workspace=None, stream=None):
+    """x ([tokens][cols] bf16 or fp16, any row stride) times the transposed
+    Fp4Weight: [tokens][rows] of out_dtype (x's type unless given) or into
+    `out` (any row stride)."""
+    _need(x.dim() == 2 and x.shape[1] == weight.cols and x.stride(1) == 1 and x.dtype in _DTYPES,
+          "x: [tokens][cols], contiguous rows")
+    T = x.shape[0]
+    if out is None:
+        out = _empty(stream, (T, weight.rows), x.dtype if out_dtype is None else out_dtype)
+    _need(out.shape == (T, weight.rows) and out.dtype in _DTYPES and (out.stride(1) == 1 or weight.rows <= 1),
+          "out: [tokens][rows] of a floating type, contiguous rows")
+    ws, addr, size = _workspace(workspace, msk_linear_fp4_workspace(T, weight.rows, weight.cols), stream)
+    st = _enqueue(stream, x, out, weight.packed) if ws is None else _enqueue(stream, x, out, weight.packed, ws)
+    _check(load_library().msk_linear_fp4(x.data_ptr(), _DTYPES[x.dtype], _step(x, 0), weight.desc, T, out.data_ptr(),
+                                         _DTYPES[out.dtype], _step(out, 0), addr, size, st), "msk_linear_fp4")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def msk_token_logprobs_workspace(rows, vocab, top):
+    """Workspace bytes of msk_token_logprobs for these sizes."""
+    return load_library().msk_token_logprobs_workspace(rows, vocab, top)
+
+
+def msk_token_logprobs(logits, tokens=None, top=0, temperature=1.0, workspace=None, stream=None):
+    """Log probabilities of `tokens` (int32 [rows]; a negative one marks a
+    padded row) under softmax(logits / temperature), logits [rows][vocab] of
+    any floating type and row stride.  Returns (logprob, entropy, rank,
+    top_ids, top_logprobs): fp32 [rows], fp32 [rows], int32 [rows], int32
+    [rows][top], fp32 [rows][top]; logprob and rank are None without tokens."""
+    _need(logits.dim() == 2 and logits.dtype in _DTYPES and (logits.stride(1) == 1 or logits.shape[1] <= 1),
+          "logits: [rows][vocab], contiguous rows")
+    R, V = logits.shape
+    _need(0 <= top <= 32, "top: 0 to 32 alternatives")
+    logprob = rank = tok = lp = rk = None
+    if tokens is not None:
+        _need(tokens.dtype == torch.int32 and tokens.shape == (R,) and tokens.is_contiguous(), "tokens: int32 [rows]")
+        logprob, rank = _empty(stream, R, torch.float32), _empty(stream, R, torch.int32)
+        tok, lp, rk = tokens.data_ptr(), logprob.data_ptr(), rank.data_ptr()
+    entropy = _empty(stream, R, torch.float32)
+    top_ids, top_logprobs = _empty(stream, (R, top), torch.int32), _empty(stream, (R, top), torch.float32)
+    ws, addr, size = _workspace(workspace, msk_token_logprobs_workspace(R, V, top), stream)
+    st = _enqueue(stream, *[t for t in (logits, tokens, ws) if t is not None])
+    _check(load_library().msk_token_logprobs(logits.data_ptr(), _DTYPES[logits.dtype], R, V, _step(logits, 0), tok,
+                                             temperature, top, lp, rk, entropy.data_ptr(), top_ids.data_ptr(),
+                                             top_logprobs.data_ptr(), addr, size, st), "msk_token_logprobs")
+    return logprob, entropy, rank, top_ids, top_logprobs
 
 
 # ----------------------------------------------------------------------------

@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libmsk.so")
-SOURCES = ["msk_layer.cu", "msk_repack.cu", "msk_api.cu", "msk_noalloc.cu"]
+SOURCES = ["msk_layer.cu", "msk_repack.cu", "msk_api.cu", "msk_noalloc.cu", "msk_kv4.cu", "msk_linear4.cu",
+           "msk_logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

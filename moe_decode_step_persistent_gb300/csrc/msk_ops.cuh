@@ -1,0 +1,63 @@
+// Shared by the operators beside the step (4-bit cache, 4-bit products, log
+// probabilities): element types, the device check of their entry points, and
+// small device helpers.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/msk.h"
+#include "msk_device.cuh"
+
+namespace msk {
+
+inline bool ops_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline int dtype_bytes(int32_t t) { return t == MSK_FP32 ? 4 : 2; }
+inline bool dtype_ok(int32_t t) { return t == MSK_BF16 || t == MSK_FP16 || t == MSK_FP32; }
+
+// Whether the current device is one these kernels are compiled for; its SM
+// count.  (Attributes are looked up by the runtime without a device call.)
+inline msk_status ops_device(int* nsm) {
+  int dev = 0, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MSK_ERR_CUDA;
+  return major == 10 && minor == 3 ? MSK_OK : MSK_ERR_UNSUPPORTED_DEVICE;
+}
+
+// The SM count the workspace sizes are made for when there is no device to
+// ask; kernels never use more blocks than a workspace has room for.
+constexpr int kOpsSms = 152;
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+// Two 16-bit elements of a 32-bit word as floats.
+__device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
+  return fp16 ? unpack_f16x2(w) : make_float2(bf16_lo(w), bf16_hi(w));
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
+  return fp16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// The power of two by which a row of 16-bit floats with largest magnitude
+// `amax` is multiplied before it is written as fp16, as an exponent: amax
+// lands in [2^8, 2^9), so that every element above 2^-22 amax is exact in
+// fp16 (bf16 has 8 significant bits, fp16 11 above 2^-14) and smaller ones
+// are off by at most 2^-25, that is 2^-33 amax: below what an fp32 sum of
+// the row's products keeps.  The factor and its inverse stay normal fp32
+// numbers; at its limit even bf16's subnormals arrive exactly.
+__device__ __forceinline__ int row_shift(float amax) {
+  const int e = (int)(__float_as_uint(amax) >> 23) - 127;  // floor(log2), -127 for zero and subnormals
+  return e < -118 ? 126 : (e > 127 ? -119 : 8 - e);
+}
+
+}  // namespace msk
