@@ -419,7 +419,7 @@ msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_stride, cons
  *   tokens : int32 [rows] given tokens, or NULL (then logprob and rank are
  *            NULL too).  A token outside [0, vocab) marks a padded row: its
  *            logprob is 0 and its rank -1;
- *   temperature: > 0;
+ *   temperature: 1e-30 to 1e30;
  *   logprob: fp32 [rows], log softmax at the given token;
  *   rank   : int32 [rows], how many logits are greater than the given one;
  *   entropy: fp32 [rows], in nats;
@@ -429,13 +429,10 @@ msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_stride, cons
  * Any output may be NULL.  Logits of -inf are barred tokens (probability 0).
  * A row with a NaN or +inf, or with nothing but -inf, has no distribution: its
  * logprob, entropy and top_logprobs are NaN, its ids in range.
- * rows == 0 does nothing.
- * workspace: msk_token_logprobs_workspace bytes (may be 0), 16-byte aligned. */
-size_t msk_token_logprobs_workspace(int64_t rows, int64_t vocab, int32_t top);
+ * rows == 0 does nothing. */
 msk_status msk_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
                               const int32_t* tokens, float temperature, int32_t top, float* logprob, int32_t* rank,
-                              float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
-                              size_t workspace_bytes, void* stream);
+                              float* entropy, int32_t* top_ids, float* top_logprobs, void* stream);
 
 /* Number of SMs (= CTAs per launch) the model uses, and bytes of device
  * memory it owns. */

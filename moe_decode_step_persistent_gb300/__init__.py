@@ -84,7 +84,7 @@ SYMBOLS = ["msk_create", "msk_load_layer", "msk_layer_step", "msk_decode_step", 
            "msk_set_fault_injection", "msk_debug_scratch", "msk_debug_dequant", "msk_debug_quantize", "msk_debug_convert",
            "msk_debug_fp4_gemm",
            "msk_attention_noalloc", "msk_kv4_write", "msk_kv4_read", "msk_attention_kv4_workspace",
-           "msk_attention_kv4", "msk_linear_fp4_workspace", "msk_linear_fp4", "msk_token_logprobs_workspace",
+           "msk_attention_kv4", "msk_linear_fp4_workspace", "msk_linear_fp4",
            "msk_token_logprobs", "msk_get_info", "msk_status_string", "msk_destroy"]
 
 _lib = None
@@ -129,8 +129,7 @@ def load_library(path: str = LIB_PATH):
                                     size, vp]
     L.msk_linear_fp4_workspace.argtypes = [i32, i64, i64]
     L.msk_linear_fp4.argtypes = [vp, i32, i64, ctypes.POINTER(Nvfp4Desc), i32, vp, i32, i64, vp, size, vp]
-    L.msk_token_logprobs_workspace.argtypes = [i64, i64, i32]
-    L.msk_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, vp, vp, vp, vp, size, vp]
+    L.msk_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, vp, vp, vp, vp]
     L.msk_get_info.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(i64)]
     L.msk_status_string.argtypes = [i32]
     L.msk_status_string.restype = ctypes.c_char_p
@@ -264,15 +263,19 @@ def _need(ok, what):
         raise ValueError(what)
 
 
+#: the current stream's handle without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _enqueue(stream, *tensors):
     """The stream handle of a call on these tensors, which all live on the
     current device."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        d = t.device
-        _need(d.type == "cuda" and d.index == dev,
-              f"every tensor must live on the current CUDA device (cuda:{dev}), got one on {d}")
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+        if t.get_device() != dev:
+            raise ValueError(f"every tensor must live on the current CUDA device (cuda:{dev}), got one on {t.device}")
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _empty(stream, shape, dtype):
@@ -441,13 +444,7 @@ def msk_linear_fp4(x, weight, out_dtype=None, out=None, workspace=None, stream=N
     return out
 
 
-@functools.lru_cache(maxsize=1024)
-def msk_token_logprobs_workspace(rows, vocab, top):
-    """Workspace bytes of msk_token_logprobs for these sizes."""
-    return load_library().msk_token_logprobs_workspace(rows, vocab, top)
-
-
-def msk_token_logprobs(logits, tokens=None, top=0, temperature=1.0, workspace=None, stream=None):
+def msk_token_logprobs(logits, tokens=None, top=0, temperature=1.0, stream=None):
     """Log probabilities of `tokens` (int32 [rows]; a negative one marks a
     padded row) under softmax(logits / temperature), logits [rows][vocab] of
     any floating type and row stride.  Returns (logprob, entropy, rank,
@@ -464,11 +461,10 @@ def msk_token_logprobs(logits, tokens=None, top=0, temperature=1.0, workspace=No
         tok, lp, rk = tokens.data_ptr(), logprob.data_ptr(), rank.data_ptr()
     entropy = _empty(stream, R, torch.float32)
     top_ids, top_logprobs = _empty(stream, (R, top), torch.int32), _empty(stream, (R, top), torch.float32)
-    ws, addr, size = _workspace(workspace, msk_token_logprobs_workspace(R, V, top), stream)
-    st = _enqueue(stream, *[t for t in (logits, tokens, ws) if t is not None])
+    st = _enqueue(stream, logits, entropy) if tokens is None else _enqueue(stream, logits, tokens, entropy)
     _check(load_library().msk_token_logprobs(logits.data_ptr(), _DTYPES[logits.dtype], R, V, _step(logits, 0), tok,
                                              temperature, top, lp, rk, entropy.data_ptr(), top_ids.data_ptr(),
-                                             top_logprobs.data_ptr(), addr, size, st), "msk_token_logprobs")
+                                             top_logprobs.data_ptr(), st), "msk_token_logprobs")
     return logprob, entropy, rank, top_ids, top_logprobs
 
 

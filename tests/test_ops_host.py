@@ -99,12 +99,12 @@ def test_linear(M, lib, change, status):
     (dict(t=0.0), INVALID), (dict(t=-1.0), INVALID), (dict(t=float("nan")), INVALID), (dict(t=float("inf")), INVALID),
     (dict(vocab=0), SHAPE), (dict(vocab=1 << 31), SHAPE), (dict(top=33), SHAPE), (dict(top=-1), SHAPE),
     (dict(vocab=4, top=5), INVALID), (dict(ld=999), INVALID), (dict(tokens=None), INVALID),
-    (dict(logits=P + 2), ALIGN), (dict(tokens=P + 2), ALIGN), (dict(lp=P + 1), ALIGN), (dict(ws=P + 8), ALIGN)])
+    (dict(logits=P + 2), ALIGN), (dict(tokens=P + 2), ALIGN), (dict(lp=P + 1), ALIGN)])
 def test_logprobs(lib, change, status):
-    a = dict(logits=P, dt=FP32, rows=3, vocab=1000, ld=1000, tokens=P, t=1.0, top=2, lp=P, ws=P)
+    a = dict(logits=P, dt=FP32, rows=3, vocab=1000, ld=1000, tokens=P, t=1.0, top=2, lp=P)
     a.update(change)
     assert lib.msk_token_logprobs(a["logits"], a["dt"], a["rows"], a["vocab"], a["ld"], a["tokens"], a["t"], a["top"],
-                                  a["lp"], P, P, P, P, a["ws"], 1 << 40, None) == status
+                                  a["lp"], P, P, P, P, None) == status
 
 
 def test_workspace_sizes(lib):
