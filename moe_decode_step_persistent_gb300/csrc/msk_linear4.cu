@@ -7,16 +7,56 @@
 namespace msk {
 namespace {
 
+constexpr int kGroup = 256;      // columns a warp takes: 64 consecutive ones a lane
+constexpr int kMaxGroups = 16;   // groups (warps along the columns) of a pass
+constexpr int kTokStride = 20;   // words between tokens of a warp's partial sums (no bank is hit twice)
+
 struct Lin4 {
   const uint16_t* x;
   const uint8_t* codes;
   const uint8_t* scales;
   void* y;
+  float* ws;  // [T][N] partial sums between passes
   long long x_stride, y_stride, N;
   int K, T, y_dtype;
-  bool fp16;
+  int groups, per_pass, passes;  // column groups, those of one pass, passes over the columns
+  int wr;                        // 16-row tiles side by side in a block
+  bool fp16, wide;               // codes aligned to 32 bytes
   float ts;
 };
+
+// A lane's share of 16 weight rows: 64 columns of rows g and g + 8.
+struct WTile {
+  uint32_t c[2][8];
+  uint32_t e[2];
+};
+
+__device__ __forceinline__ void ld_codes(uint32_t (&w)[8], const uint8_t* p, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p + 16));
+  }
+}
+
+// (col: the lane's first column, or -1 past the matrix)
+__device__ __forceinline__ void ld_tile(WTile& t, const Lin4& a, long long row, int col) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const long long r = row + 8 * i;
+    if (col >= 0 && r < a.N) {
+      ld_codes(t.c[i], a.codes + r * (a.K / 2) + col / 2, a.wide);
+      asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(t.e[i]) : "l"(a.scales + r * (a.K / 16) + col / 16));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t.c[i][j] = 0;
+      t.e[i] = 0;
+    }
+  }
+}
 
 __device__ __forceinline__ void store_y(const Lin4& a, int t, long long n, float v) {
   const long long i = t * a.y_stride + n;
@@ -25,86 +65,110 @@ __device__ __forceinline__ void store_y(const Lin4& a, int t, long long n, float
   else static_cast<__nv_bfloat16*>(a.y)[i] = __float2bfloat16_rn(v);
 }
 
-// A block takes 16 weight rows, its 8 warps the 128-column chunks in turn.
-// W is the MMA's A operand (16 rows), the tokens are its columns.  A lane
-// takes 32 consecutive columns of a chunk (16 bytes of codes a row, two
-// scales), four for each step of the contraction, and of x the same ones.
-__global__ void __launch_bounds__(256) linear4_kernel(const __grid_constant__ Lin4 a) {
-  __shared__ float red[8][16][17];
+// Persistent blocks of up to 16 warps.  A warp keeps its 256 columns of x in
+// registers for the whole pass, as the MMA's B fragments (NT tiles of 8
+// tokens), and streams weight rows through its A fragments, 16 rows at a
+// time: decoded to fp16 in registers, exact, with one multiply by the block
+// scale for two weights.  Of x and W a lane takes the same 64 columns, so a
+// row's codes are one 32-byte load and its scales one 4-byte load, and
+// neither passes through shared memory.  The warps of a row tile add their
+// partial sums up in shared memory.
+//
+// The next tile's loads are issued before the current one is computed: two
+// tiles of up to 36 KB in flight per SM are what DRAM's latency asks for.
+template <int NT>
+__global__ void __launch_bounds__(512, 1) linear4_kernel(const __grid_constant__ Lin4 a) {
+  constexpr int TOK = 8 * NT;
+  __shared__ float red[2][kMaxGroups][TOK * kTokStride];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const long long n0 = blockIdx.x * 16ll;
-  const int chunks = a.K / 128;
-  // the scaling of this warp's share of x, token by token
-  int shift[2];
+  const int wk = warp % a.per_pass, tile = warp / a.per_pass;
+  const long long step = 16ll * a.wr * gridDim.x, first = 16ll * a.wr * blockIdx.x;
+  int buf = 0;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int grp = pass * a.per_pass + wk;
+    int col = grp * kGroup + c * 64;
+    if (grp >= a.groups || col >= a.K) col = -1;
+    WTile cur;
+    ld_tile(cur, a, first + tile * 16 + g, col);
+    // x: scaled by a power of two for each (token, warp), then fp16
+    uint32_t xf[NT][32];
+    float back[NT][2];  // the scalings of this lane's accumulator columns, undone
 #pragma unroll
-  for (int nt = 0; nt < 2; ++nt) {
-    const int t = nt * 8 + g;
-    float amax = 0.f;
-    if (t < a.T)
-      for (int ch = warp; ch < chunks; ch += 8) {
-        const uint4* p = reinterpret_cast<const uint4*>(a.x + t * a.x_stride + ch * 128 + c * 32);
-        for (int i = 0; i < 4; ++i) {
-          const uint4 u = __ldg(p + i);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack16(w[j], a.fp16);
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        }
-      }
-    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-    shift[nt] = row_shift(amax);
-  }
-  float acc[2][4] = {};
-  const long long r0 = min(n0 + g, a.N - 1), r1 = min(n0 + g + 8, a.N - 1);
-  for (int ch = warp; ch < chunks; ch += 8) {
-    const uint4 u0 = __ldg(reinterpret_cast<const uint4*>(a.codes + r0 * (a.K / 2) + ch * 64 + c * 16));
-    const uint4 u1 = __ldg(reinterpret_cast<const uint4*>(a.codes + r1 * (a.K / 2) + ch * 64 + c * 16));
-    const uint32_t e0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(a.scales + r0 * (a.K / 16) + ch * 8 + c * 2));
-    const uint32_t e1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(a.scales + r1 * (a.K / 16) + ch * 8 + c * 2));
-    const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
-    uint32_t xf[2][16];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
+    for (int nt = 0; nt < NT; ++nt) {
       const int t = nt * 8 + g;
-      const float mul = exp2i(shift[nt]);
+      const uint4* p = reinterpret_cast<const uint4*>(a.x + t * a.x_stride + (col < 0 ? 0 : col));
+      const bool in = t < a.T && col >= 0;
+      float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         uint4 u = make_uint4(0, 0, 0, 0);
-        if (t < a.T) u = __ldg(reinterpret_cast<const uint4*>(a.x + t * a.x_stride + ch * 128 + c * 32) + i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = unpack16(w[j], a.fp16);
-          xf[nt][4 * i + j] = pack_f16x2(f.x * mul, f.y * mul);
-        }
+        if (in) u = __ldg(p + i);
+        xf[nt][4 * i] = u.x, xf[nt][4 * i + 1] = u.y, xf[nt][4 * i + 2] = u.z, xf[nt][4 * i + 3] = u.w;
       }
-    }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t f0 = f16x2_bcast(e0, k >= 4), f1 = f16x2_bcast(e1, k >= 4);
-      const uint32_t af[4] = {hmul2(e2m1_byte_to_f16x2(w0[k >> 1], 2 * (k & 1)), f0),
-                              hmul2(e2m1_byte_to_f16x2(w1[k >> 1], 2 * (k & 1)), f1),
-                              hmul2(e2m1_byte_to_f16x2(w0[k >> 1], 2 * (k & 1) + 1), f0),
-                              hmul2(e2m1_byte_to_f16x2(w1[k >> 1], 2 * (k & 1) + 1), f1)};
-      mma_f16(acc[0], af, xf[0][2 * k], xf[0][2 * k + 1]);
-      mma_f16(acc[1], af, xf[1][2 * k], xf[1][2 * k + 1]);
+      for (int i = 0; i < 32; ++i) {
+        const float2 f = unpack16(xf[nt][i], a.fp16);
+        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      const int sh = row_shift(amax);
+      const float mul = exp2i(sh);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 f = unpack16(xf[nt][i], a.fp16);
+        xf[nt][i] = pack_f16x2(f.x * mul, f.y * mul);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) back[nt][i] = exp2i(-__shfl_sync(0xFFFFFFFFu, sh, (2 * c + i) * 4));
+    }
+
+    for (long long r0 = first; r0 < a.N; r0 += step) {
+      WTile nxt;
+      ld_tile(nxt, a, r0 + step + tile * 16 + g, col);
+      float acc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+      uint32_t sc[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sc[i][0] = e4m3_pair_to_f16x2(cur.e[i], 0);
+        sc[i][1] = e4m3_pair_to_f16x2(cur.e[i], 1);
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const uint32_t f0 = f16x2_bcast(sc[0][k >> 3], (k >> 2) & 1), f1 = f16x2_bcast(sc[1][k >> 3], (k >> 2) & 1);
+        const uint32_t af[4] = {hmul2(e2m1_byte_to_f16x2(cur.c[0][k >> 1], 2 * (k & 1)), f0),
+                                hmul2(e2m1_byte_to_f16x2(cur.c[1][k >> 1], 2 * (k & 1)), f1),
+                                hmul2(e2m1_byte_to_f16x2(cur.c[0][k >> 1], 2 * (k & 1) + 1), f0),
+                                hmul2(e2m1_byte_to_f16x2(cur.c[1][k >> 1], 2 * (k & 1) + 1), f1)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], af, xf[nt][2 * k], xf[nt][2 * k + 1]);
+      }
+      float* part = red[buf][warp];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          part[(nt * 8 + 2 * c + i) * kTokStride + g] = acc[nt][i] * back[nt][i];
+          part[(nt * 8 + 2 * c + i) * kTokStride + g + 8] = acc[nt][2 + i] * back[nt][i];
+        }
+      __syncthreads();  // (the other buffer's readers are past it too)
+      for (int o = threadIdx.x; o < 16 * TOK * a.wr; o += blockDim.x) {
+        const int r = o & 15, t = (o >> 4) % TOK, rt = (o >> 4) / TOK;
+        const long long n = r0 + rt * 16 + r;
+        if (t >= a.T || n >= a.N) continue;
+        float s = 0.f;
+        for (int w = 0; w < a.per_pass; ++w) s += red[buf][rt * a.per_pass + w][t * kTokStride + r];
+        // (a later pass of the same thread takes the partial sum up again)
+        if (pass > 0) s += a.ws[t * a.N + n];
+        if (pass + 1 < a.passes) a.ws[t * a.N + n] = s;
+        else store_y(a, t, n, s * a.ts);
+      }
+      buf ^= 1;
+      cur = nxt;
     }
   }
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float f = exp2i(-__shfl_sync(0xFFFFFFFFu, shift[nt], (2 * c + i) * 4));
-      red[warp][g][nt * 8 + 2 * c + i] = acc[nt][i] * f;
-      red[warp][g + 8][nt * 8 + 2 * c + i] = acc[nt][2 + i] * f;
-    }
-  __syncthreads();
-  const int t = threadIdx.x >> 4, r = threadIdx.x & 15;
-  float s = 0.f;
-  for (int w = 0; w < 8; ++w) s += red[w][r][t];
-  if (t < a.T && n0 + r < a.N) store_y(a, t, n0 + r, s * a.ts);
 }
 
 }  // namespace
@@ -113,8 +177,8 @@ __global__ void __launch_bounds__(256) linear4_kernel(const __grid_constant__ Li
 using namespace msk;
 
 extern "C" size_t msk_linear_fp4_workspace(int32_t tokens, int64_t rows, int64_t cols) {
-  (void)tokens, (void)rows, (void)cols;
-  return 0;
+  if (tokens <= 0 || rows <= 0 || cols <= kGroup * kMaxGroups) return 0;
+  return (size_t)tokens * (size_t)rows * 4;
 }
 
 extern "C" msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_stride, const msk_nvfp4_desc* w,
@@ -140,6 +204,19 @@ extern "C" msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_s
   a.x = static_cast<const uint16_t*>(x), a.codes = w->packed, a.scales = w->scales, a.y = y;
   a.x_stride = x_stride, a.y_stride = y_stride, a.N = w->rows, a.K = (int)w->cols, a.T = tokens;
   a.y_dtype = y_dtype, a.fp16 = x_dtype == MSK_FP16, a.ts = w->tensor_scale;
-  linear4_kernel<<<(unsigned)((w->rows + 15) / 16), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  a.ws = static_cast<float*>(workspace);
+  a.wide = reinterpret_cast<uintptr_t>(w->packed) % 32 == 0;
+  a.groups = (a.K + kGroup - 1) / kGroup;
+  a.passes = (a.groups + kMaxGroups - 1) / kMaxGroups;
+  a.per_pass = (a.groups + a.passes - 1) / a.passes;
+  // row tiles side by side: as many as warps allow, fewer where that would
+  // leave SMs without rows
+  const long long tiles = (a.N + 15) / 16;
+  a.wr = (int)std::max<long long>(1, std::min<long long>(kMaxGroups / a.per_pass, tiles / nsm));
+  const unsigned grid = (unsigned)std::min<long long>(nsm, (tiles + a.wr - 1) / a.wr);
+  const unsigned threads = 32u * a.per_pass * a.wr;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (tokens <= 8) linear4_kernel<1><<<grid, threads, 0, st>>>(a);
+  else linear4_kernel<2><<<grid, threads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }
