@@ -325,9 +325,9 @@ msk_status msk_attention_noalloc(const void* q, const void* kv_layer, int32_t to
  * describe none of them; they serve the same batch-one verify pass.
  *
  * They differ from the step's calls in three ways: they take no model, they
- * ENQUEUE their work on `stream` and return without waiting for it (no wait
- * in them can run out, so there is no error word to read), and they may be
- * captured into a CUDA graph.  They keep nothing between calls.  Where a call
+ * ENQUEUE their work on `stream` and return without waiting for it, and they
+ * may be captured into a CUDA graph.  They keep nothing between calls but the
+ * record of a device wait that ran out (msk_ops_check).  Where a call
  * takes a workspace, the caller owns it: calls that may overlap on the GPU
  * (two streams, two graphs) need one each.  Its contents are of no meaning
  * before or after a call.
@@ -406,12 +406,15 @@ msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_stride, con
  *      between rows, aligned to its element.
  * Weights enter without rounding (the products e2m1 * e4m3), x in fp16 after an
  * exact scaling by powers of two, sums are fp32.  A NaN block scale makes the
- * outputs of its row NaN.  tokens == 0 or rows == 0 does nothing.
- * workspace: msk_linear_fp4_workspace bytes (may be 0), 16-byte aligned. */
-size_t msk_linear_fp4_workspace(int32_t tokens, int64_t rows, int64_t cols);
+ * outputs of its row NaN.  tokens == 0 or rows == 0 does nothing. */
 msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_stride, const msk_nvfp4_desc* w, int32_t tokens,
-                          void* y, int32_t y_dtype, int64_t y_stride, void* workspace, size_t workspace_bytes,
-                          void* stream);
+                          void* y, int32_t y_dtype, int64_t y_stride, void* stream);
+
+/* Synchronises `stream` and tells whether a bounded device wait of these
+ * operators ran out on the current device since the last call of this
+ * function: MSK_ERR_TIMEOUT (the outputs of the calls since then are not to be
+ * used), else MSK_OK. */
+msk_status msk_ops_check(void* stream);
 
 /* Log probabilities under softmax(logits / temperature), one pass per row:
  *   logits : [rows][vocab] of dtype (any of the three), ld elements between

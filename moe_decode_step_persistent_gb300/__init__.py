@@ -84,8 +84,7 @@ SYMBOLS = ["msk_create", "msk_load_layer", "msk_layer_step", "msk_decode_step", 
            "msk_set_fault_injection", "msk_debug_scratch", "msk_debug_dequant", "msk_debug_quantize", "msk_debug_convert",
            "msk_debug_fp4_gemm",
            "msk_attention_noalloc", "msk_kv4_write", "msk_kv4_read", "msk_attention_kv4_workspace",
-           "msk_attention_kv4", "msk_linear_fp4_workspace", "msk_linear_fp4",
-           "msk_token_logprobs", "msk_get_info", "msk_status_string", "msk_destroy"]
+           "msk_attention_kv4", "msk_linear_fp4", "msk_ops_check", "msk_token_logprobs", "msk_get_info", "msk_status_string", "msk_destroy"]
 
 _lib = None
 
@@ -127,8 +126,8 @@ def load_library(path: str = LIB_PATH):
     L.msk_attention_kv4_workspace.argtypes = [i32, i32, i32, i32]
     L.msk_attention_kv4.argtypes = [vp, i32, i64, kv4, i32, i32, i32, vp, ctypes.POINTER(i32), i32, f32, vp, vp,
                                     size, vp]
-    L.msk_linear_fp4_workspace.argtypes = [i32, i64, i64]
-    L.msk_linear_fp4.argtypes = [vp, i32, i64, ctypes.POINTER(Nvfp4Desc), i32, vp, i32, i64, vp, size, vp]
+    L.msk_linear_fp4.argtypes = [vp, i32, i64, ctypes.POINTER(Nvfp4Desc), i32, vp, i32, i64, vp]
+    L.msk_ops_check.argtypes = [vp]
     L.msk_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, vp, vp, vp, vp]
     L.msk_get_info.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(i64)]
     L.msk_status_string.argtypes = [i32]
@@ -420,13 +419,7 @@ def msk_attention_kv4(q, cache, cache_len, window=0, parents=None, softmax_scale
     return out
 
 
-@functools.lru_cache(maxsize=None)
-def msk_linear_fp4_workspace(tokens, rows, cols):
-    """Workspace bytes of msk_linear_fp4 for these sizes."""
-    return load_library().msk_linear_fp4_workspace(tokens, rows, cols)
-
-
-def msk_linear_fp4(x, weight, out_dtype=None, out=None, workspace=None, stream=None):
+def msk_linear_fp4(x, weight, out_dtype=None, out=None, stream=None):
     """x ([tokens][cols] bf16 or fp16, any row stride) times the transposed
     Fp4Weight: [tokens][rows] of out_dtype (x's type unless given) or into
     `out` (any row stride)."""
@@ -437,11 +430,16 @@ def msk_linear_fp4(x, weight, out_dtype=None, out=None, workspace=None, stream=N
         out = _empty(stream, (T, weight.rows), x.dtype if out_dtype is None else out_dtype)
     _need(out.shape == (T, weight.rows) and out.dtype in _DTYPES and (out.stride(1) == 1 or weight.rows <= 1),
           "out: [tokens][rows] of a floating type, contiguous rows")
-    ws, addr, size = _workspace(workspace, msk_linear_fp4_workspace(T, weight.rows, weight.cols), stream)
-    st = _enqueue(stream, x, out, weight.packed) if ws is None else _enqueue(stream, x, out, weight.packed, ws)
+    st = _enqueue(stream, x, out, weight.packed)
     _check(load_library().msk_linear_fp4(x.data_ptr(), _DTYPES[x.dtype], _step(x, 0), weight.desc, T, out.data_ptr(),
-                                         _DTYPES[out.dtype], _step(out, 0), addr, size, st), "msk_linear_fp4")
+                                         _DTYPES[out.dtype], _step(out, 0), st), "msk_linear_fp4")
     return out
+
+
+def msk_ops_check(stream=None):
+    """Waits for the stream and raises MskError (timeout) if a bounded device
+    wait of the operators ran out since the last check."""
+    _check(load_library().msk_ops_check(_stream(stream)), "msk_ops_check")
 
 
 def msk_token_logprobs(logits, tokens=None, top=0, temperature=1.0, stream=None):

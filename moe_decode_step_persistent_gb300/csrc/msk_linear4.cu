@@ -1,191 +1,528 @@
 // Products of up to 16 rows of 16-bit activations with NVFP4 weights.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <mutex>
 
 #include "msk_internal.h"
 #include "msk_ops.cuh"
+#include "msk_tc.cuh"
 
 namespace msk {
 namespace {
 
-constexpr int kGroup = 256;      // columns a warp takes: 64 consecutive ones a lane
-constexpr int kMaxGroups = 16;   // groups (warps along the columns) of a pass
-constexpr int kTokStride = 20;   // words between tokens of a warp's partial sums (no bank is hit twice)
+constexpr int kGroup = 256;        // columns of a stage
+constexpr int kRows = 128;         // weight rows of a tile (the MMA's M)
+constexpr int kTeams = 4;          // take the stages in turn; 4 warps of 32 rows each
+constexpr int kDeqWarps = 4 * kTeams;
+constexpr int kThreads = 32 * (kDeqWarps + kTeams);  // ... and a warp a team that issues its MMAs
+constexpr int kABufs = 3;          // decoded operands of a team in tensor memory
+constexpr int kMaxStages = 2 * kTeams;  // kTeams or twice as many: a slot is a team's own, so that the team sees each of its phases
+// x in shared memory: for every 64 columns NG groups of 8 tokens x 128 bytes,
+// swizzled.
+template <int NG>
+constexpr int kXBytes = NG * 1024;
+constexpr int kChunks = kGroup / 64;  // decoded operands of a stage
+constexpr int kCodeBytes = kRows * kGroup / 2, kScaleBytes = kRows * kGroup / 16, kStageBytes = kCodeBytes + kScaleBytes;
+constexpr int kMaxKs = 8;          // blocks of a cluster along the columns
+constexpr int kSmem = 224 * 1024;  // (dynamic; 3 KB of the block's 227 are static or aligned away)
+constexpr int kPartBytes = 2 * 16 * kRows * 4;  // partial sums for the other blocks, two tiles
+// tensor memory columns: decoded operands, then two sets of accumulators
+constexpr int kACols = 32, kDCols = 16, kD0 = kTeams * kABufs * kACols;
+
+static __device__ uint32_t g_error;  // nonzero once a wait has run out
 
 struct Lin4 {
-  const uint16_t* x;
-  const uint8_t* codes;
+  CUtensorMap codes_map;   // [rows][cols / 2] bytes, boxes of 128 x 128
+  CUtensorMap scales_map;  // [rows][cols / 16] bytes, boxes of 128 x 16 (cols a multiple of 256)
+  CUtensorMap x_map;       // [cols / 64][tokens][64], boxes of 4 x 8 NG x 64
   const uint8_t* scales;
   void* y;
-  float* ws;  // [T][N] partial sums between passes
   long long x_stride, y_stride, N;
-  int K, T, y_dtype;
-  int groups, per_pass, passes;  // column groups, those of one pass, passes over the columns
-  int wr;                        // 16-row tiles side by side in a block
-  bool fp16, wide;               // codes aligned to 32 bytes
+  int K, T, y_dtype, groups, ks, stages;
+  bool fp16, scales_tma;
   float ts;
 };
 
-// A lane's share of 16 weight rows: 64 columns of rows g and g + 8.
-struct WTile {
-  uint32_t c[2][8];
-  uint32_t e[2];
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// Shared-memory descriptor bits of the 128-byte swizzle (16-byte piece p of
+// row r at p ^ (r mod 8)).
+constexpr uint64_t kSwizzle128 = 2ull << 61;
+
+// D (tensor memory) = [D +] A B^T, A fp16 from tensor memory, B from shared
+// memory, fp32 accumulators, M = 128, N = 16, K = 16.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, bool accumulate) {
+  constexpr uint32_t idesc = (1u << 4) | ((16u / 8) << 17) | ((128u / 16) << 24);
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+struct Bars {  // mbarriers of a block
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t afull[kTeams][kABufs], aempty[kTeams][kABufs];
+  uint64_t dfull[2], dempty[2];
+  uint64_t parts[2];     // the cluster's partial sums of a tile are written
+  uint64_t xfull;
+  uint64_t done[kTeams];  // an issuer's MMAs are complete
 };
 
-__device__ __forceinline__ void ld_codes(uint32_t (&w)[8], const uint8_t* p, bool wide) {
-  if (wide) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
-  } else {
-    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p + 16));
-  }
-}
-
-// (col: the lane's first column, or -1 past the matrix)
-__device__ __forceinline__ void ld_tile(WTile& t, const Lin4& a, long long row, int col) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const long long r = row + 8 * i;
-    if (col >= 0 && r < a.N) {
-      ld_codes(t.c[i], a.codes + r * (a.K / 2) + col / 2, a.wide);
-      asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(t.e[i]) : "l"(a.scales + r * (a.K / 16) + col / 16));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t.c[i][j] = 0;
-      t.e[i] = 0;
-    }
-  }
-}
-
-__device__ __forceinline__ void store_y(const Lin4& a, int t, long long n, float v) {
-  const long long i = t * a.y_stride + n;
-  if (a.y_dtype == MSK_FP32) static_cast<float*>(a.y)[i] = v;
-  else if (a.y_dtype == MSK_FP16) static_cast<__half*>(a.y)[i] = __float2half_rn(v);
-  else static_cast<__nv_bfloat16*>(a.y)[i] = __float2bfloat16_rn(v);
-}
-
-// Persistent blocks of up to 16 warps.  A warp keeps its 256 columns of x in
-// registers for the whole pass, as the MMA's B fragments (NT tiles of 8
-// tokens), and streams weight rows through its A fragments, 16 rows at a
-// time: decoded to fp16 in registers, exact, with one multiply by the block
-// scale for two weights.  Of x and W a lane takes the same 64 columns, so a
-// row's codes are one 32-byte load and its scales one 4-byte load, and
-// neither passes through shared memory.  The warps of a row tile add their
-// partial sums up in shared memory.
+// y^T = W x^T on the fifth-generation tensor cores: M = 128 weight rows, N =
+// 16 tokens, fp16 operands, fp32 accumulators.  The weights stream through
+// shared memory by tiled copies and are decoded, exactly, into the A operand
+// in tensor memory: a thread takes 64 columns of a row, a conversion and a
+// multiply by the block scale for two weights.  x lies in shared memory as
+// the B operand for the block's life.
 //
-// The next tile's loads are issued before the current one is computed: two
-// tiles of up to 36 KB in flight per SM are what DRAM's latency asks for.
-template <int NT>
-__global__ void __launch_bounds__(512, 1) linear4_kernel(const __grid_constant__ Lin4 a) {
-  constexpr int TOK = 8 * NT;
-  __shared__ float red[2][kMaxGroups][TOK * kTokStride];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int wk = warp % a.per_pass, tile = warp / a.per_pass;
-  const long long step = 16ll * a.wr * gridDim.x, first = 16ll * a.wr * blockIdx.x;
-  int buf = 0;
-  for (int pass = 0; pass < a.passes; ++pass) {
-    const int grp = pass * a.per_pass + wk;
-    int col = grp * kGroup + c * 64;
-    if (grp >= a.groups || col >= a.K) col = -1;
-    WTile cur;
-    ld_tile(cur, a, first + tile * 16 + g, col);
-    // x: scaled by a power of two for each (token, warp), then fp16
-    uint32_t xf[NT][32];
-    float back[NT][2];  // the scalings of this lane's accumulator columns, undone
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int t = nt * 8 + g;
-      const uint4* p = reinterpret_cast<const uint4*>(a.x + t * a.x_stride + (col < 0 ? 0 : col));
-      const bool in = t < a.T && col >= 0;
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (in) u = __ldg(p + i);
-        xf[nt][4 * i] = u.x, xf[nt][4 * i + 1] = u.y, xf[nt][4 * i + 2] = u.z, xf[nt][4 * i + 3] = u.w;
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 f = unpack16(xf[nt][i], a.fp16);
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      const int sh = row_shift(amax);
-      const float mul = exp2i(sh);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 f = unpack16(xf[nt][i], a.fp16);
-        xf[nt][i] = pack_f16x2(f.x * mul, f.y * mul);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) back[nt][i] = exp2i(-__shfl_sync(0xFFFFFFFFu, sh, (2 * c + i) * 4));
-    }
+// Roles: 16 decoding warps in four teams that take the stages in turn (a
+// thread has a row's 256 columns of a stage, 64 at a time) and for each team a
+// warp that issues its MMAs and refills the slots that it has read.
+// (One thread issues an MMA in 55 cycles, four threads one in 16 each; a
+// stage's bytes leave 49 for each of its 16.)  Everything between the roles is
+// an mbarrier; a team's sums lie in an accumulator of their own and are added
+// in the epilogue, which reads tile i while tile i + 1 is decoded.
+//
+// Bound by the decoding and DRAM alike: on mma.sync the decoding and the MMAs
+// together take longer than the bytes (16 tokens x 131072 x 4096: 88 us).
+//
+// With too few tiles for the GPU, or more columns than x has room for, a
+// cluster of `ks` blocks shares a tile's columns and adds its sums up through
+// distributed shared memory, in rank order.
+template <int NG>  // 8-token groups that x has room for
+__global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_constant__ Lin4 a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ Bars bars;
+  __shared__ uint32_t amaxs[16];  // each token's largest magnitude, as an fp32 number's bits
+  __shared__ float back[16];  // undoes each token's scaling
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort, never;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % a.ks, clusters = gridDim.x / a.ks, cluster = blockIdx.x / a.ks;
+  const int ga = (int)((long long)a.groups * rank / a.ks), gb = (int)((long long)a.groups * (rank + 1) / a.ks), ng = gb - ga;
+  const int tiles = (int)((a.N + kRows - 1) / kRows);
+  const int mine = cluster < tiles ? (tiles - cluster + clusters - 1) / clusters : 0;
+  const uint64_t deadline = gtimer() + kOpsWaitNs;
+  // (dynamic shared memory starts at a multiple of 1024 in the shared window)
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t ring = smem_u32(smem);
+  uint8_t* xs = smem + a.stages * kStageBytes;
+  float* parts = reinterpret_cast<float*>(xs + ((a.groups + a.ks - 1) / a.ks) * kChunks * kXBytes<NG>);  // [2][16][128], clusters only
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
-    for (long long r0 = first; r0 < a.N; r0 += step) {
-      WTile nxt;
-      ld_tile(nxt, a, r0 + step + tile * 16 + g, col);
-      float acc[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-      uint32_t sc[2][2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sc[i][0] = e4m3_pair_to_f16x2(cur.e[i], 0);
-        sc[i][1] = e4m3_pair_to_f16x2(cur.e[i], 1);
-      }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const uint32_t f0 = f16x2_bcast(sc[0][k >> 3], (k >> 2) & 1), f1 = f16x2_bcast(sc[1][k >> 3], (k >> 2) & 1);
-        const uint32_t af[4] = {hmul2(e2m1_byte_to_f16x2(cur.c[0][k >> 1], 2 * (k & 1)), f0),
-                                hmul2(e2m1_byte_to_f16x2(cur.c[1][k >> 1], 2 * (k & 1)), f1),
-                                hmul2(e2m1_byte_to_f16x2(cur.c[0][k >> 1], 2 * (k & 1) + 1), f0),
-                                hmul2(e2m1_byte_to_f16x2(cur.c[1][k >> 1], 2 * (k & 1) + 1), f1)};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], af, xf[nt][2 * k], xf[nt][2 * k + 1]);
-      }
-      float* part = red[buf][warp];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          part[(nt * 8 + 2 * c + i) * kTokStride + g] = acc[nt][i] * back[nt][i];
-          part[(nt * 8 + 2 * c + i) * kTokStride + g + 8] = acc[nt][2 + i] * back[nt][i];
-        }
-      __syncthreads();  // (the other buffer's readers are past it too)
-      for (int o = threadIdx.x; o < 16 * TOK * a.wr; o += blockDim.x) {
-        const int r = o & 15, t = (o >> 4) % TOK, rt = (o >> 4) / TOK;
-        const long long n = r0 + rt * 16 + r;
-        if (t >= a.T || n >= a.N) continue;
-        float s = 0.f;
-        for (int w = 0; w < a.per_pass; ++w) s += red[buf][rt * a.per_pass + w][t * kTokStride + r];
-        // (a later pass of the same thread takes the partial sum up again)
-        if (pass > 0) s += a.ws[t * a.N + n];
-        if (pass + 1 < a.passes) a.ws[t * a.N + n] = s;
-        else store_y(a, t, n, s * a.ts);
-      }
-      buf ^= 1;
-      cur = nxt;
+  if (tid == 0) {
+    abort = 0, never = 0;
+    for (int i = 0; i < a.stages; ++i) mbar_init(bar(bars.full[i]), 1), mbar_init(bar(bars.empty[i]), 4);
+    for (int t = 0; t < kTeams; ++t) {
+      for (int i = 0; i < kABufs; ++i) mbar_init(bar(bars.afull[t][i]), 4), mbar_init(bar(bars.aempty[t][i]), 1);
+      mbar_init(bar(bars.done[t]), 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(bars.dfull[i]), kTeams), mbar_init(bar(bars.dempty[i]), kDeqWarps);
+      mbar_init(bar(bars.parts[i]), kDeqWarps * a.ks);
+    }
+    mbar_init(bar(bars.xfull), 1);
+    mbar_fence_init();
   }
+  if (tid < 16) amaxs[tid] = 0;
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_base), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (a.ks > 1) cluster_sync();  // (the others' barriers are set up)
+  const uint32_t tmem = tmem_base;
+  const volatile int* ab = &abort;
+  auto wait = [&](uint64_t& b, uint32_t parity) {
+    if (mbar_wait(bar(b), parity, deadline, ab)) return true;
+    abort = 1;
+    return false;
+  };
+
+  auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
+
+  // --- copies ---------------------------------------------------------------
+  const int total = mine * ng;  // stages in all
+  auto load = [&](int st, int ti, int g) {
+    const uint32_t dst = ring + st * kStageBytes, b = bar(bars.full[st]);
+    const int row = (cluster + ti * clusters) * kRows;
+    mbar_arrive_expect_tx(b, a.scales_tma ? kStageBytes : kCodeBytes);
+    tma_load_2d(dst, &a.codes_map, (ga + g) * (kGroup / 2), row, b);
+    if (a.scales_tma) tma_load_2d(dst + kCodeBytes, &a.scales_map, (ga + g) * (kGroup / 16), row, b);
+  };
+  if (warp == kDeqWarps && lane == 0 && total > 0) {
+    // x first: behind the ring's copies it would wait for all of them
+    mbar_arrive_expect_tx(bar(bars.xfull), ng * kChunks * kXBytes<NG>);
+    for (int g = 0; g < ng; ++g)
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+              smem_u32(xs) + g * kChunks * kXBytes<NG>),
+          "l"(&a.x_map), "r"(0), "r"(0), "r"((ga + g) * kChunks), "r"(bar(bars.xfull))
+          : "memory");
+    for (int i = 0; i < min(total, a.stages); ++i) load(i, i / ng, i % ng);
+  }
+
+  // --- x in place: scaled by a power of two for each token, fp16 ---------------
+  if (warp < kDeqWarps && total > 0) {
+    wait_warp(bars.xfull, 0);
+    // items: 256 columns of a token, token by token; a warp takes a run of them
+    const int items = a.T * ng, per = (items + kDeqWarps - 1) / kDeqWarps, i1 = min(items, (warp + 1) * per);
+    auto piece = [&](int t, int g) {  // this lane's 8 columns
+      const int k8 = g * 32 + lane;
+      return reinterpret_cast<uint4*>(xs + (k8 >> 3) * kXBytes<NG> + t * 128 + (((k8 ^ t) & 7) << 4));
+    };
+    if (!a.fp16) {
+      for (int it = warp * per; it < i1;) {
+        const int t = it / ng, g0 = it - t * ng, n = min(ng - g0, i1 - it);
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          const uint4 v = *piece(t, g0 + j);
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(v.x & 0x7FFF7FFFu));
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(v.y & 0x7FFF7FFFu));
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(v.z & 0x7FFF7FFFu));
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(v.w & 0x7FFF7FFFu));
+        }
+        const uint32_t f = __float_as_uint(fmaxf(fmaxf(bf16_lo(m), bf16_hi(m)), 0.f));  // (a NaN does not count)
+        const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, f);
+        if (lane == 0) atomicMax(&amaxs[t], w);
+        it += n;
+      }
+      named_bar(1, 32 * kDeqWarps);
+      for (int it = warp * per; it < i1;) {
+        const int t = it / ng, g0 = it - t * ng, n = min(ng - g0, i1 - it);
+        const float mul = exp2i(row_shift(__uint_as_float(amaxs[t])));
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          uint4* p = piece(t, g0 + j);
+          const uint4 v = *p;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = pack_f16x2(bf16_lo(w[i]) * mul, bf16_hi(w[i]) * mul);
+          *p = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        it += n;
+      }
+      fence_proxy_async_shared();
+    }
+    if (tid < 16) back[tid] = a.fp16 ? 1.f : exp2i(-row_shift(__uint_as_float(amaxs[tid])));
+  }
+  __syncthreads();
+
+  if (warp < kDeqWarps) {
+    // --- decoding and epilogue ----------------------------------------------
+    const int team = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t tlane = tmem + ((uint32_t)(quad * 32) << 16);
+    // adds the teams' sums up for four tokens of this warp's rows and stores them
+    auto epilogue = [&](int i) {
+      const int d = i & 1;
+      if (!wait_warp(bars.dfull[d], (i >> 1) & 1)) return false;
+      tc_fence_after();
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < kTeams; ++t) {
+        if (((t - i * ng) & (kTeams - 1)) >= ng) continue;  // (this team had none of the tile's stages)
+        float v[4];
+        tmem_ld4(tlane + kD0 + (d * kTeams + t) * kDCols + team * 4, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] += v[j];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.dempty[d]));
+      const long long n0 = (long long)(cluster + (long long)i * clusters) * kRows;
+      auto store = [&](int t, long long n, float v) {
+        const long long o = t * a.y_stride + n;
+        if (a.y_dtype == MSK_FP32) static_cast<float*>(a.y)[o] = v;
+        else if (a.y_dtype == MSK_FP16) static_cast<__half*>(a.y)[o] = __float2half_rn(v);
+        else static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
+      };
+      if (a.ks == 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = team * 4 + j;
+          if (t < a.T && n0 + r < a.N) store(t, n0 + r, s[j] * back[t] * a.ts);
+        }
+        return true;
+      }
+      float* mypart = parts + d * 16 * kRows;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mypart[(team * 4 + j) * kRows + r] = s[j] * back[team * 4 + j];
+      __syncwarp();
+      // (a warp arrives for tile i + 1 only after it has read tile i, and the
+      // buffer is written again for tile i + 2)
+      if (lane < a.ks)
+        asm volatile("fence.acq_rel.cluster;\n\tmbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         mapa(bar(bars.parts[d]), lane))
+                     : "memory");
+      if (!wait_warp(bars.parts[d], (i >> 1) & 1)) return false;
+      asm volatile("fence.acq_rel.cluster;" ::: "memory");
+      for (int k = rank + warp * a.ks; k < 4 * a.T; k += kDeqWarps * a.ks) {  // (token, 32 rows)
+        const int t = k >> 2, rr = (k & 3) * 32 + lane;
+        const uint32_t at = smem_u32(parts + (d * 16 + t) * kRows + rr);
+        float f[kMaxKs], v = 0.f;
+#pragma unroll
+        for (int b = 0; b < kMaxKs; ++b) {
+          f[b] = 0.f;
+          if (b < a.ks) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f[b]) : "r"(mapa(at, b)) : "memory");
+        }
+#pragma unroll
+        for (int b = 0; b < kMaxKs; ++b) v += f[b];
+        if (n0 + rr < a.N) store(t, n0 + rr, v * a.ts);
+      }
+      return true;
+    };
+
+    int buf = 0, tile = 0, g = team, done = 0;  // (g: the team's next stage, counted from the tile's first one)
+    uint32_t aph = 1;                           // (a fresh barrier passes a wait for phase 1)
+    bool ok = true;
+    int st = team;
+    uint32_t ph = 0;
+    for (int n = team; n < total && ok; n += kTeams) {
+      for (; g >= ng; g -= ng) ++tile;
+      // a tile behind: its MMAs are over by now, and the next but one tile's
+      // wait for nothing else
+      while (ok && done + 1 < tile) ok = epilogue(done++);
+      uint4 e = make_uint4(0, 0, 0, 0);
+      if (!a.scales_tma) {
+        const long long row = (long long)(cluster + (long long)tile * clusters) * kRows + r;
+        const int col = (ga + g) * kGroup;
+        const uint2* p = reinterpret_cast<const uint2*>(a.scales + row * (a.K / 16) + col / 16);
+        if (row < a.N) {
+          const uint2 lo = __ldg(p);
+          e.x = lo.x, e.y = lo.y;
+          if (col + 128 < a.K) {
+            const uint2 hi = __ldg(p + 1);
+            e.z = hi.x, e.w = hi.y;
+          }
+        }
+      }
+      ok = ok && wait_warp(bars.full[st], ph);
+      if (!ok) break;
+      const uint32_t s = ring + st * kStageBytes;
+      uint4 c[8];  // this thread's row: 256 codes, piece p of 16 bytes at p ^ (row mod 8)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = lds128(s + r * 128 + ((j ^ (r & 7)) << 4));
+      if (a.scales_tma) e = lds128(s + kCodeBytes + r * 16);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.empty[st]));
+      const uint32_t es[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const uint32_t w[8] = {c[2 * k].x, c[2 * k].y, c[2 * k].z, c[2 * k].w, c[2 * k + 1].x, c[2 * k + 1].y, c[2 * k + 1].z, c[2 * k + 1].w};
+        uint32_t v[32];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t f = f16x2_bcast(e4m3_pair_to_f16x2(es[k], b >> 1), b & 1);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[b * 8 + j] = hmul2(e2m1_byte_to_f16x2(w[2 * b + (j >> 2)], j & 3), f);
+        }
+        ok = ok && wait_warp(bars.aempty[team][buf], aph);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_st32(tlane + (team * kABufs + buf) * kACols, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars.afull[team][buf]));
+        if (++buf == kABufs) buf = 0, aph ^= 1;
+      }
+      g += kTeams;
+      st += kTeams;
+      if (st >= a.stages) st = team, ph ^= 1;
+    }
+    while (ok && done < mine) ok = epilogue(done++);
+  } else if (lane == 0) {
+    // --- a team's MMAs, and the copies into the slots that it leaves ---------------
+    const int team = warp - kDeqWarps;
+    // (8 tokens: the MMA's second group of 8 reads the first one again)
+    const uint64_t b0 = umma_desc(smem_u32(xs), 16, NG == 2 ? 1024 : 0) | kSwizzle128;
+    int buf = 0, tile = 0, g = team, st = team;
+    int rt = (team + a.stages) / ng, rg = (team + a.stages) % ng;  // the stage that goes where the team's next one was
+    uint32_t ph = 0, sph = 0;
+    bool ok = wait(bars.dempty[0], 1), fresh = true;  // (fresh: the tile's sums start from nothing)
+    for (int n = team; n < total && ok; n += kTeams) {
+      for (; g >= ng && ok; g -= ng) {
+        tc_commit(bar(bars.dfull[tile & 1]));
+        ++tile, fresh = true;
+        ok = wait(bars.dempty[tile & 1], ((tile >> 1) & 1) ^ 1);
+      }
+      const uint32_t dt = tmem + kD0 + ((tile & 1) * kTeams + team) * kDCols;
+      uint64_t b = b0 + g * (kChunks * kXBytes<NG> >> 4);
+      for (int k = 0; k < kChunks && ok; ++k) {
+        ok = wait(bars.afull[team][buf], ph);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = tmem + (team * kABufs + buf) * kACols;
+        mma_f16_ts(dt, at, b, !fresh);
+        fresh = false;
+#pragma unroll
+        for (int j = 1; j < 4; ++j) mma_f16_ts(dt, at + j * 8, b + j * 2, true);
+        tc_commit(bar(bars.aempty[team][buf]));
+        b += kXBytes<NG> >> 4;
+        if (++buf == kABufs) buf = 0, ph ^= 1;
+        if (k == 0 && n + a.stages < total) {  // (the team has read the stage: its first operand is there)
+          ok = wait(bars.empty[st], sph);
+          if (ok) load(st, rt, rg);
+        }
+      }
+      g += kTeams;
+      st += kTeams;
+      if (st >= a.stages) st = team, sph ^= 1;
+      for (rg += kTeams; rg >= ng; rg -= ng) ++rt;
+    }
+    for (; tile < mine && ok; ++tile) {
+      if (tile > 0 && g < 0) ok = wait(bars.dempty[tile & 1], ((tile >> 1) & 1) ^ 1);
+      if (ok) tc_commit(bar(bars.dfull[tile & 1]));
+      g = -1;
+    }
+    // what is still in flight ends before the block does
+    tc_commit(bar(bars.done[team]));
+    mbar_wait(bar(bars.done[team]), 0, gtimer() + kOpsWaitNs, &never);
+    if (*ab && team == 0)  // (an error: a slot's newest copy may be a use ahead of what was waited for)
+      for (int k = 0; k < a.stages; ++k)
+        for (uint32_t q = 0; q < 2; ++q) mbar_wait(bar(bars.full[k]), q, gtimer() + kOpsWaitNs / 100, &never);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0 && abort) atomicExch(&g_error, 1u);
+  if (a.ks > 1) cluster_sync();  // (no block leaves while its sums may be read)
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// A row-major matrix of bytes or 16-bit words, `pitch` bytes between rows, in
+// boxes of box_rows x box_cols; what lies outside reads as zero.
+bool matrix_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, long long rows, long long cols, long long pitch,
+                int box_rows, int box_cols, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)pitch};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return encoder() != nullptr &&
+         encoder()(map, type, 2, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What the kernel's launches go by, looked up once a device: clusters of each
+// size that run at a time.
+struct Setup {
+  std::once_flag once;
+  bool ok = false;
+  int active[kMaxKs + 1] = {};
+};
+
+template <int NG>
+const Setup* setup() {
+  static Setup devices[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  Setup& s = devices[dev];
+  std::call_once(s.once, [&s] {
+    if (cudaFuncSetAttribute(linear4_kernel<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return;
+    for (int ks = 1; ks <= kMaxKs; ++ks) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute at[1];
+      cfg.gridDim = dim3((unsigned)ks), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = kSmem;
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = (unsigned)ks, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at, cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&s.active[ks], linear4_kernel<NG>, &cfg) != cudaSuccess || s.active[ks] < 1) return;
+    }
+    s.ok = true;
+  });
+  return s.ok ? &s : nullptr;
+}
+
+template <int NG>
+msk_status launch_linear(Lin4& a, const void* x, long long x_stride, cudaStream_t st) {
+  const Setup* su = setup<NG>();
+  if (su == nullptr) return MSK_ERR_CUDA;
+  // Blocks along the columns: as many as x's room asks for, and more while
+  // all of a wave's clusters still run at once (two stages or more a block).
+  const int room = (kSmem - 1024 - kPartBytes - kTeams * kStageBytes) / (kChunks * kXBytes<NG>);  // groups of a block
+  const int tiles = (int)((a.N + kRows - 1) / kRows);
+  a.ks = (a.groups + room - 1) / room;
+  while (a.ks < kMaxKs && tiles <= su->active[a.ks + 1] && a.groups >= 2 * (a.ks + 1)) ++a.ks;
+  const int per = (a.groups + a.ks - 1) / a.ks;
+  // x as [cols / 64][tokens][64]; a box is a stage's columns
+  const cuuint64_t xd[3] = {64, (cuuint64_t)a.T, (cuuint64_t)a.K / 64}, xp[2] = {(cuuint64_t)(a.T > 1 ? x_stride : a.K) * 2, 128};
+  const cuuint32_t xb[3] = {64, 8 * NG, kChunks}, es[3] = {1, 1, 1};
+  if (encoder()(&a.x_map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(x), xd, xp, xb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return MSK_ERR_CUDA;
+  const int xbytes = per * kChunks * kXBytes<NG>, pbytes = a.ks > 1 ? kPartBytes : 0;
+  a.stages = (kSmem - 1024 - pbytes - xbytes) / kStageBytes >= kMaxStages ? kMaxStages : kTeams;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(std::min(tiles, su->active[a.ks]) * a.ks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 1024 + a.stages * kStageBytes + xbytes + pbytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)a.ks, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear4_kernel<NG>, a) == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }
 
 }  // namespace
+
+cudaError_t linear4_error(uint32_t* e) {
+  cudaError_t r = cudaMemcpyFromSymbol(e, g_error, sizeof(*e));
+  const uint32_t zero = 0;
+  if (r == cudaSuccess && *e != 0) r = cudaMemcpyToSymbol(g_error, &zero, sizeof(zero));
+  return r;
+}
+
 }  // namespace msk
 
 using namespace msk;
 
-extern "C" size_t msk_linear_fp4_workspace(int32_t tokens, int64_t rows, int64_t cols) {
-  if (tokens <= 0 || rows <= 0 || cols <= kGroup * kMaxGroups) return 0;
-  return (size_t)tokens * (size_t)rows * 4;
-}
-
 extern "C" msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_stride, const msk_nvfp4_desc* w,
-                                     int32_t tokens, void* y, int32_t y_dtype, int64_t y_stride, void* workspace,
-                                     size_t workspace_bytes, void* stream) {
+                                     int32_t tokens, void* y, int32_t y_dtype, int64_t y_stride, void* stream) {
   if (w == nullptr || (x_dtype != MSK_BF16 && x_dtype != MSK_FP16) || !dtype_ok(y_dtype)) return MSK_ERR_INVALID_ARG;
-  if (tokens < 0 || tokens > kMaxT || w->rows < 0 || w->rows > (1ll << 31) || w->cols <= 0 || w->cols % 128 ||
+  if (tokens < 0 || tokens > kMaxT || w->rows < 0 || w->rows > (1ll << 31) - kRows || w->cols <= 0 || w->cols % 128 ||
       w->cols > 32768)
     return MSK_ERR_SHAPE;
   if (tokens == 0 || w->rows == 0) return MSK_OK;
@@ -194,29 +531,29 @@ extern "C" msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_s
   if (!ops_aligned16(x) || x_stride % 8 || !ops_aligned16(w->packed) || !ops_aligned16(w->scales) ||
       reinterpret_cast<uintptr_t>(y) % dtype_bytes(y_dtype))
     return MSK_ERR_ALIGNMENT;
-  if (!ops_aligned16(workspace)) return MSK_ERR_ALIGNMENT;
-  const size_t need = msk_linear_fp4_workspace(tokens, w->rows, w->cols);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MSK_ERR_INVALID_ARG;
   int nsm = 0;
   const msk_status s = ops_device(&nsm);
   if (s != MSK_OK) return s;
   Lin4 a{};
-  a.x = static_cast<const uint16_t*>(x), a.codes = w->packed, a.scales = w->scales, a.y = y;
-  a.x_stride = x_stride, a.y_stride = y_stride, a.N = w->rows, a.K = (int)w->cols, a.T = tokens;
+  a.scales = w->scales, a.y = y;
+  a.y_stride = y_stride, a.N = w->rows, a.K = (int)w->cols, a.T = tokens;
   a.y_dtype = y_dtype, a.fp16 = x_dtype == MSK_FP16, a.ts = w->tensor_scale;
-  a.ws = static_cast<float*>(workspace);
-  a.wide = reinterpret_cast<uintptr_t>(w->packed) % 32 == 0;
   a.groups = (a.K + kGroup - 1) / kGroup;
-  a.passes = (a.groups + kMaxGroups - 1) / kMaxGroups;
-  a.per_pass = (a.groups + a.passes - 1) / a.passes;
-  // row tiles side by side: as many as warps allow, fewer where that would
-  // leave SMs without rows
-  const long long tiles = (a.N + 15) / 16;
-  a.wr = (int)std::max<long long>(1, std::min<long long>(kMaxGroups / a.per_pass, tiles / nsm));
-  const unsigned grid = (unsigned)std::min<long long>(nsm, (tiles + a.wr - 1) / a.wr);
-  const unsigned threads = 32u * a.per_pass * a.wr;
+  // (a tiled copy's rows lie a multiple of 16 bytes apart: with an odd
+  // multiple of 128 columns the scales' do not, and are loaded one by one)
+  a.scales_tma = a.K % kGroup == 0;
+  const CUtensorMapDataType bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (!matrix_map(&a.codes_map, bytes, w->packed, a.N, a.K / 2, a.K / 2, kRows, kGroup / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (a.scales_tma && !matrix_map(&a.scales_map, bytes, w->scales, a.N, a.K / 16, a.K / 16, kRows, kGroup / 16,
+                                   CU_TENSOR_MAP_SWIZZLE_NONE)))
+    return MSK_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (tokens <= 8) linear4_kernel<1><<<grid, threads, 0, st>>>(a);
-  else linear4_kernel<2><<<grid, threads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
+  return tokens <= 8 ? launch_linear<1>(a, x, x_stride, st) : launch_linear<2>(a, x, x_stride, st);
+}
+
+extern "C" msk_status msk_ops_check(void* stream) {
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MSK_ERR_CUDA;
+  uint32_t e = 0;
+  if (linear4_error(&e) != cudaSuccess) return MSK_ERR_CUDA;
+  return e ? MSK_ERR_TIMEOUT : MSK_OK;
 }

@@ -26,6 +26,10 @@ inline msk_status ops_device(int* nsm) {
   return major == 10 && minor == 3 ? MSK_OK : MSK_ERR_UNSUPPORTED_DEVICE;
 }
 
+// Bound of every wait of these kernels; after it a kernel records an error
+// (msk_ops_check), ends its copies and MMAs, and returns.
+constexpr uint64_t kOpsWaitNs = 200ull * 1000 * 1000;
+
 // The SM count the workspace sizes are made for when there is no device to
 // ask; kernels never use more blocks than a workspace has room for.
 constexpr int kOpsSms = 152;

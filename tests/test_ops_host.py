@@ -84,14 +84,13 @@ def test_attention(M, lib, change, status):
     (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(packed=None), INVALID), (dict(scales=None), INVALID),
     (dict(xdt=FP32), INVALID), (dict(ydt=7), INVALID), (dict(xs=248), INVALID), (dict(ys=99), INVALID),
     (dict(x=P + 8), ALIGN), (dict(xs=260), ALIGN), (dict(packed=P + 8), ALIGN), (dict(scales=P + 1), ALIGN),
-    (dict(y=P + 1), ALIGN), (dict(ws=P + 8), ALIGN)])
+    (dict(y=P + 1), ALIGN)])
 def test_linear(M, lib, change, status):
-    a = dict(x=P, xdt=BF16, xs=256, packed=P, scales=P, rows=100, cols=256, tokens=4, y=P, ydt=BF16, ys=100, ws=P)
+    a = dict(x=P, xdt=BF16, xs=256, packed=P, scales=P, rows=100, cols=256, tokens=4, y=P, ydt=BF16, ys=100)
     a.update(change)
     w = ctypes.pointer(M.Nvfp4Desc(a["packed"], a["scales"], 1.0, a["rows"], a["cols"]))
-    assert lib.msk_linear_fp4(a["x"], a["xdt"], a["xs"], w, a["tokens"], a["y"], a["ydt"], a["ys"], a["ws"], 1 << 40,
-                              None) == status
-    assert lib.msk_linear_fp4(P, BF16, 256, None, 4, P, BF16, 100, P, 1 << 40, None) == INVALID
+    assert lib.msk_linear_fp4(a["x"], a["xdt"], a["xs"], w, a["tokens"], a["y"], a["ydt"], a["ys"], None) == status
+    assert lib.msk_linear_fp4(P, BF16, 256, None, 4, P, BF16, 100, None) == INVALID
 
 
 @pytest.mark.parametrize("change,status", [
