@@ -366,6 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
     int buf = 0, tile = 0, g = team, st = team;
     int rt = (team + a.stages) / ng, rg = (team + a.stages) % ng;  // the stage that goes where the team's next one was
     uint32_t ph = 0, sph = 0;
+    const uint32_t afull = bar(bars.afull[team][0]), aempty = bar(bars.aempty[team][0]);
+    const uint32_t at0 = tmem + team * kABufs * kACols;
     bool ok = wait(bars.dempty[0], 1), fresh = true;  // (fresh: the tile's sums start from nothing)
     for (int n = team; n < total && ok; n += kTeams) {
       for (; g >= ng && ok; g -= ng) {
@@ -373,25 +375,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
         ++tile, fresh = true;
         ok = wait(bars.dempty[tile & 1], ((tile >> 1) & 1) ^ 1);
       }
-      const uint32_t dt = tmem + kD0 + ((tile & 1) * kTeams + team) * kDCols;
-      uint64_t b = b0 + g * (kChunks * kXBytes<NG> >> 4);
-      for (int k = 0; k < kChunks && ok; ++k) {
-        ok = wait(bars.afull[team][buf], ph);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t at = tmem + (team * kABufs + buf) * kACols;
-        mma_f16_ts(dt, at, b, !fresh);
-        fresh = false;
-#pragma unroll
-        for (int j = 1; j < 4; ++j) mma_f16_ts(dt, at + j * 8, b + j * 2, true);
-        tc_commit(bar(bars.aempty[team][buf]));
-        b += kXBytes<NG> >> 4;
-        if (++buf == kABufs) buf = 0, ph ^= 1;
-        if (k == 0 && n + a.stages < total) {  // (the team has read the stage: its first operand is there)
-          ok = wait(bars.empty[st], sph);
-          if (ok) load(st, rt, rg);
-        }
+      if (ok && n + a.stages < total) {  // as soon as the team has read the stage: its next one
+        ok = wait(bars.empty[st], sph);
+        if (ok) load(st, rt, rg);
       }
+      if (!ok) break;
+      const uint32_t dt = tmem + kD0 + ((tile & 1) * kTeams + team) * kDCols;
+      const uint64_t b = b0 + g * (kChunks * kXBytes<NG> >> 4);
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        if (!mbar_try_wait(afull + buf * 8, ph) && !(ok = wait(bars.afull[team][buf], ph))) break;
+        tc_fence_after();
+        const uint32_t at = at0 + buf * kACols;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma_f16_ts(dt, at + j * 8, b + k * (kXBytes<NG> >> 4) + j * 2, k > 0 || j > 0 || !fresh);
+        tc_commit(aempty + buf * 8);
+        buf = buf == kABufs - 1 ? 0 : buf + 1;
+        ph ^= buf == 0;
+      }
+      fresh = false;
       g += kTeams;
       st += kTeams;
       if (st >= a.stages) st = team, sph ^= 1;
