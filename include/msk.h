@@ -388,8 +388,11 @@ msk_status msk_kv4_read(const msk_kv4_desc* cache, int32_t pos0, int32_t tokens,
  * Queries and softmax weights enter the products in fp16 (queries after an
  * exact scaling of each row by a power of two), keys and values without
  * rounding, sums are fp32.
- * workspace: msk_attention_kv4_workspace bytes, 16-byte aligned. */
-size_t msk_attention_kv4_workspace(int32_t tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
+ * workspace: at least msk_attention_kv4_workspace bytes (0 for few keys, when
+ * it may be NULL), 16-byte aligned; for a call with cache_len_dev the bytes for
+ * max_seq - tokens. */
+size_t msk_attention_kv4_workspace(int32_t tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                   int32_t window, int32_t cache_len);
 msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_stride, const msk_kv4_desc* cache,
                              int32_t tokens, int32_t n_q_heads, int32_t cache_len, const int32_t* cache_len_dev,
                              const int32_t* parents, int32_t window, float softmax_scale, void* out,

@@ -15,7 +15,6 @@ weights held in torch tensors.  The operators beside the step
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -123,7 +122,7 @@ def load_library(path: str = LIB_PATH):
     f32, size, kv4 = ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(Kv4Desc)
     L.msk_kv4_write.argtypes = [kv4, vp, vp, i32, i32, i64, i64, i32, vp, vp]
     L.msk_kv4_read.argtypes = [kv4, i32, i32, vp, vp, i32, i64, i64, vp]
-    L.msk_attention_kv4_workspace.argtypes = [i32, i32, i32, i32]
+    L.msk_attention_kv4_workspace.argtypes = [i32] * 6
     L.msk_attention_kv4.argtypes = [vp, i32, i64, kv4, i32, i32, i32, vp, ctypes.POINTER(i32), i32, f32, vp, vp,
                                     size, vp]
     L.msk_linear_fp4.argtypes = [vp, i32, i64, ctypes.POINTER(Nvfp4Desc), i32, vp, i32, i64, vp]
@@ -389,10 +388,9 @@ def msk_kv4_read(cache, pos0, tokens, dtype=torch.bfloat16, out=None, stream=Non
     return k, v
 
 
-@functools.lru_cache(maxsize=None)
-def msk_attention_kv4_workspace(tokens, n_q_heads, n_kv_heads, head_dim):
-    """Workspace bytes of msk_attention_kv4 for these sizes."""
-    return load_library().msk_attention_kv4_workspace(tokens, n_q_heads, n_kv_heads, head_dim)
+def msk_attention_kv4_workspace(tokens, n_q_heads, n_kv_heads, head_dim, window, cache_len):
+    """Workspace bytes of msk_attention_kv4 (0 for few keys)."""
+    return load_library().msk_attention_kv4_workspace(tokens, n_q_heads, n_kv_heads, head_dim, window, cache_len)
 
 
 def msk_attention_kv4(q, cache, cache_len, window=0, parents=None, softmax_scale=0.0, out=None, workspace=None,
@@ -411,7 +409,8 @@ def msk_attention_kv4(q, cache, cache_len, window=0, parents=None, softmax_scale
     _need(out.dtype == q.dtype and out.numel() == q.numel() and out.is_contiguous(),
           "out: contiguous [tokens][n_q_heads * head_dim] of q's type")
     host, dev = _position(cache_len)
-    ws, addr, size = _workspace(workspace, msk_attention_kv4_workspace(T, Hq, cache.n_kv_heads, d), stream)
+    need = msk_attention_kv4_workspace(T, Hq, cache.n_kv_heads, d, window, host if dev is None else cache.max_seq - T)
+    ws, addr, size = _workspace(workspace, need, stream)
     st = _enqueue(stream, q, out, cache.codes) if ws is None else _enqueue(stream, q, out, cache.codes, ws)
     _check(load_library().msk_attention_kv4(q.data_ptr(), _DTYPES[q.dtype], _step(q, 0), cache.desc, T, Hq, host, dev,
                                             None if parents is None else _positions(parents), int(window),

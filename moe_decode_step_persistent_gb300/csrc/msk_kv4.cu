@@ -178,7 +178,9 @@ msk_status rows_call(bool write, const msk_kv4_desc* c, const void* k, const voi
 // attention
 // ---------------------------------------------------------------------------
 
-constexpr int kMaxSplits = 64;  // key ranges per kv head
+constexpr int kMaxSplits = 64;    // key ranges of a kv head, each a block's, joined by a second kernel
+constexpr int kMaxCluster = 8;    // or, of few keys, the blocks of a cluster
+constexpr int kClusterKeys = 8192;
 
 struct Kv4Attn {
   const uint16_t* q;
@@ -186,10 +188,10 @@ struct Kv4Attn {
   const uint8_t* codes;
   const uint8_t* scales;
   const int32_t* len_dev;
-  float* o_part;    // [tiles][Hkv][splits][16][HD]
-  float2* ml_part;  // [tiles][Hkv][splits][16] (maximum in log2 units, sum)
+  float* o_part;    // [tiles][Hkv][splits][rows of a tile][HD]
+  float2* ml_part;  // [tiles][Hkv][splits][rows of a tile] (reference in log2 units, sum)
   long long q_stride;
-  int T, Hq, Hkv, G, max_seq, len, window, splits;
+  int T, Hq, Hkv, G, max_seq, len, window, splits, cluster;
   bool fp16;
   float qk_scale;  // softmax scale * k_scale * log2(e)
   float v_scale;
@@ -207,42 +209,115 @@ __device__ __forceinline__ bool sees(const Kv4Attn& a, int t, int j, int len) {
   return a.window == 0 || j > len + a.depth[t] - a.window;
 }
 
-// A warp takes 16 keys at a time for a tile of 16 query rows (row = token *
-// group + head of the group).  S = Q K^T and O = P V on mma.sync with K and V
-// decoded straight into its B fragments: no shared memory on the way.
-//  K: lane (g, c) of a fragment holds key g and, of each 16 dimensions, any
-//     four, as long as Q's fragments hold the same: it takes the HD / 4
-//     dimensions from c HD / 4 (16 bytes of codes at HD = 128), four a step.
-//  V: the fragment pairs two keys for one dimension; lane (g, c) holds four
-//     keys and takes the HD / 8 dimensions from g HD / 8.  Nibbles of two
-//     keys are put into one byte before the decoding, so a byte decodes to
-//     the pair.
-// Values are exact in fp16 (at most 6 significant bits, at most 2688).
-template <int HD>
-__global__ void __launch_bounds__(256) kv4_attention_kernel(const __grid_constant__ Kv4Attn a) {
-  constexpr int KS = HD / 16;   // steps of S's contraction
-  constexpr int NT = HD / 8;    // n tiles of O
-  constexpr int KW = HD / 32;   // code words of a lane's K piece
-  constexpr int VW = HD / 64;   // code words of a lane's V piece of one key
-  extern __shared__ float smem[];  // [8 warps][16][HD + 1], then [8][16] (m, l)
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int split = blockIdx.x, h = blockIdx.y, tile = blockIdx.z;
-  const int len = cached_len(a);
-  const int rows = a.T * a.G;
+__device__ __forceinline__ void store_out(const Kv4Attn& a, int hd, int h, int row, int d, float y) {
+  uint16_t* p = a.out + ((long long)(row / a.G) * a.Hq + h * a.G + row % a.G) * hd + d;
+  *p = a.fp16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+}
 
-  // this lane's query rows g and g + 8
-  uint32_t qf[KS][4];
-  float fac[2];
-  int tok[2];
+// 8 x 8 fp16 matrix across a warp (lane (g, c): row g, columns 2c and 2c + 1),
+// transposed.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// What a lane holds of 16 keys and their values.
+template <int HD>
+struct Kv16 {
+  static constexpr int KW = HD / 32, VW = HD / 64;  // code words of a key, of a value
+  uint32_t k[2][KW], ke[2], v[4][VW], ve[4];
+};
+
+template <int W>
+__device__ __forceinline__ void ld_words(uint32_t (&w)[W], const uint8_t* p) {
+  if (W == 4) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = u.x, w[1] = u.y, w[W - 2] = u.z, w[W - 1] = u.w;
+  } else if (W == 2) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = u.x, w[W - 1] = u.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  }
+}
+
+// Few query rows (8 NT of them in a tile; row = token * group + head of the
+// group): a warp takes 16 keys at a time, as the M of S^T = K Q^T and O^T =
+// V^T P^T, so that NT n-tiles hold all rows and a key is decoded once.  K and
+// V come from global memory straight into the A fragments, no shared memory on
+// the way:
+//  K: lane (g, c) holds keys g and g + 8 and, of each 16 dimensions, any four,
+//     as long as Q's fragments hold the same: it takes the HD / 4 dimensions
+//     from c HD / 4 (16 bytes of codes at HD = 128), four a step.
+//  V: the fragment pairs two keys for one dimension; the lane holds four keys
+//     and takes the HD / 8 dimensions from g HD / 8, two for each m-tile (one
+//     byte).  Nibbles of two keys are put into one byte before the decoding,
+//     so a byte decodes to the pair.
+//  P: S^T's accumulators, as fp16, are P^T's B fragments after one 8 x 8
+//     transposition each.
+// Values are exact in fp16 (at most 6 significant bits, at most 2688).
+//
+// The softmax's reference is raised only when a score passes it by 2^8: weights
+// reach 256 (of fp16's 65504), and the sums are rescaled a few times in all.
+//
+// Two steps' loads are in flight for each warp.  Bound by the decoding (a
+// conversion and a multiply for two elements) and DRAM.
+template <int HD, int NT>
+__global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __grid_constant__ Kv4Attn a) {
+  constexpr int KS = HD / 16, MT = HD / 16, ROWS = 8 * NT, PITCH = HD + 4;
+  extern __shared__ __align__(16) float smem[];  // [8 warps][ROWS][PITCH], then [8][ROWS] (reference, sum)
+  float2* sml = reinterpret_cast<float2*>(smem + 8 * ROWS * PITCH);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int split = blockIdx.x, h = blockIdx.y, tile = blockIdx.z;
+  const int len = cached_len(a), rows = a.T * a.G;
+
+  // this block's keys: in steps of 16 handed round the warps
+  const int n = len + a.T;
+  const int lo = a.window > 0 ? max(0, len - a.window + 1) : 0, first = lo & ~15;  // (no query sees a key before lo)
+  const int steps = (n - first + 15) / 16;
+  const int per = (steps + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int s0 = split * per, s1 = min(steps, s0 + per);
+  const uint8_t* kc = a.codes + (long long)h * a.max_seq * (HD / 2) + c * (HD / 8);
+  const uint8_t* ks = a.scales + (long long)h * a.max_seq * (HD / 16) + c * (HD / 64);
+  const uint8_t* vc = a.codes + (long long)(a.Hkv + h) * a.max_seq * (HD / 2) + g * (HD / 16);
+  const uint8_t* vs = a.scales + (long long)(a.Hkv + h) * a.max_seq * (HD / 16) + g * (HD / 8) / 16;
+  auto load = [&](Kv16<HD>& t, int s) {
+    if (s >= s1) return;
+    const int j0 = first + s * 16;
+    const bool whole = j0 >= lo && j0 + 16 <= n;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = tile * 16 + g + 8 * i;
-    tok[i] = row < rows ? row / a.G : -1;
+    for (int i = 0; i < 2; ++i) {
+      int j = j0 + g + 8 * i;
+      if (!whole) j = min(j, n - 1);
+      ld_words(t.k[i], kc + (long long)j * (HD / 2));
+      if (HD == 128) t.ke[i] = __ldg(reinterpret_cast<const uint16_t*>(ks + (long long)j * (HD / 16)));
+      else t.ke[i] = __ldg(ks + (long long)j * (HD / 16));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int jj = j0 + (i >> 1) * 8 + 2 * c + (i & 1), j = whole ? jj : min(jj, n - 1);
+      ld_words(t.v[i], vc + (long long)j * (HD / 2));
+      t.ve[i] = __ldg(vs + (long long)j * (HD / 16));
+      if (!whole && (jj < lo || jj >= n)) t.ve[i] = 0;  // (such rows may hold anything, NaN scales too)
+    }
+  };
+  Kv16<HD> t0, t1;
+  load(t0, s0 + warp);
+  load(t1, s0 + warp + 8);
+
+  // Q: lane (g, c) of n-tile nt holds row 8 nt + g
+  uint32_t qf[NT][KS][2];
+  float fac[NT][2];
+  int tok[NT][2];  // the tokens of this lane's accumulator columns, -1 past the last row
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = tile * ROWS + nt * 8 + g;
     uint32_t w[HD / 8];
 #pragma unroll
     for (int j = 0; j < HD / 8; ++j) w[j] = 0;
-    if (tok[i] >= 0) {
-      const uint16_t* p = a.q + tok[i] * a.q_stride + (long long)(h * a.G + row % a.G) * HD + c * (HD / 4);
+    if (row < rows) {
+      const uint16_t* p = a.q + (row / a.G) * a.q_stride + (long long)(h * a.G + row % a.G) * HD + c * (HD / 4);
 #pragma unroll
       for (int j = 0; j < HD / 32; ++j) {
         const uint4 u = *reinterpret_cast<const uint4*>(p + 8 * j);
@@ -259,174 +334,263 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(const __grid_constan
     amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
     const int sh = row_shift(amax);
     const float mul = exp2i(sh);
-    fac[i] = a.qk_scale * exp2i(-sh);
 #pragma unroll
-    for (int j = 0; j < KS; ++j) {
-      const float2 lo = unpack16(w[2 * j], a.fp16), hi = unpack16(w[2 * j + 1], a.fp16);
-      qf[j][i] = pack_f16x2(lo.x * mul, lo.y * mul);
-      qf[j][i + 2] = pack_f16x2(hi.x * mul, hi.y * mul);
-    }
-  }
-
-  // this block's keys: [lo, hi), in steps of 16 handed round the warps
-  const int n = len + a.T;
-  const int lo = a.window > 0 ? max(0, len - a.window + 1) : 0, first = lo & ~15;  // (no query sees a key before lo)
-  const int steps = (n - first + 15) / 16;
-  const int per = (steps + a.splits - 1) / a.splits;
-  const int s0 = split * per, s1 = min(steps, s0 + per);
-  const uint8_t* kc = a.codes + (long long)h * a.max_seq * (HD / 2);
-  const uint8_t* ks = a.scales + (long long)h * a.max_seq * (HD / 16);
-  const uint8_t* vc = kc + (long long)a.Hkv * a.max_seq * (HD / 2);
-  const uint8_t* vs = ks + (long long)a.Hkv * a.max_seq * (HD / 16);
-
-  float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int j = 0; j < KS; ++j)
 #pragma unroll
-  for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-
-  for (int s = s0 + warp; s < s1; s += 8) {
-    const int j0 = first + s * 16;
-    float sc[2][4];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const long long j = min(j0 + nt * 8 + g, n - 1);
-      uint32_t w[KW], e;
-      if (KW == 4) {
-        const uint4 u = *reinterpret_cast<const uint4*>(kc + j * (HD / 2) + c * 16);
-        w[0] = u.x, w[1] = u.y, w[KW - 2] = u.z, w[KW - 1] = u.w;
-        e = *reinterpret_cast<const uint16_t*>(ks + j * (HD / 16) + c * 2);
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(kc + j * (HD / 2) + c * 8);
-        w[0] = u.x, w[1] = u.y;
-        e = ks[j * (HD / 16) + c];
+      for (int i = 0; i < 2; ++i) {
+        const float2 f = unpack16(w[2 * j + i], a.fp16);
+        qf[nt][j][i] = pack_f16x2(f.x * mul, f.y * mul);
       }
-      const uint32_t ef = e4m3x2_to_f16x2(e);
-      sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint32_t f = f16x2_bcast(ef, k >= 4);
-        mma_f16(sc[nt], qf[k], hmul2(e2m1_byte_to_f16x2(w[k >> 1], 2 * (k & 1)), f),
-                hmul2(e2m1_byte_to_f16x2(w[k >> 1], 2 * (k & 1) + 1), f));
-      }
-    }
-    // scores in log2 units, masked
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = j0 + nt * 8 + 2 * c + (i & 1), t = tok[i >> 1];
-        sc[nt][i] = t >= 0 && sees(a, t, j, len) ? sc[nt][i] * fac[i >> 1] : -INFINITY;
-      }
-    uint32_t pa[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float mx = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      const float mn = fmaxf(m[i], mx);
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      const float al = exp2f(m[i] - ref);
-      m[i] = mn;
+      fac[nt][i] = a.qk_scale * exp2i(-__shfl_sync(0xFFFFFFFFu, sh, (2 * c + i) * 4));
+      const int r = tile * ROWS + nt * 8 + 2 * c + i;
+      tok[nt][i] = r < rows ? r / a.G : -1;
+    }
+  }
+  // keys that every query sees: [seen, len)
+  const int deepest = a.T - 1;
+  const int seen = a.window > 0 ? max(0, len + deepest - a.window + 1) : 0;
+
+  float o[MT][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+  }
+
+  auto step = [&](const Kv16<HD>& t, int s) {
+    const int j0 = first + s * 16;
+    float sc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+    const uint32_t e0 = e4m3x2_to_f16x2(t.ke[0]), e1 = e4m3x2_to_f16x2(t.ke[1]);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const uint32_t f0 = f16x2_bcast(e0, k >= 4), f1 = f16x2_bcast(e1, k >= 4);
+      const uint32_t af[4] = {hmul2(e2m1_byte_to_f16x2(t.k[0][k >> 1], 2 * (k & 1)), f0),
+                              hmul2(e2m1_byte_to_f16x2(t.k[1][k >> 1], 2 * (k & 1)), f1),
+                              hmul2(e2m1_byte_to_f16x2(t.k[0][k >> 1], 2 * (k & 1) + 1), f0),
+                              hmul2(e2m1_byte_to_f16x2(t.k[1][k >> 1], 2 * (k & 1) + 1), f1)};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], af, qf[nt][k][0], qf[nt][k][1]);
+    }
+    // scores in log2 units; (key g, rows 2c, 2c + 1), (key g + 8, the same)
+    const bool whole = j0 >= seen && j0 + 16 <= len;
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x = sc[nt][i] * fac[nt][i & 1];
+        if (!whole) {
+          const int tk = tok[nt][i & 1];
+          x = tk >= 0 && sees(a, tk, j0 + g + 8 * (i >> 1), len) ? x : -INFINITY;
+        }
+        sc[nt][i] = x;
+        raise |= x > m[nt][i & 1] + 8.f;  // (-inf + 8 is -inf: the first visible score raises)
+      }
+    if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float mx = fmaxf(sc[nt][i], sc[nt][i + 2]);
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
+          mx = fmaxf(m[nt][i], mx);
+          const float al = mx == -INFINITY ? 1.f : exp2f(m[nt][i] - mx);
+          m[nt][i] = mx;
+          l[nt][i] *= al;
+#pragma unroll
+          for (int k = 0; k < MT; ++k) o[k][nt][i] *= al, o[k][nt][i + 2] *= al;
+        }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       float p[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) p[k] = exp2f(sc[k >> 1][2 * i + (k & 1)] - ref);
-      l[i] = l[i] * al + (p[0] + p[1]) + (p[2] + p[3]);
-      pa[i] = pack_f16x2(p[0], p[1]);
-      pa[i + 2] = pack_f16x2(p[2], p[3]);
-#pragma unroll
-      for (int k = 0; k < NT; ++k) o[k][2 * i] *= al, o[k][2 * i + 1] *= al;
-    }
-    // O += P V
-    uint32_t vw[4][VW], ve[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int jj = j0 + (k >> 1) * 8 + 2 * c + (k & 1);
-      const long long j = min(jj, n - 1);
-      if (VW == 2) {
-        const uint2 u = *reinterpret_cast<const uint2*>(vc + j * (HD / 2) + g * 8);
-        vw[k][0] = u.x, vw[k][VW - 1] = u.y;
-      } else {
-        vw[k][0] = *reinterpret_cast<const uint32_t*>(vc + j * (HD / 2) + g * 4);
+      for (int i = 0; i < 4; ++i) {
+        const float ref = m[nt][i & 1];
+        p[i] = exp2f(sc[nt][i] - (ref == -INFINITY ? 0.f : ref));
       }
-      ve[k] = jj >= lo && jj < n ? vs[j * (HD / 16) + (g * NT) / 16] : 0u;  // (rows outside may hold anything)
+      l[nt][0] += p[0] + p[2], l[nt][1] += p[1] + p[3];
+      pb[nt][0] = movmatrix_trans(pack_f16x2(p[0], p[1]));
+      pb[nt][1] = movmatrix_trans(pack_f16x2(p[2], p[3]));
     }
-    const uint32_t e0 = e4m3x2_to_f16x2(ve[0] | ve[1] << 8), e1 = e4m3x2_to_f16x2(ve[2] | ve[3] << 8);
+    const uint32_t v0 = e4m3x2_to_f16x2(t.ve[0] | t.ve[1] << 8), v1 = e4m3x2_to_f16x2(t.ve[2] | t.ve[3] << 8);
 #pragma unroll
-    for (int w = 0; w < VW; ++w) {
-      const uint32_t M = 0x0F0F0F0Fu;
-      const uint32_t a0 = (vw[0][w] & M) | ((vw[1][w] & M) << 4), a1 = ((vw[0][w] >> 4) & M) | (vw[1][w] & ~M);
-      const uint32_t b0 = (vw[2][w] & M) | ((vw[3][w] & M) << 4), b1 = ((vw[2][w] >> 4) & M) | (vw[3][w] & ~M);
+    for (int w = 0; w < Kv16<HD>::VW; ++w) {
+      constexpr uint32_t M = 0x0F0F0F0Fu;
+      const uint32_t a0 = (t.v[0][w] & M) | ((t.v[1][w] & M) << 4), a1 = ((t.v[0][w] >> 4) & M) | (t.v[1][w] & ~M);
+      const uint32_t b0 = (t.v[2][w] & M) | ((t.v[3][w] & M) << 4), b1 = ((t.v[2][w] >> 4) & M) | (t.v[3][w] & ~M);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        mma_f16(o[w * 8 + 2 * k], pa, hmul2(e2m1_byte_to_f16x2(a0, k), e0), hmul2(e2m1_byte_to_f16x2(b0, k), e1));
-        mma_f16(o[w * 8 + 2 * k + 1], pa, hmul2(e2m1_byte_to_f16x2(a1, k), e0), hmul2(e2m1_byte_to_f16x2(b1, k), e1));
+        const uint32_t af[4] = {hmul2(e2m1_byte_to_f16x2(a0, k), v0), hmul2(e2m1_byte_to_f16x2(a1, k), v0),
+                                hmul2(e2m1_byte_to_f16x2(b0, k), v1), hmul2(e2m1_byte_to_f16x2(b1, k), v1)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(o[w * 4 + k][nt], af, pb[nt][0], pb[nt][1]);
       }
     }
+  };
+  for (int s = s0 + warp; s < s1; s += 16) {
+    step(t0, s);
+    load(t0, s + 16);
+    if (s + 8 < s1) step(t1, s + 8);
+    load(t1, s + 24);
   }
 
-  // merge the warps
-  float* so = smem;                                              // [8][16][HD + 1]
-  float2* sml = reinterpret_cast<float2*>(smem + 8 * 16 * (HD + 1));  // [8][16]
+  // the warps' sums to shared memory
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-    const int r = g + 8 * i;
-    if (c == 0) sml[warp * 16 + r] = make_float2(m[i], l[i]);
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int k = 0; k < NT; ++k) {
-      so[(warp * 16 + r) * (HD + 1) + 2 * c * NT + k] = o[k][2 * i];
-      so[(warp * 16 + r) * (HD + 1) + (2 * c + 1) * NT + k] = o[k][2 * i + 1];
+    for (int i = 0; i < 2; ++i) {
+      float s = l[nt][i];
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
+      const int r = nt * 8 + 2 * c + i;
+      if (g == 0) sml[warp * ROWS + r] = make_float2(m[nt][i], s);
+#pragma unroll
+      for (int k = 0; k < MT; ++k)
+        *reinterpret_cast<float2*>(smem + (warp * ROWS + r) * PITCH + g * (HD / 8) + 2 * k) =
+            make_float2(o[k][nt][i], o[k][nt][i + 2]);
+    }
+  __syncthreads();
+  // joined, an element a thread; the first warp's place takes the sum
+  for (int e = tid; e < ROWS * HD; e += 256) {
+    const int r = e / HD, d = e % HD;
+    float mm = -INFINITY, sum = 0.f, ll = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) mm = fmaxf(mm, sml[w * ROWS + r].x);
+    const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const float2 ml = sml[w * ROWS + r];
+      const float f = exp2f(ml.x - ref);
+      sum += f * smem[(w * ROWS + r) * PITCH + d];
+      ll += f * ml.y;
+    }
+    const int row = tile * ROWS + r;
+    if (a.splits > 1) {
+      if (row < rows) {
+        const long long part = (((long long)tile * a.Hkv + h) * a.splits + split) * ROWS + r;
+        a.o_part[part * HD + d] = sum;
+        if (d == 0) a.ml_part[part] = make_float2(mm, ll);
+      }
+    } else if (a.cluster == 1) {
+      if (row < rows) store_out(a, HD, h, row, d, sum / ll * a.v_scale);
+    } else {
+      smem[r * PITCH + d] = sum;  // (this thread's own element)
+      if (d == 0) smem[r * PITCH + HD] = mm, smem[r * PITCH + HD + 1] = ll;
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 16 * HD; i += 256) {
-    const int r = i / HD, d = i % HD, row = tile * 16 + r;
-    if (row >= rows) break;
-    float mm = -INFINITY;
-    for (int w = 0; w < 8; ++w) mm = fmaxf(mm, sml[w * 16 + r].x);
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    float sum = 0.f, ll = 0.f;
-    for (int w = 0; w < 8; ++w) {
-      const float f = exp2f(sml[w * 16 + r].x - ref);
-      sum += f * so[(w * 16 + r) * (HD + 1) + d];
-      ll += f * sml[w * 16 + r].y;
+  if (a.cluster > 1) {  // the blocks of a head, through the cluster's shared memory
+    cluster_sync();
+    for (int e = split * 256 + tid; e < ROWS * HD; e += a.cluster * 256) {
+      const int r = e / HD, d = e % HD, row = tile * ROWS + r;
+      if (row >= rows) break;
+      const uint32_t at = smem_u32(smem + r * PITCH);
+      float ms[kMaxCluster], mm = -INFINITY, sum = 0.f, ll = 0.f;
+#pragma unroll
+      for (int b = 0; b < kMaxCluster; ++b) {
+        ms[b] = b < a.cluster ? ld_cluster(mapa(at + HD * 4, b)) : -INFINITY;
+        mm = fmaxf(mm, ms[b]);
+      }
+#pragma unroll
+      for (int b = 0; b < kMaxCluster; ++b)
+        if (b < a.cluster) {
+          const float f = exp2f(ms[b] - mm);
+          sum += f * ld_cluster(mapa(at + d * 4, b));
+          ll += f * ld_cluster(mapa(at + HD * 4 + 4, b));
+        }
+      store_out(a, HD, h, row, d, sum / ll * a.v_scale);
     }
-    const long long part = (((long long)tile * a.Hkv + h) * a.splits + split) * 16 + r;
-    a.o_part[part * HD + d] = sum;
-    if (d == 0) a.ml_part[part] = make_float2(mm, ll);
+    cluster_sync();  // (no block leaves while its sums may be read)
   }
 }
 
-// One block per (token, query head), HD threads.
+// The key ranges of a (token, query head): one block, HD threads.
 template <int HD>
-__global__ void __launch_bounds__(HD) kv4_combine_kernel(const __grid_constant__ Kv4Attn a) {
-  const int t = blockIdx.x, hq = blockIdx.y, d = threadIdx.x;
-  const int h = hq / a.G, row = t * a.G + hq % a.G;
-  const long long base = ((long long)(row >> 4) * a.Hkv + h) * a.splits * 16 + (row & 15);
+__global__ void __launch_bounds__(HD) kv4_combine_kernel(const __grid_constant__ Kv4Attn a, int tile_rows) {
+  grid_dep_wait();
+  const int row = blockIdx.x, h = blockIdx.y, d = threadIdx.x;
+  const long long base = ((long long)(row / tile_rows) * a.Hkv + h) * a.splits * tile_rows + row % tile_rows;
   float mm = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, a.ml_part[base + s * 16].x);
+  for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, a.ml_part[base + s * tile_rows].x);
   float sum = 0.f, ll = 0.f;
   for (int s = 0; s < a.splits; ++s) {
-    const float2 ml = a.ml_part[base + s * 16];
+    const float2 ml = a.ml_part[base + s * tile_rows];
+    if (ml.y == 0.f) continue;  // (a range without a visible key)
     const float f = exp2f(ml.x - mm);
-    sum += f * a.o_part[(base + s * 16) * HD + d];
+    sum += f * a.o_part[(base + s * tile_rows) * HD + d];
     ll += f * ml.y;
   }
-  const float y = sum / ll * a.v_scale;
-  uint16_t* p = a.out + (long long)t * a.Hq * HD + (long long)hq * HD + d;
-  *p = a.fp16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+  store_out(a, HD, h, row, d, sum / ll * a.v_scale);
 }
 
-int attention_splits(int tiles, int Hkv) { return std::max(1, std::min(kMaxSplits, 2 * kOpsSms / (tiles * Hkv))); }
+// How a call is laid out.  `keys`: the most keys that a head may have to read.
+struct Kv4Plan {
+  int tile_rows, tiles, cluster, splits;
+};
+Kv4Plan plan_attention(int tokens, int group, int Hkv, int keys) {
+  Kv4Plan p{};
+  const int rows = tokens * group;
+  p.tile_rows = rows <= 8 ? 8 : 16;
+  p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
+  p.cluster = p.splits = 1;
+  if (keys <= kClusterKeys) {
+    // a block for every 128 keys (16 a warp)
+    while (p.cluster < kMaxCluster && keys > 128 * p.cluster) p.cluster *= 2;
+  } else {
+    const int per_sm = p.tile_rows == 8 ? 2 : 1;  // blocks that an SM holds
+    p.splits = std::max(2, std::min(kMaxSplits, per_sm * kOpsSms / (p.tiles * Hkv)));
+  }
+  return p;
+}
+size_t plan_bytes(const Kv4Plan& p, int Hkv, int hd) {
+  return p.splits == 1 ? 0 : (size_t)p.tiles * Hkv * p.splits * p.tile_rows * (hd + 2) * 4;
+}
+int most_keys(int tokens, int window, int len) { return std::min(len, window > 0 ? window + tokens : len) + tokens; }
+
+template <int HD, int NT>
+cudaError_t launch_rows_kernel(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st) {
+  constexpr int smem = 8 * 8 * NT * (HD + 4) * 4 + 8 * 8 * NT * 8;
+  static bool ready[64] = {};  // (a function's attributes are set once a device; twice does no harm)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev]) {
+    e = cudaFuncSetAttribute(kv4_rows_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3((unsigned)(p.cluster * p.splits), (unsigned)a.Hkv, (unsigned)p.tiles);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.cluster, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_rows_kernel<HD, NT>, a);
+}
 
 template <int HD>
-cudaError_t launch_attention(const Kv4Attn& a, int tiles, cudaStream_t st) {
-  const int smem = 8 * 16 * (HD + 1) * 4 + 8 * 16 * 8;
-  cudaError_t e = cudaFuncSetAttribute(kv4_attention_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kv4_attention_kernel<HD><<<dim3(a.splits, a.Hkv, tiles), 256, smem, st>>>(a);
-  kv4_combine_kernel<HD><<<dim3(a.T, a.Hq), HD, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_attention(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st) {
+  cudaError_t e = p.tile_rows == 8 ? launch_rows_kernel<HD, 1>(a, p, st) : launch_rows_kernel<HD, 2>(a, p, st);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3((unsigned)(a.T * a.G), (unsigned)a.Hkv);
+  cfg.blockDim = dim3(HD);
+  cfg.stream = st;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<HD>, a, p.tile_rows);
 }
 
 }  // namespace
@@ -445,10 +609,13 @@ extern "C" msk_status msk_kv4_read(const msk_kv4_desc* cache, int32_t pos0, int3
   return rows_call(false, cache, k, v, dtype, tokens, token_stride, head_stride, pos0, nullptr, stream);
 }
 
-extern "C" size_t msk_attention_kv4_workspace(int32_t tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim) {
-  if (tokens <= 0 || tokens > kMaxT || n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads || head_dim <= 0) return 0;
-  const int tiles = (tokens * (n_q_heads / n_kv_heads) + 15) / 16;
-  return (size_t)tiles * n_kv_heads * attention_splits(tiles, n_kv_heads) * 16 * (head_dim + 2) * 4;
+extern "C" size_t msk_attention_kv4_workspace(int32_t tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                              int32_t window, int32_t cache_len) {
+  if (tokens <= 0 || tokens > kMaxT || n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads || head_dim <= 0 ||
+      window < 0 || cache_len < 0)
+    return 0;
+  return plan_bytes(plan_attention(tokens, n_q_heads / n_kv_heads, n_kv_heads, most_keys(tokens, window, cache_len)),
+                    n_kv_heads, head_dim);
 }
 
 extern "C" msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_stride, const msk_kv4_desc* cache,
@@ -461,8 +628,8 @@ extern "C" msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_
   if (q == nullptr || out == nullptr) return MSK_ERR_INVALID_ARG;
   if (dtype != MSK_BF16 && dtype != MSK_FP16) return MSK_ERR_INVALID_ARG;
   if (tokens <= 0 || tokens > kMaxT || n_q_heads <= 0 || n_q_heads % cache->n_kv_heads) return MSK_ERR_SHAPE;
-  const int G = n_q_heads / cache->n_kv_heads, tiles = (tokens * G + 15) / 16;
-  if (cache->n_kv_heads > 65535 || tiles > 65535 || n_q_heads > 65535) return MSK_ERR_SHAPE;  // (grid limits)
+  const int G = n_q_heads / cache->n_kv_heads;
+  if (cache->n_kv_heads > 65535 || G > 32768) return MSK_ERR_SHAPE;  // (grid limits)
   if (window < 0 || tokens > cache->max_seq) return MSK_ERR_INVALID_ARG;
   if (cache_len_dev == nullptr && (cache_len < 0 || cache_len > cache->max_seq - tokens)) return MSK_ERR_INVALID_ARG;
   if (!(softmax_scale >= 0.f && softmax_scale <= 3e38f)) return MSK_ERR_INVALID_ARG;
@@ -470,9 +637,12 @@ extern "C" msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_
   if (!ops_aligned16(q) || !ops_aligned16(out) || !ops_aligned16(workspace) || q_stride % 8) return MSK_ERR_ALIGNMENT;
   Kv4Attn a{};
   if (!tree_masks(parents, tokens, window, a.depth, a.vis)) return MSK_ERR_INVALID_ARG;
-  if (workspace == nullptr ||
-      workspace_bytes < msk_attention_kv4_workspace(tokens, n_q_heads, cache->n_kv_heads, cache->head_dim))
-    return MSK_ERR_INVALID_ARG;
+  // (a cache of few rows is laid out by its size, whatever its length now)
+  int keys = most_keys(tokens, window, cache->max_seq - tokens);
+  if (cache_len_dev == nullptr && keys > kClusterKeys) keys = most_keys(tokens, window, cache_len);
+  const Kv4Plan plan = plan_attention(tokens, G, cache->n_kv_heads, keys);
+  const size_t need = plan_bytes(plan, cache->n_kv_heads, cache->head_dim);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MSK_ERR_INVALID_ARG;
   int nsm = 0;
   s = ops_device(&nsm);
   if (s != MSK_OK) return s;
@@ -484,15 +654,15 @@ extern "C" msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_
   a.q_stride = q_stride;
   a.T = tokens, a.Hq = n_q_heads, a.Hkv = cache->n_kv_heads, a.G = G;
   a.max_seq = cache->max_seq, a.len = cache_len, a.window = window;
-  a.splits = attention_splits(tiles, a.Hkv);
+  a.splits = plan.splits, a.cluster = plan.cluster;
   a.fp16 = dtype == MSK_FP16;
   const float scale = softmax_scale > 0.f ? softmax_scale : (float)(1.0 / std::sqrt((double)cache->head_dim));
   a.qk_scale = scale * cache->k_scale * 1.4426950408889634f;
   a.v_scale = cache->v_scale;
-  const size_t parts = (size_t)tiles * a.Hkv * a.splits * 16;
+  const size_t parts = (size_t)plan.tiles * a.Hkv * a.splits * plan.tile_rows;
   a.o_part = static_cast<float*>(workspace);
   a.ml_part = reinterpret_cast<float2*>(a.o_part + parts * cache->head_dim);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->head_dim == 128 ? launch_attention<128>(a, tiles, st) : launch_attention<64>(a, tiles, st);
+  const cudaError_t e = cache->head_dim == 128 ? launch_attention<128>(a, plan, st) : launch_attention<64>(a, plan, st);
   return e == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }

@@ -78,15 +78,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ uint32_t mapa(uint32_t addr, int rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 struct Bars {  // mbarriers of a block
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t afull[kTeams][kABufs], aempty[kTeams][kABufs];
@@ -291,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
 #pragma unroll
         for (int b = 0; b < kMaxKs; ++b) {
           f[b] = 0.f;
-          if (b < a.ks) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f[b]) : "r"(mapa(at, b)) : "memory");
+          if (b < a.ks) f[b] = ld_cluster(mapa(at, b));
         }
 #pragma unroll
         for (int b = 0; b < kMaxKs; ++b) v += f[b];

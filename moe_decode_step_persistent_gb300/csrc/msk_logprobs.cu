@@ -306,18 +306,10 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
   }
   if (S > 1) {
     // segments meet in the first block, through the cluster's shared memory
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+    cluster_sync();
     if (part == 0) {
-      auto remote = [](const void* p, int rank) {
-        uint32_t r;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-        return r;
-      };
-      auto ld32 = [](uint32_t at) {
-        uint32_t v;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-        return v;
-      };
+      auto remote = [](const void* p, int rank) { return mapa(smem_u32(p), rank); };
+      auto ld32 = [](uint32_t at) { return __float_as_uint(ld_cluster(at)); };
       const int n = S * a.top;  // <= 256
       for (int i = tid; i < n; i += NT) {
         const uint32_t at = remote(&best[i % a.top], i / a.top);
@@ -338,7 +330,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
         if (k != 0ull && r < a.top) best[r] = k;
       }
     }
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+    cluster_sync();
     if (part != 0) return;
   }
   __syncthreads();

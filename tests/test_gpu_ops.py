@@ -211,7 +211,9 @@ ATTN = [  # tokens, q heads, kv heads, head_dim, cached, window, tree, dtype
     (16, 8, 2, 64, 333, 0, True, "bf16"), (7, 12, 4, 128, 15, 5, True, "fp16"), (3, 5, 1, 128, 4097, 1, False, "bf16"),
     (16, 4, 1, 128, 16, 4, True, "bf16"), (11, 24, 1, 128, 260, 0, True, "bf16"), (16, 64, 2, 64, 129, 64, False, "fp16"),
     (2, 32, 8, 128, 5003, 2048, False, "bf16"), (5, 3, 3, 128, 64, 0, False, "bf16"), (4, 48, 1, 128, 700, 0, False, "bf16"),
-    (16, 1, 1, 64, 0, 0, True, "bf16"), (16, 16, 16, 128, 127, 300, False, "bf16"), (9, 14, 2, 128, 2049, 0, False, "fp16")]
+    (16, 1, 1, 64, 0, 0, True, "bf16"), (16, 16, 16, 128, 127, 300, False, "bf16"), (9, 14, 2, 128, 2049, 0, False, "fp16"),
+    (1, 8, 2, 128, 9000, 0, False, "bf16"), (16, 16, 4, 128, 8500, 0, True, "bf16"), (3, 6, 1, 64, 20011, 0, False, "fp16"),
+    (16, 8, 8, 64, 8193, 8190, True, "bf16"), (2, 10, 1, 128, 33000, 20000, False, "bf16")]
 
 
 def tree_parents(tokens, seed):
@@ -597,7 +599,8 @@ def test_binding_refuses(M):
     with pytest.raises(M.MskError):
         M.msk_attention_kv4(q, cache, 61)
     with pytest.raises(M.MskError):
-        M.msk_attention_kv4(q, cache, 10, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        M.msk_attention_kv4(q, M.Kv4Cache.empty(2, 20000, 64), 19000,
+                            workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         M.msk_kv4_write(cache, q, q, 0)
     with pytest.raises(M.MskError):

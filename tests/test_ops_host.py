@@ -68,13 +68,14 @@ def test_no_cache(lib):
     (dict(length=-1), INVALID), (dict(length=1021), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(qs=4088), INVALID), (dict(q=P + 8), ALIGN), (dict(out=P + 2), ALIGN),
     (dict(ws=P + 8), ALIGN), (dict(qs=4100), ALIGN), (dict(parents=[-1, 1, 0, 0]), INVALID),
-    (dict(parents=[-2, 0, 0, 0]), INVALID), (dict(ws=None), INVALID), (dict(nbytes=16), INVALID)])
+    (dict(parents=[-2, 0, 0, 0]), INVALID), (dict(ws=None, rows=100000, length=90000), INVALID),
+    (dict(nbytes=16, rows=100000, length=90000), INVALID)])
 def test_attention(M, lib, change, status):
     a = dict(q=P, dt=BF16, qs=4096, tokens=4, hq=32, length=100, parents=None, window=0, scale=0.0, out=P, ws=P,
-             nbytes=1 << 40)
+             nbytes=1 << 40, rows=1024)
     a.update(change)
     par = None if a["parents"] is None else (ctypes.c_int32 * 4)(*a["parents"])
-    assert lib.msk_attention_kv4(a["q"], a["dt"], a["qs"], cache(M), a["tokens"], a["hq"], a["length"], None, par,
+    assert lib.msk_attention_kv4(a["q"], a["dt"], a["qs"], cache(M, max_seq=a["rows"]), a["tokens"], a["hq"], a["length"], None, par,
                                  a["window"], a["scale"], a["out"], a["ws"], a["nbytes"], None) == status
 
 
@@ -107,9 +108,12 @@ def test_logprobs(lib, change, status):
 
 
 def test_workspace_sizes(lib):
-    assert lib.msk_attention_kv4_workspace(16, 32, 8, 128) > 0
-    for bad in ((0, 32, 8, 128), (17, 32, 8, 128), (16, 30, 8, 128), (16, 32, 0, 128)):
-        assert lib.msk_attention_kv4_workspace(*bad) == 0
+    size = lib.msk_attention_kv4_workspace
+    assert size(16, 32, 8, 128, 0, 100000) > 0
+    assert size(16, 32, 8, 128, 2048, 100000) == 0 and size(16, 32, 8, 128, 0, 100) == 0
+    for bad in ((0, 32, 8, 128, 0, 10), (17, 32, 8, 128, 0, 10), (16, 30, 8, 128, 0, 10), (16, 32, 0, 128, 0, 10),
+                (16, 32, 8, 128, -1, 10), (16, 32, 8, 128, 0, -1)):
+        assert size(*bad) == 0
 
 
 def test_binding_refuses_on_the_host(M):
