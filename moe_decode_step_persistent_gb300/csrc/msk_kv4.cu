@@ -181,6 +181,7 @@ msk_status rows_call(bool write, const msk_kv4_desc* c, const void* k, const voi
 constexpr int kMaxSplits = 64;    // key ranges of a kv head, each a block's, joined by a second kernel
 constexpr int kMaxCluster = 8;    // or, of few keys, the blocks of a cluster
 constexpr int kClusterKeys = 8192;
+constexpr int kRing = 5;          // steps of 16 keys in a warp's ring
 
 struct Kv4Attn {
   const uint16_t* q;
@@ -222,51 +223,67 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
   return r;
 }
 
-// What a lane holds of 16 keys and their values.
+// 16 keys and their values in shared memory, as in the cache (rows one behind
+// the other), and the fragments that a lane takes from there.
 template <int HD>
 struct Kv16 {
-  static constexpr int KW = HD / 32, VW = HD / 64;  // code words of a key, of a value
-  uint32_t k[2][KW], ke[2], v[4][VW], ve[4];
+  static constexpr int KW = HD / 32, VW = HD / 64;                 // code words of a lane's key, value
+  static constexpr int CODES = 16 * HD / 2, SCALES = HD;           // bytes of 16 rows
+  static constexpr int BYTES = 2 * (CODES + SCALES);               // K codes, V codes, K scales, V scales
 };
 
 template <int W>
-__device__ __forceinline__ void ld_words(uint32_t (&w)[W], const uint8_t* p) {
+__device__ __forceinline__ void lds_words(uint32_t (&w)[W], uint32_t at) {
   if (W == 4) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 u = lds128(at);
     w[0] = u.x, w[1] = u.y, w[W - 2] = u.z, w[W - 1] = u.w;
   } else if (W == 2) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 u = lds64(at);
     w[0] = u.x, w[W - 1] = u.y;
   } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
   }
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
 }
 
 // Few query rows (8 NT of them in a tile; row = token * group + head of the
 // group): a warp takes 16 keys at a time, as the M of S^T = K Q^T and O^T =
-// V^T P^T, so that NT n-tiles hold all rows and a key is decoded once.  K and
-// V come from global memory straight into the A fragments, no shared memory on
-// the way:
-//  K: lane (g, c) holds keys g and g + 8 and, of each 16 dimensions, any four,
-//     as long as Q's fragments hold the same: it takes the HD / 4 dimensions
-//     from c HD / 4 (16 bytes of codes at HD = 128), four a step.
+// V^T P^T, so that NT n-tiles hold all rows and a key is decoded once, into the
+// A fragments:
+//  K: lane (g, c) holds the keys of A rows g and g + 8 and, of each 16
+//     dimensions, any four, as long as Q's fragments hold the same: it takes
+//     the HD / 4 dimensions from c HD / 4 (16 bytes of codes at HD = 128).
 //  V: the fragment pairs two keys for one dimension; the lane holds four keys
 //     and takes the HD / 8 dimensions from g HD / 8, two for each m-tile (one
 //     byte).  Nibbles of two keys are put into one byte before the decoding,
 //     so a byte decodes to the pair.
 //  P: S^T's accumulators, as fp16, are P^T's B fragments after one 8 x 8
 //     transposition each.
-// Values are exact in fp16 (at most 6 significant bits, at most 2688).
+// A row 2i stands for the step's key i, row 2i + 1 for key 4 + i (+ 8 in the
+// second half), so that the lanes' values lie next to each other.  Elements
+// are exact in fp16 (at most 6 significant bits, at most 2688).
 //
 // The softmax's reference is raised only when a score passes it by 2^8: weights
 // reach 256 (of fp16's 65504), and the sums are rescaled a few times in all.
 //
-// Two steps' loads are in flight for each warp.  Bound by the decoding (a
-// conversion and a multiply for two elements) and DRAM.
+// A warp's keys come through a ring of kRing steps of its own, by asynchronous
+// copies; warps meet only at the end.  Bound by the decoding (a conversion and a
+// multiply for two elements) and DRAM.
 template <int HD, int NT>
 __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __grid_constant__ Kv4Attn a) {
   constexpr int KS = HD / 16, MT = HD / 16, ROWS = 8 * NT, PITCH = HD + 4;
-  extern __shared__ __align__(16) float smem[];  // [8 warps][ROWS][PITCH], then [8][ROWS] (reference, sum)
+  using K16 = Kv16<HD>;
+  // the warps' rings; after the last step [8 warps][ROWS][PITCH] sums, [8][ROWS] (reference, sum)
+  extern __shared__ __align__(16) float smem[];
   float2* sml = reinterpret_cast<float2*>(smem + 8 * ROWS * PITCH);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int split = blockIdx.x, h = blockIdx.y, tile = blockIdx.z;
@@ -278,33 +295,36 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
   const int steps = (n - first + 15) / 16;
   const int per = (steps + (int)gridDim.x - 1) / (int)gridDim.x;
   const int s0 = split * per, s1 = min(steps, s0 + per);
-  const uint8_t* kc = a.codes + (long long)h * a.max_seq * (HD / 2) + c * (HD / 8);
-  const uint8_t* ks = a.scales + (long long)h * a.max_seq * (HD / 16) + c * (HD / 64);
-  const uint8_t* vc = a.codes + (long long)(a.Hkv + h) * a.max_seq * (HD / 2) + g * (HD / 16);
-  const uint8_t* vs = a.scales + (long long)(a.Hkv + h) * a.max_seq * (HD / 16) + g * (HD / 8) / 16;
-  auto load = [&](Kv16<HD>& t, int s) {
-    if (s >= s1) return;
-    const int j0 = first + s * 16;
-    const bool whole = j0 >= lo && j0 + 16 <= n;
+  const uint8_t* kc = a.codes + (long long)h * a.max_seq * (HD / 2);
+  const uint8_t* ks = a.scales + (long long)h * a.max_seq * (HD / 16);
+  const long long vc = (long long)a.Hkv * a.max_seq * (HD / 2), vs = (long long)a.Hkv * a.max_seq * (HD / 16);
+  const uint32_t ring = smem_u32(smem) + warp * kRing * K16::BYTES;
+  uint32_t fslot = 0;
+  auto fetch = [&](int s) {  // a step's 16 keys and values into the next slot: rows are consecutive
+    if (s < s1) {
+      const int j0 = first + s * 16, have = min(16, n - j0);  // (rows past the last one are not read)
+      const uint32_t dst = ring + fslot;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      int j = j0 + g + 8 * i;
-      if (!whole) j = min(j, n - 1);
-      ld_words(t.k[i], kc + (long long)j * (HD / 2));
-      if (HD == 128) t.ke[i] = __ldg(reinterpret_cast<const uint16_t*>(ks + (long long)j * (HD / 16)));
-      else t.ke[i] = __ldg(ks + (long long)j * (HD / 16));
+      for (int i = 0; i < K16::CODES / 512; ++i) {
+        const int at = (i * 32 + lane) * 16;
+        if (at < have * (HD / 2)) {
+          cp_async16(dst + at, kc + (long long)j0 * (HD / 2) + at);
+          cp_async16(dst + K16::CODES + at, kc + vc + (long long)j0 * (HD / 2) + at);
+        }
+      }
+      const int at = (lane & 15) * (HD / 16);  // lanes 0-15 the keys' scales, 16-31 the values'
+      if ((lane & 15) < have) {
+        const uint8_t* src = ks + (lane < 16 ? 0 : vs) + (long long)j0 * (HD / 16) + at;
+        const uint32_t to = dst + 2 * K16::CODES + (lane < 16 ? 0 : K16::SCALES) + at;
+        if (HD == 128) cp_async8(to, src);
+        else cp_async4(to, src);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int jj = j0 + (i >> 1) * 8 + 2 * c + (i & 1), j = whole ? jj : min(jj, n - 1);
-      ld_words(t.v[i], vc + (long long)j * (HD / 2));
-      t.ve[i] = __ldg(vs + (long long)j * (HD / 16));
-      if (!whole && (jj < lo || jj >= n)) t.ve[i] = 0;  // (such rows may hold anything, NaN scales too)
-    }
+    cp_async_commit();
+    fslot = fslot == (kRing - 1) * K16::BYTES ? 0 : fslot + K16::BYTES;
   };
-  Kv16<HD> t0, t1;
-  load(t0, s0 + warp);
-  load(t1, s0 + warp + 8);
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) fetch(s0 + warp + 8 * i);
 
   // Q: lane (g, c) of n-tile nt holds row 8 nt + g
   uint32_t qf[NT][KS][2];
@@ -360,23 +380,45 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
     for (int i = 0; i < MT; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
   }
 
-  auto step = [&](const Kv16<HD>& t, int s) {
+  const int kg = (g >> 1) + (g & 1) * 4;  // the key of A row g
+  const uint32_t ka = kg * (HD / 2) + c * (HD / 8), kea = 2 * K16::CODES + kg * (HD / 16) + c * (HD / 64);
+  const uint32_t va = K16::CODES + c * (HD / 2) + g * (HD / 16);
+  const uint32_t vea = 2 * K16::CODES + K16::SCALES + c * (HD / 16) + g * (HD / 8) / 16;
+  uint32_t slot = ring;
+  for (int s = s0 + warp; s < s1; s += 8) {
     const int j0 = first + s * 16;
+    cp_async_wait_group<kRing - 2>();
+    __syncwarp();
     float sc[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-    const uint32_t e0 = e4m3x2_to_f16x2(t.ke[0]), e1 = e4m3x2_to_f16x2(t.ke[1]);
+    uint32_t k0[K16::KW], k1[K16::KW], vw[4][K16::VW], ve[4];
+    lds_words(k0, slot + ka);
+    lds_words(k1, slot + ka + 8 * (HD / 2));
+    const uint32_t e0 = e4m3x2_to_f16x2(HD == 128 ? lds_u16(slot + kea) : lds_u8(slot + kea));
+    const uint32_t e1 = e4m3x2_to_f16x2(HD == 128 ? lds_u16(slot + kea + 8 * (HD / 16)) : lds_u8(slot + kea + 8 * (HD / 16)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // A rows 2c, 2c + 1, 8 + 2c, 9 + 2c: keys c, 4 + c, 8 + c, 12 + c
+      lds_words(vw[i], slot + va + i * 4 * (HD / 2));
+      ve[i] = lds_u8(slot + vea + i * 4 * (HD / 16));
+      if (j0 < lo || j0 + 16 > n) {  // (rows that no query sees may hold anything, NaN scales too)
+        const int j = j0 + i * 4 + c;
+        if (j < lo || j >= n) ve[i] = 0;
+      }
+    }
+    fetch(s + 8 * (kRing - 1));  // (into the slot of the step before: every lane is past it)
+    slot = slot == ring + (kRing - 1) * K16::BYTES ? ring : slot + K16::BYTES;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const uint32_t f0 = f16x2_bcast(e0, k >= 4), f1 = f16x2_bcast(e1, k >= 4);
-      const uint32_t af[4] = {hmul2(e2m1_byte_to_f16x2(t.k[0][k >> 1], 2 * (k & 1)), f0),
-                              hmul2(e2m1_byte_to_f16x2(t.k[1][k >> 1], 2 * (k & 1)), f1),
-                              hmul2(e2m1_byte_to_f16x2(t.k[0][k >> 1], 2 * (k & 1) + 1), f0),
-                              hmul2(e2m1_byte_to_f16x2(t.k[1][k >> 1], 2 * (k & 1) + 1), f1)};
+      const uint32_t af[4] = {hmul2(e2m1_byte_to_f16x2(k0[k >> 1], 2 * (k & 1)), f0),
+                              hmul2(e2m1_byte_to_f16x2(k1[k >> 1], 2 * (k & 1)), f1),
+                              hmul2(e2m1_byte_to_f16x2(k0[k >> 1], 2 * (k & 1) + 1), f0),
+                              hmul2(e2m1_byte_to_f16x2(k1[k >> 1], 2 * (k & 1) + 1), f1)};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], af, qf[nt][k][0], qf[nt][k][1]);
     }
-    // scores in log2 units; (key g, rows 2c, 2c + 1), (key g + 8, the same)
+    // scores in log2 units: A row g, query rows 2c and 2c + 1; A row g + 8, the same
     const bool whole = j0 >= seen && j0 + 16 <= len;
     bool raise = false;
 #pragma unroll
@@ -386,7 +428,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
         float x = sc[nt][i] * fac[nt][i & 1];
         if (!whole) {
           const int tk = tok[nt][i & 1];
-          x = tk >= 0 && sees(a, tk, j0 + g + 8 * (i >> 1), len) ? x : -INFINITY;
+          x = tk >= 0 && sees(a, tk, j0 + kg + 8 * (i >> 1), len) ? x : -INFINITY;
         }
         sc[nt][i] = x;
         raise |= x > m[nt][i & 1] + 8.f;  // (-inf + 8 is -inf: the first visible score raises)
@@ -420,12 +462,12 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
       pb[nt][0] = movmatrix_trans(pack_f16x2(p[0], p[1]));
       pb[nt][1] = movmatrix_trans(pack_f16x2(p[2], p[3]));
     }
-    const uint32_t v0 = e4m3x2_to_f16x2(t.ve[0] | t.ve[1] << 8), v1 = e4m3x2_to_f16x2(t.ve[2] | t.ve[3] << 8);
+    const uint32_t v0 = e4m3x2_to_f16x2(ve[0] | ve[1] << 8), v1 = e4m3x2_to_f16x2(ve[2] | ve[3] << 8);
 #pragma unroll
-    for (int w = 0; w < Kv16<HD>::VW; ++w) {
+    for (int w = 0; w < K16::VW; ++w) {
       constexpr uint32_t M = 0x0F0F0F0Fu;
-      const uint32_t a0 = (t.v[0][w] & M) | ((t.v[1][w] & M) << 4), a1 = ((t.v[0][w] >> 4) & M) | (t.v[1][w] & ~M);
-      const uint32_t b0 = (t.v[2][w] & M) | ((t.v[3][w] & M) << 4), b1 = ((t.v[2][w] >> 4) & M) | (t.v[3][w] & ~M);
+      const uint32_t a0 = (vw[0][w] & M) | ((vw[1][w] & M) << 4), a1 = ((vw[0][w] >> 4) & M) | (vw[1][w] & ~M);
+      const uint32_t b0 = (vw[2][w] & M) | ((vw[3][w] & M) << 4), b1 = ((vw[2][w] >> 4) & M) | (vw[3][w] & ~M);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t af[4] = {hmul2(e2m1_byte_to_f16x2(a0, k), v0), hmul2(e2m1_byte_to_f16x2(a1, k), v0),
@@ -434,13 +476,9 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
         for (int nt = 0; nt < NT; ++nt) mma_f16(o[w * 4 + k][nt], af, pb[nt][0], pb[nt][1]);
       }
     }
-  };
-  for (int s = s0 + warp; s < s1; s += 16) {
-    step(t0, s);
-    load(t0, s + 16);
-    if (s + 8 < s1) step(t1, s + 8);
-    load(t1, s + 24);
   }
+  cp_async_wait_all();
+  __syncthreads();  // (the sums take the rings' place)
 
   // the warps' sums to shared memory
 #pragma unroll
@@ -556,7 +594,7 @@ int most_keys(int tokens, int window, int len) { return std::min(len, window > 0
 
 template <int HD, int NT>
 cudaError_t launch_rows_kernel(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st) {
-  constexpr int smem = 8 * 8 * NT * (HD + 4) * 4 + 8 * 8 * NT * 8;
+  constexpr int smem = std::max(8 * kRing * Kv16<HD>::BYTES, 8 * 8 * NT * (HD + 4) * 4 + 8 * 8 * NT * 8);
   static bool ready[64] = {};  // (a function's attributes are set once a device; twice does no harm)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

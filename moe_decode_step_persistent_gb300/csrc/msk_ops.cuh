@@ -64,6 +64,11 @@ __device__ __forceinline__ int row_shift(float amax) {
   return e < -118 ? 126 : (e > 127 ? -119 : 8 - e);
 }
 
+// 8-byte global -> shared copy.
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src) : "memory");
+}
+
 // --- thread-block clusters ---------------------------------------------------
 
 // The address of block `rank`'s counterpart of a shared-memory address.
