@@ -299,32 +299,44 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
   const uint8_t* ks = a.scales + (long long)h * a.max_seq * (HD / 16);
   const long long vc = (long long)a.Hkv * a.max_seq * (HD / 2), vs = (long long)a.Hkv * a.max_seq * (HD / 16);
   const uint32_t ring = smem_u32(smem) + warp * kRing * K16::BYTES;
-  uint32_t fslot = 0;
-  auto fetch = [&](int s) {  // a step's 16 keys and values into the next slot: rows are consecutive
-    if (s < s1) {
-      const int j0 = first + s * 16, have = min(16, n - j0);  // (rows past the last one are not read)
-      const uint32_t dst = ring + fslot;
+  // the next step to fetch, this lane's parts of it: 16 bytes of codes in each
+  // half kilobyte of keys and of values, one row's scales (lanes 0-15 the
+  // keys', 16-31 the values')
+  int fs = s0 + warp;
+  uint32_t fslot = ring;
+  const uint8_t* fk = kc + (long long)(first + fs * 16) * (HD / 2) + lane * 16;
+  const uint8_t* fe = ks + (lane < 16 ? 0 : vs) + (long long)(first + fs * 16 + (lane & 15)) * (HD / 16);
+  const uint32_t fet = 2 * K16::CODES + (lane < 16 ? 0 : K16::SCALES) + (lane & 15) * (HD / 16);
+  auto fetch = [&]() {
+    if (fs < s1) {
+      const int have = n - (first + fs * 16);  // (rows past the last one are not read)
+      if (have >= 16) {
 #pragma unroll
-      for (int i = 0; i < K16::CODES / 512; ++i) {
-        const int at = (i * 32 + lane) * 16;
-        if (at < have * (HD / 2)) {
-          cp_async16(dst + at, kc + (long long)j0 * (HD / 2) + at);
-          cp_async16(dst + K16::CODES + at, kc + vc + (long long)j0 * (HD / 2) + at);
+        for (int i = 0; i < K16::CODES / 512; ++i) {
+          cp_async16(fslot + i * 512 + lane * 16, fk + i * 512);
+          cp_async16(fslot + K16::CODES + i * 512 + lane * 16, fk + vc + i * 512);
         }
-      }
-      const int at = (lane & 15) * (HD / 16);  // lanes 0-15 the keys' scales, 16-31 the values'
-      if ((lane & 15) < have) {
-        const uint8_t* src = ks + (lane < 16 ? 0 : vs) + (long long)j0 * (HD / 16) + at;
-        const uint32_t to = dst + 2 * K16::CODES + (lane < 16 ? 0 : K16::SCALES) + at;
-        if (HD == 128) cp_async8(to, src);
-        else cp_async4(to, src);
+        if (HD == 128) cp_async8(fslot + fet, fe);
+        else cp_async4(fslot + fet, fe);
+      } else {
+#pragma unroll
+        for (int i = 0; i < K16::CODES / 512; ++i)
+          if (i * 512 + lane * 16 < have * (HD / 2)) {
+            cp_async16(fslot + i * 512 + lane * 16, fk + i * 512);
+            cp_async16(fslot + K16::CODES + i * 512 + lane * 16, fk + vc + i * 512);
+          }
+        if ((lane & 15) < have) {
+          if (HD == 128) cp_async8(fslot + fet, fe);
+          else cp_async4(fslot + fet, fe);
+        }
       }
     }
     cp_async_commit();
-    fslot = fslot == (kRing - 1) * K16::BYTES ? 0 : fslot + K16::BYTES;
+    fs += 8, fk += 8 * K16::CODES, fe += 8 * K16::SCALES;
+    fslot = fslot == ring + (kRing - 1) * K16::BYTES ? ring : fslot + K16::BYTES;
   };
 #pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) fetch(s0 + warp + 8 * i);
+  for (int i = 0; i < kRing - 1; ++i) fetch();
 
   // Q: lane (g, c) of n-tile nt holds row 8 nt + g
   uint32_t qf[NT][KS][2];
@@ -372,10 +384,10 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
   const int deepest = a.T - 1;
   const int seen = a.window > 0 ? max(0, len + deepest - a.window + 1) : 0;
 
-  float o[MT][NT][4], m[NT][2], l[NT][2];
+  float o[MT][NT][4], nm[NT][2], l[NT][2];  // (nm: the reference's negative)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+    nm[nt][0] = nm[nt][1] = INFINITY, l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
   }
@@ -390,8 +402,11 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
     cp_async_wait_group<kRing - 2>();
     __syncwarp();
     float sc[NT][4];
+    bool hidden[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[nt][i] = 0.f, hidden[nt][i] = false;
     uint32_t k0[K16::KW], k1[K16::KW], vw[4][K16::VW], ve[4];
     lds_words(k0, slot + ka);
     lds_words(k1, slot + ka + 8 * (HD / 2));
@@ -406,7 +421,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
         if (j < lo || j >= n) ve[i] = 0;
       }
     }
-    fetch(s + 8 * (kRing - 1));  // (into the slot of the step before: every lane is past it)
+    fetch();  // (into the slot of the step before: every lane is past it)
     slot = slot == ring + (kRing - 1) * K16::BYTES ? ring : slot + K16::BYTES;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
@@ -419,34 +434,43 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
       for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], af, qf[nt][k][0], qf[nt][k][1]);
     }
     // scores in log2 units: A row g, query rows 2c and 2c + 1; A row g + 8, the same
-    const bool whole = j0 >= seen && j0 + 16 <= len;
+    if (j0 < seen || j0 + 16 > len) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tk = tok[nt][i & 1];
+          hidden[nt][i] = !(tk >= 0 && sees(a, tk, j0 + kg + 8 * (i >> 1), len));
+        }
+    }
+    float y[NT][4];  // relative to the reference; a row without one: +inf
     bool raise = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float x = sc[nt][i] * fac[nt][i & 1];
-        if (!whole) {
-          const int tk = tok[nt][i & 1];
-          x = tk >= 0 && sees(a, tk, j0 + kg + 8 * (i >> 1), len) ? x : -INFINITY;
-        }
-        sc[nt][i] = x;
-        raise |= x > m[nt][i & 1] + 8.f;  // (-inf + 8 is -inf: the first visible score raises)
+        y[nt][i] = fmaf(sc[nt][i], fac[nt][i & 1], nm[nt][i & 1]);
+        if (hidden[nt][i]) y[nt][i] = -INFINITY;
+        raise |= y[nt][i] > 8.f;
       }
     if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float mx = fmaxf(sc[nt][i], sc[nt][i + 2]);
+          const float x0 = hidden[nt][i] ? -INFINITY : sc[nt][i] * fac[nt][i];
+          const float x1 = hidden[nt][i + 2] ? -INFINITY : sc[nt][i + 2] * fac[nt][i];
+          float mx = fmaxf(x0, x1);
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
-          mx = fmaxf(m[nt][i], mx);
-          const float al = mx == -INFINITY ? 1.f : exp2f(m[nt][i] - mx);
-          m[nt][i] = mx;
+          mx = fmaxf(-nm[nt][i], mx);
+          const float al = mx == -INFINITY ? 1.f : ex2(-nm[nt][i] - mx);
+          nm[nt][i] = -mx;
           l[nt][i] *= al;
 #pragma unroll
           for (int k = 0; k < MT; ++k) o[k][nt][i] *= al, o[k][nt][i + 2] *= al;
+          y[nt][i] = hidden[nt][i] ? -INFINITY : x0 - mx;
+          y[nt][i + 2] = hidden[nt][i + 2] ? -INFINITY : x1 - mx;
         }
     }
     uint32_t pb[NT][2];
@@ -454,15 +478,12 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
     for (int nt = 0; nt < NT; ++nt) {
       float p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float ref = m[nt][i & 1];
-        p[i] = exp2f(sc[nt][i] - (ref == -INFINITY ? 0.f : ref));
-      }
+      for (int i = 0; i < 4; ++i) p[i] = ex2(y[nt][i]);
       l[nt][0] += p[0] + p[2], l[nt][1] += p[1] + p[3];
       pb[nt][0] = movmatrix_trans(pack_f16x2(p[0], p[1]));
       pb[nt][1] = movmatrix_trans(pack_f16x2(p[2], p[3]));
     }
-    const uint32_t v0 = e4m3x2_to_f16x2(ve[0] | ve[1] << 8), v1 = e4m3x2_to_f16x2(ve[2] | ve[3] << 8);
+    const uint32_t v0 = e4m3x2_to_f16x2(__byte_perm(ve[0], ve[1], 0x0040)), v1 = e4m3x2_to_f16x2(__byte_perm(ve[2], ve[3], 0x0040));
 #pragma unroll
     for (int w = 0; w < K16::VW; ++w) {
       constexpr uint32_t M = 0x0F0F0F0Fu;
@@ -477,6 +498,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
       }
     }
   }
+  grid_dep_launch();
   cp_async_wait_all();
   __syncthreads();  // (the sums take the rings' place)
 
@@ -489,7 +511,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
 #pragma unroll
       for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
       const int r = nt * 8 + 2 * c + i;
-      if (g == 0) sml[warp * ROWS + r] = make_float2(m[nt][i], s);
+      if (g == 0) sml[warp * ROWS + r] = make_float2(-nm[nt][i], s);
 #pragma unroll
       for (int k = 0; k < MT; ++k)
         *reinterpret_cast<float2*>(smem + (warp * ROWS + r) * PITCH + g * (HD / 8) + 2 * k) =
@@ -549,23 +571,33 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
   }
 }
 
-// The key ranges of a (token, query head): one block, HD threads.
+// The key ranges of a (token, query head): a block of four groups of HD
+// threads that take the ranges in turn.
 template <int HD>
-__global__ void __launch_bounds__(HD) kv4_combine_kernel(const __grid_constant__ Kv4Attn a, int tile_rows) {
-  grid_dep_wait();
-  const int row = blockIdx.x, h = blockIdx.y, d = threadIdx.x;
+__global__ void __launch_bounds__(4 * HD) kv4_combine_kernel(const __grid_constant__ Kv4Attn a, int tile_rows) {
+  __shared__ float fs[kMaxSplits], part[4][HD], total;
+  const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, d = tid % HD, q = tid / HD;
   const long long base = ((long long)(row / tile_rows) * a.Hkv + h) * a.splits * tile_rows + row % tile_rows;
-  float mm = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, a.ml_part[base + s * tile_rows].x);
-  float sum = 0.f, ll = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 ml = a.ml_part[base + s * tile_rows];
-    if (ml.y == 0.f) continue;  // (a range without a visible key)
-    const float f = exp2f(ml.x - mm);
-    sum += f * a.o_part[(base + s * tile_rows) * HD + d];
-    ll += f * ml.y;
+  grid_dep_wait();
+  if (tid < 32) {  // (at most 64 ranges: two a lane)
+    const float2 none = make_float2(-INFINITY, 0.f);
+    const float2 x = tid < a.splits ? a.ml_part[base + tid * tile_rows] : none;
+    const float2 y = tid + 32 < a.splits ? a.ml_part[base + (tid + 32) * tile_rows] : none;
+    float mm = fmaxf(x.x, y.x);
+    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+    const float fx = ex2(x.x - mm), fy = ex2(y.x - mm);  // (a range without a visible key: 0)
+    float s = fx * x.y + fy * y.y;
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    fs[tid] = fx, fs[tid + 32] = fy;
+    if (tid == 0) total = s;
   }
-  store_out(a, HD, h, row, d, sum / ll * a.v_scale);
+  __syncthreads();
+  float sum = 0.f;
+#pragma unroll 8
+  for (int s = q; s < a.splits; s += 4) sum += fs[s] * a.o_part[(base + (long long)s * tile_rows) * HD + d];
+  part[q][d] = sum;
+  __syncthreads();
+  if (q == 0) store_out(a, HD, h, row, d, ((part[0][d] + part[1][d]) + (part[2][d] + part[3][d])) / total * a.v_scale);
 }
 
 // How a call is laid out.  `keys`: the most keys that a head may have to read.
@@ -623,7 +655,7 @@ cudaError_t launch_attention(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3((unsigned)(a.T * a.G), (unsigned)a.Hkv);
-  cfg.blockDim = dim3(HD);
+  cfg.blockDim = dim3(4 * HD);
   cfg.stream = st;
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;

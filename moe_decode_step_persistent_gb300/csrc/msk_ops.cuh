@@ -49,6 +49,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
   return fp16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
