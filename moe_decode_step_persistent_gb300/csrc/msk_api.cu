@@ -91,7 +91,7 @@ namespace msk {
 
 // cuTensorMapEncodeTiled from the driver, looked up once through the
 // runtime (the library does not link the driver library itself).
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {

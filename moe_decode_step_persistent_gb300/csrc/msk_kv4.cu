@@ -1,10 +1,13 @@
 // The 4-bit KV cache: writing rows (quantise), reading them back, and GQA
 // attention over them.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cmath>
 
 #include "msk_internal.h"
 #include "msk_ops.cuh"
+#include "msk_tc.cuh"
 
 namespace msk {
 namespace {
@@ -253,6 +256,54 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
   return v;
+}
+
+// The end of an attention block: its sums, smem[row][PITCH] with the reference
+// and the sum of weights behind each row's elements, go to the workspace, or
+// through the cluster's shared memory, or straight to the output.
+template <int HD, int ROWS, int THREADS>
+__device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, int split, int h, int tile) {
+  constexpr int PITCH = HD + 4;
+  const int rows = a.T * a.G;
+  if (a.splits > 1) {
+    const long long part = (((long long)tile * a.Hkv + h) * a.splits + split) * ROWS;
+    for (int e = threadIdx.x; e < ROWS * HD; e += THREADS) {
+      const int r = e / HD, d = e % HD;
+      if (tile * ROWS + r >= rows) break;
+      a.o_part[(part + r) * HD + d] = smem[r * PITCH + d];
+      if (d == 0) a.ml_part[part + r] = make_float2(smem[r * PITCH + HD], smem[r * PITCH + HD + 1]);
+    }
+    return;
+  }
+  if (a.cluster == 1) {
+    for (int e = threadIdx.x; e < ROWS * HD; e += THREADS) {
+      const int r = e / HD, d = e % HD, row = tile * ROWS + r;
+      if (row >= rows) break;
+      store_out(a, HD, h, row, d, smem[r * PITCH + d] / smem[r * PITCH + HD + 1] * a.v_scale);
+    }
+    return;
+  }
+  cluster_sync();
+  for (int e = split * THREADS + threadIdx.x; e < ROWS * HD; e += a.cluster * THREADS) {
+    const int r = e / HD, d = e % HD, row = tile * ROWS + r;
+    if (row >= rows) break;
+    const uint32_t at = smem_u32(smem + r * PITCH);
+    float ms[kMaxCluster], mm = -INFINITY, sum = 0.f, ll = 0.f;
+#pragma unroll
+    for (int b = 0; b < kMaxCluster; ++b) {
+      ms[b] = b < a.cluster ? ld_cluster(mapa(at + HD * 4, b)) : -INFINITY;
+      mm = fmaxf(mm, ms[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < kMaxCluster; ++b)
+      if (b < a.cluster) {
+        const float f = ex2(ms[b] - mm);
+        sum += f * ld_cluster(mapa(at + d * 4, b));
+        ll += f * ld_cluster(mapa(at + HD * 4 + 4, b));
+      }
+    store_out(a, HD, h, row, d, sum / ll * a.v_scale);
+  }
+  cluster_sync();  // (no block leaves while its sums may be read)
 }
 
 // Few query rows (8 NT of them in a tile; row = token * group + head of the
@@ -532,43 +583,440 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
       sum += f * smem[(w * ROWS + r) * PITCH + d];
       ll += f * ml.y;
     }
-    const int row = tile * ROWS + r;
-    if (a.splits > 1) {
-      if (row < rows) {
-        const long long part = (((long long)tile * a.Hkv + h) * a.splits + split) * ROWS + r;
-        a.o_part[part * HD + d] = sum;
-        if (d == 0) a.ml_part[part] = make_float2(mm, ll);
-      }
-    } else if (a.cluster == 1) {
-      if (row < rows) store_out(a, HD, h, row, d, sum / ll * a.v_scale);
-    } else {
-      smem[r * PITCH + d] = sum;  // (this thread's own element)
-      if (d == 0) smem[r * PITCH + HD] = mm, smem[r * PITCH + HD + 1] = ll;
+    smem[r * PITCH + d] = sum;  // (this thread's own element)
+    if (d == 0) smem[r * PITCH + HD] = mm, smem[r * PITCH + HD + 1] = ll;
+  }
+  __syncthreads();
+  finish_block<HD, ROWS, 256>(a, smem, split, h, tile);
+}
+
+// ---------------------------------------------------------------------------
+// many query rows: the fifth-generation tensor cores
+// ---------------------------------------------------------------------------
+
+constexpr int kTcRows = 64;    // query rows of a tile (the MMAs' N)
+constexpr int kTcKeys = 128;   // keys of a step (the MMAs' M, and K)
+constexpr int kTcTeams = 2;    // teams of four warps that take the steps in turn
+constexpr int kTcThreads = 32 * (4 * kTcTeams + kTcTeams);
+constexpr int kTcSlots = 2;    // steps that a team has in shared memory
+static __device__ uint32_t g_error;  // nonzero once a wait has run out
+
+template <int HD>
+struct Tc {
+  static constexpr int CODES = kTcKeys * HD / 2;                // bytes of a step's keys (or values)
+  static constexpr int Q = kTcRows * HD * 2, V = kTcKeys * HD * 2, P = kTcKeys * kTcRows * 2;
+  static constexpr int TEAM = V + P + kTcSlots * 2 * CODES;     // a team's shared memory
+  static constexpr int SMEM = 1024 + Q + kTcTeams * TEAM;
+  // tensor memory columns: decoded keys, scores, output sums
+  static constexpr int A0 = 0, S0 = kTcTeams * HD / 2, O0 = S0 + kTcTeams * kTcRows, COLS = 512;
+  static_assert(O0 + kTcTeams * kTcRows <= COLS);
+  static_assert(kTcRows * (HD + 4) * 4 <= V + P);  // the block's sums at the end
+};
+
+struct TcBars {
+  uint64_t full[kTcTeams][kTcSlots], empty[kTcTeams][kTcSlots];
+  uint64_t kready[kTcTeams], sdone[kTcTeams], pready[kTcTeams], pvdone[kTcTeams];
+};
+
+struct Kv4AttnTc {
+  CUtensorMap map;  // [2 Hkv][max_seq][HD / 2] bytes, boxes of 1 x 128 x HD / 2
+  Kv4Attn a;
+};
+
+// OR of a truth value over a team (a barrier of its 128 threads).
+__device__ __forceinline__ bool team_any(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// Row of 16-byte pieces with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t piece) { return row * 128 + (((piece ^ row) & 7) << 4); }
+
+// 32 values a lane, combined over the lanes: lane i gets value i's result.
+template <typename F>
+__device__ __forceinline__ float spread32(float (&z)[32], int lane, F f) {
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float give = up ? z[i] : z[i + w], keep = up ? z[i + w] : z[i];
+      z[i] = f(keep, __shfl_xor_sync(0xFFFFFFFFu, give, w));
     }
   }
-  if (a.cluster > 1) {  // the blocks of a head, through the cluster's shared memory
-    cluster_sync();
-    for (int e = split * 256 + tid; e < ROWS * HD; e += a.cluster * 256) {
-      const int r = e / HD, d = e % HD, row = tile * ROWS + r;
-      if (row >= rows) break;
-      const uint32_t at = smem_u32(smem + r * PITCH);
-      float ms[kMaxCluster], mm = -INFINITY, sum = 0.f, ll = 0.f;
+  return z[0];
+}
+
+// 64 elements decoded to fp16: 32 bytes of codes, four block scales.
+__device__ __forceinline__ void decode64(uint32_t (&v)[32], const uint4& c0, const uint4& c1, uint32_t e) {
+  const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
-      for (int b = 0; b < kMaxCluster; ++b) {
-        ms[b] = b < a.cluster ? ld_cluster(mapa(at + HD * 4, b)) : -INFINITY;
-        mm = fmaxf(mm, ms[b]);
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t f = f16x2_bcast(e4m3_pair_to_f16x2(e, b >> 1), b & 1);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[b * 8 + j] = hmul2(e2m1_byte_to_f16x2(w[2 * b + (j >> 2)], j & 3), f);
+  }
+}
+
+// Up to 64 query rows of a kv head at once: S^T = K Q^T (M = 128 keys, N = 64
+// rows, K = HD) and O^T = V^T P^T (M = HD, N = 64, K = 128 keys), fp16 operands,
+// fp32 accumulators in tensor memory.
+//
+// Two teams of four warps take steps of 128 keys in turn, a thread for a key:
+// it decodes the key into the A operand in tensor memory (exactly), the value
+// into shared memory while the scores are computed, then takes its key's 64
+// scores, turns them into weights and writes them as the B operand.  Each team
+// has a softmax of its own (reference, sums, output sums); the two are joined at
+// the end.  A warp for each team issues its MMAs and copies.  The reference of
+// a row is raised when a score passes it by 2^8, and the sums rescaled: a few
+// times in all.  On mma.sync 64 rows cost four times the decoding or do not fit
+// the registers: 53 us for 16 tokens over 32768 keys.
+//
+// NR: rows of the 64 that are in use, 32 or 64 (the softmax skips the rest).
+template <int HD, int NR>
+__global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_constant__ Kv4AttnTc args) {
+  using L = Tc<HD>;
+  constexpr int PITCH = HD + 4, PIECES = HD / 32;  // 16-byte pieces of a row's codes
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ TcBars bars;
+  __shared__ __align__(16) float nm[kTcTeams][kTcRows];   // the references' negatives (+inf: none yet)
+  __shared__ __align__(16) float al[kTcTeams][kTcRows];   // factors of a rescaling
+  __shared__ float wmax[kTcTeams][4][kTcRows];            // a warp's maxima; its sums at the end
+  __shared__ __align__(16) float fac[kTcRows];            // a row's scores in log2 units: times this
+  __shared__ uint32_t tmem_base;
+  __shared__ uint8_t tok[kTcRows];                        // a row's token, 31 past the last row
+  __shared__ int abort, never;
+  const Kv4Attn& a = args.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = blockIdx.x, h = blockIdx.y, tile = blockIdx.z;
+  const int len = cached_len(a), rows = a.T * a.G;
+  const uint64_t deadline = gtimer() + kOpsWaitNs;
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+
+  // this block's keys: steps of 128
+  const int n = len + a.T;
+  const int lo = a.window > 0 ? max(0, len - a.window + 1) : 0;  // (no query sees a key before lo)
+  const int steps = (n - lo + kTcKeys - 1) / kTcKeys;
+  const int per = (steps + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int s0 = min(steps, split * per), s1 = min(steps, s0 + per);
+  const int seen = a.window > 0 ? max(0, len + a.T - a.window) : 0;  // keys that every query sees: [seen, len)
+
+  if (tid == 0) {
+    abort = 0, never = 0;
+    for (int t = 0; t < kTcTeams; ++t) {
+      for (int i = 0; i < kTcSlots; ++i) mbar_init(bar(bars.full[t][i]), 1), mbar_init(bar(bars.empty[t][i]), 4);
+      mbar_init(bar(bars.kready[t]), 4), mbar_init(bar(bars.sdone[t]), 1);
+      mbar_init(bar(bars.pready[t]), 4), mbar_init(bar(bars.pvdone[t]), 1);
+    }
+    mbar_fence_init();
+  }
+  if (tid < kTcRows) {
+    const int row = tile * kTcRows + tid;
+    tok[tid] = row < rows ? (uint8_t)(row / a.G) : 31;
+    for (int t = 0; t < kTcTeams; ++t) nm[t][tid] = row < rows ? INFINITY : 0.f;
+  }
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_base), L::COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const volatile int* ab = &abort;
+  auto wait = [&](uint64_t& b, uint32_t parity) {
+    if (mbar_wait(bar(b), parity, deadline, ab)) return true;
+    abort = 1;
+    return false;
+  };
+  auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
+
+  const int team = warp < 4 * kTcTeams ? warp >> 2 : warp - 4 * kTcTeams;
+  const int mine = max(0, (s1 - s0 - team + kTcTeams - 1) / kTcTeams);  // this team's steps
+  uint8_t* tsm = smem + L::Q + team * L::TEAM;
+  const uint32_t vbuf = smem_u32(tsm), pbuf = vbuf + L::V, raw = pbuf + L::P;
+  auto load = [&](int it) {  // a step's keys and values
+    const int slot = it % kTcSlots, j0 = lo + (s0 + team + it * kTcTeams) * kTcKeys;
+    const uint32_t b = bar(bars.full[team][slot]), dst = raw + slot * 2 * L::CODES;
+    mbar_arrive_expect_tx(b, 2 * L::CODES);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+              dst + i * L::CODES),
+          "l"(&args.map), "r"(0), "r"(j0), "r"(i * a.Hkv + h), "r"(b)
+          : "memory");
+  };
+  const bool issuer = warp >= 4 * kTcTeams && lane == 0;
+
+  if (issuer)
+    for (int it = 0; it < min(mine, kTcSlots); ++it) load(it);
+  if (warp < 4 * kTcTeams) {
+    // Q as the B operand: fp16 after a scaling of each row by a power of two
+    constexpr int RP = HD / 8;  // 16-byte pieces of a row, a lane for each
+#pragma unroll
+    for (int i = 0; i < kTcRows * RP / 256; ++i) {
+      const int e = tid + i * 256, r = e / RP, piece = e % RP, row = tile * kTcRows + r;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (row < rows)
+        u = *reinterpret_cast<const uint4*>(a.q + (row / a.G) * a.q_stride + (long long)(h * a.G + row % a.G) * HD + piece * 8);
+      uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      float most = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack16(w[j], a.fp16);
+        most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
       }
 #pragma unroll
-      for (int b = 0; b < kMaxCluster; ++b)
-        if (b < a.cluster) {
-          const float f = exp2f(ms[b] - mm);
-          sum += f * ld_cluster(mapa(at + d * 4, b));
-          ll += f * ld_cluster(mapa(at + HD * 4 + 4, b));
+      for (int k = 1; k < RP; k <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, k));
+      const int sh = row_shift(most);
+      const float mul = exp2i(sh);
+      if (piece == 0) fac[r] = a.qk_scale * exp2i(-sh);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack16(w[j], a.fp16);
+        w[j] = pack_f16x2(f.x * mul, f.y * mul);
+      }
+      *reinterpret_cast<uint4*>(smem + (piece >> 3) * (kTcRows * 128) + swz(r, piece & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // columns of P that the softmax never writes
+    if (NR < kTcRows)
+      for (int e = tid & 127; e < kTcKeys * 4; e += 128)
+        *reinterpret_cast<uint4*>(tsm + L::V + swz(e >> 2, 4 + (e & 3))) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_shared();
+  }
+  __syncthreads();
+
+  if (warp < 4 * kTcTeams) {
+    const int quad = warp & 3, r = quad * 32 + lane;  // the thread's key of a step; its dimension of O^T
+    const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t tk = tl + L::A0 + team * HD / 2, ts = tl + L::S0 + team * kTcRows, to = tl + L::O0 + team * kTcRows;
+    const int id = 1 + team;  // the team's barrier
+    float l[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) l[i] = 0.f;
+    // block scales of this thread's key and value, a step ahead
+    const uint8_t* es = a.scales + (long long)h * a.max_seq * (HD / 16);
+    const long long vs = (long long)a.Hkv * a.max_seq * (HD / 16);
+    uint2 ek, ev;
+    auto scales = [&](int it) {
+      const int j = lo + (s0 + team + it * kTcTeams) * kTcKeys + r;
+      ek = ev = make_uint2(0, 0);  // (rows past the last one may hold anything, NaN scales too)
+      if (it < mine && j < n) {
+        if (HD == 128) {
+          ek = __ldg(reinterpret_cast<const uint2*>(es + (long long)j * 8));
+          ev = __ldg(reinterpret_cast<const uint2*>(es + vs + (long long)j * 8));
+        } else {
+          ek.x = __ldg(reinterpret_cast<const uint32_t*>(es + (long long)j * 4));
+          ev.x = __ldg(reinterpret_cast<const uint32_t*>(es + vs + (long long)j * 4));
         }
-      store_out(a, HD, h, row, d, sum / ll * a.v_scale);
+      }
+    };
+    scales(0);
+    // (a wait that runs out sets `abort`, after which no wait waits: the warps
+    // still come to each of the team's barriers)
+    for (int it = 0; it < mine; ++it) {
+      const int slot = it % kTcSlots, j0 = lo + (s0 + team + it * kTcTeams) * kTcKeys;
+      wait_warp(bars.full[team][slot], (it / kTcSlots) & 1);
+      const uint32_t kc = raw + slot * 2 * L::CODES + r * (HD / 2), vc = kc + L::CODES;
+      // (the copies' swizzle: piece p of row r lies at p ^ (r / 2 mod 4), of 32-byte rows at p ^ (r / 4 mod 2))
+      const uint32_t x = HD == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
+      uint4 c[PIECES];
+      uint32_t v[32];
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) c[i] = lds128(kc + ((i ^ x) << 4));
+#pragma unroll
+      for (int i = 0; i < PIECES / 2; ++i) {
+        decode64(v, c[2 * i], c[2 * i + 1], i == 0 ? ek.x : ek.y);
+        tmem_st32(tk + i * 32, v);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.kready[team]));
+      // the value, while the scores are computed
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) c[i] = lds128(vc + ((i ^ x) << 4));
+      if (it > 0) wait_warp(bars.pvdone[team], (it - 1) & 1);
+#pragma unroll
+      for (int i = 0; i < PIECES / 2; ++i) {
+        decode64(v, c[2 * i], c[2 * i + 1], i == 0 ? ev.x : ev.y);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(vbuf + i * (kTcKeys * 128) + swz(r, q)), "r"(v[4 * q]),
+                       "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                       : "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.empty[team][slot]));
+      scales(it + 1);
+      // the scores of this key
+      uint32_t hide = 0;  // tokens that do not see it
+      if (j0 < seen || j0 + kTcKeys > len)
+        for (int t = 0; t < a.T; ++t) hide |= (uint32_t)!sees(a, t, j0 + r, len) << t;
+      wait_warp(bars.sdone[team], it & 1);
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < NR / 32; ++q) {  // 32 query rows at a time
+        float y[32];
+        tmem_ld32(ts + q * 32, y);
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&fac[q * 32 + i]), m = *reinterpret_cast<const float4*>(&nm[team][q * 32 + i]);
+          y[i] = fmaf(y[i], f.x, m.x), y[i + 1] = fmaf(y[i + 1], f.y, m.y);
+          y[i + 2] = fmaf(y[i + 2], f.z, m.z), y[i + 3] = fmaf(y[i + 3], f.w, m.w);
+        }
+        if (j0 < seen || j0 + kTcKeys > len) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if ((hide >> tok[q * 32 + i]) & 1u) y[i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) most = fmaxf(most, y[i]);
+        if (team_any(id, most > 8.f)) {
+          // raise the references: the rows' maxima over the step's keys, lane i
+          // ending with row i's
+          tmem_ld32(ts + q * 32, y);
+          float z[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) z[i] = y[i] = (hide >> tok[q * 32 + i]) & 1u ? -INFINITY : y[i] * fac[q * 32 + i];
+          wmax[team][quad][q * 32 + lane] = spread32(z, lane, [](float u, float w) { return fmaxf(u, w); });
+          named_bar(id, 128);
+          if (r < 32) {
+            const int row = q * 32 + r;
+            const float old = -nm[team][row];
+            float mx = fmaxf(fmaxf(wmax[team][0][row], wmax[team][1][row]), fmaxf(wmax[team][2][row], wmax[team][3][row]));
+            mx = tok[row] == 31 ? old : fmaxf(old, mx);
+            al[team][row] = mx == -INFINITY ? 1.f : ex2(old - mx);
+            nm[team][row] = -mx;
+          }
+          named_bar(id, 128);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) l[q * 32 + i] *= al[team][q * 32 + i];
+          if (it > 0) {  // (the last step's output sums are complete: pvdone was waited for)
+            tmem_ld32(to + q * 32, z);
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(z[i] * al[team][q * 32 + i]);
+            tmem_st32(to + q * 32, w);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float m = nm[team][q * 32 + i];
+            y[i] = m == INFINITY ? -INFINITY : y[i] + m;
+          }
+          named_bar(id, 128);  // (the maxima and factors may be written again)
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          y[i] = ex2(y[i]);
+          l[q * 32 + i] += y[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(pbuf + swz(r, q * 4 + i)), "r"(pack_f16x2(y[8 * i], y[8 * i + 1])),
+                       "r"(pack_f16x2(y[8 * i + 2], y[8 * i + 3])), "r"(pack_f16x2(y[8 * i + 4], y[8 * i + 5])),
+                       "r"(pack_f16x2(y[8 * i + 6], y[8 * i + 7]))
+                       : "memory");
+      }
+      fence_proxy_async_shared();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.pready[team]));
     }
-    cluster_sync();  // (no block leaves while its sums may be read)
+    if (mine > 0) wait_warp(bars.pvdone[team], (mine - 1) & 1);
+    tc_fence_after();
+    // weights summed over the team's keys: lane i ends with a warp's sum for row i
+#pragma unroll
+    for (int q = 0; q < NR / 32; ++q) {
+      float z[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = l[q * 32 + i];
+      wmax[team][quad][q * 32 + lane] = spread32(z, lane, [](float u, float w) { return u + w; });
+    }
+  } else if (issuer) {
+    // --- a team's MMAs and copies -------------------------------------------
+    constexpr uint32_t idesc_s = (1u << 4) | ((kTcRows / 8u) << 17) | ((128u / 16) << 24);
+    constexpr uint32_t idesc_o = idesc_s | (1u << 15) | (1u << 16);  // A and B with M and N contiguous
+    const uint32_t tk = tmem + L::A0 + team * HD / 2, ts = tmem + L::S0 + team * kTcRows, to = tmem + L::O0 + team * kTcRows;
+    const uint64_t qd = umma_desc(smem_u32(smem), 16, 1024) | kSwizzle128;
+    // V: blocks of 64 dimensions 16 KB apart (64 dimensions in all: the second one is the first again)
+    const uint64_t vd = umma_desc(vbuf, HD == 128 ? kTcKeys * 128 : 0, 1024) | kSwizzle128;
+    const uint64_t pd = umma_desc(pbuf, 0, 1024) | kSwizzle128;
+    bool ok = true;
+    for (int it = 0; it < mine; ++it) {
+      ok = wait(bars.kready[team], it & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k)
+        mma_f16_ts(ts, tk + k * 8, qd + (k >> 2) * (kTcRows * 128 >> 4) + (k & 3) * 2, idesc_s, k > 0);
+      tc_commit(bar(bars.sdone[team]));
+      if (it + kTcSlots < mine) {
+        ok = wait(bars.empty[team][it % kTcSlots], (it / kTcSlots) & 1);
+        if (!ok) break;
+        load(it + kTcSlots);
+      }
+      ok = wait(bars.pready[team], it & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < kTcKeys / 16; ++k)
+        mma_f16_ss(to, vd + k * (2048 >> 4), pd + k * (2048 >> 4), idesc_o, it > 0 || k > 0);
+      tc_commit(bar(bars.pvdone[team]));
+    }
+    if (!ok) {  // what is in flight ends before the block does
+      for (int i = 0; i < kTcSlots; ++i)
+        for (uint32_t q = 0; q < 2; ++q) mbar_wait(bar(bars.full[team][i]), q, gtimer() + kOpsWaitNs / 100, &never);
+      for (uint32_t q = 0; q < 2; ++q) {
+        mbar_wait(bar(bars.sdone[team]), q, gtimer() + kOpsWaitNs / 100, &never);
+        mbar_wait(bar(bars.pvdone[team]), q, gtimer() + kOpsWaitNs / 100, &never);
+      }
+    }
   }
+  grid_dep_launch();
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+
+  // the teams joined: smem[row][PITCH] (over the first team's operands)
+  float* out = reinterpret_cast<float*>(smem + L::Q);
+  {
+    const int quad = warp & 3, d = quad * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+    const bool one = s0 < s1, two = s0 + 1 < s1;  // teams that had steps
+    for (int q = warp >> 2; q < NR / 16; q += kTcTeams) {  // 16 rows
+      if (warp >= 4 * kTcTeams) break;
+      float z0[16], z1[16];
+      if (one) tmem_ld16(tl + L::O0 + q * 16, z0);
+      if (two) tmem_ld16(tl + L::O0 + kTcRows + q * 16, z1);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = q * 16 + i;
+        const float m0 = one ? -nm[0][row] : -INFINITY, m1 = two ? -nm[1][row] : -INFINITY, mm = fmaxf(m0, m1);
+        const float ref = mm == -INFINITY ? 0.f : mm, f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
+        const float o = (one ? f0 * z0[i] : 0.f) + (two ? f1 * z1[i] : 0.f);
+        if (HD == 128 || d < HD) out[row * PITCH + d] = o;
+        if (d == 0) {
+          float s = 0.f;
+          for (int w = 0; w < 4; ++w) s += (one ? f0 * wmax[0][w][row] : 0.f) + (two ? f1 * wmax[1][w][row] : 0.f);
+          out[row * PITCH + HD] = mm, out[row * PITCH + HD + 1] = s;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_relinquish();
+    tmem_dealloc(tmem, L::COLS);
+  }
+  if (tid == 0 && abort) atomicExch(&g_error, 1u);
+  finish_block<HD, kTcRows, kTcThreads>(a, out, split, h, tile);
 }
 
 // The key ranges of a (token, query head): a block of four groups of HD
@@ -607,12 +1055,13 @@ struct Kv4Plan {
 Kv4Plan plan_attention(int tokens, int group, int Hkv, int keys) {
   Kv4Plan p{};
   const int rows = tokens * group;
-  p.tile_rows = rows <= 8 ? 8 : 16;
+  p.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : kTcRows;
   p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   p.cluster = p.splits = 1;
   if (keys <= kClusterKeys) {
-    // a block for every 128 keys (16 a warp)
-    while (p.cluster < kMaxCluster && keys > 128 * p.cluster) p.cluster *= 2;
+    // a block for every 128 keys (16 a warp), or 256 (a step for each team)
+    const int block = p.tile_rows == kTcRows ? kTcTeams * kTcKeys : 128;
+    while (p.cluster < kMaxCluster && keys > block * p.cluster) p.cluster *= 2;
   } else {
     const int per_sm = p.tile_rows == 8 ? 2 : 1;  // blocks that an SM holds
     p.splits = std::max(2, std::min(kMaxSplits, per_sm * kOpsSms / (p.tiles * Hkv)));
@@ -624,33 +1073,60 @@ size_t plan_bytes(const Kv4Plan& p, int Hkv, int hd) {
 }
 int most_keys(int tokens, int window, int len) { return std::min(len, window > 0 ? window + tokens : len) + tokens; }
 
-template <int HD, int NT>
-cudaError_t launch_rows_kernel(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st) {
-  constexpr int smem = std::max(8 * kRing * Kv16<HD>::BYTES, 8 * 8 * NT * (HD + 4) * 4 + 8 * 8 * NT * 8);
-  static bool ready[64] = {};  // (a function's attributes are set once a device; twice does no harm)
+// A kernel over (key ranges, kv heads, row tiles), its shared-memory limit set
+// once a device (`ready`; twice does no harm).
+template <typename Args>
+cudaError_t launch_blocks(void (*kernel)(Args), const Args& args, bool (&ready)[64], int threads, int smem, const Kv4Plan& p,
+                          int Hkv, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev]) {
-    e = cudaFuncSetAttribute(kv4_rows_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3((unsigned)(p.cluster * p.splits), (unsigned)a.Hkv, (unsigned)p.tiles);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3((unsigned)(p.cluster * p.splits), (unsigned)Hkv, (unsigned)p.tiles);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)p.cluster, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_rows_kernel<HD, NT>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
+template <int HD, int NT>
+cudaError_t launch_rows_kernel(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st) {
+  static bool ready[64] = {};
+  constexpr int smem = std::max(8 * kRing * Kv16<HD>::BYTES, 8 * 8 * NT * (HD + 4) * 4 + 8 * 8 * NT * 8);
+  return launch_blocks(kv4_rows_kernel<HD, NT>, a, ready, 256, smem, p, a.Hkv, st);
+}
+
+template <int HD, int NR>
+cudaError_t launch_tc_kernel(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st) {
+  static bool ready[64] = {};
+  Kv4AttnTc t{};
+  t.a = a;
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  const cuuint64_t dims[3] = {HD / 2, (cuuint64_t)a.max_seq, 2ull * a.Hkv}, pitch[2] = {HD / 2, (cuuint64_t)a.max_seq * (HD / 2)};
+  const cuuint32_t box[3] = {HD / 2, kTcKeys, 1}, es[3] = {1, 1, 1};
+  if (enc == nullptr ||
+      enc(&t.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a.codes), dims, pitch, box, es,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, HD == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  return launch_blocks(kv4_tc_kernel<HD, NR>, t, ready, kTcThreads, Tc<HD>::SMEM, p, a.Hkv, st);
 }
 
 template <int HD>
 cudaError_t launch_attention(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st) {
-  cudaError_t e = p.tile_rows == 8 ? launch_rows_kernel<HD, 1>(a, p, st) : launch_rows_kernel<HD, 2>(a, p, st);
+  cudaError_t e = p.tile_rows == 8            ? launch_rows_kernel<HD, 1>(a, p, st)
+                  : p.tile_rows == 16         ? launch_rows_kernel<HD, 2>(a, p, st)
+                  : a.T * a.G <= kTcRows / 2  ? launch_tc_kernel<HD, 32>(a, p, st)
+                                              : launch_tc_kernel<HD, 64>(a, p, st);
   if (e != cudaSuccess || p.splits == 1) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
@@ -664,6 +1140,14 @@ cudaError_t launch_attention(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st
 }
 
 }  // namespace
+
+cudaError_t kv4_error(uint32_t* e) {
+  cudaError_t r = cudaMemcpyFromSymbol(e, g_error, sizeof(*e));
+  const uint32_t zero = 0;
+  if (r == cudaSuccess && *e != 0) r = cudaMemcpyToSymbol(g_error, &zero, sizeof(zero));
+  return r;
+}
+
 }  // namespace msk
 
 using namespace msk;

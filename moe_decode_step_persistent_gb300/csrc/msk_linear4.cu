@@ -51,33 +51,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Shared-memory descriptor bits of the 128-byte swizzle (16-byte piece p of
-// row r at p ^ (r mod 8)).
-constexpr uint64_t kSwizzle128 = 2ull << 61;
-
-// D (tensor memory) = [D +] A B^T, A fp16 from tensor memory, B from shared
-// memory, fp32 accumulators, M = 128, N = 16, K = 16.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, bool accumulate) {
-  constexpr uint32_t idesc = (1u << 4) | ((16u / 8) << 17) | ((128u / 16) << 24);
-  asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
 struct Bars {  // mbarriers of a block
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t afull[kTeams][kABufs], aempty[kTeams][kABufs];
@@ -357,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
     int buf = 0, tile = 0, g = team, st = team;
     int rt = (team + a.stages) / ng, rg = (team + a.stages) % ng;  // the stage that goes where the team's next one was
     uint32_t ph = 0, sph = 0;
+    constexpr uint32_t idesc = (1u << 4) | ((16u / 8) << 17) | ((128u / 16) << 24);  // fp32 += fp16 fp16, N = 16, M = 128
     const uint32_t afull = bar(bars.afull[team][0]), aempty = bar(bars.aempty[team][0]);
     const uint32_t at0 = tmem + team * kABufs * kACols;
     bool ok = wait(bars.dempty[0], 1), fresh = true;  // (fresh: the tile's sums start from nothing)
@@ -380,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
         const uint32_t at = at0 + buf * kACols;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          mma_f16_ts(dt, at + j * 8, b + k * (kXBytes<NG> >> 4) + j * 2, k > 0 || j > 0 || !fresh);
+          mma_f16_ts(dt, at + j * 8, b + k * (kXBytes<NG> >> 4) + j * 2, idesc, k > 0 || j > 0 || !fresh);
         tc_commit(aempty + buf * 8);
         buf = buf == kABufs - 1 ? 0 : buf + 1;
         ph ^= buf == 0;
@@ -415,26 +389,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
   if (a.ks > 1) cluster_sync();  // (no block leaves while its sums may be read)
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
-
 // A row-major matrix of bytes or 16-bit words, `pitch` bytes between rows, in
 // boxes of box_rows x box_cols; what lies outside reads as zero.
 bool matrix_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, long long rows, long long cols, long long pitch,
                 int box_rows, int box_cols, CUtensorMapSwizzle swizzle) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)pitch};
   const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, es[2] = {1, 1};
-  return encoder() != nullptr &&
-         encoder()(map, type, 2, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+  return tensor_map_encoder() != nullptr &&
+         tensor_map_encoder()(map, type, 2, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -482,7 +444,7 @@ msk_status launch_linear(Lin4& a, const void* x, long long x_stride, cudaStream_
   // x as [cols / 64][tokens][64]; a box is a stage's columns
   const cuuint64_t xd[3] = {64, (cuuint64_t)a.T, (cuuint64_t)a.K / 64}, xp[2] = {(cuuint64_t)(a.T > 1 ? x_stride : a.K) * 2, 128};
   const cuuint32_t xb[3] = {64, 8 * NG, kChunks}, es[3] = {1, 1, 1};
-  if (encoder()(&a.x_map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(x), xd, xp, xb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  if (tensor_map_encoder()(&a.x_map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(x), xd, xp, xb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return MSK_ERR_CUDA;
   const int xbytes = per * kChunks * kXBytes<NG>, pbytes = a.ks > 1 ? kPartBytes : 0;
@@ -501,6 +463,8 @@ msk_status launch_linear(Lin4& a, const void* x, long long x_stride, cudaStream_
 }
 
 }  // namespace
+
+cudaError_t kv4_error(uint32_t* e);  // (msk_kv4.cu)
 
 cudaError_t linear4_error(uint32_t* e) {
   cudaError_t r = cudaMemcpyFromSymbol(e, g_error, sizeof(*e));
@@ -547,7 +511,7 @@ extern "C" msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_s
 
 extern "C" msk_status msk_ops_check(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MSK_ERR_CUDA;
-  uint32_t e = 0;
-  if (linear4_error(&e) != cudaSuccess) return MSK_ERR_CUDA;
-  return e ? MSK_ERR_TIMEOUT : MSK_OK;
+  uint32_t e = 0, f = 0;
+  if (linear4_error(&e) != cudaSuccess || kv4_error(&f) != cudaSuccess) return MSK_ERR_CUDA;
+  return e || f ? MSK_ERR_TIMEOUT : MSK_OK;
 }

@@ -4,11 +4,14 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include "../../include/msk.h"
 #include "msk_device.cuh"
 
 namespace msk {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // (msk_api.cu)
 
 inline bool ops_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int dtype_bytes(int32_t t) { return t == MSK_FP32 ? 4 : 2; }
