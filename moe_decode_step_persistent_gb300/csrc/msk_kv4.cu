@@ -258,52 +258,65 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
   return v;
 }
 
+// Four elements of an output row.
+__device__ __forceinline__ void store_out4(const Kv4Attn& a, int hd, int h, int row, int d, float4 y) {
+  uint16_t* p = a.out + ((long long)(row / a.G) * a.Hq + h * a.G + row % a.G) * hd + d;
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack16(y.x, y.y, a.fp16), pack16(y.z, y.w, a.fp16));
+}
+
 // The end of an attention block: its sums, smem[row][PITCH] with the reference
 // and the sum of weights behind each row's elements, go to the workspace, or
-// through the cluster's shared memory, or straight to the output.
+// through the cluster's shared memory, or straight to the output.  A block of a
+// cluster takes the rows rank, rank + cluster, ...
 template <int HD, int ROWS, int THREADS>
 __device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, int split, int h, int tile) {
-  constexpr int PITCH = HD + 4;
-  const int rows = a.T * a.G;
+  constexpr int PITCH = HD + 4, Q4 = HD / 4;
+  __shared__ float part_f[ROWS][kMaxCluster];  // a block's share of a row's output
+  const int rows = min(ROWS, a.T * a.G - tile * ROWS), tid = threadIdx.x;
   if (a.splits > 1) {
     const long long part = (((long long)tile * a.Hkv + h) * a.splits + split) * ROWS;
-    for (int e = threadIdx.x; e < ROWS * HD; e += THREADS) {
-      const int r = e / HD, d = e % HD;
-      if (tile * ROWS + r >= rows) break;
-      a.o_part[(part + r) * HD + d] = smem[r * PITCH + d];
-      if (d == 0) a.ml_part[part + r] = make_float2(smem[r * PITCH + HD], smem[r * PITCH + HD + 1]);
+    for (int e = tid; e < rows * Q4; e += THREADS) {
+      const int r = e / Q4, q = e % Q4;
+      *reinterpret_cast<float4*>(a.o_part + (part + r) * HD + q * 4) = *reinterpret_cast<const float4*>(smem + r * PITCH + q * 4);
     }
+    for (int r = tid; r < rows; r += THREADS) a.ml_part[part + r] = make_float2(smem[r * PITCH + HD], smem[r * PITCH + HD + 1]);
     return;
   }
-  if (a.cluster == 1) {
-    for (int e = threadIdx.x; e < ROWS * HD; e += THREADS) {
-      const int r = e / HD, d = e % HD, row = tile * ROWS + r;
-      if (row >= rows) break;
-      store_out(a, HD, h, row, d, smem[r * PITCH + d] / smem[r * PITCH + HD + 1] * a.v_scale);
-    }
-    return;
-  }
-  cluster_sync();
-  for (int e = split * THREADS + threadIdx.x; e < ROWS * HD; e += a.cluster * THREADS) {
-    const int r = e / HD, d = e % HD, row = tile * ROWS + r;
-    if (row >= rows) break;
-    const uint32_t at = smem_u32(smem + r * PITCH);
-    float ms[kMaxCluster], mm = -INFINITY, sum = 0.f, ll = 0.f;
+  if (a.cluster > 1) cluster_sync();
+  const int step = a.cluster, first = a.cluster > 1 ? split : 0;
+  for (int r = first + tid * step; r < rows; r += THREADS * step) {
+    const uint32_t at = smem_u32(smem + r * PITCH + HD);
+    float m[kMaxCluster], l[kMaxCluster], mm = -INFINITY, ll = 0.f;
 #pragma unroll
     for (int b = 0; b < kMaxCluster; ++b) {
-      ms[b] = b < a.cluster ? ld_cluster(mapa(at + HD * 4, b)) : -INFINITY;
-      mm = fmaxf(mm, ms[b]);
+      m[b] = b < a.cluster ? ld_cluster(mapa(at, b)) : -INFINITY;
+      l[b] = b < a.cluster ? ld_cluster(mapa(at + 4, b)) : 0.f;
+      mm = fmaxf(mm, m[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < kMaxCluster; ++b) m[b] = ex2(m[b] - mm), ll += m[b] * l[b];
+#pragma unroll
+    for (int b = 0; b < kMaxCluster; ++b) part_f[r][b] = m[b] / ll * a.v_scale;
+  }
+  __syncthreads();
+  for (int e = tid; e < (rows - first + step - 1) / step * Q4; e += THREADS) {
+    const int r = first + e / Q4 * step, q = e % Q4;
+    const uint32_t at = smem_u32(smem + r * PITCH + q * 4);
+    float4 v[kMaxCluster], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int b = 0; b < kMaxCluster; ++b) {
+      v[b] = y;
+      if (b < a.cluster) v[b] = ld_cluster4(mapa(at, b));
     }
 #pragma unroll
     for (int b = 0; b < kMaxCluster; ++b)
       if (b < a.cluster) {
-        const float f = ex2(ms[b] - mm);
-        sum += f * ld_cluster(mapa(at + d * 4, b));
-        ll += f * ld_cluster(mapa(at + HD * 4 + 4, b));
+        const float f = part_f[r][b];
+        y.x += f * v[b].x, y.y += f * v[b].y, y.z += f * v[b].z, y.w += f * v[b].w;
       }
-    store_out(a, HD, h, row, d, sum / ll * a.v_scale);
+    store_out4(a, HD, h, tile * ROWS + r, q * 4, y);
   }
-  cluster_sync();  // (no block leaves while its sums may be read)
+  if (a.cluster > 1) cluster_sync();  // (no block leaves while its sums may be read)
 }
 
 // Few query rows (8 NT of them in a tile; row = token * group + head of the
@@ -596,8 +609,9 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
 
 constexpr int kTcRows = 64;    // query rows of a tile (the MMAs' N)
 constexpr int kTcKeys = 128;   // keys of a step (the MMAs' M, and K)
-constexpr int kTcTeams = 2;    // teams of four warps that take the steps in turn
-constexpr int kTcThreads = 32 * (4 * kTcTeams + kTcTeams);
+constexpr int kTcTeams = 2;    // teams of eight warps that take the steps in turn
+constexpr int kTcWorkers = 8 * kTcTeams;
+constexpr int kTcThreads = 32 * (kTcWorkers + kTcTeams);
 constexpr int kTcSlots = 2;    // steps that a team has in shared memory
 static __device__ uint32_t g_error;  // nonzero once a wait has run out
 
@@ -623,8 +637,8 @@ struct Kv4AttnTc {
   Kv4Attn a;
 };
 
-// OR of a truth value over a team (a barrier of its 128 threads).
-__device__ __forceinline__ bool team_any(int id, bool v) {
+// OR of a truth value over four warps (a barrier of their 128 threads).
+__device__ __forceinline__ bool half_any(int id, bool v) {
   uint32_t r;
   asm volatile(
       "{ .reg .pred p, q; setp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q; }"
@@ -637,11 +651,16 @@ __device__ __forceinline__ bool team_any(int id, bool v) {
 // Row of 16-byte pieces with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t piece) { return row * 128 + (((piece ^ row) & 7) << 4); }
 
-// 32 values a lane, combined over the lanes: lane i gets value i's result.
-template <typename F>
-__device__ __forceinline__ float spread32(float (&z)[32], int lane, F f) {
+// N values a lane (32 or 16), combined over the lanes: lane i gets value i mod
+// N's result.
+template <int N, typename F>
+__device__ __forceinline__ float spread(float (&z)[N], int lane, F f) {
+  if (N == 16) {
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
+    for (int i = 0; i < N; ++i) z[i] = f(z[i], __shfl_xor_sync(0xFFFFFFFFu, z[i], 16));
+  }
+#pragma unroll
+  for (int w = N / 2; w > 0; w >>= 1) {
     const bool up = lane & w;
 #pragma unroll
     for (int i = 0; i < w; ++i) {
@@ -652,30 +671,47 @@ __device__ __forceinline__ float spread32(float (&z)[32], int lane, F f) {
   return z[0];
 }
 
-// 64 elements decoded to fp16: 32 bytes of codes, four block scales.
-__device__ __forceinline__ void decode64(uint32_t (&v)[32], const uint4& c0, const uint4& c1, uint32_t e) {
-  const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+// 32 N elements decoded to fp16: N 16-byte pieces of codes, two block scales
+// each.
+template <int N>
+__device__ __forceinline__ void decode_codes(uint32_t (&v)[32], const uint4 (&c)[2], uint32_t e) {
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const uint32_t f = f16x2_bcast(e4m3_pair_to_f16x2(e, b >> 1), b & 1);
+  for (int i = 0; i < N; ++i) {
+    const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[b * 8 + j] = hmul2(e2m1_byte_to_f16x2(w[2 * b + (j >> 2)], j & 3), f);
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t f = f16x2_bcast(e4m3_pair_to_f16x2(e, i), b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i * 16 + b * 8 + j] = hmul2(e2m1_byte_to_f16x2(w[2 * b + (j >> 2)], j & 3), f);
+    }
   }
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[N]) {
+  if constexpr (N == 32) tmem_ld32(at, v);
+  else tmem_ld16(at, v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N]) {
+  if constexpr (N == 32) tmem_st32(at, v);
+  else tmem_st16(at, v);
 }
 
 // Up to 64 query rows of a kv head at once: S^T = K Q^T (M = 128 keys, N = 64
 // rows, K = HD) and O^T = V^T P^T (M = HD, N = 64, K = 128 keys), fp16 operands,
 // fp32 accumulators in tensor memory.
 //
-// Two teams of four warps take steps of 128 keys in turn, a thread for a key:
-// it decodes the key into the A operand in tensor memory (exactly), the value
-// into shared memory while the scores are computed, then takes its key's 64
-// scores, turns them into weights and writes them as the B operand.  Each team
-// has a softmax of its own (reference, sums, output sums); the two are joined at
-// the end.  A warp for each team issues its MMAs and copies.  The reference of
-// a row is raised when a score passes it by 2^8, and the sums rescaled: a few
-// times in all.  On mma.sync 64 rows cost four times the decoding or do not fit
-// the registers: 53 us for 16 tokens over 32768 keys.
+// Two teams of eight warps take steps of 128 keys in turn, two threads for a
+// key: each decodes half of the key's dimensions into the A operand in tensor
+// memory (exactly) and half of the value's into shared memory while the scores
+// are computed, then takes its half of the query rows: the key's scores, turned
+// into weights and written as the B operand.  Each team has a softmax of its own
+// (references, sums, output sums); the two are joined at the end.  A warp for
+// each team issues its MMAs and copies.  The reference of a row is raised when a
+// score passes it by 2^8, and the sums rescaled: a few times in all.  On mma.sync
+// 64 rows cost four times the decoding or do not fit the registers: 53 us for
+// 16 tokens over 32768 keys.
 //
 // NR: rows of the 64 that are in use, 32 or 64 (the softmax skips the rest).
 template <int HD, int NR>
@@ -687,6 +723,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   __shared__ __align__(16) float nm[kTcTeams][kTcRows];   // the references' negatives (+inf: none yet)
   __shared__ __align__(16) float al[kTcTeams][kTcRows];   // factors of a rescaling
   __shared__ float wmax[kTcTeams][4][kTcRows];            // a warp's maxima; its sums at the end
+  __shared__ float jf[kTcTeams][kTcRows];                 // a team's share when the two are joined
   __shared__ __align__(16) float fac[kTcRows];            // a row's scores in log2 units: times this
   __shared__ uint32_t tmem_base;
   __shared__ uint8_t tok[kTcRows];                        // a row's token, 31 past the last row
@@ -710,9 +747,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   if (tid == 0) {
     abort = 0, never = 0;
     for (int t = 0; t < kTcTeams; ++t) {
-      for (int i = 0; i < kTcSlots; ++i) mbar_init(bar(bars.full[t][i]), 1), mbar_init(bar(bars.empty[t][i]), 4);
-      mbar_init(bar(bars.kready[t]), 4), mbar_init(bar(bars.sdone[t]), 1);
-      mbar_init(bar(bars.pready[t]), 4), mbar_init(bar(bars.pvdone[t]), 1);
+      for (int i = 0; i < kTcSlots; ++i) mbar_init(bar(bars.full[t][i]), 1), mbar_init(bar(bars.empty[t][i]), 8);
+      mbar_init(bar(bars.kready[t]), 8), mbar_init(bar(bars.sdone[t]), 1);
+      mbar_init(bar(bars.pready[t]), 8), mbar_init(bar(bars.pvdone[t]), 1);
     }
     mbar_fence_init();
   }
@@ -734,7 +771,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   };
   auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
 
-  const int team = warp < 4 * kTcTeams ? warp >> 2 : warp - 4 * kTcTeams;
+  const int team = warp < kTcWorkers ? warp >> 3 : warp - kTcWorkers;
   const int mine = max(0, (s1 - s0 - team + kTcTeams - 1) / kTcTeams);  // this team's steps
   uint8_t* tsm = smem + L::Q + team * L::TEAM;
   const uint32_t vbuf = smem_u32(tsm), pbuf = vbuf + L::V, raw = pbuf + L::P;
@@ -750,16 +787,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
           "l"(&args.map), "r"(0), "r"(j0), "r"(i * a.Hkv + h), "r"(b)
           : "memory");
   };
-  const bool issuer = warp >= 4 * kTcTeams && lane == 0;
+  const bool issuer = warp >= kTcWorkers && lane == 0;
 
   if (issuer)
     for (int it = 0; it < min(mine, kTcSlots); ++it) load(it);
-  if (warp < 4 * kTcTeams) {
+  if (warp < kTcWorkers) {
     // Q as the B operand: fp16 after a scaling of each row by a power of two
     constexpr int RP = HD / 8;  // 16-byte pieces of a row, a lane for each
 #pragma unroll
-    for (int i = 0; i < kTcRows * RP / 256; ++i) {
-      const int e = tid + i * 256, r = e / RP, piece = e % RP, row = tile * kTcRows + r;
+    for (int i = 0; i < kTcRows * RP / (32 * kTcWorkers); ++i) {
+      const int e = tid + i * 32 * kTcWorkers, r = e / RP, piece = e % RP, row = tile * kTcRows + r;
       uint4 u = make_uint4(0, 0, 0, 0);
       if (row < rows)
         u = *reinterpret_cast<const uint4*>(a.q + (row / a.G) * a.q_stride + (long long)(h * a.G + row % a.G) * HD + piece * 8);
@@ -784,34 +821,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
     }
     // columns of P that the softmax never writes
     if (NR < kTcRows)
-      for (int e = tid & 127; e < kTcKeys * 4; e += 128)
+      for (int e = tid & 255; e < kTcKeys * 4; e += 256)
         *reinterpret_cast<uint4*>(tsm + L::V + swz(e >> 2, 4 + (e & 3))) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_shared();
   }
   __syncthreads();
 
-  if (warp < 4 * kTcTeams) {
-    const int quad = warp & 3, r = quad * 32 + lane;  // the thread's key of a step; its dimension of O^T
+  if (warp < kTcWorkers) {
+    constexpr int RW = NR / 2, CP = PIECES / 2;  // query rows, pieces of codes of a thread
+    const int quad = warp & 3, half = (warp >> 2) & 1, r = quad * 32 + lane;  // r: the thread's key of a step
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t tk = tl + L::A0 + team * HD / 2, ts = tl + L::S0 + team * kTcRows, to = tl + L::O0 + team * kTcRows;
-    const int id = 1 + team;  // the team's barrier
-    float l[NR];
+    const uint32_t tk = tl + L::A0 + team * HD / 2 + half * HD / 4, ts = tl + L::S0 + team * kTcRows + half * RW;
+    const uint32_t to = tl + L::O0 + team * kTcRows + half * RW;
+    const int id = 1 + 2 * team + half;  // the barrier of the four warps with the same rows
+    const float* hfac = fac + half * RW;
+    float *hnm = nm[team] + half * RW, *hal = al[team] + half * RW;
+    const uint8_t* htok = tok + half * RW;
+    float l[RW];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) l[i] = 0.f;
+    for (int i = 0; i < RW; ++i) l[i] = 0.f;
     // block scales of this thread's key and value, a step ahead
-    const uint8_t* es = a.scales + (long long)h * a.max_seq * (HD / 16);
+    const uint8_t* es = a.scales + (long long)h * a.max_seq * (HD / 16) + half * (HD / 32);
     const long long vs = (long long)a.Hkv * a.max_seq * (HD / 16);
-    uint2 ek, ev;
+    uint32_t ek, ev;
     auto scales = [&](int it) {
       const int j = lo + (s0 + team + it * kTcTeams) * kTcKeys + r;
-      ek = ev = make_uint2(0, 0);  // (rows past the last one may hold anything, NaN scales too)
+      ek = ev = 0;  // (rows past the last one may hold anything, NaN scales too)
       if (it < mine && j < n) {
+        const uint8_t* p = es + (long long)j * (HD / 16);
         if (HD == 128) {
-          ek = __ldg(reinterpret_cast<const uint2*>(es + (long long)j * 8));
-          ev = __ldg(reinterpret_cast<const uint2*>(es + vs + (long long)j * 8));
+          ek = __ldg(reinterpret_cast<const uint32_t*>(p));
+          ev = __ldg(reinterpret_cast<const uint32_t*>(p + vs));
         } else {
-          ek.x = __ldg(reinterpret_cast<const uint32_t*>(es + (long long)j * 4));
-          ev.x = __ldg(reinterpret_cast<const uint32_t*>(es + vs + (long long)j * 4));
+          ek = __ldg(reinterpret_cast<const uint16_t*>(p));
+          ev = __ldg(reinterpret_cast<const uint16_t*>(p + vs));
         }
       }
     };
@@ -824,30 +867,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
       const uint32_t kc = raw + slot * 2 * L::CODES + r * (HD / 2), vc = kc + L::CODES;
       // (the copies' swizzle: piece p of row r lies at p ^ (r / 2 mod 4), of 32-byte rows at p ^ (r / 4 mod 2))
       const uint32_t x = HD == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
-      uint4 c[PIECES];
+      uint4 c[2];
       uint32_t v[32];
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) c[i] = lds128(kc + ((i ^ x) << 4));
-#pragma unroll
-      for (int i = 0; i < PIECES / 2; ++i) {
-        decode64(v, c[2 * i], c[2 * i + 1], i == 0 ? ek.x : ek.y);
-        tmem_st32(tk + i * 32, v);
-      }
+      for (int i = 0; i < CP; ++i) c[i] = lds128(kc + (((half * CP + i) ^ x) << 4));
+      decode_codes<CP>(v, c, ek);
+      if (HD == 128) tmem_st32(tk, v);
+      else tmem_st16(tk, reinterpret_cast<const uint32_t(&)[16]>(v));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars.kready[team]));
       // the value, while the scores are computed
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) c[i] = lds128(vc + ((i ^ x) << 4));
+      for (int i = 0; i < CP; ++i) c[i] = lds128(vc + (((half * CP + i) ^ x) << 4));
+      decode_codes<CP>(v, c, ev);
       if (it > 0) wait_warp(bars.pvdone[team], (it - 1) & 1);
 #pragma unroll
-      for (int i = 0; i < PIECES / 2; ++i) {
-        decode64(v, c[2 * i], c[2 * i + 1], i == 0 ? ev.x : ev.y);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(vbuf + i * (kTcKeys * 128) + swz(r, q)), "r"(v[4 * q]),
-                       "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
-                       : "memory");
+      for (int q = 0; q < 4 * CP; ++q) {  // 8 dimensions
+        const int piece = half * 4 * CP + q;
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(vbuf + (piece >> 3) * (kTcKeys * 128) + swz(r, piece & 7)),
+                     "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                     : "memory");
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars.empty[team][slot]));
@@ -858,70 +898,67 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
         for (int t = 0; t < a.T; ++t) hide |= (uint32_t)!sees(a, t, j0 + r, len) << t;
       wait_warp(bars.sdone[team], it & 1);
       tc_fence_after();
+      const bool edge = j0 < seen || j0 + kTcKeys > len;
+      float y[RW];
+      auto scores = [&]() {  // in log2 units, relative to the references
+        tmem_ld<RW>(ts, y);
 #pragma unroll
-      for (int q = 0; q < NR / 32; ++q) {  // 32 query rows at a time
-        float y[32];
-        tmem_ld32(ts + q * 32, y);
-        float most = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&fac[q * 32 + i]), m = *reinterpret_cast<const float4*>(&nm[team][q * 32 + i]);
+        for (int i = 0; i < RW; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(hfac + i), m = *reinterpret_cast<const float4*>(hnm + i);
           y[i] = fmaf(y[i], f.x, m.x), y[i + 1] = fmaf(y[i + 1], f.y, m.y);
           y[i + 2] = fmaf(y[i + 2], f.z, m.z), y[i + 3] = fmaf(y[i + 3], f.w, m.w);
         }
-        if (j0 < seen || j0 + kTcKeys > len) {
+        if (edge) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if ((hide >> tok[q * 32 + i]) & 1u) y[i] = -INFINITY;
+          for (int i = 0; i < RW; ++i)
+            if ((hide >> htok[i]) & 1u) y[i] = -INFINITY;
         }
+      };
+      scores();
+      float most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) most = fmaxf(most, y[i]);
-        if (team_any(id, most > 8.f)) {
-          // raise the references: the rows' maxima over the step's keys, lane i
-          // ending with row i's
-          tmem_ld32(ts + q * 32, y);
-          float z[32];
+      for (int i = 0; i < RW; ++i) most = fmaxf(most, y[i]);
+      if (half_any(id, most > 8.f)) {
+        // raise the references: the rows' maxima over the step's keys, lane i
+        // ending with row i's
+        tmem_ld<RW>(ts, y);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = y[i] = (hide >> tok[q * 32 + i]) & 1u ? -INFINITY : y[i] * fac[q * 32 + i];
-          wmax[team][quad][q * 32 + lane] = spread32(z, lane, [](float u, float w) { return fmaxf(u, w); });
-          named_bar(id, 128);
-          if (r < 32) {
-            const int row = q * 32 + r;
-            const float old = -nm[team][row];
-            float mx = fmaxf(fmaxf(wmax[team][0][row], wmax[team][1][row]), fmaxf(wmax[team][2][row], wmax[team][3][row]));
-            mx = tok[row] == 31 ? old : fmaxf(old, mx);
-            al[team][row] = mx == -INFINITY ? 1.f : ex2(old - mx);
-            nm[team][row] = -mx;
-          }
-          named_bar(id, 128);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) l[q * 32 + i] *= al[team][q * 32 + i];
-          if (it > 0) {  // (the last step's output sums are complete: pvdone was waited for)
-            tmem_ld32(to + q * 32, z);
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(z[i] * al[team][q * 32 + i]);
-            tmem_st32(to + q * 32, w);
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float m = nm[team][q * 32 + i];
-            y[i] = m == INFINITY ? -INFINITY : y[i] + m;
-          }
-          named_bar(id, 128);  // (the maxima and factors may be written again)
+        for (int i = 0; i < RW; ++i) y[i] = (hide >> htok[i]) & 1u ? -INFINITY : y[i] * hfac[i];
+        const float zm = spread(y, lane, [](float u, float w) { return fmaxf(u, w); });
+        if (lane < RW) wmax[team][quad][half * RW + lane] = zm;
+        named_bar(id, 128);
+        if (r < RW) {
+          const int row = half * RW + r;
+          const float old = -hnm[r];
+          float mx = fmaxf(fmaxf(wmax[team][0][row], wmax[team][1][row]), fmaxf(wmax[team][2][row], wmax[team][3][row]));
+          mx = htok[r] == 31 ? old : fmaxf(old, mx);
+          hal[r] = mx == -INFINITY ? 1.f : ex2(old - mx);
+          hnm[r] = -mx;
         }
+        named_bar(id, 128);
+        if (it > 0) {  // (the last step's output sums are complete: pvdone was waited for)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          y[i] = ex2(y[i]);
-          l[q * 32 + i] += y[i];
+          for (int i = 0; i < RW; ++i) l[i] *= hal[i];
+          tmem_ld<RW>(to, y);
+          uint32_t w[RW];
+#pragma unroll
+          for (int i = 0; i < RW; ++i) w[i] = __float_as_uint(y[i] * hal[i]);
+          tmem_st<RW>(to, w);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(pbuf + swz(r, q * 4 + i)), "r"(pack_f16x2(y[8 * i], y[8 * i + 1])),
-                       "r"(pack_f16x2(y[8 * i + 2], y[8 * i + 3])), "r"(pack_f16x2(y[8 * i + 4], y[8 * i + 5])),
-                       "r"(pack_f16x2(y[8 * i + 6], y[8 * i + 7]))
-                       : "memory");
+        scores();  // (a row still without a reference sees none of these keys)
+        named_bar(id, 128);  // (the maxima and factors may be written again)
       }
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        y[i] = ex2(y[i]);
+        l[i] += y[i];
+      }
+#pragma unroll
+      for (int i = 0; i < RW / 8; ++i)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(pbuf + swz(r, half * (RW / 8) + i)),
+                     "r"(pack_f16x2(y[8 * i], y[8 * i + 1])), "r"(pack_f16x2(y[8 * i + 2], y[8 * i + 3])),
+                     "r"(pack_f16x2(y[8 * i + 4], y[8 * i + 5])), "r"(pack_f16x2(y[8 * i + 6], y[8 * i + 7]))
+                     : "memory");
       fence_proxy_async_shared();
       tc_fence_before();
       __syncwarp();
@@ -929,14 +966,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
     }
     if (mine > 0) wait_warp(bars.pvdone[team], (mine - 1) & 1);
     tc_fence_after();
-    // weights summed over the team's keys: lane i ends with a warp's sum for row i
-#pragma unroll
-    for (int q = 0; q < NR / 32; ++q) {
-      float z[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = l[q * 32 + i];
-      wmax[team][quad][q * 32 + lane] = spread32(z, lane, [](float u, float w) { return u + w; });
-    }
+    // weights summed over the team's keys: lane i ends with its warp's sum for row i
+    const float ls = spread(l, lane, [](float u, float w) { return u + w; });
+    if (lane < RW) wmax[team][quad][half * RW + lane] = ls;
   } else if (issuer) {
     // --- a team's MMAs and copies -------------------------------------------
     constexpr uint32_t idesc_s = (1u << 4) | ((kTcRows / 8u) << 17) | ((128u / 16) << 24);
@@ -984,28 +1016,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
 
   // the teams joined: smem[row][PITCH] (over the first team's operands)
   float* out = reinterpret_cast<float*>(smem + L::Q);
-  {
-    const int quad = warp & 3, d = quad * 32 + lane;
-    const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-    const bool one = s0 < s1, two = s0 + 1 < s1;  // teams that had steps
-    for (int q = warp >> 2; q < NR / 16; q += kTcTeams) {  // 16 rows
-      if (warp >= 4 * kTcTeams) break;
-      float z0[16], z1[16];
-      if (one) tmem_ld16(tl + L::O0 + q * 16, z0);
-      if (two) tmem_ld16(tl + L::O0 + kTcRows + q * 16, z1);
+  const bool one = s0 < s1, two = s0 + 1 < s1;  // teams that had steps
+  if (tid < NR) {
+    const float m0 = one ? -nm[0][tid] : -INFINITY, m1 = two ? -nm[1][tid] : -INFINITY, mm = fmaxf(m0, m1);
+    const float ref = mm == -INFINITY ? 0.f : mm, f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
+    jf[0][tid] = f0, jf[1][tid] = f1;
+    float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int row = q * 16 + i;
-        const float m0 = one ? -nm[0][row] : -INFINITY, m1 = two ? -nm[1][row] : -INFINITY, mm = fmaxf(m0, m1);
-        const float ref = mm == -INFINITY ? 0.f : mm, f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
-        const float o = (one ? f0 * z0[i] : 0.f) + (two ? f1 * z1[i] : 0.f);
-        if (HD == 128 || d < HD) out[row * PITCH + d] = o;
-        if (d == 0) {
-          float s = 0.f;
-          for (int w = 0; w < 4; ++w) s += (one ? f0 * wmax[0][w][row] : 0.f) + (two ? f1 * wmax[1][w][row] : 0.f);
-          out[row * PITCH + HD] = mm, out[row * PITCH + HD + 1] = s;
-        }
-      }
+    for (int w = 0; w < 4; ++w) s += (one ? f0 * wmax[0][w][tid] : 0.f) + (two ? f1 * wmax[1][w][tid] : 0.f);
+    out[tid * PITCH + HD] = mm, out[tid * PITCH + HD + 1] = s;
+  }
+  __syncthreads();
+  if (warp < 4 * (NR / 16)) {  // 16 rows a warp
+    const int quad = warp & 3, d = quad * 32 + lane, q = (warp >> 2) * 16;
+    const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+    float z0[16], z1[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z0[i] = z1[i] = 0.f;
+    if (one) tmem_ld16(tl + L::O0 + q, z0);
+    if (two) tmem_ld16(tl + L::O0 + kTcRows + q, z1);
+    if (HD == 128 || d < HD) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) out[(q + i) * PITCH + d] = jf[0][q + i] * z0[i] + jf[1][q + i] * z1[i];
     }
   }
   tc_fence_before();
