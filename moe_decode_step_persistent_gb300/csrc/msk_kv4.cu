@@ -27,110 +27,141 @@ struct Kv4Rows {
   float k_scale, v_scale;
 };
 
-// 16 consecutive elements of type T as floats.
+// 8 consecutive elements of type DT as floats.
 template <int DT>
-__device__ __forceinline__ void load16(const void* base, long long off, float (&x)[16]) {
+__device__ __forceinline__ void load8(const void* base, long long off, float (&x)[8]) {
   if (DT == MSK_FP32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = __ldg(p + i);
-      x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
-    }
+    const float4 f = __ldg(p), g = __ldg(p + 1);
+    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w, x[4] = g.x, x[5] = g.y, x[6] = g.z, x[7] = g.w;
   } else {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 u = __ldg(p + i);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack16(w[j], DT == MSK_FP16);
-        x[8 * i + 2 * j] = f.x, x[8 * i + 2 * j + 1] = f.y;
-      }
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack16(w[j], DT == MSK_FP16);
+      x[2 * j] = f.x, x[2 * j + 1] = f.y;
     }
   }
 }
 
-// One thread per block of 16 elements: two 16-byte loads (of 16-bit rows),
-// one 8-byte and one 1-byte store.  Bound by DRAM for long conversions and by
+// x / d rounded to nearest, y the rounded reciprocal of d, quotient and
+// remainder within the normal range: Markstein's correction of x y by its
+// remainder (IBM J. Res. Dev. 34, 1990).  The codes depend on the quotient's
+// last bit where it lies half way between two of them.
+__device__ __forceinline__ float quotient(float x, float d, float y) {
+  const float q = x * y;
+  return fmaf(fmaf(-q, d, x), y, q);
+}
+
+constexpr int kRowsUnroll = 4;  // pieces of a thread
+
+// A thread takes 8 elements (16 bytes of 16-bit rows), kRowsUnroll times: two
+// neighbours share a block's scale.  blockIdx.y is K's and then V's heads; the
+// pieces of a head are consecutive.  Bound by DRAM for long conversions and by
 // the launch for a step's 16 rows.
 template <int HD, int DT>
 __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4Rows a) {
-  constexpr int NB = HD / 16;
-  const long long idx = blockIdx.x * 256ll + threadIdx.x;
-  const int b = (int)(idx % NB);
-  const long long r = idx / NB;  // ((kv * Hkv) + h) * tokens + t
-  if (r >= 2ll * a.Hkv * a.tokens) return;
-  const int t = (int)(r % a.tokens);
-  const int kvh = (int)(r / a.tokens);
-  const int h = kvh % a.Hkv;
+  constexpr int NP = HD / 8;
+  const int kvh = blockIdx.y, h = kvh < a.Hkv ? kvh : kvh - a.Hkv;
   const bool is_v = kvh >= a.Hkv;
-  float x[16];
-  load16<DT>(is_v ? a.v : a.k, t * a.token_stride + h * a.head_stride + b * 16, x);
-  const float ts = is_v ? a.v_scale : a.k_scale;
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    x[i] = __fdiv_rn(x[i], ts);
-    amax = fmaxf(amax, fabsf(x[i]));
-  }
-  const uint32_t sc = f32_to_e4m3(__fdiv_rn(amax, 6.0f));
-  const float dec = e4m3_to_f32(sc);
-  uint32_t w[2] = {0u, 0u};
-  if (dec > 0.f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i >> 2] |= f32x2_to_e2m1x2(__fdiv_rn(x[2 * i], dec), __fdiv_rn(x[2 * i + 1], dec)) << (8 * (i & 3));
-  }
+  const void* src = is_v ? a.v : a.k;
+  const float ts = is_v ? a.v_scale : a.k_scale, yts = __frcp_rn(ts);
+  const bool plain = ts > 1e-18f && ts < 1e18f;
   int pos0 = a.pos0;
   if (a.pos0_dev) pos0 = max(0, min(*a.pos0_dev, a.max_seq - a.tokens));
-  const long long row = (long long)kvh * a.max_seq + pos0 + t;
-  *reinterpret_cast<uint2*>(a.codes + row * (HD / 2) + b * 8) = make_uint2(w[0], w[1]);
-  a.scales[row * NB + b] = (uint8_t)sc;
+  const long long n = (long long)a.tokens * NP, i0 = (long long)blockIdx.x * (256 * kRowsUnroll) + threadIdx.x;
+  float x[kRowsUnroll][8];
+#pragma unroll
+  for (int k = 0; k < kRowsUnroll; ++k) {
+    const long long i = i0 + k * 256;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
+    if (i < n) load8<DT>(src, i / NP * a.token_stride + h * a.head_stride + i % NP * 8, x[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kRowsUnroll; ++k) {
+    const long long i = i0 + k * 256;
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[k][j]));
+    if (ts != 1.f) {
+      const bool fast = plain && amax < 1e18f;  // (smaller quotients than normal ones leave codes of 0)
+      amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[k][j] = fast ? quotient(x[k][j], ts, yts) : __fdiv_rn(x[k][j], ts);
+        amax = fmaxf(amax, fabsf(x[k][j]));
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));  // (pieces of a block have neighbouring lanes)
+    const uint32_t sc = f32_to_e4m3(__fdiv_rn(amax, 6.0f));
+    const float dec = e4m3_to_f32(sc);
+    uint32_t w = 0;
+    if (amax > 2688.f) {  // saturates, with infinities perhaps
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w |= f32x2_to_e2m1x2(__fdiv_rn(x[k][2 * j], dec), __fdiv_rn(x[k][2 * j + 1], dec)) << (8 * j);
+    } else if (dec > 0.f) {
+      const float y = __frcp_rn(dec);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w |= f32x2_to_e2m1x2(quotient(x[k][2 * j], dec, y), quotient(x[k][2 * j + 1], dec, y)) << (8 * j);
+    }
+    if (i < n) {
+      const long long at = ((long long)kvh * a.max_seq + pos0) * NP + i;  // (rows of a head are consecutive)
+      *reinterpret_cast<uint32_t*>(a.codes + at * 4) = w;
+      if ((i & 1) == 0) a.scales[at >> 1] = (uint8_t)sc;
+    }
+  }
 }
 
 template <int HD, int DT>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4Rows a) {
-  constexpr int NB = HD / 16;
-  const long long idx = blockIdx.x * 256ll + threadIdx.x;
-  const int b = (int)(idx % NB);
-  const long long r = idx / NB;
-  if (r >= 2ll * a.Hkv * a.tokens) return;
-  const int t = (int)(r % a.tokens);
-  const int kvh = (int)(r / a.tokens);
-  const int h = kvh % a.Hkv;
+  constexpr int NP = HD / 8;
+  const int kvh = blockIdx.y, h = kvh < a.Hkv ? kvh : kvh - a.Hkv;
   const bool is_v = kvh >= a.Hkv;
-  const long long row = (long long)kvh * a.max_seq + a.pos0 + t;
-  const uint2 c = *reinterpret_cast<const uint2*>(a.codes + row * (HD / 2) + b * 8);
-  const float dec = e4m3_to_f32(a.scales[row * NB + b]);
+  void* dst = const_cast<void*>(is_v ? a.v : a.k);
   const float ts = is_v ? a.v_scale : a.k_scale;
-  float x[16];
+  const long long n = (long long)a.tokens * NP, i0 = (long long)blockIdx.x * (256 * kRowsUnroll) + threadIdx.x;
+  const long long at = ((long long)kvh * a.max_seq + a.pos0) * NP;
+  uint32_t c[kRowsUnroll], e[kRowsUnroll];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = unpack_f16x2(e2m1_byte_to_f16x2(i < 4 ? c.x : c.y, i & 3));
-    x[2 * i] = f.x * dec * ts, x[2 * i + 1] = f.y * dec * ts;
+  for (int k = 0; k < kRowsUnroll; ++k) {
+    const long long i = i0 + k * 256;
+    c[k] = e[k] = 0;
+    if (i < n) {
+      c[k] = __ldg(reinterpret_cast<const uint32_t*>(a.codes + (at + i) * 4));
+      e[k] = __ldg(a.scales + ((at + i) >> 1));
+    }
   }
-  void* base = const_cast<void*>(is_v ? a.v : a.k);
-  const long long off = t * a.token_stride + h * a.head_stride + b * 16;
-  if (DT == MSK_FP32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + off);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-  } else {
-    uint32_t w[8];
+  for (int k = 0; k < kRowsUnroll; ++k) {
+    const long long i = i0 + k * 256;
+    if (i >= n) break;
+    const float dec = e4m3_to_f32(e[k]);
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack16(x[2 * i], x[2 * i + 1], DT == MSK_FP16);
-    uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + off);
-    p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack_f16x2(e2m1_byte_to_f16x2(c[k], j));
+      x[2 * j] = f.x * dec * ts, x[2 * j + 1] = f.y * dec * ts;
+    }
+    const long long off = i / NP * a.token_stride + h * a.head_stride + i % NP * 8;
+    if (DT == MSK_FP32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + off);
+      p[0] = make_float4(x[0], x[1], x[2], x[3]);
+      p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack16(x[2 * j], x[2 * j + 1], DT == MSK_FP16);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + off) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
 template <int HD>
 void launch_rows(bool write, int32_t dt, const Kv4Rows& a, cudaStream_t st) {
-  const long long n = 2ll * a.Hkv * a.tokens * (HD / 16);
-  const unsigned grid = (unsigned)((n + 255) / 256);
+  constexpr int per = 256 * kRowsUnroll;
+  const dim3 grid((unsigned)(((long long)a.tokens * (HD / 8) + per - 1) / per), 2u * a.Hkv);
 #define MSK_ROWS(D)                                                    \
   do {                                                                 \
     if (write) kv4_write_kernel<HD, D><<<grid, 256, 0, st>>>(a);       \
@@ -162,8 +193,7 @@ msk_status rows_call(bool write, const msk_kv4_desc* c, const void* k, const voi
   if (tokens > c->max_seq || (pos0_dev == nullptr && (pos0 < 0 || pos0 > c->max_seq - tokens))) return MSK_ERR_INVALID_ARG;
   const int per16 = 16 / dtype_bytes(dtype);
   if (!ops_aligned16(k) || !ops_aligned16(v) || ts % per16 || hs % per16) return MSK_ERR_ALIGNMENT;
-  // the kernels' grid is one-dimensional
-  if (2ll * c->n_kv_heads * tokens * (c->head_dim / 16) / 256 >= 0x7FFFFFFFll) return MSK_ERR_SHAPE;
+  if (c->n_kv_heads > 32767) return MSK_ERR_SHAPE;  // (the grid's second axis)
   int nsm = 0;
   s = ops_device(&nsm);
   if (s != MSK_OK) return s;

@@ -41,10 +41,44 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
 template <int DT>
 struct Vec {  // a 16-byte vector of logits
   static constexpr int N = DT == MSK_FP32 ? 4 : 8;
+  // below this a clamp of 16-bit logits would meet the type's lowest number
+  static constexpr float LOW = DT == MSK_FP16 ? -65000.f : -1e37f;
   uint4 u;
   __device__ __forceinline__ void none() {
     const uint32_t w = DT == MSK_FP32 ? 0xFF800000u : DT == MSK_FP16 ? 0xFC00FC00u : 0xFF80FF80u;  // -inf
     u = make_uint4(w, w, w, w);
+  }
+  __device__ __forceinline__ void at_least(uint32_t lb) {  // (16-bit types)
+    uint32_t* w = &u.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (DT == MSK_FP16) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(lb));
+      else asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(lb));
+    }
+  }
+  // How many are greater than x (a 16-bit type's number twice, or fp32).
+  __device__ __forceinline__ void count_above(uint32_t x, uint32_t& n2) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (DT == MSK_FP32) {
+        n2 += __uint_as_float(w[i]) > __uint_as_float(x);
+      } else {  // 1 or 0 for each half, added up as 16-bit floats (at most 16 a half)
+        uint32_t g;
+        if (DT == MSK_FP16) {
+          asm("set.gt.f16x2.f16x2 %0, %1, %2;" : "=r"(g) : "r"(w[i]), "r"(x));
+          asm("add.f16x2 %0, %0, %1;" : "+r"(n2) : "r"(g));
+        } else {
+          asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(g) : "r"(w[i]), "r"(x));
+          asm("add.bf16x2 %0, %0, %1;" : "+r"(n2) : "r"(g));
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ int counted(uint32_t n2) {
+    if (DT == MSK_FP32) return (int)n2;
+    const float2 f = unpack16(n2, DT == MSK_FP16);
+    return (int)(f.x + f.y);
   }
   __device__ __forceinline__ void get(float (&x)[N]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -103,19 +137,75 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
 
-// Softmax statistics relative to a maximum m: s = sum 2^t and u = sum 2^t t,
-// t = (x - m) log2(e) / temperature <= 0.  m starts at the lowest number, so
-// that every difference is defined; +inf and NaN end in an s that is not a
-// positive number, and so does a row without any number above -inf.
+// Softmax statistics of logits with maximum m: s = sum 2^t and u = sum 2^t t,
+// t = (x - m) c <= 0, c = log2(e) / temperature.  The difference is taken before
+// the product, so that the maximum's t is 0 and steep temperatures stay exact.
+// +inf and NaN end in an s that is not a positive number, and so does a row of
+// nothing but -inf (m = -inf, s = 0).
 struct Stat {
   float m, s, u;
 };
-constexpr float kLowest = -3.402823466e38f;
+__device__ __forceinline__ float anchor(float m) { return m == -INFINITY ? 0.f : m; }
 __device__ __forceinline__ Stat stat_join(const Stat& a, const Stat& b, float c) {
-  const float m = max_nan(a.m, b.m);
-  const float da = fmaxf((a.m - m) * c, -200.f), db = fmaxf((b.m - m) * c, -200.f);
-  const float fa = ex2((a.m - m) * c), fb = ex2((b.m - m) * c);
-  return {m, a.s * fa + b.s * fb, fa * (a.u + da * a.s) + fb * (b.u + db * b.s)};
+  const float m = max_nan(a.m, b.m), r = anchor(m);
+  const float da = (a.m - r) * c, db = (b.m - r) * c, fa = ex2(da), fb = ex2(db);
+  return {m, a.s * fa + b.s * fb, fa * (a.u + fmaxf(da, -200.f) * a.s) + fb * (b.u + fmaxf(db, -200.f) * b.s)};
+}
+__device__ __forceinline__ Stat stat_shfl(const Stat& a, int o) {
+  return {__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o), __shfl_xor_sync(0xFFFFFFFFu, a.u, o)};
+}
+
+// Pairs of fp32 numbers and operations on them.
+__device__ __forceinline__ unsigned long long pair(float x, float y) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(unsigned long long v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// K vectors' sums relative to the maximum m.  A logit far below it counts as one
+// some 300 powers of two below, so that 2^t t is a number (0) for -inf too:
+// 16-bit logits are clamped in pairs at `lb`, or (SLOW: fp32, a type without a
+// number that low) every t is.
+template <int DT, int K, bool SLOW>
+__device__ __forceinline__ void vec_sums(const Vec<DT> (&v)[K], float c, float m, float lb, unsigned long long& s,
+                                         unsigned long long& u) {
+  constexpr int N = Vec<DT>::N;
+  const unsigned long long cc = pair(c, c), nm = pair(-m, -m);
+  const uint32_t lb2 = pack16(lb, lb, DT == MSK_FP16);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    Vec<DT> w = v[k];
+    if (!SLOW) w.at_least(lb2);
+    float y[N];
+    w.get(y);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float t0, t1;
+      unpair(mul2(add2(pair(y[i], y[i + 1]), nm), cc), t0, t1);
+      if (SLOW) t0 = max_nan(t0, -300.f), t1 = max_nan(t1, -300.f);
+      const unsigned long long e = pair(ex2(t0), ex2(t1));
+      s = add2(s, e);
+      u = fma2(e, pair(t0, t1), u);
+    }
+  }
 }
 
 // `key` into the warp's list of its 32 greatest keys (lane i holds the i-th).
@@ -130,11 +220,10 @@ __device__ __forceinline__ void list_insert(unsigned long long& list, unsigned l
 // and the sums relative to it over vectors of 16 bytes, four at a time, so
 // that the sums are rescaled once for 16 or 32 logits.  DRAM bounds it.
 //
-// Alternatives cost no second pass: the top k logits lie in the threads whose
-// own maxima are at least the k-th greatest thread maximum, so a bisection on
-// those maxima names the few threads (k of them unless maxima tie) whose
-// logits are looked at again, a warp for each, against a sorted list in the
-// warp's lanes.
+// Alternatives cost no second pass: of 32 groups of threads, k have maxima that
+// reach the k-th greatest group maximum, so the top k logits lie in the (few)
+// threads whose own maxima reach it.  Those threads' logits are looked at again,
+// a warp for each thread, against a sorted list in the warp's lanes.
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ LogProbs a) {
   constexpr int VN = Vec<DT>::N, NW = NT / 32, U = 4;
@@ -142,10 +231,13 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
   __shared__ int cnt[NW];
   __shared__ int owners[NT];
   __shared__ int n_owners, n_cand;
+  __shared__ uint32_t group_max[32], bound;  // (a thread without a logit: 0)
   __shared__ unsigned long long cand[NW * 32];
   __shared__ unsigned long long best[kMaxTop];  // this segment's greatest keys; read by the cluster
   __shared__ Stat seg;                          // ... and its statistics
   __shared__ int seg_above;
+  __shared__ Stat joined;  // all segments'
+  __shared__ int joined_above;
   const long long row = blockIdx.y + (long long)blockIdx.z * gridDim.y;
   if (row >= a.rows) return;  // (the whole cluster)
   const int S = gridDim.x, part = blockIdx.x;
@@ -169,15 +261,20 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
                                                                          : -1;
 
   const float c = a.inv_t * 1.4426950408889634f;
-  Stat q = {kLowest, 0.f, 0.f};
+  // the clamp's distance below the maximum: at least 300 powers of two, and
+  // enough steps of the type (|m| / 64; fp16's smallest) that rounding it keeps
+  // more than 260 of them
+  const float reach = fmaxf(300.f / c, 0x1p-20f);
+  Stat q = {-INFINITY, 0.f, 0.f};
   int above = 0;
   if (mine >= 0) {
     const float v = load1<DT>(x, mine);
     above += v > xg;
     q.m = max_nan(q.m, v);
-    const float t = fmaxf((v - q.m) * c, -200.f);
-    q.s = v == v ? ex2(t) : NAN;
+    q.s = v == -INFINITY ? 0.f : ex2((v - v) * c);  // (NaN for what is no number)
   }
+  unsigned long long s2 = pair(q.s, 0.f), u2 = pair(q.u, 0.f);
+  const uint32_t xg2 = DT == MSK_FP32 ? __float_as_uint(xg) : pack16(xg, xg, DT == MSK_FP16);
   for (long long v = v0 + tid; v < v1; v += U * NT) {
     Vec<DT> w[U];
 #pragma unroll
@@ -187,65 +284,64 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
     }
     const float bm = vec_max<DT, U>(w);
     const float mn = max_nan(q.m, bm);
-    const float d = (q.m - mn) * c, f = ex2(d);
-    q.u = f * (q.u + fmaxf(d, -200.f) * q.s);
-    q.s *= f;
-    q.m = mn;
+    const float r = anchor(mn);
+    if (mn != q.m) {
+      const float d = (q.m - r) * c, f = ex2(d), dd = fmaxf(d, -300.f);
+      u2 = mul2(fma2(s2, pair(dd, dd), u2), pair(f, f));
+      s2 = mul2(s2, pair(f, f));
+      q.m = mn;
+    }
+    const float lb = r - fmaxf(reach, fabsf(r) * 0.015625f);
+    if (DT != MSK_FP32 && lb > Vec<DT>::LOW) vec_sums<DT, U, false>(w, c, r, lb, s2, u2);
+    else vec_sums<DT, U, true>(w, c, r, lb, s2, u2);
+    if (!(bm <= xg)) {
+      uint32_t n2 = 0;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      float y[VN];
-      w[k].get(y);
-#pragma unroll
-      for (int i = 0; i < VN; ++i) {
-        const float t = fmaxf((y[i] - mn) * c, -200.f), e = ex2(t);  // (-200: 2^t is 0 and 2^t t a number)
-        q.s += e;
-        q.u = fmaf(e, t, q.u);
-      }
-      if (bm > xg) {
-#pragma unroll
-        for (int i = 0; i < VN; ++i) above += y[i] > xg;
-      }
+      for (int k = 0; k < U; ++k) w[k].count_above(xg2, n2);
+      above += Vec<DT>::counted(n2);
     }
   }
-  const float my_max = q.m;
-  for (int o = 16; o; o >>= 1) {
-    const Stat b = {__shfl_xor_sync(0xFFFFFFFFu, q.m, o), __shfl_xor_sync(0xFFFFFFFFu, q.s, o),
-                    __shfl_xor_sync(0xFFFFFFFFu, q.u, o)};
-    q = stat_join(q, b, c);
+  {
+    float s0, s1, u0, u1;
+    unpair(s2, s0, s1);
+    unpair(u2, u0, u1);
+    q.s = s0 + s1, q.u = u0 + u1;
   }
+  const uint32_t key = v0 + tid < v1 || mine >= 0 ? ordered(q.m) : 0u;  // of this thread's greatest logit
+#pragma unroll
+  for (int o = 16; o; o >>= 1) q = stat_join(q, stat_shfl(q, o), c);
   above = __reduce_add_sync(0xFFFFFFFFu, above);
   if (lane == 0) st[warp] = q, cnt[warp] = above;
   if (tid == 0) n_owners = 0, n_cand = 0;
   if (tid < kMaxTop) best[tid] = 0ull;
+  if (a.top > 0) {
+    uint32_t gm = key;
+#pragma unroll
+    for (int o = 1; o < NT / 32; o <<= 1) gm = max(gm, __shfl_xor_sync(0xFFFFFFFFu, gm, o));
+    if (lane % (NT / 32) == 0) group_max[tid / (NT / 32)] = gm;
+  }
   __syncthreads();
   if (warp == 0) {
-    q = lane < NW ? st[lane] : Stat{kLowest, 0.f, 0.f};
-    above = lane < NW ? cnt[lane] : 0;
-    for (int o = NW / 2; o; o >>= 1) {
-      const Stat b = {__shfl_xor_sync(0xFFFFFFFFu, q.m, o), __shfl_xor_sync(0xFFFFFFFFu, q.s, o),
-                      __shfl_xor_sync(0xFFFFFFFFu, q.u, o)};
-      q = stat_join(q, b, c);
-      above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
-    }
+    q = lane < NW ? st[lane] : Stat{-INFINITY, 0.f, 0.f};
+    above = __reduce_add_sync(0xFFFFFFFFu, lane < NW ? cnt[lane] : 0);
+#pragma unroll
+    for (int o = NW / 2; o; o >>= 1) q = stat_join(q, stat_shfl(q, o), c);
     if (lane == 0) seg = q, seg_above = above;
+  } else if (warp == 1 && a.top > 0) {
+    // the bound: the `top`-th greatest group maximum
+    const uint32_t g = group_max[lane];
+    int r = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const uint32_t o = __shfl_sync(0xFFFFFFFFu, g, j);
+      r += o > g || (o == g && j < lane);
+    }
+    if (r == a.top - 1) bound = g;
   }
 
   if (a.top > 0) {
-    // a bound that at least `top` thread maxima reach: the greatest one, or
-    // one that few reach (0, which every thread reaches, if there are no
-    // `top` maxima above the lowest number)
-    const uint32_t key = my_max == kLowest ? 0u : ordered(my_max);
-    uint32_t lo = 0, hi = 0xFFFFFFFFu;  // (reached by >= top threads; by fewer)
-    while (hi - lo > 1) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      const int n = __syncthreads_count(key >= mid);
-      if (n >= a.top) {
-        lo = mid;
-        if (n <= 2 * kMaxTop) break;
-      } else {
-        hi = mid;
-      }
-    }
+    __syncthreads();
+    const uint32_t lo = bound;
     if (key >= lo) owners[atomicAdd(&n_owners, 1)] = tid;
     __syncthreads();
     const int no = n_owners;
@@ -311,12 +407,18 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
         cand[i] = ((unsigned long long)ld32(at + 4) << 32) | ld32(at);
       }
       __syncthreads();
-      if (tid == 0) {
-        for (int r = 1; r < S; ++r) {
-          const uint32_t at = remote(&seg, r);
-          seg = stat_join(seg, {__uint_as_float(ld32(at)), __uint_as_float(ld32(at + 4)), __uint_as_float(ld32(at + 8))}, c);
-          seg_above += (int)ld32(remote(&seg_above, r));
+      if (warp == 1) {  // the segments' statistics, a lane for each
+        Stat z = {-INFINITY, 0.f, 0.f};
+        int n_above = 0;
+        if (lane < S) {
+          const uint32_t at = remote(&seg, lane);
+          z = {__uint_as_float(ld32(at)), __uint_as_float(ld32(at + 4)), __uint_as_float(ld32(at + 8))};
+          n_above = (int)ld32(remote(&seg_above, lane));
         }
+        n_above = __reduce_add_sync(0xFFFFFFFFu, n_above);
+#pragma unroll
+        for (int o = 4; o; o >>= 1) z = stat_join(z, stat_shfl(z, o), c);
+        if (lane == 0) joined = z, joined_above = n_above;
       }
       for (int i = tid; i < n; i += NT) {
         const unsigned long long k = cand[i];
@@ -329,17 +431,20 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
     if (part != 0) return;
   }
   __syncthreads();
-  const bool bad = !(seg.s > 0.f && seg.s < INFINITY);
-  const float log_s = bad ? NAN : logf(seg.s);
+  const Stat z = S > 1 ? joined : seg;
+  const bool bad = !(z.s > 0.f && z.s < INFINITY);
+  // in log2 units, then nats
+  constexpr float kLn2 = 0.6931471805599453f;
+  const float log_s = bad ? NAN : log2f(z.s);
   if (tid == 0) {
-    if (a.logprob) a.logprob[row] = given ? (xg - seg.m) * a.inv_t - log_s : 0.f;
-    if (a.rank) a.rank[row] = given ? seg_above : -1;
-    if (a.entropy) a.entropy[row] = bad ? NAN : log_s - 0.6931471805599453f * (seg.u / seg.s);
+    if (a.logprob) a.logprob[row] = given ? ((xg - z.m) * c - log_s) * kLn2 : 0.f;
+    if (a.rank) a.rank[row] = given ? (S > 1 ? joined_above : seg_above) : -1;
+    if (a.entropy) a.entropy[row] = bad ? NAN : (log_s - z.u / z.s) * kLn2;
   }
   if (tid < a.top) {
     const unsigned long long k = best[tid];
     if (a.top_ids) a.top_ids[row * a.top + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)k);
-    if (a.top_logprobs) a.top_logprobs[row * a.top + tid] = bad ? NAN : (key_value(k) - seg.m) * a.inv_t - log_s;
+    if (a.top_logprobs) a.top_logprobs[row * a.top + tid] = bad ? NAN : ((key_value(k) - z.m) * c - log_s) * kLn2;
   }
 }
 

@@ -465,6 +465,36 @@ def test_logprobs_without_a_distribution(M):
     check_logprobs([g[[0, 5]] for g in (lp, ent, rank, ids, tlp)], x[[0, 5]], tok[[0, 5]], 4, 1.0)
 
 
+@pytest.mark.parametrize("dtype,size,temperature", [
+    ("bf16", 1e6, 1.0), ("bf16", 1e6, 1e5), ("bf16", 1e37, 1.0), ("bf16", 1e-36, 1e-30), ("fp16", 2e4, 1.0), ("fp16", 2e4, 1e-5),
+    ("fp16", 1e-6, 1e-7), ("fp32", 1e9, 1e-3), ("fp32", 1e20, 1e20), ("fp32", 1.0, 1e-30), ("fp32", 1.0, 1e30),
+    ("bf16", 1e-3, 1e30)])
+@pytest.mark.parametrize("R,V", [(2, 20011), (40, 1003)])
+def test_logprobs_of_very_small_and_large_logits(M, dtype, size, temperature, R, V):
+    x = (randn(95, R, V) * size).to(DT[dtype])
+    x[:, 5::97] = float("-inf")
+    x[0] -= size * 3
+    tokens = torch.randint(0, V, (R,), generator=gen(96), dtype=torch.int32)
+    got = M.msk_token_logprobs(x.cuda(), tokens.cuda(), top=9, temperature=temperature)
+    check_logprobs(got, x, tokens, 9, float(np.float32(temperature)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_logprobs_of_16_bits_without_a_distribution(M, dtype):
+    x = randn(97, 5, 20001).to(DT[dtype])
+    x[1] = float("-inf")
+    x[2, 7] = float("nan")
+    x[3, 8] = float("inf")
+    x[4, 1:] = float("-inf")
+    tok = torch.zeros(5, dtype=torch.int32)
+    lp, ent, rank, ids, tlp = (g.cpu() for g in M.msk_token_logprobs(x.cuda(), tok.cuda(), top=4))
+    for r in (1, 2, 3):
+        assert torch.isnan(lp[r]) and torch.isnan(ent[r]) and torch.isnan(tlp[r]).all()
+    assert torch.equal(rank.long(), (x > x[:, :1]).sum(-1))
+    assert ids[3, 0] == 8
+    assert lp[4] == 0 and ent[4] == 0 and ids[4].tolist() == [0, 1, 2, 3]
+
+
 def test_logprobs_strides_and_missing_tokens(M):
     wide = randn(92, 9, 5011).cuda()
     logits = wide[1:8, 3:4999]  # rows that start off any 16-byte boundary
