@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
     if (key >= lo) owners[atomicAdd(&n_owners, 1)] = tid;
     __syncthreads();
     const int no = n_owners;
+    const float lo_value = lo == 0u ? -INFINITY : key_value((unsigned long long)lo << 32);
     unsigned long long list = 0ull;
     for (int i = warp; i < no; i += NW) {
       const int o = owners[i];
@@ -335,18 +336,21 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
         const long long v = vb + (long long)lane * NT;
         Vec<DT> w;
         w.none();
-        const bool in = v < v1;
-        if (in) w.u = load_stream(xv + v * 16);
+        if (v < v1) w.u = load_stream(xv + v * 16);
         float y[VN];
         w.get(y);
+        uint32_t in = 0;  // which of them reach the bound (few)
 #pragma unroll
-        for (int j = 0; j < VN; ++j) {
-          const uint32_t k = ordered(y[j]);
+        for (int j = 0; j < VN; ++j) in |= (uint32_t)!(y[j] < lo_value) << j;
+        if (v >= v1) in = 0;
+        while (uint32_t hit = __ballot_sync(0xFFFFFFFFu, in != 0)) {
+          const int j = __ffs(in) - 1;
+          float best_y = 0.f;
+#pragma unroll
+          for (int k = 0; k < VN; ++k) best_y = k == j ? y[k] : best_y;
           const unsigned long long full =
-              ((unsigned long long)k << 32) | (0xFFFFFFFFu - (uint32_t)(head + v * VN + j));
-          // (the list's last key bounds what can still enter)
-          const unsigned long long last = __shfl_sync(0xFFFFFFFFu, list, 31);
-          uint32_t hit = __ballot_sync(0xFFFFFFFFu, in && k >= lo && full > last);
+              ((unsigned long long)ordered(best_y) << 32) | (0xFFFFFFFFu - (uint32_t)(head + v * VN + j));
+          in &= in - 1;
           while (hit) {
             const int src = __ffs(hit) - 1;
             hit &= hit - 1;
