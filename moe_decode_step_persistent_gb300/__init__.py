@@ -354,22 +354,32 @@ def _position(pos):
 
 
 def _kv_rows(cache, k, v):
-    _need(k.dim() == 3 and k.shape == v.shape and k.dtype == v.dtype and k.dtype in _DTYPES
-          and _step(k, 0) == _step(v, 0) and _step(k, 1) == _step(v, 1) and v.stride(2) == 1,
-          "k and v: [tokens][n_kv_heads][head_dim], one shape, type and layout")
-    _need(k.shape[1] == cache.n_kv_heads and k.shape[2] == cache.head_dim and k.stride(2) == 1,
-          "k and v do not fit the cache's heads")
+    """(type, rows, steps between rows and between heads) of k and v."""
+    shape, dtype = k.shape, _DTYPES.get(k.dtype)
+    _need(len(shape) == 3 and shape == v.shape and dtype is not None and v.dtype == k.dtype,
+          "k and v: [tokens][n_kv_heads][head_dim], one shape and floating type")
+    T, H, d = shape
+    _need(H == cache.n_kv_heads and d == cache.head_dim, "k and v do not fit the cache's heads")
+    ts, hs, es = k.stride()
+    tv, hv, ev = v.stride()
+    # (the stride of an axis of one is arbitrary)
+    if T == 1:
+        ts = tv = 0
+    if H == 1:
+        hs = hv = 0
+    _need(es == 1 and ev == 1 and ts == tv and hs == hv, "k and v: contiguous heads, one layout")
+    return dtype, T, ts, hs
 
 
 def msk_kv4_write(cache, k, v, pos0, stream=None):
     """Quantises k and v ([tokens][n_kv_heads][head_dim], any strides of the
     first two axes) into cache rows pos0, pos0 + 1, ...  pos0: an int, or a
     CUDA int32 tensor read when the kernel runs."""
-    _kv_rows(cache, k, v)
+    dtype, T, ts, hs = _kv_rows(cache, k, v)
     host, dev = _position(pos0)
     st = _enqueue(stream, k, v, cache.codes)
-    _check(load_library().msk_kv4_write(cache.desc, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.shape[0],
-                                        _step(k, 0), _step(k, 1), host, dev, st), "msk_kv4_write")
+    _check(load_library().msk_kv4_write(cache.desc, k.data_ptr(), v.data_ptr(), dtype, T, ts, hs, host, dev, st),
+           "msk_kv4_write")
 
 
 def msk_kv4_read(cache, pos0, tokens, dtype=torch.bfloat16, out=None, stream=None):
@@ -380,11 +390,11 @@ def msk_kv4_read(cache, pos0, tokens, dtype=torch.bfloat16, out=None, stream=Non
         shape = (tokens, cache.n_kv_heads, cache.head_dim)
         out = _empty(stream, shape, dtype), _empty(stream, shape, dtype)
     k, v = out
-    _kv_rows(cache, k, v)
-    _need(k.shape[0] == tokens, "out does not hold `tokens` rows")
+    dt, T, ts, hs = _kv_rows(cache, k, v)
+    _need(T == tokens, "out does not hold `tokens` rows")
     st = _enqueue(stream, k, v, cache.codes)
-    _check(load_library().msk_kv4_read(cache.desc, int(pos0), tokens, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype],
-                                       _step(k, 0), _step(k, 1), st), "msk_kv4_read")
+    _check(load_library().msk_kv4_read(cache.desc, int(pos0), tokens, k.data_ptr(), v.data_ptr(), dt, ts, hs, st),
+           "msk_kv4_read")
     return k, v
 
 
