@@ -100,6 +100,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   return r;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Greatest value of N vectors.
 template <int DT, int K>
 __device__ __forceinline__ float vec_max(const Vec<DT> (&v)[K]) {
@@ -190,76 +196,77 @@ __device__ __forceinline__ void list_insert(unsigned long long& list, unsigned l
   if (lane >= at) list = lane == at ? key : up;
 }
 
-// One row, or one of `gridDim.x` segments of a row that a cluster of blocks
-// works on.  One pass over the logits: every thread keeps a running maximum
-// and the sums relative to it over vectors of 16 bytes, four at a time, so
-// that the sums are rescaled once for 16 or 32 logits.  DRAM bounds it.
-//
-// Alternatives cost no second pass: of 32 groups of threads, k have maxima that
-// reach the k-th greatest group maximum, so the top k logits lie in the (few)
-// threads whose own maxima reach it.  Those threads' logits are looked at again,
-// a warp for each thread, against a sorted list in the warp's lanes.
-template <int DT, int NT>
-__global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ LogProbs a) {
-  constexpr int VN = Vec<DT>::N, NW = NT / 32, U = 4;
-  __shared__ Stat st[NW];
-  __shared__ int cnt[NW];
-  __shared__ int owners[NT];
-  __shared__ int n_owners, n_cand;
-  __shared__ uint32_t group_max[32], bound;  // (a thread without a logit: 0)
-  __shared__ unsigned long long cand[NW * 32];
-  __shared__ unsigned long long best[kMaxTop];  // this segment's greatest keys; read by the cluster
-  __shared__ Stat seg;                          // ... and its statistics
-  __shared__ int seg_above;
-  __shared__ Stat joined;  // all segments'
-  __shared__ int joined_above;
-  const long long row = blockIdx.y + (long long)blockIdx.z * gridDim.y;
-  if (row >= a.rows) return;  // (the whole cluster)
-  const int S = gridDim.x, part = blockIdx.x;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const char* x = static_cast<const char*>(a.logits) + row * a.ld * (DT == MSK_FP32 ? 4 : 2);
-  const int tok = a.tokens ? a.tokens[row] : -1;
-  const bool given = tok >= 0 && tok < a.V;
-  const float xg = given ? load1<DT>(x, tok) : INFINITY;
+// A row's aligned vectors, and the single logits before and behind them.
+template <int DT>
+struct Row {
+  const char* xv;  // first vector of this block's segment
+  int nv;          // vectors of the segment
+  int first;       // logits of the row before them
+  int head, tail;  // single logits of the row's ends, 0 unless this block's
+  __device__ __forceinline__ Row(const LogProbs& a, long long row, int S, int part) {
+    constexpr int es = DT == MSK_FP32 ? 4 : 2;
+    const char* x = static_cast<const char*>(a.logits) + row * a.ld * es;
+    head = (int)min(a.V, (long long)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / es);
+    const int n = (int)((a.V - head) / Vec<DT>::N);
+    tail = (int)(a.V - head) - n * Vec<DT>::N;
+    const int v0 = (int)((long long)n * part / S);
+    nv = (int)((long long)n * (part + 1) / S) - v0;
+    first = head + v0 * Vec<DT>::N;
+    xv = x + (long long)first * es;
+    if (part != 0) head = 0;
+    if (part != S - 1) tail = 0;
+  }
+  __device__ __forceinline__ const char* row() const { return xv - (long long)first * (DT == MSK_FP32 ? 4 : 2); }
+  // The index of thread t's single logit, or -1.
+  __device__ __forceinline__ int single(int t, const LogProbs& a) const {
+    return t < head ? t : t >= 32 && t < 32 + tail ? (int)a.V - tail + (t - 32) : -1;
+  }
+};
 
-  // the aligned vectors of this segment; single logits before (first
-  // segment) and behind them (last segment)
-  const int es = DT == MSK_FP32 ? 4 : 2;
-  const int head = (int)min(a.V, (long long)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / es);
-  const long long nv = (a.V - head) / VN;
-  const int tail = (int)(a.V - head - nv * VN);
-  const long long v0 = nv * part / S, v1 = nv * (part + 1) / S;
-  const char* xv = x + head * es;
-  // the single logit of this thread, if it has one
-  const long long mine = part == 0 && tid < head                       ? tid
-                         : part == S - 1 && tid >= 32 && tid < 32 + tail ? a.V - tail + (tid - 32)
-                                                                         : -1;
-
-  const float c = a.inv_t * 1.4426950408889634f;
+__device__ __forceinline__ float clamp_reach(float c) {
   // the clamp's distance below the maximum: at least 300 powers of two, and
   // enough steps of the type (|m| / 64; fp16's smallest) that rounding it keeps
   // more than 260 of them
-  const float reach = fmaxf(300.f / c, 0x1p-20f);
+  return fmaxf(300.f / c, 0x1p-20f);
+}
+
+// One thread's share of a row: a single logit perhaps, and every NT-th vector,
+// four a step, so that the sums are rescaled once for 16 or 32 logits.  Returns
+// the statistics; key: the greatest logit's (0 without one), above: how many
+// are greater than xg; steps: where that logit is and what the other steps hold.
+struct Steps {
+  float second;  // the greatest logit outside the step with the greatest one (NaN: unknown)
+  int left;      // vectors from that step's first on, 0: it is not in a vector
+};
+template <int DT, int NT, bool STEPS>
+__device__ __forceinline__ Stat thread_stats(const Row<DT>& x, const LogProbs& a, int tid, float c, float reach, float xg,
+                                             uint32_t& key, int& above, Steps& steps) {
+  constexpr int U = 4;
+  const int mine = x.single(tid, a);
   Stat q = {-INFINITY, 0.f, 0.f};
-  int above = 0;
+  above = 0;
+  steps = {-INFINITY, 0};
   if (mine >= 0) {
-    const float v = load1<DT>(x, mine);
+    const float v = load1<DT>(x.row(), mine);
     above += v > xg;
     q.m = max_nan(q.m, v);
     q.s = v == -INFINITY ? 0.f : ex2((v - v) * c);  // (NaN for what is no number)
   }
-  unsigned long long s2 = pair(q.s, 0.f), u2 = pair(q.u, 0.f);
+  unsigned long long s2 = pair(q.s, 0.f), u2 = pair(0.f, 0.f);
   const uint32_t xg2 = DT == MSK_FP32 ? __float_as_uint(xg) : pack16(xg, xg, DT == MSK_FP16);
-  for (long long v = v0 + tid; v < v1; v += U * NT) {
+  const char* at = x.xv + (long long)tid * 16;
+  for (int left = x.nv - tid; left > 0; left -= U * NT, at += U * NT * 16) {
     Vec<DT> w[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      if (v + k * NT < v1) w[k].u = load_stream(xv + (v + k * NT) * 16);
+      if (k * NT < left) w[k].u = load_stream(at + k * (NT * 16));
       else w[k].none();
     }
-    const float bm = vec_max<DT, U>(w);
-    const float mn = max_nan(q.m, bm);
-    const float r = anchor(mn);
+    const float bm = vec_max<DT, U>(w), mn = max_nan(q.m, bm), r = anchor(mn);
+    if (STEPS) {
+      steps.second = max_nan(steps.second, min_nan(bm, q.m));
+      if (bm > q.m) steps.left = left;
+    }
     if (mn != q.m) {
       const float d = (q.m - r) * c, f = ex2(d), dd = fmaxf(d, -300.f);
       u2 = mul2(fma2(s2, pair(dd, dd), u2), pair(f, f));
@@ -276,15 +283,336 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
       above += Vec<DT>::counted(n2);
     }
   }
-  {
-    float s0, s1, u0, u1;
-    unpair(s2, s0, s1);
-    unpair(u2, u0, u1);
-    q.s = s0 + s1, q.u = u0 + u1;
-  }
-  const uint32_t key = v0 + tid < v1 || mine >= 0 ? ordered(q.m) : 0u;  // of this thread's greatest logit
+  float s0, s1, u0, u1;
+  unpair(s2, s0, s1);
+  unpair(u2, u0, u1);
+  key = tid < x.nv || mine >= 0 ? ordered(q.m) : 0u;
+  return {q.m, s0 + s1, u0 + u1};
+}
+
+// The warp's statistics, all relative to its maximum.
+__device__ __forceinline__ Stat warp_stats(const Stat& q, uint32_t key, float c) {
+  const uint32_t wk = __reduce_max_sync(0xFFFFFFFFu, key);
+  const float m = wk == 0u ? -INFINITY : key_value((unsigned long long)wk << 32);
+  const float d = (q.m - anchor(m)) * c, f = ex2(d);
+  float s = f * q.s, u = f * (q.u + fmaxf(d, -300.f) * q.s);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) q = stat_join(q, stat_shfl(q, o), c);
+  for (int o = 16; o; o >>= 1) {
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+  }
+  return {m, s, u};
+}
+
+// The logits of the lanes' vectors that reach `lo` (few), into the warp's list.
+// in: whether a lane has a vector; first, step: the index of lane 0's first
+// logit, and from one lane's to the next.
+template <int DT>
+__device__ __forceinline__ void list_vectors(unsigned long long& list, const Vec<DT>& w, bool in, int first, int step,
+                                             float lo, int lane) {
+  constexpr int VN = Vec<DT>::N;
+  const Vec<DT> one[1] = {w};
+  uint32_t lanes = __ballot_sync(0xFFFFFFFFu, in && !(vec_max<DT, 1>(one) < lo));
+  while (lanes) {
+    const int src = __ffs(lanes) - 1;
+    lanes &= lanes - 1;
+    // a lane for each of the vector's logits
+    const uint32_t u[4] = {__shfl_sync(0xFFFFFFFFu, w.u.x, src), __shfl_sync(0xFFFFFFFFu, w.u.y, src),
+                           __shfl_sync(0xFFFFFFFFu, w.u.z, src), __shfl_sync(0xFFFFFFFFu, w.u.w, src)};
+    const int i = DT == MSK_FP32 ? lane & 3 : lane >> 1 & 3;
+    const uint32_t p = i < 2 ? (i == 0 ? u[0] : u[1]) : (i == 2 ? u[2] : u[3]);
+    float y = __uint_as_float(p);
+    if (DT != MSK_FP32) {
+      const float2 f = unpack16(p, DT == MSK_FP16);
+      y = lane & 1 ? f.y : f.x;
+    }
+    const unsigned long long key =
+        ((unsigned long long)ordered(y) << 32) | (0xFFFFFFFFu - (uint32_t)(first + src * step + lane));
+    uint32_t hit = __ballot_sync(0xFFFFFFFFu, lane < VN && !(y < lo));
+    while (hit) {
+      const int from = __ffs(hit) - 1;
+      hit &= hit - 1;
+      list_insert(list, __shfl_sync(0xFFFFFFFFu, key, from), lane);
+    }
+  }
+}
+
+// A row's results from its statistics and sorted alternatives (a lane's each).
+__device__ __forceinline__ void put_row(const LogProbs& a, long long row, const Stat& z, int above, int tok, float xg, float c,
+                                        unsigned long long alt, int lane) {
+  const bool given = tok >= 0 && tok < a.V, bad = !(z.s > 0.f && z.s < INFINITY);
+  // in log2 units, then nats
+  constexpr float kLn2 = 0.6931471805599453f;
+  const float log_s = bad ? NAN : log2f(z.s);
+  if (lane == 0) {
+    if (a.logprob) a.logprob[row] = given ? ((xg - z.m) * c - log_s) * kLn2 : 0.f;
+    if (a.rank) a.rank[row] = given ? above : -1;
+    if (a.entropy) a.entropy[row] = bad ? NAN : (log_s - z.u / z.s) * kLn2;
+  }
+  if (lane < a.top) {
+    if (a.top_ids) a.top_ids[row * a.top + lane] = (int32_t)(0xFFFFFFFFu - (uint32_t)alt);
+    if (a.top_logprobs) a.top_logprobs[row * a.top + lane] = bad ? NAN : ((key_value(alt) - z.m) * c - log_s) * kLn2;
+  }
+}
+
+__device__ __forceinline__ int row_token(const LogProbs& a, long long row) {
+  return a.tokens && row < a.rows ? a.tokens[row] : -1;
+}
+template <int DT>
+__device__ __forceinline__ float row_logit(const LogProbs& a, long long row, int tok) {
+  if (tok < 0 || tok >= a.V) return INFINITY;
+  return load1<DT>(static_cast<const char*>(a.logits) + row * a.ld * (DT == MSK_FP32 ? 4 : 2), tok);
+}
+
+// The n-th greatest (1 <= n <= 64) of the warp's 64 numbers, two a lane: the
+// greatest left, n times (fewer with ties).
+__device__ __forceinline__ uint32_t greatest(uint32_t g0, uint32_t g1, int n) {
+  for (;;) {
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(g0, g1));
+    n -= __popc(__ballot_sync(0xFFFFFFFFu, g0 == m)) + __popc(__ballot_sync(0xFFFFFFFFu, g1 == m));
+    if (n <= 0 || m == 0u) return m;
+    g0 = g0 == m ? 0u : g0, g1 = g1 == m ? 0u : g1;
+  }
+}
+
+// Alternatives cost no second pass: if `top` groups of threads have maxima that
+// reach a bound, so do `top` logits, and all of those lie in the (few) threads
+// whose own maxima reach it.  Those threads' logits are looked at again, a warp
+// for each thread, against a sorted list in the warp's lanes.
+
+// Many long rows.  Blocks take rows blockIdx.x, + gridDim.x, ...: 16 warps read
+// one row after the other without a stop, and two more end the rows (join the
+// warps' sums, find the alternatives, write the results) in turn while the 16
+// read on.  Each of the two has a place for a row's statistics, which it gives
+// back once it holds them in registers (named barriers, one each way).
+constexpr int kStreamThreads = 512, kFetch = 16, kHits = 128;
+enum { kFull0 = 1, kFree0 = 3 };  // barriers; + 1 for the second place
+template <int ID>
+__device__ __forceinline__ void place_sync(int place) {
+  if (place == 0) asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(kStreamThreads + 32) : "memory");
+  else asm volatile("bar.sync %0, %1;" ::"n"(ID + 1), "n"(kStreamThreads + 32) : "memory");
+}
+template <int ID>
+__device__ __forceinline__ void place_arrive(int place) {
+  if (place == 0) asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(kStreamThreads + 32) : "memory");
+  else asm volatile("bar.arrive %0, %1;" ::"n"(ID + 1), "n"(kStreamThreads + 32) : "memory");
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kStreamThreads + 64, 2) logprobs_stream_kernel(const __grid_constant__ LogProbs a) {
+  constexpr int NT = kStreamThreads, NW = NT / 32, PER = NT / 32, VN = Vec<DT>::N;
+  __shared__ Stat st[2][NW];
+  __shared__ int cnt[2][NW];
+  __shared__ uint32_t keys[2][NT];
+  __shared__ float second[2][NT];  // (see Steps)
+  __shared__ int where[2][NT];
+  __shared__ uint16_t owners[2][NT], scan[2][NT];
+  __shared__ uint4 fetched[2][kFetch][32];
+  __shared__ unsigned long long hits[2][kHits];
+  __shared__ int n_hits[2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float c = a.inv_t * 1.4426950408889634f, reach = clamp_reach(c);
+  if (warp < NW) {
+    int place = 0;
+    int tok = row_token(a, blockIdx.x);
+    float xg = row_logit<DT>(a, blockIdx.x, tok);
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+      tok = row_token(a, row + gridDim.x);
+      uint32_t key;
+      int above;
+      Steps steps;
+      const Stat t = thread_stats<DT, NT, true>(Row<DT>(a, row, 1, 0), a, tid, c, reach, xg, key, above, steps);
+      xg = row_logit<DT>(a, row + gridDim.x, tok);
+      const Stat q = warp_stats(t, key, c);
+      above = __reduce_add_sync(0xFFFFFFFFu, above);
+      if (row >= 2ll * gridDim.x) place_sync<kFree0>(place);
+      keys[place][tid] = key, second[place][tid] = steps.second, where[place][tid] = steps.left;
+      if (lane == 0) st[place][warp] = q, cnt[place][warp] = above;
+      place_arrive<kFull0>(place);
+      place ^= 1;
+    }
+    return;
+  }
+  const int end = warp - NW;
+  for (long long row = blockIdx.x + (long long)end * gridDim.x; row < a.rows; row += 2ll * gridDim.x) {
+    const int tok = row_token(a, row);
+    const float xg = row_logit<DT>(a, row, tok);
+    const Row<DT> x(a, row, 1, 0);
+    place_sync<kFull0>(end);
+    Stat z = lane < NW ? st[end][lane] : Stat{-INFINITY, 0.f, 0.f};
+    const int above = __reduce_add_sync(0xFFFFFFFFu, lane < NW ? cnt[end][lane] : 0);
+    uint32_t k[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) k[i] = keys[end][i * 32 + lane];
+    const bool more = row + 2ll * gridDim.x < a.rows;
+    if (more && a.top == 0) place_arrive<kFree0>(end);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) z = stat_join(z, stat_shfl(z, o), c);
+    unsigned long long list = 0ull;
+    if (a.top > 0) {
+      // the bound: the `top`-th greatest maximum of 64 groups of threads, two a lane
+      uint32_t g0 = 0, g1 = 0;
+#pragma unroll
+      for (int i = 0; i < PER; i += 2) g0 = max(g0, k[i]), g1 = max(g1, k[i + 1]);
+      const uint32_t lo = greatest(g0, g1, a.top);
+      const float lo_value = lo == 0u ? -INFINITY : key_value((unsigned long long)lo << 32);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const uint32_t has = __ballot_sync(0xFFFFFFFFu, k[i] >= lo);
+        if (k[i] >= lo) owners[end][n + __popc(has & ((1u << lane) - 1))] = (uint16_t)(i * 32 + lane);
+        n += __popc(has);
+      }
+      if (lane == 0) n_hits[end] = 0;
+      __syncwarp();
+      // Logits that reach the bound go to `hits`, in any order.
+      auto hit = [&](float y, int index) {
+        const int at = atomicAdd(&n_hits[end], 1);
+        if (at < kHits) hits[end][at] = ((unsigned long long)ordered(y) << 32) | (0xFFFFFFFFu - (uint32_t)index);
+      };
+      // A lane for each of the threads: most have them in one step of their
+      // vectors only.  The others' vectors are all looked at, below.
+      int n_scan = 0;
+      for (int i = 0; i < n; i += 32) {
+        const int o = owners[end][min(i + lane, n - 1)];
+        const int left = where[end][o];
+        const bool one = second[end][o] < lo_value, rest = i + lane < n && !one;
+        const uint32_t some = __ballot_sync(0xFFFFFFFFu, rest);
+        if (rest) scan[end][n_scan + __popc(some & ((1u << lane) - 1))] = (uint16_t)o;
+        n_scan += __popc(some);
+        if (i + lane < n && one) {
+          constexpr int U = 4;
+          Vec<DT> w[U];
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            w[k].none();
+            if (k * NT < left) w[k].u = load_stream(x.xv + (long long)(x.nv - left + k * NT) * 16);
+          }
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            float y[VN];
+            w[k].get(y);
+#pragma unroll
+            for (int j = 0; j < VN; ++j)
+              if (k * NT < left && !(y[j] < lo_value)) hit(y[j], x.first + (x.nv - left + k * NT) * VN + j);
+          }
+        }
+      }
+      if (more) place_arrive<kFree0>(end);
+      __syncwarp();
+      // The hits are ranked; should there be more than the place holds (ties), the
+      // list is made one by one instead.
+      for (int way = 0; way < 2; ++way) {
+        const uint16_t* look = way == 0 ? scan[end] : owners[end];
+        const int n_look = way == 0 ? n_scan : n;
+        if (x.head + x.tail > 0) {  // single logits
+          for (int i = 0; i < n; i += 32) {
+            const int single = i + lane < n ? x.single(owners[end][i + lane], a) : -1;
+            const float v = single >= 0 ? load1<DT>(x.row(), single) : 0.f;
+            const bool in = single >= 0 && !(v < lo_value);
+            if (way == 0 && in) hit(v, single);
+            const unsigned long long key = ((unsigned long long)ordered(v) << 32) | (0xFFFFFFFFu - (uint32_t)single);
+            uint32_t lanes = __ballot_sync(0xFFFFFFFFu, way == 1 && in);
+            while (lanes) {
+              const int src = __ffs(lanes) - 1;
+              lanes &= lanes - 1;
+              list_insert(list, __shfl_sync(0xFFFFFFFFu, key, src), lane);
+            }
+          }
+        }
+        // vectors, a lane for each, several loads under way
+        const uint32_t mine = smem_u32(&fetched[end][0][lane]);
+        for (int i = 0, v = n_look > 0 ? look[0] : 0; i < n_look;) {
+          int m = 0, my_v = 0;  // this batch's; the first of the 32 vectors of its item `lane`
+          for (; m < kFetch && i < n_look; ++m) {
+            if (m == lane) my_v = v;
+            if (v + lane * NT < x.nv) cp_async16(mine + m * 512, x.xv + (long long)(v + lane * NT) * 16);
+            v += 32 * NT;
+            if (v >= x.nv) v = ++i < n_look ? look[i] : 0;
+          }
+          cp_async_wait_all();
+          uint32_t which = 0;  // of the lane's vectors
+#pragma unroll 4
+          for (int j = 0; j < m; ++j) {
+            Vec<DT> w[1];
+            w[0].u = lds128(mine + j * 512);
+            const bool in = __shfl_sync(0xFFFFFFFFu, my_v, j) + lane * NT < x.nv;
+            if (way == 1) list_vectors<DT>(list, w[0], in, x.first + __shfl_sync(0xFFFFFFFFu, my_v, j) * VN, NT * VN, lo_value, lane);
+            else if (in && !(vec_max<DT, 1>(w) < lo_value)) which |= 1u << j;
+          }
+          while (way == 0 && __any_sync(0xFFFFFFFFu, which != 0)) {
+            const int j = which ? __ffs(which) - 1 : 0;
+            const int first = x.first + (__shfl_sync(0xFFFFFFFFu, my_v, j) + lane * NT) * VN;
+            if (which) {
+              Vec<DT> w;
+              w.u = lds128(mine + j * 512);
+              float y[VN];
+              w.get(y);
+#pragma unroll
+              for (int k = 0; k < VN; ++k)
+                if (!(y[k] < lo_value)) hit(y[k], first + k);
+              which &= which - 1;
+            }
+            __syncwarp();
+          }
+        }
+        __syncwarp();
+        const int have = n_hits[end];
+        if (way == 1 || have > kHits) continue;
+        constexpr int H = kHits / 32;
+        unsigned long long h[H];
+        int rank[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) h[i] = lane + 32 * i < have ? hits[end][lane + 32 * i] : 0ull, rank[i] = 0;
+#pragma unroll 2
+        for (int j = 0; j < have; ++j) {
+          const unsigned long long other = hits[end][j];
+#pragma unroll
+          for (int i = 0; i < H; ++i) rank[i] += other > h[i];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < H; ++i)
+          if (h[i] != 0ull) hits[end][rank[i]] = h[i];
+        __syncwarp();
+        list = lane < have ? hits[end][lane] : 0ull;
+        break;
+      }
+      __syncwarp();
+    }
+    put_row(a, row, z, above, tok, xg, c, list, lane);
+  }
+}
+
+// Few rows, or short ones: a block for a row, or a cluster of blocks for
+// `gridDim.x` segments of it.  All warps take part in the row's end.
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_constant__ LogProbs a) {
+  constexpr int VN = Vec<DT>::N, NW = NT / 32;
+  __shared__ Stat st[NW];
+  __shared__ int cnt[NW];
+  __shared__ int owners[NT];
+  __shared__ int n_owners, n_cand;
+  __shared__ uint32_t group_max[64], bound;  // (a thread without a logit: 0)
+  __shared__ unsigned long long cand[NW * 32];
+  __shared__ unsigned long long best[kMaxTop];  // this segment's greatest keys; read by the cluster
+  __shared__ Stat seg;                          // ... and its statistics
+  __shared__ int seg_above;
+  __shared__ Stat joined;  // all segments'
+  __shared__ int joined_above;
+  const long long row = blockIdx.y + (long long)blockIdx.z * gridDim.y;
+  if (row >= a.rows) return;  // (the whole cluster)
+  const int S = gridDim.x, part = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float c = a.inv_t * 1.4426950408889634f;
+  const int tok = row_token(a, row);
+  const float xg = row_logit<DT>(a, row, tok);
+  const Row<DT> x(a, row, S, part);
+  uint32_t key;
+  int above;
+  Steps steps;
+  const Stat t = thread_stats<DT, NT, false>(x, a, tid, c, clamp_reach(c), xg, key, above, steps);
+  Stat q = warp_stats(t, key, c);
   above = __reduce_add_sync(0xFFFFFFFFu, above);
   if (lane == 0) st[warp] = q, cnt[warp] = above;
   if (tid == 0) n_owners = 0, n_cand = 0;
@@ -292,8 +620,8 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
   if (a.top > 0) {
     uint32_t gm = key;
 #pragma unroll
-    for (int o = 1; o < NT / 32; o <<= 1) gm = max(gm, __shfl_xor_sync(0xFFFFFFFFu, gm, o));
-    if (lane % (NT / 32) == 0) group_max[tid / (NT / 32)] = gm;
+    for (int o = 1; o < NT / 64; o <<= 1) gm = max(gm, __shfl_xor_sync(0xFFFFFFFFu, gm, o));
+    if (lane % (NT / 64) == 0) group_max[tid / (NT / 64)] = gm;
   }
   __syncthreads();
   if (warp == 0) {
@@ -304,14 +632,8 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
     if (lane == 0) seg = q, seg_above = above;
   } else if (warp == 1 && a.top > 0) {
     // the bound: the `top`-th greatest group maximum
-    const uint32_t g = group_max[lane];
-    int r = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const uint32_t o = __shfl_sync(0xFFFFFFFFu, g, j);
-      r += o > g || (o == g && j < lane);
-    }
-    if (r == a.top - 1) bound = g;
+    const uint32_t lo = greatest(group_max[lane], group_max[lane + 32], a.top);
+    if (lane == 0) bound = lo;
   }
 
   if (a.top > 0) {
@@ -324,39 +646,17 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
     unsigned long long list = 0ull;
     for (int i = warp; i < no; i += NW) {
       const int o = owners[i];
-      // the owner's single logit
-      const long long single = part == 0 && o < head                       ? o
-                               : part == S - 1 && o >= 32 && o < 32 + tail ? a.V - tail + (o - 32)
-                                                                           : -1;
+      const int single = x.single(o, a);
       if (single >= 0) {
-        const uint32_t k = ordered(load1<DT>(x, single));
+        const uint32_t k = ordered(load1<DT>(x.row(), single));
         if (k >= lo) list_insert(list, ((unsigned long long)k << 32) | (0xFFFFFFFFu - (uint32_t)single), lane);
       }
-      for (long long vb = v0 + o; vb < v1; vb += 32 * NT) {
-        const long long v = vb + (long long)lane * NT;
+      for (int vb = o; vb < x.nv; vb += 32 * NT) {
+        const int v = vb + lane * NT;
         Vec<DT> w;
         w.none();
-        if (v < v1) w.u = load_stream(xv + v * 16);
-        float y[VN];
-        w.get(y);
-        uint32_t in = 0;  // which of them reach the bound (few)
-#pragma unroll
-        for (int j = 0; j < VN; ++j) in |= (uint32_t)!(y[j] < lo_value) << j;
-        if (v >= v1) in = 0;
-        while (uint32_t hit = __ballot_sync(0xFFFFFFFFu, in != 0)) {
-          const int j = __ffs(in) - 1;
-          float best_y = 0.f;
-#pragma unroll
-          for (int k = 0; k < VN; ++k) best_y = k == j ? y[k] : best_y;
-          const unsigned long long full =
-              ((unsigned long long)ordered(best_y) << 32) | (0xFFFFFFFFu - (uint32_t)(head + v * VN + j));
-          in &= in - 1;
-          while (hit) {
-            const int src = __ffs(hit) - 1;
-            hit &= hit - 1;
-            list_insert(list, __shfl_sync(0xFFFFFFFFu, full, src), lane);
-          }
-        }
+        if (v < x.nv) w.u = load_stream(x.xv + (long long)v * 16);
+        list_vectors<DT>(list, w, v < x.nv, x.first + vb * VN, NT * VN, lo_value, lane);
       }
     }
     // the warps' lists, joined by counting how many keys are greater
@@ -410,42 +710,33 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Lo
     if (part != 0) return;
   }
   __syncthreads();
-  const Stat z = S > 1 ? joined : seg;
-  const bool bad = !(z.s > 0.f && z.s < INFINITY);
-  // in log2 units, then nats
-  constexpr float kLn2 = 0.6931471805599453f;
-  const float log_s = bad ? NAN : log2f(z.s);
-  if (tid == 0) {
-    if (a.logprob) a.logprob[row] = given ? ((xg - z.m) * c - log_s) * kLn2 : 0.f;
-    if (a.rank) a.rank[row] = given ? (S > 1 ? joined_above : seg_above) : -1;
-    if (a.entropy) a.entropy[row] = bad ? NAN : (log_s - z.u / z.s) * kLn2;
-  }
-  if (tid < a.top) {
-    const unsigned long long k = best[tid];
-    if (a.top_ids) a.top_ids[row * a.top + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)k);
-    if (a.top_logprobs) a.top_logprobs[row * a.top + tid] = bad ? NAN : ((key_value(k) - z.m) * c - log_s) * kLn2;
-  }
+  if (warp == 0) put_row(a, row, S > 1 ? joined : seg, S > 1 ? joined_above : seg_above, tok, xg, c, best[lane], lane);
 }
 
 template <int DT>
 cudaError_t launch_logprobs(const LogProbs& a, int nsm, cudaStream_t st) {
-  // Few rows: up to 8 segments a row (a cluster, portable size), as long as
-  // they all fit the GPU at once and are worth a block; small vocabularies:
-  // blocks of 128 threads.
+  // Few rows: 2 segments a row while all blocks are resident at once, 4 and 8
+  // (portable cluster sizes) while each has an SM of its own, and if a segment
+  // is worth a block.  131072 logits, 20 alternatives: 16 rows in 8 segments
+  // 7.6 us; 76 rows in 2 segments 11.2 us, in 4 17.0; 152 rows in 2 14.1, whole
+  // 16.0; 304 rows whole 23.7, in 2 29.0.
   int S = 1;
-  while (S < 8 && a.rows * S * 2 <= 4ll * nsm && a.V / (S * 2) >= 4096) S *= 2;
+  while (S < 8 && a.rows * S * 2 <= (S == 1 ? 2ll : 1ll) * nsm && a.V / (S * 2) >= 4096) S *= 2;
+  if (S == 1 && a.V > 4096) {
+    logprobs_stream_kernel<DT><<<(unsigned)std::min<long long>(a.rows, 2 * nsm), kStreamThreads + 64, 0, st>>>(a);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
   const unsigned gy = (unsigned)std::min<long long>(a.rows, 65535);
   cfg.gridDim = dim3((unsigned)S, gy, (unsigned)((a.rows + gy - 1) / gy));
-  const bool small = S == 1 && a.V <= 4096;
-  cfg.blockDim = dim3(small ? 128 : 512);
+  cfg.blockDim = dim3(S == 1 ? 128 : 512);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)S, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return small ? cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, 128>, a) : cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, 512>, a);
+  return S == 1 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, 128>, a) : cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, 512>, a);
 }
 
 }  // namespace
