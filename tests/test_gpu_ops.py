@@ -465,11 +465,36 @@ def test_logprobs_without_a_distribution(M):
     check_logprobs([g[[0, 5]] for g in (lp, ent, rank, ids, tlp)], x[[0, 5]], tok[[0, 5]], 4, 1.0)
 
 
+@pytest.mark.parametrize("R,V,top,dtype", [(640, 5003, 20, "bf16"), (1300, 8192, 32, "fp16"), (330, 40001, 32, "fp32"),
+                                           (305, 70000, 0, "bf16"), (2500, 129, 9, "bf16"), (600, 4099, 1, "fp32")])
+def test_logprobs_of_many_rows(M, R, V, top, dtype):
+    x = (randn(98, R, V) * 4).to(DT[dtype])
+    tokens = torch.randint(-1, V + 1, (R,), generator=gen(99), dtype=torch.int32)
+    check_logprobs(M.msk_token_logprobs(x.cuda(), tokens.cuda(), top=top), x, tokens, top, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16"])
+def test_logprobs_of_many_rows_with_ties(M, dtype):
+    R, V = 700, 6007
+    i = torch.arange(V)
+    kinds = [torch.full((V,), -3.0), i / 500.0, -i / 500.0, (i % 7).float(), (i // 100).float(),
+             torch.where((i == 5999) | (i == 2001), 5.0, float("-inf")), torch.where(i == 1234, 100.0, 0.0),
+             torch.where(i % 2 == 0, -0.0, 0.0), torch.where(i % 512 == 7, i / 1000.0, -9.0), randn(89, V).round()]
+    x = torch.stack([kinds[r % len(kinds)] for r in range(R)]).to(DT[dtype])
+    tokens = torch.randint(0, V, (R,), generator=gen(90), dtype=torch.int32)
+    logits = x.cuda()
+    for top in (32, 3):
+        check_logprobs(M.msk_token_logprobs(logits, tokens.cuda(), top=top), x, tokens, top, 1.0)
+    wide = torch.zeros(R, V + 5, dtype=DT[dtype], device="cuda")
+    wide[:, 3:V + 3] = logits
+    check_logprobs(M.msk_token_logprobs(wide[:, 3:V + 3], tokens.cuda(), top=32), x, tokens, 32, 1.0)
+
+
 @pytest.mark.parametrize("dtype,size,temperature", [
     ("bf16", 1e6, 1.0), ("bf16", 1e6, 1e5), ("bf16", 1e37, 1.0), ("bf16", 1e-36, 1e-30), ("fp16", 2e4, 1.0), ("fp16", 2e4, 1e-5),
     ("fp16", 1e-6, 1e-7), ("fp32", 1e9, 1e-3), ("fp32", 1e20, 1e20), ("fp32", 1.0, 1e-30), ("fp32", 1.0, 1e30),
     ("bf16", 1e-3, 1e30)])
-@pytest.mark.parametrize("R,V", [(2, 20011), (40, 1003)])
+@pytest.mark.parametrize("R,V", [(2, 20011), (40, 1003), (310, 5001)])
 def test_logprobs_of_very_small_and_large_logits(M, dtype, size, temperature, R, V):
     x = (randn(95, R, V) * size).to(DT[dtype])
     x[:, 5::97] = float("-inf")
