@@ -213,7 +213,8 @@ ATTN = [  # tokens, q heads, kv heads, head_dim, cached, window, tree, dtype
     (2, 32, 8, 128, 5003, 2048, False, "bf16"), (5, 3, 3, 128, 64, 0, False, "bf16"), (4, 48, 1, 128, 700, 0, False, "bf16"),
     (16, 1, 1, 64, 0, 0, True, "bf16"), (16, 16, 16, 128, 127, 300, False, "bf16"), (9, 14, 2, 128, 2049, 0, False, "fp16"),
     (1, 8, 2, 128, 9000, 0, False, "bf16"), (16, 16, 4, 128, 8500, 0, True, "bf16"), (3, 6, 1, 64, 20011, 0, False, "fp16"),
-    (16, 8, 8, 64, 8193, 8190, True, "bf16"), (2, 10, 1, 128, 33000, 20000, False, "bf16")]
+    (16, 8, 8, 64, 8193, 8190, True, "bf16"), (2, 10, 1, 128, 33000, 20000, False, "bf16"),
+        (1, 8, 1, 128, 131000, 0, False, "bf16"), (16, 8, 1, 64, 70001, 0, True, "fp16"), (6, 24, 2, 128, 70002, 0, True, "bf16")]
 
 
 def tree_parents(tokens, seed):
@@ -336,6 +337,11 @@ def test_linear(M, T, N, K, xt, yt):
     M.msk_linear_fp4(x, w, out=y)
     check_linear(y, x, packed, scales, 0.0125)
     assert torch.equal(y, M.msk_linear_fp4(x, w, out_dtype=DT[yt]))
+
+
+def test_no_wait_has_run_out(M):
+    """After whatever ran before in this process."""
+    M.msk_ops_check()
 
 
 def test_linear_strides_and_untouched_neighbours(M):
