@@ -312,7 +312,11 @@ __device__ __forceinline__ void list_vectors(unsigned long long& list, const Vec
                                              float lo, int lane) {
   constexpr int VN = Vec<DT>::N;
   const Vec<DT> one[1] = {w};
-  uint32_t lanes = __ballot_sync(0xFFFFFFFFu, in && !(vec_max<DT, 1>(one) < lo));
+  const float most = vec_max<DT, 1>(one);
+  // (a vector none of whose keys passes the list's last one is left out: ties)
+  const unsigned long long bound = ((unsigned long long)ordered(most) << 32) | (0xFFFFFFFFu - (uint32_t)(first + lane * step));
+  const unsigned long long last = __shfl_sync(0xFFFFFFFFu, list, 31);
+  uint32_t lanes = __ballot_sync(0xFFFFFFFFu, in && !(most < lo) && bound > last);
   while (lanes) {
     const int src = __ffs(lanes) - 1;
     lanes &= lanes - 1;
@@ -328,7 +332,8 @@ __device__ __forceinline__ void list_vectors(unsigned long long& list, const Vec
     }
     const unsigned long long key =
         ((unsigned long long)ordered(y) << 32) | (0xFFFFFFFFu - (uint32_t)(first + src * step + lane));
-    uint32_t hit = __ballot_sync(0xFFFFFFFFu, lane < VN && !(y < lo));
+    const unsigned long long least = __shfl_sync(0xFFFFFFFFu, list, 31);
+    uint32_t hit = __ballot_sync(0xFFFFFFFFu, lane < VN && !(y < lo) && key > least);
     while (hit) {
       const int from = __ffs(hit) - 1;
       hit &= hit - 1;
@@ -428,6 +433,7 @@ __global__ void __launch_bounds__(kStreamThreads + 64, 2) logprobs_stream_kernel
       if (row >= 2ll * gridDim.x) place_sync<kFree0>(place);
       keys[place][tid] = key, second[place][tid] = steps.second, where[place][tid] = steps.left;
       if (lane == 0) st[place][warp] = q, cnt[place][warp] = above;
+      __syncwarp();
       place_arrive<kFull0>(place);
       place ^= 1;
     }
@@ -438,6 +444,7 @@ __global__ void __launch_bounds__(kStreamThreads + 64, 2) logprobs_stream_kernel
     const int tok = row_token(a, row);
     const float xg = row_logit<DT>(a, row, tok);
     const Row<DT> x(a, row, 1, 0);
+    __syncwarp();
     place_sync<kFull0>(end);
     Stat z = lane < NW ? st[end][lane] : Stat{-INFINITY, 0.f, 0.f};
     const int above = __reduce_add_sync(0xFFFFFFFFu, lane < NW ? cnt[end][lane] : 0);
@@ -445,6 +452,7 @@ __global__ void __launch_bounds__(kStreamThreads + 64, 2) logprobs_stream_kernel
 #pragma unroll
     for (int i = 0; i < PER; ++i) k[i] = keys[end][i * 32 + lane];
     const bool more = row + 2ll * gridDim.x < a.rows;
+    __syncwarp();
     if (more && a.top == 0) place_arrive<kFree0>(end);
 #pragma unroll
     for (int o = 16; o; o >>= 1) z = stat_join(z, stat_shfl(z, o), c);
@@ -498,8 +506,8 @@ __global__ void __launch_bounds__(kStreamThreads + 64, 2) logprobs_stream_kernel
           }
         }
       }
-      if (more) place_arrive<kFree0>(end);
       __syncwarp();
+      if (more) place_arrive<kFree0>(end);
       // The hits are ranked; should there be more than the place holds (ties), the
       // list is made one by one instead.
       for (int way = 0; way < 2; ++way) {
@@ -536,8 +544,9 @@ __global__ void __launch_bounds__(kStreamThreads + 64, 2) logprobs_stream_kernel
           for (int j = 0; j < m; ++j) {
             Vec<DT> w[1];
             w[0].u = lds128(mine + j * 512);
-            const bool in = __shfl_sync(0xFFFFFFFFu, my_v, j) + lane * NT < x.nv;
-            if (way == 1) list_vectors<DT>(list, w[0], in, x.first + __shfl_sync(0xFFFFFFFFu, my_v, j) * VN, NT * VN, lo_value, lane);
+            const int v0 = __shfl_sync(0xFFFFFFFFu, my_v, j);
+            const bool in = v0 + lane * NT < x.nv;
+            if (way == 1) list_vectors<DT>(list, w[0], in, x.first + v0 * VN, NT * VN, lo_value, lane);
             else if (in && !(vec_max<DT, 1>(w) < lo_value)) which |= 1u << j;
           }
           while (way == 0 && __any_sync(0xFFFFFFFFu, which != 0)) {
@@ -555,6 +564,7 @@ __global__ void __launch_bounds__(kStreamThreads + 64, 2) logprobs_stream_kernel
             }
             __syncwarp();
           }
+          if (way == 0 && __any_sync(0xFFFFFFFFu, n_hits[end] > kHits)) break;
         }
         __syncwarp();
         const int have = n_hits[end];
