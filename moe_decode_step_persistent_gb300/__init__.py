@@ -347,8 +347,8 @@ def _position(pos):
     """(host value, device address) of a position given as an int or as a
     CUDA int32 tensor of one element."""
     if isinstance(pos, torch.Tensor):
-        _need(pos.dtype == torch.int32 and pos.numel() == 1 and pos.is_cuda,
-              "a position tensor is one int32 on the GPU")
+        _need(pos.dtype == torch.int32 and pos.numel() == 1 and pos.get_device() == torch.cuda.current_device(),
+              "a position tensor is one int32 on the current CUDA device")
         return 0, pos.data_ptr()
     return int(pos), None
 

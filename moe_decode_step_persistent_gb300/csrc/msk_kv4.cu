@@ -190,10 +190,12 @@ void launch_rows(bool write, int32_t dt, const Kv4Rows& a, cudaStream_t st) {
 #undef MSK_ROWS
 }
 
+constexpr int kMaxRows = 1 << 30;  // of a cache: positions and steps stay within 32 bits
+
 msk_status check_cache(const msk_kv4_desc* c) {
   if (c == nullptr || c->codes == nullptr || c->scales == nullptr) return MSK_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return MSK_ERR_SHAPE;
-  if (c->n_kv_heads <= 0 || c->max_seq <= 0) return MSK_ERR_SHAPE;
+  if (c->n_kv_heads <= 0 || c->max_seq <= 0 || c->max_seq > kMaxRows) return MSK_ERR_SHAPE;
   // (also false for NaN)
   if (!(c->k_scale > 0.f && c->k_scale <= 3e38f) || !(c->v_scale > 0.f && c->v_scale <= 3e38f)) return MSK_ERR_INVALID_ARG;
   if (!ops_aligned16(c->codes) || !ops_aligned16(c->scales)) return MSK_ERR_ALIGNMENT;
@@ -207,6 +209,8 @@ msk_status rows_call(bool write, const msk_kv4_desc* c, const void* k, const voi
   if (!dtype_ok(dtype) || tokens < 0) return MSK_ERR_INVALID_ARG;
   if (tokens == 0) return MSK_OK;
   if (k == nullptr || v == nullptr || ts < 0 || hs < 0) return MSK_ERR_INVALID_ARG;
+  // (rows that are read may be one and the same, those that are written may not)
+  if (!write && ((tokens > 1 && ts == 0) || (c->n_kv_heads > 1 && hs == 0))) return MSK_ERR_INVALID_ARG;
   if (tokens > c->max_seq || (pos0_dev == nullptr && (pos0 < 0 || pos0 > c->max_seq - tokens))) return MSK_ERR_INVALID_ARG;
   const int per16 = 16 / dtype_bytes(dtype);
   if (!ops_aligned16(k) || !ops_aligned16(v) || ts % per16 || hs % per16) return MSK_ERR_ALIGNMENT;
@@ -779,7 +783,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, h = blockIdx.y, tile = blockIdx.z;
   const int len = cached_len(a), rows = a.T * a.G;
-  const uint64_t deadline = gtimer() + kOpsWaitNs;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
@@ -790,6 +793,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   const int per = (steps + (int)gridDim.x - 1) / (int)gridDim.x;
   const int s0 = min(steps, split * per), s1 = min(steps, s0 + per);
   const int seen = a.window > 0 ? max(0, len + a.T - a.window) : 0;  // keys that every query sees: [seen, len)
+  const uint64_t deadline = gtimer() + kOpsWaitNs + (uint64_t)(s1 - s0) * kOpsStepNs;
 
   if (tid == 0) {
     abort = 0, never = 0;
@@ -1161,7 +1165,10 @@ Kv4Plan plan_attention(int tokens, int group, int Hkv, int keys) {
 size_t plan_bytes(const Kv4Plan& p, int Hkv, int hd) {
   return p.splits == 1 ? 0 : (size_t)p.tiles * Hkv * p.splits * p.tile_rows * (hd + 2) * 4;
 }
-int most_keys(int tokens, int window, int len) { return std::min(len, window > 0 ? window + tokens : len) + tokens; }
+int most_keys(int tokens, int window, int len) {
+  const long long keys = std::min<long long>(len, window > 0 ? (long long)window + tokens : len) + tokens;
+  return (int)std::min<long long>(keys, kMaxRows);
+}
 
 // A kernel over (key ranges, kv heads, row tiles), its shared-memory limit set
 // once a device (`ready`; twice does no harm).

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
   const int ga = (int)((long long)a.groups * rank / a.ks), gb = (int)((long long)a.groups * (rank + 1) / a.ks), ng = gb - ga;
   const int tiles = (int)((a.N + kRows - 1) / kRows);
   const int mine = cluster < tiles ? (tiles - cluster + clusters - 1) / clusters : 0;
-  const uint64_t deadline = gtimer() + kOpsWaitNs;
+  const uint64_t deadline = gtimer() + kOpsWaitNs + (uint64_t)mine * ng * kOpsStepNs;
   // (dynamic shared memory starts at a multiple of 1024 in the shared window)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t ring = smem_u32(smem);

@@ -32,6 +32,8 @@ inline msk_status ops_device(int* nsm) {
 // Bound of every wait of these kernels; after it a kernel records an error
 // (msk_ops_check), ends its copies and MMAs, and returns.
 constexpr uint64_t kOpsWaitNs = 200ull * 1000 * 1000;
+// ... and more for each step of a block's work, many times what it takes.
+constexpr uint64_t kOpsStepNs = 20ull * 1000;
 
 // The SM count the workspace sizes are made for when there is no device to
 // ask; kernels never use more blocks than a workspace has room for.

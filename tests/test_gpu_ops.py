@@ -627,6 +627,42 @@ def test_captured_with_device_positions(M):
                 assert torch.equal(a, b)
 
 
+FIRST_CAPTURED = """
+import torch
+import moe_decode_step_persistent_gb300 as M
+c = M.Kv4Cache.empty(2, 20000, 128)
+kv = torch.randn(16, 2, 128, device="cuda").bfloat16()
+q = torch.randn(16, 8, 128, device="cuda").bfloat16()
+w = M.Fp4Weight(torch.full((1000, 512), 0x22, dtype=torch.uint8, device="cuda"),
+                torch.full((1000, 64), 0x38, dtype=torch.uint8, device="cuda"))
+x = torch.ones(16, 1024, device="cuda").bfloat16()
+tok = torch.zeros(16, dtype=torch.int32, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    M.msk_kv4_write(c, kv, kv, 0)
+    k, v = M.msk_kv4_read(c, 0, 16)
+    o = [M.msk_attention_kv4(q[:t], c, n) for t in (1, 3, 16) for n in (0, 100, 15000)]
+    y = [M.msk_linear_fp4(x[:t], w, out_dtype=torch.float32) for t in (1, 16)]
+    lp = M.msk_token_logprobs(y[1], tok, top=4)
+g.replay()
+torch.cuda.synchronize()
+assert all((t == 1024).all() for t in y) and (k.float() - kv.float()).abs().max() < 2
+assert all(torch.isfinite(t).all() for t in o) and torch.isfinite(lp[0]).all()
+M.msk_ops_check()
+print("captured")
+"""
+
+
+def test_captured_without_a_call_before(M):
+    """The process's first calls are captured ones."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
+
+
 def test_two_calls_at_once(M):
     """Calls on two streams, each with its own workspace, do not disturb each
     other."""

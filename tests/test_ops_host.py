@@ -32,7 +32,7 @@ def cache(M, codes=P, scales=P, heads=8, d=128, max_seq=1024, ks=1.0, vs=1.0):
 BAD_CACHES = [(dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(d=96), SHAPE), (dict(heads=0), SHAPE),
               (dict(max_seq=0), SHAPE), (dict(ks=0.0), INVALID), (dict(vs=-1.0), INVALID),
               (dict(ks=float("nan")), INVALID), (dict(vs=float("inf")), INVALID), (dict(codes=P + 8), ALIGN),
-              (dict(scales=P + 4), ALIGN)]
+              (dict(scales=P + 4), ALIGN), (dict(max_seq=(1 << 30) + 1), SHAPE)]
 
 
 @pytest.mark.parametrize("bad,status", BAD_CACHES)
@@ -54,6 +54,11 @@ def test_rows(M, lib, args, status):
     k, v, dt, tokens, ts, hs, pos = args
     assert lib.msk_kv4_write(cache(M), k, v, dt, tokens, ts, hs, pos, None, None) == status
     assert lib.msk_kv4_read(cache(M), pos, tokens, k, v, dt, ts, hs, None) == status
+
+
+def test_rows_that_overlap_are_not_written(M, lib):
+    for strides in ((0, 128), (1024, 0)):
+        assert lib.msk_kv4_read(cache(M), 0, 4, P, P, BF16, *strides, None) == INVALID
 
 
 def test_no_cache(lib):
@@ -111,6 +116,9 @@ def test_workspace_sizes(lib):
     size = lib.msk_attention_kv4_workspace
     assert size(16, 32, 8, 128, 0, 100000) > 0
     assert size(16, 32, 8, 128, 2048, 100000) == 0 and size(16, 32, 8, 128, 0, 100) == 0
+    most = 2 ** 31 - 1  # (no overflow; a shorter cache or window never needs more)
+    assert size(16, 32, 8, 128, 0, most) >= size(16, 32, 8, 128, 0, 10 ** 6) >= size(16, 32, 8, 128, 0, 10 ** 5)
+    assert size(16, 32, 8, 128, most, most) == size(16, 32, 8, 128, 0, most)
     for bad in ((0, 32, 8, 128, 0, 10), (17, 32, 8, 128, 0, 10), (16, 30, 8, 128, 0, 10), (16, 32, 0, 128, 0, 10),
                 (16, 32, 8, 128, -1, 10), (16, 32, 8, 128, 0, -1)):
         assert size(*bad) == 0
