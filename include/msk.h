@@ -339,7 +339,7 @@ typedef enum { MSK_BF16 = 0, MSK_FP16 = 1, MSK_FP32 = 2 } msk_dtype;
  *           2i in the low nibble of byte i;
  *   scales: [2][n_kv_heads][max_seq][head_dim / 16] E4M3 block scales.
  * Value = e2m1 * e4m3 * k_scale (keys) or v_scale (values); both positive.
- * Both pointers 16-byte aligned; head_dim 64 or 128. */
+ * Both pointers 16-byte aligned; head_dim 64 or 128; max_seq up to 2^30. */
 typedef struct {
   uint8_t* codes;
   uint8_t* scales;
@@ -364,7 +364,8 @@ msk_status msk_kv4_write(const msk_kv4_desc* cache, const void* k, const void* v
 
 /* The reverse: rows pos0 .. pos0 + tokens - 1 of the cache as values of type
  * dtype (exact in bf16 and fp16 where the tensor's scale is 1, else rounded
- * once), to k and v laid out as above. */
+ * once), to k and v laid out as above; their rows must not overlap (a stride
+ * of 0 is refused). */
 msk_status msk_kv4_read(const msk_kv4_desc* cache, int32_t pos0, int32_t tokens, void* k, void* v, int32_t dtype,
                         int64_t token_stride, int64_t head_stride, void* stream);
 
@@ -413,9 +414,9 @@ msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_stride, con
 msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_stride, const msk_nvfp4_desc* w, int32_t tokens,
                           void* y, int32_t y_dtype, int64_t y_stride, void* stream);
 
-/* Synchronises `stream` and tells whether a bounded device wait of these
- * operators ran out on the current device since the last call of this
- * function: MSK_ERR_TIMEOUT (the outputs of the calls since then are not to be
+/* Synchronises `stream` (so not under capture) and tells whether a bounded
+ * device wait of these operators ran out on the current device since the last
+ * call of this function: MSK_ERR_TIMEOUT (the outputs of the calls since then are not to be
  * used), else MSK_OK. */
 msk_status msk_ops_check(void* stream);
 

@@ -75,8 +75,10 @@ struct Bars {  // mbarriers of a block
 // an mbarrier; a team's sums lie in an accumulator of their own and are added
 // in the epilogue, which reads tile i while tile i + 1 is decoded.
 //
-// Bound by the decoding and DRAM alike: on mma.sync the decoding and the MMAs
-// together take longer than the bytes (16 tokens x 131072 x 4096: 88 us).
+// 131072 x 4096: 61 us for 16 tokens, 59 for one (5.1 TB/s, 75% of what a copy
+// reaches).  Bound by the decoding and DRAM alike: issue slots are 64% in use,
+// the ALU that converts 55%.  On mma.sync the decoding and the MMAs together
+// take longer than the bytes (88 us for 16 tokens).
 //
 // With too few tiles for the GPU, or more columns than x has room for, a
 // cluster of `ks` blocks shares a tile's columns and adds its sums up through

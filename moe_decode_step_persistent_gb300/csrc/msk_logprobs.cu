@@ -390,6 +390,9 @@ __device__ __forceinline__ uint32_t greatest(uint32_t g0, uint32_t g1, int n) {
 // warps' sums, find the alternatives, write the results) in turn while the 16
 // read on.  Each of the two has a place for a row's statistics, which it gives
 // back once it holds them in registers (named barriers, one each way).
+// 1024 x 131072 with 20 alternatives: bf16 56 us (4.8 TB/s), fp32 91 (5.9); a
+// block a row, all warps at its end: 67 and 115.  Issue slots bound it in 16 bits
+// (62% in use; eight instructions for two logits), DRAM in fp32.
 constexpr int kStreamThreads = 512, kFetch = 16, kHits = 128;
 enum { kFull0 = 1, kFree0 = 3 };  // barriers; + 1 for the second place
 template <int ID>
