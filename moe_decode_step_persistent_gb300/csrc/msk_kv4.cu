@@ -233,7 +233,7 @@ msk_status rows_call(bool write, const msk_kv4_desc* c, const void* k, const voi
 // ---------------------------------------------------------------------------
 
 constexpr int kMaxSplits = 128;   // key ranges of a kv head, each a block's, joined by a second kernel
-constexpr int kMaxCluster = 8;    // or, of few keys, the blocks of a cluster
+constexpr int kMaxCluster = 9;    // or, of few keys, the blocks of a cluster (as many clusters of 9 run at once as of 8)
 constexpr int kClusterKeys = 8192;
 constexpr int kRing = 5;          // steps of 16 keys in a warp's ring
 
@@ -318,11 +318,11 @@ __device__ __forceinline__ void store_out4(const Kv4Attn& a, int hd, int h, int 
 // The end of an attention block: its sums, smem[row][PITCH] with the reference
 // and the sum of weights behind each row's elements, go to the workspace, or
 // through the cluster's shared memory, or straight to the output.  A block of a
-// cluster takes the rows rank, rank + cluster, ...
+// cluster takes the rows rank, rank + cluster, ...; every thread reads all that
+// it needs of the others at once.
 template <int HD, int ROWS, int THREADS>
 __device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, int split, int h, int tile) {
   constexpr int PITCH = HD + 4, Q4 = HD / 4;
-  __shared__ float part_f[ROWS][kMaxCluster];  // a block's share of a row's output
   const int rows = min(ROWS, a.T * a.G - tile * ROWS), tid = threadIdx.x;
   if (a.splits > 1) {
     const long long part = (((long long)tile * a.Hkv + h) * a.splits + split) * ROWS;
@@ -335,37 +335,28 @@ __device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, int 
   }
   if (a.cluster > 1) cluster_sync();
   const int step = a.cluster, first = a.cluster > 1 ? split : 0;
-  for (int r = first + tid * step; r < rows; r += THREADS * step) {
-    const uint32_t at = smem_u32(smem + r * PITCH + HD);
-    float m[kMaxCluster], l[kMaxCluster], mm = -INFINITY, ll = 0.f;
-#pragma unroll
-    for (int b = 0; b < kMaxCluster; ++b) {
-      m[b] = b < a.cluster ? ld_cluster(mapa(at, b)) : -INFINITY;
-      l[b] = b < a.cluster ? ld_cluster(mapa(at + 4, b)) : 0.f;
-      mm = fmaxf(mm, m[b]);
-    }
-#pragma unroll
-    for (int b = 0; b < kMaxCluster; ++b) m[b] = ex2(m[b] - mm), ll += m[b] * l[b];
-#pragma unroll
-    for (int b = 0; b < kMaxCluster; ++b) part_f[r][b] = m[b] / ll * a.v_scale;
-  }
-  __syncthreads();
   for (int e = tid; e < (rows - first + step - 1) / step * Q4; e += THREADS) {
     const int r = first + e / Q4 * step, q = e % Q4;
-    const uint32_t at = smem_u32(smem + r * PITCH + q * 4);
-    float4 v[kMaxCluster], y = make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint32_t at = smem_u32(smem + r * PITCH);
+    float4 v[kMaxCluster];
+    float2 ml[kMaxCluster];
 #pragma unroll
     for (int b = 0; b < kMaxCluster; ++b) {
-      v[b] = y;
-      if (b < a.cluster) v[b] = ld_cluster4(mapa(at, b));
+      v[b] = make_float4(0.f, 0.f, 0.f, 0.f), ml[b] = make_float2(-INFINITY, 0.f);
+      if (b < a.cluster) v[b] = ld_cluster4(mapa(at + q * 16, b)), ml[b] = ld_cluster2(mapa(at + HD * 4, b));
     }
+    float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-    for (int b = 0; b < kMaxCluster; ++b)
-      if (b < a.cluster) {
-        const float f = part_f[r][b];
-        y.x += f * v[b].x, y.y += f * v[b].y, y.z += f * v[b].z, y.w += f * v[b].w;
-      }
-    store_out4(a, HD, h, tile * ROWS + r, q * 4, y);
+    for (int b = 0; b < kMaxCluster; ++b) mm = fmaxf(mm, ml[b].x);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int b = 0; b < kMaxCluster; ++b) {
+      const float f = ex2(ml[b].x - mm);
+      ll += f * ml[b].y;
+      y.x += f * v[b].x, y.y += f * v[b].y, y.z += f * v[b].z, y.w += f * v[b].w;
+    }
+    const float f = a.v_scale / ll;
+    store_out4(a, HD, h, tile * ROWS + r, q * 4, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
   }
   if (a.cluster > 1) cluster_sync();  // (no block leaves while its sums may be read)
 }
@@ -1157,7 +1148,9 @@ Kv4Plan plan_attention(int tokens, int group, int Hkv, int keys) {
   if (keys <= kClusterKeys) {
     // a block for every 128 keys (16 a warp), or 256 (a step for each team)
     const int block = p.tile_rows == kTcRows ? kTcTeams * kTcKeys : 128;
-    while (p.cluster < kMaxCluster && keys > block * p.cluster) p.cluster *= 2;
+    // (a window of 2048 and the tokens' own keys: 9 blocks, not 8 of which some
+    // have a step more)
+    p.cluster = std::max(1, std::min(kMaxCluster, (keys + block - 1) / block));
   } else {
     const int per_sm = p.tile_rows == 8 ? 2 : 1;  // blocks that an SM holds
     // up to 64 ranges; more only of 1024 keys each (1 row, 131071 keys, one kv
@@ -1185,6 +1178,7 @@ cudaError_t launch_blocks(void (*kernel)(Args), const Args& args, bool (&ready)[
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev]) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
