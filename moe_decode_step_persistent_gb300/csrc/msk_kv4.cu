@@ -316,12 +316,14 @@ __device__ __forceinline__ void store_out4(const Kv4Attn& a, int hd, int h, int 
 }
 
 // The end of an attention block: its sums, smem[row][PITCH] with the reference
-// and the sum of weights behind each row's elements, go to the workspace, or
-// through the cluster's shared memory, or straight to the output.  A block of a
-// cluster takes the rows rank, rank + cluster, ...; every thread reads all that
-// it needs of the others at once.
+// and the sum of weights behind each row's elements, go to the workspace or
+// straight to the output; or to the block of the cluster that joins the row, rank
+// r mod cluster: all blocks push into `recv` there, so that one barrier lies
+// between the sums and the output and nothing remote is read.  (The cluster's
+// first barrier, entered at the block's start, says that all blocks are there.)
+constexpr int recv_bytes(int rows, int hd) { return (rows + kMaxCluster - 1) * (hd + 4) * 4; }
 template <int HD, int ROWS, int THREADS>
-__device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, int split, int h, int tile) {
+__device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, float* recv, int split, int h, int tile) {
   constexpr int PITCH = HD + 4, Q4 = HD / 4;
   const int rows = min(ROWS, a.T * a.G - tile * ROWS), tid = threadIdx.x;
   if (a.splits > 1) {
@@ -333,32 +335,36 @@ __device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, int 
     for (int r = tid; r < rows; r += THREADS) a.ml_part[part + r] = make_float2(smem[r * PITCH + HD], smem[r * PITCH + HD + 1]);
     return;
   }
-  if (a.cluster > 1) cluster_sync();
-  const int step = a.cluster, first = a.cluster > 1 ? split : 0;
-  for (int e = tid; e < (rows - first + step - 1) / step * Q4; e += THREADS) {
-    const int r = first + e / Q4 * step, q = e % Q4;
-    const uint32_t at = smem_u32(smem + r * PITCH);
-    float4 v[kMaxCluster];
-    float2 ml[kMaxCluster];
-#pragma unroll
-    for (int b = 0; b < kMaxCluster; ++b) {
-      v[b] = make_float4(0.f, 0.f, 0.f, 0.f), ml[b] = make_float2(-INFINITY, 0.f);
-      if (b < a.cluster) v[b] = ld_cluster4(mapa(at + q * 16, b)), ml[b] = ld_cluster2(mapa(at + HD * 4, b));
+  const int n = a.cluster, rank = n > 1 ? split : 0;
+  const float* from = smem;
+  if (n > 1) {
+    cluster_wait();
+    for (int e = tid; e < rows * Q4; e += THREADS) {
+      const int r = e / Q4, q = e % Q4, to = r % n;
+      const float* x = smem + r * PITCH + q * 4;
+      const uint32_t at = smem_u32(recv + (r / n * n + rank) * PITCH + q * 4);
+      st_cluster4(mapa(at, to), *reinterpret_cast<const float4*>(x));
+      if (q == Q4 - 1) st_cluster4(mapa(at + 16, to), *reinterpret_cast<const float4*>(x + 4));
     }
+    cluster_arrive();
+    cluster_wait();
+    from = recv;
+  }
+  for (int e = tid; e < (rows - rank + n - 1) / n * Q4; e += THREADS) {
+    const int i = e / Q4, q = e % Q4;
+    const float* x = from + i * n * PITCH;
     float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-    for (int b = 0; b < kMaxCluster; ++b) mm = fmaxf(mm, ml[b].x);
+    for (int b = 0; b < n; ++b) mm = fmaxf(mm, x[b * PITCH + HD]);
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int b = 0; b < kMaxCluster; ++b) {
-      const float f = ex2(ml[b].x - mm);
-      ll += f * ml[b].y;
-      y.x += f * v[b].x, y.y += f * v[b].y, y.z += f * v[b].z, y.w += f * v[b].w;
+    for (int b = 0; b < n; ++b) {
+      const float f = ex2(x[b * PITCH + HD] - mm);  // (a block without a visible key: 0)
+      const float4 v = *reinterpret_cast<const float4*>(x + b * PITCH + q * 4);
+      ll += f * x[b * PITCH + HD + 1];
+      y.x += f * v.x, y.y += f * v.y, y.z += f * v.z, y.w += f * v.w;
     }
     const float f = a.v_scale / ll;
-    store_out4(a, HD, h, tile * ROWS + r, q * 4, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+    store_out4(a, HD, h, tile * ROWS + i * n + rank, q * 4, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
   }
-  if (a.cluster > 1) cluster_sync();  // (no block leaves while its sums may be read)
 }
 
 // Few query rows (8 NT of them in a tile; row = token * group + head of the
@@ -387,6 +393,10 @@ __device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, int 
 // and a multiply for two elements; the ALU 56%, issue slots 59% in use) beside
 // DRAM.  Q in shared memory for three blocks an SM instead of two: 43 us.
 template <int HD, int NT>
+constexpr int rows_smem() {  // the rings, then the warps' sums
+  return std::max(8 * kRing * Kv16<HD>::BYTES, 8 * 8 * NT * (HD + 4) * 4 + 8 * 8 * NT * 8);
+}
+template <int HD, int NT>
 __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __grid_constant__ Kv4Attn a) {
   constexpr int KS = HD / 16, MT = HD / 16, ROWS = 8 * NT, PITCH = HD + 4;
   using K16 = Kv16<HD>;
@@ -395,6 +405,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
   float2* sml = reinterpret_cast<float2*>(smem + 8 * ROWS * PITCH);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int split = blockIdx.x, h = blockIdx.y, tile = blockIdx.z;
+  if (a.cluster > 1) cluster_arrive();
   const int len = cached_len(a), rows = a.T * a.G;
 
   // this block's keys: in steps of 16 handed round the warps
@@ -644,7 +655,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
     if (d == 0) smem[r * PITCH + HD] = mm, smem[r * PITCH + HD + 1] = ll;
   }
   __syncthreads();
-  finish_block<HD, ROWS, 256>(a, smem, split, h, tile);
+  finish_block<HD, ROWS, 256>(a, smem, smem + rows_smem<HD, NT>() / 4, split, h, tile);
 }
 
 // ---------------------------------------------------------------------------
@@ -664,7 +675,7 @@ struct Tc {
   static constexpr int CODES = kTcKeys * HD / 2;                // bytes of a step's keys (or values)
   static constexpr int Q = kTcRows * HD * 2, V = kTcKeys * HD * 2, P = kTcKeys * kTcRows * 2;
   static constexpr int TEAM = V + P + kTcSlots * 2 * CODES;     // a team's shared memory
-  static constexpr int SMEM = 1024 + Q + kTcTeams * TEAM;
+  static constexpr int SMEM = 1024 + Q + kTcTeams * TEAM + recv_bytes(kTcRows, HD);
   // tensor memory columns: decoded keys, scores, output sums
   static constexpr int A0 = 0, S0 = kTcTeams * HD / 2, O0 = S0 + kTcTeams * kTcRows, COLS = 512;
   static_assert(O0 + kTcTeams * kTcRows <= COLS);
@@ -778,6 +789,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   const Kv4Attn& a = args.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, h = blockIdx.y, tile = blockIdx.z;
+  if (a.cluster > 1) cluster_arrive();
   const int len = cached_len(a), rows = a.T * a.G;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
@@ -791,33 +803,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   const int seen = a.window > 0 ? max(0, len + a.T - a.window) : 0;  // keys that every query sees: [seen, len)
   const uint64_t deadline = gtimer() + kOpsWaitNs + (uint64_t)(s1 - s0) * kOpsStepNs;
 
-  if (tid == 0) {
-    abort = 0, never = 0;
-    for (int t = 0; t < kTcTeams; ++t) {
-      for (int i = 0; i < kTcSlots; ++i) mbar_init(bar(bars.full[t][i]), 1), mbar_init(bar(bars.empty[t][i]), 8);
-      mbar_init(bar(bars.kready[t]), 8), mbar_init(bar(bars.sdone[t]), 1);
-      mbar_init(bar(bars.pready[t]), 8), mbar_init(bar(bars.pvdone[t]), 1);
-    }
-    mbar_fence_init();
-  }
   if (tid < kTcRows) {
     const int row = tile * kTcRows + tid;
     tok[tid] = row < rows ? (uint8_t)(row / a.G) : 31;
     for (int t = 0; t < kTcTeams; ++t) nm[t][tid] = row < rows ? INFINITY : 0.f;
   }
-  if (warp == 0) tmem_alloc(smem_u32(&tmem_base), L::COLS);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_base;
-  const volatile int* ab = &abort;
-  auto wait = [&](uint64_t& b, uint32_t parity) {
-    if (mbar_wait(bar(b), parity, deadline, ab)) return true;
-    abort = 1;
-    return false;
-  };
-  auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
-
   const int team = warp < kTcWorkers ? warp >> 3 : warp - kTcWorkers;
   const int mine = max(0, (s1 - s0 - team + kTcTeams - 1) / kTcTeams);  // this team's steps
   uint8_t* tsm = smem + L::Q + team * L::TEAM;
@@ -836,18 +826,67 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   };
   const bool issuer = warp >= kTcWorkers && lane == 0;
 
-  if (issuer)
+  // everything from memory that the first step needs is under way before the
+  // block's set-up: the keys and values, their scales, the queries
+  if (issuer) {
+    for (int i = 0; i < kTcSlots; ++i) mbar_init(bar(bars.full[team][i]), 1), mbar_init(bar(bars.empty[team][i]), 8);
+    mbar_init(bar(bars.kready[team]), 8), mbar_init(bar(bars.sdone[team]), 1);
+    mbar_init(bar(bars.pready[team]), 8), mbar_init(bar(bars.pvdone[team]), 1);
+    mbar_fence_init();
+    fence_proxy_async_shared();
     for (int it = 0; it < min(mine, kTcSlots); ++it) load(it);
+  }
+  const int quad = warp & 3, half = (warp >> 2) & 1, r = quad * 32 + lane;  // (workers) r: the thread's key of a step
+  // block scales of this thread's key and value, a step ahead
+  const uint8_t* es = a.scales + (long long)h * a.max_seq * (HD / 16) + half * (HD / 32);
+  const long long vs = (long long)a.Hkv * a.max_seq * (HD / 16);
+  uint32_t ek = 0, ev = 0;
+  auto scales = [&](int it) {
+    const int j = lo + (s0 + team + it * kTcTeams) * kTcKeys + r;
+    ek = ev = 0;  // (rows past the last one may hold anything, NaN scales too)
+    if (it < mine && j < n) {
+      const uint8_t* p = es + (long long)j * (HD / 16);
+      if (HD == 128) {
+        ek = __ldg(reinterpret_cast<const uint32_t*>(p));
+        ev = __ldg(reinterpret_cast<const uint32_t*>(p + vs));
+      } else {
+        ek = __ldg(reinterpret_cast<const uint16_t*>(p));
+        ev = __ldg(reinterpret_cast<const uint16_t*>(p + vs));
+      }
+    }
+  };
+  constexpr int RP = HD / 8, QN = kTcRows * RP / (32 * kTcWorkers);  // 16-byte pieces of a query row, a lane for each
+  uint4 qv[QN];
+  if (warp < kTcWorkers) {
+    scales(0);
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+      const int e = tid + i * 32 * kTcWorkers, row = tile * kTcRows + e / RP;
+      qv[i] = make_uint4(0, 0, 0, 0);
+      if (row < rows)
+        qv[i] = *reinterpret_cast<const uint4*>(a.q + (row / a.G) * a.q_stride + (long long)(h * a.G + row % a.G) * HD + e % RP * 8);
+    }
+  }
+  if (tid == 0) abort = 0, never = 0;
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_base), L::COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const volatile int* ab = &abort;
+  auto wait = [&](uint64_t& b, uint32_t parity) {
+    if (mbar_wait(bar(b), parity, deadline, ab)) return true;
+    abort = 1;
+    return false;
+  };
+  auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
+
   if (warp < kTcWorkers) {
     // Q as the B operand: fp16 after a scaling of each row by a power of two
-    constexpr int RP = HD / 8;  // 16-byte pieces of a row, a lane for each
 #pragma unroll
-    for (int i = 0; i < kTcRows * RP / (32 * kTcWorkers); ++i) {
-      const int e = tid + i * 32 * kTcWorkers, r = e / RP, piece = e % RP, row = tile * kTcRows + r;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (row < rows)
-        u = *reinterpret_cast<const uint4*>(a.q + (row / a.G) * a.q_stride + (long long)(h * a.G + row % a.G) * HD + piece * 8);
-      uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int i = 0; i < QN; ++i) {
+      const int e = tid + i * 32 * kTcWorkers, r = e / RP, piece = e % RP;
+      uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
       float most = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -876,7 +915,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
 
   if (warp < kTcWorkers) {
     constexpr int RW = NR / 2, CP = PIECES / 2;  // query rows, pieces of codes of a thread
-    const int quad = warp & 3, half = (warp >> 2) & 1, r = quad * 32 + lane;  // r: the thread's key of a step
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t tk = tl + L::A0 + team * HD / 2 + half * HD / 4, ts = tl + L::S0 + team * kTcRows + half * RW;
     const uint32_t to = tl + L::O0 + team * kTcRows + half * RW;
@@ -887,25 +925,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
     float l[RW];
 #pragma unroll
     for (int i = 0; i < RW; ++i) l[i] = 0.f;
-    // block scales of this thread's key and value, a step ahead
-    const uint8_t* es = a.scales + (long long)h * a.max_seq * (HD / 16) + half * (HD / 32);
-    const long long vs = (long long)a.Hkv * a.max_seq * (HD / 16);
-    uint32_t ek, ev;
-    auto scales = [&](int it) {
-      const int j = lo + (s0 + team + it * kTcTeams) * kTcKeys + r;
-      ek = ev = 0;  // (rows past the last one may hold anything, NaN scales too)
-      if (it < mine && j < n) {
-        const uint8_t* p = es + (long long)j * (HD / 16);
-        if (HD == 128) {
-          ek = __ldg(reinterpret_cast<const uint32_t*>(p));
-          ev = __ldg(reinterpret_cast<const uint32_t*>(p + vs));
-        } else {
-          ek = __ldg(reinterpret_cast<const uint16_t*>(p));
-          ev = __ldg(reinterpret_cast<const uint16_t*>(p + vs));
-        }
-      }
-    };
-    scales(0);
     // (a wait that runs out sets `abort`, after which no wait waits: the warps
     // still come to each of the team's barriers)
     for (int it = 0; it < mine; ++it) {
@@ -961,16 +980,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
             if ((hide >> htok[i]) & 1u) y[i] = -INFINITY;
         }
       };
-      scores();
-      float most = -INFINITY;
+      bool raise = it == 0;
+      if (!raise) {
+        scores();
+        float most = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < RW; ++i) most = fmaxf(most, y[i]);
-      if (half_any(id, most > 8.f)) {
+        for (int i = 0; i < RW; ++i) most = fmaxf(most, y[i]);
+        raise = half_any(id, most > 8.f);
+      }
+      if (raise) {
         // raise the references: the rows' maxima over the step's keys, lane i
         // ending with row i's
         tmem_ld<RW>(ts, y);
 #pragma unroll
-        for (int i = 0; i < RW; ++i) y[i] = (hide >> htok[i]) & 1u ? -INFINITY : y[i] * hfac[i];
+        for (int i = 0; i < RW; ++i) y[i] *= hfac[i];
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < RW; ++i)
+            if ((hide >> htok[i]) & 1u) y[i] = -INFINITY;
+        }
         const float zm = spread(y, lane, [](float u, float w) { return fmaxf(u, w); });
         if (lane < RW) wmax[team][quad][half * RW + lane] = zm;
         named_bar(id, 128);
@@ -992,8 +1020,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
           for (int i = 0; i < RW; ++i) w[i] = __float_as_uint(y[i] * hal[i]);
           tmem_st<RW>(to, w);
         }
-        scores();  // (a row still without a reference sees none of these keys)
-        named_bar(id, 128);  // (the maxima and factors may be written again)
+        // (a row still without a reference sees none of these keys; the maxima
+        // and factors are written again after another barrier of these warps)
+        scores();
       }
 #pragma unroll
       for (int i = 0; i < RW; ++i) {
@@ -1095,7 +1124,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
     tmem_dealloc(tmem, L::COLS);
   }
   if (tid == 0 && abort) atomicExch(&g_error, 1u);
-  finish_block<HD, kTcRows, kTcThreads>(a, out, split, h, tile);
+  finish_block<HD, kTcRows, kTcThreads>(a, out, reinterpret_cast<float*>(smem + L::Q + kTcTeams * L::TEAM), split, h, tile);
 }
 
 // The key ranges of a (token, query head): a block of four groups of HD
@@ -1197,7 +1226,7 @@ cudaError_t launch_blocks(void (*kernel)(Args), const Args& args, bool (&ready)[
 template <int HD, int NT>
 cudaError_t launch_rows_kernel(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st) {
   static bool ready[64] = {};
-  constexpr int smem = std::max(8 * kRing * Kv16<HD>::BYTES, 8 * 8 * NT * (HD + 4) * 4 + 8 * 8 * NT * 8);
+  constexpr int smem = rows_smem<HD, NT>() + recv_bytes(8 * NT, HD);
   return launch_blocks(kv4_rows_kernel<HD, NT>, a, ready, 256, smem, p, a.Hkv, st);
 }
 
