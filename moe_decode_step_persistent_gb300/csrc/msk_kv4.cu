@@ -687,6 +687,14 @@ struct TcBars {
   uint64_t kready[kTcTeams], sdone[kTcTeams], pready[kTcTeams], pvdone[kTcTeams];
 };
 
+struct TcQuery {  // what the block holds of its query rows
+  float fac[kTcRows];            // scores in log2 units: times this
+  int unseen[kTcRows];           // the last cached key that the row does not see
+  uint32_t own[kTcRows];         // which of the tokens' own keys it sees (all, past the last row)
+  float nm[kTcTeams][kTcRows];   // the references' negatives (+inf: none yet)
+  float al[kTcTeams][kTcRows];   // factors of a rescaling
+};
+
 struct Kv4AttnTc {
   CUtensorMap map;  // [2 Hkv][max_seq][HD / 2] bytes, boxes of 1 x 128 x HD / 2
   Kv4Attn a;
@@ -778,13 +786,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   constexpr int PITCH = HD + 4, PIECES = HD / 32;  // 16-byte pieces of a row's codes
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ TcBars bars;
-  __shared__ __align__(16) float nm[kTcTeams][kTcRows];   // the references' negatives (+inf: none yet)
-  __shared__ __align__(16) float al[kTcTeams][kTcRows];   // factors of a rescaling
+  __shared__ __align__(16) TcQuery query;
   __shared__ float wmax[kTcTeams][4][kTcRows];            // a warp's maxima; its sums at the end
   __shared__ float jf[kTcTeams][kTcRows];                 // a team's share when the two are joined
-  __shared__ __align__(16) float fac[kTcRows];            // a row's scores in log2 units: times this
   __shared__ uint32_t tmem_base;
-  __shared__ uint8_t tok[kTcRows];                        // a row's token, 31 past the last row
   __shared__ int abort, never;
   const Kv4Attn& a = args.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -805,8 +810,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
 
   if (tid < kTcRows) {
     const int row = tile * kTcRows + tid;
-    tok[tid] = row < rows ? (uint8_t)(row / a.G) : 31;
-    for (int t = 0; t < kTcTeams; ++t) nm[t][tid] = row < rows ? INFINITY : 0.f;
+    const int t = row < rows ? row / a.G : -1;
+    query.unseen[tid] = t >= 0 && a.window > 0 ? len + a.depth[t] - a.window : -1;
+    query.own[tid] = t >= 0 ? a.vis[t] : ~0u;
+    for (int i = 0; i < kTcTeams; ++i) query.nm[i][tid] = t >= 0 ? INFINITY : 0.f;
   }
   const int team = warp < kTcWorkers ? warp >> 3 : warp - kTcWorkers;
   const int mine = max(0, (s1 - s0 - team + kTcTeams - 1) / kTcTeams);  // this team's steps
@@ -829,6 +836,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   // everything from memory that the first step needs is under way before the
   // block's set-up: the keys and values, their scales, the queries
   if (issuer) {
+    prefetch_tensormap(&args.map);
     for (int i = 0; i < kTcSlots; ++i) mbar_init(bar(bars.full[team][i]), 1), mbar_init(bar(bars.empty[team][i]), 8);
     mbar_init(bar(bars.kready[team]), 8), mbar_init(bar(bars.sdone[team]), 1);
     mbar_init(bar(bars.pready[team]), 8), mbar_init(bar(bars.pvdone[team]), 1);
@@ -897,7 +905,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
       for (int k = 1; k < RP; k <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, k));
       const int sh = row_shift(most);
       const float mul = exp2i(sh);
-      if (piece == 0) fac[r] = a.qk_scale * exp2i(-sh);
+      if (piece == 0) query.fac[r] = a.qk_scale * exp2i(-sh);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = unpack16(w[j], a.fp16);
@@ -919,9 +927,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
     const uint32_t tk = tl + L::A0 + team * HD / 2 + half * HD / 4, ts = tl + L::S0 + team * kTcRows + half * RW;
     const uint32_t to = tl + L::O0 + team * kTcRows + half * RW;
     const int id = 1 + 2 * team + half;  // the barrier of the four warps with the same rows
-    const float* hfac = fac + half * RW;
-    float *hnm = nm[team] + half * RW, *hal = al[team] + half * RW;
-    const uint8_t* htok = tok + half * RW;
+    // this thread's rows; its team's references lie 3 arrays on, their factors 2 more
+    float* hq = query.fac + half * RW;
+    const float* hfac = hq;
+    float *hnm = hq + (3 + team) * kTcRows, *hal = hnm + 2 * kTcRows;
+    static_assert(offsetof(TcQuery, nm) == 3 * kTcRows * 4 && kTcTeams == 2);
     float l[RW];
 #pragma unroll
     for (int i = 0; i < RW; ++i) l[i] = 0.f;
@@ -958,14 +968,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars.empty[team][slot]));
       scales(it + 1);
-      // the scores of this key
-      uint32_t hide = 0;  // tokens that do not see it
-      if (j0 < seen || j0 + kTcKeys > len)
-        for (int t = 0; t < a.T; ++t) hide |= (uint32_t)!sees(a, t, j0 + r, len) << t;
       wait_warp(bars.sdone[team], it & 1);
       tc_fence_after();
       const bool edge = j0 < seen || j0 + kTcKeys > len;
-      float y[RW];
+      float y[RW];  // the scores of this key
+      auto mask = [&]() {
+        const int j = j0 + r, bit = min(j - len, 31);  // (a real row sees none of the keys past its own)
+#pragma unroll
+        for (int i = 0; i < RW; i += 4) {
+          if (j < len) {
+            const int4 u = *reinterpret_cast<const int4*>(hq + kTcRows + i);
+            y[i] = j > u.x ? y[i] : -INFINITY, y[i + 1] = j > u.y ? y[i + 1] : -INFINITY;
+            y[i + 2] = j > u.z ? y[i + 2] : -INFINITY, y[i + 3] = j > u.w ? y[i + 3] : -INFINITY;
+          } else {
+            const uint4 u = *reinterpret_cast<const uint4*>(hq + 2 * kTcRows + i);
+            y[i] = u.x >> bit & 1 ? y[i] : -INFINITY, y[i + 1] = u.y >> bit & 1 ? y[i + 1] : -INFINITY;
+            y[i + 2] = u.z >> bit & 1 ? y[i + 2] : -INFINITY, y[i + 3] = u.w >> bit & 1 ? y[i + 3] : -INFINITY;
+          }
+        }
+      };
       auto scores = [&]() {  // in log2 units, relative to the references
         tmem_ld<RW>(ts, y);
 #pragma unroll
@@ -974,11 +995,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
           y[i] = fmaf(y[i], f.x, m.x), y[i + 1] = fmaf(y[i + 1], f.y, m.y);
           y[i + 2] = fmaf(y[i + 2], f.z, m.z), y[i + 3] = fmaf(y[i + 3], f.w, m.w);
         }
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < RW; ++i)
-            if ((hide >> htok[i]) & 1u) y[i] = -INFINITY;
-        }
+        if (edge) mask();
       };
       bool raise = it == 0;
       if (!raise) {
@@ -994,11 +1011,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
         tmem_ld<RW>(ts, y);
 #pragma unroll
         for (int i = 0; i < RW; ++i) y[i] *= hfac[i];
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < RW; ++i)
-            if ((hide >> htok[i]) & 1u) y[i] = -INFINITY;
-        }
+        if (edge) mask();
         const float zm = spread(y, lane, [](float u, float w) { return fmaxf(u, w); });
         if (lane < RW) wmax[team][quad][half * RW + lane] = zm;
         named_bar(id, 128);
@@ -1006,7 +1019,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
           const int row = half * RW + r;
           const float old = -hnm[r];
           float mx = fmaxf(fmaxf(wmax[team][0][row], wmax[team][1][row]), fmaxf(wmax[team][2][row], wmax[team][3][row]));
-          mx = htok[r] == 31 ? old : fmaxf(old, mx);
+          mx = tile * kTcRows + row < rows ? fmaxf(old, mx) : old;
           hal[r] = mx == -INFINITY ? 1.f : ex2(old - mx);
           hnm[r] = -mx;
         }
@@ -1094,7 +1107,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   float* out = reinterpret_cast<float*>(smem + L::Q);
   const bool one = s0 < s1, two = s0 + 1 < s1;  // teams that had steps
   if (tid < NR) {
-    const float m0 = one ? -nm[0][tid] : -INFINITY, m1 = two ? -nm[1][tid] : -INFINITY, mm = fmaxf(m0, m1);
+    const float m0 = one ? -query.nm[0][tid] : -INFINITY, m1 = two ? -query.nm[1][tid] : -INFINITY, mm = fmaxf(m0, m1);
     const float ref = mm == -INFINITY ? 0.f : mm, f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
     jf[0][tid] = f0, jf[1][tid] = f1;
     float s = 0.f;
