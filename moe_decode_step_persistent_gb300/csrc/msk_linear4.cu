@@ -26,7 +26,9 @@ constexpr int kChunks = kGroup / 64;  // decoded operands of a stage
 constexpr int kCodeBytes = kRows * kGroup / 2, kScaleBytes = kRows * kGroup / 16, kStageBytes = kCodeBytes + kScaleBytes;
 constexpr int kMaxKs = 8;          // blocks of a cluster along the columns
 constexpr int kSmem = 224 * 1024;  // (dynamic; 3 KB of the block's 227 are static or aligned away)
-constexpr int kPartBytes = 2 * 16 * kRows * 4;  // partial sums for the other blocks, two tiles
+// Partial sums from the cluster's blocks, two tiles: units of a token's 32 rows
+// that this block adds up, a slot for each block.
+constexpr int kUnits = 16 * kRows / 32, kPartFloats = (kUnits + kMaxKs) * 32, kPartBytes = 2 * kPartFloats * 4;
 // tensor memory columns: decoded operands, then two sets of accumulators
 constexpr int kACols = 32, kDCols = 16, kD0 = kTeams * kABufs * kACols;
 
@@ -55,7 +57,7 @@ struct Bars {  // mbarriers of a block
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t afull[kTeams][kABufs], aempty[kTeams][kABufs];
   uint64_t dfull[2], dempty[2];
-  uint64_t parts[2];     // the cluster's partial sums of a tile are written
+  uint64_t parts[2], pfree[2];  // the cluster's partial sums of a tile are there; have been read in every block
   uint64_t xfull;
   uint64_t done[kTeams];  // an issuer's MMAs are complete
 };
@@ -81,9 +83,11 @@ struct Bars {  // mbarriers of a block
 // take longer than the bytes (88 us for 16 tokens).
 //
 // With too few tiles for the GPU, or more columns than x has room for, a
-// cluster of `ks` blocks shares a tile's columns and adds its sums up through
-// distributed shared memory, in rank order.
-template <int NG>  // 8-token groups that x has room for
+// cluster of `ks` blocks shares a tile's columns and adds its sums up in rank
+// order, each block a share of the tile that the others store into its shared
+// memory (reading them there instead, behind fences: 1 us more for one tile).
+// NG: 8-token groups that x has room for; CL: blocks share tiles in clusters.
+template <int NG, bool CL>
 __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_constant__ Lin4 a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Bars bars;
@@ -92,8 +96,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
   __shared__ uint32_t tmem_base;
   __shared__ int abort, never;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = blockIdx.x % a.ks, clusters = gridDim.x / a.ks, cluster = blockIdx.x / a.ks;
-  const int ga = (int)((long long)a.groups * rank / a.ks), gb = (int)((long long)a.groups * (rank + 1) / a.ks), ng = gb - ga;
+  const int ks = CL ? a.ks : 1;
+  const int rank = blockIdx.x % ks, clusters = gridDim.x / ks, cluster = blockIdx.x / ks;
+  const int ga = a.groups * rank / ks, gb = a.groups * (rank + 1) / ks, ng = gb - ga;  // (at most 128 groups)
   const int tiles = (int)((a.N + kRows - 1) / kRows);
   const int mine = cluster < tiles ? (tiles - cluster + clusters - 1) / clusters : 0;
   const uint64_t deadline = gtimer() + kOpsWaitNs + (uint64_t)mine * ng * kOpsStepNs;
@@ -101,38 +106,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t ring = smem_u32(smem);
   uint8_t* xs = smem + a.stages * kStageBytes;
-  float* parts = reinterpret_cast<float*>(xs + ((a.groups + a.ks - 1) / a.ks) * kChunks * kXBytes<NG>);  // [2][16][128], clusters only
+  float* parts = reinterpret_cast<float*>(xs + ((a.groups + ks - 1) / ks) * kChunks * kXBytes<NG>);  // clusters only
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
-  if (tid == 0) {
-    abort = 0, never = 0;
-    for (int i = 0; i < a.stages; ++i) mbar_init(bar(bars.full[i]), 1), mbar_init(bar(bars.empty[i]), 4);
-    for (int t = 0; t < kTeams; ++t) {
-      for (int i = 0; i < kABufs; ++i) mbar_init(bar(bars.afull[t][i]), 4), mbar_init(bar(bars.aempty[t][i]), 1);
-      mbar_init(bar(bars.done[t]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(bars.dfull[i]), kTeams), mbar_init(bar(bars.dempty[i]), kDeqWarps);
-      mbar_init(bar(bars.parts[i]), kDeqWarps * a.ks);
-    }
-    mbar_init(bar(bars.xfull), 1);
-    mbar_fence_init();
-  }
-  if (tid < 16) amaxs[tid] = 0;
-  if (warp == 0) tmem_alloc(smem_u32(&tmem_base), 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (a.ks > 1) cluster_sync();  // (the others' barriers are set up)
-  const uint32_t tmem = tmem_base;
-  const volatile int* ab = &abort;
-  auto wait = [&](uint64_t& b, uint32_t parity) {
-    if (mbar_wait(bar(b), parity, deadline, ab)) return true;
-    abort = 1;
-    return false;
+  // (what the cluster's blocks have stored)
+  auto wait_parts = [&](uint64_t& b, uint32_t parity) {
+    bool ok = false;
+    for (uint32_t spins = 1; !(ok = mbar_try_wait_cluster(bar(b), parity)); ++spins)
+      if (spins % 64 == 0 && (*(const volatile int*)&abort || gtimer() > deadline)) break;
+    if (!ok) abort = 1;
+    return (bool)__all_sync(0xFFFFFFFFu, ok);
   };
-
-  auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
 
   // --- copies ---------------------------------------------------------------
   const int total = mine * ng;  // stages in all
@@ -143,7 +127,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
     tma_load_2d(dst, &a.codes_map, (ga + g) * (kGroup / 2), row, b);
     if (a.scales_tma) tma_load_2d(dst + kCodeBytes, &a.scales_map, (ga + g) * (kGroup / 16), row, b);
   };
-  if (warp == kDeqWarps && lane == 0 && total > 0) {
+  if (warp == kDeqWarps && lane == 0) {  // under way before the block's set-up
+    prefetch_tensormap(&a.x_map);
+    prefetch_tensormap(&a.codes_map);
+    if (a.scales_tma) prefetch_tensormap(&a.scales_map);
+    for (int i = 0; i < a.stages; ++i) mbar_init(bar(bars.full[i]), 1), mbar_init(bar(bars.empty[i]), 4);
+    mbar_init(bar(bars.xfull), 1);
+    mbar_fence_init();
+    fence_proxy_async_shared();
     // x first: behind the ring's copies it would wait for all of them
     mbar_arrive_expect_tx(bar(bars.xfull), ng * kChunks * kXBytes<NG>);
     for (int g = 0; g < ng; ++g)
@@ -154,6 +145,34 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
           : "memory");
     for (int i = 0; i < min(total, a.stages); ++i) load(i, i / ng, i % ng);
   }
+
+  if (tid == 0) {
+    abort = 0, never = 0;
+    for (int t = 0; t < kTeams; ++t) {
+      for (int i = 0; i < kABufs; ++i) mbar_init(bar(bars.afull[t][i]), 4), mbar_init(bar(bars.aempty[t][i]), 1);
+      mbar_init(bar(bars.done[t]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(bars.dfull[i]), kTeams), mbar_init(bar(bars.dempty[i]), kDeqWarps);
+      mbar_init(bar(bars.parts[i]), 1), mbar_init(bar(bars.pfree[i]), kDeqWarps * ks);
+    }
+    mbar_fence_init();
+  }
+  if (tid < 16) amaxs[tid] = 0;
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_base), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (CL) cluster_arrive();  // (waited for below: the others' barriers are set up)
+  const uint32_t tmem = tmem_base;
+  const volatile int* ab = &abort;
+  auto wait = [&](uint64_t& b, uint32_t parity) {
+    if (mbar_wait(bar(b), parity, deadline, ab)) return true;
+    abort = 1;
+    return false;
+  };
+
+  auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
 
   // --- x in place: scaled by a power of two for each token, fp16 ---------------
   if (warp < kDeqWarps && total > 0) {
@@ -201,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
     if (tid < 16) back[tid] = a.fp16 ? 1.f : exp2i(-row_shift(__uint_as_float(amaxs[tid])));
   }
   __syncthreads();
+  if (CL) cluster_wait();
 
   if (warp < kDeqWarps) {
     // --- decoding and epilogue ----------------------------------------------
@@ -230,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
         else if (a.y_dtype == MSK_FP16) static_cast<__half*>(a.y)[o] = __float2half_rn(v);
         else static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
       };
-      if (a.ks == 1) {
+      if (!CL) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int t = team * 4 + j;
@@ -238,30 +258,29 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
         }
         return true;
       }
-      float* mypart = parts + d * 16 * kRows;
+      // Unit u = 4 token + quarter of the rows is added up by block u mod ks.
+      // The sums go there by asynchronous stores that its barrier counts.
+      const int units = 4 * a.T, owned = units > rank ? (units - rank + ks - 1) / ks : 0;
+      if (tid == 0 && owned > 0) mbar_arrive_expect_tx(bar(bars.parts[d]), (uint32_t)(owned * ks * 128));
+      if (i >= 2 && !wait_warp(bars.pfree[d], ((i >> 1) - 1) & 1)) return false;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mypart[(team * 4 + j) * kRows + r] = s[j] * back[team * 4 + j];
-      __syncwarp();
-      // (a warp arrives for tile i + 1 only after it has read tile i, and the
-      // buffer is written again for tile i + 2)
-      if (lane < a.ks)
-        asm volatile("fence.acq_rel.cluster;\n\tmbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                         mapa(bar(bars.parts[d]), lane))
-                     : "memory");
-      if (!wait_warp(bars.parts[d], (i >> 1) & 1)) return false;
-      asm volatile("fence.acq_rel.cluster;" ::: "memory");
-      for (int k = rank + warp * a.ks; k < 4 * a.T; k += kDeqWarps * a.ks) {  // (token, 32 rows)
-        const int t = k >> 2, rr = (k & 3) * 32 + lane;
-        const uint32_t at = smem_u32(parts + (d * 16 + t) * kRows + rr);
-        float f[kMaxKs], v = 0.f;
-#pragma unroll
-        for (int b = 0; b < kMaxKs; ++b) {
-          f[b] = 0.f;
-          if (b < a.ks) f[b] = ld_cluster(mapa(at, b));
-        }
-#pragma unroll
-        for (int b = 0; b < kMaxKs; ++b) v += f[b];
-        if (n0 + rr < a.N) store(t, n0 + rr, v * a.ts);
+      for (int j = 0; j < 4; ++j) {
+        const int t = team * 4 + j, u = 4 * t + quad, to = u % ks;
+        if (t < a.T)
+          st_async(mapa(smem_u32(parts + d * kPartFloats + (u / ks * ks + rank) * 32 + lane), to), s[j] * back[t],
+                   mapa(bar(bars.parts[d]), to));
+      }
+      if (owned > 0 && !wait_parts(bars.parts[d], (i >> 1) & 1)) return false;
+      for (int k = warp; k < owned; k += kDeqWarps) {
+        const int u = k * ks + rank, rr = (u & 3) * 32 + lane;
+        const float* f = parts + d * kPartFloats + k * ks * 32 + lane;
+        float v = 0.f;
+        for (int b = 0; b < ks; ++b) v += f[b * 32];
+        if (n0 + rr < a.N) store(u >> 2, n0 + rr, v * a.ts);
+      }
+      if (i + 2 < mine) {  // the place is written again for tile i + 2
+        __syncwarp();
+        if (lane < ks) mbar_arrive_cluster(mapa(bar(bars.pfree[d]), lane));
       }
       return true;
     };
@@ -388,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
     tmem_dealloc(tmem, 512);
   }
   if (tid == 0 && abort) atomicExch(&g_error, 1u);
-  if (a.ks > 1) cluster_sync();  // (no block leaves while its sums may be read)
+  if (CL) cluster_sync();  // (no block leaves while others may store into it)
 }
 
 // A row-major matrix of bytes or 16-bit words, `pitch` bytes between rows, in
@@ -410,25 +429,28 @@ struct Setup {
   int active[kMaxKs + 1] = {};
 };
 
+template <int NG, bool CL>
+bool look_up(Setup& s, int from, int to) {
+  if (cudaFuncSetAttribute(linear4_kernel<NG, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return false;
+  for (int ks = from; ks <= to; ++ks) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3((unsigned)ks), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = kSmem;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)ks, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at, cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&s.active[ks], linear4_kernel<NG, CL>, &cfg) != cudaSuccess || s.active[ks] < 1) return false;
+  }
+  return true;
+}
+
 template <int NG>
 const Setup* setup() {
   static Setup devices[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   Setup& s = devices[dev];
-  std::call_once(s.once, [&s] {
-    if (cudaFuncSetAttribute(linear4_kernel<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return;
-    for (int ks = 1; ks <= kMaxKs; ++ks) {
-      cudaLaunchConfig_t cfg = {};
-      cudaLaunchAttribute at[1];
-      cfg.gridDim = dim3((unsigned)ks), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = kSmem;
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = (unsigned)ks, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-      cfg.attrs = at, cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&s.active[ks], linear4_kernel<NG>, &cfg) != cudaSuccess || s.active[ks] < 1) return;
-    }
-    s.ok = true;
-  });
+  std::call_once(s.once, [&s] { s.ok = look_up<NG, false>(s, 1, 1) && look_up<NG, true>(s, 2, kMaxKs); });
   return s.ok ? &s : nullptr;
 }
 
@@ -461,7 +483,8 @@ msk_status launch_linear(Lin4& a, const void* x, long long x_stride, cudaStream_
   at[0].val.clusterDim.x = (unsigned)a.ks, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear4_kernel<NG>, a) == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
+  const cudaError_t e = a.ks > 1 ? cudaLaunchKernelEx(&cfg, linear4_kernel<NG, true>, a) : cudaLaunchKernelEx(&cfg, linear4_kernel<NG, false>, a);
+  return e == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }
 
 }  // namespace

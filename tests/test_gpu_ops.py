@@ -322,7 +322,8 @@ LIN = [  # tokens, rows, cols, x type, y type
     (16, 6144, 4096, "bf16", "bf16"), (16, 1000, 4096, "bf16", "fp32"), (8, 2048, 1024, "fp16", "fp16"),
     (9, 333, 2048, "bf16", "bf16"), (5, 77, 384, "fp16", "fp32"), (16, 31, 8320, "bf16", "bf16"),
     (3, 5003, 640, "bf16", "bf16"), (2, 257, 16384, "bf16", "bf16"), (16, 65, 12288, "fp16", "fp16"),
-    (16, 130, 32768, "bf16", "fp32"), (13, 40000, 256, "bf16", "bf16"), (7, 4864, 2176, "bf16", "fp32")]
+    (16, 130, 32768, "bf16", "fp32"), (13, 40000, 256, "bf16", "bf16"), (7, 4864, 2176, "bf16", "fp32"),
+    (16, 17800, 8320, "bf16", "fp32"), (1, 19600, 8576, "fp16", "bf16")]  # (clusters that take several tiles)
 
 
 @pytest.mark.parametrize("T,N,K,xt,yt", LIN)
