@@ -291,6 +291,7 @@ def _workspace(given, need, stream):
         if need == 0:
             return None, None, 0
         given = _empty(stream, need, torch.uint8)
+        return given, given.data_ptr(), need
     _need(given.is_contiguous(), "workspace must be contiguous")
     return given, given.data_ptr(), given.numel() * given.element_size()
 
@@ -411,18 +412,21 @@ def msk_attention_kv4(q, cache, cache_len, window=0, parents=None, softmax_scale
     int32 tensor read when the kernels run.  parents: the candidate tree as in
     msk_decode_step_tree, None for the chain.  Nothing is waited for."""
     T, Hq, d = q.shape
-    _need(q.dtype in _DTYPES and d == cache.head_dim and q.stride(2) == 1 and _step(q, 1) in (0, d),
+    ts, hs, es = q.stride()
+    dtype = _DTYPES.get(q.dtype)
+    _need(dtype is not None and d == cache.head_dim and es == 1 and (hs == d or Hq == 1),
           "q: [tokens][n_q_heads][head_dim] with contiguous heads")
     _need(parents is None or len(parents) == T, "parents: one for each token")
     if out is None:
         out = _empty(stream, (T, Hq * d), q.dtype)
-    _need(out.dtype == q.dtype and out.numel() == q.numel() and out.is_contiguous(),
-          "out: contiguous [tokens][n_q_heads * head_dim] of q's type")
+    else:
+        _need(out.dtype == q.dtype and out.numel() == q.numel() and out.is_contiguous(),
+              "out: contiguous [tokens][n_q_heads * head_dim] of q's type")
     host, dev = _position(cache_len)
     need = msk_attention_kv4_workspace(T, Hq, cache.n_kv_heads, d, window, host if dev is None else cache.max_seq - T)
     ws, addr, size = _workspace(workspace, need, stream)
     st = _enqueue(stream, q, out, cache.codes) if ws is None else _enqueue(stream, q, out, cache.codes, ws)
-    _check(load_library().msk_attention_kv4(q.data_ptr(), _DTYPES[q.dtype], _step(q, 0), cache.desc, T, Hq, host, dev,
+    _check(load_library().msk_attention_kv4(q.data_ptr(), dtype, ts if T > 1 else 0, cache.desc, T, Hq, host, dev,
                                             None if parents is None else _positions(parents), int(window),
                                             softmax_scale, out.data_ptr(), addr, size, st), "msk_attention_kv4")
     return out
@@ -432,16 +436,22 @@ def msk_linear_fp4(x, weight, out_dtype=None, out=None, stream=None):
     """x ([tokens][cols] bf16 or fp16, any row stride) times the transposed
     Fp4Weight: [tokens][rows] of out_dtype (x's type unless given) or into
     `out` (any row stride)."""
-    _need(x.dim() == 2 and x.shape[1] == weight.cols and x.stride(1) == 1 and x.dtype in _DTYPES,
+    shape, xt = x.shape, _DTYPES.get(x.dtype)
+    _need(len(shape) == 2 and shape[1] == weight.cols and x.stride(1) == 1 and xt is not None,
           "x: [tokens][cols], contiguous rows")
-    T = x.shape[0]
+    T = shape[0]
+    yt = _DTYPES.get((x.dtype if out_dtype is None else out_dtype) if out is None else out.dtype)
+    _need(yt is not None, "out: of a floating type")
     if out is None:
         out = _empty(stream, (T, weight.rows), x.dtype if out_dtype is None else out_dtype)
-    _need(out.shape == (T, weight.rows) and out.dtype in _DTYPES and (out.stride(1) == 1 or weight.rows <= 1),
-          "out: [tokens][rows] of a floating type, contiguous rows")
+        ys = weight.rows
+    else:
+        _need(out.shape == (T, weight.rows) and (out.stride(1) == 1 or weight.rows <= 1),
+              "out: [tokens][rows], contiguous rows")
+        ys = _step(out, 0)
     st = _enqueue(stream, x, out, weight.packed)
-    _check(load_library().msk_linear_fp4(x.data_ptr(), _DTYPES[x.dtype], _step(x, 0), weight.desc, T, out.data_ptr(),
-                                         _DTYPES[out.dtype], _step(out, 0), st), "msk_linear_fp4")
+    _check(load_library().msk_linear_fp4(x.data_ptr(), xt, _step(x, 0), weight.desc, T, out.data_ptr(), yt, ys, st),
+           "msk_linear_fp4")
     return out
 
 
