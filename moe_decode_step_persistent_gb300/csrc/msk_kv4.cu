@@ -774,10 +774,10 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N]) {
 // each team issues its MMAs and copies.  The reference of a row is raised when a
 // score passes it by 2^8, and the sums rescaled: a few times in all.  On mma.sync
 // 64 rows cost four times the decoding or do not fit the registers: 53 us for
-// 16 tokens over 32768 keys of 8 kv heads, here 27.5 (131072 keys: 70.6).  Bound
+// 16 tokens over 32768 keys of 8 kv heads, here 25.7 (131072 keys: 68.4).  Bound
 // by the chain of a step (decoding, scores, softmax, weights, each through
-// tensor memory) with two teams: issue slots 49%, tensor pipe 22% in use.  A
-// third team has no room in tensor memory and registers.
+// tensor memory; 2.1 us) with two teams: issue slots 49%, tensor pipe 22% in
+// use.  A third team has no room in tensor memory and registers.
 //
 // NR: rows of the 64 that are in use, 32 or 64 (the softmax skips the rest).
 template <int HD, int NR>
