@@ -454,31 +454,33 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
     fs += 8, fk += 8 * K16::CODES, fe += 8 * K16::SCALES;
     fslot = fslot == ring + (kRing - 1) * K16::BYTES ? ring : fslot + K16::BYTES;
   };
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) fetch();
-
   // Q: lane (g, c) of n-tile nt holds row 8 nt + g
-  uint32_t qf[NT][KS][2];
-  float fac[NT][2];
-  int tok[NT][2];  // the tokens of this lane's accumulator columns, -1 past the last row
+  // (its loads go out before the ring's, which would keep them waiting)
+  uint32_t qf[NT][KS][2], w[NT][HD / 8];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int row = tile * ROWS + nt * 8 + g;
-    uint32_t w[HD / 8];
 #pragma unroll
-    for (int j = 0; j < HD / 8; ++j) w[j] = 0;
+    for (int j = 0; j < HD / 8; ++j) w[nt][j] = 0;
     if (row < rows) {
       const uint16_t* p = a.q + (row / a.G) * a.q_stride + (long long)(h * a.G + row % a.G) * HD + c * (HD / 4);
 #pragma unroll
       for (int j = 0; j < HD / 32; ++j) {
         const uint4 u = *reinterpret_cast<const uint4*>(p + 8 * j);
-        w[4 * j] = u.x, w[4 * j + 1] = u.y, w[4 * j + 2] = u.z, w[4 * j + 3] = u.w;
+        w[nt][4 * j] = u.x, w[nt][4 * j + 1] = u.y, w[nt][4 * j + 2] = u.z, w[nt][4 * j + 3] = u.w;
       }
     }
+  }
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) fetch();
+  float fac[NT][2];
+  int tok[NT][2];  // the tokens of this lane's accumulator columns, -1 past the last row
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
     float amax = 0.f;
 #pragma unroll
     for (int j = 0; j < HD / 8; ++j) {
-      const float2 f = unpack16(w[j], a.fp16);
+      const float2 f = unpack16(w[nt][j], a.fp16);
       amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
     for (int j = 0; j < KS; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 f = unpack16(w[2 * j + i], a.fp16);
+        const float2 f = unpack16(w[nt][2 * j + i], a.fp16);
         qf[nt][j][i] = pack_f16x2(f.x * mul, f.y * mul);
       }
 #pragma unroll
@@ -1141,40 +1143,52 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
 }
 
 // The key ranges of a (token, query head): a block of four groups of HD
-// threads that take the ranges in turn.
-template <int HD>
-__global__ void __launch_bounds__(4 * HD) kv4_combine_kernel(const __grid_constant__ Kv4Attn a, int tile_rows) {
-  __shared__ float fs[kMaxSplits], part[4][HD], total;
+// threads.  A group takes every fourth range, all that it needs of N of them at
+// once (their references too: nothing waits for a maximum over all), and the
+// groups meet in shared memory.
+template <int HD, int N>
+__global__ void __launch_bounds__(4 * HD, N > 8 ? 1 : 4) kv4_combine_kernel(const __grid_constant__ Kv4Attn a, int tile_rows) {
+  __shared__ float part[4][HD], pm[4], pl[4];
   const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, d = tid % HD, q = tid / HD;
   const long long base = ((long long)(row / tile_rows) * a.Hkv + h) * a.splits * tile_rows + row % tile_rows;
+  float mm = -INFINITY, l = 0.f, sum = 0.f;
   grid_dep_wait();
-  if (tid < 32) {
-    constexpr int E = kMaxSplits / 32;
-    float2 x[E];
-    float mm = -INFINITY, s = 0.f;
+  for (int s0 = q; s0 < a.splits; s0 += 4 * N) {
+    float o[N];
+    float2 ml[N];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int r = tid + i * 32;
-      x[i] = r < a.splits ? a.ml_part[base + r * tile_rows] : make_float2(-INFINITY, 0.f);
-      mm = fmaxf(mm, x[i].x);
+    for (int i = 0; i < N; ++i) {
+      const int s = s0 + 4 * i;
+      o[i] = 0.f, ml[i] = make_float2(-INFINITY, 0.f);
+      if (s < a.splits) {
+        ml[i] = a.ml_part[base + (long long)s * tile_rows];
+        o[i] = a.o_part[(base + (long long)s * tile_rows) * HD + d];
+      }
     }
-    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+    float m = mm;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float f = ex2(x[i].x - mm);  // (a range without a visible key: 0)
-      fs[tid + i * 32] = f;
-      s += f * x[i].y;
+    for (int i = 0; i < N; ++i) m = fmaxf(m, ml[i].x);
+    const float ref = m == -INFINITY ? 0.f : m, f = ex2(mm - ref);
+    mm = m, l *= f, sum *= f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float g = ex2(ml[i].x - ref);  // (a range without a visible key: 0)
+      l += g * ml[i].y, sum += g * o[i];
     }
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if (tid == 0) total = s;
   }
-  __syncthreads();
-  float sum = 0.f;
-#pragma unroll 8
-  for (int s = q; s < a.splits; s += 4) sum += fs[s] * a.o_part[(base + (long long)s * tile_rows) * HD + d];
   part[q][d] = sum;
+  if (d == 0) pm[q] = mm, pl[q] = l;
   __syncthreads();
-  if (q == 0) store_out(a, HD, h, row, d, ((part[0][d] + part[1][d]) + (part[2][d] + part[3][d])) / total * a.v_scale);
+  if (q == 0) {
+    const float m = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+    float total = 0.f, y = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = ex2(pm[i] - m);
+      total += f * pl[i], y += f * part[i][d];
+    }
+    store_out(a, HD, h, row, d, y / total * a.v_scale);
+  }
 }
 
 // How a call is laid out.  `keys`: the most keys that a head may have to read.
@@ -1274,7 +1288,10 @@ cudaError_t launch_attention(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<HD>, a, p.tile_rows);
+  // many blocks: few registers, so that all run at once (16 tokens x 32 heads, 19
+  // ranges: 25.7 us in all, with 16 ranges at once 30.7; one token, 38: 35.4 and 35.1)
+  return a.T * a.Hq > kOpsSms ? cudaLaunchKernelEx(&cfg, kv4_combine_kernel<HD, 5>, a, p.tile_rows)
+                              : cudaLaunchKernelEx(&cfg, kv4_combine_kernel<HD, 16>, a, p.tile_rows);
 }
 
 }  // namespace
