@@ -388,8 +388,8 @@ __device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, floa
 // reach 256 (of fp16's 65504), and the sums are rescaled a few times in all.
 //
 // A warp's keys come through a ring of kRing steps of its own, by asynchronous
-// copies; warps meet only at the end.  One token, 131071 keys of 8 kv heads: 35
-// us (4.3 TB/s, 63% of what a copy reaches).  Bound by the decoding (a conversion
+// copies; warps meet only at the end.  One token, 131071 keys of 8 kv heads: 34.6
+// us (4.4 TB/s, 64% of what a copy reaches).  Bound by the decoding (a conversion
 // and a multiply for two elements; the ALU 56%, issue slots 59% in use) beside
 // DRAM.  Q in shared memory for three blocks an SM instead of two: 43 us.
 template <int HD, int NT>
@@ -1289,7 +1289,8 @@ cudaError_t launch_attention(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at, cfg.numAttrs = 1;
   // many blocks: few registers, so that all run at once (16 tokens x 32 heads, 19
-  // ranges: 25.7 us in all, with 16 ranges at once 30.7; one token, 38: 35.4 and 35.1)
+  // ranges: 25.7 us in all, with 16 at once a group 30.7; one token, 38 ranges: 35.4
+  // and 35.1)
   return a.T * a.Hq > kOpsSms ? cudaLaunchKernelEx(&cfg, kv4_combine_kernel<HD, 5>, a, p.tile_rows)
                               : cudaLaunchKernelEx(&cfg, kv4_combine_kernel<HD, 16>, a, p.tile_rows);
 }
