@@ -234,7 +234,10 @@ msk_status rows_call(bool write, const msk_kv4_desc* c, const void* k, const voi
 
 constexpr int kMaxSplits = 128;   // key ranges of a kv head, each a block's, joined by a second kernel
 constexpr int kMaxCluster = 9;    // or, of few keys, the blocks of a cluster (as many clusters of 9 run at once as of 8)
-constexpr int kClusterKeys = 8192;
+// Up to so many keys (of a tile of 8 rows, of more) a cluster and its one launch
+// beat ranges and a second kernel: 1 token x 6000 keys 7.9 us and 9.1, 12000 10.8
+// and 10.1; 16 tokens x 2000 11.5 either way, 4000 13.0 and 12.4, 8000 16.8 and 14.5.
+constexpr int cluster_keys(int rows) { return rows <= 8 ? 8192 : 256 * kMaxCluster; }
 constexpr int kRing = 5;          // steps of 16 keys in a warp's ring
 
 struct Kv4Attn {
@@ -781,7 +784,8 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N]) {
 // tensor memory; 2.1 us) with two teams: issue slots 49%, tensor pipe 22% in
 // use.  A third team has no room in tensor memory and registers.
 //
-// NR: rows of the 64 that are in use, 32 or 64 (the softmax skips the rest).
+// NR: rows of the 64 that are in use, 32 or 64 (the softmax skips the rest: 32
+// rows, 32768 keys 22.0 us, as 64 24.9).
 template <int HD, int NR>
 __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_constant__ Kv4AttnTc args) {
   using L = Tc<HD>;
@@ -1198,10 +1202,11 @@ struct Kv4Plan {
 Kv4Plan plan_attention(int tokens, int group, int Hkv, int keys) {
   Kv4Plan p{};
   const int rows = tokens * group;
+  // (16 rows, 16384 keys of 8 kv heads: 13.3 us in a tile of 16, 15.0 in one of 64)
   p.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : kTcRows;
   p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   p.cluster = p.splits = 1;
-  if (keys <= kClusterKeys) {
+  if (keys <= cluster_keys(rows)) {
     // a block for every 128 keys (16 a warp), or 256 (a step for each team)
     const int block = p.tile_rows == kTcRows ? kTcTeams * kTcKeys : 128;
     // (a window of 2048 and the tokens' own keys: 9 blocks, not 8 of which some
@@ -1349,7 +1354,7 @@ extern "C" msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_
   if (!tree_masks(parents, tokens, window, a.depth, a.vis)) return MSK_ERR_INVALID_ARG;
   // (a cache of few rows is laid out by its size, whatever its length now)
   int keys = most_keys(tokens, window, cache->max_seq - tokens);
-  if (cache_len_dev == nullptr && keys > kClusterKeys) keys = most_keys(tokens, window, cache_len);
+  if (cache_len_dev == nullptr && keys > cluster_keys(tokens * G)) keys = most_keys(tokens, window, cache_len);
   const Kv4Plan plan = plan_attention(tokens, G, cache->n_kv_heads, keys);
   const size_t need = plan_bytes(plan, cache->n_kv_heads, cache->head_dim);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MSK_ERR_INVALID_ARG;

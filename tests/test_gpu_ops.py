@@ -473,7 +473,8 @@ def test_logprobs_without_a_distribution(M):
 
 
 @pytest.mark.parametrize("R,V,top,dtype", [(640, 5003, 20, "bf16"), (1300, 8192, 32, "fp16"), (330, 40001, 32, "fp32"),
-                                           (305, 70000, 0, "bf16"), (2500, 129, 9, "bf16"), (600, 4099, 1, "fp32")])
+                                           (305, 70000, 0, "bf16"), (2500, 129, 9, "bf16"), (600, 4099, 1, "fp32"),
+                                           (640, 35003, 20, "bf16"), (320, 17003, 32, "fp32"), (307, 300007, 32, "fp16")])
 def test_logprobs_of_many_rows(M, R, V, top, dtype):
     x = (randn(98, R, V) * 4).to(DT[dtype])
     tokens = torch.randint(-1, V + 1, (R,), generator=gen(99), dtype=torch.int32)
@@ -481,8 +482,8 @@ def test_logprobs_of_many_rows(M, R, V, top, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "fp16"])
-def test_logprobs_of_many_rows_with_ties(M, dtype):
-    R, V = 700, 6007
+@pytest.mark.parametrize("R,V", [(700, 6007), (620, 34007)])
+def test_logprobs_of_many_rows_with_ties(M, dtype, R, V):
     i = torch.arange(V)
     kinds = [torch.full((V,), -3.0), i / 500.0, -i / 500.0, (i % 7).float(), (i // 100).float(),
              torch.where((i == 5999) | (i == 2001), 5.0, float("-inf")), torch.where(i == 1234, 100.0, 0.0),
@@ -501,7 +502,7 @@ def test_logprobs_of_many_rows_with_ties(M, dtype):
     ("bf16", 1e6, 1.0), ("bf16", 1e6, 1e5), ("bf16", 1e37, 1.0), ("bf16", 1e-36, 1e-30), ("fp16", 2e4, 1.0), ("fp16", 2e4, 1e-5),
     ("fp16", 1e-6, 1e-7), ("fp32", 1e9, 1e-3), ("fp32", 1e20, 1e20), ("fp32", 1.0, 1e-30), ("fp32", 1.0, 1e30),
     ("bf16", 1e-3, 1e30)])
-@pytest.mark.parametrize("R,V", [(2, 20011), (40, 1003), (310, 5001)])
+@pytest.mark.parametrize("R,V", [(2, 20011), (40, 1003), (310, 5001), (306, 34001)])
 def test_logprobs_of_very_small_and_large_logits(M, dtype, size, temperature, R, V):
     x = (randn(95, R, V) * size).to(DT[dtype])
     x[:, 5::97] = float("-inf")
@@ -512,16 +513,18 @@ def test_logprobs_of_very_small_and_large_logits(M, dtype, size, temperature, R,
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-def test_logprobs_of_16_bits_without_a_distribution(M, dtype):
-    x = randn(97, 5, 20001).to(DT[dtype])
+@pytest.mark.parametrize("R,V", [(5, 20001), (310, 34001)])
+def test_logprobs_of_16_bits_without_a_distribution(M, dtype, R, V):
+    x = randn(97, R, V).to(DT[dtype])
     x[1] = float("-inf")
     x[2, 7] = float("nan")
     x[3, 8] = float("inf")
     x[4, 1:] = float("-inf")
-    tok = torch.zeros(5, dtype=torch.int32)
+    tok = torch.zeros(R, dtype=torch.int32)
     lp, ent, rank, ids, tlp = (g.cpu() for g in M.msk_token_logprobs(x.cuda(), tok.cuda(), top=4))
     for r in (1, 2, 3):
         assert torch.isnan(lp[r]) and torch.isnan(ent[r]) and torch.isnan(tlp[r]).all()
+        assert ((ids[r] >= 0) & (ids[r] < V)).all()
     assert torch.equal(rank.long(), (x > x[:, :1]).sum(-1))
     assert ids[3, 0] == 8
     assert lp[4] == 0 and ent[4] == 0 and ids[4].tolist() == [0, 1, 2, 3]
