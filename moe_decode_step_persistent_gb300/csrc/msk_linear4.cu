@@ -459,7 +459,8 @@ msk_status launch_linear(Lin4& a, const void* x, long long x_stride, cudaStream_
   const Setup* su = setup<NG>();
   if (su == nullptr) return MSK_ERR_CUDA;
   // Blocks along the columns: as many as x's room asks for, and more while
-  // all of a wave's clusters still run at once (two stages or more a block).
+  // all of a wave's clusters still run at once (two stages or more a block):
+  // 1 x 4096 x 4096 8.9 us, with one block a tile 13.0.
   const int room = (kSmem - 1024 - kPartBytes - kTeams * kStageBytes) / (kChunks * kXBytes<NG>);  // groups of a block
   const int tiles = (int)((a.N + kRows - 1) / kRows);
   a.ks = (a.groups + room - 1) / room;
@@ -472,6 +473,7 @@ msk_status launch_linear(Lin4& a, const void* x, long long x_stride, cudaStream_
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return MSK_ERR_CUDA;
   const int xbytes = per * kChunks * kXBytes<NG>, pbytes = a.ks > 1 ? kPartBytes : 0;
+  // (two slots a team where there is room: 8 x 65536 x 4096 36.5 us, with one 37.5)
   a.stages = (kSmem - 1024 - pbytes - xbytes) / kStageBytes >= kMaxStages ? kMaxStages : kTeams;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(std::min(tiles, su->active[a.ks]) * a.ks));
@@ -531,6 +533,7 @@ extern "C" msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_s
                                    CU_TENSOR_MAP_SWIZZLE_NONE)))
     return MSK_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // (up to 8 tokens x takes half the room: 8 x 65536 x 4096 36.5 us, with room for 16 38.2)
   return tokens <= 8 ? launch_linear<1>(a, x, x_stride, st) : launch_linear<2>(a, x, x_stride, st);
 }
 
