@@ -309,9 +309,13 @@ class Kv4Cache:
         _need(scales.shape == (2, self.n_kv_heads, self.max_seq, self.head_dim // 16) and scales.is_contiguous(),
               "scales: contiguous [2][n_kv_heads][max_seq][head_dim / 16]")
         _need(codes.is_cuda and codes.device == scales.device, "codes and scales live on one CUDA device")
-        self.codes, self.scales = codes, scales
+        # (fixed: the descriptor holds their addresses)
+        self._codes, self._scales = codes, scales
         self.desc = ctypes.pointer(Kv4Desc(codes.data_ptr(), scales.data_ptr(), self.n_kv_heads, self.head_dim,
                                            self.max_seq, k_scale, v_scale))
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
 
     @classmethod
     def empty(cls, n_kv_heads, max_seq, head_dim, k_scale=1.0, v_scale=1.0, device="cuda"):
@@ -333,9 +337,14 @@ class Fp4Weight:
         _need(scales.shape == (self.rows, self.cols // 16) and scales.is_contiguous(),
               "scales: contiguous [rows][cols / 16]")
         _need(packed.is_cuda and packed.device == scales.device, "packed and scales live on one CUDA device")
-        self.packed, self.scales, self.tensor_scale = packed, scales, float(tensor_scale)
-        self.desc = ctypes.pointer(Nvfp4Desc(packed.data_ptr(), scales.data_ptr(), self.tensor_scale, self.rows,
+        # (fixed: the descriptor holds their addresses)
+        self._packed, self._scales, self._tensor_scale = packed, scales, float(tensor_scale)
+        self.desc = ctypes.pointer(Nvfp4Desc(packed.data_ptr(), scales.data_ptr(), self._tensor_scale, self.rows,
                                              self.cols))
+
+    packed = property(lambda self: self._packed)
+    scales = property(lambda self: self._scales)
+    tensor_scale = property(lambda self: self._tensor_scale)
 
 
 def _step(t, axis):
@@ -378,7 +387,7 @@ def msk_kv4_write(cache, k, v, pos0, stream=None):
     CUDA int32 tensor read when the kernel runs."""
     dtype, T, ts, hs = _kv_rows(cache, k, v)
     host, dev = _position(pos0)
-    st = _enqueue(stream, k, v, cache.codes)
+    st = _enqueue(stream, k, v, cache._codes)
     _check(load_library().msk_kv4_write(cache.desc, k.data_ptr(), v.data_ptr(), dtype, T, ts, hs, host, dev, st),
            "msk_kv4_write")
 
@@ -393,7 +402,7 @@ def msk_kv4_read(cache, pos0, tokens, dtype=torch.bfloat16, out=None, stream=Non
     k, v = out
     dt, T, ts, hs = _kv_rows(cache, k, v)
     _need(T == tokens, "out does not hold `tokens` rows")
-    st = _enqueue(stream, k, v, cache.codes)
+    st = _enqueue(stream, k, v, cache._codes)
     _check(load_library().msk_kv4_read(cache.desc, int(pos0), tokens, k.data_ptr(), v.data_ptr(), dt, ts, hs, st),
            "msk_kv4_read")
     return k, v
@@ -425,7 +434,7 @@ def msk_attention_kv4(q, cache, cache_len, window=0, parents=None, softmax_scale
     host, dev = _position(cache_len)
     need = msk_attention_kv4_workspace(T, Hq, cache.n_kv_heads, d, window, host if dev is None else cache.max_seq - T)
     ws, addr, size = _workspace(workspace, need, stream)
-    st = _enqueue(stream, q, out, cache.codes) if ws is None else _enqueue(stream, q, out, cache.codes, ws)
+    st = _enqueue(stream, q, out, cache._codes) if ws is None else _enqueue(stream, q, out, cache._codes, ws)
     _check(load_library().msk_attention_kv4(q.data_ptr(), dtype, ts if T > 1 else 0, cache.desc, T, Hq, host, dev,
                                             None if parents is None else _positions(parents), int(window),
                                             softmax_scale, out.data_ptr(), addr, size, st), "msk_attention_kv4")
@@ -449,7 +458,7 @@ def msk_linear_fp4(x, weight, out_dtype=None, out=None, stream=None):
         _need(out.shape == (T, weight.rows) and (out.stride(1) == 1 or weight.rows <= 1),
               "out: [tokens][rows], contiguous rows")
         ys = _step(out, 0)
-    st = _enqueue(stream, x, out, weight.packed)
+    st = _enqueue(stream, x, out, weight._packed)
     _check(load_library().msk_linear_fp4(x.data_ptr(), xt, _step(x, 0), weight.desc, T, out.data_ptr(), yt, ys, st),
            "msk_linear_fp4")
     return out

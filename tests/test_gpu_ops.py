@@ -13,7 +13,8 @@ the output's type.
     out: h |o| + (2^-11 + score + 2^-16) sum p |v| + 2^-25 n max |v|.
   linear: fp32 sums of exact products: h |y| + (K + 64) 2^-23 sum |x w|.
   logprobs: fp32 differences and sums: lse off by 2^-21 (1 + max |x / T|) +
-    (V / 512 + 64) 2^-24 (serial partial sums of V / 512 or fewer terms)."""
+    (V / 512 + 64) 2^-24 (serial partial sums of V / 512 or fewer terms, up to
+    32768 logits of V / 256: no more than V / 512 + 64)."""
 
 import math
 
@@ -708,8 +709,12 @@ def test_binding_refuses(M):
         M.msk_kv4_write(cache, q[:, :2], q[:, :2], 61)
     with pytest.raises(M.MskError):
         M.msk_kv4_read(cache, 60, 5)
+    with pytest.raises(AttributeError):  # (the handle's tensors stay)
+        cache.codes = cache.codes.clone()
     packed, scales = random_fp4(113, 32, 256)
     w = M.Fp4Weight(packed.cuda(), scales.cuda())
+    with pytest.raises(AttributeError):
+        w.packed = w.packed.clone()
     x = randn(114, 17, 256).bfloat16().cuda()
     with pytest.raises(M.MskError):
         M.msk_linear_fp4(x, w)
