@@ -86,6 +86,8 @@ __device__ __forceinline__ RowsAt rows_at(const Kv4Rows& a, int pos0, int per) {
 template <int HD, int DT>
 __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4Rows a) {
   constexpr int NP = HD / 16;
+  grid_dep_wait();
+  grid_dep_launch();
   int pos0 = a.pos0;
   if (a.pos0_dev) pos0 = max(0, min(*a.pos0_dev, a.max_seq - a.tokens));
   const RowsAt w = rows_at<NP>(a, pos0, 256);
@@ -142,6 +144,8 @@ template <int HD, int DT>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4Rows a) {
   constexpr int E = DT == MSK_FP32 ? 4 : 8, NP = HD / E, U = kReadUnroll;
   using Codes = std::conditional_t<E == 4, uint16_t, uint32_t>;
+  grid_dep_wait();
+  grid_dep_launch();
   const RowsAt w = rows_at<NP>(a, a.pos0, 256 * U);
   const float ts = w.is_v ? a.v_scale : a.k_scale;
   uint32_t c[U], e[U];
@@ -179,10 +183,11 @@ void launch_rows(bool write, int32_t dt, const Kv4Rows& a, cudaStream_t st) {
   const int piece = write ? 16 : dt == MSK_FP32 ? 4 : 8, per = write ? 256 : 256 * kReadUnroll;
   const long long n = (long long)a.tokens * HD / piece;
   const dim3 grid((unsigned)((n + per - 1) / per), 2u * a.Hkv);
+  const OpsLaunch l(grid, 256, 0, st);
 #define MSK_ROWS(D)                                                    \
   do {                                                                 \
-    if (write) kv4_write_kernel<HD, D><<<grid, 256, 0, st>>>(a);       \
-    else kv4_read_kernel<HD, D><<<grid, 256, 0, st>>>(a);              \
+    if (write) cudaLaunchKernelEx(&l.cfg, kv4_write_kernel<HD, D>, a); \
+    else cudaLaunchKernelEx(&l.cfg, kv4_read_kernel<HD, D>, a);        \
   } while (0)
   if (dt == MSK_BF16) MSK_ROWS(MSK_BF16);
   else if (dt == MSK_FP16) MSK_ROWS(MSK_FP16);
@@ -409,6 +414,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int split = blockIdx.x, h = blockIdx.y, tile = blockIdx.z;
   if (a.cluster > 1) cluster_arrive();
+  grid_dep_wait();
   const int len = cached_len(a), rows = a.T * a.G;
 
   // this block's keys: in steps of 16 handed round the warps
@@ -801,6 +807,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, h = blockIdx.y, tile = blockIdx.z;
   if (a.cluster > 1) cluster_arrive();
+  grid_dep_wait();
   const int len = cached_len(a), rows = a.T * a.G;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
@@ -1157,6 +1164,7 @@ __global__ void __launch_bounds__(4 * HD, N > 8 ? 1 : 4) kv4_combine_kernel(cons
   const long long base = ((long long)(row / tile_rows) * a.Hkv + h) * a.splits * tile_rows + row % tile_rows;
   float mm = -INFINITY, l = 0.f, sum = 0.f;
   grid_dep_wait();
+  grid_dep_launch();
   for (int s0 = q; s0 < a.splits; s0 += 4 * N) {
     float o[N];
     float2 ml[N];
@@ -1243,16 +1251,8 @@ cudaError_t launch_blocks(void (*kernel)(Args), const Args& args, bool (&ready)[
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3((unsigned)(p.cluster * p.splits), (unsigned)Hkv, (unsigned)p.tiles);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)p.cluster, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args);
+  const OpsLaunch l(dim3((unsigned)(p.cluster * p.splits), (unsigned)Hkv, (unsigned)p.tiles), threads, smem, st, p.cluster);
+  return cudaLaunchKernelEx(&l.cfg, kernel, args);
 }
 
 template <int HD, int NT>
@@ -1285,19 +1285,12 @@ cudaError_t launch_attention(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st
                   : a.T * a.G <= kTcRows / 2  ? launch_tc_kernel<HD, 32>(a, p, st)
                                               : launch_tc_kernel<HD, 64>(a, p, st);
   if (e != cudaSuccess || p.splits == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3((unsigned)(a.T * a.G), (unsigned)a.Hkv);
-  cfg.blockDim = dim3(4 * HD);
-  cfg.stream = st;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at, cfg.numAttrs = 1;
+  const OpsLaunch l(dim3((unsigned)(a.T * a.G), (unsigned)a.Hkv), 4 * HD, 0, st);
   // many blocks: few registers, so that all run at once (16 tokens x 32 heads, 19
   // ranges: 25.7 us in all, with 16 at once a group 30.7; one token, 38 ranges: 35.4
   // and 35.1)
-  return a.T * a.Hq > kOpsSms ? cudaLaunchKernelEx(&cfg, kv4_combine_kernel<HD, 5>, a, p.tile_rows)
-                              : cudaLaunchKernelEx(&cfg, kv4_combine_kernel<HD, 16>, a, p.tile_rows);
+  return a.T * a.Hq > kOpsSms ? cudaLaunchKernelEx(&l.cfg, kv4_combine_kernel<HD, 5>, a, p.tile_rows)
+                              : cudaLaunchKernelEx(&l.cfg, kv4_combine_kernel<HD, 16>, a, p.tile_rows);
 }
 
 }  // namespace

@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
   const int ga = a.groups * rank / ks, gb = a.groups * (rank + 1) / ks, ng = gb - ga;  // (at most 128 groups)
   const int tiles = (int)((a.N + kRows - 1) / kRows);
   const int mine = cluster < tiles ? (tiles - cluster + clusters - 1) / clusters : 0;
-  const uint64_t deadline = gtimer() + kOpsWaitNs + (uint64_t)mine * ng * kOpsStepNs;
+  uint64_t deadline;
   // (dynamic shared memory starts at a multiple of 1024 in the shared window)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t ring = smem_u32(smem);
@@ -118,16 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
     return (bool)__all_sync(0xFFFFFFFFu, ok);
   };
 
-  // --- copies ---------------------------------------------------------------
-  const int total = mine * ng;  // stages in all
-  auto load = [&](int st, int ti, int g) {
-    const uint32_t dst = ring + st * kStageBytes, b = bar(bars.full[st]);
-    const int row = (cluster + ti * clusters) * kRows;
-    mbar_arrive_expect_tx(b, a.scales_tma ? kStageBytes : kCodeBytes);
-    tma_load_2d(dst, &a.codes_map, (ga + g) * (kGroup / 2), row, b);
-    if (a.scales_tma) tma_load_2d(dst + kCodeBytes, &a.scales_map, (ga + g) * (kGroup / 16), row, b);
-  };
-  if (warp == kDeqWarps && lane == 0) {  // under way before the block's set-up
+  if (warp == kDeqWarps && lane == 0) {
     prefetch_tensormap(&a.x_map);
     prefetch_tensormap(&a.codes_map);
     if (a.scales_tma) prefetch_tensormap(&a.scales_map);
@@ -135,17 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
     mbar_init(bar(bars.xfull), 1);
     mbar_fence_init();
     fence_proxy_async_shared();
-    // x first: behind the ring's copies it would wait for all of them
-    mbar_arrive_expect_tx(bar(bars.xfull), ng * kChunks * kXBytes<NG>);
-    for (int g = 0; g < ng; ++g)
-      asm volatile(
-          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-              smem_u32(xs) + g * kChunks * kXBytes<NG>),
-          "l"(&a.x_map), "r"(0), "r"(0), "r"((ga + g) * kChunks), "r"(bar(bars.xfull))
-          : "memory");
-    for (int i = 0; i < min(total, a.stages); ++i) load(i, i / ng, i % ng);
   }
-
   if (tid == 0) {
     abort = 0, never = 0;
     for (int t = 0; t < kTeams; ++t) {
@@ -160,6 +141,31 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
   }
   if (tid < 16) amaxs[tid] = 0;
   if (warp == 0) tmem_alloc(smem_u32(&tmem_base), 512);
+  grid_dep_wait();
+  grid_dep_launch();
+  deadline = gtimer() + kOpsWaitNs + (uint64_t)mine * ng * kOpsStepNs;
+
+  // --- copies ---------------------------------------------------------------
+  const int total = mine * ng;  // stages in all
+  auto load = [&](int st, int ti, int g) {
+    const uint32_t dst = ring + st * kStageBytes, b = bar(bars.full[st]);
+    const int row = (cluster + ti * clusters) * kRows;
+    mbar_arrive_expect_tx(b, a.scales_tma ? kStageBytes : kCodeBytes);
+    tma_load_2d(dst, &a.codes_map, (ga + g) * (kGroup / 2), row, b);
+    if (a.scales_tma) tma_load_2d(dst + kCodeBytes, &a.scales_map, (ga + g) * (kGroup / 16), row, b);
+  };
+  if (warp == kDeqWarps && lane == 0) {  // under way before the block has met
+    // x first: behind the ring's copies it would wait for all of them
+    mbar_arrive_expect_tx(bar(bars.xfull), ng * kChunks * kXBytes<NG>);
+    for (int g = 0; g < ng; ++g)
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+              smem_u32(xs) + g * kChunks * kXBytes<NG>),
+          "l"(&a.x_map), "r"(0), "r"(0), "r"((ga + g) * kChunks), "r"(bar(bars.xfull))
+          : "memory");
+    for (int i = 0; i < min(total, a.stages); ++i) load(i, i / ng, i % ng);
+  }
+
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -475,17 +481,9 @@ msk_status launch_linear(Lin4& a, const void* x, long long x_stride, cudaStream_
   const int xbytes = per * kChunks * kXBytes<NG>, pbytes = a.ks > 1 ? kPartBytes : 0;
   // (two slots a team where there is room: 8 x 65536 x 4096 36.5 us, with one 37.5)
   a.stages = (kSmem - 1024 - pbytes - xbytes) / kStageBytes >= kMaxStages ? kMaxStages : kTeams;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(std::min(tiles, su->active[a.ks]) * a.ks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 1024 + a.stages * kStageBytes + xbytes + pbytes;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)a.ks, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = a.ks > 1 ? cudaLaunchKernelEx(&cfg, linear4_kernel<NG, true>, a) : cudaLaunchKernelEx(&cfg, linear4_kernel<NG, false>, a);
+  const OpsLaunch l(dim3((unsigned)(std::min(tiles, su->active[a.ks]) * a.ks)), kThreads, 1024 + a.stages * kStageBytes + xbytes + pbytes, st,
+                    a.ks);
+  const cudaError_t e = a.ks > 1 ? cudaLaunchKernelEx(&l.cfg, linear4_kernel<NG, true>, a) : cudaLaunchKernelEx(&l.cfg, linear4_kernel<NG, false>, a);
   return e == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }
 

@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(kStreamThreads + 64, 2) logprobs_stream_kernel
   __shared__ int n_hits[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float c = a.inv_t * 1.4426950408889634f, reach = clamp_reach(c);
+  grid_dep_wait();  // (the next kernel does not start early: its blocks would share the rows out unevenly)
   if (warp < NW) {
     int place = 0;
     int tok = row_token(a, blockIdx.x);
@@ -620,6 +621,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
   const int S = gridDim.x, part = blockIdx.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float c = a.inv_t * 1.4426950408889634f;
+  grid_dep_wait();
+  grid_dep_launch();
   const int tok = row_token(a, row);
   const float xg = row_logit<DT>(a, row, tok);
   const Row<DT> x(a, row, S, part);
@@ -741,20 +744,12 @@ cudaError_t launch_logprobs(const LogProbs& a, int nsm, cudaStream_t st) {
   // 14.5 us, the warps that read on 24.1; 2048 x 32768 33.3 and 38.6; 400 x 50021
   // 17.0 and 14.2; 400 x 20000 fp32 13.9 and 11.8).
   if (S == 1 && a.V * (DT == MSK_FP32 ? 4 : 2) > 65536) {
-    logprobs_stream_kernel<DT><<<(unsigned)std::min<long long>(a.rows, 2 * nsm), kStreamThreads + 64, 0, st>>>(a);
-    return cudaGetLastError();
+    const OpsLaunch l(dim3((unsigned)std::min<long long>(a.rows, 2 * nsm)), kStreamThreads + 64, 0, st);
+    return cudaLaunchKernelEx(&l.cfg, logprobs_stream_kernel<DT>, a);
   }
-  cudaLaunchConfig_t cfg = {};
   const unsigned gy = (unsigned)std::min<long long>(a.rows, 65535);
-  cfg.gridDim = dim3((unsigned)S, gy, (unsigned)((a.rows + gy - 1) / gy));
-  cfg.blockDim = dim3(S == 1 ? 128 : 512);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)S, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return S == 1 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, 128>, a) : cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, 512>, a);
+  const OpsLaunch l(dim3((unsigned)S, gy, (unsigned)((a.rows + gy - 1) / gy)), S == 1 ? 128 : 512, 0, st, S);
+  return S == 1 ? cudaLaunchKernelEx(&l.cfg, logprobs_kernel<DT, 128>, a) : cudaLaunchKernelEx(&l.cfg, logprobs_kernel<DT, 512>, a);
 }
 
 }  // namespace

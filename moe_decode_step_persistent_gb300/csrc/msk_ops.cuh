@@ -35,6 +35,22 @@ constexpr uint64_t kOpsWaitNs = 200ull * 1000 * 1000;
 // ... and more for each step of a block's work, many times what it takes.
 constexpr uint64_t kOpsStepNs = 20ull * 1000;
 
+// The launches' attributes: a cluster, and that the kernel may start before the
+// one in front of it has ended: it sets itself up, and touches global memory
+// only behind grid_dep_wait().
+struct OpsLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  OpsLaunch(dim3 grid, int threads, int smem, cudaStream_t st, int cluster = 1) {
+    cfg.gridDim = grid, cfg.blockDim = dim3((unsigned)threads), cfg.dynamicSmemBytes = (size_t)smem, cfg.stream = st;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster, at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at, cfg.numAttrs = 2;
+  }
+};
+
 // The SM count the workspace sizes are made for when there is no device to
 // ask; kernels never use more blocks than a workspace has room for.
 constexpr int kOpsSms = 152;

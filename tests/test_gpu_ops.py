@@ -668,6 +668,60 @@ def test_captured_without_a_call_before(M):
     assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_back_to_back(M, captured):
+    """Kernels that start before the one in front of them has ended read and
+    write as if they did not: the same buffers over and over, torch's kernels in
+    between, against the same calls one at a time."""
+    T, hq, hkv, d, N, V = 16, 8, 2, 64, 256, 9001
+    packed, scales = (t.cuda() for t in random_fp4(131, N, hq * d))
+    w = M.Fp4Weight(packed, scales, 0.03)
+    packed, scales = (t.cuda() for t in random_fp4(132, V, N))
+    head = M.Fp4Weight(packed, scales, 0.05)
+    kv = randn(133, 6, T, hkv, d).bfloat16().cuda()
+    tok = torch.randint(0, V, (T,), generator=gen(134), dtype=torch.int32).cuda()
+
+    def chain(after):
+        cache, q = filled_cache(M, 135, hkv, 9500, d), randn(136, T, hq, d).bfloat16().cuda()
+        o, h = torch.zeros(T, hq * d, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+        logits = torch.zeros(T, V, device="cuda")
+        start = q.clone()
+
+        def run():
+            got = []
+            q.copy_(start), o.zero_(), h.zero_(), after()  # (a second run starts as the first one)
+            for i in range(18):
+                length = (40, 700, 9300)[i % 3]
+                M.msk_kv4_write(cache, kv[i % 6], kv[(i + 1) % 6], length), after()
+                M.msk_attention_kv4(q[:1 + 5 * (i % 4)], cache, length, out=o[:1 + 5 * (i % 4)]), after()
+                M.msk_linear_fp4(o, w, out=h), after()
+                if i % 2:
+                    h.add_(1), after()
+                M.msk_linear_fp4(h, head, out=logits), after()
+                got += [t for t in M.msk_token_logprobs(logits, tok, top=3)]
+                after()
+                logits.fill_(float("nan")), after()
+                q.copy_(o.view(T, hq, d)), after()
+            got += [o.clone(), h.clone()]
+            return got
+        return run
+
+    want = chain(torch.cuda.synchronize)()
+    run = chain(lambda: None)
+    if captured:
+        run()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = run()
+        g.replay(), g.replay()
+    else:
+        got = run()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
+    M.msk_ops_check()
+
+
 def test_two_calls_at_once(M):
     """Calls on two streams, each with its own workspace, do not disturb each
     other."""
