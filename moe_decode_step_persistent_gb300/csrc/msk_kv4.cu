@@ -396,7 +396,7 @@ __device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, floa
 // reach 256 (of fp16's 65504), and the sums are rescaled a few times in all.
 //
 // A warp's keys come through a ring of kRing steps of its own, by asynchronous
-// copies; warps meet only at the end.  One token, 131071 keys of 8 kv heads: 34.6
+// copies; warps meet only at the end.  One token, 131071 keys of 8 kv heads: 34.3
 // us (4.4 TB/s, 64% of what a copy reaches).  Bound by the decoding (a conversion
 // and a multiply for two elements; the ALU 56%, issue slots 59% in use) beside
 // DRAM.  Q in shared memory for three blocks an SM instead of two: 43 us.
@@ -785,7 +785,7 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N]) {
 // each team issues its MMAs and copies.  The reference of a row is raised when a
 // score passes it by 2^8, and the sums rescaled: a few times in all.  On mma.sync
 // 64 rows cost four times the decoding or do not fit the registers: 53 us for
-// 16 tokens over 32768 keys of 8 kv heads, here 25.7 (131072 keys: 68.4).  Bound
+// 16 tokens over 32768 keys of 8 kv heads, here 25.2 (131072 keys: 68.0).  Bound
 // by the chain of a step (decoding, scores, softmax, weights, each through
 // tensor memory; 2.1 us) with two teams: issue slots 49%, tensor pipe 22% in
 // use.  A third team has no room in tensor memory and registers.

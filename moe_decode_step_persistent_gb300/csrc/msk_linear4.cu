@@ -77,7 +77,7 @@ struct Bars {  // mbarriers of a block
 // an mbarrier; a team's sums lie in an accumulator of their own and are added
 // in the epilogue, which reads tile i while tile i + 1 is decoded.
 //
-// 131072 x 4096: 61 us for 16 tokens, 59 for one (5.1 TB/s, 75% of what a copy
+// 131072 x 4096: 60 us for 16 tokens, 58 for one (5.1 TB/s, 76% of what a copy
 // reaches).  Bound by the decoding and DRAM alike: issue slots are 64% in use,
 // the ALU that converts 55%.  On mma.sync the decoding and the MMAs together
 // take longer than the bytes (88 us for 16 tokens).
@@ -466,7 +466,7 @@ msk_status launch_linear(Lin4& a, const void* x, long long x_stride, cudaStream_
   if (su == nullptr) return MSK_ERR_CUDA;
   // Blocks along the columns: as many as x's room asks for, and more while
   // all of a wave's clusters still run at once (two stages or more a block):
-  // 1 x 4096 x 4096 8.9 us, with one block a tile 13.0.
+  // 1 x 4096 x 4096 8.9 us, with one block a tile 13.0 (both before early starts).
   const int room = (kSmem - 1024 - kPartBytes - kTeams * kStageBytes) / (kChunks * kXBytes<NG>);  // groups of a block
   const int tiles = (int)((a.N + kRows - 1) / kRows);
   a.ks = (a.groups + room - 1) / room;

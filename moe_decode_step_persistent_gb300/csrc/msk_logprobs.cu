@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kStreamThreads + 64, 2) logprobs_stream_kernel
   __shared__ int n_hits[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float c = a.inv_t * 1.4426950408889634f, reach = clamp_reach(c);
-  grid_dep_wait();  // (the next kernel does not start early: its blocks would share the rows out unevenly)
+  grid_dep_wait();  // (and the next kernel does not start early: its blocks would come to lie unevenly, 65 us for 56)
   if (warp < NW) {
     int place = 0;
     int tok = row_token(a, blockIdx.x);

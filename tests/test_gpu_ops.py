@@ -668,6 +668,41 @@ def test_captured_without_a_call_before(M):
     assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
 
 
+def test_around_a_step(M):
+    """A verify step, its layers' bf16 caches turned into 4-bit ones and attended
+    to, the step's hidden state through the head, the drafted tokens' log
+    probabilities: enqueued without a wait in between."""
+    import msk_synth as S
+    from tests._gpu import Setup
+    wl = S.scaled(S.WORKLOADS["tiny"], tokens=16, cached=300, windows=(8, 0))
+    st = Setup(wl, gamma_std=0.1)
+    kv, h = st.fresh_kv(), st.hidden()
+    hkv, d, T = wl.n_kv_heads, wl.head_dim, wl.tokens
+    q = randn(141, T, wl.n_q_heads, d).bfloat16().cuda()
+    packed, scales = (t.cuda() for t in random_fp4(142, 777, wl.hidden))
+    w = M.Fp4Weight(packed, scales, 0.02)
+    tok = torch.randint(0, 777, (T,), generator=gen(143), dtype=torch.int32).cuda()
+    st.model.decode_step(h, kv, [wl.cached + t for t in range(T)])
+    outs = []
+    for layer in range(wl.n_layers):
+        cache = M.Kv4Cache.empty(hkv, wl.max_seq, d)
+        k, v = (kv[layer, i].transpose(0, 1)[:wl.cached + T] for i in (0, 1))
+        M.msk_kv4_write(cache, k, v, 0)
+        outs.append((cache, M.msk_attention_kv4(q, cache, wl.cached, window=wl.windows[layer])))
+    logits = M.msk_linear_fp4(h, w, out_dtype=torch.float32)
+    got = M.msk_token_logprobs(logits, tok, top=5)
+    for layer, (cache, out) in enumerate(outs):
+        for i in (0, 1):
+            c, e, _ = F.q4(kv[layer, i, :, :wl.cached + T].cpu().double().numpy())
+            assert np.array_equal(cache.codes[i, :, :wl.cached + T].cpu().numpy(), pack(c).numpy())
+            assert np.array_equal(cache.scales[i, :, :wl.cached + T].cpu().numpy(), e)
+        check_attention(M, out, q, cache, wl.cached, wl.windows[layer], None)
+    check_linear(logits, h, packed, scales, 0.02)
+    check_logprobs(got, logits, tok, 5, 1.0)
+    M.msk_ops_check()
+    st.model.close()
+
+
 @pytest.mark.parametrize("captured", [False, True])
 def test_back_to_back(M, captured):
     """Kernels that start before the one in front of them has ended read and
