@@ -668,6 +668,42 @@ def test_captured_without_a_call_before(M):
     assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_behind_an_event_of_another_stream(M, captured):
+    """A call waits for what its stream waits for, whatever ran before it."""
+    packed, scales = (t.cuda() for t in random_fp4(151, 512, 256))
+    w = M.Fp4Weight(packed, scales)
+    src = randn(152, 8, 16, 256).bfloat16().cuda()
+    big = torch.zeros(1 << 26, device="cuda")
+    x, side = torch.zeros(16, 256, dtype=torch.bfloat16, device="cuda"), torch.cuda.Stream()
+    y = torch.zeros(8, 16, 512, dtype=torch.bfloat16, device="cuda")
+    want = torch.stack([M.msk_linear_fp4(t, w) for t in src])
+    torch.cuda.synchronize()
+
+    def run():
+        for i in range(8):
+            M.msk_linear_fp4(x, w, out=y[i])  # (the kernel in front, of the same kind)
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                big.add_(1.0)  # tens of microseconds, then the input
+                x.copy_(src[i])
+            torch.cuda.current_stream().wait_stream(side)
+            M.msk_linear_fp4(x, w, out=y[i])
+
+    if captured:
+        run()
+        torch.cuda.synchronize()
+        y.zero_()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        g.replay()
+    else:
+        run()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
 def test_around_a_step(M):
     """A verify step, its layers' bf16 caches turned into 4-bit ones and attended
     to, the step's hidden state through the head, the drafted tokens' log
