@@ -386,9 +386,9 @@ msk_status msk_kv4_read(const msk_kv4_desc* cache, int32_t pos0, int32_t tokens,
  *   softmax_scale: factor of the scores, 0 for 1 / sqrt(head_dim).
  * n_q_heads a multiple of cache->n_kv_heads, any quotient.  Cache rows that no
  * query sees are not read, or do not count whatever they hold.
- * Queries and softmax weights enter the products in fp16 (queries after an
- * exact scaling of each row by a power of two), keys and values without
- * rounding, sums are fp32.
+ * Queries enter the products in fp16 (after a scaling of each row by a power
+ * of two), softmax weights as two fp16 numbers (22 bits, below that 2^-32 of
+ * a row's greatest), keys and values without rounding; sums are fp32.
  * workspace: at least msk_attention_kv4_workspace bytes (0 for few keys, when
  * it may be NULL), 16-byte aligned; for a call with cache_len_dev the bytes for
  * max_seq - tokens. */

@@ -317,6 +317,24 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
   return v;
 }
 
+// A softmax's reference lies kBelow powers of two under the greatest score that it
+// was set from, and is raised when a weight would pass 2^kMost: weights reach 2^15 of
+// fp16's 65504, and the sums are rescaled a few times in all.
+constexpr float kBelow = 7.f, kMost = 15.f;
+
+// Two weights for an fp16 operand, and what their rounding left out for a second
+// one: together 22 bits, and off by at most 2^-25 where that is more, 2^-32 of the
+// greatest weight.  (In one operand of 11 bits the weights differ from those in the
+// fp32 sum of weights by up to 2^-12, and all below 2^-25 are lost.)
+struct Split {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Split split_f16x2(float x, float y) {
+  const uint32_t hi = pack_f16x2(x, y);
+  const float2 f = unpack_f16x2(hi);
+  return {hi, pack_f16x2(x - f.x, y - f.y)};
+}
+
 // Four elements of an output row.
 __device__ __forceinline__ void store_out4(const Kv4Attn& a, int hd, int h, int row, int d, float4 y) {
   uint16_t* p = a.out + ((long long)(row / a.G) * a.Hq + h * a.G + row % a.G) * hd + d;
@@ -328,7 +346,8 @@ __device__ __forceinline__ void store_out4(const Kv4Attn& a, int hd, int h, int 
 // straight to the output; or to the block of the cluster that joins the row, rank
 // r mod cluster: all blocks push into `recv` there, so that one barrier lies
 // between the sums and the output and nothing remote is read.  (The cluster's
-// first barrier, entered at the block's start, says that all blocks are there.)
+// first barrier, which the block has entered before, says that all blocks are there
+// and that their `recv` is free.)
 constexpr int recv_bytes(int rows, int hd) { return (rows + kMaxCluster - 1) * (hd + 4) * 4; }
 template <int HD, int ROWS, int THREADS>
 __device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, float* recv, int split, int h, int tile) {
@@ -392,12 +411,10 @@ __device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, floa
 // second half), so that the lanes' values lie next to each other.  Elements
 // are exact in fp16 (at most 6 significant bits, at most 2688).
 //
-// The softmax's reference is raised only when a score passes it by 2^8: weights
-// reach 256 (of fp16's 65504), and the sums are rescaled a few times in all.
-//
 // A warp's keys come through a ring of kRing steps of its own, by asynchronous
-// copies; warps meet only at the end.  One token, 131071 keys of 8 kv heads: 34.3
-// us (4.4 TB/s, 64% of what a copy reaches).  Bound by the decoding (a conversion
+// copies; warps meet only at the end.  One token, 131071 keys of 8 kv heads: 36.0
+// us (4.2 TB/s, 62% of what a copy reaches; with weights of one part 34.3).  Bound by
+// the decoding (a conversion
 // and a multiply for two elements; the ALU 56%, issue slots 59% in use) beside
 // DRAM.  Q in shared memory for three blocks an SM instead of two: 43 us.
 template <int HD, int NT>
@@ -581,7 +598,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
       for (int i = 0; i < 4; ++i) {
         y[nt][i] = fmaf(sc[nt][i], fac[nt][i & 1], nm[nt][i & 1]);
         if (hidden[nt][i]) y[nt][i] = -INFINITY;
-        raise |= y[nt][i] > 8.f;
+        raise |= y[nt][i] > kMost;
       }
     if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
@@ -593,25 +610,27 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
           float mx = fmaxf(x0, x1);
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
-          mx = fmaxf(-nm[nt][i], mx);
-          const float al = mx == -INFINITY ? 1.f : ex2(-nm[nt][i] - mx);
-          nm[nt][i] = -mx;
+          const float ref = fmaxf(-nm[nt][i], mx - kBelow), al = ref == -INFINITY ? 1.f : ex2(-nm[nt][i] - ref);
+          nm[nt][i] = -ref;
           l[nt][i] *= al;
 #pragma unroll
           for (int k = 0; k < MT; ++k) o[k][nt][i] *= al, o[k][nt][i + 2] *= al;
-          y[nt][i] = hidden[nt][i] ? -INFINITY : x0 - mx;
-          y[nt][i + 2] = hidden[nt][i + 2] ? -INFINITY : x1 - mx;
+          y[nt][i] = hidden[nt][i] ? -INFINITY : x0 - ref;
+          y[nt][i + 2] = hidden[nt][i + 2] ? -INFINITY : x1 - ref;
         }
     }
-    uint32_t pb[NT][2];
+    uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float p[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[i] = ex2(y[nt][i]);
       l[nt][0] += p[0] + p[2], l[nt][1] += p[1] + p[3];
-      pb[nt][0] = movmatrix_trans(pack_f16x2(p[0], p[1]));
-      pb[nt][1] = movmatrix_trans(pack_f16x2(p[2], p[3]));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const Split w = split_f16x2(p[2 * i], p[2 * i + 1]);
+        ph[nt][i] = movmatrix_trans(w.hi), pl[nt][i] = movmatrix_trans(w.lo);
+      }
     }
     const uint32_t v0 = e4m3x2_to_f16x2(__byte_perm(ve[0], ve[1], 0x0040)), v1 = e4m3x2_to_f16x2(__byte_perm(ve[2], ve[3], 0x0040));
 #pragma unroll
@@ -624,7 +643,10 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) kv4_rows_kernel(const __
         const uint32_t af[4] = {hmul2(e2m1_byte_to_f16x2(a0, k), v0), hmul2(e2m1_byte_to_f16x2(a1, k), v0),
                                 hmul2(e2m1_byte_to_f16x2(b0, k), v1), hmul2(e2m1_byte_to_f16x2(b1, k), v1)};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(o[w * 4 + k][nt], af, pb[nt][0], pb[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(o[w * 4 + k][nt], af, ph[nt][0], ph[nt][1]);
+          mma_f16(o[w * 4 + k][nt], af, pl[nt][0], pl[nt][1]);
+        }
       }
     }
   }
@@ -685,12 +707,14 @@ template <int HD>
 struct Tc {
   static constexpr int CODES = kTcKeys * HD / 2;                // bytes of a step's keys (or values)
   static constexpr int Q = kTcRows * HD * 2, V = kTcKeys * HD * 2, P = kTcKeys * kTcRows * 2;
-  static constexpr int TEAM = V + P + kTcSlots * 2 * CODES;     // a team's shared memory
-  static constexpr int SMEM = 1024 + Q + kTcTeams * TEAM + recv_bytes(kTcRows, HD);
-  // tensor memory columns: decoded keys, scores, output sums
+  static constexpr int TEAM = V + 2 * P + kTcSlots * 2 * CODES;  // a team's shared memory (P: the weights' two parts)
+  static constexpr int SMEM = 1024 + Q + kTcTeams * TEAM;
+  // tensor memory columns: decoded keys, scores, output sums of the weights' two parts
   static constexpr int A0 = 0, S0 = kTcTeams * HD / 2, O0 = S0 + kTcTeams * kTcRows, COLS = 512;
-  static_assert(O0 + kTcTeams * kTcRows <= COLS);
-  static_assert(kTcRows * (HD + 4) * 4 <= V + P);  // the block's sums at the end
+  static_assert(O0 + kTcTeams * 2 * kTcRows <= COLS);
+  // at the end the first team's place takes the block's sums, the second one's those
+  // that the cluster's blocks push
+  static_assert(kTcRows * (HD + 4) * 4 <= TEAM && recv_bytes(kTcRows, HD) <= TEAM && kTcTeams == 2);
 };
 
 struct TcBars {
@@ -720,6 +744,10 @@ __device__ __forceinline__ bool half_any(int id, bool v) {
       : "r"((uint32_t)v), "r"(id)
       : "memory");
   return r != 0;
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // Row of 16-byte pieces with the 128-byte swizzle.
@@ -785,10 +813,14 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N]) {
 // each team issues its MMAs and copies.  The reference of a row is raised when a
 // score passes it by 2^8, and the sums rescaled: a few times in all.  On mma.sync
 // 64 rows cost four times the decoding or do not fit the registers: 53 us for
-// 16 tokens over 32768 keys of 8 kv heads, here 25.2 (131072 keys: 68.0).  Bound
+// 16 tokens over 32768 keys of 8 kv heads, here 28.0 (131072 keys: 77.3).  Bound
 // by the chain of a step (decoding, scores, softmax, weights, each through
 // tensor memory; 2.1 us) with two teams: issue slots 49%, tensor pipe 22% in
 // use.  A third team has no room in tensor memory and registers.
+//
+// The weights' two parts (see Split) lie side by side as the N of one MMA, columns r
+// and NR + r of the sums, which are added at the end (one MMA after the other, V read
+// twice: 30.0 us for 28.0).  The second part costs 2.8 us of the 28.0.
 //
 // NR: rows of the 64 that are in use, 32 or 64 (the softmax skips the rest: 32
 // rows, 32768 keys 22.0 us, as 64 24.9).
@@ -806,7 +838,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   const Kv4Attn& a = args.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, h = blockIdx.y, tile = blockIdx.z;
-  if (a.cluster > 1) cluster_arrive();
   grid_dep_wait();
   const int len = cached_len(a), rows = a.T * a.G;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -831,7 +862,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   const int team = warp < kTcWorkers ? warp >> 3 : warp - kTcWorkers;
   const int mine = max(0, (s1 - s0 - team + kTcTeams - 1) / kTcTeams);  // this team's steps
   uint8_t* tsm = smem + L::Q + team * L::TEAM;
-  const uint32_t vbuf = smem_u32(tsm), pbuf = vbuf + L::V, raw = pbuf + L::P;
+  const uint32_t vbuf = smem_u32(tsm), pbuf = vbuf + L::V, raw = pbuf + 2 * L::P;
   auto load = [&](int it) {  // a step's keys and values
     const int slot = it % kTcSlots, j0 = lo + (s0 + team + it * kTcTeams) * kTcKeys;
     const uint32_t b = bar(bars.full[team][slot]), dst = raw + slot * 2 * L::CODES;
@@ -926,10 +957,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
       }
       *reinterpret_cast<uint4*>(smem + (piece >> 3) * (kTcRows * 128) + swz(r, piece & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // columns of P that the softmax never writes
-    if (NR < kTcRows)
-      for (int e = tid & 255; e < kTcKeys * 4; e += 256)
-        *reinterpret_cast<uint4*>(tsm + L::V + swz(e >> 2, 4 + (e & 3))) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_shared();
   }
   __syncthreads();
@@ -938,7 +965,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
     constexpr int RW = NR / 2, CP = PIECES / 2;  // query rows, pieces of codes of a thread
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t tk = tl + L::A0 + team * HD / 2 + half * HD / 4, ts = tl + L::S0 + team * kTcRows + half * RW;
-    const uint32_t to = tl + L::O0 + team * kTcRows + half * RW;
+    const uint32_t to = tl + L::O0 + team * 2 * kTcRows + half * RW;
     const int id = 1 + 2 * team + half;  // the barrier of the four warps with the same rows
     // this thread's rows; its team's references lie 3 arrays on, their factors 2 more
     float* hq = query.fac + half * RW;
@@ -974,9 +1001,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
 #pragma unroll
       for (int q = 0; q < 4 * CP; ++q) {  // 8 dimensions
         const int piece = half * 4 * CP + q;
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(vbuf + (piece >> 3) * (kTcKeys * 128) + swz(r, piece & 7)),
-                     "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
-                     : "memory");
+        sts128(vbuf + (piece >> 3) * (kTcKeys * 128) + swz(r, piece & 7),
+               make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars.empty[team][slot]));
@@ -1016,7 +1042,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
         float most = -INFINITY;
 #pragma unroll
         for (int i = 0; i < RW; ++i) most = fmaxf(most, y[i]);
-        raise = half_any(id, most > 8.f);
+        raise = half_any(id, most > kMost);
       }
       if (raise) {
         // raise the references: the rows' maxima over the step's keys, lane i
@@ -1031,20 +1057,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
         if (r < RW) {
           const int row = half * RW + r;
           const float old = -hnm[r];
-          float mx = fmaxf(fmaxf(wmax[team][0][row], wmax[team][1][row]), fmaxf(wmax[team][2][row], wmax[team][3][row]));
-          mx = tile * kTcRows + row < rows ? fmaxf(old, mx) : old;
-          hal[r] = mx == -INFINITY ? 1.f : ex2(old - mx);
-          hnm[r] = -mx;
+          const float mx =
+              fmaxf(fmaxf(wmax[team][0][row], wmax[team][1][row]), fmaxf(wmax[team][2][row], wmax[team][3][row]));
+          const float ref = tile * kTcRows + row < rows ? fmaxf(old, mx - kBelow) : old;
+          hal[r] = ref == -INFINITY ? 1.f : ex2(old - ref);
+          hnm[r] = -ref;
         }
         named_bar(id, 128);
         if (it > 0) {  // (the last step's output sums are complete: pvdone was waited for)
 #pragma unroll
           for (int i = 0; i < RW; ++i) l[i] *= hal[i];
-          tmem_ld<RW>(to, y);
-          uint32_t w[RW];
+#pragma unroll 1
+          for (int p = 0; p < RW / 8; ++p) {  // 16 rows of each part at a time
+            const int row = p % (RW / 16) * 16;
+            const uint32_t at = to + p / (RW / 16) * NR + row;
+            float z[16];
+            uint32_t w[16];
+            tmem_ld16(at, z);
 #pragma unroll
-          for (int i = 0; i < RW; ++i) w[i] = __float_as_uint(y[i] * hal[i]);
-          tmem_st<RW>(to, w);
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(z[i] * hal[row + i]);
+            tmem_st16(at, w);
+          }
         }
         // (a row still without a reference sees none of these keys; the maxima
         // and factors are written again after another barrier of these warps)
@@ -1056,11 +1089,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
         l[i] += y[i];
       }
 #pragma unroll
-      for (int i = 0; i < RW / 8; ++i)
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(pbuf + swz(r, half * (RW / 8) + i)),
-                     "r"(pack_f16x2(y[8 * i], y[8 * i + 1])), "r"(pack_f16x2(y[8 * i + 2], y[8 * i + 3])),
-                     "r"(pack_f16x2(y[8 * i + 4], y[8 * i + 5])), "r"(pack_f16x2(y[8 * i + 6], y[8 * i + 7]))
-                     : "memory");
+      for (int i = 0; i < RW / 8; ++i) {
+        Split w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = split_f16x2(y[8 * i + 2 * j], y[8 * i + 2 * j + 1]);
+        const uint32_t piece = half * (RW / 8) + i;
+        sts128(pbuf + swz(r, piece), make_uint4(w[0].hi, w[1].hi, w[2].hi, w[3].hi));
+        sts128(NR == kTcRows ? pbuf + L::P + swz(r, piece) : pbuf + swz(r, 4 + piece), make_uint4(w[0].lo, w[1].lo, w[2].lo, w[3].lo));
+      }
       fence_proxy_async_shared();
       tc_fence_before();
       __syncwarp();
@@ -1074,12 +1110,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   } else if (issuer) {
     // --- a team's MMAs and copies -------------------------------------------
     constexpr uint32_t idesc_s = (1u << 4) | ((kTcRows / 8u) << 17) | ((128u / 16) << 24);
-    constexpr uint32_t idesc_o = idesc_s | (1u << 15) | (1u << 16);  // A and B with M and N contiguous
-    const uint32_t tk = tmem + L::A0 + team * HD / 2, ts = tmem + L::S0 + team * kTcRows, to = tmem + L::O0 + team * kTcRows;
+    // A and B with M and N contiguous, N = the weights' two parts
+    constexpr uint32_t idesc_o = (1u << 4) | (2 * NR / 8u << 17) | ((128u / 16) << 24) | (1u << 15) | (1u << 16);
+    const uint32_t tk = tmem + L::A0 + team * HD / 2, ts = tmem + L::S0 + team * kTcRows, to = tmem + L::O0 + team * 2 * kTcRows;
     const uint64_t qd = umma_desc(smem_u32(smem), 16, 1024) | kSwizzle128;
     // V: blocks of 64 dimensions 16 KB apart (64 dimensions in all: the second one is the first again)
     const uint64_t vd = umma_desc(vbuf, HD == 128 ? kTcKeys * 128 : 0, 1024) | kSwizzle128;
-    const uint64_t pd = umma_desc(pbuf, 0, 1024) | kSwizzle128;
+    const uint64_t pd = umma_desc(pbuf, L::P, 1024) | kSwizzle128;  // (64 columns, then the next 64)
     bool ok = true;
     for (int it = 0; it < mine; ++it) {
       ok = wait(bars.kready[team], it & 1);
@@ -1114,6 +1151,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   grid_dep_launch();
   __syncwarp();
   __syncthreads();
+  if (a.cluster > 1) cluster_arrive();  // (the operands' places are free)
   tc_fence_after();
 
   // the teams joined: smem[row][PITCH] (over the first team's operands)
@@ -1132,14 +1170,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
   if (warp < 4 * (NR / 16)) {  // 16 rows a warp
     const int quad = warp & 3, d = quad * 32 + lane, q = (warp >> 2) * 16;
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-    float z0[16], z1[16];
+    float z[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z0[i] = z1[i] = 0.f;
-    if (one) tmem_ld16(tl + L::O0 + q, z0);
-    if (two) tmem_ld16(tl + L::O0 + kTcRows + q, z1);
+    for (int i = 0; i < 16; ++i) z[i] = 0.f;
+#pragma unroll
+    for (int t = 0; t < kTcTeams; ++t)
+      if (t == 0 ? one : two) {
+        const uint32_t at = tl + L::O0 + t * 2 * kTcRows + q;
+        float y[16];
+        tmem_ld16(at, y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] += jf[t][q + i] * y[i];
+        tmem_ld16(at + NR, y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] += jf[t][q + i] * y[i];
+      }
     if (HD == 128 || d < HD) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) out[(q + i) * PITCH + d] = jf[0][q + i] * z0[i] + jf[1][q + i] * z1[i];
+      for (int i = 0; i < 16; ++i) out[(q + i) * PITCH + d] = z[i];
     }
   }
   tc_fence_before();
@@ -1150,7 +1198,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_cons
     tmem_dealloc(tmem, L::COLS);
   }
   if (tid == 0 && abort) atomicExch(&g_error, 1u);
-  finish_block<HD, kTcRows, kTcThreads>(a, out, reinterpret_cast<float*>(smem + L::Q + kTcTeams * L::TEAM), split, h, tile);
+  finish_block<HD, kTcRows, kTcThreads>(a, out, reinterpret_cast<float*>(smem + L::Q + L::TEAM), split, h, tile);
 }
 
 // The key ranges of a (token, query head): a block of four groups of HD
