@@ -386,9 +386,10 @@ msk_status msk_kv4_read(const msk_kv4_desc* cache, int32_t pos0, int32_t tokens,
  *   softmax_scale: factor of the scores, 0 for 1 / sqrt(head_dim).
  * n_q_heads a multiple of cache->n_kv_heads, any quotient.  Cache rows that no
  * query sees are not read, or do not count whatever they hold.
- * Queries enter the products in fp16 (after a scaling of each row by a power
- * of two), softmax weights as two fp16 numbers (22 bits, below that 2^-32 of
- * a row's greatest), keys and values without rounding; sums are fp32.
+ * Queries enter the products in fp16 after a scaling of each row by a power of
+ * two (elements above 2^-31 of the row's greatest without rounding, smaller ones
+ * off by at most 2^-39 of it), softmax weights as two fp16 numbers (22 bits, below
+ * that 2^-32 of a row's greatest), keys and values without rounding; sums are fp32.
  * workspace: at least msk_attention_kv4_workspace bytes (0 for few keys, when
  * it may be NULL), 16-byte aligned; for a call with cache_len_dev the bytes for
  * max_seq - tokens. */
@@ -408,8 +409,10 @@ msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_stride, con
  *      16-byte aligned, read where they are (no repacking);
  *   y: [tokens][rows] of y_dtype (bf16, fp16 or fp32), y_stride elements
  *      between rows, aligned to its element.
- * Weights enter without rounding (the products e2m1 * e4m3), x in fp16 after an
- * exact scaling by powers of two, sums are fp32.  A NaN block scale makes the
+ * Weights enter without rounding (the products e2m1 * e4m3), x in fp16 after a
+ * scaling of each row by a power of two (elements above 2^-31 of the row's
+ * greatest without rounding, smaller ones off by at most 2^-39 of it), sums are
+ * fp32.  A NaN block scale makes the
  * outputs of its row NaN.  tokens == 0 or rows == 0 does nothing. */
 msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_stride, const msk_nvfp4_desc* w, int32_t tokens,
                           void* y, int32_t y_dtype, int64_t y_stride, void* stream);

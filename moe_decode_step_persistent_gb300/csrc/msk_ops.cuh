@@ -106,14 +106,16 @@ __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) 
 
 // The power of two by which a row of 16-bit floats with largest magnitude
 // `amax` is multiplied before it is written as fp16, as an exponent: amax
-// lands in [2^8, 2^9), so that every element above 2^-22 amax is exact in
-// fp16 (bf16 has 8 significant bits, fp16 11 above 2^-14) and smaller ones
-// are off by at most 2^-25, that is 2^-33 amax: below what an fp32 sum of
-// the row's products keeps.  The factor and its inverse stay normal fp32
-// numbers; at its limit even bf16's subnormals arrive exactly.
+// lands in [2^14, 2^15) of fp16's 65504, so that every element above 2^-31
+// amax is exact in fp16 (bf16 has 8 significant bits; 2^-17 and above lie in
+// steps of 2^-24 or wider), and smaller ones are off by at most 2^-25, that is
+// 2^-39 amax.  An fp32 sum keeps less than that where amax has a part in it;
+// where amax meets zeros, elements that small are what a caller loses.  The
+// factor and its inverse stay normal fp32 numbers; at its limit even bf16's
+// subnormals arrive exactly.
 __device__ __forceinline__ int row_shift(float amax) {
   const int e = (int)(__float_as_uint(amax) >> 23) - 127;  // floor(log2), -127 for zero and subnormals
-  return e < -118 ? 126 : (e > 127 ? -119 : 8 - e);
+  return e < -112 ? 126 : (e > 127 ? -113 : 14 - e);
 }
 
 // 8-byte global -> shared copy.

@@ -1,0 +1,47 @@
+"""The operators beside the step at the ends of their ranges, against their
+definitions in 64 bits with the tolerances of test_gpu_ops.py."""
+
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_ops import (  # noqa: F401
+    DT, M, check_attention, check_linear, filled_cache, gen, half_step, random_fp4, randn)
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------------------
+# rows with one element far above the rest
+# ----------------------------------------------------------------------------
+
+
+def small_elements(seed, *shape):
+    """bf16 numbers of all significands, 2^-31 up to 2^-30."""
+    s = torch.randint(128, 256, shape, generator=gen(seed)).float() * 2.0 ** -38
+    return s * (1 - 2.0 * torch.randint(0, 2, shape, generator=gen(seed + 1)))
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 130, 512), (5, 300, 4096), (16, 77, 1024)])
+def test_linear_with_one_element_far_above_the_rest(M, T, N, K):
+    """Elements down to 2^-31 of their row's greatest enter without rounding: with
+    weights of 0 for the greatest only they are left."""
+    packed, scales = random_fp4(201, N, K)
+    packed[:, 0] &= 0xF0
+    x = small_elements(202, T, K)
+    x[:, 0] = 255 / 128
+    x = x.bfloat16().cuda()
+    y = M.msk_linear_fp4(x, M.Fp4Weight(packed.cuda(), scales.cuda()), out_dtype=torch.float32)
+    check_linear(y, x, packed, scales, 1.0)
+
+
+@pytest.mark.parametrize("T,hq,d", [(1, 4, 64), (4, 4, 128), (16, 4, 128)])
+def test_attention_with_one_element_far_above_the_rest(M, T, hq, d):
+    cache = filled_cache(M, 203, 1, 300, d)
+    cache.codes[0, :, :, 0] &= 0xF0
+    q = small_elements(204, T, hq, d)
+    q[..., 0] = 255 / 128
+    q = q.bfloat16().cuda()
+    scale = 2.0 ** 30 / math.sqrt(d)
+    check_attention(M, M.msk_attention_kv4(q, cache, 280, softmax_scale=scale), q, cache, 280, 0, None, scale)
