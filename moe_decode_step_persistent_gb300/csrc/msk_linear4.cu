@@ -2,6 +2,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "msk_internal.h"
@@ -43,7 +44,8 @@ struct Lin4 {
   long long x_stride, y_stride, N;
   int K, T, y_dtype, groups, ks, stages;
   bool fp16, scales_tma;
-  float ts;
+  float ts;    // the tensor's scale: its significand ...
+  int ts_exp;  // ... and the power of two that it is multiplied with
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -92,7 +94,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Bars bars;
   __shared__ uint32_t amaxs[16];  // each token's largest magnitude, as an fp32 number's bits
-  __shared__ float back[16];  // undoes each token's scaling
+  // undo each token's scaling and apply the tensor's: two factors, a half of the
+  // power of two each, so that no product leaves fp32's range unless the result does
+  __shared__ float back[16], back2[16];
   __shared__ uint32_t tmem_base;
   __shared__ int abort, never;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -223,7 +227,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
       }
       fence_proxy_async_shared();
     }
-    if (tid < 16) back[tid] = a.fp16 ? 1.f : exp2i(-row_shift(__uint_as_float(amaxs[tid])));
+    if (tid < 16) {
+      // (below -252 every sum, at most 2^41, ends in 0 all the same)
+      const int e = max(a.ts_exp - (a.fp16 ? 0 : row_shift(__uint_as_float(amaxs[tid]))), -252), half = e / 2;
+      back[tid] = a.ts * exp2i(half), back2[tid] = exp2i(e - half);
+    }
   }
   __syncthreads();
   if (CL) cluster_wait();
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int t = team * 4 + j;
-          if (t < a.T && n0 + r < a.N) store(t, n0 + r, s[j] * back[t] * a.ts);
+          if (t < a.T && n0 + r < a.N) store(t, n0 + r, s[j] * back[t] * back2[t]);
         }
         return true;
       }
@@ -273,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
       for (int j = 0; j < 4; ++j) {
         const int t = team * 4 + j, u = 4 * t + quad, to = u % ks;
         if (t < a.T)
-          st_async(mapa(smem_u32(parts + d * kPartFloats + (u / ks * ks + rank) * 32 + lane), to), s[j] * back[t],
+          st_async(mapa(smem_u32(parts + d * kPartFloats + (u / ks * ks + rank) * 32 + lane), to), s[j] * back[t] * back2[t],
                    mapa(bar(bars.parts[d]), to));
       }
       if (owned > 0 && !wait_parts(bars.parts[d], (i >> 1) & 1)) return false;
@@ -282,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
         const float* f = parts + d * kPartFloats + k * ks * 32 + lane;
         float v = 0.f;
         for (int b = 0; b < ks; ++b) v += f[b * 32];
-        if (n0 + rr < a.N) store(u >> 2, n0 + rr, v * a.ts);
+        if (n0 + rr < a.N) store(u >> 2, n0 + rr, v);
       }
       if (i + 2 < mine) {  // the place is written again for tile i + 2
         __syncwarp();
@@ -520,7 +528,9 @@ extern "C" msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_s
   Lin4 a{};
   a.scales = w->scales, a.y = y;
   a.y_stride = y_stride, a.N = w->rows, a.K = (int)w->cols, a.T = tokens;
-  a.y_dtype = y_dtype, a.fp16 = x_dtype == MSK_FP16, a.ts = w->tensor_scale;
+  a.y_dtype = y_dtype, a.fp16 = x_dtype == MSK_FP16;
+  a.ts = w->tensor_scale;
+  if (std::isfinite(a.ts) && a.ts != 0.f) a.ts = 2.f * std::frexp(a.ts, &a.ts_exp), --a.ts_exp;  // [1, 2)
   a.groups = (a.K + kGroup - 1) / kGroup;
   // (a tiled copy's rows lie a multiple of 16 bytes apart: with an odd
   // multiple of 128 columns the scales' do not, and are loaded one by one)

@@ -45,3 +45,35 @@ def test_attention_with_one_element_far_above_the_rest(M, T, hq, d):
     q = q.bfloat16().cuda()
     scale = 2.0 ** 30 / math.sqrt(d)
     check_attention(M, M.msk_attention_kv4(q, cache, 280, softmax_scale=scale), q, cache, 280, 0, None, scale)
+
+
+# ----------------------------------------------------------------------------
+# results in range whose parts are not
+# ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("T,N,K", [(2, 48, 1024), (16, 20000, 256), (3, 40, 8192)])
+@pytest.mark.parametrize("xt,yt,size,ts", [
+    ("bf16", "fp32", 2e36, 4.4e-5), ("bf16", "bf16", 3e37, 1e-38), ("bf16", "fp32", 1e-36, 1e36), ("bf16", "fp32", 1e-38, 3e38),
+    ("fp16", "fp32", 6e4, 1e-38), ("fp16", "fp32", 6e-5, 1e35)])
+def test_linear_of_far_apart_scales(M, T, N, K, xt, yt, size, ts):
+    """Rows and tensor scales at the two ends of their types: the products of one
+    alone with the weights (up to 2688) pass fp32's range, the result does not."""
+    packed, scales = random_fp4(211, N, K)
+    scales[:] = 0x7E - scales % 16  # block scales of 112 to 448
+    x = randn(212, T, K).clamp(-3, 3) / 3
+    x = (x.double() * size).to(DT[xt]).cuda()
+    y = M.msk_linear_fp4(x, M.Fp4Weight(packed.cuda(), scales.cuda(), ts), out_dtype=DT[yt])
+    assert torch.isfinite(y).all()
+    check_linear(y, x, packed, scales, ts)
+
+
+@pytest.mark.parametrize("ts", [0.0, -0.75, float("inf"), float("nan")])
+def test_linear_of_any_tensor_scale(M, ts):
+    packed, scales = random_fp4(213, 40, 256)
+    x = randn(214, 2, 256).bfloat16().cuda()
+    y = M.msk_linear_fp4(x, M.Fp4Weight(packed.cuda(), scales.cuda(), ts), out_dtype=torch.float32)
+    if math.isfinite(ts):
+        check_linear(y, x, packed, scales, ts)
+    else:
+        assert not torch.isfinite(y).any()
