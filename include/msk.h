@@ -383,7 +383,8 @@ msk_status msk_kv4_read(const msk_kv4_desc* cache, int32_t pos0, int32_t tokens,
  *            (read during the call, so a graph keeps the tree it was captured
  *            with);
  *   window : 0 for global attention, else keys [p - window + 1, p];
- *   softmax_scale: factor of the scores, 0 for 1 / sqrt(head_dim).
+ *   softmax_scale: factor of the scores, 0 for 1 / sqrt(head_dim); with k_scale
+ *            and log2(e) a finite fp32 number.
  * n_q_heads a multiple of cache->n_kv_heads, any quotient.  Cache rows that no
  * query sees are not read, or do not count whatever they hold.
  * Queries enter the products in fp16 after a scaling of each row by a power of

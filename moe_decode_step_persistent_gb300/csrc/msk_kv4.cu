@@ -1389,6 +1389,9 @@ extern "C" msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_
   if (window < 0 || tokens > cache->max_seq) return MSK_ERR_INVALID_ARG;
   if (cache_len_dev == nullptr && (cache_len < 0 || cache_len > cache->max_seq - tokens)) return MSK_ERR_INVALID_ARG;
   if (!(softmax_scale >= 0.f && softmax_scale <= 3e38f)) return MSK_ERR_INVALID_ARG;
+  const float scale = softmax_scale > 0.f ? softmax_scale : (float)(1.0 / std::sqrt((double)cache->head_dim));
+  const float qk_scale = scale * cache->k_scale * 1.4426950408889634f;
+  if (!std::isfinite(qk_scale)) return MSK_ERR_INVALID_ARG;  // (every score would be a NaN)
   if (q_stride < (int64_t)n_q_heads * cache->head_dim && tokens > 1) return MSK_ERR_INVALID_ARG;
   if (!ops_aligned16(q) || !ops_aligned16(out) || !ops_aligned16(workspace) || q_stride % 8) return MSK_ERR_ALIGNMENT;
   Kv4Attn a{};
@@ -1412,8 +1415,7 @@ extern "C" msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_
   a.max_seq = cache->max_seq, a.len = cache_len, a.window = window;
   a.splits = plan.splits, a.cluster = plan.cluster;
   a.fp16 = dtype == MSK_FP16;
-  const float scale = softmax_scale > 0.f ? softmax_scale : (float)(1.0 / std::sqrt((double)cache->head_dim));
-  a.qk_scale = scale * cache->k_scale * 1.4426950408889634f;
+  a.qk_scale = qk_scale;
   a.v_scale = cache->v_scale;
   const size_t parts = (size_t)plan.tiles * a.Hkv * a.splits * plan.tile_rows;
   a.o_part = static_cast<float*>(workspace);

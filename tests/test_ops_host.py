@@ -137,3 +137,10 @@ def test_binding_refuses_on_the_host(M):
         M.Fp4Weight(cpu[0, 0], sc[0, 0])
     with pytest.raises(ValueError):
         M.Fp4Weight(cpu[0, 0], sc[0, 0, :, :3])
+
+
+@pytest.mark.parametrize("k_scale,scale,status", [(1e20, 1e20, INVALID), (3e38, 2.0, INVALID), (3e38, 0.0, None), (1e-30, 1e30, None)])
+def test_attention_scales_that_leave_the_range_together(M, lib, k_scale, scale, status):
+    got = lib.msk_attention_kv4(P, BF16, 4096, cache(M, ks=k_scale), 0 if status is None else 4, 32, 100, None, None, 0, scale, P, P,
+                                1 << 30, None)
+    assert got == (SHAPE if status is None else status)  # (no tokens: refused for that alone)
