@@ -53,13 +53,15 @@ __device__ __forceinline__ void load16(const void* base, long long off, float (&
   }
 }
 
-// Two x / d rounded to nearest (y: two rounded reciprocals of d; quotients and
-// remainders within the normal range): Markstein's correction of x y by its
-// remainder (IBM J. Res. Dev. 34, 1990).  The codes depend on the quotient's
-// last bit where it lies half way between two of them.
-__device__ __forceinline__ void quotients(float& x0, float& x1, unsigned long long minus_d, unsigned long long y) {
-  const unsigned long long x = pair(x0, x1), q = mul2(x, y);
-  unpair(fma2(fma2(q, minus_d, x), y, q), x0, x1);
+// Two -x / d rounded to nearest (my: two rounded reciprocals of d, negative;
+// quotients and remainders within the normal range): Markstein's correction of
+// x my by its remainder (IBM J. Res. Dev. 34, 1990).  The codes depend on the
+// quotient's last bit where it lies half way between two of them.  The negative
+// quotient, because a remainder of 0 is +0: times my it is -0, which leaves the
+// sign of a zero alone, and +0, times y, would not.
+__device__ __forceinline__ void minus_quotients(float& x0, float& x1, unsigned long long d, unsigned long long my) {
+  const unsigned long long x = pair(x0, x1), q = mul2(x, my);
+  unpair(fma2(fma2(q, d, x), my, q), x0, x1);
 }
 
 // Both kernels: blockIdx.y is K's and then V's heads, a block takes `per`
@@ -80,9 +82,10 @@ __device__ __forceinline__ RowsAt rows_at(const Kv4Rows& a, int pos0, int per) {
 }
 
 // A piece is a block of 16 elements, one a thread.  16384 rows of 8 heads of 128
-// in bf16: 15.7 us with scales of 1, 18.1 with others (two pieces a thread 20.0
-// and 22.0; half a piece, so that two threads do each block's scale, 23.7 and
-// 26.3): the quantiser's instructions bound it beside DRAM (12.7 us for the bytes).
+// in bf16: 17.0 us with scales of 1, 19.1 with others (without the signs of zeros
+// 16.4 and 18.9; two pieces a thread 4 us more, half a piece, so that two threads do
+// each block's scale, 8): the quantiser's instructions bound it beside DRAM (12.7 us
+// for the bytes).
 template <int HD, int DT>
 __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4Rows a) {
   constexpr int NP = HD / 16;
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4Rows a) {
   const RowsAt w = rows_at<NP>(a, pos0, 256);
   if (w.piece >= w.n) return;
   const float ts = w.is_v ? a.v_scale : a.k_scale, yts = __frcp_rn(ts);
-  const unsigned long long mts = pair(-ts, -ts), yts2 = pair(yts, yts);
+  const unsigned long long ts2 = pair(ts, ts), myts2 = pair(-yts, -yts);
   const bool plain = ts > 1e-18f && ts < 1e18f;
   const void* src = w.is_v ? a.v : a.k;
   const long long from = w.piece / NP * a.token_stride + w.h * a.head_stride + w.piece % NP * 16;
@@ -102,13 +105,14 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4Rows a) {
   float amax = 0.f;
 #pragma unroll
   for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(x[j]));
-  if (ts != 1.f) {
+  const bool whole = ts == 1.f;
+  if (!whole) {  // x becomes -x / ts
     if (plain && amax < 1e18f) {  // (smaller quotients than normal ones leave codes of 0)
 #pragma unroll
-      for (int j = 0; j < 16; j += 2) quotients(x[j], x[j + 1], mts, yts2);
+      for (int j = 0; j < 16; j += 2) minus_quotients(x[j], x[j + 1], ts2, myts2);
     } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = __fdiv_rn(x[j], ts);
+      for (int j = 0; j < 16; ++j) x[j] = __fdiv_rn(x[j], -ts);
     }
     amax = 0.f;
 #pragma unroll
@@ -120,16 +124,22 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4Rows a) {
   const float dec = e4m3_to_f32(sc);
   uint32_t c[2] = {0u, 0u};
   if (amax > 2688.f) {  // saturates, with infinities perhaps
+    const float d = whole ? dec : -dec;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      c[j >> 2] |= f32x2_to_e2m1x2(__fdiv_rn(x[2 * j], dec), __fdiv_rn(x[2 * j + 1], dec)) << (8 * (j & 3));
+      c[j >> 2] |= f32x2_to_e2m1x2(__fdiv_rn(x[2 * j], d), __fdiv_rn(x[2 * j + 1], d)) << (8 * (j & 3));
   } else if (dec > 0.f) {
     const float y = __frcp_rn(dec);
+    auto codes = [&](auto negate) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      quotients(x[2 * j], x[2 * j + 1], pair(-dec, -dec), pair(y, y));
-      c[j >> 2] |= f32x2_to_e2m1x2(x[2 * j], x[2 * j + 1]) << (8 * (j & 3));
-    }
+      for (int j = 0; j < 8; ++j) {
+        float u = x[2 * j], v = x[2 * j + 1];
+        minus_quotients(u, v, pair(dec, dec), pair(-y, -y));
+        c[j >> 2] |= (negate() ? f32x2_to_e2m1x2(-u, -v) : f32x2_to_e2m1x2(u, v)) << (8 * (j & 3));
+      }
+    };
+    if (whole) codes(std::true_type());
+    else codes(std::false_type());  // (two negative quotients)
   }
   const long long at = w.at + w.piece;  // (rows of a head are consecutive)
   *reinterpret_cast<uint2*>(a.codes + at * 8) = make_uint2(c[0], c[1]);

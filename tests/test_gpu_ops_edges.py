@@ -3,11 +3,12 @@ definitions in 64 bits with the tolerances of test_gpu_ops.py."""
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_ops import (  # noqa: F401
-    DT, M, check_attention, check_linear, filled_cache, gen, half_step, random_fp4, randn)
+from oracle import formats as F
+from tests.test_gpu_ops import DT, M, check_attention, check_linear, filled_cache, gen, pack, random_fp4, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,33 @@ def test_linear_of_any_tensor_scale(M, ts):
         check_linear(y, x, packed, scales, ts)
     else:
         assert not torch.isfinite(y).any()
+
+
+# ----------------------------------------------------------------------------
+# signs of zeros in the cache
+# ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("scales", [(1.0, 0.37), (2.5, 1.0), (1e-20, 1e20)])
+def test_write_keeps_the_signs_of_zeros(M, dtype, scales):
+    """Codes and scales bit for bit the oracle's where elements are -0, among others, among
+    elements that round to 0, among saturating ones and alone."""
+    x = randn(221, 2, 6, 1, 64)
+    x[:, :, :, ::3] = -0.0
+    x[:, :, :, 1::7] *= -1e-3
+    x[:, 1] = -0.0
+    x[:, 2, 0, 17] = 6e4
+    x[:, 3, 0, ::2] = 0.0
+    if scales[0] < 1e-10 and dtype != "fp16":
+        x[0] *= scales[0]
+        x[1] *= scales[1]
+    x = x.to(DT[dtype])
+    cache = M.Kv4Cache.empty(1, 6, 64, *scales)
+    M.msk_kv4_write(cache, x[0].cuda(), x[1].cuda(), 0)
+    for i in (0, 1):
+        y = (x[i].float() / torch.tensor(scales[i], dtype=torch.float32)).transpose(0, 1)
+        codes, sc, _ = F.q4(y.double().numpy())
+        assert np.array_equal(cache.codes[i].cpu().numpy(), pack(codes).numpy())
+        assert np.array_equal(cache.scales[i].cpu().numpy(), sc)
+        assert ((codes == 8) & (y.numpy() == 0)).any() or not sc.any()
