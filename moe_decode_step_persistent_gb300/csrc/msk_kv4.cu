@@ -189,20 +189,17 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4Rows a) {
 }
 
 template <int HD>
-void launch_rows(bool write, int32_t dt, const Kv4Rows& a, cudaStream_t st) {
+cudaError_t launch_rows(bool write, int32_t dt, const Kv4Rows& a, cudaStream_t st) {
   const int piece = write ? 16 : dt == MSK_FP32 ? 4 : 8, per = write ? 256 : 256 * kReadUnroll;
   const long long n = (long long)a.tokens * HD / piece;
   const dim3 grid((unsigned)((n + per - 1) / per), 2u * a.Hkv);
   const OpsLaunch l(grid, 256, 0, st);
-#define MSK_ROWS(D)                                                    \
-  do {                                                                 \
-    if (write) cudaLaunchKernelEx(&l.cfg, kv4_write_kernel<HD, D>, a); \
-    else cudaLaunchKernelEx(&l.cfg, kv4_read_kernel<HD, D>, a);        \
-  } while (0)
-  if (dt == MSK_BF16) MSK_ROWS(MSK_BF16);
-  else if (dt == MSK_FP16) MSK_ROWS(MSK_FP16);
-  else MSK_ROWS(MSK_FP32);
-#undef MSK_ROWS
+  auto launch = [&](void (*write_kernel)(Kv4Rows), void (*read_kernel)(Kv4Rows)) {
+    return cudaLaunchKernelEx(&l.cfg, write ? write_kernel : read_kernel, a);
+  };
+  return dt == MSK_BF16   ? launch(kv4_write_kernel<HD, MSK_BF16>, kv4_read_kernel<HD, MSK_BF16>)
+         : dt == MSK_FP16 ? launch(kv4_write_kernel<HD, MSK_FP16>, kv4_read_kernel<HD, MSK_FP16>)
+                          : launch(kv4_write_kernel<HD, MSK_FP32>, kv4_read_kernel<HD, MSK_FP32>);
 }
 
 constexpr int kMaxRows = 1 << 30;  // of a cache: positions and steps stay within 32 bits
@@ -238,9 +235,9 @@ msk_status rows_call(bool write, const msk_kv4_desc* c, const void* k, const voi
   a.token_stride = ts, a.head_stride = hs;
   a.Hkv = c->n_kv_heads, a.max_seq = c->max_seq, a.tokens = tokens, a.pos0 = pos0;
   a.k_scale = c->k_scale, a.v_scale = c->v_scale;
-  if (c->head_dim == 128) launch_rows<128>(write, dtype, a, static_cast<cudaStream_t>(stream));
-  else launch_rows<64>(write, dtype, a, static_cast<cudaStream_t>(stream));
-  return cudaGetLastError() == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = c->head_dim == 128 ? launch_rows<128>(write, dtype, a, st) : launch_rows<64>(write, dtype, a, st);
+  return e == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
