@@ -156,8 +156,17 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _int32(value, what):
+    """`value` as an int that the C call takes as it is (ctypes drops the bits
+    that do not fit)."""
+    value = int(value)
+    if not -0x80000000 <= value <= 0x7FFFFFFF:
+        raise ValueError(f"{what} does not fit 32 bits: {value}")
+    return value
+
+
 def _positions(positions):
-    return (ctypes.c_int32 * len(positions))(*[int(p) for p in positions])
+    return (ctypes.c_int32 * len(positions))(*[_int32(p, "a position") for p in positions])
 
 
 # ----------------------------------------------------------------------------
@@ -360,7 +369,7 @@ def _position(pos):
         _need(pos.dtype == torch.int32 and pos.numel() == 1 and pos.get_device() == torch.cuda.current_device(),
               "a position tensor is one int32 on the current CUDA device")
         return 0, pos.data_ptr()
-    return int(pos), None
+    return _int32(pos, "a position"), None
 
 
 def _kv_rows(cache, k, v):
@@ -403,13 +412,15 @@ def msk_kv4_read(cache, pos0, tokens, dtype=torch.bfloat16, out=None, stream=Non
     dt, T, ts, hs = _kv_rows(cache, k, v)
     _need(T == tokens, "out does not hold `tokens` rows")
     st = _enqueue(stream, k, v, cache._codes)
-    _check(load_library().msk_kv4_read(cache.desc, int(pos0), tokens, k.data_ptr(), v.data_ptr(), dt, ts, hs, st),
-           "msk_kv4_read")
+    _check(load_library().msk_kv4_read(cache.desc, _int32(pos0, "a position"), tokens, k.data_ptr(), v.data_ptr(), dt,
+                                       ts, hs, st), "msk_kv4_read")
     return k, v
 
 
 def msk_attention_kv4_workspace(tokens, n_q_heads, n_kv_heads, head_dim, window, cache_len):
     """Workspace bytes of msk_attention_kv4 (0 for few keys)."""
+    sizes = (tokens, n_q_heads, n_kv_heads, head_dim, window, cache_len)
+    _need(-0x80000000 <= min(sizes) and max(sizes) <= 0x7FFFFFFF, "sizes that fit 32 bits")
     return load_library().msk_attention_kv4_workspace(tokens, n_q_heads, n_kv_heads, head_dim, window, cache_len)
 
 
@@ -432,11 +443,12 @@ def msk_attention_kv4(q, cache, cache_len, window=0, parents=None, softmax_scale
         _need(out.dtype == q.dtype and out.numel() == q.numel() and out.is_contiguous(),
               "out: contiguous [tokens][n_q_heads * head_dim] of q's type")
     host, dev = _position(cache_len)
+    window = _int32(window, "window")
     need = msk_attention_kv4_workspace(T, Hq, cache.n_kv_heads, d, window, host if dev is None else cache.max_seq - T)
     ws, addr, size = _workspace(workspace, need, stream)
     st = _enqueue(stream, q, out, cache._codes) if ws is None else _enqueue(stream, q, out, cache._codes, ws)
     _check(load_library().msk_attention_kv4(q.data_ptr(), dtype, ts if T > 1 else 0, cache.desc, T, Hq, host, dev,
-                                            None if parents is None else _positions(parents), int(window),
+                                            None if parents is None else _positions(parents), window,
                                             softmax_scale, out.data_ptr(), addr, size, st), "msk_attention_kv4")
     return out
 

@@ -144,3 +144,22 @@ def test_attention_scales_that_leave_the_range_together(M, lib, k_scale, scale, 
     got = lib.msk_attention_kv4(P, BF16, 4096, cache(M, ks=k_scale), 0 if status is None else 4, 32, 100, None, None, 0, scale, P, P,
                                 1 << 30, None)
     assert got == (SHAPE if status is None else status)  # (no tokens: refused for that alone)
+
+
+def test_binding_refuses_numbers_that_do_not_fit(M):
+    """2^32 is not row 0, and a window of 2^32 not a global one: refused, and not cut to 32 bits."""
+    class Cache:  # (nothing of it is reached)
+        n_kv_heads, head_dim, max_seq = 2, 64, 16
+    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    q, out = k.new_zeros(3, 4, 64), k.new_zeros(3, 256)
+    for big in (1 << 32, (1 << 32) + 5, 1 << 31, -(1 << 31) - 1, -(1 << 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            M.msk_kv4_write(Cache, k, k, big)
+        with pytest.raises(ValueError, match="32 bits"):
+            M.msk_attention_kv4(q, Cache, big, out=out)
+        with pytest.raises(ValueError, match="32 bits"):
+            M.msk_attention_kv4(q, Cache, 5, window=big, out=out)
+        with pytest.raises(ValueError, match="32 bits"):
+            M.msk_attention_kv4_workspace(3, 4, 2, 64, 0, big)
+        with pytest.raises(ValueError, match="32 bits"):
+            M._positions([-1, 0, big])
