@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -1293,10 +1294,10 @@ int most_keys(int tokens, int window, int len) {
 }
 
 // A kernel over (key ranges, kv heads, row tiles), its shared-memory limit set
-// once a device (`ready`; twice does no harm).
+// once a device (`ready`; by two threads at once does no harm).
 template <typename Args>
-cudaError_t launch_blocks(void (*kernel)(Args), const Args& args, bool (&ready)[64], int threads, int smem, const Kv4Plan& p,
-                          int Hkv, cudaStream_t st) {
+cudaError_t launch_blocks(void (*kernel)(Args), const Args& args, std::atomic<bool> (&ready)[64], int threads, int smem,
+                          const Kv4Plan& p, int Hkv, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1312,14 +1313,14 @@ cudaError_t launch_blocks(void (*kernel)(Args), const Args& args, bool (&ready)[
 
 template <int HD, int NT>
 cudaError_t launch_rows_kernel(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st) {
-  static bool ready[64] = {};
+  static std::atomic<bool> ready[64] = {};
   constexpr int smem = rows_smem<HD, NT>() + recv_bytes(8 * NT, HD);
   return launch_blocks(kv4_rows_kernel<HD, NT>, a, ready, 256, smem, p, a.Hkv, st);
 }
 
 template <int HD, int NR>
 cudaError_t launch_tc_kernel(const Kv4Attn& a, const Kv4Plan& p, cudaStream_t st) {
-  static bool ready[64] = {};
+  static std::atomic<bool> ready[64] = {};
   Kv4AttnTc t{};
   t.a = a;
   const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();

@@ -144,3 +144,45 @@ def test_rows_do_not_report_the_errors_of_other_calls(M):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     run = subprocess.run([sys.executable, "-c", AFTER_AN_ERROR], cwd=root, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and "written" in run.stdout, run.stderr[-2000:]
+
+
+# ----------------------------------------------------------------------------
+# first calls from several threads
+# ----------------------------------------------------------------------------
+
+FIRST_FROM_THREADS = """
+import threading
+import torch
+import moe_decode_step_persistent_gb300 as M
+caches = [M.Kv4Cache.empty(2, 20000, 128) for _ in range(8)]
+q = torch.randn(16, 8, 128, device="cuda").bfloat16()
+kv = torch.randn(16000, 2, 128, device="cuda").bfloat16()
+w = M.Fp4Weight(torch.full((1000, 512), 0x23, dtype=torch.uint8, device="cuda"),
+                torch.full((1000, 64), 0x38, dtype=torch.uint8, device="cuda"))
+x = torch.randn(16, 1024, device="cuda").bfloat16()
+torch.cuda.synchronize()
+outs, go = [None] * 8, threading.Barrier(8)
+
+def calls(i):
+    s, c = torch.cuda.Stream(), caches[i]
+    go.wait()
+    M.msk_kv4_write(c, kv, kv, 0, stream=s)
+    got = [M.msk_attention_kv4(q[:t], c, n, stream=s) for t in (1, 3, 16) for n in (100, 15000)]
+    got += [M.msk_linear_fp4(x[:t], w, stream=s) for t in (1, 16)]
+    got += [M.msk_token_logprobs(got[-1], top=3, stream=s)[4]]
+    s.synchronize()
+    outs[i] = got
+
+threads = [threading.Thread(target=calls, args=(i,)) for i in range(8)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert all(torch.equal(a, b) for o in outs for a, b in zip(o, outs[0]))
+M.msk_ops_check()
+print("the same")
+"""
+
+
+def test_first_calls_from_several_threads(M):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_FROM_THREADS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "the same" in run.stdout, run.stderr[-2000:]
