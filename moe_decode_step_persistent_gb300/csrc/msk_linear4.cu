@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
   __shared__ uint32_t amaxs[16];  // each token's largest magnitude, as an fp32 number's bits
   // undo each token's scaling and apply the tensor's: two factors, a half of the
   // power of two each, so that no product leaves fp32's range unless the result does
-  __shared__ float back[16], back2[16];
+  __shared__ float2 back[16];
   __shared__ uint32_t tmem_base;
   __shared__ int abort, never;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
     if (tid < 16) {
       // (below -252 every sum, at most 2^41, ends in 0 all the same)
       const int e = max(a.ts_exp - (a.fp16 ? 0 : row_shift(__uint_as_float(amaxs[tid]))), -252), half = e / 2;
-      back[tid] = a.ts * exp2i(half), back2[tid] = exp2i(e - half);
+      back[tid] = make_float2(a.ts * exp2i(half), exp2i(e - half));
     }
   }
   __syncthreads();
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int t = team * 4 + j;
-          if (t < a.T && n0 + r < a.N) store(t, n0 + r, s[j] * back[t] * back2[t]);
+          if (t < a.T && n0 + r < a.N) store(t, n0 + r, s[j] * back[t].x * back[t].y);
         }
         return true;
       }
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
       for (int j = 0; j < 4; ++j) {
         const int t = team * 4 + j, u = 4 * t + quad, to = u % ks;
         if (t < a.T)
-          st_async(mapa(smem_u32(parts + d * kPartFloats + (u / ks * ks + rank) * 32 + lane), to), s[j] * back[t] * back2[t],
+          st_async(mapa(smem_u32(parts + d * kPartFloats + (u / ks * ks + rank) * 32 + lane), to), s[j] * back[t].x * back[t].y,
                    mapa(bar(bars.parts[d]), to));
       }
       if (owned > 0 && !wait_parts(bars.parts[d], (i >> 1) & 1)) return false;
@@ -408,9 +408,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
     // what is still in flight ends before the block does
     tc_commit(bar(bars.done[team]));
     mbar_wait(bar(bars.done[team]), 0, gtimer() + kOpsWaitNs, &never);
-    if (*ab && team == 0)  // (an error: a slot's newest copy may be a use ahead of what was waited for)
-      for (int k = 0; k < a.stages; ++k)
-        for (uint32_t q = 0; q < 2; ++q) mbar_wait(bar(bars.full[k]), q, gtimer() + kOpsWaitNs / 100, &never);
   }
   __syncwarp();
   tc_fence_before();
@@ -420,8 +417,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
     tmem_relinquish();
     tmem_dealloc(tmem, 512);
   }
-  if (tid == 0 && abort) atomicExch(&g_error, 1u);
-  if (CL) cluster_sync();  // (no block leaves while others may store into it)
+  if (tid == 0 && abort) {
+    atomicExch(&g_error, 1u);
+    // copies too (no issuer starts one any more): a slot's newest may be a use ahead
+    // of what was waited for
+    for (uint32_t q = 0; q < 2; ++q) {
+      mbar_wait(bar(bars.xfull), q, gtimer() + kOpsWaitNs / 100, &never);
+      for (int k = 0; k < a.stages; ++k) mbar_wait(bar(bars.full[k]), q, gtimer() + kOpsWaitNs / 100, &never);
+    }
+  }
+  if (CL) {
+    __syncwarp();
+    cluster_sync();  // (no block leaves while others may store into it)
+    if (tid == 0 && abort)  // (sums that this block has not waited for may still be on their way)
+      for (const uint64_t end = gtimer() + kOpsWaitNs / 100; gtimer() < end;) __nanosleep(1000);
+  }
 }
 
 // A row-major matrix of bytes or 16-bit words, `pitch` bytes between rows, in
