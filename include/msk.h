@@ -378,7 +378,8 @@ msk_status msk_kv4_read(const msk_kv4_desc* cache, int32_t pos0, int32_t tokens,
  *            before; S + tokens <= max_seq;
  *   cache_len_dev: NULL, or a DEVICE int32 that is read instead of cache_len
  *            when the kernels run (for graphs); clamped to
- *            [0, max_seq - tokens];
+ *            [0, max_seq - tokens].  The call is then laid out for the
+ *            longest length, which costs a short one 1 to 3 us;
  *   parents: HOST [tokens] as in msk_decode_step_tree, or NULL for the chain
  *            (read during the call, so a graph keeps the tree it was captured
  *            with);
@@ -420,8 +421,12 @@ msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_stride, cons
 
 /* Synchronises `stream` (so not under capture) and tells whether a bounded
  * device wait of these operators ran out on the current device since the last
- * call of this function: MSK_ERR_TIMEOUT (the outputs of the calls since then are not to be
- * used), else MSK_OK. */
+ * call of this function: MSK_ERR_TIMEOUT (the outputs of the calls since then are
+ * not to be used), else MSK_OK.  Such waits are in msk_linear_fp4 and in
+ * msk_attention_kv4 for more than 16 query rows of a kv head; the other kernels
+ * wait for nothing that may stay away.  There is one record for a device: a check
+ * clears it, and takes note of other threads' and streams' calls too, so of several
+ * users of a device one has to check for all. */
 msk_status msk_ops_check(void* stream);
 
 /* Log probabilities under softmax(logits / temperature), one pass per row:

@@ -248,8 +248,9 @@ msk_status rows_call(bool write, const msk_kv4_desc* c, const void* k, const voi
 constexpr int kMaxSplits = 128;   // key ranges of a kv head, each a block's, joined by a second kernel
 constexpr int kMaxCluster = 9;    // or, of few keys, the blocks of a cluster (as many clusters of 9 run at once as of 8)
 // Up to so many keys (of a tile of 8 rows, of more) a cluster and its one launch
-// beat ranges and a second kernel: 1 token x 6000 keys 7.9 us and 9.1, 12000 10.8
-// and 10.1; 16 tokens x 2000 11.5 either way, 4000 13.0 and 12.4, 8000 16.8 and 14.5.
+// beat ranges and a second kernel.  4 rows (1 token of a group of 4) x 6000 keys 7.4 us
+// and 8.8, 12000 10.3 and 9.9; 12 rows x 2000 8.4 and 9.0, 4000 9.8 either way, 6000
+// 10.9 and 9.8; 64 rows x 2000 11.3 and 12.1, 4000 13.4 and 12.5, 8000 17.5 and 14.9.
 constexpr int cluster_keys(int rows) { return rows <= 8 ? 8192 : 256 * kMaxCluster; }
 constexpr int kRing = 5;          // steps of 16 keys in a warp's ring
 
@@ -422,9 +423,9 @@ __device__ __forceinline__ void finish_block(const Kv4Attn& a, float* smem, floa
 // A warp's keys come through a ring of kRing steps of its own, by asynchronous
 // copies; warps meet only at the end.  One token, 131071 keys of 8 kv heads: 36.0
 // us (4.2 TB/s, 62% of what a copy reaches; with weights of one part 34.3).  Bound by
-// the decoding (a conversion
-// and a multiply for two elements; the ALU 56%, issue slots 59% in use) beside
-// DRAM.  Q in shared memory for three blocks an SM instead of two: 43 us.
+// the decoding (a conversion and a multiply for two elements; the ALU 55%, issue
+// slots 60% in use) beside DRAM.  Q in shared memory for three blocks an SM instead
+// of two lost 8 us.
 template <int HD, int NT>
 constexpr int rows_smem() {  // the rings, then the warps' sums
   return std::max(8 * kRing * Kv16<HD>::BYTES, 8 * 8 * NT * (HD + 4) * 4 + 8 * 8 * NT * 8);
@@ -823,7 +824,7 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N]) {
 // 64 rows cost four times the decoding or do not fit the registers: 53 us for
 // 16 tokens over 32768 keys of 8 kv heads, here 28.0 (131072 keys: 77.3).  Bound
 // by the chain of a step (decoding, scores, softmax, weights, each through
-// tensor memory; 2.1 us) with two teams: issue slots 49%, tensor pipe 22% in
+// tensor memory; 2.4 us) with two teams: issue slots 50%, tensor pipe 30% in
 // use.  A third team has no room in tensor memory and registers.
 //
 // The weights' two parts (see Split) lie side by side as the N of one MMA, columns r
@@ -831,7 +832,7 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N]) {
 // twice: 30.0 us for 28.0).  The second part costs 2.8 us of the 28.0.
 //
 // NR: rows of the 64 that are in use, 32 or 64 (the softmax skips the rest: 32
-// rows, 32768 keys 22.0 us, as 64 24.9).
+// rows, 32768 keys 22.0 us, as 64 26.8).
 template <int HD, int NR>
 __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc_kernel(const __grid_constant__ Kv4AttnTc args) {
   using L = Tc<HD>;
@@ -1266,7 +1267,7 @@ struct Kv4Plan {
 Kv4Plan plan_attention(int tokens, int group, int Hkv, int keys) {
   Kv4Plan p{};
   const int rows = tokens * group;
-  // (16 rows, 16384 keys of 8 kv heads: 13.3 us in a tile of 16, 15.0 in one of 64)
+  // (16 rows, 16384 keys of 8 kv heads: 13.8 us in a tile of 16, 14.7 in one of 64)
   p.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : kTcRows;
   p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   p.cluster = p.splits = 1;
@@ -1404,7 +1405,9 @@ extern "C" msk_status msk_attention_kv4(const void* q, int32_t dtype, int64_t q_
   if (!ops_aligned16(q) || !ops_aligned16(out) || !ops_aligned16(workspace) || q_stride % 8) return MSK_ERR_ALIGNMENT;
   Kv4Attn a{};
   if (!tree_masks(parents, tokens, window, a.depth, a.vis)) return MSK_ERR_INVALID_ARG;
-  // (a cache of few rows is laid out by its size, whatever its length now)
+  // (a cache of few rows is laid out by its size, whatever its length now, and so is
+  // any where the length is read on the device: 4 rows x 128 keys in a cache of 20000 7.5
+  // us, of a length known here 4.6, 4000 8.5 and 6.6; 64 rows 11.7 and 10.4, 12.6 and 12.5)
   int keys = most_keys(tokens, window, cache->max_seq - tokens);
   if (cache_len_dev == nullptr && keys > cluster_keys(tokens * G)) keys = most_keys(tokens, window, cache_len);
   const Kv4Plan plan = plan_attention(tokens, G, cache->n_kv_heads, keys);

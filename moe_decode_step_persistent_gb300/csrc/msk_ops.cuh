@@ -29,8 +29,10 @@ inline msk_status ops_device(int* nsm) {
   return major == 10 && minor == 3 ? MSK_OK : MSK_ERR_UNSUPPORTED_DEVICE;
 }
 
-// Bound of every wait of these kernels; after it a kernel records an error
-// (msk_ops_check), ends its copies and MMAs, and returns.
+// Bound of every wait on an mbarrier (linear4_kernel and kv4_tc_kernel have
+// them); after it a kernel records an error (msk_ops_check), ends its copies and
+// MMAs, and returns.  Barriers of a block's threads and of a cluster's blocks have
+// no limit: all of them come to each, also after a wait that ran out.
 constexpr uint64_t kOpsWaitNs = 200ull * 1000 * 1000;
 // ... and more for each step of a block's work, many times what it takes.
 constexpr uint64_t kOpsStepNs = 20ull * 1000;
