@@ -28,6 +28,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import subprocess
 import sys
 import tempfile
@@ -187,10 +188,22 @@ def launch_bytes(wl, layer, n_used, prologue):
     return dense + expert + kv_read + kv_write + act
 
 
-def source_hash():
+def step_sources(csrc):
+    """The layer kernel's sources, its launches' and its weights' layout, with
+    what they include: the operators beside the step are not among them."""
+    todo, seen = ["msk_layer.cu", "msk_api.cu", "msk_repack.cu"], set()
+    while todo:
+        f = todo.pop()
+        if f not in seen and os.path.exists(os.path.join(csrc, f)):
+            seen.add(f)
+            with open(os.path.join(csrc, f)) as fh:
+                todo += re.findall(r'^#include "([^"/]+)"', fh.read(), re.M)
+    return sorted(seen)
+
+
+def source_hash(csrc=os.path.join(ROOT, "moe_decode_step_persistent_gb300", "csrc")):
     h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "moe_decode_step_persistent_gb300", "csrc")
-    for f in sorted(os.listdir(csrc)):
+    for f in step_sources(csrc):
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode())
             h.update(fh.read())

@@ -71,3 +71,30 @@ def test_reference_line_reports_what_it_timed():
     assert line["config"] == bench.workload_config(S.WORKLOADS["tiny"], 1)
     assert line["cpu_baseline"]["value"] == line["value"] and line["cpu_baseline"]["cores"] >= 1
     assert line["e2e"]["h2d_bytes_per_step"] == 0
+
+
+def test_traffic_record_goes_by_the_step_s_sources(tmp_path):
+    """A change to an operator beside the step leaves the recorded traffic of the layer kernel
+    alone, a change to anything that the kernel is built from does not."""
+    import os
+    import shutil
+    csrc = str(tmp_path / "csrc")
+    shutil.copytree(os.path.join(bench.ROOT, "moe_decode_step_persistent_gb300", "csrc"), csrc)
+    before = bench.source_hash(csrc)
+    assert before == bench.source_hash()
+    for f in ("msk_kv4.cu", "msk_linear4.cu", "msk_logprobs.cu", "msk_ops.cuh"):
+        with open(os.path.join(csrc, f), "a") as fh:
+            fh.write("// changed\n")
+    assert bench.source_hash(csrc) == before
+    for f in ("msk_layer.cu", "msk_api.cu", "msk_repack.cu", "msk_phases_moe.cuh", "msk_phases_dense.cuh", "msk_kernel_core.cuh",
+              "msk_tc.cuh", "msk_device.cuh", "msk_internal.h"):
+        with open(os.path.join(csrc, f), "a") as fh:
+            fh.write("// changed\n")
+        after = bench.source_hash(csrc)
+        assert after != before
+        before = after
+
+
+def test_traffic_record_is_of_these_sources():
+    """bench.py gives no traffic where the capture is of another kernel."""
+    assert bench.traffic_per_launch("full62") is not None
