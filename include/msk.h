@@ -95,7 +95,7 @@ typedef struct {
   int64_t rows, cols, ld_elems;
 } msk_bf16_desc;
 
-/* An NVFP4 matrix [rows][cols] (cols a multiple of 128):
+/* An NVFP4 matrix [rows][cols] (cols a multiple of 128, unless a call says otherwise):
  *   packed: [rows][cols/2] bytes, element 2i in the low nibble of byte i,
  *           element 2i+1 in the high nibble; E2M1 codes (bit 3 = sign);
  *   scales: [rows][cols/16] E4M3 codes, one per 16 consecutive elements
@@ -422,8 +422,9 @@ msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_stride, cons
 /* Synchronises `stream` (so not under capture) and tells whether a bounded
  * device wait of these operators ran out on the current device since the last
  * call of this function: MSK_ERR_TIMEOUT (the outputs of the calls since then are
- * not to be used), else MSK_OK.  Such waits are in msk_linear_fp4 and in
- * msk_attention_kv4 for more than 16 query rows of a kv head; the other kernels
+ * not to be used), else MSK_OK.  Such waits are in msk_linear_fp4, in
+ * msk_experts_fp4 and in msk_attention_kv4 for more than 16 query rows of a kv
+ * head; the other kernels
  * wait for nothing that may stay away.  There is one record for a device: a check
  * clears it, and takes note of other threads' and streams' calls too, so of several
  * users of a device one has to check for all. */
@@ -449,6 +450,106 @@ msk_status msk_ops_check(void* stream);
 msk_status msk_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
                               const int32_t* tokens, float temperature, int32_t top, float* logprob, int32_t* rank,
                               float* entropy, int32_t* top_ids, float* top_logprobs, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The experts of a whole prompt: what the step does for 16 tokens inside its
+ * launch, as operators for any number.  In the order of their use:
+ *   msk_moe_route     router logits -> each token's experts and gates
+ *   msk_moe_sort      the tokens' slots by expert
+ *   msk_quantize_fp4  rows to 4 bits (as the step quantises activations)
+ *   msk_experts_fp4   gate and up projections with SwiGLU; once more for the
+ *                     down projection, on rows quantised again
+ *   msk_moe_combine   outputs back at their tokens, weighted and summed
+ * A token's slots are its experts by rank: slot = token * top_k + rank.  The
+ * slots in sorted order are at places 0, 1, ...  The conventions are those of
+ * the operators above: calls enqueue on `stream` and return, may be captured,
+ * and keep nothing between calls; none takes a workspace. */
+
+/* The step's router on any number of tokens: x = fp32(logits) + bias, the
+ * top_k greatest, of equal ones the lowest index first, and their softmax.
+ *   logits : [tokens][n_experts] of dtype (any of the three), ld elements
+ *            between rows (>= n_experts, no alignment asked beyond the element's);
+ *   bias   : fp32 [n_experts] or NULL;
+ *   experts: int32 [tokens][top_k], gates: fp32 [tokens][top_k], by rank.
+ * n_experts up to 1024, top_k up to 32 and n_experts.  An x of -inf or NaN is a
+ * barred expert; where fewer than top_k are left the ranks behind them get expert
+ * -1 and gate 0.  A token with an x of +inf has gates of NaN.  tokens == 0 does
+ * nothing. */
+msk_status msk_moe_route(const void* logits, int32_t dtype, int64_t tokens, int32_t n_experts, int64_t ld,
+                         const float* bias, int32_t top_k, int32_t* experts, float* gates, void* stream);
+
+/* Sorts n slots by expert, within an expert by slot.
+ *   experts: int32 [n]; one outside [0, n_experts) (-1, say) drops its slot;
+ *   offsets: int32 [n_experts + 1]: expert e has places offsets[e] ..
+ *            offsets[e + 1] - 1;
+ *   slots  : int32 [n]: the slot at a place, -1 from offsets[n_experts] on;
+ *   places : int32 [n]: the place of a slot, -1 for a dropped one.
+ * n_experts up to 1024, n up to 2^30.  n == 0 writes offsets of 0. */
+msk_status msk_moe_sort(const int32_t* experts, int64_t n, int32_t n_experts, int32_t* offsets, int32_t* slots,
+                        int32_t* places, void* stream);
+
+/* Rows to 4 bits: x ([rows][cols] of dtype, any of the three, x_stride elements
+ * between rows) to codes [rows][cols / 2] and scales [rows][cols / 16] as in
+ * msk_nvfp4_desc.  The activation quantiser of the step (see msk_debug_quantize)
+ * on fp32(x / tensor_scale); what msk_kv4_write says of values that saturate, of
+ * infinities and of NaN holds here too.  cols a multiple of 16 up to 2^24; x,
+ * its rows, codes and scales 16-byte aligned; tensor_scale positive.  rows == 0
+ * does nothing. */
+msk_status msk_quantize_fp4(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                            float tensor_scale, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The reverse: values of type dtype (exact in bf16 and fp16 where tensor_scale is
+ * 1, else rounded once behind fp32) into rows of x, which must not overlap. */
+msk_status msk_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, float tensor_scale, int64_t rows,
+                              int64_t cols, void* x, int32_t dtype, int64_t x_stride, void* stream);
+
+/* One matrix of each expert, all of one size: packed [n_experts][rows][cols / 2],
+ * scales [n_experts][rows][cols / 16] as in msk_nvfp4_desc (16-byte aligned, read
+ * where they are), tensor_scales: DEVICE fp32 [n_experts], or NULL for 1. */
+typedef struct {
+  const uint8_t* packed;
+  const uint8_t* scales;
+  const float* tensor_scales;
+  int32_t n_experts;
+  int64_t rows, cols;
+} msk_fp4_experts;
+
+/* Products of quantised rows with their experts' weights: for every place p of
+ * expert e
+ *   y[p][i] = sum_j x[row(p)][j] w[e][i][j],  or with `up`
+ *   y[p][i] = silu(sum_j x[row(p)][j] w[e][i][j]) * sum_j x[row(p)][j] up[e][i][j].
+ *   x      : quantised rows (both 4-bit operands enter the tensor cores as they
+ *            are; sums are fp32); x->rows any number, 16-byte aligned;
+ *   slots  : NULL: row(p) = p; else int32 [n] as from msk_moe_sort:
+ *            row(p) = slots[p] / top_k, so that a token's row is read where it
+ *            is by all of its experts (rows outside x are taken as its nearest);
+ *   n      : number of places, x->rows at most where slots is NULL;
+ *   offsets: DEVICE int32 [n_experts + 1], ascending, as from msk_moe_sort;
+ *            what goes beyond [0, n] or back is cut off;
+ *   up     : NULL, or weights of w's size;
+ *   y      : [n][w->rows] of y_dtype (any of the three), y_stride elements between
+ *            rows, aligned to its element; places of no expert are left as
+ *            they were.
+ * One expert (offsets {0, n}) is a plain product.  cols a multiple of 64, 64 to
+ * 131072; n_experts up to 1024, rows up to 2^24, n_experts * rows below 2^31 - 256;
+ * n up to 2^30.  A NaN block scale makes its row's outputs NaN.  n == 0 or
+ * rows == 0 does nothing.  Waits on the device are bounded: see msk_ops_check. */
+msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* slots, int32_t top_k, int64_t n,
+                           const int32_t* offsets, const msk_fp4_experts* w, const msk_fp4_experts* up, void* y,
+                           int32_t y_dtype, int64_t y_stride, void* stream);
+
+/* out[t] = sum over ranks r of gates[t][r] * y[places[t][r]], in order of rank, in
+ * fp32, rounded once.
+ *   y     : [y_rows][cols] of y_dtype, y_stride elements between rows;
+ *   places: int32 [tokens][top_k] as from msk_moe_sort; one outside [0, y_rows)
+ *           is a dropped slot: nothing of it is read;
+ *   gates : fp32 [tokens][top_k], or NULL for 1;
+ *   out   : [tokens][cols] of out_dtype, out_stride elements between rows.
+ * Everything aligned to its element (rows of 16-byte pieces are faster).
+ * tokens == 0 or cols == 0 does nothing. */
+msk_status msk_moe_combine(const void* y, int32_t y_dtype, int64_t y_rows, int64_t y_stride, const int32_t* places,
+                           const float* gates, int64_t tokens, int32_t top_k, int64_t cols, void* out,
+                           int32_t out_dtype, int64_t out_stride, void* stream);
 
 /* Number of SMs (= CTAs per launch) the model uses, and bytes of device
  * memory it owns. */

@@ -8,8 +8,11 @@ The entry points carry the C names (``msk_create``, ``msk_load_layer``,
 ``msk_layer_step``, ``msk_decode_step``, ...); :class:`Model` bundles them for
 weights held in torch tensors.  The operators beside the step
 (``msk_kv4_write``, ``msk_kv4_read``, ``msk_attention_kv4``, ``msk_linear_fp4``,
-``msk_token_logprobs``) take torch tensors, with :class:`Kv4Cache` and
-:class:`Fp4Weight` as the handles of a 4-bit cache and a 4-bit matrix.
+``msk_token_logprobs``) and those of a whole prompt's experts
+(``msk_moe_route``, ``msk_moe_sort``, ``msk_quantize_fp4``,
+``msk_dequantize_fp4``, ``msk_experts_fp4``, ``msk_moe_combine``) take torch
+tensors, with :class:`Kv4Cache`, :class:`Fp4Weight` and :class:`Fp4Experts` as
+the handles of a 4-bit cache, a 4-bit matrix and one matrix of each expert.
 """
 
 from __future__ import annotations
@@ -76,6 +79,11 @@ class Kv4Desc(ctypes.Structure):
                 ("v_scale", ctypes.c_float)]
 
 
+class Fp4ExpertsC(ctypes.Structure):
+    _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tensor_scales", ctypes.c_void_p),
+                ("n_experts", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
 #: every symbol include/msk.h declares
 SYMBOLS = ["msk_create", "msk_load_layer", "msk_layer_step", "msk_decode_step", "msk_layer_step_tree",
            "msk_decode_step_tree", "msk_step_graph_capture", "msk_step_graph_launch", "msk_set_timing",
@@ -83,7 +91,9 @@ SYMBOLS = ["msk_create", "msk_load_layer", "msk_layer_step", "msk_decode_step", 
            "msk_set_fault_injection", "msk_debug_scratch", "msk_debug_dequant", "msk_debug_quantize", "msk_debug_convert",
            "msk_debug_fp4_gemm",
            "msk_attention_noalloc", "msk_kv4_write", "msk_kv4_read", "msk_attention_kv4_workspace",
-           "msk_attention_kv4", "msk_linear_fp4", "msk_ops_check", "msk_token_logprobs", "msk_get_info", "msk_status_string", "msk_destroy"]
+           "msk_attention_kv4", "msk_linear_fp4", "msk_ops_check", "msk_token_logprobs",
+           "msk_moe_route", "msk_moe_sort", "msk_quantize_fp4", "msk_dequantize_fp4", "msk_experts_fp4",
+           "msk_moe_combine", "msk_get_info", "msk_status_string", "msk_destroy"]
 
 _lib = None
 
@@ -128,6 +138,13 @@ def load_library(path: str = LIB_PATH):
     L.msk_linear_fp4.argtypes = [vp, i32, i64, ctypes.POINTER(Nvfp4Desc), i32, vp, i32, i64, vp]
     L.msk_ops_check.argtypes = [vp]
     L.msk_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, vp, vp, vp, vp]
+    fp4, experts = ctypes.POINTER(Nvfp4Desc), ctypes.POINTER(Fp4ExpertsC)
+    L.msk_moe_route.argtypes = [vp, i32, i64, i32, i64, vp, i32, vp, vp, vp]
+    L.msk_moe_sort.argtypes = [vp, i64, i32, vp, vp, vp, vp]
+    L.msk_quantize_fp4.argtypes = [vp, i32, i64, i64, i64, f32, vp, vp, vp]
+    L.msk_dequantize_fp4.argtypes = [vp, vp, f32, i64, i64, vp, i32, i64, vp]
+    L.msk_experts_fp4.argtypes = [fp4, vp, i32, i64, vp, experts, experts, vp, i32, i64, vp]
+    L.msk_moe_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i32, i64, vp, i32, i64, vp]
     L.msk_get_info.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(i64)]
     L.msk_status_string.argtypes = [i32]
     L.msk_status_string.restype = ctypes.c_char_p
@@ -356,6 +373,35 @@ class Fp4Weight:
     tensor_scale = property(lambda self: self._tensor_scale)
 
 
+class Fp4Experts:
+    """One 4-bit matrix [rows][cols] of each expert (see msk_fp4_experts in
+    include/msk.h) over the caller's tensors: packed [n_experts][rows]
+    [cols / 2] and scales [n_experts][rows][cols / 16], uint8, and
+    tensor_scales, fp32 [n_experts] or None for 1."""
+
+    def __init__(self, packed, scales, tensor_scales=None):
+        _need(packed.dtype == torch.uint8 and scales.dtype == torch.uint8, "packed and scales are uint8")
+        _need(packed.dim() == 3 and packed.is_contiguous(), "packed: contiguous [n_experts][rows][cols / 2]")
+        self.n_experts, self.rows, self.cols = packed.shape[0], packed.shape[1], 2 * packed.shape[2]
+        _need(scales.shape == (self.n_experts, self.rows, self.cols // 16) and scales.is_contiguous(),
+              "scales: contiguous [n_experts][rows][cols / 16]")
+        _need(tensor_scales is None or (tensor_scales.dtype == torch.float32 and tensor_scales.is_contiguous() and
+                                        tensor_scales.shape == (self.n_experts,)),
+              "tensor_scales: contiguous fp32 [n_experts]")
+        _need(packed.is_cuda and packed.device == scales.device and
+              (tensor_scales is None or tensor_scales.device == packed.device),
+              "packed, scales and tensor_scales live on one CUDA device")
+        # (fixed: the descriptor holds their addresses)
+        self._packed, self._scales, self._tensor_scales = packed, scales, tensor_scales
+        self.desc = ctypes.pointer(Fp4ExpertsC(packed.data_ptr(), scales.data_ptr(),
+                                               None if tensor_scales is None else tensor_scales.data_ptr(),
+                                               self.n_experts, self.rows, self.cols))
+
+    packed = property(lambda self: self._packed)
+    scales = property(lambda self: self._scales)
+    tensor_scales = property(lambda self: self._tensor_scales)
+
+
 def _step(t, axis):
     """Elements between neighbours of an axis; 0 where there are none (the
     stride of an axis of one is arbitrary)."""
@@ -504,6 +550,123 @@ def msk_token_logprobs(logits, tokens=None, top=0, temperature=1.0, stream=None)
                                              temperature, top, lp, rk, entropy.data_ptr(), top_ids.data_ptr(),
                                              top_logprobs.data_ptr(), st), "msk_token_logprobs")
     return logprob, entropy, rank, top_ids, top_logprobs
+
+
+def msk_moe_route(logits, top_k, bias=None, stream=None):
+    """Each token's top_k experts and their gates: (experts int32, gates
+    fp32), both [tokens][top_k], from logits [tokens][n_experts] of any
+    floating type and row stride, with an fp32 bias [n_experts] added.  A
+    barred expert has a logit of -inf; ranks that find none are -1, gate 0."""
+    _need(logits.dim() == 2 and logits.dtype in _DTYPES and (logits.stride(1) == 1 or logits.shape[1] <= 1),
+          "logits: [tokens][n_experts], contiguous rows")
+    T, E = logits.shape
+    _need(1 <= top_k <= min(32, E), "top_k: 1 to 32, n_experts at most")
+    _need(bias is None or (bias.dtype == torch.float32 and bias.shape == (E,) and bias.is_contiguous()),
+          "bias: contiguous fp32 [n_experts]")
+    experts, gates = _empty(stream, (T, top_k), torch.int32), _empty(stream, (T, top_k), torch.float32)
+    st = _enqueue(stream, logits, experts) if bias is None else _enqueue(stream, logits, experts, bias)
+    _check(load_library().msk_moe_route(logits.data_ptr(), _DTYPES[logits.dtype], T, E, _step(logits, 0),
+                                        None if bias is None else bias.data_ptr(), top_k, experts.data_ptr(),
+                                        gates.data_ptr(), st), "msk_moe_route")
+    return experts, gates
+
+
+def msk_moe_sort(experts, n_experts, stream=None):
+    """The slots of `experts` (int32, any shape, usually [tokens][top_k])
+    sorted by expert: (offsets int32 [n_experts + 1], slots int32 [n], places
+    int32 of experts' shape).  An expert outside [0, n_experts) drops its
+    slot: its place is -1, and slots ends in as many -1."""
+    _need(experts.dtype == torch.int32 and experts.is_contiguous(), "experts: contiguous int32")
+    _need(1 <= n_experts <= 1024, "n_experts: 1 to 1024")
+    n = experts.numel()
+    offsets, slots = _empty(stream, n_experts + 1, torch.int32), _empty(stream, n, torch.int32)
+    places = _empty(stream, experts.shape, torch.int32)
+    st = _enqueue(stream, experts, offsets)
+    _check(load_library().msk_moe_sort(experts.data_ptr(), n, n_experts, offsets.data_ptr(), slots.data_ptr(),
+                                       places.data_ptr(), st), "msk_moe_sort")
+    return offsets, slots, places
+
+
+def msk_quantize_fp4(x, tensor_scale=1.0, out=None, stream=None):
+    """x ([rows][cols] of any floating type and row stride, cols a multiple of
+    16) in 4 bits, an Fp4Weight: a new one, or `out`, whose tensor's scale is
+    taken."""
+    _need(x.dim() == 2 and x.dtype in _DTYPES and x.stride(1) == 1 and x.shape[1] % 16 == 0 and x.shape[1] > 0,
+          "x: [rows][cols], contiguous rows of whole blocks of 16")
+    R, C = x.shape
+    if out is None:
+        out = Fp4Weight(_empty(stream, (R, C // 2), torch.uint8), _empty(stream, (R, C // 16), torch.uint8), tensor_scale)
+    _need(out.rows == R and out.cols == C, "out: [rows][cols] of x")
+    st = _enqueue(stream, x, out._packed)
+    _check(load_library().msk_quantize_fp4(x.data_ptr(), _DTYPES[x.dtype], R, C, _step(x, 0), out._tensor_scale,
+                                           out._packed.data_ptr(), out._scales.data_ptr(), st), "msk_quantize_fp4")
+    return out
+
+
+def msk_dequantize_fp4(w, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of an Fp4Weight, [rows][cols] of `dtype`, or into `out` (any
+    row stride)."""
+    if out is None:
+        _need(dtype in _DTYPES, "a floating type")
+        out = _empty(stream, (w.rows, w.cols), dtype)
+    _need(out.shape == (w.rows, w.cols) and out.dtype in _DTYPES and out.stride(1) == 1,
+          "out: [rows][cols], contiguous rows")
+    st = _enqueue(stream, out, w._packed)
+    _check(load_library().msk_dequantize_fp4(w._packed.data_ptr(), w._scales.data_ptr(), w._tensor_scale, w.rows, w.cols,
+                                             out.data_ptr(), _DTYPES[out.dtype], _step(out, 0), st), "msk_dequantize_fp4")
+    return out
+
+
+def msk_experts_fp4(x, experts, offsets, up=None, slots=None, top_k=1, out_dtype=torch.bfloat16, out=None, stream=None):
+    """Products of the 4-bit rows x (an Fp4Weight) with their experts'
+    matrices (Fp4Experts): places offsets[e] .. offsets[e + 1] - 1 are expert
+    e's, and place p takes row p of x, or with `slots` (int32 [n], as from
+    msk_moe_sort) row slots[p] // top_k.  With `up` (a second Fp4Experts of
+    the same size) the result is silu(x w^T) * (x up^T).  Returns
+    [n][experts.rows] of out_dtype, or `out` (any row stride); rows of places
+    behind the last expert's are not written."""
+    _need(offsets.dtype == torch.int32 and offsets.shape == (experts.n_experts + 1,) and offsets.is_contiguous(),
+          "offsets: contiguous int32 [n_experts + 1]")
+    _need(x.cols == experts.cols and x.cols % 64 == 0, "x has the weights' columns, a multiple of 64")
+    _need(up is None or (up.n_experts, up.rows, up.cols) == (experts.n_experts, experts.rows, experts.cols),
+          "up: of the other weights' size")
+    _need(slots is None or (slots.dtype == torch.int32 and slots.dim() == 1 and slots.is_contiguous() and top_k >= 1),
+          "slots: contiguous int32 [n], with top_k")
+    n = x.rows if slots is None else slots.shape[0]
+    if out is None:
+        _need(out_dtype in _DTYPES, "out_dtype: a floating type")
+        out = _empty(stream, (n, experts.rows), out_dtype)
+    _need(out.shape == (n, experts.rows) and out.dtype in _DTYPES and (out.stride(1) == 1 or experts.rows <= 1),
+          "out: [n][rows], contiguous rows")
+    given = [t for t in (x._packed, experts._packed, offsets, out, slots, None if up is None else up._packed)
+             if t is not None]
+    st = _enqueue(stream, *given)
+    _check(load_library().msk_experts_fp4(x.desc, None if slots is None else slots.data_ptr(), _int32(top_k, "top_k"), n,
+                                          offsets.data_ptr(), experts.desc, None if up is None else up.desc,
+                                          out.data_ptr(), _DTYPES[out.dtype], _step(out, 0), st), "msk_experts_fp4")
+    return out
+
+
+def msk_moe_combine(y, places, gates=None, out_dtype=None, out=None, stream=None):
+    """out[t] = sum over ranks of gates[t][r] * y[places[t][r]] (gates None:
+    1), y [rows][cols] of any floating type and row stride, places int32 and
+    gates fp32 [tokens][top_k]; a place outside y's rows is a dropped slot.
+    Returns [tokens][cols] of out_dtype (y's unless given), or `out`."""
+    _need(y.dim() == 2 and y.dtype in _DTYPES and (y.stride(1) == 1 or y.shape[1] <= 1), "y: [rows][cols], contiguous rows")
+    _need(places.dim() == 2 and places.dtype == torch.int32 and places.is_contiguous() and places.shape[1] >= 1,
+          "places: contiguous int32 [tokens][top_k]")
+    _need(gates is None or (gates.dtype == torch.float32 and gates.shape == places.shape and gates.is_contiguous()),
+          "gates: contiguous fp32 [tokens][top_k]")
+    (T, k), C = places.shape, y.shape[1]
+    if out is None:
+        _need(out_dtype is None or out_dtype in _DTYPES, "out_dtype: a floating type")
+        out = _empty(stream, (T, C), y.dtype if out_dtype is None else out_dtype)
+    _need(out.shape == (T, C) and out.dtype in _DTYPES and (out.stride(1) == 1 or C <= 1), "out: [tokens][cols], contiguous rows")
+    st = _enqueue(stream, y, places, out) if gates is None else _enqueue(stream, y, places, out, gates)
+    _check(load_library().msk_moe_combine(y.data_ptr(), _DTYPES[y.dtype], y.shape[0], _step(y, 0), places.data_ptr(),
+                                          None if gates is None else gates.data_ptr(), T, k, C, out.data_ptr(),
+                                          _DTYPES[out.dtype], _step(out, 0), st), "msk_moe_combine")
+    return out
 
 
 # ----------------------------------------------------------------------------

@@ -9,6 +9,7 @@
 
 #include "msk_internal.h"
 #include "msk_ops.cuh"
+#include "msk_quant.cuh"
 #include "msk_tc.cuh"
 
 namespace msk {
@@ -28,42 +29,6 @@ struct Kv4Rows {
   int Hkv, max_seq, tokens, pos0;
   float k_scale, v_scale;
 };
-
-// 16 consecutive elements of type DT as floats.
-template <int DT>
-__device__ __forceinline__ void load16(const void* base, long long off, float (&x)[16]) {
-  if (DT == MSK_FP32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = __ldg(p + i);
-      x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
-    }
-  } else {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 u = __ldg(p + i);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack16(w[j], DT == MSK_FP16);
-        x[8 * i + 2 * j] = f.x, x[8 * i + 2 * j + 1] = f.y;
-      }
-    }
-  }
-}
-
-// Two -x / d rounded to nearest (my: two rounded reciprocals of d, negative;
-// quotients and remainders within the normal range): Markstein's correction of
-// x my by its remainder (IBM J. Res. Dev. 34, 1990).  The codes depend on the
-// quotient's last bit where it lies half way between two of them.  The negative
-// quotient, because a remainder of 0 is +0: times my it is -0, which leaves the
-// sign of a zero alone, and +0, times y, would not.
-__device__ __forceinline__ void minus_quotients(float& x0, float& x1, unsigned long long d, unsigned long long my) {
-  const unsigned long long x = pair(x0, x1), q = mul2(x, my);
-  unpair(fma2(fma2(q, d, x), my, q), x0, x1);
-}
 
 // Both kernels: blockIdx.y is K's and then V's heads, a block takes `per`
 // consecutive pieces of its head's rows.
@@ -96,54 +61,15 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4Rows a) {
   if (a.pos0_dev) pos0 = max(0, min(*a.pos0_dev, a.max_seq - a.tokens));
   const RowsAt w = rows_at<NP>(a, pos0, 256);
   if (w.piece >= w.n) return;
-  const float ts = w.is_v ? a.v_scale : a.k_scale, yts = __frcp_rn(ts);
-  const unsigned long long ts2 = pair(ts, ts), myts2 = pair(-yts, -yts);
-  const bool plain = ts > 1e-18f && ts < 1e18f;
+  const float ts = w.is_v ? a.v_scale : a.k_scale;
   const void* src = w.is_v ? a.v : a.k;
   const long long from = w.piece / NP * a.token_stride + w.h * a.head_stride + w.piece % NP * 16;
   float x[16];
   load16<DT>(src, from, x);
-  float amax = 0.f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(x[j]));
-  const bool whole = ts == 1.f;
-  if (!whole) {  // x becomes -x / ts
-    if (plain && amax < 1e18f) {  // (smaller quotients than normal ones leave codes of 0)
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) minus_quotients(x[j], x[j + 1], ts2, myts2);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = __fdiv_rn(x[j], -ts);
-    }
-    amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(x[j]));
-  }
-  // amax / 6 (what is beyond 448 saturates)
-  const float y6 = 1.f / 6.f, am = fminf(amax, 1e6f), q6 = am * y6;
-  const uint32_t sc = f32_to_e4m3(fmaf(fmaf(-q6, 6.f, am), y6, q6));
-  const float dec = e4m3_to_f32(sc);
-  uint32_t c[2] = {0u, 0u};
-  if (amax > 2688.f) {  // saturates, with infinities perhaps
-    const float d = whole ? dec : -dec;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      c[j >> 2] |= f32x2_to_e2m1x2(__fdiv_rn(x[2 * j], d), __fdiv_rn(x[2 * j + 1], d)) << (8 * (j & 3));
-  } else if (dec > 0.f) {
-    const float y = __frcp_rn(dec);
-    auto codes = [&](auto negate) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float u = x[2 * j], v = x[2 * j + 1];
-        minus_quotients(u, v, pair(dec, dec), pair(-y, -y));
-        c[j >> 2] |= (negate() ? f32x2_to_e2m1x2(-u, -v) : f32x2_to_e2m1x2(u, v)) << (8 * (j & 3));
-      }
-    };
-    if (whole) codes(std::true_type());
-    else codes(std::false_type());  // (two negative quotients)
-  }
+  uint32_t sc;
+  const uint2 c = quantise16(x, ts, sc);
   const long long at = w.at + w.piece;  // (rows of a head are consecutive)
-  *reinterpret_cast<uint2*>(a.codes + at * 8) = make_uint2(c[0], c[1]);
+  *reinterpret_cast<uint2*>(a.codes + at * 8) = c;
   a.scales[at] = (uint8_t)sc;
 }
 

@@ -48,13 +48,6 @@ struct Lin4 {
   int ts_exp;  // ... and the power of two that it is multiplied with
 };
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
 struct Bars {  // mbarriers of a block
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t afull[kTeams][kABufs], aempty[kTeams][kABufs];
@@ -434,17 +427,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear4_kernel(const __grid_const
   }
 }
 
-// A row-major matrix of bytes or 16-bit words, `pitch` bytes between rows, in
-// boxes of box_rows x box_cols; what lies outside reads as zero.
-bool matrix_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, long long rows, long long cols, long long pitch,
-                int box_rows, int box_cols, CUtensorMapSwizzle swizzle) {
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)pitch};
-  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, es[2] = {1, 1};
-  return tensor_map_encoder() != nullptr &&
-         tensor_map_encoder()(map, type, 2, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // What the kernel's launches go by, looked up once a device: clusters of each
 // size that run at a time.
 struct Setup {
@@ -507,7 +489,8 @@ msk_status launch_linear(Lin4& a, const void* x, long long x_stride, cudaStream_
 
 }  // namespace
 
-cudaError_t kv4_error(uint32_t* e);  // (msk_kv4.cu)
+cudaError_t kv4_error(uint32_t* e);       // (msk_kv4.cu)
+cudaError_t experts4_error(uint32_t* e);  // (msk_experts4.cu)
 
 cudaError_t linear4_error(uint32_t* e) {
   cudaError_t r = cudaMemcpyFromSymbol(e, g_error, sizeof(*e));
@@ -557,7 +540,7 @@ extern "C" msk_status msk_linear_fp4(const void* x, int32_t x_dtype, int64_t x_s
 
 extern "C" msk_status msk_ops_check(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MSK_ERR_CUDA;
-  uint32_t e = 0, f = 0;
-  if (linear4_error(&e) != cudaSuccess || kv4_error(&f) != cudaSuccess) return MSK_ERR_CUDA;
-  return e || f ? MSK_ERR_TIMEOUT : MSK_OK;
+  uint32_t e = 0, f = 0, g = 0;
+  if (linear4_error(&e) != cudaSuccess || kv4_error(&f) != cudaSuccess || experts4_error(&g) != cudaSuccess) return MSK_ERR_CUDA;
+  return e || f || g ? MSK_ERR_TIMEOUT : MSK_OK;
 }

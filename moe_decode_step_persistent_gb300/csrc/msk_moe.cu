@@ -1,0 +1,444 @@
+// A prompt's tokens to their experts and back: the router's choice, the slots
+// sorted by expert, and the experts' outputs weighted and summed at their tokens.
+#include <algorithm>
+#include <atomic>
+
+#include "msk_internal.h"
+#include "msk_ops.cuh"
+
+namespace msk {
+namespace {
+
+// ---------------------------------------------------------------------------
+// route: the top_k greatest of logits + bias, and their softmax
+// ---------------------------------------------------------------------------
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 32;
+
+struct Route {
+  const void* logits;
+  const float* bias;
+  int32_t* experts;
+  float* gates;
+  long long tokens, ld;
+  int E, top_k;
+};
+
+// An fp32 number's bits in an order that unsigned comparison follows, and back.
+// Two zeros of either sign are one (x + 0 is +0), a NaN is below everything.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  if (x != x) return 0u;
+  return b >> 31 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float ordered_value(uint32_t k) {
+  return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k);
+}
+constexpr uint32_t kMinusInf = 0x007FFFFFu;  // ordered(-inf): an expert up to here is barred
+
+template <int DT>
+__device__ __forceinline__ float element(const void* p, long long i) {
+  if (DT == MSK_FP32) return __ldg(static_cast<const float*>(p) + i);
+  const uint16_t v = __ldg(static_cast<const uint16_t*>(p) + i);
+  return DT == MSK_FP16 ? __half2float(__ushort_as_half(v)) : __uint_as_float((uint32_t)v << 16);
+}
+
+// A warp a token, C candidates a lane: lane l's are experts C l .. C l + C - 1,
+// so that of equal logits the lowest lane, and in a lane the first, is the lowest
+// index.  A round takes the warp's greatest key; only its lane looks for its next.
+template <int DT, int C, bool VEC>
+__global__ void __launch_bounds__(128) route_kernel(const Route a) {
+  const int lane = threadIdx.x & 31;
+  const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  grid_dep_wait();
+  grid_dep_launch();
+  if (t >= a.tokens) return;
+  uint32_t key[C];
+  const int e0 = lane * C;
+  if (VEC && e0 + C <= a.E) {
+    constexpr int W = C * (DT == MSK_FP32 ? 4 : 2) / 4;  // 32-bit words
+    uint32_t w[W];
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.logits) + (t * a.ld + e0) * (DT == MSK_FP32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const uint4 u = __ldg(p + i);
+      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      float x;
+      if (DT == MSK_FP32) x = __uint_as_float(w[j % W]);
+      else {
+        const float2 f = unpack16(w[j / 2], DT == MSK_FP16);
+        x = j & 1 ? f.y : f.x;
+      }
+      key[j] = ordered(a.bias != nullptr ? x + __ldg(a.bias + e0 + j) : x);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      key[j] = 0u;
+      if (e0 + j < a.E) {
+        const float x = element<DT>(a.logits, t * a.ld + e0 + j);
+        key[j] = ordered(a.bias != nullptr ? x + __ldg(a.bias + e0 + j) : x);
+      }
+    }
+  }
+  uint32_t best = key[0];
+#pragma unroll
+  for (int j = 1; j < C; ++j) best = max(best, key[j]);
+  uint32_t mine = 0u;  // lane r: the key of rank r
+  int chosen = -1;
+  for (int r = 0; r < a.top_k; ++r) {
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+    if (m <= kMinusInf) break;  // (uniform: none is left)
+    const int win = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
+    int at = 0;
+    if (lane == win) {
+      at = C;
+#pragma unroll
+      for (int j = C - 1; j >= 0; --j)
+        if (key[j] == m) at = j;
+      best = 0u;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        if (j == at) key[j] = 0u;
+        best = max(best, key[j]);
+      }
+      at += e0;
+    }
+    at = __shfl_sync(0xFFFFFFFFu, at, win);
+    if (lane == r) mine = m, chosen = at;
+  }
+  // the softmax of the chosen, in their order of rank
+  const float v = ordered_value(mine), v0 = __shfl_sync(0xFFFFFFFFu, v, 0);
+  float e = chosen >= 0 ? expf(v - v0) : 0.f, sum = e;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane < a.top_k) {
+    a.experts[t * a.top_k + lane] = chosen;
+    a.gates[t * a.top_k + lane] = chosen >= 0 ? e / sum : 0.f;
+  }
+}
+
+template <int DT, int C>
+cudaError_t launch_route(const Route& a, bool aligned, cudaStream_t st) {
+  const OpsLaunch l(dim3((unsigned)((a.tokens + 3) / 4)), 128, 0, st);
+  if (C * (DT == MSK_FP32 ? 4 : 2) % 16 == 0 && aligned)
+    return cudaLaunchKernelEx(&l.cfg, route_kernel<DT, C, C * (DT == MSK_FP32 ? 4 : 2) % 16 == 0>, a);
+  return cudaLaunchKernelEx(&l.cfg, route_kernel<DT, C, false>, a);
+}
+
+template <int DT>
+cudaError_t launch_route(const Route& a, bool aligned, cudaStream_t st) {
+  const int c = (a.E + 31) / 32;
+  return c <= 2    ? launch_route<DT, 2>(a, aligned, st)
+         : c <= 4  ? launch_route<DT, 4>(a, aligned, st)
+         : c <= 8  ? launch_route<DT, 8>(a, aligned, st)
+         : c <= 16 ? launch_route<DT, 16>(a, aligned, st)
+                   : launch_route<DT, 32>(a, aligned, st);
+}
+
+// ---------------------------------------------------------------------------
+// sort: a stable counting sort of the slots by expert
+// ---------------------------------------------------------------------------
+
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortCluster = 16;
+
+struct Sort {
+  const int32_t* experts;
+  int32_t *offsets, *slots, *places;
+  long long n;
+  long long per_warp;  // slots of a warp, a multiple of 32
+  int E, blocks;
+};
+
+// One cluster (of one block for few slots) sorts everything in one launch: the
+// slots are split into runs, one a warp, in their order.  Each warp counts its
+// run's experts, in shared memory, the lanes with the same expert as one; the
+// block sums its warps' counts, the cluster its blocks', and the experts' are
+// scanned.  Then each warp goes through its run again with its first place of
+// each expert.  No atomics: the places do not depend on an order of arrival.
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const Sort a) {
+  extern __shared__ __align__(16) int32_t sort_smem[];
+  int32_t* count = sort_smem;                      // [warps][E], then each warp's next place
+  int32_t* total = count + kSortWarps * a.E;       // [E]: this block's (the cluster reads it)
+  int32_t* base = total + a.E;                     // [E]: first place of this block
+  __shared__ int32_t warp_sum[kSortWarps];
+  __shared__ int32_t all;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x;
+  for (int i = tid; i < kSortWarps * a.E; i += kSortThreads) count[i] = 0;
+  grid_dep_wait();
+  grid_dep_launch();
+  __syncthreads();
+  const long long s0 = ((long long)rank * kSortWarps + warp) * a.per_warp, s1 = min(a.n, s0 + a.per_warp);
+  int32_t* mine = count + warp * a.E;
+  auto expert = [&](long long s) {
+    const int e = s < s1 ? __ldg(a.experts + s) : -1;
+    return e >= 0 && e < a.E ? e : -1;
+  };
+  for (long long s = s0; s < s1; s += 32) {
+    const int e = expert(s + lane);
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    if (e >= 0 && (same & ((1u << lane) - 1)) == 0) mine[e] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = tid; e < a.E; e += kSortThreads) {
+    int32_t sum = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int32_t c = count[w * a.E + e];
+      count[w * a.E + e] = sum;
+      sum += c;
+    }
+    total[e] = sum;
+  }
+  if (a.blocks > 1) cluster_sync();
+  else __syncthreads();
+  // (E <= the threads of a block: thread e has expert e)
+  int32_t before = 0, sum = 0;
+  if (tid < a.E) {
+    if (a.blocks > 1) {
+      const uint32_t at = smem_u32(total + tid);
+      for (int b = 0; b < a.blocks; ++b) {
+        int32_t c;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(mapa(at, b)) : "memory");
+        if (b < rank) before += c;
+        sum += c;
+      }
+    } else {
+      sum = total[tid];
+    }
+  }
+  int32_t scan = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) warp_sum[warp] = scan;
+  __syncthreads();
+  if (warp == 0) {
+    int32_t v = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
+    }
+    warp_sum[lane] = v;
+    if (lane == 31) all = v;
+  }
+  __syncthreads();
+  scan += warp > 0 ? warp_sum[warp - 1] : 0;
+  if (tid < a.E) {
+    base[tid] = scan - sum + before;
+    if (rank == 0) {
+      a.offsets[tid + 1] = scan;
+      if (tid == 0) a.offsets[0] = 0;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < kSortWarps * a.E; i += kSortThreads) count[i] += base[i % a.E];
+  __syncthreads();
+  for (long long s = s0; s < s1; s += 32) {
+    const int e = expert(s + lane);
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e), less = same & ((1u << lane) - 1);
+    int32_t place = -1;
+    if (e >= 0) place = mine[e] + __popc(less);
+    __syncwarp();
+    if (e >= 0 && less == 0) mine[e] = place + __popc(same);
+    __syncwarp();
+    if (s + lane < s1) {
+      a.places[s + lane] = place;
+      if (place >= 0) a.slots[place] = (int32_t)(s + lane);
+    }
+  }
+  for (long long p = all + (long long)rank * kSortThreads + tid; p < a.n; p += (long long)a.blocks * kSortThreads) a.slots[p] = -1;
+  if (a.blocks > 1) cluster_sync();  // (its totals have been read)
+}
+
+// ---------------------------------------------------------------------------
+// combine: out[t] = sum over ranks of gate * y[place]
+// ---------------------------------------------------------------------------
+
+struct Combine {
+  const void* y;
+  const int32_t* places;
+  const float* gates;
+  void* out;
+  long long tokens, y_rows, y_stride, out_stride, pieces;  // pieces of a token
+  int cols, top_k;
+};
+
+// A thread has 16 bytes of a token's columns (V elements; one element where
+// rows are not aligned to 16 bytes), its ranks' rows all loaded before they are
+// summed, eight at a time.  Sums in fp32, by rank.
+template <int DT, int ODT, bool VEC>
+__global__ void __launch_bounds__(256) combine_kernel(const Combine a) {
+  constexpr int S = DT == MSK_FP32 ? 4 : 2, V = VEC ? 16 / S : 1, U = 8;
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long t = i / a.pieces;
+  if (t >= a.tokens) return;
+  const int c = (int)(i - t * a.pieces) * V;
+  float sum[V] = {};
+  for (int r0 = 0; r0 < a.top_k; r0 += U) {
+    uint4 w[U];
+    float g[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long slot = t * a.top_k + r0 + u;
+      const int p = r0 + u < a.top_k ? __ldg(a.places + slot) : -1;
+      const bool in = p >= 0 && p < a.y_rows;  // (a dropped slot's row is not read)
+      g[u] = in && a.gates != nullptr ? __ldg(a.gates + slot) : 1.f;
+      w[u] = make_uint4(0, 0, 0, 0);
+      const long long at = p * a.y_stride + c;
+      if (!in) g[u] = 0.f;
+      else if (VEC) w[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.y) + at * S));
+      else w[u].x = __float_as_uint(element<DT>(a.y, at));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      if (!VEC || DT == MSK_FP32) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] = fmaf(g[u], __uint_as_float(x[j]), sum[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float2 f = unpack16(x[j], DT == MSK_FP16);
+          sum[2 * j] = fmaf(g[u], f.x, sum[2 * j]), sum[2 * j + 1 < V ? 2 * j + 1 : 0] = fmaf(g[u], f.y, sum[2 * j + 1 < V ? 2 * j + 1 : 0]);
+        }
+      }
+    }
+  }
+  const long long o = t * a.out_stride + c;
+  if (VEC) {
+    if (ODT == MSK_FP32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j) p[j] = make_float4(sum[4 * j % V], sum[(4 * j + 1) % V], sum[(4 * j + 2) % V], sum[(4 * j + 3) % V]);
+    } else {
+      uint32_t x[V / 2 ? V / 2 : 1];
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) x[j] = pack16(sum[2 * j], sum[(2 * j + 1) % V], ODT == MSK_FP16);
+      uint16_t* p = static_cast<uint16_t*>(a.out) + o;
+      if (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1 % (V / 2 ? V / 2 : 1)], x[2 % (V / 2 ? V / 2 : 1)], x[3 % (V / 2 ? V / 2 : 1)]);
+      else *reinterpret_cast<uint2*>(p) = make_uint2(x[0], x[1 % (V / 2 ? V / 2 : 1)]);
+    }
+  } else {
+    if (ODT == MSK_FP32) static_cast<float*>(a.out)[o] = sum[0];
+    else if (ODT == MSK_FP16) static_cast<__half*>(a.out)[o] = __float2half_rn(sum[0]);
+    else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(sum[0]);
+  }
+}
+
+template <int DT, int ODT>
+cudaError_t launch_combine(Combine& a, cudaStream_t st) {
+  constexpr int S = DT == MSK_FP32 ? 4 : 2, O = ODT == MSK_FP32 ? 4 : 2, V = 16 / S;
+  // (an output piece has V elements of the output's type: 8 to 32 bytes)
+  constexpr int OA = V * O < 16 ? V * O : 16;
+  const bool vec = a.cols % V == 0 && ops_aligned16(a.y) && a.y_stride % V == 0 && reinterpret_cast<uintptr_t>(a.out) % OA == 0 &&
+                   a.out_stride * O % OA == 0;
+  a.pieces = vec ? a.cols / V : a.cols;
+  const long long blocks = (a.tokens * a.pieces + 255) / 256;
+  const OpsLaunch l(dim3((unsigned)blocks), 256, 0, st);
+  return cudaLaunchKernelEx(&l.cfg, vec ? combine_kernel<DT, ODT, true> : combine_kernel<DT, ODT, false>, a);
+}
+
+template <int DT>
+cudaError_t launch_combine(Combine& a, int odt, cudaStream_t st) {
+  return odt == MSK_BF16   ? launch_combine<DT, MSK_BF16>(a, st)
+         : odt == MSK_FP16 ? launch_combine<DT, MSK_FP16>(a, st)
+                           : launch_combine<DT, MSK_FP32>(a, st);
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+constexpr long long kMaxSlots = 1ll << 30;  // places are 32-bit
+
+}  // namespace
+}  // namespace msk
+
+using namespace msk;
+
+extern "C" msk_status msk_moe_route(const void* logits, int32_t dtype, int64_t tokens, int32_t n_experts, int64_t ld,
+                                    const float* bias, int32_t top_k, int32_t* experts, float* gates, void* stream) {
+  if (!dtype_ok(dtype) || tokens < 0) return MSK_ERR_INVALID_ARG;
+  if (n_experts < 1 || n_experts > kMaxExperts || top_k < 1 || top_k > kMaxTopK || top_k > n_experts) return MSK_ERR_SHAPE;
+  if (tokens > kMaxSlots / top_k) return MSK_ERR_SHAPE;
+  if (tokens == 0) return MSK_OK;
+  if (logits == nullptr || experts == nullptr || gates == nullptr || (tokens > 1 && ld < n_experts)) return MSK_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) % dtype_bytes(dtype) || !aligned4(bias) || !aligned4(experts) || !aligned4(gates))
+    return MSK_ERR_ALIGNMENT;
+  int nsm = 0;
+  const msk_status s = ops_device(&nsm);
+  if (s != MSK_OK) return s;
+  Route a{};
+  a.logits = logits, a.bias = bias, a.experts = experts, a.gates = gates;
+  a.tokens = tokens, a.ld = ld, a.E = n_experts, a.top_k = top_k;
+  const bool aligned = ops_aligned16(logits) && (tokens == 1 || ld * dtype_bytes(dtype) % 16 == 0);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == MSK_BF16   ? launch_route<MSK_BF16>(a, aligned, st)
+                        : dtype == MSK_FP16 ? launch_route<MSK_FP16>(a, aligned, st)
+                                            : launch_route<MSK_FP32>(a, aligned, st);
+  return e == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
+}
+
+extern "C" msk_status msk_moe_sort(const int32_t* experts, int64_t n, int32_t n_experts, int32_t* offsets, int32_t* slots,
+                                   int32_t* places, void* stream) {
+  if (n < 0) return MSK_ERR_INVALID_ARG;
+  if (n_experts < 1 || n_experts > kMaxExperts || n > kMaxSlots) return MSK_ERR_SHAPE;
+  if (offsets == nullptr || (n > 0 && (experts == nullptr || slots == nullptr || places == nullptr))) return MSK_ERR_INVALID_ARG;
+  if (!aligned4(experts) || !aligned4(offsets) || !aligned4(slots) || !aligned4(places)) return MSK_ERR_ALIGNMENT;
+  int nsm = 0;
+  const msk_status s = ops_device(&nsm);
+  if (s != MSK_OK) return s;
+  Sort a{};
+  a.experts = experts, a.offsets = offsets, a.slots = slots, a.places = places, a.n = n, a.E = n_experts;
+  // (a block goes through 4096 slots, 4 steps a warp, in the time that a cluster's barriers take)
+  a.blocks = n <= 4096 ? 1 : n <= 8 * 4096 ? 8 : kSortCluster;
+  const long long warps = (long long)a.blocks * kSortWarps;
+  a.per_warp = ((n + warps - 1) / warps + 31) / 32 * 32;
+  const int smem = (kSortWarps + 2) * n_experts * 4;
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSK_ERR_CUDA;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSortWarps + 2) * kMaxExperts * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return MSK_ERR_CUDA;
+    ready[dev].store(true, std::memory_order_release);
+  }
+  const OpsLaunch l(dim3((unsigned)a.blocks), kSortThreads, smem, static_cast<cudaStream_t>(stream), a.blocks);
+  return cudaLaunchKernelEx(&l.cfg, sort_kernel, a) == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
+}
+
+extern "C" msk_status msk_moe_combine(const void* y, int32_t y_dtype, int64_t y_rows, int64_t y_stride, const int32_t* places,
+                                      const float* gates, int64_t tokens, int32_t top_k, int64_t cols, void* out,
+                                      int32_t out_dtype, int64_t out_stride, void* stream) {
+  if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype) || tokens < 0 || y_rows < 0) return MSK_ERR_INVALID_ARG;
+  if (top_k < 1 || cols < 0 || cols > (1ll << 30) || tokens > kMaxSlots / top_k || y_rows > kMaxSlots) return MSK_ERR_SHAPE;
+  if (tokens * cols >= (1ll << 38)) return MSK_ERR_SHAPE;  // (the grid)
+  if (tokens == 0 || cols == 0) return MSK_OK;
+  if ((y == nullptr && y_rows > 0) || places == nullptr || out == nullptr) return MSK_ERR_INVALID_ARG;
+  if ((y_rows > 1 && y_stride < cols) || (tokens > 1 && out_stride < cols)) return MSK_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(y) % dtype_bytes(y_dtype) || reinterpret_cast<uintptr_t>(out) % dtype_bytes(out_dtype) ||
+      !aligned4(places) || !aligned4(gates))
+    return MSK_ERR_ALIGNMENT;
+  int nsm = 0;
+  const msk_status s = ops_device(&nsm);
+  if (s != MSK_OK) return s;
+  Combine a{};
+  a.y = y, a.places = places, a.gates = gates, a.out = out;
+  a.tokens = tokens, a.y_rows = y_rows, a.y_stride = y_rows > 1 ? y_stride : 0, a.out_stride = tokens > 1 ? out_stride : 0;
+  a.cols = (int)cols, a.top_k = top_k;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = y_dtype == MSK_BF16   ? launch_combine<MSK_BF16>(a, out_dtype, st)
+                        : y_dtype == MSK_FP16 ? launch_combine<MSK_FP16>(a, out_dtype, st)
+                                              : launch_combine<MSK_FP32>(a, out_dtype, st);
+  return e == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
+}

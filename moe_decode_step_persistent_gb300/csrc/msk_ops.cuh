@@ -13,6 +13,17 @@ namespace msk {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // (msk_api.cu)
 
+// A row-major matrix of bytes or 16-bit words, `pitch` bytes between rows, in
+// boxes of box_rows x box_cols; what lies outside reads as zero.
+inline bool matrix_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, long long rows, long long cols, long long pitch,
+                int box_rows, int box_cols, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)pitch};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return tensor_map_encoder() != nullptr &&
+         tensor_map_encoder()(map, type, 2, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline bool ops_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int dtype_bytes(int32_t t) { return t == MSK_FP32 ? 4 : 2; }
 inline bool dtype_ok(int32_t t) { return t == MSK_BF16 || t == MSK_FP16 || t == MSK_FP32; }
@@ -56,6 +67,14 @@ struct OpsLaunch {
 // The SM count the workspace sizes are made for when there is no device to
 // ask; kernels never use more blocks than a workspace has room for.
 constexpr int kOpsSms = 152;
+
+// A box of a 2-D tensor map, `x` and `y` its first column and row.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);

@@ -1,0 +1,484 @@
+"""The operators of a whole prompt's experts on the GPU, against their
+definitions in 64 bits (the quantiser against the oracle's, bit for bit).
+
+Tolerances, from the arithmetic.  h(t) = eps(t) / 2 is half a rounding step of
+the output's type.
+  route: a gate is e^(v - v0) over a sum of such.  v - v0 is rounded once
+    (2^-24 of it), the exponential is off by 2^-22, the sum of k by k 2^-24, the
+    quotient by 2^-24: relative 2 (2^-22 + max |v - v0| 2^-24) + (k + 1) 2^-24.
+  products: fp32 sums of K exact products: (K + 64) 2^-23 sum |x w|, and the
+    tensors' scales: three roundings of 2^-24.
+  SwiGLU: s = g sigma(g), |ds / dg| <= 1.1; the exponential, sum, quotient and
+    two products add 2^-20 of s u.
+  combine: k fused products and sums: k 2^-23 sum |gate y|."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import formats as F
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def half_step(t):
+    return torch.finfo(t).eps / 2
+
+
+def tiny(t):
+    """Half a step among the type's subnormal numbers."""
+    return torch.finfo(t).smallest_normal * half_step(t)
+
+
+@pytest.fixture(scope="module")
+def M():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import moe_decode_step_persistent_gb300 as mod
+    mod.load_library()
+    return mod
+
+
+@pytest.fixture(autouse=True)
+def no_wait_ran_out(M):
+    yield
+    M.msk_ops_check()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def randn(seed, *shape):
+    return torch.randn(*shape, generator=gen(seed))
+
+
+def values64(codes, scales, ts=1.0):
+    cols = codes.shape[-1] * 2
+    v = F.nvfp4_dequant(codes.reshape(-1, cols // 2).numpy(), scales.reshape(-1, cols // 16).numpy(), 1.0, cols)
+    return torch.from_numpy(v).reshape(*codes.shape[:-1], cols) * float(np.float32(ts))
+
+
+def random_fp4(seed, *shape):
+    """Codes and scales as a quantiser makes them."""
+    c, s, _ = F.q4(randn(seed, *shape).numpy())
+    c = torch.from_numpy(c)
+    return c[..., 0::2] | (c[..., 1::2] << 4), torch.from_numpy(s)
+
+
+def strided(t, extra):
+    """t's values in rows `extra` elements further apart."""
+    if extra == 0:
+        return t.cuda()
+    wide = torch.full((t.shape[0], t.shape[1] + extra), 7.0, dtype=t.dtype, device="cuda")
+    wide[:, :t.shape[1]] = t.cuda()
+    return wide[:, :t.shape[1]]
+
+
+# ----------------------------------------------------------------------------
+# route
+# ----------------------------------------------------------------------------
+
+
+def route_ref(logits, bias, k):
+    """(experts, gates in 64 bits) by a loop over the ranks."""
+    x = logits.float()
+    if bias is not None:
+        x = x + bias
+    x = torch.where(torch.isnan(x), -math.inf, x)
+    T, E = x.shape
+    experts = torch.full((T, k), -1, dtype=torch.int32)
+    vals = torch.full((T, k), -math.inf, dtype=torch.float64)
+    for t in range(T):
+        left = x[t].tolist()
+        for r in range(k):
+            best = max(range(E), key=lambda e: (left[e], -e))
+            if left[best] == -math.inf:
+                break
+            experts[t, r], vals[t, r] = best, left[best]
+            left[best] = -math.inf
+    gates = torch.softmax(vals, -1)
+    return experts, torch.where(experts >= 0, gates, 0.0), vals
+
+
+@pytest.mark.parametrize("tokens,E,k,dtype,bias,extra", [
+    (1, 16, 2, "fp32", False, 0), (16, 256, 8, "fp32", True, 0), (37, 256, 8, "bf16", True, 0), (5, 1, 1, "fp32", True, 3),
+    (9, 60, 4, "fp16", False, 0), (33, 1024, 32, "bf16", True, 8), (7, 1000, 9, "fp32", False, 1), (130, 128, 5, "fp32", True, 4),
+    (3, 33, 32, "bf16", False, 1), (64, 512, 8, "fp16", True, 8), (6, 200, 8, "fp32", True, 0)])
+def test_route(M, tokens, E, k, dtype, bias, extra):
+    logits = (randn(1, tokens, E) * 2).to(DT[dtype])
+    if tokens > 4 and E > 8:
+        logits[1] = 0.5                                 # all alike: the lowest indices
+        logits[2, ::3] = -math.inf                      # barred experts
+        logits[3] = -math.inf                           # none left
+        logits[4] = -math.inf                           # fewer than k left, a NaN among the barred
+        logits[4, E // 2], logits[4, 3], logits[4, 1] = 1.25, -2.0, math.nan
+        logits[0, 5], logits[0, 2] = 0.0, -0.0          # two zeros are alike
+    b = randn(2, E) if bias else None
+    if bias:
+        b[0] = -math.inf
+    want, gates, vals = route_ref(logits, b, k)
+    got_e, got_g = M.msk_moe_route(strided(logits, extra), k, bias=None if b is None else b.cuda())
+    assert torch.equal(got_e.cpu(), want)
+    spread = torch.where(want >= 0, vals[:, :1] - vals, 0.0).amax()
+    tol = 2 * (2.0 ** -22 + float(spread) * 2.0 ** -24) + (k + 1) * 2.0 ** -24
+    assert ((got_g.cpu().double() - gates).abs() <= tol * gates + 1e-37).all()
+
+
+def test_route_of_an_infinite_logit(M):
+    logits = randn(3, 4, 64)
+    logits[2, 9] = math.inf
+    e, g = M.msk_moe_route(logits.cuda(), 4)
+    want, _, _ = route_ref(logits, None, 4)
+    assert torch.equal(e.cpu(), want)
+    assert torch.isnan(g[2]).all() and not torch.isnan(g[[0, 1, 3]]).any()
+
+
+# ----------------------------------------------------------------------------
+# sort
+# ----------------------------------------------------------------------------
+
+
+def sort_ref(experts, E):
+    flat = experts.flatten().tolist()
+    order = sorted((s for s in range(len(flat)) if 0 <= flat[s] < E), key=lambda s: (flat[s], s))
+    count = np.bincount([flat[s] for s in order], minlength=E) if order else np.zeros(E, int)
+    offsets = np.concatenate(([0], np.cumsum(count)))
+    places = np.full(len(flat), -1)
+    places[order] = np.arange(len(order))
+    return offsets, np.array(order + [-1] * (len(flat) - len(order))), places.reshape(experts.shape)
+
+
+@pytest.mark.parametrize("tokens,k,E", [(0, 8, 4), (1, 1, 1), (1, 8, 256), (16, 8, 256), (31, 5, 7), (512, 8, 60), (513, 8, 1024),
+                                        (4096, 1, 256), (4097, 8, 256), (8192, 5, 1000), (20000, 8, 3)])
+@pytest.mark.parametrize("kind", ["mixed", "one", "dropped"])
+def test_sort(M, tokens, k, E, kind):
+    g = gen(tokens * 7 + E)
+    e = torch.randint(-2, E + 2, (tokens, k), generator=g, dtype=torch.int32)  # (some outside: dropped)
+    if kind == "one":
+        e.fill_(E - 1)
+    elif kind == "dropped":
+        e.fill_(-1)
+    offsets, slots, places = (x.cpu().numpy() for x in M.msk_moe_sort(e.cuda(), E))
+    want = sort_ref(e, E)
+    assert np.array_equal(offsets, want[0]) and np.array_equal(slots, want[1]) and np.array_equal(places, want[2])
+
+
+# ----------------------------------------------------------------------------
+# rows in and out
+# ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("rows,cols,dtype,ts,extra", [
+    (1, 16, "bf16", 1.0, 0), (3, 48, "fp16", 1.0, 0), (16, 2048, "bf16", 1.0, 8), (130, 64, "fp32", 0.37, 4), (33, 112, "bf16", 2.5, 16),
+    (5, 4096, "fp32", 4.4e-5, 0), (7, 1040, "fp16", 0.01, 8), (2, 32, "fp32", 1e-30, 0), (2, 32, "fp32", 3e30, 0)])
+def test_quantize_and_back(M, rows, cols, dtype, ts, extra):
+    x = randn(1, rows, cols)
+    x[:, ::5] *= 40.0
+    x[rows // 2, :16] = 0.0             # a block of zeros
+    x[0, -16:] = 3e-4                   # a scale among E4M3's subnormals
+    x[-1, -16:] *= 1e-5                 # a scale that rounds to zero
+    x = x * ts if dtype == "fp32" or ts > 1e-3 else x
+    if dtype != "fp16" and rows > 2:
+        x[1, :16] *= 1e5                # saturates
+    x = x.to(DT[dtype])
+    w = M.msk_quantize_fp4(strided(x, extra), ts)
+    c, s, _ = F.q4((x.float() / torch.tensor(ts, dtype=torch.float32)).double().numpy())
+    c = torch.from_numpy(c)
+    assert torch.equal(w.packed.cpu(), c[..., 0::2] | (c[..., 1::2] << 4))
+    assert np.array_equal(w.scales.cpu().numpy(), s)
+    ref = values64(w.packed.cpu(), w.scales.cpu(), ts)
+    for out in DT.values():
+        if out == torch.float16 and float(ref.abs().max()) > 65504:
+            continue
+        got = M.msk_dequantize_fp4(w, dtype=out)
+        # two fp32 products, the second one rounding, then the type's
+        ref32 = (values64(w.packed.cpu(), w.scales.cpu()).float() * torch.tensor(ts, dtype=torch.float32))
+        assert torch.equal(got.cpu(), ref32.to(out))
+    wide = torch.full((rows, cols + 8), 3.0, device="cuda")
+    M.msk_dequantize_fp4(w, out=wide[:, :cols])
+    assert torch.equal(wide[:, :cols], M.msk_dequantize_fp4(w, dtype=torch.float32)) and (wide[:, cols:] == 3.0).all()
+
+
+def test_quantize_special_values(M):
+    x = randn(5, 4, 64)
+    x[0, 3], x[1, 20], x[2, 40], x[3, 0] = math.inf, -math.inf, math.nan, -0.0
+    w = M.msk_quantize_fp4(x.cuda())
+    v = M.msk_dequantize_fp4(w, dtype=torch.float32).cpu()
+    assert v[0, 3] == 2688.0 and v[1, 20] == -2688.0
+    assert torch.isfinite(v).all() and v[2, 40].abs() == 6 * values64(torch.full((1, 8), 0x22, dtype=torch.uint8), w.scales[2:3, 2:3].cpu())[0, 0]
+    assert (w.packed[3, 0].item() & 15) == 8
+
+
+# ----------------------------------------------------------------------------
+# products
+# ----------------------------------------------------------------------------
+
+
+def make_experts(M, seed, E, rows, cols, ts=True):
+    p, s = random_fp4(seed, E, rows, cols)
+    t = 0.02 * (0.5 + torch.rand(E, generator=gen(seed))) if ts else None
+    h = M.Fp4Experts(p.cuda(), s.cuda(), None if t is None else t.cuda())
+    v = values64(p, s)
+    return h, v if t is None else v * t.double().view(E, 1, 1)
+
+
+def products_ref(x, w, up, counts, source):
+    """(y, bound of the error before the output's rounding) in 64 bits."""
+    K = x.shape[1]
+    ys, errs, at = [], [], 0
+    for e, n in enumerate(counts):
+        part = x[source[at:at + n]]
+        at += n
+        g = part @ w[e].T
+        dg = (K + 64) * 2.0 ** -23 * (part.abs() @ w[e].abs().T) + 3 * 2.0 ** -24 * g.abs()
+        if up is not None:
+            u = part @ up[e].T
+            du = (K + 64) * 2.0 ** -23 * (part.abs() @ up[e].abs().T) + 3 * 2.0 ** -24 * u.abs()
+            s = g * torch.sigmoid(g)
+            ys.append(s * u)
+            errs.append(s.abs() * du + (u.abs() + du) * 1.1 * dg + 2.0 ** -20 * (s * u).abs())
+        else:
+            ys.append(g)
+            errs.append(dg)
+    return torch.cat(ys), torch.cat(errs)
+
+
+def run_products(M, counts, rows, cols, glu=False, gather=False, out="bf16", x_ts=1.0, seed=11, extra=0, top_k=3, ts=True):
+    E, n = len(counts), sum(counts)
+    w, wv = make_experts(M, seed, E, rows, cols, ts)
+    up, uv = make_experts(M, seed + 1, E, rows, cols, ts) if glu else (None, None)
+    g = gen(seed + 2)
+    if gather:
+        xr = max(1, (n + top_k - 1) // top_k)
+        slots = torch.randint(0, xr * top_k, (n,), generator=g, dtype=torch.int32)  # (the same index twice, too)
+        source = (slots // top_k).long()
+    else:
+        xr, slots, source = n, None, torch.arange(n)
+    c, s = random_fp4(seed + 3, xr, cols)
+    x = M.Fp4Weight(c.cuda(), s.cuda(), x_ts)
+    offsets = torch.tensor([0] + counts).cumsum(0).int()
+    y = torch.full((n + 3, rows + extra), 5.0, dtype=DT[out], device="cuda")
+    got = M.msk_experts_fp4(x, w, offsets.cuda(), up=up, slots=None if slots is None else slots.cuda(), top_k=top_k,
+                            out=y[:n, :rows])
+    ref, err = products_ref(values64(c, s, x_ts), wv, uv, counts, source)
+    diff = (got.cpu().double() - ref).abs()
+    bound = half_step(DT[out]) * (ref.abs() + err) + err + tiny(DT[out])
+    assert (diff <= bound).all(), float((diff / bound).max())
+    # nothing beside the rows
+    assert (y[n:] == 5.0).all() and (y[:, rows:] == 5.0).all()
+
+
+@pytest.mark.parametrize("counts,rows,cols", [
+    ([1], 128, 256), ([16], 128, 64), ([17], 64, 128), ([5], 1, 192), ([3], 129, 320), ([128], 256, 512), ([129], 128, 256),
+    ([224], 128, 1024), ([225], 200, 256), ([700], 136, 576), ([0, 1, 0], 128, 256), ([3, 0, 40, 1, 130, 0, 300], 160, 384),
+    ([2] * 40, 72, 128), ([0, 0, 0, 33], 31, 448)])
+@pytest.mark.parametrize("glu,gather", [(False, False), (True, False), (False, True), (True, True)])
+def test_products(M, counts, rows, cols, glu, gather):
+    run_products(M, counts, rows, cols, glu, gather)
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("glu", [False, True])
+def test_products_types_and_strides(M, out, glu):
+    run_products(M, [7, 0, 250, 31], 100, 256, glu, True, out, extra=5)
+    run_products(M, [20, 1], 96, 4096, glu, False, out, extra=8, ts=False)
+
+
+@pytest.mark.parametrize("x_ts,out", [(0.37, "bf16"), (1e-20, "fp32"), (3e18, "fp32")])
+def test_products_scales(M, x_ts, out):
+    run_products(M, [30, 3], 130, 256, x_ts=x_ts, out=out)
+
+
+def test_products_scales_that_leave_the_range_alone(M):
+    """Two tensors' scales whose product leaves fp32's range, with results in it."""
+    c = torch.full((1, 32), 0x22, dtype=torch.uint8)          # ones
+    s = torch.full((1, 4), 0x01, dtype=torch.uint8)           # 2^-9
+    w = M.Fp4Experts(c.view(1, 1, 32).cuda(), s.view(1, 1, 4).cuda(), torch.tensor([2.0 ** 100], device="cuda"))
+    x = M.Fp4Weight(c.cuda(), s.cuda(), 2.0 ** 36)
+    off = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    y = M.msk_experts_fp4(x, w, off, out_dtype=torch.float32)
+    assert y.item() == 64 * 2.0 ** (-18 + 100 + 36 - 0)
+    x = M.Fp4Weight(c.cuda(), torch.full((1, 4), 0x78, dtype=torch.uint8).cuda(), 2.0 ** -100)  # 256
+    w = M.Fp4Experts(c.view(1, 1, 32).cuda(), torch.full((1, 1, 4), 0x78, dtype=torch.uint8).cuda(),
+                     torch.tensor([2.0 ** -55], device="cuda"))
+    y = M.msk_experts_fp4(x, w, off, out_dtype=torch.float32)
+    assert y.item() == 2.0 ** (6 + 16 - 155)
+
+
+def test_every_scale_code(M):
+    """Every finite E4M3 scale on both sides: exact sums of one product."""
+    codes = torch.arange(0x7F, dtype=torch.uint8)
+    n = codes.numel()
+    wp = torch.zeros(1, n, 128, dtype=torch.uint8)
+    wp[:, :, 8 * 5] = 0x07                                       # element 80: 6
+    ws = torch.zeros(1, n, 16, dtype=torch.uint8)
+    ws[0, :, 5] = codes
+    xp = torch.zeros(n, 128, dtype=torch.uint8)
+    xp[:, 40] = 0x03                                             # 1.5
+    xs = torch.zeros(n, 16, dtype=torch.uint8)
+    xs[:, 5] = codes
+    y = M.msk_experts_fp4(M.Fp4Weight(xp.cuda(), xs.cuda()), M.Fp4Experts(wp.cuda(), ws.cuda()),
+                          torch.tensor([0, n], dtype=torch.int32, device="cuda"), out_dtype=torch.float32)
+    v = values64(torch.full((n, 8), 0x22, dtype=torch.uint8), codes.view(n, 1))[:, 0]
+    assert torch.equal(y.cpu().double(), 9.0 * v.view(n, 1) * v.view(1, n))
+
+
+def test_nan_scales_stay_in_their_rows(M):
+    counts, rows, cols = [20, 9], 70, 256
+    w, _ = make_experts(M, 5, 2, rows, cols)
+    c, s = random_fp4(6, 29, cols)
+    off = torch.tensor([0, 20, 29], dtype=torch.int32, device="cuda")
+    base = M.msk_experts_fp4(M.Fp4Weight(c.cuda(), s.cuda()), w, off)
+    w.scales[0, 33, 2] = 0x7F
+    s[25, 7] = 0x7F
+    got = M.msk_experts_fp4(M.Fp4Weight(c.cuda(), s.cuda()), w, off)
+    bad = torch.zeros(29, rows, dtype=torch.bool, device="cuda")
+    bad[:20, 33] = True
+    bad[25] = True
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], base[~bad])
+
+
+def test_places_of_no_expert_are_left(M):
+    """Offsets that begin behind 0, end before n, or are cut off: only experts' places are written."""
+    w, wv = make_experts(M, 7, 3, 40, 128)
+    c, s = random_fp4(8, 50, 128)
+    x = M.Fp4Weight(c.cuda(), s.cuda())
+    xv = values64(c, s)
+    for offsets, ranges in (([4, 10, 10, 30], [(4, 10), (10, 10), (10, 30)]), ([0, 0, 0, 0], [(0, 0)] * 3),
+                            ([-5, 7, 60, 80], [(0, 7), (7, 50), (50, 50)]), ([0, 20, 10, 30], [(0, 20), (20, 20), (20, 30)])):
+        y = torch.full((50, 40), 9.0, device="cuda")
+        M.msk_experts_fp4(x, w, torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=y)
+        want = torch.full((50, 40), 9.0, dtype=torch.float64)
+        for e, (a, b) in enumerate(ranges):
+            want[a:b] = xv[a:b] @ wv[e].T
+        assert torch.allclose(y.cpu().double(), want, rtol=1e-4, atol=1e-3)
+        assert torch.equal(y.cpu() == 9.0, want == 9.0)
+
+
+def test_slots_beyond_x_are_cut_off(M):
+    w, wv = make_experts(M, 9, 1, 16, 64)
+    c, s = random_fp4(10, 5, 64)
+    slots = torch.tensor([-1, 0, 9, 10, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    y = M.msk_experts_fp4(M.Fp4Weight(c.cuda(), s.cuda()), w, torch.tensor([0, 6], dtype=torch.int32, device="cuda"),
+                          slots=slots.cuda(), top_k=2, out_dtype=torch.float32)
+    want = values64(c, s)[[0, 0, 4, 4, 4, 0]] @ wv[0].T
+    assert torch.allclose(y.cpu().double(), want, rtol=1e-4, atol=1e-3)
+
+
+# ----------------------------------------------------------------------------
+# combine
+# ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("tokens,k,cols,ydt,odt,extra", [
+    (1, 1, 8, "bf16", "bf16", 0), (16, 8, 2048, "bf16", "bf16", 0), (5, 2, 7, "fp16", "fp32", 0), (33, 9, 136, "fp32", "bf16", 0),
+    (3, 17, 64, "bf16", "fp32", 8), (20, 4, 1000, "fp16", "fp16", 3), (7, 8, 1, "bf16", "bf16", 0), (130, 5, 24, "fp32", "fp32", 4),
+    (9, 8, 64, "fp32", "fp16", 0)])
+@pytest.mark.parametrize("gated", [True, False])
+def test_combine(M, tokens, k, cols, ydt, odt, extra, gated):
+    n = tokens * k
+    y = randn(1, n, cols).to(DT[ydt])
+    places = torch.randperm(n, generator=gen(2)).int().view(tokens, k)
+    if n > 8:
+        drop = torch.rand(tokens, k, generator=gen(3)) < 0.2
+        y[places[drop].long()] = math.nan                         # (not read)
+        places[drop] = torch.tensor([-1, n, 2 ** 31 - 1, -2 ** 31])[torch.arange(int(drop.sum())) % 4].int()
+        places[0] = -1                                            # a token with nothing: zeros
+        places[1, 0] = places[1, k - 1]                           # the same place twice
+    gates = torch.rand(tokens, k, generator=gen(4)) if gated else None
+    out = torch.full((tokens, cols + extra), 5.0, dtype=DT[odt], device="cuda")
+    got = M.msk_moe_combine(strided(y, extra), places.cuda(), None if gates is None else gates.cuda(), out=out[:, :cols])
+    ok = (places >= 0) & (places < n)
+    terms = torch.where(ok.unsqueeze(-1), y[places.long().clamp(0, n - 1)].double(), 0.0)
+    if gated:
+        terms = terms * gates.double().unsqueeze(-1)
+    ref, mag = terms.sum(1), terms.abs().sum(1)
+    diff = (got.cpu().double() - ref).abs()
+    assert (diff <= half_step(DT[odt]) * (ref.abs() + 2.0 ** -20 * mag) + k * 2.0 ** -23 * mag + tiny(DT[odt])).all()
+    assert (out[:, cols:] == 5.0).all()
+
+
+# ----------------------------------------------------------------------------
+# together
+# ----------------------------------------------------------------------------
+
+
+def moe(M, logits, bias, x, gate, up, down, k, stream=None):
+    experts, gates = M.msk_moe_route(logits, k, bias=bias, stream=stream)
+    offsets, slots, places = M.msk_moe_sort(experts, gate.n_experts, stream=stream)
+    xq = M.msk_quantize_fp4(x, stream=stream)
+    h = M.msk_experts_fp4(xq, gate, offsets, up=up, slots=slots, top_k=k, stream=stream)
+    hq = M.msk_quantize_fp4(h, stream=stream)
+    y = M.msk_experts_fp4(hq, down, offsets, stream=stream)
+    return M.msk_moe_combine(y, places, gates, stream=stream), (experts, gates, offsets, slots, xq, h, hq, y)
+
+
+@pytest.mark.parametrize("tokens,E,k,P,I", [(1, 16, 2, 128, 128), (16, 64, 8, 256, 192), (150, 8, 3, 320, 128)])
+def test_a_prompt_through_its_experts(M, tokens, E, k, P, I):
+    """The operators one after the other, each stage against its definition on the stage's own input."""
+    logits, bias = randn(1, tokens, E).cuda(), randn(2, E).cuda()
+    x = randn(3, tokens, P).bfloat16().cuda()
+    gate, gv = make_experts(M, 4, E, I, P)
+    up, uv = make_experts(M, 5, E, I, P)
+    down, dv = make_experts(M, 6, E, P, I)
+    out, (experts, gates, offsets, slots, xq, h, hq, y) = moe(M, logits, bias, x, gate, up, down, k)
+    counts = np.diff(offsets.cpu().numpy()).tolist()
+    s = slots.cpu().long()
+    ref, err = products_ref(values64(xq.packed.cpu(), xq.scales.cpu()), gv, uv, counts, s // k)
+    assert ((h.cpu().double() - ref).abs() <= 2.0 ** -8 * (ref.abs() + err) + err + 1e-38).all()
+    c, sc, _ = F.q4(h.cpu().double().numpy())
+    c = torch.from_numpy(c)
+    assert torch.equal(hq.packed.cpu(), c[..., 0::2] | (c[..., 1::2] << 4)) and np.array_equal(hq.scales.cpu().numpy(), sc)
+    ref, err = products_ref(values64(hq.packed.cpu(), hq.scales.cpu()), dv, None, counts, torch.arange(tokens * k))
+    assert ((y.cpu().double() - ref).abs() <= 2.0 ** -8 * (ref.abs() + err) + err + 1e-38).all()
+    # back at the tokens, from the slots' own order and not from the places
+    yv, total, mag = y.cpu().double(), torch.zeros(tokens, P, dtype=torch.float64), torch.zeros(tokens, P, dtype=torch.float64)
+    for p in range(tokens * k):
+        t, r = int(s[p]) // k, int(s[p]) % k
+        total[t] += gates[t, r].item() * yv[p]
+        mag[t] += abs(gates[t, r].item()) * yv[p].abs()
+    assert ((out.cpu().double() - total).abs() <= 2.0 ** -8 * total.abs() + (k + 1) * 2.0 ** -23 * mag + 1e-38).all()
+
+
+def test_captured_and_on_two_streams(M):
+    """A captured run gives the eager one's bits for new inputs, and so do two streams at once."""
+    E, k, T, P, I = 32, 4, 200, 256, 128
+    gate, up, down = (make_experts(M, s, E, r, c)[0] for s, r, c in ((4, I, P), (5, I, P), (6, P, I)))
+    logits, x = randn(1, T, E).cuda(), randn(3, T, P).bfloat16().cuda()
+    inputs = [(randn(10 + i, T, E).cuda(), randn(20 + i, T, P).bfloat16().cuda()) for i in range(3)]
+    want = [moe(M, l, None, v, gate, up, down, k)[0] for l, v in inputs]
+    moe(M, logits, None, x, gate, up, down, k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _ = moe(M, logits, None, x, gate, up, down, k)
+    for (l, v), w in zip(inputs, want):
+        logits.copy_(l)
+        x.copy_(v)
+        graph.replay()
+        assert torch.equal(out, w)
+    streams = [torch.cuda.Stream() for _ in inputs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [moe(M, l, None, v, gate, up, down, k, stream=s) for (l, v), s in zip(inputs, streams)]
+        torch.cuda.synchronize()
+        for (o, _), w in zip(outs, want):
+            assert torch.equal(o, w)
+
+
+def test_runs_repeat_bit_for_bit(M):
+    E, k, T = 64, 8, 1500
+    gate, _ = make_experts(M, 4, E, 128, 256)
+    experts = torch.randint(0, E, (T, k), generator=gen(1), dtype=torch.int32).cuda()
+    first = None
+    for _ in range(10):
+        offsets, slots, places = M.msk_moe_sort(experts, E)
+        c, s = random_fp4(3, T, 256) if first is None else (c, s)
+        y = M.msk_experts_fp4(M.Fp4Weight(c.cuda(), s.cuda()), gate, offsets, slots=slots, top_k=k)
+        now = (offsets, slots, places, y)
+        first = first or now
+        assert all(torch.equal(a, b) for a, b in zip(first, now))
