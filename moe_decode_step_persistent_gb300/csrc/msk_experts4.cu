@@ -111,83 +111,134 @@ msk_status rows_call(bool write, const void* x, int32_t dtype, int64_t rows, int
 // products
 // ---------------------------------------------------------------------------
 
-constexpr int kM = 128;            // weight rows of a tile (the MMA's M)
+constexpr int kM = 128;            // weight rows of a block (a pair's MMA has M = 256)
 constexpr int kStageK = 256;       // columns of a stage
 constexpr int kSteps = kStageK / 64;  // MMAs of a stage
-constexpr int kMaxN = 224;         // tokens of a tile at most (the MMA's N): two accumulators and the scales fill tensor memory
+constexpr int kMaxN = 256;         // tokens of a tile at most (the MMA's N)
+constexpr int kStepN = 32;         // ... and what they are filled up to: each block has half of them, in boxes of 16
 constexpr int kMaxStages = 10;
 constexpr int kMaxE = 1024;
 constexpr int kScaleWarps = 4, kEpiWarps = 8;
-constexpr int kWarps = 2 + kScaleWarps + kEpiWarps;
-constexpr int kProductThreads = 32 * kWarps;
-constexpr int kAhead = 4;          // stages whose scales are on their way in registers
-constexpr int kACodes = kM * kStageK / 2;
-constexpr int kRing = 204 * 1024;  // (dynamic shared memory: beside it 12 KB for the experts' tables and what aligns the ring)
-constexpr int kTables = (3 * kMaxE + 4) * 4;
+constexpr int kScaleWarp0 = 4, kEpiWarp0 = kScaleWarp0 + kScaleWarps;
+constexpr int kProductThreads = 32 * (kEpiWarp0 + kEpiWarps);
+// Tiles whose places are known ahead: the scales are asked for two tiles ahead where
+// a tile is one stage, while kLag stages behind are not handed over yet.
+constexpr int kTiles = 8;
+constexpr int kLag = 3;            // stages of gathered rows on their way when one is handed over
+static_assert(kTiles > kLag + 1, "a tile that is waited for is not held up by one that is not handed over");
+constexpr int kACodes = kM * kStageK / 2, kSfABytes = kM * kStageK / 16;
+constexpr int kRing = 204 * 1024;  // (dynamic shared memory: beside it the tables below and what aligns the ring)
+constexpr int kTables = 3 * kMaxE * 4;
 constexpr int kSmem = 1024 + kRing + kTables;
-// tensor memory columns: two accumulators, then the scales of a stage's rows and tokens
-constexpr int kAccCols = kMaxN, kSfA = 2 * kAccCols, kSfB = kSfA + 4 * kSteps;
-static_assert(kSfB + 8 * kSteps <= 512, "tensor memory");
+// Tensor memory columns: two accumulators, which overlap where a tile has more
+// than kAcc1 tokens, then the scales of a stage's rows and tokens.
+constexpr int kAcc1 = 208, kSfA = kAcc1 + kMaxN, kSfB = kSfA + 4 * kSteps;
+static_assert(kSfB + 8 * kSteps == 512, "tensor memory");
 
 static __device__ uint32_t g_error;  // nonzero once a wait has run out
 
 struct Experts4 {
   CUtensorMap w_map, up_map;  // [E rows][cols / 2] bytes, boxes of 128 x 128 (GLU: of 16 x 128)
-  CUtensorMap x_map;          // [x_rows][cols / 2] bytes, boxes of 16 x 128 (gathered: of one row)
-  const uint8_t *x_scales, *w_scales, *up_scales;
+  CUtensorMap x_map;          // [x_rows][cols / 2] bytes, boxes of 16 x 128
+  const uint8_t *x_codes, *x_scales, *w_scales, *up_scales;
   const float *w_ts, *up_ts;
   const int32_t *offsets, *slots;
   void* y;
   long long y_stride, x_rows;
   int n, E, rows, K, top_k, y_dtype, nt, stages, mblocks;
   float x_ts;
-  bool vec;  // scales in pieces of 16 bytes
+  int vec;  // scales in pieces of 32, 16 or 4 bytes
+};
+
+// A tile: the pair's 256 weight rows of an expert and up to nt of its tokens.
+struct Tile {
+  int e, m;       // expert, block of weight rows
+  int p0, count;  // first place and number of places
+  int n;          // count, up to the MMA's next N
+  float f[4];     // w's scale as two factors, up's
 };
 
 struct Bars {
   uint64_t full[kMaxStages], sfull[kMaxStages], empty[kMaxStages];
-  uint64_t accf[2], acce[2];
+  uint64_t accf[2], acce[2], over[2];
+  uint64_t tfull[kTiles], tempty[kTiles];
   uint64_t done;
 };
 
-// Four rows of a 2-D tensor map, one after the other.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&r)[4], uint32_t bar) {
+// --- what a pair of blocks does together (the first block's thread issues) ------
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred q; elect.sync _|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_tmem_free(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         bool accumulate) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-      "[%7];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p; }" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+// 32 rows x 16 bytes of each block's shared memory into its tensor memory.
+__device__ __forceinline__ void pair_cp_sf(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+// Arrives on the barrier of both blocks (or of `mask`'s) when the MMAs before are complete.
+__device__ __forceinline__ void pair_commit(uint32_t mbar, uint16_t mask) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(mbar),
+               "h"(mask)
+               : "memory");
+}
+// A box into this block's shared memory, counted by a barrier of the first block's.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// A tile: 128 weight rows of an expert and up to nt of its tokens' rows.
-struct Tile {
-  int e, m;       // expert, block of weight rows
-  int p0, count;  // first place and number of places
-  int n;          // count, up to the MMA's next N
-};
-
-// y^T = W x^T by block-scaled NVFP4 on the fifth-generation tensor cores: M =
-// 128 weight rows, N = up to 224 tokens of one expert, K = 64 a step.  Weights
-// and tokens come by tiled copies (gathered ones, four rows each, where tokens
-// are named by slots), both with the 128-byte swizzle; the scales, row-major in
-// memory, by plain loads some stages ahead, written as the tensor cores want
-// them.  Tiles run over experts, then blocks of weight rows, then tokens, so that
-// neighbouring blocks share weights in L2; a block takes every grid-th one.
-// GLU: a tile's rows are 64 gate and 64 up rows, 16 and 16 in turn, so that a
+// y^T = W x^T by block-scaled NVFP4 on the fifth-generation tensor cores.  A pair
+// of blocks (a cluster) has a tile of M = 256 weight rows, 128 each, and N = up to
+// 256 tokens of one expert, of which each block loads half: an SM takes no more
+// than 50 bytes a clock out of L2, and a tile of a block's own would need 192 bytes
+// a K step of 64 where a pair's needs 128 (for 128 clocks of MMA).
+// Weights and tokens come by tiled copies with the 128-byte swizzle, tokens named
+// by slots by asynchronous copies of 16 bytes (gathering tiled copies take 66
+// clocks for four rows of 128 bytes); the scales, row-major in memory, by plain
+// loads some stages ahead, written as the tensor cores want them.  Tiles run over
+// experts, then blocks of weight rows, then tokens, so that neighbouring pairs
+// share weights in L2; a pair takes every one that is a multiple of the pairs on.
+// GLU: a block's rows are 64 gate and 64 up rows, 16 and 16 in turn, so that a
 // lane's partner 16 lanes on holds the up value of its gate value.
 //
-// Roles: a warp that copies, one that issues, four that write scales, eight that
-// end the tiles from one of two accumulators while the other fills.
-template <bool GLU>
+// Roles: a warp that finds the tiles and their tokens, one that copies weights, one
+// that copies tokens, one that issues (of the pair's first block), four that write
+// scales and gather, eight that end the tiles from one of two accumulators while
+// the other fills.  Everything that one thread issues is issued by the elected lane
+// of a warp that stays together: from a branch of one lane an MMA or a copy takes
+// three times as long.
+template <bool GLU, bool GATHER>
 __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __grid_constant__ Experts4 a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Bars bars;
+  __shared__ Tile tile_ring[kTiles];
+  __shared__ int source_ring[kTiles][kMaxN];  // rows of x of a tile's tokens
   __shared__ uint32_t tmem_base;
   __shared__ int abort, never, tiles_all;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   // (dynamic shared memory starts at a multiple of 1024 in the shared window)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t ring = smem_u32(smem);
@@ -195,322 +246,458 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   int* counts = starts + kMaxE;                         // [E]
   int* ends = counts + kMaxE;                           // [E]: tiles up to and with each expert
   const int chunks = a.nt > 128 ? 2 : 1;                // of tokens' scales, 128 rows each
-  const int slot_a = kACodes, slot_b = a.nt * (kStageK / 2), slot_sfa = kM * kStageK / 16;
-  const int slot_bytes = slot_a + slot_b + slot_sfa + chunks * 512 * kSteps;
+  const int slot_b = a.nt / 2 * (kStageK / 2);
+  const int slot_bytes = kACodes + slot_b + kSfABytes + chunks * 512 * kSteps;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  auto first = [&](uint64_t& b) { return mapa(smem_u32(&b), 0); };  // the pair's first block's
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&a.w_map);
-    prefetch_tensormap(&a.x_map);
     if (GLU) prefetch_tensormap(&a.up_map);
+    if (!GATHER) prefetch_tensormap(&a.x_map);
   }
   if (tid == 32) {
     abort = 0, never = 0;
     for (int i = 0; i < a.stages; ++i)
-      mbar_init(bar(bars.full[i]), 1), mbar_init(bar(bars.sfull[i]), kScaleWarps), mbar_init(bar(bars.empty[i]), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(bars.accf[i]), 1), mbar_init(bar(bars.acce[i]), kEpiWarps);
+      mbar_init(bar(bars.full[i]), GATHER ? 1 : 2), mbar_init(bar(bars.sfull[i]), 2 * kScaleWarps), mbar_init(bar(bars.empty[i]), 1);
+    for (int i = 0; i < 2; ++i)
+      mbar_init(bar(bars.accf[i]), 1), mbar_init(bar(bars.acce[i]), 2 * kEpiWarps), mbar_init(bar(bars.over[i]), 2 * kEpiWarps);
+    for (int i = 0; i < kTiles; ++i)
+      mbar_init(bar(bars.tfull[i]), 1), mbar_init(bar(bars.tempty[i]), 1 + !GATHER + !rank + kScaleWarps + kEpiWarps);
     mbar_init(bar(bars.done), 1);
     mbar_fence_init();
     fence_proxy_async_shared();
   }
-  if (warp == 2) tmem_alloc(smem_u32(&tmem_base), 512);
+  if (warp == 3) pair_tmem_alloc(smem_u32(&tmem_base), 512);
   grid_dep_wait();
   grid_dep_launch();
 
   // The experts' places (whatever the offsets hold, ranges in [0, n] that do not
   // overlap) and tiles.
-  if (warp == 0) {
+  if (warp == 2) {
     int at = 0, tiles = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      int first = 0, last = 0;
+      int from = 0, last = 0;
       if (e < a.E) {
-        first = max(0, min(a.n, __ldg(a.offsets + e)));
+        from = max(0, min(a.n, __ldg(a.offsets + e)));
         last = max(0, min(a.n, __ldg(a.offsets + e + 1)));
       }
-      int end = max(first, last);
+      int end = max(from, last);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, end, o);
         if (lane >= o) end = max(end, v);
       }
       const int before = __shfl_up_sync(0xFFFFFFFFu, end, 1);
-      first = max(first, lane > 0 ? max(at, before) : at);
+      from = max(from, lane > 0 ? max(at, before) : at);
       end = max(end, at);
-      const int count = max(0, last - first);
+      const int count = max(0, last - from);
       int t = (count + a.nt - 1) / a.nt * a.mblocks;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, t, o);
         if (lane >= o) t += v;
       }
-      if (e < a.E) starts[e] = first, counts[e] = count, ends[e] = tiles + t;
+      if (e < a.E) starts[e] = from, counts[e] = count, ends[e] = tiles + t;
       tiles += __shfl_sync(0xFFFFFFFFu, t, 31);
       at = __shfl_sync(0xFFFFFFFFu, end, 31);
     }
     if (lane == 0) tiles_all = tiles;
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // (of the block too)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  const int mine = (int)blockIdx.x < tiles_all ? (tiles_all - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
+  const int mine = pair < tiles_all ? (tiles_all - pair + pairs - 1) / pairs : 0;
   const int kst = (a.K + kStageK - 1) / kStageK;  // stages of a tile
   const uint64_t deadline = gtimer() + kOpsWaitNs + (uint64_t)mine * kst * kOpsStepNs;
   const volatile int* ab = &abort;
+  // Waits by whole warps, for arrivals of this block and of the pair.
   auto wait = [&](uint64_t& b, uint32_t parity) {
-    if (mbar_wait(bar(b), parity, deadline, ab)) return true;
-    abort = 1;
-    return false;
+    const bool ok = mbar_wait(bar(b), parity, deadline, ab);
+    if (!ok) abort = 1;
+    return (bool)__all_sync(0xFFFFFFFFu, ok);
   };
-  auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
-  auto tile_at = [&](int i) {
-    const int t = (int)blockIdx.x + i * (int)gridDim.x;
-    int lo = 0, hi = a.E - 1;  // the first expert whose tiles go beyond t
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (ends[mid] > t) hi = mid;
-      else lo = mid + 1;
-    }
-    const int count = counts[lo], nb = (count + a.nt - 1) / a.nt;
-    const int local = t - (lo > 0 ? ends[lo - 1] : 0);
-    const int m = local / nb, j = local - m * nb;
-    const int step = ((count + nb - 1) / nb + 15) & ~15;  // tokens of a tile, the same for all but the last
-    Tile r;
-    r.e = lo, r.m = m, r.p0 = starts[lo] + j * step, r.count = min(step, count - j * step), r.n = (r.count + 15) & ~15;
-    return r;
+  auto wait_pair = [&](uint64_t& b, uint32_t parity) {
+    bool ok = false;
+    for (uint32_t spins = 1; !(ok = mbar_try_wait_cluster(bar(b), parity)); ++spins)
+      if (spins % 64 == 0 && (*ab || gtimer() > deadline)) break;
+    if (!ok) abort = 1;
+    return (bool)__all_sync(0xFFFFFFFFu, ok);
   };
-  // The row of x at a place.
-  auto source = [&](int p) {
-    if (a.slots == nullptr) return p;
-    const int s = __ldg(a.slots + p);
-    return max(0, min((int)a.x_rows - 1, (int)((unsigned)max(s, 0) / (unsigned)a.top_k)));
+  auto wait_tile = [&](int i) { return wait(bars.tfull[i % kTiles], (i / kTiles) & 1); };
+  auto leave_tile = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(bars.tempty[i % kTiles]));
   };
 
-  if (warp == 0) {
-    // --- copies ---------------------------------------------------------------
+  if (warp == 3) {
+    // --- tiles ----------------------------------------------------------------
+    for (int i = 0; i < mine; ++i) {
+      if (!wait(bars.tempty[i % kTiles], ((i / kTiles) & 1) ^ 1)) break;
+      const int t = pair + i * pairs;
+      int lo = 0, hi = a.E - 1;  // the first expert whose tiles go beyond t
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (ends[mid] > t) hi = mid;
+        else lo = mid + 1;
+      }
+      const int all = counts[lo], nb = (all + a.nt - 1) / a.nt;
+      const int local = t - (lo > 0 ? ends[lo - 1] : 0);
+      const int m = local / nb, j = local - m * nb;
+      const int step = ((all + nb - 1) / nb + kStepN - 1) / kStepN * kStepN;  // tokens of a tile, the same for all but the last
+      const int p0 = starts[lo] + j * step, count = min(step, all - j * step);
+      Tile& r = tile_ring[i % kTiles];
+      for (int k = lane; k < kMaxN; k += 32) {
+        int p = k < count ? p0 + k : -1;
+        if (GATHER && k < count) p = max(0, min((int)a.x_rows - 1, (int)((unsigned)max(__ldg(a.slots + p), 0) / (unsigned)a.top_k)));
+        source_ring[i % kTiles][k] = p;
+      }
+      if (lane < (GLU ? 2 : 1)) {
+        // The tensors' scales: a significand and a power of two in two halves, so
+        // that no product leaves fp32's range unless the result does.
+        const float* p = lane ? a.up_ts : a.w_ts;
+        const float wt = p != nullptr ? __ldg(p + lo) : 1.f;
+        float s = wt * a.x_ts, h = 1.f;
+        const int ew = (__float_as_uint(wt) >> 23) & 255, ex = (__float_as_uint(a.x_ts) >> 23) & 255;
+        if (ew != 0 && ew != 255 && ex != 0 && ex != 255) {
+          const int e2 = max(-250, min(250, ew + ex - 254)), e1 = e2 / 2;
+          const float mw = __uint_as_float((__float_as_uint(wt) & 0x807FFFFFu) | 0x3F800000u);
+          const float mx = __uint_as_float((__float_as_uint(a.x_ts) & 0x807FFFFFu) | 0x3F800000u);
+          s = mw * mx * exp2i(e1), h = exp2i(e2 - e1);
+        }
+        r.f[2 * lane] = s, r.f[2 * lane + 1] = h;
+      }
+      if (lane == 0) r.e = lo, r.m = m, r.p0 = p0, r.count = count, r.n = (count + kStepN - 1) / kStepN * kStepN;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.tfull[i % kTiles]));
+    }
+  } else if (warp == 0 || (!GATHER && warp == 1)) {
+    // --- copies of weights (warp 0) and tokens (warp 1) --------------------------
+    const bool el = elect_one();
     int st = 0;
     uint32_t ph = 1;  // (a fresh barrier passes a wait for phase 1)
     bool ok = true;
     for (int i = 0; i < mine && ok; ++i) {
-      const Tile t = tile_at(i);
-      int r[2][4];
-      if (a.slots != nullptr) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = 4 * (lane + 32 * u) + j;
-            r[u][j] = k < t.count ? source(t.p0 + k) : 0;
-          }
-      }
-      const int wrow = t.e * a.rows + t.m * (GLU ? 64 : kM);
-      for (int s = 0; s < kst && ok; ++s) {
-        ok = wait_warp(bars.empty[st], ph);
+      ok = wait_tile(i);
+      if (!ok) break;
+      const Tile& t = tile_ring[i % kTiles];
+      const int n = t.n;
+      const int row = warp == 0 ? t.e * a.rows + t.m * (GLU ? 128 : 256) + rank * (GLU ? 64 : 128) : t.p0 + rank * (n / 2);
+      for (int s = 0; s < kst; ++s) {
+        ok = wait(bars.empty[st], ph);
         if (!ok) break;
-        const uint32_t dst = ring + st * slot_bytes, b = bar(bars.full[st]);
-        const int x = s * (kStageK / 2);
-        if (lane == 0) mbar_arrive_expect_tx(b, (uint32_t)(slot_a + t.n * (kStageK / 2)));
-        __syncwarp();
-        if (GLU) {
-          if (lane < 8) tma_load_2d(dst + lane * 2048, lane & 1 ? &a.up_map : &a.w_map, x, wrow + (lane >> 1) * 16, b);
-        } else if (lane == 0) {
-          tma_load_2d(dst, &a.w_map, x, wrow, b);
-        }
-        if (a.slots != nullptr) {
+        if (el) {
+          const uint32_t dst = ring + st * slot_bytes, b = first(bars.full[st]);
+          const int x = s * (kStageK / 2);
+          if (rank == 0) mbar_arrive_expect_tx(bar(bars.full[st]), warp == 0 ? 2 * kACodes : n * (kStageK / 2));
+          if (warp == 1) {
+            for (int j = 0; j < n / 2; j += 16) pair_load_2d(dst + kACodes + j * 128, &a.x_map, x, row + j, b);
+          } else if (GLU) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            if (4 * (lane + 32 * u) < t.n) tma_gather4(dst + slot_a + (lane + 32 * u) * 512, &a.x_map, x, r[u], b);
-        } else if (16 * lane < t.n) {
-          tma_load_2d(dst + slot_a + lane * 2048, &a.x_map, x, t.p0 + 16 * lane, b);
+            for (int j = 0; j < 8; ++j) pair_load_2d(dst + j * 2048, j & 1 ? &a.up_map : &a.w_map, x, row + (j >> 1) * 16, b);
+          } else {
+            pair_load_2d(dst, &a.w_map, x, row, b);
+          }
         }
+        __syncwarp();
         if (++st == a.stages) st = 0, ph ^= 1;
       }
+      leave_tile(i);
     }
-  } else if (warp == 1) {
+  } else if (warp == 2) {
     // --- MMAs -----------------------------------------------------------------
-    if (lane == 0) {
-      int st = 0;
+    if (rank == 0) {
+      const bool el = elect_one();
+      int st = 0, before = 0;  // (the tokens of the tile before)
       uint32_t ph = 0;
       bool ok = true;
       for (int i = 0; i < mine && ok; ++i) {
-        const Tile t = tile_at(i);
-        const int d = i & 1;
-        ok = wait(bars.acce[d], ((i >> 1) & 1) ^ 1);
+        ok = wait_tile(i);
         if (!ok) break;
+        const int n = __shfl_sync(0xFFFFFFFFu, tile_ring[i % kTiles].n, 0), d = i & 1;
+        leave_tile(i);
+        ok = wait_pair(bars.acce[d], ((i >> 1) & 1) ^ 1);
+        // (accumulators that overlap: the tile before has been read there)
+        if (ok && i > 0 && (d ? before : n) > kAcc1) ok = wait_pair(bars.over[d ^ 1], ((i - 1) >> 1) & 1);
+        if (!ok) break;
+        before = n;
         tc_fence_after();
-        const uint32_t acc = tmem + d * kAccCols, idesc = idesc_mxf4nvf4(t.n);
-        const int nc = t.n > 128 ? 2 : 1;
+        const uint32_t acc = tmem + d * kAcc1, idesc = idesc_mxf4nvf4(n) + (1u << 27);  // (M = 256)
         for (int s = 0; s < kst; ++s) {
-          ok = wait(bars.full[st], ph) && wait(bars.sfull[st], ph);
+          ok = wait(bars.full[st], ph) && wait_pair(bars.sfull[st], ph);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t at = ring + st * slot_bytes, sfa = at + slot_a + slot_b, sfb = sfa + slot_sfa;
-          const uint64_t ad = umma_desc(at, 16, 1024) | kSwizzle128, bd = umma_desc(at + slot_a, 16, 1024) | kSwizzle128;
-          const int steps = min(kSteps, (a.K - s * kStageK) / 64);
-          for (int k = 0; k < steps; ++k) {
-            tc_cp_sf(tmem + kSfA + 4 * k, umma_desc(sfa + 512 * k, 128, 128));
-            tc_cp_sf(tmem + kSfB + 8 * k, umma_desc(sfb + 512 * chunks * k, 128, 128));
-            if (nc == 2) tc_cp_sf(tmem + kSfB + 8 * k + 4, umma_desc(sfb + 512 * chunks * k + 512, 128, 128));
-            mma_mxf4nvf4(acc, ad + 2 * k, bd + 2 * k, idesc, tmem + kSfA + 4 * k, tmem + kSfB + 8 * k, s > 0 || k > 0);
+          if (el) {
+            const uint32_t at = ring + st * slot_bytes, sfa = at + kACodes + slot_b, sfb = sfa + kSfABytes;
+            const uint64_t ad = umma_desc(at, 16, 1024) | kSwizzle128, bd = umma_desc(at + kACodes, 16, 1024) | kSwizzle128;
+            const int steps = min(kSteps, (a.K - s * kStageK) / 64);
+            for (int k = 0; k < steps; ++k) {
+              pair_cp_sf(tmem + kSfA + 4 * k, umma_desc(sfa + 512 * k, 128, 128));
+              pair_cp_sf(tmem + kSfB + 8 * k, umma_desc(sfb + 512 * chunks * k, 128, 128));
+              if (n > 128) pair_cp_sf(tmem + kSfB + 8 * k + 4, umma_desc(sfb + 512 * chunks * k + 512, 128, 128));
+              pair_mma(acc, ad + 2 * k, bd + 2 * k, idesc, tmem + kSfA + 4 * k, tmem + kSfB + 8 * k, s > 0 || k > 0);
+            }
+            pair_commit(bar(bars.empty[st]), 3);
           }
-          tc_commit(bar(bars.empty[st]));
+          __syncwarp();
           if (++st == a.stages) st = 0, ph ^= 1;
         }
-        if (ok) tc_commit(bar(bars.accf[d]));
+        if (ok && el) pair_commit(bar(bars.accf[d]), 3);
+        __syncwarp();
       }
       // what is still in flight ends before the block does
-      tc_commit(bar(bars.done));
-      mbar_wait(bar(bars.done), 0, gtimer() + kOpsWaitNs, &never);
+      if (el) {
+        pair_commit(bar(bars.done), 1);
+        mbar_wait(bar(bars.done), 0, gtimer() + kOpsWaitNs, &never);
+      }
+      __syncwarp();
     }
-  } else if (warp < 2 + kScaleWarps) {
-    // --- scales ---------------------------------------------------------------
-    // A thread has a row of the tile and up to two tokens.  Four lanes of a
-    // quarter warp's rows, 32 apart, make the 16 bytes that follow each other.
-    const int r32 = (warp - 2) * 8 + (lane >> 2), r4 = lane & 3, row = 32 * r4 + r32;
-    const int total = mine * kst, pitch = a.K / 16;
+  } else if (warp >= kScaleWarp0 && warp < kEpiWarp0) {
+    // --- scales, and gathered tokens ----------------------------------------------
+    // A thread has a row of the block's weights and up to two tokens.  Four lanes
+    // of a quarter warp's rows, 32 apart, make the 16 bytes that follow each other.
+    const int sw = warp - kScaleWarp0, r32 = sw * 8 + (lane >> 2), r4 = lane & 3, row = 32 * r4 + r32;
+    const int pitch = a.K / 16, units = (kst + 1) / 2;  // (a unit: two stages)
     const uint8_t *pa = nullptr, *pb[2] = {nullptr, nullptr};
-    int fi = 0, fs = 0;  // tile and stage of the next loads
-    uint4 va[kAhead], vb[kAhead][2];
-    auto load = [&](const uint8_t* p, int s) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (p == nullptr) return v;
-      if (a.vec) return __ldg(reinterpret_cast<const uint4*>(p) + s);
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + 4 * s;
-      const int left = a.K / 64 - 4 * s;
-      v.x = __ldg(q);
-      if (left > 1) v.y = __ldg(q + 1);
-      if (left > 2) v.z = __ldg(q + 2);
-      if (left > 3) v.w = __ldg(q + 3);
-      return v;
+    int fi = 0, fu = 0;  // tile and unit of the next loads
+    uint32_t v[2][3][8];
+    auto load = [&](const uint8_t* p, int u, uint32_t (&w)[8]) {
+      if (p == nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 0u;
+      } else if (a.vec == 32) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p + u * 32));
+      } else {
+        const int left = a.K / 64 - 8 * u;  // (words of the row from here)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 0u;
+        if (a.vec == 16) {
+          const uint4 lo = __ldg(reinterpret_cast<const uint4*>(p + u * 32));
+          w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
+          if (left > 4) {
+            const uint4 hi = __ldg(reinterpret_cast<const uint4*>(p + u * 32 + 16));
+            w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < left) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p + u * 32) + j);
+        }
+      }
     };
-    auto fetch = [&](uint4& ra, uint4 (&rb)[2]) {
-      if (fi >= mine) return;
-      if (fs == 0) {
-        const Tile t = tile_at(fi);
-        int wr = t.m * kM + row;  // the row of the matrix
+    bool ok = true;
+    auto fetch = [&](uint32_t (&w)[3][8]) {
+      if (fi >= mine || !ok) return;
+      if (fu == 0) {
+        ok = wait_tile(fi);
+        if (!ok) return;
+        const Tile& t = tile_ring[fi % kTiles];
+        int wr = t.m * 256 + rank * 128 + row;  // the row of the matrix
         const uint8_t* base = a.w_scales;
         if (GLU) {
-          wr = t.m * 64 + (row >> 5) * 16 + (row & 15);
+          wr = t.m * 128 + rank * 64 + (row >> 5) * 16 + (row & 15);
           if (row & 16) base = a.up_scales;
         }
         pa = wr < a.rows ? base + ((long long)t.e * a.rows + wr) * pitch : nullptr;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int k = row + 128 * c;
-          pb[c] = k < t.count ? a.x_scales + (long long)source(t.p0 + k) * pitch : nullptr;
+          const int src = source_ring[fi % kTiles][row + 128 * c];
+          pb[c] = src >= 0 ? a.x_scales + (long long)src * pitch : nullptr;
         }
       }
-      ra = load(pa, fs);
-      rb[0] = load(pb[0], fs);
-      rb[1] = load(pb[1], fs);
-      if (++fs == kst) fs = 0, ++fi;
+      load(pa, fu, w[0]);
+      load(pb[0], fu, w[1]);
+      if (chunks == 2) load(pb[1], fu, w[2]);
+      if (++fu == units) fu = 0, ++fi;
     };
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) fetch(va[d], vb[d]);
-    int st = 0;
-    uint32_t ph = 1;
-    bool ok = true;
-    for (int n0 = 0; n0 < total && ok; n0 += kAhead) {
-#pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
-        if (n0 + d >= total || !ok) break;
-        ok = wait_warp(bars.empty[st], ph);
-        if (!ok) break;
-        const uint32_t sfa = ring + st * slot_bytes + slot_a + slot_b + 16 * r32 + 4 * r4, sfb = sfa + slot_sfa;
-        const uint32_t wa[4] = {va[d].x, va[d].y, va[d].z, va[d].w};
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) sts32(sfa + 512 * k, wa[k]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c >= chunks) break;
-          const uint32_t wb[4] = {vb[d][c].x, vb[d][c].y, vb[d][c].z, vb[d][c].w};
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k) sts32(sfb + 512 * (chunks * k + c), wb[k]);
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bars.sfull[st]));
-        fetch(va[d], vb[d]);
-        if (++st == a.stages) st = 0, ph ^= 1;
-      }
-    }
-  } else {
-    // --- epilogue -------------------------------------------------------------
-    const int quad = warp & 3, half = (warp - 2 - kScaleWarps) >> 2;
-    bool ok = true;
-    for (int i = 0; i < mine && ok; ++i) {
-      const Tile t = tile_at(i);
-      const int d = i & 1;
-      // The tensors' scales: a significand and two halves of a power of two, so
-      // that no product leaves fp32's range unless the result does.
-      float f[2][2];
-#pragma unroll
-      for (int u = 0; u < (GLU ? 2 : 1); ++u) {
-        const float* p = u ? a.up_ts : a.w_ts;
-        const double ts = (double)(p != nullptr ? __ldg(p + t.e) : 1.f) * (double)a.x_ts;
-        const int ex = (int)((__double2hiint(ts) >> 20) & 0x7FF);
-        if (ex == 0 || ex == 0x7FF) {  // (zero, infinite or NaN)
-          f[u][0] = (float)ts, f[u][1] = 1.f;
-        } else {
-          const int e2 = max(-250, min(250, ex - 1023)), h = e2 / 2;
-          f[u][0] = (float)(__hiloint2double((__double2hiint(ts) & 0x800FFFFF) | 0x3FF00000, __double2loint(ts))) * exp2i(h);
-          f[u][1] = exp2i(e2 - h);
-        }
-      }
-      ok = wait_warp(bars.accf[d], (i >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + d * kAccCols;
-      auto store = [&](int c, int row, float v) {
-        const long long o = (long long)(t.p0 + c) * a.y_stride + row;
-        if (a.y_dtype == MSK_FP32) static_cast<float*>(a.y)[o] = v;
-        else if (a.y_dtype == MSK_FP16) static_cast<__half*>(a.y)[o] = __float2half_rn(v);
-        else static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
-      };
-      for (int c0 = 16 * half; c0 < t.n; c0 += 32) {
-        float v[16];
-        tmem_ld16(at + c0, v);
-        if (!GLU) {
-          const int row = t.m * kM + quad * 32 + lane;
-          if (row < a.rows) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c0 + j < t.count) store(c0 + j, row, v[j] * f[0][0] * f[0][1]);
-          }
-        } else {
-          // lane l < 16 ends column j, lane l + 16 column j + 1
-          const bool up = lane >= 16;
-          const int row = t.m * 64 + quad * 16 + (lane & 15);
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float mine_v = up ? v[j + 1] : v[j], other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + 1], 16);
-            const float g = (up ? other : mine_v) * f[0][0] * f[0][1], u = (up ? mine_v : other) * f[1][0] * f[1][1];
-            // silu(g) = g / (1 + e^-g), from e^-|g|, which does not overflow
-            const float ex = expf(-fabsf(g)), s = g * ((g >= 0.f ? 1.f : ex) / (1.f + ex));
-            if (row < a.rows && c0 + j + up < t.count) store(c0 + j + up, row, s * u);
-          }
-        }
-      }
-      tc_fence_before();
+    // hands a stage over: what this warp's threads have written is seen by the tensor cores
+    auto hand_over = [&](int slot) {
+      fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(bars.acce[d]));
+      if (lane == 0) mbar_arrive_cluster(first(bars.sfull[slot]));
+    };
+    fetch(v[0]);
+    fetch(v[1]);
+    int st = 0, behind = 0, flight = 0;  // (stages whose gathered rows are on their way, and the first one's slot)
+    uint32_t ph = 1;
+    int i = 0, s = 0;  // tile and stage
+    const uint8_t* src[8];
+    int n = 0;
+    while (i < mine && ok) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        if (i >= mine || !ok) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (s >= kst || !ok) break;
+          if (GATHER && s == 0) {
+            // (the tile is there: its scales have been asked for)
+            const Tile& t = tile_ring[i % kTiles];
+            n = t.n;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int k = 4 * (sw + 4 * j) + (lane >> 3);
+              const int r = k < n / 2 ? source_ring[i % kTiles][rank * (n / 2) + k] : -1;
+              src[j] = r >= 0 ? a.x_codes + (long long)r * (a.K / 2) + (lane & 7) * 16 : nullptr;
+            }
+          }
+          ok = wait(bars.empty[st], ph);
+          if (!ok) break;
+          const uint32_t slot = ring + st * slot_bytes;
+          if (GATHER) {
+            const bool inside = s * (kStageK / 2) + (lane & 7) * 16 < a.K / 2;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int k = 4 * (sw + 4 * j) + (lane >> 3);
+              if (4 * (sw + 4 * j) >= n / 2) break;
+              // (what is not copied may hold anything but a NaN's scale: codes have none)
+              if (src[j] != nullptr && inside)
+                cp_async16(slot + kACodes + k * 128 + ((((lane & 7) ^ k) & 7) << 4), src[j] + s * (kStageK / 2));
+            }
+            cp_async_commit();
+          }
+          const uint32_t sfa = slot + kACodes + slot_b + 16 * r32 + 4 * r4, sfb = sfa + kSfABytes;
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) sts32(sfa + 512 * k, v[d][0][4 * h + k]);
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) sts32(sfb + 512 * chunks * k, v[d][1][4 * h + k]);
+          if (chunks == 2) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) sts32(sfb + 512 * (2 * k + 1), v[d][2][4 * h + k]);
+          }
+          if (!GATHER) {
+            hand_over(st);
+          } else if (++flight > kLag) {
+            cp_async_wait_group<kLag>();
+            hand_over(behind);
+            if (++behind == a.stages) behind = 0;
+            --flight;
+          }
+          if (++st == a.stages) st = 0, ph ^= 1;
+          ++s;
+        }
+        fetch(v[d]);
+        if (s == kst) leave_tile(i), ++i, s = 0;
+      }
     }
+    if (GATHER) {
+      cp_async_wait_all();
+      for (; flight > 0 && ok; --flight) {
+        hand_over(behind);
+        if (++behind == a.stages) behind = 0;
+      }
+    }
+  } else if (warp >= kEpiWarp0) {
+    // --- epilogue -------------------------------------------------------------
+    const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    auto run = [&](auto type) {
+      using T = decltype(type);
+      bool ok = true;
+      for (int i = 0; i < mine && ok; ++i) {
+        const int d = i & 1;
+        ok = wait_tile(i) && wait(bars.accf[d], (i >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const Tile& t = tile_ring[i % kTiles];
+        const int n = t.n, count = t.count;
+        const float f0 = t.f[0], f1 = t.f[1], u0 = t.f[2], u1 = t.f[3];
+        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + d * kAcc1;
+        const int up = GLU ? lane >> 4 : 0;
+        const int row = GLU ? t.m * 128 + rank * 64 + quad * 16 + (lane & 15) : t.m * 256 + rank * 128 + quad * 32 + lane;
+        T* y = static_cast<T*>(a.y) + (long long)(t.p0 + up) * a.y_stride + row;
+        const bool in = row < a.rows;
+        // chunks of 16 tokens, this half's first or last ones first: those that overlap the other accumulator
+        const int nc = (n / 16 + 1 - half) / 2;  // (of this half)
+        bool told = false;
+        for (int c = 0; c < nc; ++c) {
+          const int c0 = 16 * half + 32 * (d ? c : nc - 1 - c);
+          if (!told && (d ? c0 >= kMaxN - kAcc1 : c0 < kAcc1)) {
+            told = true;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(first(bars.over[d]));
+          }
+          float v[16];
+          tmem_ld16(at + c0, v);
+          if (!GLU) {
+            T* p = y + (long long)c0 * a.y_stride;
+            if (in) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (c0 + j < count) *p = static_cast<T>(v[j] * f0 * f1);
+                p += a.y_stride;
+              }
+            }
+          } else {
+            // lane l < 16 ends column j, lane l + 16 column j + 1
+            T* p = y + (long long)c0 * a.y_stride;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float own = up ? v[j + 1] : v[j], other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + 1], 16);
+              const float g = (up ? other : own) * f0 * f1, u = (up ? own : other) * u0 * u1;
+              // silu(g) = g / (1 + e^-g), from e^-|g|, which does not overflow
+              const float ex = expf(-fabsf(g)), s = g * ((g >= 0.f ? 1.f : ex) / (1.f + ex));
+              if (in && c0 + j + up < count) *p = static_cast<T>(s * u);
+              p += 2 * a.y_stride;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (!told) mbar_arrive_cluster(first(bars.over[d]));
+          mbar_arrive_cluster(first(bars.acce[d]));
+        }
+        leave_tile(i);
+      }
+    };
+    if (a.y_dtype == MSK_FP32) run(float());
+    else if (a.y_dtype == MSK_FP16) run(__half());
+    else run(__nv_bfloat16());
   }
   __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 2) {
-    tmem_relinquish();
-    tmem_dealloc(tmem, 512);
-  }
-  if (tid == 0 && abort) {
+  if (tid == 0 && *ab) {
     atomicExch(&g_error, 1u);
     // copies end before the block does: a slot's newest may be a use ahead of what was waited for
     for (uint32_t q = 0; q < 2; ++q)
       for (int k = 0; k < a.stages; ++k) mbar_wait(bar(bars.full[k]), q, gtimer() + kOpsWaitNs / 100, &never);
   }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // (no block leaves while the pair's MMAs, copies or arrivals may come to it)
+  tc_fence_after();
+  if (warp == 3) pair_tmem_free(tmem, 512);
+}
+
+// Clusters of two that run at a time, looked up once a device.
+template <bool GLU, bool GATHER>
+int pairs_at_once() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev].load(std::memory_order_acquire);
+  if (n == 0) {
+    if (cudaFuncSetAttribute(experts4_kernel<GLU, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return 0;
+    const OpsLaunch l(dim3(2), kProductThreads, kSmem, nullptr, 2);
+    cudaLaunchConfig_t cfg = l.cfg;
+    cudaLaunchAttribute at = l.at[1];
+    cfg.attrs = &at, cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, experts4_kernel<GLU, GATHER>, &cfg) != cudaSuccess || n < 1) return 0;
+    known[dev].store(n, std::memory_order_release);
+  }
+  return n;
+}
+
+template <bool GLU, bool GATHER>
+cudaError_t launch_products(const Experts4& a, long long tiles, cudaStream_t st) {
+  const int pairs = pairs_at_once<GLU, GATHER>();
+  if (pairs == 0) return cudaErrorInvalidConfiguration;
+  const OpsLaunch l(dim3(2 * (unsigned)std::min<long long>(pairs, tiles)), kProductThreads, kSmem, st, 2);
+  return cudaLaunchKernelEx(&l.cfg, experts4_kernel<GLU, GATHER>, a);
 }
 
 bool check_experts(const msk_fp4_experts* w, msk_status& s) {
@@ -570,35 +757,30 @@ extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* sl
   s = ops_device(&nsm);
   if (s != MSK_OK) return s;
   Experts4 a{};
-  a.x_scales = x->scales, a.w_scales = w->scales, a.w_ts = w->tensor_scales;
+  a.x_codes = x->packed, a.x_scales = x->scales, a.w_scales = w->scales, a.w_ts = w->tensor_scales;
   if (up != nullptr) a.up_scales = up->scales, a.up_ts = up->tensor_scales;
   a.offsets = offsets, a.slots = slots, a.y = y, a.y_stride = n > 1 ? y_stride : 0, a.x_rows = x->rows;
   a.n = (int)n, a.E = w->n_experts, a.rows = (int)w->rows, a.K = (int)w->cols, a.top_k = top_k, a.y_dtype = y_dtype;
   a.x_ts = x->tensor_scale;
-  a.vec = a.K % kStageK == 0;
-  a.mblocks = (a.rows + (up != nullptr ? 64 : kM) - 1) / (up != nullptr ? 64 : kM);
-  a.nt = (int)std::min<int64_t>(kMaxN, (n + 15) / 16 * 16);
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(x->scales) | reinterpret_cast<uintptr_t>(w->scales) |
+                         (up != nullptr ? reinterpret_cast<uintptr_t>(up->scales) : 0) | (uintptr_t)(a.K / 16);
+  a.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 4;
+  const int per = up != nullptr ? 128 : 256;  // the matrix's rows of a tile
+  a.mblocks = (a.rows + per - 1) / per;
+  a.nt = (int)std::min<int64_t>(kMaxN, (n + kStepN - 1) / kStepN * kStepN);
   const long long tiles = (long long)a.mblocks * ((n + a.nt - 1) / a.nt + std::min<int64_t>(n, a.E));  // at most
   if (tiles > (1ll << 31) - 1 - 65536) return MSK_ERR_SHAPE;
-  const int slot = kACodes + a.nt * (kStageK / 2) + kM * kStageK / 16 + (a.nt > 128 ? 2 : 1) * 512 * kSteps;
+  const int slot = kACodes + a.nt / 2 * (kStageK / 2) + kSfABytes + (a.nt > 128 ? 2 : 1) * 512 * kSteps;
   a.stages = std::min(kMaxStages, kRing / slot);
   const CUtensorMapDataType bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const long long wrows = (long long)a.E * a.rows;
   const int box = up != nullptr ? 16 : kM;
   if (!matrix_map(&a.w_map, bytes, w->packed, wrows, a.K / 2, a.K / 2, box, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
       (up != nullptr && !matrix_map(&a.up_map, bytes, up->packed, wrows, a.K / 2, a.K / 2, box, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B)) ||
-      !matrix_map(&a.x_map, bytes, x->packed, x->rows, a.K / 2, a.K / 2, slots != nullptr ? 1 : 16, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B))
+      (slots == nullptr && !matrix_map(&a.x_map, bytes, x->packed, x->rows, a.K / 2, a.K / 2, 16, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B)))
     return MSK_ERR_CUDA;
-  static std::atomic<bool> ready[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSK_ERR_CUDA;
-  if (!ready[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(experts4_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(experts4_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-      return MSK_ERR_CUDA;
-    ready[dev].store(true, std::memory_order_release);
-  }
-  const OpsLaunch l(dim3((unsigned)std::min<long long>(nsm, tiles)), kProductThreads, kSmem, static_cast<cudaStream_t>(stream));
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, up != nullptr ? experts4_kernel<true> : experts4_kernel<false>, a);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = up != nullptr ? (slots != nullptr ? launch_products<true, true>(a, tiles, st) : launch_products<true, false>(a, tiles, st))
+                                      : (slots != nullptr ? launch_products<false, true>(a, tiles, st) : launch_products<false, false>(a, tiles, st));
   return e == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }

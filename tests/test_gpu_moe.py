@@ -282,6 +282,15 @@ def test_products(M, counts, rows, cols, glu, gather):
     run_products(M, counts, rows, cols, glu, gather)
 
 
+@pytest.mark.parametrize("counts,rows,cols", [
+    ([3] * 300, 600, 64), ([40, 0] * 100, 520, 128), ([256] * 40, 1030, 320), ([209, 256, 208, 31, 255, 240, 1, 224] * 12, 520, 512),
+    ([500, 7, 213] * 20, 600, 192)])
+@pytest.mark.parametrize("glu,gather", [(False, False), (True, False), (False, True), (True, True)])
+def test_products_of_many_tiles(M, counts, rows, cols, glu, gather):
+    """Several tiles for a pair of blocks, of one stage and more, of few tokens and so many that accumulators overlap."""
+    run_products(M, counts, rows, cols, glu, gather)
+
+
 @pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("glu", [False, True])
 def test_products_types_and_strides(M, out, glu):
