@@ -205,8 +205,27 @@ __device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* ma
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// Arrives on a barrier of the pair's first block.  At the block's scope: a release
+// at the cluster's waits for everything that the thread has under way, some 1200
+// clocks.  What is said is that tensor memory has been read (tcgen05's own fences
+// order that), or that this block's shared memory is ready for its own SM's tensor
+// core (the fence between the proxies orders that).
+__device__ __forceinline__ void pair_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// g / (1 + e^-g), off by some 2^-22: from e^-|g|, which does not overflow, by 2^t for
+// t = -|g| log2(e) and what t's rounding and the constant's leave.
+__device__ __forceinline__ float silu(float g) {
+  const float m = -fabsf(g), t = m * 1.4426950409f, left = fmaf(m, 1.4426950409f, -t) + m * 1.9259629911e-8f;
+  float p, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(p) : "f"(t));
+  p = fmaf(p, left * 0.6931471806f, p);
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + p));
+  return g * ((g >= 0.f ? 1.f : p) * r);
 }
 
 // y^T = W x^T by block-scaled NVFP4 on the fifth-generation tensor cores.  A pair
@@ -236,7 +255,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   __shared__ Tile tile_ring[kTiles];
   __shared__ int source_ring[kTiles][kMaxN];  // rows of x of a tile's tokens
   __shared__ uint32_t tmem_base;
-  __shared__ int abort, never, tiles_all;
+  __shared__ int abort, never, tiles_all, warp_tiles[kProductThreads / 32];
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   // (dynamic shared memory starts at a multiple of 1024 in the shared window)
@@ -272,38 +291,60 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   grid_dep_wait();
   grid_dep_launch();
 
-  // The experts' places (whatever the offsets hold, ranges in [0, n] that do not
-  // overlap) and tiles.
-  if (warp == 2) {
-    int at = 0, tiles = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      int from = 0, last = 0;
-      if (e < a.E) {
-        from = max(0, min(a.n, __ldg(a.offsets + e)));
-        last = max(0, min(a.n, __ldg(a.offsets + e + 1)));
-      }
-      int end = max(from, last);
+  // The experts' places and tiles.  Whatever the offsets hold, ranges lie in [0, n]
+  // and do not overlap: an expert begins where the ones before have ended.
+  constexpr int kPer = kMaxE / kProductThreads;
+  {
+    int from[kPer], last[kPer];
+    bool rising = true;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, end, o);
-        if (lane >= o) end = max(end, v);
-      }
-      const int before = __shfl_up_sync(0xFFFFFFFFu, end, 1);
-      from = max(from, lane > 0 ? max(at, before) : at);
-      end = max(end, at);
-      const int count = max(0, last - from);
-      int t = (count + a.nt - 1) / a.nt * a.mblocks;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, t, o);
-        if (lane >= o) t += v;
-      }
-      if (e < a.E) starts[e] = from, counts[e] = count, ends[e] = tiles + t;
-      tiles += __shfl_sync(0xFFFFFFFFu, t, 31);
-      at = __shfl_sync(0xFFFFFFFFu, end, 31);
+    for (int j = 0; j < kPer; ++j) {
+      const int e = kPer * tid + j;
+      from[j] = e < a.E ? max(0, min(a.n, __ldg(a.offsets + e))) : 0;
+      last[j] = e < a.E ? max(0, min(a.n, __ldg(a.offsets + e + 1))) : 0;
+      rising = rising && from[j] <= last[j];
     }
-    if (lane == 0) tiles_all = tiles;
+    if (!__syncthreads_and(rising)) {  // (not what a sort gives)
+      for (int j = 0; j < kPer; ++j) counts[kPer * tid + j] = last[j];
+      __syncthreads();
+      if (tid == 0) {
+        int at = 0;
+        for (int e = 0; e < a.E; ++e) {
+          starts[e] = max(at, e > 0 ? counts[e - 1] : max(0, min(a.n, __ldg(a.offsets))));
+          at = max(starts[e], counts[e]);
+          if (e > 0) counts[e - 1] = ends[e - 1];
+          ends[e] = max(0, counts[e] - starts[e]);
+        }
+        counts[a.E - 1] = ends[a.E - 1];
+      }
+      __syncthreads();
+      for (int j = 0; j < kPer; ++j)
+        if (kPer * tid + j < a.E) from[j] = starts[kPer * tid + j], last[j] = from[j] + counts[kPer * tid + j];
+      __syncthreads();
+    }
+    int sum = 0, upto[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) sum += (last[j] - from[j] + a.nt - 1) / a.nt * a.mblocks, upto[j] = sum;
+    int scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) warp_tiles[warp] = scan;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kProductThreads / 32; ++w) {
+      const int v = warp_tiles[w];
+      before += w < warp ? v : 0, all += v;
+    }
+    if (tid == 0) tiles_all = all;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int e = kPer * tid + j;
+      if (e < a.E) starts[e] = from[j], counts[e] = last[j] - from[j], ends[e] = before + scan - sum + upto[j];
+    }
   }
   tc_fence_before();
   cluster_sync();  // (of the block too)
@@ -349,10 +390,16 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
       const int step = ((all + nb - 1) / nb + kStepN - 1) / kStepN * kStepN;  // tokens of a tile, the same for all but the last
       const int p0 = starts[lo] + j * step, count = min(step, all - j * step);
       Tile& r = tile_ring[i % kTiles];
-      for (int k = lane; k < kMaxN; k += 32) {
-        int p = k < count ? p0 + k : -1;
-        if (GATHER && k < count) p = max(0, min((int)a.x_rows - 1, (int)((unsigned)max(__ldg(a.slots + p), 0) / (unsigned)a.top_k)));
-        source_ring[i % kTiles][k] = p;
+      int p[kMaxN / 32];
+#pragma unroll
+      for (int k = 0; k < kMaxN / 32; ++k) {
+        p[k] = lane + 32 * k < count ? p0 + lane + 32 * k : -1;
+        if (GATHER && p[k] >= 0) p[k] = __ldg(a.slots + p[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kMaxN / 32; ++k) {
+        if (GATHER && lane + 32 * k < count) p[k] = min((int)a.x_rows - 1, (int)((unsigned)max(p[k], 0) / (unsigned)a.top_k));
+        source_ring[i % kTiles][lane + 32 * k] = p[k];
       }
       if (lane < (GLU ? 2 : 1)) {
         // The tensors' scales: a significand and a power of two in two halves, so
@@ -518,7 +565,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     auto hand_over = [&](int slot) {
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(first(bars.sfull[slot]));
+      if (lane == 0) pair_arrive(first(bars.sfull[slot]));
     };
     fetch(v[0]);
     fetch(v[1]);
@@ -619,7 +666,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
             told = true;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(first(bars.over[d]));
+            if (lane == 0) pair_arrive(first(bars.over[d]));
           }
           float v[16];
           tmem_ld16(at + c0, v);
@@ -639,8 +686,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
             for (int j = 0; j < 16; j += 2) {
               const float own = up ? v[j + 1] : v[j], other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + 1], 16);
               const float g = (up ? other : own) * f0 * f1, u = (up ? own : other) * u0 * u1;
-              // silu(g) = g / (1 + e^-g), from e^-|g|, which does not overflow
-              const float ex = expf(-fabsf(g)), s = g * ((g >= 0.f ? 1.f : ex) / (1.f + ex));
+              const float s = silu(g);
               if (in && c0 + j + up < count) *p = static_cast<T>(s * u);
               p += 2 * a.y_stride;
             }
@@ -649,8 +695,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (!told) mbar_arrive_cluster(first(bars.over[d]));
-          mbar_arrive_cluster(first(bars.acce[d]));
+          if (!told) pair_arrive(first(bars.over[d]));
+          pair_arrive(first(bars.acce[d]));
         }
         leave_tile(i);
       }
