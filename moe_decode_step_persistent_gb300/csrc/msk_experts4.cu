@@ -114,32 +114,33 @@ msk_status rows_call(bool write, const void* x, int32_t dtype, int64_t rows, int
 constexpr int kM = 128;            // weight rows of a block (a pair's MMA has M = 256)
 constexpr int kStageK = 256;       // columns of a stage
 constexpr int kSteps = kStageK / 64;  // MMAs of a stage
-constexpr int kMaxN = 256;         // tokens of a tile at most (the MMA's N)
+constexpr int kMaxN = 256;         // tokens of a tile at most (the MMA's N); half of it where a tile has gate and up
 constexpr int kStepN = 32;         // ... and what they are filled up to: each block has half of them, in boxes of 16
 constexpr int kMaxStages = 10;
 constexpr int kMaxE = 1024;
 constexpr int kScaleWarps = 4, kEpiWarps = 8;
 constexpr int kScaleWarp0 = 4, kEpiWarp0 = kScaleWarp0 + kScaleWarps;
 constexpr int kProductThreads = 32 * (kEpiWarp0 + kEpiWarps);
-// Tiles whose places are known ahead: the scales are asked for two tiles ahead where
-// a tile is one stage, while kLag stages behind are not handed over yet.
+// Tiles whose places are known ahead: four are at the warps that write scales where
+// a tile is one stage, and two at their ends.
 constexpr int kTiles = 8;
-constexpr int kLag = 3;            // stages of gathered rows on their way when one is handed over
-static_assert(kTiles > kLag + 1, "a tile that is waited for is not held up by one that is not handed over");
 constexpr int kACodes = kM * kStageK / 2, kSfABytes = kM * kStageK / 16;
 constexpr int kRing = 204 * 1024;  // (dynamic shared memory: beside it the tables below and what aligns the ring)
 constexpr int kTables = 3 * kMaxE * 4;
 constexpr int kSmem = 1024 + kRing + kTables;
 // Tensor memory columns: two accumulators, which overlap where a tile has more
-// than kAcc1 tokens, then the scales of a stage's rows and tokens.
-constexpr int kAcc1 = 208, kSfA = kAcc1 + kMaxN, kSfB = kSfA + 4 * kSteps;
-static_assert(kSfB + 8 * kSteps == 512, "tensor memory");
+// than kAcc1 columns (a token's, or a token's gate and up), then the scales of a
+// stage: of weights and up to 256 tokens, or of gate, up and up to 128 tokens.
+constexpr int kAcc1 = 208, kSf = kAcc1 + 256;
+static_assert(kSf + 12 * kSteps == 512, "tensor memory");
 
 static __device__ uint32_t g_error;  // nonzero once a wait has run out
 
 struct Experts4 {
-  CUtensorMap w_map, up_map;  // [E rows][cols / 2] bytes, boxes of 128 x 128 (GLU: of 16 x 128)
-  CUtensorMap x_map;          // [x_rows][cols / 2] bytes, boxes of 16 x 128
+  CUtensorMap w_map, up_map;     // [E rows][cols / 2] bytes, boxes of 128 x 128
+  CUtensorMap x_map, x16_map;    // [x_rows][cols / 2] bytes, boxes of 64 x 128, of 16 x 128
+  CUtensorMap ws_map, us_map;    // [E rows][cols / 16] bytes of scales, boxes of 128 x 16
+  CUtensorMap xs_map;            // [x_rows][cols / 16], boxes of nt x 16
   const uint8_t *x_codes, *x_scales, *w_scales, *up_scales;
   const float *w_ts, *up_ts;
   const int32_t *offsets, *slots;
@@ -147,7 +148,8 @@ struct Experts4 {
   long long y_stride, x_rows;
   int n, E, rows, K, top_k, y_dtype, nt, stages, mblocks;
   float x_ts;
-  int vec;  // scales in pieces of 32, 16 or 4 bytes
+  int vec;    // scales that threads load: in pieces of 16 or 4 bytes
+  bool tiled; // the weights' scales, and those of tokens that are not gathered, come by tiled copies
 };
 
 // A tile: the pair's 256 weight rows of an expert and up to nt of its tokens.
@@ -159,7 +161,7 @@ struct Tile {
 };
 
 struct Bars {
-  uint64_t full[kMaxStages], sfull[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxStages], rfull[kMaxStages], sfull[kMaxStages], empty[kMaxStages];
   uint64_t accf[2], acce[2], over[2];
   uint64_t tfull[kTiles], tempty[kTiles];
   uint64_t done;
@@ -217,6 +219,11 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// A row's scales of four steps, `step` bytes from one to the next.
+__device__ __forceinline__ void put_scales(uint32_t addr, int step, uint4 w) {
+  sts32(addr, w.x), sts32(addr + step, w.y), sts32(addr + 2 * step, w.z), sts32(addr + 3 * step, w.w);
+}
+
 // g / (1 + e^-g), off by some 2^-22: from e^-|g|, which does not overflow, by 2^t for
 // t = -|g| log2(e) and what t's rounding and the constant's leave.
 __device__ __forceinline__ float silu(float g) {
@@ -230,17 +237,18 @@ __device__ __forceinline__ float silu(float g) {
 
 // y^T = W x^T by block-scaled NVFP4 on the fifth-generation tensor cores.  A pair
 // of blocks (a cluster) has a tile of M = 256 weight rows, 128 each, and N = up to
-// 256 tokens of one expert, of which each block loads half: an SM takes no more
-// than 50 bytes a clock out of L2, and a tile of a block's own would need 192 bytes
-// a K step of 64 where a pair's needs 128 (for 128 clocks of MMA).
+// 256 tokens of one expert, of which each block loads half: alone, a block would
+// load 384 rows where it loads 256 now, and loads bound the kernel as much as MMAs.
+// GLU: a tile has 256 rows of gate and the same of up, and up to 128 tokens, so that
+// a lane's accumulators hold both of its row.
 // Weights and tokens come by tiled copies with the 128-byte swizzle, tokens named
 // by slots by asynchronous copies of 16 bytes (gathering tiled copies take 66
-// clocks for four rows of 128 bytes); the scales, row-major in memory, by plain
-// loads some stages ahead, written as the tensor cores want them.  Tiles run over
-// experts, then blocks of weight rows, then tokens, so that neighbouring pairs
+// clocks for four rows of 128 bytes).  Scales, row-major in memory, come by tiled
+// copies too and are put into the tensor cores' order by threads, those of gathered
+// tokens, and of columns that are no multiple of 256, by plain loads some stages
+// ahead (a load of 32 rows' scales holds the load unit for 61 clocks).  Tiles run
+// over experts, then blocks of weight rows, then tokens, so that neighbouring pairs
 // share weights in L2; a pair takes every one that is a multiple of the pairs on.
-// GLU: a block's rows are 64 gate and 64 up rows, 16 and 16 in turn, so that a
-// lane's partner 16 lanes on holds the up value of its gate value.
 //
 // Roles: a warp that finds the tiles and their tokens, one that copies weights, one
 // that copies tokens, one that issues (of the pair's first block), four that write
@@ -266,19 +274,28 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   int* ends = counts + kMaxE;                           // [E]: tiles up to and with each expert
   const int chunks = a.nt > 128 ? 2 : 1;                // of tokens' scales, 128 rows each
   const int slot_b = a.nt / 2 * (kStageK / 2);
-  const int slot_bytes = kACodes + slot_b + kSfABytes + chunks * 512 * kSteps;
+  // in a slot: weights (gate, up), tokens, the weights' scales, the tokens'.  Scales are put in
+  // order where they have come to: a warp's threads write what they have read.
+  constexpr int kMats = GLU ? 2 : 1, off_b = kMats * kACodes;
+  const int off_sfa = off_b + slot_b, off_sfb = off_sfa + kMats * kSfABytes, slot_bytes = off_sfb + chunks * 512 * kSteps;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
   auto first = [&](uint64_t& b) { return mapa(smem_u32(&b), 0); };  // the pair's first block's
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&a.w_map);
     if (GLU) prefetch_tensormap(&a.up_map);
-    if (!GATHER) prefetch_tensormap(&a.x_map);
+    if (!GATHER) prefetch_tensormap(&a.x_map), prefetch_tensormap(&a.x16_map);
+    if (a.tiled) {
+      prefetch_tensormap(&a.ws_map);
+      if (GLU) prefetch_tensormap(&a.us_map);
+      if (!GATHER) prefetch_tensormap(&a.xs_map);
+    }
   }
   if (tid == 32) {
     abort = 0, never = 0;
     for (int i = 0; i < a.stages; ++i)
-      mbar_init(bar(bars.full[i]), GATHER ? 1 : 2), mbar_init(bar(bars.sfull[i]), 2 * kScaleWarps), mbar_init(bar(bars.empty[i]), 1);
+      mbar_init(bar(bars.full[i]), GATHER ? 1 : 2), mbar_init(bar(bars.rfull[i]), GATHER ? 1 : 2),
+          mbar_init(bar(bars.sfull[i]), 2), mbar_init(bar(bars.empty[i]), 1);
     for (int i = 0; i < 2; ++i)
       mbar_init(bar(bars.accf[i]), 1), mbar_init(bar(bars.acce[i]), 2 * kEpiWarps), mbar_init(bar(bars.over[i]), 2 * kEpiWarps);
     for (int i = 0; i < kTiles; ++i)
@@ -354,16 +371,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   const int kst = (a.K + kStageK - 1) / kStageK;  // stages of a tile
   const uint64_t deadline = gtimer() + kOpsWaitNs + (uint64_t)mine * kst * kOpsStepNs;
   const volatile int* ab = &abort;
-  // Waits by whole warps, for arrivals of this block and of the pair.
+  // Waits by whole warps.
   auto wait = [&](uint64_t& b, uint32_t parity) {
     const bool ok = mbar_wait(bar(b), parity, deadline, ab);
-    if (!ok) abort = 1;
-    return (bool)__all_sync(0xFFFFFFFFu, ok);
-  };
-  auto wait_pair = [&](uint64_t& b, uint32_t parity) {
-    bool ok = false;
-    for (uint32_t spins = 1; !(ok = mbar_try_wait_cluster(bar(b), parity)); ++spins)
-      if (spins % 64 == 0 && (*ab || gtimer() > deadline)) break;
     if (!ok) abort = 1;
     return (bool)__all_sync(0xFFFFFFFFu, ok);
   };
@@ -431,21 +441,32 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
       if (!ok) break;
       const Tile& t = tile_ring[i % kTiles];
       const int n = t.n;
-      const int row = warp == 0 ? t.e * a.rows + t.m * (GLU ? 128 : 256) + rank * (GLU ? 64 : 128) : t.p0 + rank * (n / 2);
+      const int row = warp == 0 ? t.e * a.rows + t.m * 256 + rank * 128 : t.p0 + rank * (n / 2), p0 = t.p0;
       for (int s = 0; s < kst; ++s) {
         ok = wait(bars.empty[st], ph);
         if (!ok) break;
         if (el) {
           const uint32_t dst = ring + st * slot_bytes, b = first(bars.full[st]);
           const int x = s * (kStageK / 2);
-          if (rank == 0) mbar_arrive_expect_tx(bar(bars.full[st]), warp == 0 ? 2 * kACodes : n * (kStageK / 2));
+          if (rank == 0) mbar_arrive_expect_tx(bar(bars.full[st]), warp == 0 ? 2 * kMats * kACodes : n * (kStageK / 2));
+          const uint32_t r = bar(bars.rfull[st]);
+          const int xs = s * (kStageK / 16);
           if (warp == 1) {
-            for (int j = 0; j < n / 2; j += 16) pair_load_2d(dst + kACodes + j * 128, &a.x_map, x, row + j, b);
-          } else if (GLU) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) pair_load_2d(dst + j * 2048, j & 1 ? &a.up_map : &a.w_map, x, row + (j >> 1) * 16, b);
+            int j = 0;
+            for (; j + 64 <= n / 2; j += 64) pair_load_2d(dst + off_b + j * 128, &a.x_map, x, row + j, b);
+            for (; j < n / 2; j += 16) pair_load_2d(dst + off_b + j * 128, &a.x16_map, x, row + j, b);
+            if (a.tiled) {
+              mbar_arrive_expect_tx(r, a.nt * (kStageK / 16));
+              tma_load_2d(dst + off_sfb, &a.xs_map, xs, p0, r);
+            }
           } else {
             pair_load_2d(dst, &a.w_map, x, row, b);
+            if (GLU) pair_load_2d(dst + kACodes, &a.up_map, x, row, b);
+            if (a.tiled) {
+              mbar_arrive_expect_tx(r, kMats * kSfABytes);
+              tma_load_2d(dst + off_sfa, &a.ws_map, xs, row, r);
+              if (GLU) tma_load_2d(dst + off_sfa + kSfABytes, &a.us_map, xs, row, r);
+            }
           }
         }
         __syncwarp();
@@ -465,26 +486,29 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         if (!ok) break;
         const int n = __shfl_sync(0xFFFFFFFFu, tile_ring[i % kTiles].n, 0), d = i & 1;
         leave_tile(i);
-        ok = wait_pair(bars.acce[d], ((i >> 1) & 1) ^ 1);
+        ok = wait(bars.acce[d], ((i >> 1) & 1) ^ 1);
         // (accumulators that overlap: the tile before has been read there)
-        if (ok && i > 0 && (d ? before : n) > kAcc1) ok = wait_pair(bars.over[d ^ 1], ((i - 1) >> 1) & 1);
+        if (ok && i > 0 && kMats * (d ? before : n) > kAcc1) ok = wait(bars.over[d ^ 1], ((i - 1) >> 1) & 1);
         if (!ok) break;
         before = n;
         tc_fence_after();
         const uint32_t acc = tmem + d * kAcc1, idesc = idesc_mxf4nvf4(n) + (1u << 27);  // (M = 256)
         for (int s = 0; s < kst; ++s) {
-          ok = wait(bars.full[st], ph) && wait_pair(bars.sfull[st], ph);
+          ok = wait(bars.full[st], ph) && wait(bars.sfull[st], ph);
           if (!ok) break;
           tc_fence_after();
           if (el) {
-            const uint32_t at = ring + st * slot_bytes, sfa = at + kACodes + slot_b, sfb = sfa + kSfABytes;
-            const uint64_t ad = umma_desc(at, 16, 1024) | kSwizzle128, bd = umma_desc(at + kACodes, 16, 1024) | kSwizzle128;
+            const uint32_t at = ring + st * slot_bytes, sfa = at + off_sfa, sfb = at + off_sfb;
+            const uint64_t ad = umma_desc(at, 16, 1024) | kSwizzle128, bd = umma_desc(at + off_b, 16, 1024) | kSwizzle128;
             const int steps = min(kSteps, (a.K - s * kStageK) / 64);
             for (int k = 0; k < steps; ++k) {
-              pair_cp_sf(tmem + kSfA + 4 * k, umma_desc(sfa + 512 * k, 128, 128));
-              pair_cp_sf(tmem + kSfB + 8 * k, umma_desc(sfb + 512 * chunks * k, 128, 128));
-              if (n > 128) pair_cp_sf(tmem + kSfB + 8 * k + 4, umma_desc(sfb + 512 * chunks * k + 512, 128, 128));
-              pair_mma(acc, ad + 2 * k, bd + 2 * k, idesc, tmem + kSfA + 4 * k, tmem + kSfB + 8 * k, s > 0 || k > 0);
+              const uint32_t ta = tmem + kSf + 4 * k, tb = tmem + kSf + 4 * kMats * kSteps + (GLU ? 4 : 8) * k;
+              pair_cp_sf(ta, umma_desc(sfa + 512 * k, 128, 128));
+              if (GLU) pair_cp_sf(ta + 4 * kSteps, umma_desc(sfa + kSfABytes + 512 * k, 128, 128));
+              pair_cp_sf(tb, umma_desc(sfb + 512 * chunks * k, 128, 128));
+              if (!GLU && n > 128) pair_cp_sf(tb + 4, umma_desc(sfb + 512 * chunks * k + 512, 128, 128));
+              pair_mma(acc, ad + 2 * k, bd + 2 * k, idesc, ta, tb, s > 0 || k > 0);
+              if (GLU) pair_mma(acc + n, ad + (kACodes >> 4) + 2 * k, bd + 2 * k, idesc, ta + 4 * kSteps, tb, s > 0 || k > 0);
             }
             pair_commit(bar(bars.empty[st]), 3);
           }
@@ -503,140 +527,112 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     }
   } else if (warp >= kScaleWarp0 && warp < kEpiWarp0) {
     // --- scales, and gathered tokens ----------------------------------------------
-    // A thread has a row of the block's weights and up to two tokens.  Four lanes
-    // of a quarter warp's rows, 32 apart, make the 16 bytes that follow each other.
-    const int sw = warp - kScaleWarp0, r32 = sw * 8 + (lane >> 2), r4 = lane & 3, row = 32 * r4 + r32;
-    const int pitch = a.K / 16, units = (kst + 1) / 2;  // (a unit: two stages)
-    const uint8_t *pa = nullptr, *pb[2] = {nullptr, nullptr};
-    int fi = 0, fu = 0;  // tile and unit of the next loads
-    uint32_t v[2][3][8];
-    auto load = [&](const uint8_t* p, int u, uint32_t (&w)[8]) {
-      if (p == nullptr) {
+    // Each of these warps takes a stage in turn, so that four are under way: a stage
+    // takes some 700 clocks from its first wait to its hand-over, 1300 where tokens
+    // are gathered.  A thread has every 8th row and token of a block's 128, of which
+    // four make the 16 bytes that follow each other.
+    constexpr int kOf = 3;  // rows' scales of a stage, 128 each: weights (gate), tokens or up, tokens
+    const int sw = warp - kScaleWarp0, r8 = lane & 7, r4 = lane >> 3;
+    const int pitch = a.K / 16;
+    uint4 w[kOf][4];
+    // loads the scales that threads load of tile `t`, stage `s`
+    auto load = [&](const uint8_t* p, int s) {
+      if (a.vec == 16) return __ldg(reinterpret_cast<const uint4*>(p) + s);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + 4 * s;
+      const int left = a.K / 64 - 4 * s;
+      uint4 v = make_uint4(__ldg(q), 0, 0, 0);
+      if (left > 1) v.y = __ldg(q + 1);
+      if (left > 2) v.z = __ldg(q + 2);
+      if (left > 3) v.w = __ldg(q + 3);
+      return v;
+    };
+    auto fetch = [&](int i, int s) {
+      if (!GATHER && a.tiled) return;
+      const Tile& t = tile_ring[i % kTiles];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 0u;
-      } else if (a.vec == 32) {
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "l"(p + u * 32));
-      } else {
-        const int left = a.K / 64 - 8 * u;  // (words of the row from here)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 0u;
-        if (a.vec == 16) {
-          const uint4 lo = __ldg(reinterpret_cast<const uint4*>(p + u * 32));
-          w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
-          if (left > 4) {
-            const uint4 hi = __ldg(reinterpret_cast<const uint4*>(p + u * 32 + 16));
-            w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+      for (int q = 0; q < 4; ++q) {
+        const int row = 32 * r4 + 8 * q + r8;
+        if (!a.tiled) {
+          const int wr = t.m * 256 + rank * 128 + row;  // the row of the matrix
+          const long long at = ((long long)t.e * a.rows + wr) * pitch;
+          w[0][q] = make_uint4(0, 0, 0, 0);
+          if (GLU) w[1][q] = w[0][q];
+          if (wr < a.rows) {
+            w[0][q] = load(a.w_scales + at, s);
+            if (GLU) w[1][q] = load(a.up_scales + at, s);
           }
-        } else {
+        }
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < left) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p + u * 32) + j);
+        for (int c = 0; c < (GLU ? 1 : 2); ++c) {
+          const int src = source_ring[i % kTiles][row + 128 * c];
+          uint4& v = w[(GLU ? 2 : 1) + c][q];
+          v = make_uint4(0, 0, 0, 0);
+          if (src >= 0) v = load(a.x_scales + (long long)src * pitch, s);
         }
       }
     };
     bool ok = true;
-    auto fetch = [&](uint32_t (&w)[3][8]) {
-      if (fi >= mine || !ok) return;
-      if (fu == 0) {
-        ok = wait_tile(fi);
-        if (!ok) return;
-        const Tile& t = tile_ring[fi % kTiles];
-        int wr = t.m * 256 + rank * 128 + row;  // the row of the matrix
-        const uint8_t* base = a.w_scales;
-        if (GLU) {
-          wr = t.m * 128 + rank * 64 + (row >> 5) * 16 + (row & 15);
-          if (row & 16) base = a.up_scales;
-        }
-        pa = wr < a.rows ? base + ((long long)t.e * a.rows + wr) * pitch : nullptr;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int src = source_ring[fi % kTiles][row + 128 * c];
-          pb[c] = src >= 0 ? a.x_scales + (long long)src * pitch : nullptr;
+    int i = 0, s = sw, st = sw;
+    uint32_t ph = 1;
+    // to the tile of stage s, counted from the one of tile i
+    auto settle = [&] {
+      while (ok && i < mine && (ok = wait_tile(i)) && s >= kst) leave_tile(i), ++i, s -= kst;
+    };
+    settle();
+    if (ok && i < mine) fetch(i, s);
+    while (ok && i < mine) {
+      ok = wait(bars.empty[st], ph);
+      if (!ok) break;
+      const uint32_t slot = ring + st * slot_bytes;
+      if (GATHER) {
+        // eight lanes have a row's 128 bytes (what is not copied may hold any codes:
+        // their scales are 0)
+        const int n = tile_ring[i % kTiles].n;
+        const int col = s * (kStageK / 2) + r8 * 16;
+#pragma unroll 4
+        for (int k = r4; k < n / 2; k += 4) {
+          const int r = source_ring[i % kTiles][rank * (n / 2) + k];
+          if (r >= 0 && col < a.K / 2) cp_async16(slot + off_b + k * 128 + (((r8 ^ k) & 7) << 4), a.x_codes + (long long)r * (a.K / 2) + col);
         }
       }
-      load(pa, fu, w[0]);
-      load(pb[0], fu, w[1]);
-      if (chunks == 2) load(pb[1], fu, w[2]);
-      if (++fu == units) fu = 0, ++fi;
-    };
-    // hands a stage over: what this warp's threads have written is seen by the tensor cores
-    auto hand_over = [&](int slot) {
+      if (a.tiled) {
+        ok = wait(bars.rfull[st], ph ^ 1);
+        if (!ok) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t at = slot + 16 * (32 * r4 + 8 * q + r8);
+          w[0][q] = lds128(at + off_sfa);
+          if (GLU) w[1][q] = lds128(at + off_sfa + kSfABytes);
+          if (!GATHER) {
+            w[GLU ? 2 : 1][q] = lds128(at + off_sfb);
+            if (!GLU && chunks == 2) w[2][q] = lds128(at + off_sfb + 2048);
+          }
+        }
+        __syncwarp();  // (they are put in order where they have come to)
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // (chunk c of step k at 512 (chunks k + c))
+        const uint32_t to = slot + 16 * (8 * q + r8) + 4 * r4;
+        put_scales(to + off_sfa, 512, w[0][q]);
+        if (GLU) {
+          put_scales(to + off_sfa + kSfABytes, 512, w[1][q]);
+          put_scales(to + off_sfb, 512, w[2][q]);
+        } else {
+          put_scales(to + off_sfb, 512 * chunks, w[1][q]);
+          if (chunks == 2) put_scales(to + off_sfb + 512, 1024, w[2][q]);
+        }
+      }
+      // what this warp's threads have written is seen by the tensor cores
+      if (GATHER) cp_async_wait_all();
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) pair_arrive(first(bars.sfull[slot]));
-    };
-    fetch(v[0]);
-    fetch(v[1]);
-    int st = 0, behind = 0, flight = 0;  // (stages whose gathered rows are on their way, and the first one's slot)
-    uint32_t ph = 1;
-    int i = 0, s = 0;  // tile and stage
-    const uint8_t* src[8];
-    int n = 0;
-    while (i < mine && ok) {
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        if (i >= mine || !ok) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (s >= kst || !ok) break;
-          if (GATHER && s == 0) {
-            // (the tile is there: its scales have been asked for)
-            const Tile& t = tile_ring[i % kTiles];
-            n = t.n;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int k = 4 * (sw + 4 * j) + (lane >> 3);
-              const int r = k < n / 2 ? source_ring[i % kTiles][rank * (n / 2) + k] : -1;
-              src[j] = r >= 0 ? a.x_codes + (long long)r * (a.K / 2) + (lane & 7) * 16 : nullptr;
-            }
-          }
-          ok = wait(bars.empty[st], ph);
-          if (!ok) break;
-          const uint32_t slot = ring + st * slot_bytes;
-          if (GATHER) {
-            const bool inside = s * (kStageK / 2) + (lane & 7) * 16 < a.K / 2;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int k = 4 * (sw + 4 * j) + (lane >> 3);
-              if (4 * (sw + 4 * j) >= n / 2) break;
-              // (what is not copied may hold anything but a NaN's scale: codes have none)
-              if (src[j] != nullptr && inside)
-                cp_async16(slot + kACodes + k * 128 + ((((lane & 7) ^ k) & 7) << 4), src[j] + s * (kStageK / 2));
-            }
-            cp_async_commit();
-          }
-          const uint32_t sfa = slot + kACodes + slot_b + 16 * r32 + 4 * r4, sfb = sfa + kSfABytes;
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k) sts32(sfa + 512 * k, v[d][0][4 * h + k]);
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k) sts32(sfb + 512 * chunks * k, v[d][1][4 * h + k]);
-          if (chunks == 2) {
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) sts32(sfb + 512 * (2 * k + 1), v[d][2][4 * h + k]);
-          }
-          if (!GATHER) {
-            hand_over(st);
-          } else if (++flight > kLag) {
-            cp_async_wait_group<kLag>();
-            hand_over(behind);
-            if (++behind == a.stages) behind = 0;
-            --flight;
-          }
-          if (++st == a.stages) st = 0, ph ^= 1;
-          ++s;
-        }
-        fetch(v[d]);
-        if (s == kst) leave_tile(i), ++i, s = 0;
-      }
-    }
-    if (GATHER) {
-      cp_async_wait_all();
-      for (; flight > 0 && ok; --flight) {
-        hand_over(behind);
-        if (++behind == a.stages) behind = 0;
-      }
+      if (lane == 0) pair_arrive(first(bars.sfull[st]));
+      s += kScaleWarps;
+      settle();
+      if (ok && i < mine) fetch(i, s);
+      st += kScaleWarps;
+      if (st >= a.stages) st -= a.stages, ph ^= 1;
     }
   } else if (warp >= kEpiWarp0) {
     // --- epilogue -------------------------------------------------------------
@@ -653,42 +649,31 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         const int n = t.n, count = t.count;
         const float f0 = t.f[0], f1 = t.f[1], u0 = t.f[2], u1 = t.f[3];
         const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + d * kAcc1;
-        const int up = GLU ? lane >> 4 : 0;
-        const int row = GLU ? t.m * 128 + rank * 64 + quad * 16 + (lane & 15) : t.m * 256 + rank * 128 + quad * 32 + lane;
-        T* y = static_cast<T*>(a.y) + (long long)(t.p0 + up) * a.y_stride + row;
+        const int row = t.m * 256 + rank * 128 + quad * 32 + lane;
+        T* y = static_cast<T*>(a.y) + (long long)t.p0 * a.y_stride + row;
         const bool in = row < a.rows;
         // chunks of 16 tokens, this half's first or last ones first: those that overlap the other accumulator
-        const int nc = (n / 16 + 1 - half) / 2;  // (of this half)
+        const int nc = n / 32;  // (of this half)
         bool told = false;
         for (int c = 0; c < nc; ++c) {
           const int c0 = 16 * half + 32 * (d ? c : nc - 1 - c);
-          if (!told && (d ? c0 >= kMaxN - kAcc1 : c0 < kAcc1)) {
+          if (!told && (d ? c0 >= 256 - kAcc1 : (GLU ? n : 0) + c0 + 16 <= kAcc1)) {
             told = true;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) pair_arrive(first(bars.over[d]));
           }
-          float v[16];
+          float v[16], u[16];
           tmem_ld16(at + c0, v);
-          if (!GLU) {
-            T* p = y + (long long)c0 * a.y_stride;
-            if (in) {
+          if (GLU) tmem_ld16(at + n + c0, u);
+          T* p = y + (long long)c0 * a.y_stride;
+          if (in) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if (c0 + j < count) *p = static_cast<T>(v[j] * f0 * f1);
-                p += a.y_stride;
-              }
-            }
-          } else {
-            // lane l < 16 ends column j, lane l + 16 column j + 1
-            T* p = y + (long long)c0 * a.y_stride;
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const float own = up ? v[j + 1] : v[j], other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + 1], 16);
-              const float g = (up ? other : own) * f0 * f1, u = (up ? own : other) * u0 * u1;
-              const float s = silu(g);
-              if (in && c0 + j + up < count) *p = static_cast<T>(s * u);
-              p += 2 * a.y_stride;
+            for (int j = 0; j < 16; ++j) {
+              float r = v[j] * f0 * f1;
+              if (GLU) r = silu(r) * (u[j] * u0 * u1);
+              if (c0 + j < count) *p = static_cast<T>(r);
+              p += a.y_stride;
             }
           }
         }
@@ -710,7 +695,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     atomicExch(&g_error, 1u);
     // copies end before the block does: a slot's newest may be a use ahead of what was waited for
     for (uint32_t q = 0; q < 2; ++q)
-      for (int k = 0; k < a.stages; ++k) mbar_wait(bar(bars.full[k]), q, gtimer() + kOpsWaitNs / 100, &never);
+      for (int k = 0; k < a.stages; ++k) {
+        mbar_wait(bar(bars.full[k]), q, gtimer() + kOpsWaitNs / 100, &never);
+        mbar_wait(bar(bars.rfull[k]), q, gtimer() + kOpsWaitNs / 100, &never);
+      }
   }
   __syncwarp();
   tc_fence_before();
@@ -808,22 +796,27 @@ extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* sl
   a.offsets = offsets, a.slots = slots, a.y = y, a.y_stride = n > 1 ? y_stride : 0, a.x_rows = x->rows;
   a.n = (int)n, a.E = w->n_experts, a.rows = (int)w->rows, a.K = (int)w->cols, a.top_k = top_k, a.y_dtype = y_dtype;
   a.x_ts = x->tensor_scale;
-  const uintptr_t bits = reinterpret_cast<uintptr_t>(x->scales) | reinterpret_cast<uintptr_t>(w->scales) |
-                         (up != nullptr ? reinterpret_cast<uintptr_t>(up->scales) : 0) | (uintptr_t)(a.K / 16);
-  a.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 4;
-  const int per = up != nullptr ? 128 : 256;  // the matrix's rows of a tile
-  a.mblocks = (a.rows + per - 1) / per;
-  a.nt = (int)std::min<int64_t>(kMaxN, (n + kStepN - 1) / kStepN * kStepN);
+  a.vec = a.K % kStageK == 0 ? 16 : 4;
+  a.mblocks = (a.rows + 255) / 256;
+  const int mats = up != nullptr ? 2 : 1;
+  a.nt = (int)std::min<int64_t>(kMaxN / mats, (n + kStepN - 1) / kStepN * kStepN);
   const long long tiles = (long long)a.mblocks * ((n + a.nt - 1) / a.nt + std::min<int64_t>(n, a.E));  // at most
   if (tiles > (1ll << 31) - 1 - 65536) return MSK_ERR_SHAPE;
-  const int slot = kACodes + a.nt / 2 * (kStageK / 2) + kSfABytes + (a.nt > 128 ? 2 : 1) * 512 * kSteps;
-  a.stages = std::min(kMaxStages, kRing / slot);
+  const int slot = mats * (kACodes + kSfABytes) + a.nt / 2 * (kStageK / 2) + (a.nt > 128 ? 2 : 1) * 512 * kSteps;
+  a.stages = std::min(kMaxStages, kRing / slot);  // (4 at least: a scale warp's next stage has a slot of its own)
   const CUtensorMapDataType bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const long long wrows = (long long)a.E * a.rows;
-  const int box = up != nullptr ? 16 : kM;
-  if (!matrix_map(&a.w_map, bytes, w->packed, wrows, a.K / 2, a.K / 2, box, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      (up != nullptr && !matrix_map(&a.up_map, bytes, up->packed, wrows, a.K / 2, a.K / 2, box, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B)) ||
-      (slots == nullptr && !matrix_map(&a.x_map, bytes, x->packed, x->rows, a.K / 2, a.K / 2, 16, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B)))
+  auto codes = [&](CUtensorMap* m, const uint8_t* p, long long rows, int box) {
+    return matrix_map(m, bytes, p, rows, a.K / 2, a.K / 2, box, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  auto scales = [&](CUtensorMap* m, const uint8_t* p, long long rows, int box) {
+    return matrix_map(m, bytes, p, rows, a.K / 16, a.K / 16, box, kStageK / 16, CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  a.tiled = a.K % kStageK == 0;  // (a tiled copy's rows lie a multiple of 16 bytes apart)
+  if (!codes(&a.w_map, w->packed, wrows, kM) || (up != nullptr && !codes(&a.up_map, up->packed, wrows, kM)) ||
+      (slots == nullptr && (!codes(&a.x_map, x->packed, x->rows, 64) || !codes(&a.x16_map, x->packed, x->rows, 16))) ||
+      (a.tiled && (!scales(&a.ws_map, w->scales, wrows, kM) || (up != nullptr && !scales(&a.us_map, up->scales, wrows, kM)) ||
+                   (slots == nullptr && !scales(&a.xs_map, x->scales, x->rows, a.nt)))))
     return MSK_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = up != nullptr ? (slots != nullptr ? launch_products<true, true>(a, tiles, st) : launch_products<true, false>(a, tiles, st))
