@@ -161,7 +161,8 @@ struct Tile {
 };
 
 struct Bars {
-  uint64_t full[kMaxStages], rfull[kMaxStages], sfull[kMaxStages], empty[kMaxStages];
+  // a stage is full (weights, tokens, and both blocks' scales in order); its scales have come; it may be filled
+  uint64_t full[kMaxStages], rfull[kMaxStages], empty[kMaxStages];
   uint64_t accf[2], acce[2], over[2];
   uint64_t tfull[kTiles], tempty[kTiles];
   uint64_t done;
@@ -235,6 +236,14 @@ __device__ __forceinline__ float silu(float g) {
   return g * ((g >= 0.f ? 1.f : p) * r);
 }
 
+// v[j] without an address of v.
+__device__ __forceinline__ float pick(const float (&v)[16], int j) {
+  float r = v[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) r = i == j ? v[i] : r;
+  return r;
+}
+
 // y^T = W x^T by block-scaled NVFP4 on the fifth-generation tensor cores.  A pair
 // of blocks (a cluster) has a tile of M = 256 weight rows, 128 each, and N = up to
 // 256 tokens of one expert, of which each block loads half: alone, a block would
@@ -294,8 +303,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   if (tid == 32) {
     abort = 0, never = 0;
     for (int i = 0; i < a.stages; ++i)
-      mbar_init(bar(bars.full[i]), GATHER ? 1 : 2), mbar_init(bar(bars.rfull[i]), GATHER ? 1 : 2),
-          mbar_init(bar(bars.sfull[i]), 2), mbar_init(bar(bars.empty[i]), 1);
+      mbar_init(bar(bars.full[i]), (GATHER ? 1 : 2) + 2), mbar_init(bar(bars.rfull[i]), GATHER ? 1 : 2), mbar_init(bar(bars.empty[i]), 1);
     for (int i = 0; i < 2; ++i)
       mbar_init(bar(bars.accf[i]), 1), mbar_init(bar(bars.acce[i]), 2 * kEpiWarps), mbar_init(bar(bars.over[i]), 2 * kEpiWarps);
     for (int i = 0; i < kTiles; ++i)
@@ -412,13 +420,14 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         source_ring[i % kTiles][lane + 32 * k] = p[k];
       }
       if (lane < (GLU ? 2 : 1)) {
-        // The tensors' scales: a significand and a power of two in two halves, so
-        // that no product leaves fp32's range unless the result does.
+        // The tensors' scales in one factor or, where it might leave fp32's range, in
+        // a significand and a power of two in two halves, so that no product leaves it
+        // unless the result does.
         const float* p = lane ? a.up_ts : a.w_ts;
         const float wt = p != nullptr ? __ldg(p + lo) : 1.f;
         float s = wt * a.x_ts, h = 1.f;
         const int ew = (__float_as_uint(wt) >> 23) & 255, ex = (__float_as_uint(a.x_ts) >> 23) & 255;
-        if (ew != 0 && ew != 255 && ex != 0 && ex != 255) {
+        if (ew != 0 && ew != 255 && ex != 0 && ex != 255 && (ew + ex < 128 || ew + ex > 380)) {
           const int e2 = max(-250, min(250, ew + ex - 254)), e1 = e2 / 2;
           const float mw = __uint_as_float((__float_as_uint(wt) & 0x807FFFFFu) | 0x3F800000u);
           const float mx = __uint_as_float((__float_as_uint(a.x_ts) & 0x807FFFFFu) | 0x3F800000u);
@@ -494,22 +503,33 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         tc_fence_after();
         const uint32_t acc = tmem + d * kAcc1, idesc = idesc_mxf4nvf4(n) + (1u << 27);  // (M = 256)
         for (int s = 0; s < kst; ++s) {
-          ok = wait(bars.full[st], ph) && wait(bars.sfull[st], ph);
+          ok = wait(bars.full[st], ph);
           if (!ok) break;
           tc_fence_after();
           if (el) {
-            const uint32_t at = ring + st * slot_bytes, sfa = at + off_sfa, sfb = at + off_sfb;
+            const uint32_t at = ring + st * slot_bytes;
             const uint64_t ad = umma_desc(at, 16, 1024) | kSwizzle128, bd = umma_desc(at + off_b, 16, 1024) | kSwizzle128;
-            const int steps = min(kSteps, (a.K - s * kStageK) / 64);
-            for (int k = 0; k < steps; ++k) {
-              const uint32_t ta = tmem + kSf + 4 * k, tb = tmem + kSf + 4 * kMats * kSteps + (GLU ? 4 : 8) * k;
-              pair_cp_sf(ta, umma_desc(sfa + 512 * k, 128, 128));
-              if (GLU) pair_cp_sf(ta + 4 * kSteps, umma_desc(sfa + kSfABytes + 512 * k, 128, 128));
-              pair_cp_sf(tb, umma_desc(sfb + 512 * chunks * k, 128, 128));
-              if (!GLU && n > 128) pair_cp_sf(tb + 4, umma_desc(sfb + 512 * chunks * k + 512, 128, 128));
-              pair_mma(acc, ad + 2 * k, bd + 2 * k, idesc, ta, tb, s > 0 || k > 0);
-              if (GLU) pair_mma(acc + n, ad + (kACodes >> 4) + 2 * k, bd + 2 * k, idesc, ta + 4 * kSteps, tb, s > 0 || k > 0);
-            }
+            const uint64_t fa = umma_desc(at + off_sfa, 128, 128), fb = umma_desc(at + off_sfb, 128, 128);
+            const uint32_t ta = tmem + kSf, tb = ta + 4 * kMats * kSteps;
+            auto step = [&](int k, bool two) {
+              pair_cp_sf(ta + 4 * k, fa + 32 * k);
+              if (GLU) pair_cp_sf(ta + 4 * kSteps + 4 * k, fa + (kSfABytes >> 4) + 32 * k);
+              pair_cp_sf(tb + (GLU ? 4 : 8) * k, fb + (two ? 64 : 32) * k);
+              if (two && n > 128) pair_cp_sf(tb + 8 * k + 4, fb + 64 * k + 32);
+              pair_mma(acc, ad + 2 * k, bd + 2 * k, idesc, ta + 4 * k, tb + (GLU ? 4 : 8) * k, s > 0 || k > 0);
+              if (GLU)
+                pair_mma(acc + n, ad + (kACodes >> 4) + 2 * k, bd + 2 * k, idesc, ta + 4 * kSteps + 4 * k, tb + 4 * k, s > 0 || k > 0);
+            };
+            auto steps = [&](bool two) {
+              if (a.K - s * kStageK >= kStageK) {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) step(k, two);
+              } else {
+                for (int k = 0; k < (a.K - s * kStageK) / 64; ++k) step(k, two);
+              }
+            };
+            if (!GLU && chunks == 2) steps(true);
+            else steps(false);
             pair_commit(bar(bars.empty[st]), 3);
           }
           __syncwarp();
@@ -627,7 +647,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
       if (GATHER) cp_async_wait_all();
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) pair_arrive(first(bars.sfull[st]));
+      if (lane == 0) pair_arrive(first(bars.full[st]));
       s += kScaleWarps;
       settle();
       if (ok && i < mine) fetch(i, s);
@@ -655,6 +675,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         // chunks of 16 tokens, this half's first or last ones first: those that overlap the other accumulator
         const int nc = n / 32;  // (of this half)
         bool told = false;
+        const bool one = f1 == 1.f && (!GLU || u1 == 1.f);
         for (int c = 0; c < nc; ++c) {
           const int c0 = 16 * half + 32 * (d ? c : nc - 1 - c);
           if (!told && (d ? c0 >= 256 - kAcc1 : (GLU ? n : 0) + c0 + 16 <= kAcc1)) {
@@ -666,14 +687,15 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
           float v[16], u[16];
           tmem_ld16(at + c0, v);
           if (GLU) tmem_ld16(at + n + c0, u);
+          if (!in) continue;
           T* p = y + (long long)c0 * a.y_stride;
-          if (in) {
+          if (one && c0 + 16 <= count) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float r = v[j] * f0 * f1;
-              if (GLU) r = silu(r) * (u[j] * u0 * u1);
-              if (c0 + j < count) *p = static_cast<T>(r);
-              p += a.y_stride;
+            for (int j = 0; j < 16; ++j, p += a.y_stride) *p = static_cast<T>(GLU ? silu(v[j] * f0) * (u[j] * u0) : v[j] * f0);
+          } else {
+            for (int j = 0; j < min(16, count - c0); ++j, p += a.y_stride) {
+              const float g = pick(v, j) * f0 * f1;
+              *p = static_cast<T>(GLU ? silu(g) * (pick(u, j) * u0 * u1) : g);
             }
           }
         }
