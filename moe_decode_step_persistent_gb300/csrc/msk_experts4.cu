@@ -225,23 +225,22 @@ __device__ __forceinline__ void put_scales(uint32_t addr, int step, uint4 w) {
   sts32(addr, w.x), sts32(addr + step, w.y), sts32(addr + 2 * step, w.z), sts32(addr + 3 * step, w.w);
 }
 
-// g / (1 + e^-g), off by some 2^-22: from e^-|g|, which does not overflow, by 2^t for
-// t = -|g| log2(e) and what t's rounding and the constant's leave.
-__device__ __forceinline__ float silu(float g) {
-  const float m = -fabsf(g), t = m * 1.4426950409f, left = fmaf(m, 1.4426950409f, -t) + m * 1.9259629911e-8f;
-  float p, r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(p) : "f"(t));
-  p = fmaf(p, left * 0.6931471806f, p);
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + p));
-  return g * ((g >= 0.f ? 1.f : p) * r);
-}
-
-// v[j] without an address of v.
-__device__ __forceinline__ float pick(const float (&v)[16], int j) {
-  float r = v[0];
-#pragma unroll
-  for (int i = 1; i < 16; ++i) r = i == j ? v[i] : r;
-  return r;
+// silu(g) = g / (1 + e^-g) of two numbers, off by some 2^-21: 2^t for t = -g
+// log2(e), times a factor for what t's rounding and the constant's leave; results
+// below 2^-119 are 0.
+__device__ __forceinline__ unsigned long long silu2(unsigned long long g) {
+  const unsigned long long one = pair(1.f, 1.f), l = pair(-1.4426950409f, -1.4426950409f);
+  float g0, g1, t0, t1, r0, r1;
+  unpair(g, g0, g1);
+  const unsigned long long m = pair(fminf(g0, 1e30f), fminf(g1, 1e30f));  // (an infinity stays one)
+  const unsigned long long t = mul2(m, l);
+  const unsigned long long rest = fma2(m, pair(-1.9259629911e-8f, -1.9259629911e-8f), fma2(m, l, mul2(t, pair(-1.f, -1.f))));
+  unpair(t, t0, t1);
+  const unsigned long long p = mul2(pair(ex2(t0), ex2(t1)), fma2(rest, pair(0.6931471806f, 0.6931471806f), one));
+  unpair(add2(p, one), t0, t1);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(t0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(t1));
+  return mul2(g, pair(r0, r1));
 }
 
 // y^T = W x^T by block-scaled NVFP4 on the fifth-generation tensor cores.  A pair
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   __shared__ uint32_t tmem_base;
   __shared__ int abort, never, tiles_all, warp_tiles[kProductThreads / 32];
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
-  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int rank = blockIdx.x & 1, team = blockIdx.x >> 1, teams = gridDim.x >> 1;
   // (dynamic shared memory starts at a multiple of 1024 in the shared window)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t ring = smem_u32(smem);
@@ -375,7 +374,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   cluster_sync();  // (of the block too)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  const int mine = pair < tiles_all ? (tiles_all - pair + pairs - 1) / pairs : 0;
+  const int mine = team < tiles_all ? (tiles_all - team + teams - 1) / teams : 0;
   const int kst = (a.K + kStageK - 1) / kStageK;  // stages of a tile
   const uint64_t deadline = gtimer() + kOpsWaitNs + (uint64_t)mine * kst * kOpsStepNs;
   const volatile int* ab = &abort;
@@ -395,7 +394,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     // --- tiles ----------------------------------------------------------------
     for (int i = 0; i < mine; ++i) {
       if (!wait(bars.tempty[i % kTiles], ((i / kTiles) & 1) ^ 1)) break;
-      const int t = pair + i * pairs;
+      const int t = team + i * teams;
       int lo = 0, hi = a.E - 1;  // the first expert whose tiles go beyond t
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -672,38 +671,58 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         const int row = t.m * 256 + rank * 128 + quad * 32 + lane;
         T* y = static_cast<T*>(a.y) + (long long)t.p0 * a.y_stride + row;
         const bool in = row < a.rows;
-        // chunks of 16 tokens, this half's first or last ones first: those that overlap the other accumulator
-        const int nc = n / 32;  // (of this half)
-        bool told = false;
         const bool one = f1 == 1.f && (!GLU || u1 == 1.f);
+        // Chunks of 32 tokens, in turn with the other warps of these lanes, those first
+        // that overlap the other accumulator: the first chunk of each.
+        const int nc = (n / 32 + 1 - half) / 2;
         for (int c = 0; c < nc; ++c) {
-          const int c0 = 16 * half + 32 * (d ? c : nc - 1 - c);
-          if (!told && (d ? c0 >= 256 - kAcc1 : (GLU ? n : 0) + c0 + 16 <= kAcc1)) {
-            told = true;
+          const int c0 = 32 * (half + 2 * (d ? c : nc - 1 - c));
+          float v[32], u[32];
+          tmem_ld32(at + c0, v);
+          if (GLU) tmem_ld32(at + n + c0, u);
+          if (c == 0) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) pair_arrive(first(bars.over[d]));
           }
-          float v[16], u[16];
-          tmem_ld16(at + c0, v);
-          if (GLU) tmem_ld16(at + n + c0, u);
+          if (c == nc - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) pair_arrive(first(bars.acce[d]));
+          }
           if (!in) continue;
           T* p = y + (long long)c0 * a.y_stride;
-          if (one && c0 + 16 <= count) {
+          auto values = [&](auto single, int j, float& x, float& z) {  // tokens j and j + 1
+            unsigned long long g = mul2(pair(v[j], v[j + 1]), pair(f0, f0));
+            if (!single()) g = mul2(g, pair(f1, f1));
+            if (GLU) {
+              unsigned long long h = mul2(pair(u[j], u[j + 1]), pair(u0, u0));
+              if (!single()) h = mul2(h, pair(u1, u1));
+              g = mul2(silu2(g), h);
+            }
+            unpair(g, x, z);
+          };
+          if (one && c0 + 32 <= count) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j, p += a.y_stride) *p = static_cast<T>(GLU ? silu(v[j] * f0) * (u[j] * u0) : v[j] * f0);
+            for (int j = 0; j < 32; j += 2, p += 2 * a.y_stride) {
+              float x, z;
+              values(std::true_type(), j, x, z);
+              p[0] = static_cast<T>(x), p[a.y_stride] = static_cast<T>(z);
+            }
           } else {
-            for (int j = 0; j < min(16, count - c0); ++j, p += a.y_stride) {
-              const float g = pick(v, j) * f0 * f1;
-              *p = static_cast<T>(GLU ? silu(g) * (pick(u, j) * u0 * u1) : g);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2, p += 2 * a.y_stride) {
+              if (c0 + j >= count) break;
+              float x, z;
+              values(std::false_type(), j, x, z);
+              p[0] = static_cast<T>(x);
+              if (c0 + j + 1 < count) p[a.y_stride] = static_cast<T>(z);
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (!told) pair_arrive(first(bars.over[d]));
-          pair_arrive(first(bars.acce[d]));
+        if (nc == 0) {
+          __syncwarp();
+          if (lane == 0) pair_arrive(first(bars.over[d])), pair_arrive(first(bars.acce[d]));
         }
         leave_tile(i);
       }
