@@ -363,10 +363,26 @@ class Fp4Weight:
         _need(scales.shape == (self.rows, self.cols // 16) and scales.is_contiguous(),
               "scales: contiguous [rows][cols / 16]")
         _need(packed.is_cuda and packed.device == scales.device, "packed and scales live on one CUDA device")
+        self._set(packed, scales, tensor_scale)
+
+    def _set(self, packed, scales, tensor_scale):
         # (fixed: the descriptor holds their addresses)
-        self._packed, self._scales, self._tensor_scale = packed, scales, float(tensor_scale)
-        self.desc = ctypes.pointer(Nvfp4Desc(packed.data_ptr(), scales.data_ptr(), self._tensor_scale, self.rows,
-                                             self.cols))
+        self._packed, self._scales, self._tensor_scale, self._desc = packed, scales, float(tensor_scale), None
+
+    @classmethod
+    def _new(cls, rows, cols, tensor_scale, stream):
+        """A new matrix on the current device."""
+        w = cls.__new__(cls)
+        w.rows, w.cols = rows, cols
+        w._set(_empty(stream, (rows, cols // 2), torch.uint8), _empty(stream, (rows, cols // 16), torch.uint8), tensor_scale)
+        return w
+
+    @property
+    def desc(self):
+        if self._desc is None:
+            self._desc = ctypes.pointer(Nvfp4Desc(self._packed.data_ptr(), self._scales.data_ptr(), self._tensor_scale,
+                                                  self.rows, self.cols))
+        return self._desc
 
     packed = property(lambda self: self._packed)
     scales = property(lambda self: self._scales)
@@ -595,8 +611,9 @@ def msk_quantize_fp4(x, tensor_scale=1.0, out=None, stream=None):
           "x: [rows][cols], contiguous rows of whole blocks of 16")
     R, C = x.shape
     if out is None:
-        out = Fp4Weight(_empty(stream, (R, C // 2), torch.uint8), _empty(stream, (R, C // 16), torch.uint8), tensor_scale)
-    _need(out.rows == R and out.cols == C, "out: [rows][cols] of x")
+        out = Fp4Weight._new(R, C, tensor_scale, stream)
+    else:
+        _need(out.rows == R and out.cols == C, "out: [rows][cols] of x")
     st = _enqueue(stream, x, out._packed)
     _check(load_library().msk_quantize_fp4(x.data_ptr(), _DTYPES[x.dtype], R, C, _step(x, 0), out._tensor_scale,
                                            out._packed.data_ptr(), out._scales.data_ptr(), st), "msk_quantize_fp4")

@@ -46,98 +46,116 @@ __device__ __forceinline__ float element(const void* p, long long i) {
 
 // A warp a token, C candidates a lane: lane l's are experts C l .. C l + C - 1,
 // so that of equal logits the lowest lane, and in a lane the first, is the lowest
-// index.  A round takes the warp's greatest key; only its lane looks for its next.
+// index.  A round takes the warp's greatest key; its lane goes on to its next, of
+// which it has three at hand (that a lane has a fourth among 8 chosen ones of 256
+// happens once in 700 tokens).  Which of a lane's candidates they were is
+// found out at the end, for all ranks at once.
 template <int DT, int C, bool VEC>
 __global__ void __launch_bounds__(128) route_kernel(const Route a) {
-  const int lane = threadIdx.x & 31;
-  const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  constexpr int S = DT == MSK_FP32 ? 4 : 2;
+  const int lane = threadIdx.x & 31, e0 = lane * C;
   grid_dep_wait();
   grid_dep_launch();
-  if (t >= a.tokens) return;
-  uint32_t key[C];
-  const int e0 = lane * C;
-  if (VEC && e0 + C <= a.E) {
-    constexpr int W = C * (DT == MSK_FP32 ? 4 : 2) / 4;  // 32-bit words
-    uint32_t w[W];
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.logits) + (t * a.ld + e0) * (DT == MSK_FP32 ? 4 : 2));
+  float bias[C];
 #pragma unroll
-    for (int i = 0; i < W / 4; ++i) {
-      const uint4 u = __ldg(p + i);
-      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-    }
+  for (int j = 0; j < C; ++j) bias[j] = a.bias != nullptr && e0 + j < a.E ? __ldg(a.bias + e0 + j) : 0.f;
+  for (long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 5); t < a.tokens; t += (long long)gridDim.x * 4) {
+    uint32_t key[C];
+    if (VEC && e0 + C <= a.E) {
+      constexpr int W = C * S / 4;  // 32-bit words
+      uint32_t w[W];
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.logits) + (t * a.ld + e0) * S);
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      float x;
-      if (DT == MSK_FP32) x = __uint_as_float(w[j % W]);
-      else {
-        const float2 f = unpack16(w[j / 2], DT == MSK_FP16);
-        x = j & 1 ? f.y : f.x;
+      for (int i = 0; i < W / 4; ++i) {
+        const uint4 u = __ldg(p + i);
+        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
       }
-      key[j] = ordered(a.bias != nullptr ? x + __ldg(a.bias + e0 + j) : x);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      key[j] = 0u;
-      if (e0 + j < a.E) {
-        const float x = element<DT>(a.logits, t * a.ld + e0 + j);
-        key[j] = ordered(a.bias != nullptr ? x + __ldg(a.bias + e0 + j) : x);
-      }
-    }
-  }
-  uint32_t best = key[0];
-#pragma unroll
-  for (int j = 1; j < C; ++j) best = max(best, key[j]);
-  uint32_t mine = 0u;  // lane r: the key of rank r
-  int chosen = -1;
-  for (int r = 0; r < a.top_k; ++r) {
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
-    if (m <= kMinusInf) break;  // (uniform: none is left)
-    const int win = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
-    int at = 0;
-    if (lane == win) {
-      at = C;
-#pragma unroll
-      for (int j = C - 1; j >= 0; --j)
-        if (key[j] == m) at = j;
-      best = 0u;
 #pragma unroll
       for (int j = 0; j < C; ++j) {
-        if (j == at) key[j] = 0u;
-        best = max(best, key[j]);
+        float x;
+        if (DT == MSK_FP32) x = __uint_as_float(w[j % W]);
+        else {
+          const float2 f = unpack16(w[j / 2], DT == MSK_FP16);
+          x = j & 1 ? f.y : f.x;
+        }
+        key[j] = ordered(x + bias[j]);
       }
-      at += e0;
-    }
-    at = __shfl_sync(0xFFFFFFFFu, at, win);
-    if (lane == r) mine = m, chosen = at;
-  }
-  // the softmax of the chosen, in their order of rank
-  const float v = ordered_value(mine), v0 = __shfl_sync(0xFFFFFFFFu, v, 0);
-  float e = chosen >= 0 ? expf(v - v0) : 0.f, sum = e;
+    } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane < a.top_k) {
-    a.experts[t * a.top_k + lane] = chosen;
-    a.gates[t * a.top_k + lane] = chosen >= 0 ? e / sum : 0.f;
+      for (int j = 0; j < C; ++j) key[j] = e0 + j < a.E ? ordered(element<DT>(a.logits, t * a.ld + e0 + j) + bias[j]) : 0u;
+    }
+    uint32_t best[3] = {0u, 0u, 0u};
+    auto enter = [&](uint32_t k) {
+      const uint32_t x = min(best[0], k), y = min(best[1], x);
+      best[0] = max(best[0], k), best[1] = max(best[1], x), best[2] = max(best[2], y);
+    };
+#pragma unroll
+    for (int j = 0; j < C; ++j) enter(key[j]);
+    uint32_t mine = 0u;      // lane r: the key of rank r,
+    int from = 0, skip = 0;  // the lane that has it, and which of its keys like that
+    uint32_t last = 0u;      // this lane's last key that has won,
+    int won = 0, same = 0;   // ranks of this lane's, of those like that
+    int ranks = a.top_k;
+    for (int r = 0; r < a.top_k; ++r) {
+      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best[0]);
+      if (m <= kMinusInf) {  // (uniform: none is left)
+        ranks = r;
+        break;
+      }
+      const int win = __ffs(__ballot_sync(0xFFFFFFFFu, best[0] == m)) - 1;
+      const int next = m == last ? same + 1 : 0, of = __shfl_sync(0xFFFFFFFFu, next, win);
+      if (lane == r) mine = m, from = win, skip = of;
+      if (lane == win) {
+        last = m, same = next, ++won;
+        best[0] = best[1], best[1] = best[2], best[2] = 0u;
+        if (won % 3 == 0) {  // three are used up: those behind the ones that have won
+          int like = same + 1;  // of the keys like the last, this many have
+          best[0] = 0u;
+#pragma unroll
+          for (int j = 0; j < C; ++j) {
+            if (key[j] < m || (key[j] == m && --like < 0)) enter(key[j]);
+          }
+        }
+      }
+    }
+    // lane r: which of lane `from`'s keys; of several like it, the one behind those of earlier ranks
+    const bool in = lane < ranks;
+    int chosen = -1;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const uint32_t k = __shfl_sync(0xFFFFFFFFu, key[j], from);
+      if (k == mine && skip-- == 0) chosen = from * C + j;
+    }
+    if (!in) chosen = -1;
+    // the softmax of the chosen, in their order of rank
+    const float v = ordered_value(mine), v0 = __shfl_sync(0xFFFFFFFFu, v, 0);
+    float e = in ? expf(v - v0) : 0.f, sum = e;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane < a.top_k) {
+      a.experts[t * a.top_k + lane] = chosen;
+      a.gates[t * a.top_k + lane] = in ? e / sum : 0.f;
+    }
   }
 }
 
 template <int DT, int C>
-cudaError_t launch_route(const Route& a, bool aligned, cudaStream_t st) {
-  const OpsLaunch l(dim3((unsigned)((a.tokens + 3) / 4)), 128, 0, st);
+cudaError_t launch_route(const Route& a, bool aligned, int nsm, cudaStream_t st) {
+  // (as many blocks as run at once: a warp goes on with its bias in registers)
+  const OpsLaunch l(dim3((unsigned)std::min<long long>((a.tokens + 3) / 4, nsm * 10)), 128, 0, st);
   if (C * (DT == MSK_FP32 ? 4 : 2) % 16 == 0 && aligned)
     return cudaLaunchKernelEx(&l.cfg, route_kernel<DT, C, C * (DT == MSK_FP32 ? 4 : 2) % 16 == 0>, a);
   return cudaLaunchKernelEx(&l.cfg, route_kernel<DT, C, false>, a);
 }
 
 template <int DT>
-cudaError_t launch_route(const Route& a, bool aligned, cudaStream_t st) {
+cudaError_t launch_route(const Route& a, bool aligned, int nsm, cudaStream_t st) {
   const int c = (a.E + 31) / 32;
-  return c <= 2    ? launch_route<DT, 2>(a, aligned, st)
-         : c <= 4  ? launch_route<DT, 4>(a, aligned, st)
-         : c <= 8  ? launch_route<DT, 8>(a, aligned, st)
-         : c <= 16 ? launch_route<DT, 16>(a, aligned, st)
-                   : launch_route<DT, 32>(a, aligned, st);
+  return c <= 2    ? launch_route<DT, 2>(a, aligned, nsm, st)
+         : c <= 4  ? launch_route<DT, 4>(a, aligned, nsm, st)
+         : c <= 8  ? launch_route<DT, 8>(a, aligned, nsm, st)
+         : c <= 16 ? launch_route<DT, 16>(a, aligned, nsm, st)
+                   : launch_route<DT, 32>(a, aligned, nsm, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -155,19 +173,32 @@ struct Sort {
   int E, blocks;
 };
 
+// The lanes whose expert is this lane's, e in [-1, 2^bits): a ballot a bit (the
+// match instruction takes its time for each expert of 32).
+__device__ __forceinline__ uint32_t same_expert(int e, int bits) {
+  uint32_t m = __ballot_sync(0xFFFFFFFFu, e >= 0);
+  if (e < 0) m = ~m;
+  for (int b = 0; b < bits; ++b) {
+    const uint32_t s = __ballot_sync(0xFFFFFFFFu, (e >> b) & 1);
+    m &= (e >> b) & 1 ? s : ~s;
+  }
+  return m;
+}
+
 // One cluster (of one block for few slots) sorts everything in one launch: the
 // slots are split into runs, one a warp, in their order.  Each warp counts its
 // run's experts, in shared memory, the lanes with the same expert as one; the
 // block sums its warps' counts, the cluster its blocks', and the experts' are
-// scanned.  Then each warp goes through its run again with its first place of
-// each expert.  No atomics: the places do not depend on an order of arrival.
+// scanned.  A slot's place is its warp's first one of its expert and its number
+// among the warp's.  No atomics: the places do not depend on an order of arrival.
+// 131072 slots: bound by the 16 SMs' issue of ballots and of single stores; few
+// slots: by a chain of latencies.
+constexpr int kHeld = 8;
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const Sort a) {
   extern __shared__ __align__(16) int32_t sort_smem[];
-  int32_t* count = sort_smem;                      // [warps][E], then each warp's next place
-  int32_t* total = count + kSortWarps * a.E;       // [E]: this block's (the cluster reads it)
-  int32_t* base = total + a.E;                     // [E]: first place of this block
+  int32_t* count = sort_smem;                 // [warps][E], then each warp's next place
+  int32_t* total = count + kSortWarps * a.E;  // [E]: this block's (the cluster reads it)
   __shared__ int32_t warp_sum[kSortWarps];
-  __shared__ int32_t all;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x;
   for (int i = tid; i < kSortWarps * a.E; i += kSortThreads) count[i] = 0;
   grid_dep_wait();
@@ -175,42 +206,58 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const Sort a) {
   __syncthreads();
   const long long s0 = ((long long)rank * kSortWarps + warp) * a.per_warp, s1 = min(a.n, s0 + a.per_warp);
   int32_t* mine = count + warp * a.E;
-  auto expert = [&](long long s) {
-    const int e = s < s1 ? __ldg(a.experts + s) : -1;
-    return e >= 0 && e < a.E ? e : -1;
+  const int bits = 32 - __clz(a.E - 1 | 1);
+  // a step's experts, and its slots' numbers among those of their expert in the run: of a
+  // run of up to kHeld steps here, of a longer one in `places`, where each thread reads its own
+  int held[kHeld], number[kHeld];
+  const bool longer = a.per_warp > 32 * kHeld;
+  auto load = [&](long long s) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int e = s + 32 * j + lane < s1 ? __ldg(a.experts + s + 32 * j + lane) : -1;
+      held[j] = e >= 0 && e < a.E ? e : -1;
+    }
   };
-  for (long long s = s0; s < s1; s += 32) {
-    const int e = expert(s + lane);
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    if (e >= 0 && (same & ((1u << lane) - 1)) == 0) mine[e] += __popc(same);
-    __syncwarp();
+  for (long long s = s0; s < s1; s += 32 * kHeld) {
+    load(s);
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (s + 32 * j >= s1) break;
+      const int e = held[j];
+      const uint32_t same = same_expert(e, bits), less = same & ((1u << lane) - 1);
+      const int before = e >= 0 ? mine[e] : 0;
+      __syncwarp();
+      if (e >= 0 && less == 0) mine[e] = before + __popc(same);
+      __syncwarp();
+      number[j] = before + __popc(less);
+      if (longer && s + 32 * j + lane < s1) a.places[s + 32 * j + lane] = number[j];
+    }
   }
   __syncthreads();
-  for (int e = tid; e < a.E; e += kSortThreads) {
-    int32_t sum = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int32_t c = count[w * a.E + e];
-      count[w * a.E + e] = sum;
-      sum += c;
-    }
-    total[e] = sum;
-  }
-  if (a.blocks > 1) cluster_sync();
-  else __syncthreads();
   // (E <= the threads of a block: thread e has expert e)
-  int32_t before = 0, sum = 0;
+  int32_t c[kSortWarps], sum = 0, before = 0;
   if (tid < a.E) {
-    if (a.blocks > 1) {
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) c[w] = count[w * a.E + tid];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) sum += c[w];
+    total[tid] = sum;
+  }
+  if (a.blocks > 1) {
+    cluster_sync();
+    if (tid < a.E) {
       const uint32_t at = smem_u32(total + tid);
-      for (int b = 0; b < a.blocks; ++b) {
-        int32_t c;
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(mapa(at, b)) : "memory");
-        if (b < rank) before += c;
-        sum += c;
+      int32_t v[kSortCluster];
+#pragma unroll
+      for (int b = 0; b < kSortCluster; ++b) {
+        v[b] = 0;
+        if (b < a.blocks) asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[b]) : "r"(mapa(at, b)) : "memory");
       }
-    } else {
-      sum = total[tid];
+      sum = 0;
+#pragma unroll
+      for (int b = 0; b < kSortCluster; ++b) before += b < rank ? v[b] : 0, sum += v[b];
     }
+    cluster_arrive();  // (waited for at the end: its totals have been read)
   }
   int32_t scan = sum;
 #pragma unroll
@@ -220,43 +267,40 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const Sort a) {
   }
   if (lane == 31) warp_sum[warp] = scan;
   __syncthreads();
-  if (warp == 0) {
-    int32_t v = warp_sum[lane];
+  int32_t all = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-      if (lane >= o) v += u;
-    }
-    warp_sum[lane] = v;
-    if (lane == 31) all = v;
+  for (int w = 0; w < kSortWarps; ++w) {
+    const int32_t v = warp_sum[w];
+    scan += w < warp ? v : 0, all += v;
   }
-  __syncthreads();
-  scan += warp > 0 ? warp_sum[warp - 1] : 0;
   if (tid < a.E) {
-    base[tid] = scan - sum + before;
+    int32_t place = scan - sum + before;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) count[w * a.E + tid] = place, place += c[w];
     if (rank == 0) {
       a.offsets[tid + 1] = scan;
       if (tid == 0) a.offsets[0] = 0;
     }
   }
   __syncthreads();
-  for (int i = tid; i < kSortWarps * a.E; i += kSortThreads) count[i] += base[i % a.E];
-  __syncthreads();
-  for (long long s = s0; s < s1; s += 32) {
-    const int e = expert(s + lane);
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e), less = same & ((1u << lane) - 1);
-    int32_t place = -1;
-    if (e >= 0) place = mine[e] + __popc(less);
-    __syncwarp();
-    if (e >= 0 && less == 0) mine[e] = place + __popc(same);
-    __syncwarp();
-    if (s + lane < s1) {
-      a.places[s + lane] = place;
-      if (place >= 0) a.slots[place] = (int32_t)(s + lane);
+  for (long long s = s0; s < s1; s += 32 * kHeld) {
+    if (longer) {
+      load(s);
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) number[j] = s + 32 * j + lane < s1 ? a.places[s + 32 * j + lane] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const long long slot = s + 32 * j + lane;
+      if (slot >= s1) break;
+      const int e = held[j];
+      const int32_t place = e >= 0 ? mine[e] + number[j] : -1;
+      a.places[slot] = place;
+      if (place >= 0) a.slots[place] = (int32_t)slot;
     }
   }
   for (long long p = all + (long long)rank * kSortThreads + tid; p < a.n; p += (long long)a.blocks * kSortThreads) a.slots[p] = -1;
-  if (a.blocks > 1) cluster_sync();  // (its totals have been read)
+  if (a.blocks > 1) cluster_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -382,9 +426,9 @@ extern "C" msk_status msk_moe_route(const void* logits, int32_t dtype, int64_t t
   a.tokens = tokens, a.ld = ld, a.E = n_experts, a.top_k = top_k;
   const bool aligned = ops_aligned16(logits) && (tokens == 1 || ld * dtype_bytes(dtype) % 16 == 0);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == MSK_BF16   ? launch_route<MSK_BF16>(a, aligned, st)
-                        : dtype == MSK_FP16 ? launch_route<MSK_FP16>(a, aligned, st)
-                                            : launch_route<MSK_FP32>(a, aligned, st);
+  const cudaError_t e = dtype == MSK_BF16   ? launch_route<MSK_BF16>(a, aligned, nsm, st)
+                        : dtype == MSK_FP16 ? launch_route<MSK_FP16>(a, aligned, nsm, st)
+                                            : launch_route<MSK_FP32>(a, aligned, nsm, st);
   return e == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }
 
@@ -403,12 +447,12 @@ extern "C" msk_status msk_moe_sort(const int32_t* experts, int64_t n, int32_t n_
   a.blocks = n <= 4096 ? 1 : n <= 8 * 4096 ? 8 : kSortCluster;
   const long long warps = (long long)a.blocks * kSortWarps;
   a.per_warp = ((n + warps - 1) / warps + 31) / 32 * 32;
-  const int smem = (kSortWarps + 2) * n_experts * 4;
+  const int smem = (kSortWarps + 1) * n_experts * 4;
   static std::atomic<bool> ready[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSK_ERR_CUDA;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSortWarps + 2) * kMaxExperts * 4) != cudaSuccess ||
+    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSortWarps + 1) * kMaxExperts * 4) != cudaSuccess ||
         cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       return MSK_ERR_CUDA;
     ready[dev].store(true, std::memory_order_release);
