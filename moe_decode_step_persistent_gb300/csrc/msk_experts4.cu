@@ -126,6 +126,8 @@ constexpr int kProductThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kTiles = 8;
 constexpr int kACodes = kM * kStageK / 2, kSfABytes = kM * kStageK / 16;
 constexpr int kRing = 204 * 1024;  // (dynamic shared memory: beside it the tables below and what aligns the ring)
+// Gathered tokens' scales: of four stages and 128 tokens, twice.
+constexpr int kQuadBytes = 128 * kStageK / 16 * 4, kQuads = 2 * kQuadBytes;
 constexpr int kTables = 3 * kMaxE * 4;
 constexpr int kSmem = 1024 + kRing + kTables;
 // Tensor memory columns: two accumulators, which overlap where a tile has more
@@ -148,8 +150,7 @@ struct Experts4 {
   long long y_stride, x_rows;
   int n, E, rows, K, top_k, y_dtype, nt, stages, mblocks;
   float x_ts;
-  int vec;    // scales that threads load: in pieces of 16 or 4 bytes
-  bool tiled; // the weights' scales, and those of tokens that are not gathered, come by tiled copies
+  bool tiled;  // scales come by copies: columns are a multiple of 256
 };
 
 // A tile: the pair's 256 weight rows of an expert and up to nt of its tokens.
@@ -165,6 +166,7 @@ struct Bars {
   uint64_t full[kMaxStages], rfull[kMaxStages], empty[kMaxStages];
   uint64_t accf[2], acce[2], over[2];
   uint64_t tfull[kTiles], tempty[kTiles];
+  uint64_t qfull[2], qempty[2];  // gathered tokens' scales
   uint64_t done;
 };
 
@@ -252,9 +254,9 @@ __device__ __forceinline__ unsigned long long silu2(unsigned long long g) {
 // Weights and tokens come by tiled copies with the 128-byte swizzle, tokens named
 // by slots by asynchronous copies of 16 bytes (gathering tiled copies take 66
 // clocks for four rows of 128 bytes).  Scales, row-major in memory, come by tiled
-// copies too and are put into the tensor cores' order by threads, those of gathered
-// tokens, and of columns that are no multiple of 256, by plain loads some stages
-// ahead (a load of 32 rows' scales holds the load unit for 61 clocks).  Tiles run
+// copies too and are put into the tensor cores' order by threads; where columns are
+// no multiple of 256 threads load them (a load of 32 rows' scales holds the load unit
+// for 61 clocks).  Tiles run
 // over experts, then blocks of weight rows, then tokens, so that neighbouring pairs
 // share weights in L2; a pair takes every one that is a multiple of the pairs on.
 //
@@ -306,7 +308,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     for (int i = 0; i < 2; ++i)
       mbar_init(bar(bars.accf[i]), 1), mbar_init(bar(bars.acce[i]), 2 * kEpiWarps), mbar_init(bar(bars.over[i]), 2 * kEpiWarps);
     for (int i = 0; i < kTiles; ++i)
-      mbar_init(bar(bars.tfull[i]), 1), mbar_init(bar(bars.tempty[i]), 1 + !GATHER + !rank + kScaleWarps + kEpiWarps);
+      mbar_init(bar(bars.tfull[i]), 1), mbar_init(bar(bars.tempty[i]), 1 + (!GATHER || a.tiled) + !rank + kScaleWarps + kEpiWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(bars.qfull[i]), 1), mbar_init(bar(bars.qempty[i]), kScaleWarps);
     mbar_init(bar(bars.done), 1);
     mbar_fence_init();
     fence_proxy_async_shared();
@@ -482,6 +485,34 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
       }
       leave_tile(i);
     }
+  } else if (warp == 1) {
+    // --- gathered tokens' scales, four stages at a time -----------------------------
+    // (four lanes have 64 bytes of a row: a load of 16 bytes each of 32 rows would
+    // hold the load unit four times as long)
+    if (a.tiled) {
+      const int pitch = a.K / 16, piece = lane & 3;
+      int quad = 0;
+      bool ok = true;
+      for (int i = 0; i < mine && ok; ++i) {
+        ok = wait_tile(i);
+        const int count = ok ? tile_ring[i % kTiles].count : 0;
+        for (int s = 0; s < kst && ok; s += 4, ++quad) {
+          ok = wait(bars.qempty[quad & 1], ((quad >> 1) & 1) ^ 1);
+          if (!ok) break;
+          const uint32_t dst = ring + kRing - kQuads + (quad & 1) * kQuadBytes;
+          if (s + piece < kst) {
+#pragma unroll 4
+            for (int k = lane >> 2; k < count; k += 8)  // (columns behind them may have any scales)
+              cp_async16(dst + k * 64 + ((piece ^ ((k >> 1) & 3)) << 4),
+                         a.x_scales + (long long)source_ring[i % kTiles][k] * pitch + (s + piece) * 16);
+          }
+          cp_async_wait_all();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bars.qfull[quad & 1]));
+        }
+        leave_tile(i);
+      }
+    }
   } else if (warp == 2) {
     // --- MMAs -----------------------------------------------------------------
     if (rank == 0) {
@@ -546,17 +577,15 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     }
   } else if (warp >= kScaleWarp0 && warp < kEpiWarp0) {
     // --- scales, and gathered tokens ----------------------------------------------
-    // Each of these warps takes a stage in turn, so that four are under way: a stage
-    // takes some 700 clocks from its first wait to its hand-over, 1300 where tokens
-    // are gathered.  A thread has every 8th row and token of a block's 128, of which
-    // four make the 16 bytes that follow each other.
+    // Of four stages each of these warps takes one, so that four are under way: a stage takes some 700 clocks from its first wait to its hand-over, 1300
+    // where tokens are gathered.  A thread has every 8th row and token of a block's
+    // 128, of which four make the 16 bytes that follow each other.
     constexpr int kOf = 3;  // rows' scales of a stage, 128 each: weights (gate), tokens or up, tokens
     const int sw = warp - kScaleWarp0, r8 = lane & 7, r4 = lane >> 3;
     const int pitch = a.K / 16;
     uint4 w[kOf][4];
-    // loads the scales that threads load of tile `t`, stage `s`
+    // what a row's scales of stage s are where they do not come by copies
     auto load = [&](const uint8_t* p, int s) {
-      if (a.vec == 16) return __ldg(reinterpret_cast<const uint4*>(p) + s);
       const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + 4 * s;
       const int left = a.K / 64 - 4 * s;
       uint4 v = make_uint4(__ldg(q), 0, 0, 0);
@@ -566,23 +595,21 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
       return v;
     };
     auto fetch = [&](int i, int s) {
-      if (!GATHER && a.tiled) return;
+      if (a.tiled) return;
       const Tile& t = tile_ring[i % kTiles];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int row = 32 * r4 + 8 * q + r8;
-        if (!a.tiled) {
-          const int wr = t.m * 256 + rank * 128 + row;  // the row of the matrix
-          const long long at = ((long long)t.e * a.rows + wr) * pitch;
-          w[0][q] = make_uint4(0, 0, 0, 0);
-          if (GLU) w[1][q] = w[0][q];
-          if (wr < a.rows) {
-            w[0][q] = load(a.w_scales + at, s);
-            if (GLU) w[1][q] = load(a.up_scales + at, s);
-          }
+        const int wr = t.m * 256 + rank * 128 + row;  // the row of the matrix
+        const long long at = ((long long)t.e * a.rows + wr) * pitch;
+        w[0][q] = make_uint4(0, 0, 0, 0);
+        if (GLU) w[1][q] = w[0][q];
+        if (wr < a.rows) {
+          w[0][q] = load(a.w_scales + at, s);
+          if (GLU) w[1][q] = load(a.up_scales + at, s);
         }
 #pragma unroll
-        for (int c = 0; c < (GLU ? 1 : 2); ++c) {
+        for (int c = 0; c < (GLU || GATHER ? 1 : 2); ++c) {
           const int src = source_ring[i % kTiles][row + 128 * c];
           uint4& v = w[(GLU ? 2 : 1) + c][q];
           v = make_uint4(0, 0, 0, 0);
@@ -590,68 +617,87 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         }
       }
     };
-    bool ok = true;
-    int i = 0, s = sw, st = sw;
+    // Of stages s0 .. s0 + 3 of tile i this warp's is s (there may be none), every
+    // fourth of all tiles' (no more apart than there are slots: a slot's barrier would
+    // be mistaken for its next but one use); st: the slot it goes to.
+    int i = 0, s0 = 0, s = sw, st = sw, quad = 0;
     uint32_t ph = 1;
-    // to the tile of stage s, counted from the one of tile i
-    auto settle = [&] {
-      while (ok && i < mine && (ok = wait_tile(i)) && s >= kst) leave_tile(i), ++i, s -= kst;
-    };
-    settle();
-    if (ok && i < mine) fetch(i, s);
-    while (ok && i < mine) {
-      ok = wait(bars.empty[st], ph);
-      if (!ok) break;
+    bool ok = mine > 0 && wait_tile(0);
+    if (ok && s < kst) fetch(i, s);
+    for (; ok && i < mine; ++quad) {
       const uint32_t slot = ring + st * slot_bytes;
-      if (GATHER) {
-        // eight lanes have a row's 128 bytes (what is not copied may hold any codes:
-        // their scales are 0)
-        const int n = tile_ring[i % kTiles].n;
-        const int col = s * (kStageK / 2) + r8 * 16;
-#pragma unroll 4
-        for (int k = r4; k < n / 2; k += 4) {
-          const int r = source_ring[i % kTiles][rank * (n / 2) + k];
-          if (r >= 0 && col < a.K / 2) cp_async16(slot + off_b + k * 128 + (((r8 ^ k) & 7) << 4), a.x_codes + (long long)r * (a.K / 2) + col);
-        }
-      }
-      if (a.tiled) {
-        ok = wait(bars.rfull[st], ph ^ 1);
+      if (s < kst) {
+        ok = wait(bars.empty[st], ph);
         if (!ok) break;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t at = slot + 16 * (32 * r4 + 8 * q + r8);
-          w[0][q] = lds128(at + off_sfa);
-          if (GLU) w[1][q] = lds128(at + off_sfa + kSfABytes);
-          if (!GATHER) {
-            w[GLU ? 2 : 1][q] = lds128(at + off_sfb);
-            if (!GLU && chunks == 2) w[2][q] = lds128(at + off_sfb + 2048);
+        if (GATHER) {
+          // eight lanes have a row's 128 bytes (columns behind the tokens may have any)
+          const int n = tile_ring[i % kTiles].n;
+          const int col = s * (kStageK / 2) + r8 * 16;
+#pragma unroll 4
+          for (int k = r4; k < n / 2; k += 4) {
+            const int r = source_ring[i % kTiles][rank * (n / 2) + k];
+            if (r >= 0 && col < a.K / 2) cp_async16(slot + off_b + k * 128 + (((r8 ^ k) & 7) << 4), a.x_codes + (long long)r * (a.K / 2) + col);
           }
         }
-        __syncwarp();  // (they are put in order where they have come to)
       }
+      if (GATHER && a.tiled) {
+        ok = wait(bars.qfull[quad & 1], (quad >> 1) & 1);
+        if (!ok) break;
+        if (s < kst) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        // (chunk c of step k at 512 (chunks k + c))
-        const uint32_t to = slot + 16 * (8 * q + r8) + 4 * r4;
-        put_scales(to + off_sfa, 512, w[0][q]);
-        if (GLU) {
-          put_scales(to + off_sfa + kSfABytes, 512, w[1][q]);
-          put_scales(to + off_sfb, 512, w[2][q]);
-        } else {
-          put_scales(to + off_sfb, 512 * chunks, w[1][q]);
-          if (chunks == 2) put_scales(to + off_sfb + 512, 1024, w[2][q]);
+          for (int q = 0; q < 4; ++q) {
+            const int row = 32 * r4 + 8 * q + r8;
+            w[GLU ? 2 : 1][q] = lds128(ring + kRing - kQuads + (quad & 1) * kQuadBytes + row * 64 + (((s - s0) ^ ((row >> 1) & 3)) << 4));
+          }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars.qempty[quad & 1]));
       }
-      // what this warp's threads have written is seen by the tensor cores
-      if (GATHER) cp_async_wait_all();
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) pair_arrive(first(bars.full[st]));
-      s += kScaleWarps;
-      settle();
-      if (ok && i < mine) fetch(i, s);
-      st += kScaleWarps;
-      if (st >= a.stages) st -= a.stages, ph ^= 1;
+      if (s < kst) {
+        if (a.tiled) {
+          ok = wait(bars.rfull[st], ph ^ 1);
+          if (!ok) break;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t at = slot + 16 * (32 * r4 + 8 * q + r8);
+            w[0][q] = lds128(at + off_sfa);
+            if (GLU) w[1][q] = lds128(at + off_sfa + kSfABytes);
+            if (!GATHER) {
+              w[GLU ? 2 : 1][q] = lds128(at + off_sfb);
+              if (!GLU && chunks == 2) w[2][q] = lds128(at + off_sfb + 2048);
+            }
+          }
+          __syncwarp();  // (they are put in order where they have come to)
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          // (chunk c of step k at 512 (chunks k + c))
+          const uint32_t to = slot + 16 * (8 * q + r8) + 4 * r4;
+          put_scales(to + off_sfa, 512, w[0][q]);
+          if (GLU) {
+            put_scales(to + off_sfa + kSfABytes, 512, w[1][q]);
+            put_scales(to + off_sfb, 512, w[2][q]);
+          } else {
+            put_scales(to + off_sfb, 512 * chunks, w[1][q]);
+            if (chunks == 2) put_scales(to + off_sfb + 512, 1024, w[2][q]);
+          }
+        }
+        // what this warp's threads have written is seen by the tensor cores
+        if (GATHER) cp_async_wait_all();
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) pair_arrive(first(bars.full[st]));
+      }
+      // on to the next four
+      if (s < kst && (st += kScaleWarps) >= a.stages) st -= a.stages, ph ^= 1;
+      if (s0 + 4 < kst) {
+        s0 += 4, s += 4;
+      } else {
+        leave_tile(i);
+        ++i, s0 = 0, s = (int)((unsigned)sw - (unsigned)i * (unsigned)kst) & 3;
+        ok = i >= mine || wait_tile(i);
+      }
+      if (ok && i < mine && s < kst) fetch(i, s);
     }
   } else if (warp >= kEpiWarp0) {
     // --- epilogue -------------------------------------------------------------
@@ -837,14 +883,16 @@ extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* sl
   a.offsets = offsets, a.slots = slots, a.y = y, a.y_stride = n > 1 ? y_stride : 0, a.x_rows = x->rows;
   a.n = (int)n, a.E = w->n_experts, a.rows = (int)w->rows, a.K = (int)w->cols, a.top_k = top_k, a.y_dtype = y_dtype;
   a.x_ts = x->tensor_scale;
-  a.vec = a.K % kStageK == 0 ? 16 : 4;
   a.mblocks = (a.rows + 255) / 256;
-  const int mats = up != nullptr ? 2 : 1;
-  a.nt = (int)std::min<int64_t>(kMaxN / mats, (n + kStepN - 1) / kStepN * kStepN);
+  // (128 tokens leave a deeper ring: 16384 rows of 256 experts, 2048 x 1024, 68.9 us, with
+  // 256 73.7; where experts have more, weights are loaded less often: 65536 rows 105, with 128 116)
+  const bool half = up != nullptr || slots != nullptr || n <= 128ll * w->n_experts;
+  a.nt = (int)std::min<int64_t>(half ? kMaxN / 2 : kMaxN, (n + kStepN - 1) / kStepN * kStepN);
   const long long tiles = (long long)a.mblocks * ((n + a.nt - 1) / a.nt + std::min<int64_t>(n, a.E));  // at most
   if (tiles > (1ll << 31) - 1 - 65536) return MSK_ERR_SHAPE;
+  const int mats = up != nullptr ? 2 : 1;
   const int slot = mats * (kACodes + kSfABytes) + a.nt / 2 * (kStageK / 2) + (a.nt > 128 ? 2 : 1) * 512 * kSteps;
-  a.stages = std::min(kMaxStages, kRing / slot);  // (4 at least: a scale warp's next stage has a slot of its own)
+  a.stages = std::min(kMaxStages, (kRing - (slots != nullptr ? kQuads : 0)) / slot);  // (4 at least)
   const CUtensorMapDataType bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const long long wrows = (long long)a.E * a.rows;
   auto codes = [&](CUtensorMap* m, const uint8_t* p, long long rows, int box) {
