@@ -27,15 +27,34 @@ struct Rows4 {
   float ts;
 };
 
-// A block of 16 elements a thread, as in the 4-bit cache's writer.
-template <int DT>
+// 32 bytes (aligned so).
+__device__ __forceinline__ void ldg256(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+
+// A block of 16 elements a thread, as in the 4-bit cache's writer.  WIDE: rows of
+// 16-bit elements are aligned to 32 bytes, one load's.
+template <int DT, bool WIDE>
 __global__ void __launch_bounds__(256) quantize_kernel(const Rows4 a) {
   grid_dep_wait();
   grid_dep_launch();
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x, r = i / a.pieces;
   if (r >= a.rows) return;
   float x[16];
-  load16<DT>(a.x, r * a.x_stride + (i - r * a.pieces) * 16, x);
+  const long long from = r * a.x_stride + (i - r * a.pieces) * 16;
+  if (WIDE) {
+    uint32_t w[8];
+    ldg256(static_cast<const uint16_t*>(a.x) + from, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 f = unpack16(w[j], DT == MSK_FP16);
+      x[2 * j] = f.x, x[2 * j + 1] = f.y;
+    }
+  } else {
+    load16<DT>(a.x, from, x);
+  }
   uint32_t sc;
   const uint2 c = quantise16(x, a.ts, sc);
   *reinterpret_cast<uint2*>(a.codes + i * 8) = c;
@@ -100,10 +119,14 @@ msk_status rows_call(bool write, const void* x, int32_t dtype, int64_t rows, int
   const int piece = write ? 16 : dtype == MSK_FP32 ? 4 : 8, per = write ? 256 : 256 * kReadUnroll;
   a.pieces = (int)(cols / piece);
   const OpsLaunch l(dim3((unsigned)((rows * a.pieces + per - 1) / per)), 256, 0, static_cast<cudaStream_t>(stream));
-  auto launch = [&](void (*q)(Rows4), void (*d)(Rows4)) { return cudaLaunchKernelEx(&l.cfg, write ? q : d, a); };
-  const cudaError_t e = dtype == MSK_BF16   ? launch(quantize_kernel<MSK_BF16>, dequantize_kernel<MSK_BF16>)
-                        : dtype == MSK_FP16 ? launch(quantize_kernel<MSK_FP16>, dequantize_kernel<MSK_FP16>)
-                                            : launch(quantize_kernel<MSK_FP32>, dequantize_kernel<MSK_FP32>);
+  const bool wide = dtype != MSK_FP32 && ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(a.x_stride * 2)) & 31) == 0;
+  auto launch = [&](void (*q)(Rows4), void (*qw)(Rows4), void (*d)(Rows4)) {
+    return cudaLaunchKernelEx(&l.cfg, !write ? d : wide ? qw : q, a);
+  };
+  const cudaError_t e =
+      dtype == MSK_BF16   ? launch(quantize_kernel<MSK_BF16, false>, quantize_kernel<MSK_BF16, true>, dequantize_kernel<MSK_BF16>)
+      : dtype == MSK_FP16 ? launch(quantize_kernel<MSK_FP16, false>, quantize_kernel<MSK_FP16, true>, dequantize_kernel<MSK_FP16>)
+                          : launch(quantize_kernel<MSK_FP32, false>, quantize_kernel<MSK_FP32, false>, dequantize_kernel<MSK_FP32>);
   return e == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }
 
