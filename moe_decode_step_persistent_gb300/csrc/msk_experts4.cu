@@ -245,6 +245,10 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// `bytes` (0 or 16) of 16, zeros for the rest.
+__device__ __forceinline__ void cp_async16_some(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 // A row's scales of four steps, `step` bytes from one to the next.
 __device__ __forceinline__ void put_scales(uint32_t addr, int step, uint4 w) {
   sts32(addr, w.x), sts32(addr + step, w.y), sts32(addr + 2 * step, w.z), sts32(addr + 3 * step, w.w);
@@ -653,13 +657,20 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         ok = wait(bars.empty[st], ph);
         if (!ok) break;
         if (GATHER) {
-          // eight lanes have a row's 128 bytes (columns behind the tokens may have any)
-          const int n = tile_ring[i % kTiles].n;
-          const int col = s * (kStageK / 2) + r8 * 16;
-#pragma unroll 4
-          for (int k = r4; k < n / 2; k += 4) {
-            const int r = source_ring[i % kTiles][rank * (n / 2) + k];
-            if (r >= 0 && col < a.K / 2) cp_async16(slot + off_b + k * 128 + (((r8 ^ k) & 7) << 4), a.x_codes + (long long)r * (a.K / 2) + col);
+          // eight lanes have a row's 128 bytes (columns behind the tokens get none of it)
+          const int n = tile_ring[i % kTiles].n, col = s * (kStageK / 2) + r8 * 16;
+          const int* rows = source_ring[i % kTiles] + rank * (n / 2) + r4;
+          const bool inside = col < a.K / 2;
+          int r[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (8 * j < n) r[j] = rows[4 * j];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (8 * j >= n) break;
+            const int k = r4 + 4 * j;
+            cp_async16_some(slot + off_b + k * 128 + (((r8 ^ k) & 7) << 4), a.x_codes + (long long)max(r[j], 0) * (a.K / 2) + (inside ? col : 0),
+                            r[j] >= 0 && inside ? 16 : 0);
           }
         }
       }
