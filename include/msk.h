@@ -512,7 +512,16 @@ typedef struct {
   const float* tensor_scales;
   int32_t n_experts;
   int64_t rows, cols;
+  const void* maps; /* NULL, or what msk_fp4_experts_maps has made of these weights (HOST) */
 } msk_fp4_experts;
+
+/* The copy engine's descriptors of the weights, which msk_experts_fp4 makes anew at
+ * every call that is not given them (1.2 us each, two a matrix): into
+ * MSK_FP4_MAPS_BYTES of HOST memory, 128-byte aligned, that the caller keeps with
+ * the weights.  w->maps is not read.  They hold for these addresses and sizes: a
+ * call with others in the struct beside them is MSK_ERR_INVALID_ARG. */
+#define MSK_FP4_MAPS_BYTES 384
+msk_status msk_fp4_experts_maps(const msk_fp4_experts* w, void* maps);
 
 /* Products of quantised rows with their experts' weights: for every place p of
  * expert e

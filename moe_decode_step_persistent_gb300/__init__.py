@@ -81,8 +81,11 @@ class Kv4Desc(ctypes.Structure):
 
 class Fp4ExpertsC(ctypes.Structure):
     _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tensor_scales", ctypes.c_void_p),
-                ("n_experts", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+                ("n_experts", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("maps", ctypes.c_void_p)]
 
+
+MSK_FP4_MAPS_BYTES = 384
 
 #: every symbol include/msk.h declares
 SYMBOLS = ["msk_create", "msk_load_layer", "msk_layer_step", "msk_decode_step", "msk_layer_step_tree",
@@ -92,7 +95,7 @@ SYMBOLS = ["msk_create", "msk_load_layer", "msk_layer_step", "msk_decode_step", 
            "msk_debug_fp4_gemm",
            "msk_attention_noalloc", "msk_kv4_write", "msk_kv4_read", "msk_attention_kv4_workspace",
            "msk_attention_kv4", "msk_linear_fp4", "msk_ops_check", "msk_token_logprobs",
-           "msk_moe_route", "msk_moe_sort", "msk_quantize_fp4", "msk_dequantize_fp4", "msk_experts_fp4",
+           "msk_moe_route", "msk_moe_sort", "msk_quantize_fp4", "msk_dequantize_fp4", "msk_fp4_experts_maps", "msk_experts_fp4",
            "msk_moe_combine", "msk_get_info", "msk_status_string", "msk_destroy"]
 
 _lib = None
@@ -143,6 +146,7 @@ def load_library(path: str = LIB_PATH):
     L.msk_moe_sort.argtypes = [vp, i64, i32, vp, vp, vp, vp]
     L.msk_quantize_fp4.argtypes = [vp, i32, i64, i64, i64, f32, vp, vp, vp]
     L.msk_dequantize_fp4.argtypes = [vp, vp, f32, i64, i64, vp, i32, i64, vp]
+    L.msk_fp4_experts_maps.argtypes = [experts, vp]
     L.msk_experts_fp4.argtypes = [fp4, vp, i32, i64, vp, experts, experts, vp, i32, i64, vp]
     L.msk_moe_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i32, i64, vp, i32, i64, vp]
     L.msk_get_info.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(i64)]
@@ -411,7 +415,13 @@ class Fp4Experts:
         self._packed, self._scales, self._tensor_scales = packed, scales, tensor_scales
         self.desc = ctypes.pointer(Fp4ExpertsC(packed.data_ptr(), scales.data_ptr(),
                                                None if tensor_scales is None else tensor_scales.data_ptr(),
-                                               self.n_experts, self.rows, self.cols))
+                                               self.n_experts, self.rows, self.cols, None))
+        # (of weights that the products take: the others are refused when they are used)
+        self._maps = ctypes.create_string_buffer(MSK_FP4_MAPS_BYTES + 128)
+        at = ctypes.addressof(self._maps) + 127 & ~127
+        with torch.cuda.device(packed.device):
+            if load_library().msk_fp4_experts_maps(self.desc, at) == MSK_OK:
+                self.desc.contents.maps = at
 
     packed = property(lambda self: self._packed)
     scales = property(lambda self: self._scales)
@@ -579,8 +589,10 @@ def msk_moe_route(logits, top_k, bias=None, stream=None):
     _need(1 <= top_k <= min(32, E), "top_k: 1 to 32, n_experts at most")
     _need(bias is None or (bias.dtype == torch.float32 and bias.shape == (E,) and bias.is_contiguous()),
           "bias: contiguous fp32 [n_experts]")
+    st = _enqueue(stream, logits) if bias is None else _enqueue(stream, logits, bias)
+    # (here and below, outputs last: an allocation waits for the launch before it to leave the
+    # core, which the checks above take part of)
     experts, gates = _empty(stream, (T, top_k), torch.int32), _empty(stream, (T, top_k), torch.float32)
-    st = _enqueue(stream, logits, experts) if bias is None else _enqueue(stream, logits, experts, bias)
     _check(load_library().msk_moe_route(logits.data_ptr(), _DTYPES[logits.dtype], T, E, _step(logits, 0),
                                         None if bias is None else bias.data_ptr(), top_k, experts.data_ptr(),
                                         gates.data_ptr(), st), "msk_moe_route")
@@ -594,10 +606,9 @@ def msk_moe_sort(experts, n_experts, stream=None):
     slot: its place is -1, and slots ends in as many -1."""
     _need(experts.dtype == torch.int32 and experts.is_contiguous(), "experts: contiguous int32")
     _need(1 <= n_experts <= 1024, "n_experts: 1 to 1024")
-    n = experts.numel()
+    n, st = experts.numel(), _enqueue(stream, experts)
     offsets, slots = _empty(stream, n_experts + 1, torch.int32), _empty(stream, n, torch.int32)
     places = _empty(stream, experts.shape, torch.int32)
-    st = _enqueue(stream, experts, offsets)
     _check(load_library().msk_moe_sort(experts.data_ptr(), n, n_experts, offsets.data_ptr(), slots.data_ptr(),
                                        places.data_ptr(), st), "msk_moe_sort")
     return offsets, slots, places
@@ -611,10 +622,11 @@ def msk_quantize_fp4(x, tensor_scale=1.0, out=None, stream=None):
           "x: [rows][cols], contiguous rows of whole blocks of 16")
     R, C = x.shape
     if out is None:
+        st = _enqueue(stream, x)
         out = Fp4Weight._new(R, C, tensor_scale, stream)
     else:
         _need(out.rows == R and out.cols == C, "out: [rows][cols] of x")
-    st = _enqueue(stream, x, out._packed)
+        st = _enqueue(stream, x, out._packed)
     _check(load_library().msk_quantize_fp4(x.data_ptr(), _DTYPES[x.dtype], R, C, _step(x, 0), out._tensor_scale,
                                            out._packed.data_ptr(), out._scales.data_ptr(), st), "msk_quantize_fp4")
     return out
@@ -625,10 +637,12 @@ def msk_dequantize_fp4(w, dtype=torch.bfloat16, out=None, stream=None):
     row stride)."""
     if out is None:
         _need(dtype in _DTYPES, "a floating type")
+        st = _enqueue(stream, w._packed)
         out = _empty(stream, (w.rows, w.cols), dtype)
-    _need(out.shape == (w.rows, w.cols) and out.dtype in _DTYPES and out.stride(1) == 1,
-          "out: [rows][cols], contiguous rows")
-    st = _enqueue(stream, out, w._packed)
+    else:
+        _need(out.shape == (w.rows, w.cols) and out.dtype in _DTYPES and out.stride(1) == 1,
+              "out: [rows][cols], contiguous rows")
+        st = _enqueue(stream, out, w._packed)
     _check(load_library().msk_dequantize_fp4(w._packed.data_ptr(), w._scales.data_ptr(), w._tensor_scale, w.rows, w.cols,
                                              out.data_ptr(), _DTYPES[out.dtype], _step(out, 0), st), "msk_dequantize_fp4")
     return out
@@ -649,18 +663,30 @@ def msk_experts_fp4(x, experts, offsets, up=None, slots=None, top_k=1, out_dtype
           "up: of the other weights' size")
     _need(slots is None or (slots.dtype == torch.int32 and slots.dim() == 1 and slots.is_contiguous() and top_k >= 1),
           "slots: contiguous int32 [n], with top_k")
+    top_k = _int32(top_k, "top_k")
     n = x.rows if slots is None else slots.shape[0]
     if out is None:
         _need(out_dtype in _DTYPES, "out_dtype: a floating type")
-        out = _empty(stream, (n, experts.rows), out_dtype)
-    _need(out.shape == (n, experts.rows) and out.dtype in _DTYPES and (out.stride(1) == 1 or experts.rows <= 1),
-          "out: [n][rows], contiguous rows")
-    given = [t for t in (x._packed, experts._packed, offsets, out, slots, None if up is None else up._packed)
-             if t is not None]
-    st = _enqueue(stream, *given)
-    _check(load_library().msk_experts_fp4(x.desc, None if slots is None else slots.data_ptr(), _int32(top_k, "top_k"), n,
-                                          offsets.data_ptr(), experts.desc, None if up is None else up.desc,
-                                          out.data_ptr(), _DTYPES[out.dtype], _step(out, 0), st), "msk_experts_fp4")
+    else:
+        _need(out.shape == (n, experts.rows) and out.dtype in _DTYPES and (out.stride(1) == 1 or experts.rows <= 1),
+              "out: [n][rows], contiguous rows")
+    given = [x._packed, experts._packed, offsets]
+    slot_ptr = up_desc = None
+    if slots is not None:
+        slot_ptr = slots.data_ptr()
+        given.append(slots)
+    if up is not None:
+        up_desc = up.desc
+        given.append(up._packed)
+    if out is not None:
+        given.append(out)
+    st, x_desc, ptr = _enqueue(stream, *given), x.desc, offsets.data_ptr()
+    if out is None:
+        step, out = experts.rows, _empty(stream, (n, experts.rows), out_dtype)
+    else:
+        step = _step(out, 0)
+    _check(load_library().msk_experts_fp4(x_desc, slot_ptr, top_k, n, ptr, experts.desc, up_desc, out.data_ptr(),
+                                          _DTYPES[out.dtype], step, st), "msk_experts_fp4")
     return out
 
 
@@ -677,9 +703,12 @@ def msk_moe_combine(y, places, gates=None, out_dtype=None, out=None, stream=None
     (T, k), C = places.shape, y.shape[1]
     if out is None:
         _need(out_dtype is None or out_dtype in _DTYPES, "out_dtype: a floating type")
+    else:
+        _need(out.shape == (T, C) and out.dtype in _DTYPES and (out.stride(1) == 1 or C <= 1), "out: [tokens][cols], contiguous rows")
+        _enqueue(stream, out)
+    st = _enqueue(stream, y, places) if gates is None else _enqueue(stream, y, places, gates)
+    if out is None:
         out = _empty(stream, (T, C), y.dtype if out_dtype is None else out_dtype)
-    _need(out.shape == (T, C) and out.dtype in _DTYPES and (out.stride(1) == 1 or C <= 1), "out: [tokens][cols], contiguous rows")
-    st = _enqueue(stream, y, places, out) if gates is None else _enqueue(stream, y, places, out, gates)
     _check(load_library().msk_moe_combine(y.data_ptr(), _DTYPES[y.dtype], y.shape[0], _step(y, 0), places.data_ptr(),
                                           None if gates is None else gates.data_ptr(), T, k, C, out.data_ptr(),
                                           _DTYPES[out.dtype], _step(out, 0), st), "msk_moe_combine")

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&a.w_map);
     if (GLU) prefetch_tensormap(&a.up_map);
-    if (!GATHER) prefetch_tensormap(&a.x_map), prefetch_tensormap(&a.x16_map);
+    if (!GATHER) prefetch_tensormap(a.nt >= 128 ? &a.x_map : &a.x16_map);
     if (a.tiled) {
       prefetch_tensormap(&a.ws_map);
       if (GLU) prefetch_tensormap(&a.us_map);
@@ -855,12 +855,51 @@ cudaError_t launch_products(const Experts4& a, long long tiles, cudaStream_t st)
   return cudaLaunchKernelEx(&l.cfg, experts4_kernel<GLU, GATHER>, a);
 }
 
-bool check_experts(const msk_fp4_experts* w, msk_status& s) {
-  s = MSK_OK;
+msk_status check_experts(const msk_fp4_experts* w) {
   if (w->n_experts < 1 || w->n_experts > kMaxE || w->rows < 0 || w->rows > (1 << 24) || w->cols < 64 || w->cols > (1 << 17) ||
       w->cols % 64 || (int64_t)w->n_experts * w->rows > (1ll << 31) - 256)
-    s = MSK_ERR_SHAPE;
-  return s == MSK_OK;
+    return MSK_ERR_SHAPE;
+  return MSK_OK;
+}
+
+// What msk_fp4_experts_maps writes.
+struct WeightMaps {
+  CUtensorMap codes, scales;
+  const uint8_t *packed, *scale_codes;
+  int64_t experts, rows, cols, tiled;
+};
+static_assert(sizeof(WeightMaps) <= MSK_FP4_MAPS_BYTES && alignof(WeightMaps) <= 128, "msk.h");
+
+bool tiled_scales(int64_t cols) { return cols % kStageK == 0; }  // (a tiled copy's rows lie a multiple of 16 bytes apart)
+
+// Rows of codes in boxes of `box` x 128 bytes, of scales in boxes of `box` x 16.
+bool codes_map(CUtensorMap* m, const uint8_t* p, long long rows, long long cols, int box) {
+  return matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, rows, cols / 2, cols / 2, box, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool scales_map(CUtensorMap* m, const uint8_t* p, long long rows, long long cols, int box) {
+  return matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, rows, cols / 16, cols / 16, box, kStageK / 16, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+bool make_maps(const msk_fp4_experts* w, WeightMaps* m) {
+  const long long rows = (long long)w->n_experts * w->rows;
+  m->packed = w->packed, m->scale_codes = w->scales, m->experts = w->n_experts, m->rows = w->rows, m->cols = w->cols;
+  m->tiled = tiled_scales(w->cols);
+  return codes_map(&m->codes, w->packed, rows, w->cols, kM) && (!m->tiled || scales_map(&m->scales, w->scales, rows, w->cols, kM));
+}
+
+// The weights' maps, the caller's or new ones.
+msk_status weight_maps(const msk_fp4_experts* w, CUtensorMap* codes, CUtensorMap* scales) {
+  WeightMaps own;
+  const WeightMaps* m = static_cast<const WeightMaps*>(w->maps);
+  if (m == nullptr) {
+    if (!make_maps(w, &own)) return MSK_ERR_CUDA;
+    m = &own;
+  } else if (m->packed != w->packed || m->scale_codes != w->scales || m->experts != w->n_experts || m->rows != w->rows || m->cols != w->cols) {
+    return MSK_ERR_INVALID_ARG;
+  }
+  *codes = m->codes;
+  if (m->tiled) *scales = m->scales;
+  return MSK_OK;
 }
 
 }  // namespace
@@ -886,12 +925,23 @@ extern "C" msk_status msk_dequantize_fp4(const uint8_t* codes, const uint8_t* sc
   return rows_call(false, x, dtype, rows, cols, x_stride, tensor_scale, codes, scales, stream);
 }
 
+extern "C" msk_status msk_fp4_experts_maps(const msk_fp4_experts* w, void* maps) {
+  if (w == nullptr || maps == nullptr) return MSK_ERR_INVALID_ARG;
+  const msk_status s = check_experts(w);
+  if (s != MSK_OK) return s;
+  if (w->rows == 0) return MSK_ERR_SHAPE;
+  if (w->packed == nullptr || w->scales == nullptr) return MSK_ERR_INVALID_ARG;
+  if (!ops_aligned16(w->packed) || !ops_aligned16(w->scales) || (reinterpret_cast<uintptr_t>(maps) & 127)) return MSK_ERR_ALIGNMENT;
+  return make_maps(w, static_cast<WeightMaps*>(maps)) ? MSK_OK : MSK_ERR_CUDA;
+}
+
 extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* slots, int32_t top_k, int64_t n,
                                       const int32_t* offsets, const msk_fp4_experts* w, const msk_fp4_experts* up, void* y,
                                       int32_t y_dtype, int64_t y_stride, void* stream) {
   if (x == nullptr || w == nullptr || !dtype_ok(y_dtype) || n < 0) return MSK_ERR_INVALID_ARG;
-  msk_status s;
-  if (!check_experts(w, s) || (up != nullptr && !check_experts(up, s))) return s;
+  msk_status s = check_experts(w);
+  if (s == MSK_OK && up != nullptr) s = check_experts(up);
+  if (s != MSK_OK) return s;
   if (up != nullptr && (up->n_experts != w->n_experts || up->rows != w->rows || up->cols != w->cols)) return MSK_ERR_INVALID_ARG;
   if (x->cols != w->cols) return MSK_ERR_INVALID_ARG;
   if (n > (1ll << 30) || x->rows < 0 || x->rows > (1ll << 30)) return MSK_ERR_SHAPE;
@@ -904,6 +954,7 @@ extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* sl
   if (n > 1 && y_stride < w->rows) return MSK_ERR_INVALID_ARG;
   if (!ops_aligned16(x->packed) || !ops_aligned16(x->scales) || !ops_aligned16(w->packed) || !ops_aligned16(w->scales) ||
       (up != nullptr && (!ops_aligned16(up->packed) || !ops_aligned16(up->scales))) ||
+      ((reinterpret_cast<uintptr_t>(w->maps) | (up != nullptr ? reinterpret_cast<uintptr_t>(up->maps) : 0)) & 127) ||
       reinterpret_cast<uintptr_t>(y) % dtype_bytes(y_dtype) ||
       ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(offsets) | reinterpret_cast<uintptr_t>(w->tensor_scales)) & 3) ||
       (up != nullptr && (reinterpret_cast<uintptr_t>(up->tensor_scales) & 3)))
@@ -927,19 +978,13 @@ extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* sl
   const int mats = up != nullptr ? 2 : 1;
   const int slot = mats * (kACodes + kSfABytes) + a.nt / 2 * (kStageK / 2) + (a.nt > 128 ? 2 : 1) * 512 * kSteps;
   a.stages = std::min(kMaxStages, (kRing - (slots != nullptr ? kQuads : 0)) / slot);  // (4 at least)
-  const CUtensorMapDataType bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const long long wrows = (long long)a.E * a.rows;
-  auto codes = [&](CUtensorMap* m, const uint8_t* p, long long rows, int box) {
-    return matrix_map(m, bytes, p, rows, a.K / 2, a.K / 2, box, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B);
-  };
-  auto scales = [&](CUtensorMap* m, const uint8_t* p, long long rows, int box) {
-    return matrix_map(m, bytes, p, rows, a.K / 16, a.K / 16, box, kStageK / 16, CU_TENSOR_MAP_SWIZZLE_NONE);
-  };
-  a.tiled = a.K % kStageK == 0;  // (a tiled copy's rows lie a multiple of 16 bytes apart)
-  if (!codes(&a.w_map, w->packed, wrows, kM) || (up != nullptr && !codes(&a.up_map, up->packed, wrows, kM)) ||
-      (slots == nullptr && (!codes(&a.x_map, x->packed, x->rows, 64) || !codes(&a.x16_map, x->packed, x->rows, 16))) ||
-      (a.tiled && (!scales(&a.ws_map, w->scales, wrows, kM) || (up != nullptr && !scales(&a.us_map, up->scales, wrows, kM)) ||
-                   (slots == nullptr && !scales(&a.xs_map, x->scales, x->rows, a.nt)))))
+  a.tiled = tiled_scales(a.K);
+  s = weight_maps(w, &a.w_map, &a.ws_map);
+  if (s == MSK_OK && up != nullptr) s = weight_maps(up, &a.up_map, &a.us_map);
+  if (s != MSK_OK) return s;
+  if (slots == nullptr && ((a.nt >= 128 && !codes_map(&a.x_map, x->packed, x->rows, a.K, 64)) ||
+                           !codes_map(&a.x16_map, x->packed, x->rows, a.K, 16) ||
+                           (a.tiled && !scales_map(&a.xs_map, x->scales, x->rows, a.K, a.nt))))
     return MSK_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = up != nullptr ? (slots != nullptr ? launch_products<true, true>(a, tiles, st) : launch_products<true, false>(a, tiles, st))

@@ -93,6 +93,21 @@ def test_experts(M, lib, change, status):
 
 
 @pytest.mark.parametrize("change,status", [
+    (dict(w=None), INVALID), (dict(ws=None), INVALID), (dict(maps=None), INVALID), (dict(E=0), SHAPE), (dict(E=1025), SHAPE),
+    (dict(rows=0), SHAPE), (dict(cols=96), SHAPE), (dict(w=P + 8), ALIGN), (dict(ws=P + 8), ALIGN), (dict(maps=P + 32), ALIGN)])
+def test_experts_maps(M, lib, change, status):
+    a = dict(w=P, ws=P, E=4, rows=128, cols=128, maps=P)
+    a.update(change)
+    w = ctypes.pointer(M.Fp4ExpertsC(a["w"], a["ws"], None, a["E"], a["rows"], a["cols"], None))
+    assert lib.msk_fp4_experts_maps(w, a["maps"]) == status
+    assert lib.msk_fp4_experts_maps(None, P) == INVALID
+    # an address of maps that is not aligned is refused before it is read
+    x = ctypes.pointer(M.Nvfp4Desc(P, P, 1.0, 50, 128))
+    w = ctypes.pointer(M.Fp4ExpertsC(P, P, None, 4, 128, 128, P + 8))
+    assert lib.msk_experts_fp4(x, P, 2, 100, P, w, None, P, BF16, 128, None) == ALIGN
+
+
+@pytest.mark.parametrize("change,status", [
     (dict(tokens=0), OK), (dict(cols=0), OK), (dict(tokens=-1), INVALID), (dict(ydt=3), INVALID), (dict(odt=9), INVALID),
     (dict(rows=-1), INVALID), (dict(k=0), SHAPE), (dict(cols=-1), SHAPE), (dict(tokens=1 << 30), SHAPE),
     (dict(tokens=1 << 20, cols=1 << 19, k=1, ys=1 << 20, os=1 << 20), SHAPE), (dict(y=None), INVALID), (dict(places=None), INVALID),
