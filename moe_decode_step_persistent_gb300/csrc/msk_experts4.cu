@@ -486,25 +486,26 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         if (el) {
           const uint32_t dst = ring + st * slot_bytes, b = first(bars.full[st]);
           const int x = s * (kStageK / 2);
+          // (scales first: they are put in order while the codes are on their way)
+          if (a.tiled) {
+            const uint32_t r = bar(bars.rfull[st]);
+            const int xs = s * (kStageK / 16);
+            mbar_arrive_expect_tx(r, warp == 0 ? kMats * kSfABytes : a.nt * (kStageK / 16));
+            if (warp == 1) {
+              tma_load_2d(dst + off_sfb, &a.xs_map, xs, p0, r);
+            } else {
+              tma_load_2d(dst + off_sfa, &a.ws_map, xs, row, r);
+              if (GLU) tma_load_2d(dst + off_sfa + kSfABytes, &a.us_map, xs, row, r);
+            }
+          }
           if (rank == 0) mbar_arrive_expect_tx(bar(bars.full[st]), warp == 0 ? 2 * kMats * kACodes : n * (kStageK / 2));
-          const uint32_t r = bar(bars.rfull[st]);
-          const int xs = s * (kStageK / 16);
           if (warp == 1) {
             int j = 0;
             for (; j + 64 <= n / 2; j += 64) pair_load_2d(dst + off_b + j * 128, &a.x_map, x, row + j, b);
             for (; j < n / 2; j += 16) pair_load_2d(dst + off_b + j * 128, &a.x16_map, x, row + j, b);
-            if (a.tiled) {
-              mbar_arrive_expect_tx(r, a.nt * (kStageK / 16));
-              tma_load_2d(dst + off_sfb, &a.xs_map, xs, p0, r);
-            }
           } else {
             pair_load_2d(dst, &a.w_map, x, row, b);
             if (GLU) pair_load_2d(dst + kACodes, &a.up_map, x, row, b);
-            if (a.tiled) {
-              mbar_arrive_expect_tx(r, kMats * kSfABytes);
-              tma_load_2d(dst + off_sfa, &a.ws_map, xs, row, r);
-              if (GLU) tma_load_2d(dst + off_sfa + kSfABytes, &a.us_map, xs, row, r);
-            }
           }
         }
         __syncwarp();
