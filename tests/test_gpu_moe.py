@@ -491,3 +491,134 @@ def test_runs_repeat_bit_for_bit(M):
         now = (offsets, slots, places, y)
         first = first or now
         assert all(torch.equal(a, b) for a, b in zip(first, now))
+
+
+FIRST_CAPTURED = """
+import torch
+import moe_decode_step_persistent_gb300 as M
+E, k, T = 40, 4, 900
+logits = torch.randn(T, E, device="cuda")
+x = torch.randn(T, 256, device="cuda").bfloat16()
+def weights(rows, cols):
+    return M.Fp4Experts(torch.full((E, rows, cols // 2), 0x22, dtype=torch.uint8, device="cuda"),
+                        torch.full((E, rows, cols // 16), 0x38, dtype=torch.uint8, device="cuda"))
+gate, up, down, odd = weights(96, 256), weights(96, 256), weights(256, 96 // 32 * 64), weights(32, 320)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    experts, gates = M.msk_moe_route(logits, k)
+    offsets, slots, places = M.msk_moe_sort(experts, E)
+    xq = M.msk_quantize_fp4(x)
+    xv = M.msk_dequantize_fp4(xq, dtype=torch.float32)
+    h = M.msk_experts_fp4(xq, gate, offsets, up=up, slots=slots, top_k=k)
+    p = M.msk_experts_fp4(xq, gate, offsets, slots=slots, top_k=k, out_dtype=torch.float32)
+    z = M.msk_experts_fp4(M.msk_quantize_fp4(torch.cat((h, h), 1)), down, offsets)
+    out = M.msk_moe_combine(z, places, gates)
+g.replay()
+torch.cuda.synchronize()
+want = xv.sum(1)[slots.long() // k]
+assert (p - want.unsqueeze(1)).abs().max() < 1e-3 * want.abs().max()
+assert torch.isfinite(out).all()
+M.msk_ops_check()
+print("captured")
+"""
+
+
+def test_captured_without_a_call_before(M):
+    """The process's first calls are captured ones."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
+
+
+def test_behind_an_event_of_another_stream(M):
+    """Calls wait for what their stream waits for, whatever ran before them: they start early."""
+    gate, _ = make_experts(M, 4, 8, 128, 256)
+    k, T = 2, 300
+    src = [(randn(30 + i, T, 8).cuda(), randn(40 + i, T, 256).bfloat16().cuda()) for i in range(4)]
+    logits, x = torch.zeros(T, 8, device="cuda"), torch.zeros(T, 256, dtype=torch.bfloat16, device="cuda")
+    big, side = torch.zeros(1 << 26, device="cuda"), torch.cuda.Stream()
+
+    def run(l, v):
+        experts, gates = M.msk_moe_route(l, k)
+        offsets, slots, places = M.msk_moe_sort(experts, 8)
+        y = M.msk_experts_fp4(M.msk_quantize_fp4(v), gate, offsets, slots=slots, top_k=k)
+        return M.msk_moe_combine(y, places, gates)
+
+    want = [run(l, v) for l, v in src]
+    torch.cuda.synchronize()
+    got = []
+    for l, v in src:
+        run(logits, x)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            big.add_(1.0)  # tens of microseconds, then the inputs
+            logits.copy_(l)
+            x.copy_(v)
+        torch.cuda.current_stream().wait_stream(side)
+        got.append(run(logits, x))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("counts,rows,cols,glu,gather", [
+    ([2], 8, 131072, False, False), ([1, 2], 24, 16384, True, True), ([1] * 1024, 16, 64, False, True), ([1] * 1024, 40, 256, True, False)])
+def test_products_of_extreme_sizes(M, counts, rows, cols, glu, gather):
+    run_products(M, counts, rows, cols, glu, gather, out="fp32")
+
+
+def test_maps_of_other_weights_are_refused(M):
+    import ctypes
+    a, _ = make_experts(M, 1, 2, 64, 128)
+    b, _ = make_experts(M, 2, 2, 64, 128)
+    c, s = random_fp4(3, 5, 128)
+    x, off = M.Fp4Weight(c.cuda(), s.cuda()), torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
+    base = M.msk_experts_fp4(x, a, off)
+    made = a.desc.contents.maps
+    a.desc.contents.maps = None                   # made for the call instead
+    assert torch.equal(M.msk_experts_fp4(x, a, off), base)
+    a.desc.contents.maps = b.desc.contents.maps
+    with pytest.raises(M.MskError) as e:
+        M.msk_experts_fp4(x, a, off)
+    assert e.value.status == M.MSK_ERR_INVALID_ARG
+    with pytest.raises(M.MskError):
+        M.msk_experts_fp4(x, b, off, up=a)
+    a.desc.contents.maps = made
+
+
+def test_quantised_weights_in_a_product_of_unquantised_rows(M):
+    """An Fp4Weight made by msk_quantize_fp4 is a weight of msk_linear_fp4."""
+    w, x = randn(1, 300, 512) * 0.02, randn(2, 5, 512).bfloat16()
+    q = M.msk_quantize_fp4(w.cuda(), 4.4e-5)
+    y = M.msk_linear_fp4(x.cuda(), q, out_dtype=torch.float32)
+    v = values64(q.packed.cpu(), q.scales.cpu(), 4.4e-5)
+    ref, mag = x.double() @ v.T, x.double().abs() @ v.abs().T
+    assert ((y.cpu().double() - ref).abs() <= 2.0 ** -24 * ref.abs() + (512 + 64) * 2.0 ** -23 * mag).all()
+
+
+def test_beside_a_launch_of_the_step(M):
+    """What the step's launch does between its pooled vectors and their experts' sum, done by the operators on the same
+    vectors.  Rows between the two projections are kept in fp32, as in the launch.  The experts are the same; codes of
+    the rows between differ where the two exponentials and orders of summation put a value on another side of a border:
+    at most one in 500 of them here, and the sums' cosine stays above 0.999 (the step's own bar)."""
+    import msk_synth as S
+    from tests._gpu import Setup, read_scratch, run_layers
+    wl = S.scaled(S.WORKLOADS["tiny"], tokens=16, cached=64, windows=(0, 0), pooled=256, inter=256, top_k=4)
+    st = Setup(wl)
+    run_layers(st, st.hidden(), st.fresh_kv(), wl.positions)
+    torch.cuda.synchronize()
+    pooled, logits, sq_codes, m = (read_scratch(st, n) for n in ("pooled", "logits", "sq_codes", "mvec"))
+    lt = st.lts_cpu[1]
+    gate, up, down = (M.Fp4Experts(*(t.cuda() for t in w)) for w in (lt.gate, lt.up, lt.down))
+    experts, gates = M.msk_moe_route(logits, wl.top_k)
+    offsets, slots, places = M.msk_moe_sort(experts, wl.n_experts)
+    h = M.msk_experts_fp4(M.msk_quantize_fp4(pooled), gate, offsets, up=up, slots=slots, top_k=wl.top_k, out_dtype=torch.float32)
+    hq = M.msk_quantize_fp4(h)
+    out = M.msk_moe_combine(M.msk_experts_fp4(hq, down, offsets), places, gates)
+    mine = hq.packed[places.flatten().long()]                # by slot, as in the launch
+    assert (mine != sq_codes).float().mean().item() <= 1 / 500
+    a, b = out.double().flatten(), m.double().flatten()
+    assert float(a @ b / (a.norm() * b.norm())) >= 0.999
+    st.model.close()
