@@ -22,10 +22,19 @@ struct Rows4 {
   const void* x;
   uint8_t* codes;
   uint8_t* scales;
-  long long rows, x_stride;
-  int pieces;  // of a row
+  long long n, x_stride;  // pieces in all
+  int pieces;             // of a row; 0 where rows lie one behind the other
   float ts;
 };
+
+// Where piece i of E elements begins in x, in elements.
+template <int E>
+__device__ __forceinline__ long long piece_at(const Rows4& a, long long i) {
+  if (a.pieces == 0) return i * E;
+  // (a division of 64 bits is some 40 instructions)
+  const long long r = a.n <= 0xFFFFFFFFll ? (long long)((uint32_t)i / (uint32_t)a.pieces) : i / a.pieces;
+  return r * a.x_stride + (i - r * a.pieces) * E;
+}
 
 // 32 bytes (aligned so).
 __device__ __forceinline__ void ldg256(const void* p, uint32_t (&w)[8]) {
@@ -40,21 +49,30 @@ template <int DT, bool WIDE>
 __global__ void __launch_bounds__(256) quantize_kernel(const Rows4 a) {
   grid_dep_wait();
   grid_dep_launch();
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, r = i / a.pieces;
-  if (r >= a.rows) return;
-  float x[16];
-  const long long from = r * a.x_stride + (i - r * a.pieces) * 16;
+  const long long step = (long long)gridDim.x * 256;
+  long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (WIDE) {
+    // (the next block's elements are on their way while one is quantised)
     uint32_t w[8];
-    ldg256(static_cast<const uint16_t*>(a.x) + from, w);
+    if (i < a.n) ldg256(static_cast<const uint16_t*>(a.x) + piece_at<16>(a, i), w);
+    for (; i < a.n; i += step) {
+      float x[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 f = unpack16(w[j], DT == MSK_FP16);
-      x[2 * j] = f.x, x[2 * j + 1] = f.y;
+      for (int j = 0; j < 8; ++j) {
+        const float2 f = unpack16(w[j], DT == MSK_FP16);
+        x[2 * j] = f.x, x[2 * j + 1] = f.y;
+      }
+      if (i + step < a.n) ldg256(static_cast<const uint16_t*>(a.x) + piece_at<16>(a, i + step), w);
+      uint32_t sc;
+      const uint2 c = quantise16(x, a.ts, sc);
+      *reinterpret_cast<uint2*>(a.codes + i * 8) = c;
+      a.scales[i] = (uint8_t)sc;
     }
-  } else {
-    load16<DT>(a.x, from, x);
+    return;
   }
+  if (i >= a.n) return;
+  float x[16];
+  load16<DT>(a.x, piece_at<16>(a, i), x);
   uint32_t sc;
   const uint2 c = quantise16(x, a.ts, sc);
   *reinterpret_cast<uint2*>(a.codes + i * 8) = c;
@@ -69,7 +87,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const Rows4 a) {
   using Codes = std::conditional_t<E == 4, uint16_t, uint32_t>;
   grid_dep_wait();
   grid_dep_launch();
-  const long long i0 = (long long)blockIdx.x * (256 * U) + threadIdx.x, n = a.rows * a.pieces;
+  const long long i0 = (long long)blockIdx.x * (256 * U) + threadIdx.x, n = a.n;
   uint32_t c[U], e[U];
 #pragma unroll
   for (int k = 0; k < U; ++k) {
@@ -94,7 +112,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const Rows4 a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       o[j] = DT == MSK_FP32 ? __float_as_uint(x[j]) : pack16(x[2 * j % E], x[(2 * j + 1) % E], DT == MSK_FP16);
-    const long long r = i / a.pieces, off = r * a.x_stride + (i - r * a.pieces) * E;
+    const long long off = piece_at<E>(a, i);
     *reinterpret_cast<uint4*>(static_cast<char*>(const_cast<void*>(a.x)) + off * (16 / E)) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
@@ -115,11 +133,13 @@ msk_status rows_call(bool write, const void* x, int32_t dtype, int64_t rows, int
   if (s != MSK_OK) return s;
   Rows4 a{};
   a.x = x, a.codes = const_cast<uint8_t*>(codes), a.scales = const_cast<uint8_t*>(scales);
-  a.rows = rows, a.x_stride = rows > 1 ? stride : 0, a.ts = ts;
   const int piece = write ? 16 : dtype == MSK_FP32 ? 4 : 8, per = write ? 256 : 256 * kReadUnroll;
-  a.pieces = (int)(cols / piece);
-  const OpsLaunch l(dim3((unsigned)((rows * a.pieces + per - 1) / per)), 256, 0, static_cast<cudaStream_t>(stream));
-  const bool wide = dtype != MSK_FP32 && ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(a.x_stride * 2)) & 31) == 0;
+  a.n = rows * (cols / piece), a.x_stride = rows > 1 ? stride : 0, a.ts = ts;
+  a.pieces = rows == 1 || stride == cols ? 0 : (int)(cols / piece);
+  const bool wide = write && dtype != MSK_FP32 && ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(a.x_stride * 2)) & 31) == 0;
+  // (wide: as many blocks as run at once, each going on)
+  const long long blocks = (a.n + per - 1) / per;
+  const OpsLaunch l(dim3((unsigned)(wide ? std::min<long long>(blocks, 8ll * nsm) : blocks)), 256, 0, static_cast<cudaStream_t>(stream));
   auto launch = [&](void (*q)(Rows4), void (*qw)(Rows4), void (*d)(Rows4)) {
     return cudaLaunchKernelEx(&l.cfg, !write ? d : wide ? qw : q, a);
   };
