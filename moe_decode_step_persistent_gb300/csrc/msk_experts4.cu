@@ -36,13 +36,6 @@ __device__ __forceinline__ long long piece_at(const Rows4& a, long long i) {
   return r * a.x_stride + (i - r * a.pieces) * E;
 }
 
-// 32 bytes (aligned so).
-__device__ __forceinline__ void ldg256(const void* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
-}
-
 // A block of 16 elements a thread, as in the 4-bit cache's writer.  WIDE: rows of
 // 16-bit elements are aligned to 32 bytes, one load's.
 template <int DT, bool WIDE>

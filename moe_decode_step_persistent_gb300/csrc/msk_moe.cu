@@ -316,81 +316,103 @@ struct Combine {
   int cols, top_k;
 };
 
-// A thread has 16 bytes of a token's columns (V elements; one element where
-// rows are not aligned to 16 bytes), its ranks' rows all loaded before they are
-// summed, eight at a time.  Sums in fp32, by rank.
-template <int DT, int ODT, bool VEC>
+__device__ __forceinline__ long long token_of(const Combine& a, long long i) {
+  // (a division of 64 bits is some 40 instructions)
+  return a.tokens * a.pieces <= 0xFFFFFFFFll ? (long long)((uint32_t)i / (uint32_t)a.pieces) : i / a.pieces;
+}
+
+// V sums as V elements of type ODT (an address aligned to 16 bytes or to V elements).
+template <int ODT, int V>
+__device__ __forceinline__ void store_sums(void* out, long long at, const float (&s)[V]) {
+  if constexpr (V == 1) {
+    if (ODT == MSK_FP32) static_cast<float*>(out)[at] = s[0];
+    else if (ODT == MSK_FP16) static_cast<__half*>(out)[at] = __float2half_rn(s[0]);
+    else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(s[0]);
+  } else if constexpr (ODT == MSK_FP32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) p[j] = make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+  } else {
+    uint32_t x[V / 2];
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) x[j] = pack16(s[2 * j], s[2 * j + 1], ODT == MSK_FP16);
+    uint16_t* p = static_cast<uint16_t*>(out) + at;
+    if constexpr (V == 4) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(x[0], x[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V / 8; ++j) reinterpret_cast<uint4*>(p)[j] = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+    }
+  }
+}
+
+// A thread has B bytes of a token's columns (V elements; B = 0: one element, where
+// rows are not aligned), its ranks' rows all loaded before they are summed, eight at
+// a time.  Sums in fp32, by rank.
+template <int DT, int ODT, int B>
 __global__ void __launch_bounds__(256) combine_kernel(const Combine a) {
-  constexpr int S = DT == MSK_FP32 ? 4 : 2, V = VEC ? 16 / S : 1, U = 8;
+  constexpr int S = DT == MSK_FP32 ? 4 : 2, V = B ? B / S : 1, U = 8, W = B ? B / 4 : 1;
   grid_dep_wait();
   grid_dep_launch();
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long t = i / a.pieces;
-  if (t >= a.tokens) return;
+  if (i >= a.tokens * a.pieces) return;
+  const long long t = token_of(a, i);
   const int c = (int)(i - t * a.pieces) * V;
   float sum[V] = {};
   for (int r0 = 0; r0 < a.top_k; r0 += U) {
-    uint4 w[U];
+    uint32_t w[U][W];
     float g[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const long long slot = t * a.top_k + r0 + u;
       const int p = r0 + u < a.top_k ? __ldg(a.places + slot) : -1;
       const bool in = p >= 0 && p < a.y_rows;  // (a dropped slot's row is not read)
-      g[u] = in && a.gates != nullptr ? __ldg(a.gates + slot) : 1.f;
-      w[u] = make_uint4(0, 0, 0, 0);
+      g[u] = !in ? 0.f : a.gates != nullptr ? __ldg(a.gates + slot) : 1.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[u][j] = 0u;
+      if (!in) continue;
       const long long at = p * a.y_stride + c;
-      if (!in) g[u] = 0.f;
-      else if (VEC) w[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.y) + at * S));
-      else w[u].x = __float_as_uint(element<DT>(a.y, at));
+      const char* from = static_cast<const char*>(a.y) + at * S;
+      if constexpr (B == 32) {
+        ldg256(from, w[u]);
+      } else if constexpr (B == 16) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(from));
+        w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
+      } else {
+        w[u][0] = __float_as_uint(element<DT>(a.y, at));
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-      if (!VEC || DT == MSK_FP32) {
+      if constexpr (B == 0 || DT == MSK_FP32) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] = fmaf(g[u], __uint_as_float(x[j]), sum[j]);
+        for (int j = 0; j < V; ++j) sum[j] = fmaf(g[u], __uint_as_float(w[u][j]), sum[j]);
       } else {
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) {
-          const float2 f = unpack16(x[j], DT == MSK_FP16);
-          sum[2 * j] = fmaf(g[u], f.x, sum[2 * j]), sum[2 * j + 1 < V ? 2 * j + 1 : 0] = fmaf(g[u], f.y, sum[2 * j + 1 < V ? 2 * j + 1 : 0]);
+          const float2 f = unpack16(w[u][j], DT == MSK_FP16);
+          sum[2 * j] = fmaf(g[u], f.x, sum[2 * j]), sum[2 * j + 1] = fmaf(g[u], f.y, sum[2 * j + 1]);
         }
       }
     }
   }
-  const long long o = t * a.out_stride + c;
-  if (VEC) {
-    if (ODT == MSK_FP32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
-#pragma unroll
-      for (int j = 0; j < V / 4; ++j) p[j] = make_float4(sum[4 * j % V], sum[(4 * j + 1) % V], sum[(4 * j + 2) % V], sum[(4 * j + 3) % V]);
-    } else {
-      uint32_t x[V / 2 ? V / 2 : 1];
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) x[j] = pack16(sum[2 * j], sum[(2 * j + 1) % V], ODT == MSK_FP16);
-      uint16_t* p = static_cast<uint16_t*>(a.out) + o;
-      if (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1 % (V / 2 ? V / 2 : 1)], x[2 % (V / 2 ? V / 2 : 1)], x[3 % (V / 2 ? V / 2 : 1)]);
-      else *reinterpret_cast<uint2*>(p) = make_uint2(x[0], x[1 % (V / 2 ? V / 2 : 1)]);
-    }
-  } else {
-    if (ODT == MSK_FP32) static_cast<float*>(a.out)[o] = sum[0];
-    else if (ODT == MSK_FP16) static_cast<__half*>(a.out)[o] = __float2half_rn(sum[0]);
-    else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(sum[0]);
-  }
+  store_sums<ODT, V>(a.out, t * a.out_stride + c, sum);
 }
 
 template <int DT, int ODT>
 cudaError_t launch_combine(Combine& a, cudaStream_t st) {
-  constexpr int S = DT == MSK_FP32 ? 4 : 2, O = ODT == MSK_FP32 ? 4 : 2, V = 16 / S;
-  // (an output piece has V elements of the output's type: 8 to 32 bytes)
-  constexpr int OA = V * O < 16 ? V * O : 16;
-  const bool vec = a.cols % V == 0 && ops_aligned16(a.y) && a.y_stride % V == 0 && reinterpret_cast<uintptr_t>(a.out) % OA == 0 &&
-                   a.out_stride * O % OA == 0;
-  a.pieces = vec ? a.cols / V : a.cols;
-  const long long blocks = (a.tokens * a.pieces + 255) / 256;
-  const OpsLaunch l(dim3((unsigned)blocks), 256, 0, st);
-  return cudaLaunchKernelEx(&l.cfg, vec ? combine_kernel<DT, ODT, true> : combine_kernel<DT, ODT, false>, a);
+  constexpr int S = DT == MSK_FP32 ? 4 : 2, O = ODT == MSK_FP32 ? 4 : 2;
+  auto fits = [&](int bytes) {  // rows of y in pieces of `bytes`, of out in what they become, 16 at most
+    const int v = bytes / S, o = std::min(16, v * O);
+    return a.cols % v == 0 && reinterpret_cast<uintptr_t>(a.y) % bytes == 0 && a.y_stride * S % bytes == 0 &&
+           reinterpret_cast<uintptr_t>(a.out) % o == 0 && a.out_stride * O % o == 0;
+  };
+  // (32 bytes where 4M outputs and more fill the GPU all the same: 8192 tokens x 8 x 2048
+  // columns 50.4 us, with 16 52.6; fewer have the more threads for it)
+  const int b = fits(32) && a.tokens * a.cols >= 1 << 22 ? 32 : fits(16) ? 16 : 0;
+  a.pieces = b ? a.cols / (b / S) : a.cols;
+  const OpsLaunch l(dim3((unsigned)((a.tokens * a.pieces + 255) / 256)), 256, 0, st);
+  return cudaLaunchKernelEx(&l.cfg, b == 32 ? combine_kernel<DT, ODT, 32> : b == 16 ? combine_kernel<DT, ODT, 16> : combine_kernel<DT, ODT, 0>, a);
 }
 
 template <int DT>
