@@ -163,14 +163,14 @@ cudaError_t launch_route(const Route& a, bool aligned, int nsm, cudaStream_t st)
 // ---------------------------------------------------------------------------
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kSortCluster = 16;
+constexpr int kSortCluster = 16, kSortClusters = 4;
 
 struct Sort {
   const int32_t* experts;
   int32_t *offsets, *slots, *places;
   long long n;
   long long per_warp;  // slots of a warp, a multiple of 32
-  int E, blocks;
+  int E, blocks;       // blocks of a cluster
 };
 
 // The lanes whose expert is this lane's, e in [-1, 2^bits): a ballot a bit (the
@@ -185,26 +185,32 @@ __device__ __forceinline__ uint32_t same_expert(int e, int bits) {
   return m;
 }
 
-// One cluster (of one block for few slots) sorts everything in one launch: the
-// slots are split into runs, one a warp, in their order.  Each warp counts its
-// run's experts, in shared memory, the lanes with the same expert as one; the
-// block sums its warps' counts, the cluster its blocks', and the experts' are
-// scanned.  A slot's place is its warp's first one of its expert and its number
-// among the warp's.  No atomics: the places do not depend on an order of arrival.
-// 131072 slots: bound by the 16 SMs' issue of ballots and of single stores; few
-// slots: by a chain of latencies.
+// The slots are split into runs, one a warp, in their order, the runs over the
+// blocks of a cluster (one block for few slots) and, of many slots, over several
+// clusters.  Each warp counts its run's experts, in shared memory, the lanes with the
+// same expert as one; the block sums its warps' counts, the cluster its blocks', and
+// the experts' are scanned.  A slot's place is its warp's first one of its expert
+// and its number among the warp's.  Clusters do not wait for one another: each
+// counts the slots of the others too, where the order in which counts are added
+// does not matter.  One launch, no workspace; the places do not depend on an order
+// of arrival.
+// 131072 slots of 256 experts: 9.4 us, bound by the SMs' issue of ballots and of single
+// stores; few slots: a chain of latencies, 3.5.
 constexpr int kHeld = 8;
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const Sort a) {
   extern __shared__ __align__(16) int32_t sort_smem[];
   int32_t* count = sort_smem;                 // [warps][E], then each warp's next place
-  int32_t* total = count + kSortWarps * a.E;  // [E]: this block's (the cluster reads it)
+  // [E] each, of this block (the cluster reads them): its runs' slots, and its share of those of
+  // the clusters before and of all the others
+  int32_t *total = count + kSortWarps * a.E, *earlier = total + a.E, *others = earlier + a.E;
   __shared__ int32_t warp_sum[kSortWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x;
-  for (int i = tid; i < kSortWarps * a.E; i += kSortThreads) count[i] = 0;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % a.blocks, cluster = blockIdx.x / a.blocks, clusters = gridDim.x / a.blocks;
+  for (int i = tid; i < (kSortWarps + 3) * a.E; i += kSortThreads) count[i] = 0;
   grid_dep_wait();
   grid_dep_launch();
   __syncthreads();
-  const long long s0 = ((long long)rank * kSortWarps + warp) * a.per_warp, s1 = min(a.n, s0 + a.per_warp);
+  const long long s0 = ((long long)blockIdx.x * kSortWarps + warp) * a.per_warp, s1 = min(a.n, s0 + a.per_warp);
   int32_t* mine = count + warp * a.E;
   const int bits = 32 - __clz(a.E - 1 | 1);
   // a step's experts, and its slots' numbers among those of their expert in the run: of a
@@ -233,14 +239,30 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const Sort a) {
       if (longer && s + 32 * j + lane < s1) a.places[s + 32 * j + lane] = number[j];
     }
   }
+  if (clusters > 1) {
+    // the other clusters' slots, every blocks-th 4096 of them here
+    const long long c0 = (long long)cluster * a.blocks * kSortWarps * a.per_warp, c1 = min(a.n, c0 + a.blocks * kSortWarps * a.per_warp);
+    for (long long s = (long long)rank * 4 * kSortThreads; s < a.n; s += (long long)a.blocks * 4 * kSortThreads) {
+      int e[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const long long slot = s + j * kSortThreads + tid;
+        e[j] = slot < a.n && (slot < c0 || slot >= c1) ? __ldg(a.experts + slot) : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (e[j] < 0 || e[j] >= a.E) continue;
+        atomicAdd(others + e[j], 1);
+        if (s + j * kSortThreads + tid < c0) atomicAdd(earlier + e[j], 1);
+      }
+    }
+  }
   __syncthreads();
   // (E <= the threads of a block: thread e has expert e)
-  int32_t c[kSortWarps], sum = 0, before = 0;
+  int32_t sum = 0, before = 0;
   if (tid < a.E) {
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) c[w] = count[w * a.E + tid];
-#pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) sum += c[w];
+    for (int w = 0; w < kSortWarps; ++w) sum += count[w * a.E + tid];
     total[tid] = sum;
   }
   if (a.blocks > 1) {
@@ -256,6 +278,23 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const Sort a) {
       sum = 0;
 #pragma unroll
       for (int b = 0; b < kSortCluster; ++b) before += b < rank ? v[b] : 0, sum += v[b];
+      if (clusters > 1) {
+        const uint32_t ae = smem_u32(earlier + tid), ao = smem_u32(others + tid);
+#pragma unroll
+        for (int b = 0; b < kSortCluster; ++b) {
+          v[b] = 0;
+          if (b < a.blocks) asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[b]) : "r"(mapa(ae, b)) : "memory");
+        }
+#pragma unroll
+        for (int b = 0; b < kSortCluster; ++b) before += v[b];
+#pragma unroll
+        for (int b = 0; b < kSortCluster; ++b) {
+          v[b] = 0;
+          if (b < a.blocks) asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[b]) : "r"(mapa(ao, b)) : "memory");
+        }
+#pragma unroll
+        for (int b = 0; b < kSortCluster; ++b) sum += v[b];
+      }
     }
     cluster_arrive();  // (waited for at the end: its totals have been read)
   }
@@ -275,9 +314,12 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const Sort a) {
   }
   if (tid < a.E) {
     int32_t place = scan - sum + before;
-#pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) count[w * a.E + tid] = place, place += c[w];
-    if (rank == 0) {
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int32_t c = count[w * a.E + tid];
+      count[w * a.E + tid] = place, place += c;
+    }
+    if (blockIdx.x == 0) {
       a.offsets[tid + 1] = scan;
       if (tid == 0) a.offsets[0] = 0;
     }
@@ -299,7 +341,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const Sort a) {
       if (place >= 0) a.slots[place] = (int32_t)slot;
     }
   }
-  for (long long p = all + (long long)rank * kSortThreads + tid; p < a.n; p += (long long)a.blocks * kSortThreads) a.slots[p] = -1;
+  for (long long p = all + (long long)blockIdx.x * kSortThreads + tid; p < a.n; p += (long long)gridDim.x * kSortThreads) a.slots[p] = -1;
   if (a.blocks > 1) cluster_wait();
 }
 
@@ -465,21 +507,24 @@ extern "C" msk_status msk_moe_sort(const int32_t* experts, int64_t n, int32_t n_
   if (s != MSK_OK) return s;
   Sort a{};
   a.experts = experts, a.offsets = offsets, a.slots = slots, a.places = places, a.n = n, a.E = n_experts;
-  // (a block goes through 4096 slots, 4 steps a warp, in the time that a cluster's barriers take)
+  // (a block goes through 4096 slots, 4 steps a warp, in the time that a cluster's barriers take;
+  // with four clusters of 16 65536 slots take 8.0 us and 131072 9.4, with one 9.0 and 13.3, with
+  // two 8.7 and 11.4, with eight, which do not all run at once, 8.0 and 16.5)
   a.blocks = n <= 4096 ? 1 : n <= 8 * 4096 ? 8 : kSortCluster;
-  const long long warps = (long long)a.blocks * kSortWarps;
+  const int clusters = a.blocks < kSortCluster ? 1 : (int)std::min<int64_t>(kSortClusters, (n + 16383) / 16384);
+  const long long warps = (long long)a.blocks * clusters * kSortWarps;
   a.per_warp = ((n + warps - 1) / warps + 31) / 32 * 32;
-  const int smem = (kSortWarps + 1) * n_experts * 4;
+  const int smem = (kSortWarps + 3) * n_experts * 4;
   static std::atomic<bool> ready[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSK_ERR_CUDA;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSortWarps + 1) * kMaxExperts * 4) != cudaSuccess ||
+    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSortWarps + 3) * kMaxExperts * 4) != cudaSuccess ||
         cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       return MSK_ERR_CUDA;
     ready[dev].store(true, std::memory_order_release);
   }
-  const OpsLaunch l(dim3((unsigned)a.blocks), kSortThreads, smem, static_cast<cudaStream_t>(stream), a.blocks);
+  const OpsLaunch l(dim3((unsigned)(a.blocks * clusters)), kSortThreads, smem, static_cast<cudaStream_t>(stream), a.blocks);
   return cudaLaunchKernelEx(&l.cfg, sort_kernel, a) == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }
 
