@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(128) route_kernel(const Route a) {
 template <int DT, int C>
 cudaError_t launch_route(const Route& a, bool aligned, int nsm, cudaStream_t st) {
   // (as many blocks as run at once: a warp goes on with its bias in registers)
-  const OpsLaunch l(dim3((unsigned)std::min<long long>((a.tokens + 3) / 4, nsm * 10)), 128, 0, st);
+  const OpsLaunch l(dim3((unsigned)std::min<long long>((a.tokens + 3) / 4, nsm * 16)), 128, 0, st);
   if (C * (DT == MSK_FP32 ? 4 : 2) % 16 == 0 && aligned)
     return cudaLaunchKernelEx(&l.cfg, route_kernel<DT, C, C * (DT == MSK_FP32 ? 4 : 2) % 16 == 0>, a);
   return cudaLaunchKernelEx(&l.cfg, route_kernel<DT, C, false>, a);
