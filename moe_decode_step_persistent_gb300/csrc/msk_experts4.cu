@@ -194,7 +194,6 @@ struct Tile {
   int e, m;       // expert, block of weight rows
   int p0, count;  // first place and number of places
   int n;          // count, up to the MMA's next N
-  float f[4];     // w's scale as two factors, up's
 };
 
 struct Bars {
@@ -258,6 +257,18 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// Two tensors' scales as a factor and 1 or, where the product might leave fp32's
+// range, as a significand with a half of the power of two and the other half, so that
+// no product with them leaves it unless the result does.
+__device__ __forceinline__ float2 scale_factors(float w, float x) {
+  const int ew = (__float_as_uint(w) >> 23) & 255, ex = (__float_as_uint(x) >> 23) & 255;
+  if (ew == 0 || ew == 255 || ex == 0 || ex == 255 || (ew + ex >= 128 && ew + ex <= 380)) return make_float2(w * x, 1.f);
+  const int e2 = max(-250, min(250, ew + ex - 254)), e1 = e2 / 2;
+  const float mw = __uint_as_float((__float_as_uint(w) & 0x807FFFFFu) | 0x3F800000u);
+  const float mx = __uint_as_float((__float_as_uint(x) & 0x807FFFFFu) | 0x3F800000u);
+  return make_float2(mw * mx * exp2i(e1), exp2i(e2 - e1));
+}
+
 // `bytes` (0 or 16) of 16, zeros for the rest.
 __device__ __forceinline__ void cp_async16_some(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -300,8 +311,8 @@ __device__ __forceinline__ unsigned long long silu2(unsigned long long g) {
 // that neighbouring pairs share weights in L2; a pair takes every one that is a
 // multiple of the pairs on.
 //
-// 65536 rows of 256 experts, gate and up of 1024 x 2048: 151 us, 3.6 PFLOP/s, 5.0 TB/s;
-// 8192 x 8192 x 8192: 182 us, 6.0 PFLOP/s.  What bounds full tiles is what a stage takes
+// 65536 rows of 256 experts, gate and up of 1024 x 2048: 150 us, 3.7 PFLOP/s, 5.0 TB/s;
+// 8192 x 8192 x 8192: 180 us, 6.1 PFLOP/s.  What bounds full tiles is what a stage takes
 // of shared memory's 128 bytes a clock (copies in, the MMAs' reads, scales in, read,
 // put in order and read again: 94 KB, with gate and up 110 to 130), and, with weights
 // from DRAM, its latency behind four or five stages.
@@ -466,22 +477,6 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
       for (int k = 0; k < kMaxN / 32; ++k) {
         if (GATHER && lane + 32 * k < count) p[k] = min((int)a.x_rows - 1, (int)((unsigned)max(p[k], 0) / (unsigned)a.top_k));
         source_ring[i % kTiles][lane + 32 * k] = p[k];
-      }
-      if (lane < (GLU ? 2 : 1)) {
-        // The tensors' scales in one factor or, where it might leave fp32's range, in
-        // a significand and a power of two in two halves, so that no product leaves it
-        // unless the result does.
-        const float* p = lane ? a.up_ts : a.w_ts;
-        const float wt = p != nullptr ? __ldg(p + lo) : 1.f;
-        float s = wt * a.x_ts, h = 1.f;
-        const int ew = (__float_as_uint(wt) >> 23) & 255, ex = (__float_as_uint(a.x_ts) >> 23) & 255;
-        if (ew != 0 && ew != 255 && ex != 0 && ex != 255 && (ew + ex < 128 || ew + ex > 380)) {
-          const int e2 = max(-250, min(250, ew + ex - 254)), e1 = e2 / 2;
-          const float mw = __uint_as_float((__float_as_uint(wt) & 0x807FFFFFu) | 0x3F800000u);
-          const float mx = __uint_as_float((__float_as_uint(a.x_ts) & 0x807FFFFFu) | 0x3F800000u);
-          s = mw * mx * exp2i(e1), h = exp2i(e2 - e1);
-        }
-        r.f[2 * lane] = s, r.f[2 * lane + 1] = h;
       }
       if (lane == 0) r.e = lo, r.m = m, r.p0 = p0, r.count = count, r.n = (count + kStepN - 1) / kStepN * kStepN;
       __syncwarp();
@@ -761,12 +756,16 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
       bool ok = true;
       for (int i = 0; i < mine && ok; ++i) {
         const int d = i & 1;
-        ok = wait_tile(i) && wait(bars.accf[d], (i >> 1) & 1);
+        ok = wait_tile(i);
         if (!ok) break;
-        tc_fence_after();
         const Tile& t = tile_ring[i % kTiles];
         const int n = t.n, count = t.count;
-        const float f0 = t.f[0], f1 = t.f[1], u0 = t.f[2], u1 = t.f[3];
+        const float2 f = scale_factors(a.w_ts != nullptr ? __ldg(a.w_ts + t.e) : 1.f, a.x_ts);
+        const float2 g = GLU ? scale_factors(a.up_ts != nullptr ? __ldg(a.up_ts + t.e) : 1.f, a.x_ts) : f;
+        const float f0 = f.x, f1 = f.y, u0 = g.x, u1 = g.y;
+        ok = wait(bars.accf[d], (i >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
         const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + d * kAcc1;
         const int row = t.m * 256 + rank * 128 + quad * 32 + lane;
         T* y = static_cast<T*>(a.y) + (long long)t.p0 * a.y_stride + row;
