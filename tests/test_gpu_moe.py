@@ -633,3 +633,55 @@ def test_beside_a_launch_of_the_step(M):
     a, b = out.double().flatten(), m.double().flatten()
     assert float(a @ b / (a.norm() * b.norm())) >= 0.999
     st.model.close()
+
+
+def test_no_tokens(M):
+    """A prompt of no tokens goes through all of it; experts without tokens write nothing."""
+    E, k, P, I = 6, 2, 128, 64
+    gate, up, down = (make_experts(M, s, E, r, c)[0] for s, r, c in ((1, I, P), (2, I, P), (3, P, I)))
+    x = torch.zeros(0, P, dtype=torch.bfloat16, device="cuda")
+    out, (experts, gates, offsets, slots, xq, h, hq, y) = moe(M, torch.zeros(0, E, device="cuda"), None, x, gate, up, down, k)
+    assert out.shape == (0, P) and experts.shape == (0, k) and y.shape == (0, P) and hq.rows == 0
+    assert offsets.tolist() == [0] * (E + 1)
+    # every slot dropped: nothing is written, sums are 0
+    experts = torch.full((5, k), -1, dtype=torch.int32, device="cuda")
+    offsets, slots, places = M.msk_moe_sort(experts, E)
+    c, s = random_fp4(4, 5, P)
+    y = torch.full((5 * k, I), 4.0, device="cuda")
+    M.msk_experts_fp4(M.Fp4Weight(c.cuda(), s.cuda()), gate, offsets, up=up, slots=slots, top_k=k, out=y)
+    assert (y == 4.0).all() and (M.msk_moe_combine(y, places) == 0).all()
+
+
+def test_rows_that_are_one_and_the_same(M):
+    """A row stride of 0 is read, and refused where rows are written."""
+    x = randn(1, 1, 96).bfloat16().cuda()
+    w = M.msk_quantize_fp4(x.expand(7, 96))
+    one = M.msk_quantize_fp4(x)
+    assert torch.equal(w.packed, one.packed.expand(7, 48)) and torch.equal(w.scales, one.scales.expand(7, 6))
+    flat = torch.zeros(1, 96, device="cuda").expand(7, 96)
+    with pytest.raises(M.MskError):
+        M.msk_dequantize_fp4(w, out=flat)
+    l = randn(2, 1, 16).cuda()
+    e, g = M.msk_moe_route(l.contiguous(), 3)
+    gate, _ = make_experts(M, 1, 1, 16, 96 // 32 * 64)
+    with pytest.raises(ValueError):
+        M.msk_experts_fp4(w, gate, torch.tensor([0, 7], dtype=torch.int32, device="cuda"))
+    v, vv = make_experts(M, 2, 1, 16, 128)
+    c, s = random_fp4(3, 7, 128)
+    with pytest.raises(M.MskError):
+        M.msk_experts_fp4(M.Fp4Weight(c.cuda(), s.cuda()), v, torch.tensor([0, 7], dtype=torch.int32, device="cuda"),
+                          out=torch.zeros(1, 16, device="cuda").expand(7, 16))
+    with pytest.raises(M.MskError):
+        M.msk_moe_combine(randn(4, 6, 16).cuda(), torch.zeros(3, 2, dtype=torch.int32, device="cuda"), out=torch.zeros(1, 16, device="cuda").expand(3, 16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_route_of_many_tokens_with_ties(M, dtype):
+    """Tokens whose logits take few values, several times what runs at once: against a stable sort."""
+    T, E, k = 30000, 256, 8
+    logits = (randn(7, T, E) * 2).round().div(2).to(DT[dtype]).cuda()
+    order = torch.sort(logits.float(), dim=-1, descending=True, stable=True)
+    e, g = M.msk_moe_route(logits, k)
+    assert torch.equal(e, order.indices[:, :k].int())
+    want = torch.softmax(order.values[:, :k].double(), -1)
+    assert ((g.double() - want).abs() <= (2 * (2.0 ** -22 + 16 * 2.0 ** -24) + (k + 1) * 2.0 ** -24) * want).all()
