@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "msk_internal.h"
 #include "msk_ops.cuh"
@@ -161,6 +162,9 @@ constexpr int kProductThreads = 32 * (kEpiWarp0 + kEpiWarps);
 // a tile is one stage, and two at their ends.
 constexpr int kTiles = 8;
 constexpr int kACodes = kM * kStageK / 2, kSfABytes = kM * kStageK / 16;
+// Weights' scales as they come: 32 bytes of a row, which hold the stage's 16, where rows lie
+// no multiple of 16 bytes apart.
+__host__ __device__ constexpr int weight_scales_bytes(int group) { return group > 1 ? 2 * kSfABytes : kSfABytes; }
 constexpr int kRing = 204 * 1024;  // (dynamic shared memory: beside it the tables below and what aligns the ring)
 // Gathered tokens' scales: of four stages and 128 tokens, twice.
 constexpr int kQuadBytes = 128 * kStageK / 16 * 4, kQuads = 2 * kQuadBytes;
@@ -177,7 +181,7 @@ static __device__ uint32_t g_error;  // nonzero once a wait has run out
 struct Experts4 {
   CUtensorMap w_map, up_map;     // [E rows][cols / 2] bytes, boxes of 128 x 128
   CUtensorMap x_map, x16_map;    // [x_rows][cols / 2] bytes, boxes of 64 x 128, of 16 x 128
-  CUtensorMap ws_map, us_map;    // [E rows][cols / 16] bytes of scales, boxes of 128 x 16
+  CUtensorMap ws_map, us_map;    // scales: [E rows / w_group][w_group cols / 16] bytes, boxes of 128 rows
   CUtensorMap xs_map;            // [x_rows][cols / 16], boxes of nt x 16
   const uint8_t *x_codes, *x_scales, *w_scales, *up_scales;
   const float *w_ts, *up_ts;
@@ -186,7 +190,7 @@ struct Experts4 {
   long long y_stride, x_rows;
   int n, E, rows, K, top_k, y_dtype, nt, stages, mblocks;
   float x_ts;
-  bool tiled;  // scales come by copies: columns are a multiple of 256
+  int w_group;  // weights' scales come by copies of so many rows as one (0: threads load them)
 };
 
 // A tile: the pair's 256 weight rows of an expert and up to nt of its tokens.
@@ -256,6 +260,14 @@ __device__ __forceinline__ void pair_arrive(uint32_t bar) {
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 
 // Two tensors' scales as a factor and 1 or, where the product might leave fp32's
 // range, as a significand with a half of the power of two and the other half, so that
@@ -272,10 +284,6 @@ __device__ __forceinline__ float2 scale_factors(float w, float x) {
 // `bytes` (0 or 16) of 16, zeros for the rest.
 __device__ __forceinline__ void cp_async16_some(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// A row's scales of four steps, `step` bytes from one to the next.
-__device__ __forceinline__ void put_scales(uint32_t addr, int step, uint4 w) {
-  sts32(addr, w.x), sts32(addr + step, w.y), sts32(addr + 2 * step, w.z), sts32(addr + 3 * step, w.w);
 }
 
 // silu(g) = g / (1 + e^-g) of two numbers, off by some 2^-21: 2^t for t = -g
@@ -306,8 +314,8 @@ __device__ __forceinline__ unsigned long long silu2(unsigned long long g) {
 // by slots by asynchronous copies of 16 bytes (gathering tiled copies take 66
 // clocks for four rows of 128 bytes).  Scales, row-major in memory, come by tiled
 // copies too and are put into the tensor cores' order by threads; where columns are
-// no multiple of 256 threads load them (a load of 32 rows' scales holds the load unit
-// for 61 clocks).  Tiles run over experts, then blocks of weight rows, then tokens, so
+// no multiple of 256 (!TILED) tokens' are loaded by threads (128 rows hold the load unit
+// for 256 clocks) and weights' come as scale_group has it.  Tiles run over experts, then blocks of weight rows, then tokens, so
 // that neighbouring pairs share weights in L2; a pair takes every one that is a
 // multiple of the pairs on.
 //
@@ -323,7 +331,7 @@ __device__ __forceinline__ unsigned long long silu2(unsigned long long g) {
 // the other fills.  Everything that one thread issues is issued by the elected lane
 // of a warp that stays together: from a branch of one lane an MMA or a copy takes
 // three times as long.
-template <bool GLU, bool GATHER>
+template <bool GLU, bool GATHER, bool TILED>
 __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __grid_constant__ Experts4 a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Bars bars;
@@ -344,7 +352,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   // in a slot: weights (gate, up), tokens, the weights' scales, the tokens'.  Scales are put in
   // order where they have come to: a warp's threads write what they have read.
   constexpr int kMats = GLU ? 2 : 1, off_b = kMats * kACodes;
-  const int off_sfa = off_b + slot_b, off_sfb = off_sfa + kMats * kSfABytes, slot_bytes = off_sfb + chunks * 512 * kSteps;
+  const int w_group = TILED ? 1 : a.w_group, sfa = weight_scales_bytes(w_group);
+  const int off_sfa = off_b + slot_b, off_sfb = off_sfa + kMats * sfa, slot_bytes = off_sfb + chunks * 512 * kSteps;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
   auto first = [&](uint64_t& b) { return mapa(smem_u32(&b), 0); };  // the pair's first block's
 
@@ -352,20 +361,20 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     prefetch_tensormap(&a.w_map);
     if (GLU) prefetch_tensormap(&a.up_map);
     if (!GATHER) prefetch_tensormap(a.nt >= 128 ? &a.x_map : &a.x16_map);
-    if (a.tiled) {
+    if (w_group > 0) {
       prefetch_tensormap(&a.ws_map);
       if (GLU) prefetch_tensormap(&a.us_map);
-      if (!GATHER) prefetch_tensormap(&a.xs_map);
     }
+    if (!GATHER && TILED) prefetch_tensormap(&a.xs_map);
   }
   if (tid == 32) {
     abort = 0, never = 0;
     for (int i = 0; i < a.stages; ++i)
-      mbar_init(bar(bars.full[i]), (GATHER ? 1 : 2) + 2), mbar_init(bar(bars.rfull[i]), GATHER ? 1 : 2), mbar_init(bar(bars.empty[i]), 1);
+      mbar_init(bar(bars.full[i]), (GATHER ? 1 : 2) + 2), mbar_init(bar(bars.rfull[i]), 1 + (!GATHER && TILED)), mbar_init(bar(bars.empty[i]), 1);
     for (int i = 0; i < 2; ++i)
       mbar_init(bar(bars.accf[i]), 1), mbar_init(bar(bars.acce[i]), 2 * kEpiWarps), mbar_init(bar(bars.over[i]), 2 * kEpiWarps);
     for (int i = 0; i < kTiles; ++i)
-      mbar_init(bar(bars.tfull[i]), 1), mbar_init(bar(bars.tempty[i]), 1 + (!GATHER || a.tiled) + !rank + kScaleWarps + kEpiWarps);
+      mbar_init(bar(bars.tfull[i]), 1), mbar_init(bar(bars.tempty[i]), 1 + (!GATHER || TILED) + !rank + kScaleWarps + kEpiWarps);
     for (int i = 0; i < 2; ++i) mbar_init(bar(bars.qfull[i]), 1), mbar_init(bar(bars.qempty[i]), kScaleWarps);
     mbar_init(bar(bars.done), 1);
     mbar_fence_init();
@@ -485,6 +494,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   } else if (warp == 0 || (!GATHER && warp == 1)) {
     // --- copies of weights (warp 0) and tokens (warp 1) --------------------------
     const bool el = elect_one();
+    const int groups = max(1, w_group), part = sfa / groups;
     int st = 0;
     uint32_t ph = 1;  // (a fresh barrier passes a wait for phase 1)
     bool ok = true;
@@ -493,7 +503,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
       if (!ok) break;
       const Tile& t = tile_ring[i % kTiles];
       const int n = t.n;
-      const int row = warp == 0 ? t.e * a.rows + t.m * 256 + rank * 128 : t.p0 + rank * (n / 2), p0 = t.p0;
+      const int row = warp == 0 ? t.e * a.rows + t.m * 256 + rank * 128 : t.p0 + rank * (n / 2), p0 = t.p0, row_group = row / groups;
       for (int s = 0; s < kst; ++s) {
         ok = wait(bars.empty[st], ph);
         if (!ok) break;
@@ -501,15 +511,20 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
           const uint32_t dst = ring + st * slot_bytes, b = first(bars.full[st]);
           const int x = s * (kStageK / 2);
           // (scales first: they are put in order while the codes are on their way)
-          if (a.tiled) {
-            const uint32_t r = bar(bars.rfull[st]);
-            const int xs = s * (kStageK / 16);
-            mbar_arrive_expect_tx(r, warp == 0 ? kMats * kSfABytes : a.nt * (kStageK / 16));
-            if (warp == 1) {
+          const uint32_t r = bar(bars.rfull[st]);
+          const int xs = s * (kStageK / 16);
+          if (warp == 1) {
+            if (TILED) {
+              mbar_arrive_expect_tx(r, a.nt * (kStageK / 16));
               tma_load_2d(dst + off_sfb, &a.xs_map, xs, p0, r);
-            } else {
-              tma_load_2d(dst + off_sfa, &a.ws_map, xs, row, r);
-              if (GLU) tma_load_2d(dst + off_sfa + kSfABytes, &a.us_map, xs, row, r);
+            }
+          } else if (w_group > 0) {
+            mbar_arrive_expect_tx(r, kMats * sfa);
+            for (int u = 0; u < w_group; ++u) {  // the rows that are u of their group
+              const uint32_t to = dst + off_sfa + u * part;
+              const int xu = (u * (a.K / 16) + xs) & ~15;
+              tma_load_2d(to, &a.ws_map, xu, row_group, r);
+              if (GLU) tma_load_2d(to + sfa, &a.us_map, xu, row_group, r);
             }
           }
           if (rank == 0) mbar_arrive_expect_tx(bar(bars.full[st]), warp == 0 ? 2 * kMats * kACodes : n * (kStageK / 2));
@@ -531,7 +546,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     // --- gathered tokens' scales, four stages at a time -----------------------------
     // (four lanes have 64 bytes of a row: a load of 16 bytes each of 32 rows would
     // hold the load unit four times as long)
-    if (a.tiled) {
+    if (TILED) {
       const int pitch = a.K / 16, piece = lane & 3;
       int quad = 0;
       bool ok = true;
@@ -585,7 +600,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
             const uint32_t ta = tmem + kSf, tb = ta + 4 * kMats * kSteps;
             auto step = [&](int k, bool two) {
               pair_cp_sf(ta + 4 * k, fa + 32 * k);
-              if (GLU) pair_cp_sf(ta + 4 * kSteps + 4 * k, fa + (kSfABytes >> 4) + 32 * k);
+              if (GLU) pair_cp_sf(ta + 4 * kSteps + 4 * k, fa + (sfa >> 4) + 32 * k);
               pair_cp_sf(tb + (GLU ? 4 : 8) * k, fb + (two ? 64 : 32) * k);
               if (two && n > 128) pair_cp_sf(tb + 8 * k + 4, fb + 64 * k + 32);
               pair_mma(acc, ad + 2 * k, bd + 2 * k, idesc, ta + 4 * k, tb + (GLU ? 4 : 8) * k, s > 0 || k > 0);
@@ -619,46 +634,54 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     }
   } else if (warp >= kScaleWarp0 && warp < kEpiWarp0) {
     // --- scales, and gathered tokens ----------------------------------------------
-    // Of four stages each of these warps takes one, so that four are under way: a stage takes some 700 clocks from its first wait to its hand-over, 1300
-    // where tokens are gathered.  A thread has every 8th row and token of a block's
-    // 128, of which four make the 16 bytes that follow each other.
+    // Of four stages each of these warps takes one, so that four are under way: a stage
+    // takes some 700 clocks from its first wait to its hand-over, 1300 where tokens are
+    // gathered.  A lane has every 8th row and token of a block's 128, of which four make 16
+    // bytes that follow each other in order: all steps of four or, where scales have come
+    // by threads' loads or 32 bytes of a row, one step of 16.
     constexpr int kOf = 3;  // rows' scales of a stage, 128 each: weights (gate), tokens or up, tokens
+    constexpr int kTok = GLU ? 2 : 1, kChunks = GLU || GATHER ? 1 : 2;
     const int sw = warp - kScaleWarp0, r8 = lane & 7, r4 = lane >> 3;
     const int pitch = a.K / 16;
-    uint4 w[kOf][4];
-    // what a row's scales of stage s are where they do not come by copies
-    auto load = [&](const uint8_t* p, int s) {
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + 4 * s;
-      const int left = a.K / 64 - 4 * s;
-      uint4 v = make_uint4(__ldg(q), 0, 0, 0);
-      if (left > 1) v.y = __ldg(q + 1);
-      if (left > 2) v.z = __ldg(q + 2);
-      if (left > 3) v.w = __ldg(q + 3);
-      return v;
-    };
+    // at [q][j]: of row 32 r4 + 8 q + r8 step j's where TILED, else of row 32 j + 8 q + r8 step r4's
+    uint32_t w[kOf][4][4];
+    auto put = [&](uint32_t (&v)[4], uint4 u) { v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w; };
+    // Scales that do not come by copies: eight rows' 16 bytes at a time (what holds the load
+    // unit is rows, two clocks each, whatever it takes of them).
     auto fetch = [&](int i, int s) {
-      if (a.tiled) return;
-      const Tile& t = tile_ring[i % kTiles];
+      const int at = 16 * s + 4 * r4;
+      const bool in = at < pitch;
+      auto word = [](const uint8_t* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); };
+      if (w_group == 0) {
+        const Tile& t = tile_ring[i % kTiles];
+        const int row0 = t.m * 256 + rank * 128 + r8;
+        const long long from = ((long long)t.e * a.rows + row0) * pitch + at;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = 32 * r4 + 8 * q + r8;
-        const int wr = t.m * 256 + rank * 128 + row;  // the row of the matrix
-        const long long at = ((long long)t.e * a.rows + wr) * pitch;
-        w[0][q] = make_uint4(0, 0, 0, 0);
-        if (GLU) w[1][q] = w[0][q];
-        if (wr < a.rows) {
-          w[0][q] = load(a.w_scales + at, s);
-          if (GLU) w[1][q] = load(a.up_scales + at, s);
-        }
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int c = 0; c < (GLU || GATHER ? 1 : 2); ++c) {
-          const int src = source_ring[i % kTiles][row + 128 * c];
-          uint4& v = w[(GLU ? 2 : 1) + c][q];
-          v = make_uint4(0, 0, 0, 0);
-          if (src >= 0) v = load(a.x_scales + (long long)src * pitch, s);
-        }
+          for (int j = 0; j < 4; ++j) {
+            const int row = 32 * j + 8 * q;
+            const bool have = in && row0 + row < a.rows;
+            w[0][q][j] = have ? word(a.w_scales + from + row * pitch) : 0;
+            if (GLU) w[1][q][j] = have ? word(a.up_scales + from + row * pitch) : 0;
+          }
+      }
+      if (!TILED) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              const int src = source_ring[i % kTiles][128 * c + 32 * j + 8 * q + r8];
+              w[kTok + c][q][j] = in && src >= 0 ? word(a.x_scales + (long long)src * pitch + at) : 0;
+            }
       }
     };
+    // Where the copies put this lane's of weights' rows, and how far on the next eight rows are.
+    const int group = max(w_group, 1), u = r8 & (group - 1);
+    const int w_at = off_sfa + u * (sfa / group) + r8 / group * 32 + ((u * pitch) & 15) + 4 * r4;
+    const int w_next = group == 4 ? 64 : 128;
     // Of stages s0 .. s0 + 3 of tile i this warp's is s (there may be none), every
     // fourth of all tiles' (no more apart than there are slots: a slot's barrier would
     // be mistaken for its next but one use); st: the slot it goes to.
@@ -689,46 +712,67 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
           }
         }
       }
-      if (GATHER && a.tiled) {
+      if (GATHER && TILED) {
         ok = wait(bars.qfull[quad & 1], (quad >> 1) & 1);
         if (!ok) break;
         if (s < kst) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int row = 32 * r4 + 8 * q + r8;
-            w[GLU ? 2 : 1][q] = lds128(ring + kRing - kQuads + (quad & 1) * kQuadBytes + row * 64 + (((s - s0) ^ ((row >> 1) & 3)) << 4));
+            put(w[kTok][q], lds128(ring + kRing - kQuads + (quad & 1) * kQuadBytes + row * 64 + (((s - s0) ^ ((row >> 1) & 3)) << 4)));
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bars.qempty[quad & 1]));
       }
       if (s < kst) {
-        if (a.tiled) {
+        if (w_group > 0) {
           ok = wait(bars.rfull[st], ph ^ 1);
           if (!ok) break;
+          if (TILED) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t at = slot + 16 * (32 * r4 + 8 * q + r8);
-            w[0][q] = lds128(at + off_sfa);
-            if (GLU) w[1][q] = lds128(at + off_sfa + kSfABytes);
-            if (!GATHER) {
-              w[GLU ? 2 : 1][q] = lds128(at + off_sfb);
-              if (!GLU && chunks == 2) w[2][q] = lds128(at + off_sfb + 2048);
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t at = slot + 16 * (32 * r4 + 8 * q + r8);
+              put(w[0][q], lds128(at + off_sfa));
+              if (GLU) put(w[1][q], lds128(at + off_sfa + sfa));
+              if (!GATHER) {
+                put(w[kTok][q], lds128(at + off_sfb));
+                if (!GLU && chunks == 2) put(w[2][q], lds128(at + off_sfb + 2048));
+              }
             }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t at = slot + w_at + (4 * j + q) * w_next;
+                w[0][q][j] = lds32(at);
+                if (GLU) w[1][q][j] = lds32(at + sfa);
+              }
           }
           __syncwarp();  // (they are put in order where they have come to)
         }
+        // (chunk c of step k at 512 (chunks k + c))
+        if (TILED) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          // (chunk c of step k at 512 (chunks k + c))
-          const uint32_t to = slot + 16 * (8 * q + r8) + 4 * r4;
-          put_scales(to + off_sfa, 512, w[0][q]);
-          if (GLU) {
-            put_scales(to + off_sfa + kSfABytes, 512, w[1][q]);
-            put_scales(to + off_sfb, 512, w[2][q]);
-          } else {
-            put_scales(to + off_sfb, 512 * chunks, w[1][q]);
-            if (chunks == 2) put_scales(to + off_sfb + 512, 1024, w[2][q]);
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t to = slot + 16 * (8 * q + r8) + 4 * r4;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+              sts32(to + off_sfa + 512 * k, w[0][q][k]);
+              if (GLU) sts32(to + off_sfa + sfa + 512 * k, w[1][q][k]);
+              sts32(to + off_sfb + 512 * (GLU ? 1 : chunks) * k, w[kTok][q][k]);
+              if (!GLU && chunks == 2) sts32(to + off_sfb + 512 + 1024 * k, w[2][q][k]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t to = slot + 16 * (8 * q + r8), to_b = to + off_sfb + 512 * (GLU ? 1 : chunks) * r4;
+            sts128(to + off_sfa + 512 * r4, w[0][q]);
+            if (GLU) sts128(to + off_sfa + sfa + 512 * r4, w[1][q]);
+            sts128(to_b, w[kTok][q]);
+            if (!GLU && chunks == 2) sts128(to_b + 512, w[2][q]);
           }
         }
         // what this warp's threads have written is seen by the tensor cores
@@ -848,30 +892,30 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
 }
 
 // Clusters of two that run at a time, looked up once a device.
-template <bool GLU, bool GATHER>
+template <bool GLU, bool GATHER, bool TILED>
 int pairs_at_once() {
   static std::atomic<int> known[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int n = known[dev].load(std::memory_order_acquire);
   if (n == 0) {
-    if (cudaFuncSetAttribute(experts4_kernel<GLU, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return 0;
+    if (cudaFuncSetAttribute(experts4_kernel<GLU, GATHER, TILED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return 0;
     const OpsLaunch l(dim3(2), kProductThreads, kSmem, nullptr, 2);
     cudaLaunchConfig_t cfg = l.cfg;
     cudaLaunchAttribute at = l.at[1];
     cfg.attrs = &at, cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, experts4_kernel<GLU, GATHER>, &cfg) != cudaSuccess || n < 1) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, experts4_kernel<GLU, GATHER, TILED>, &cfg) != cudaSuccess || n < 1) return 0;
     known[dev].store(n, std::memory_order_release);
   }
   return n;
 }
 
-template <bool GLU, bool GATHER>
+template <bool GLU, bool GATHER, bool TILED>
 cudaError_t launch_products(const Experts4& a, long long tiles, cudaStream_t st) {
-  const int pairs = pairs_at_once<GLU, GATHER>();
+  const int pairs = pairs_at_once<GLU, GATHER, TILED>();
   if (pairs == 0) return cudaErrorInvalidConfiguration;
   const OpsLaunch l(dim3(2 * (unsigned)std::min<long long>(pairs, tiles)), kProductThreads, kSmem, st, 2);
-  return cudaLaunchKernelEx(&l.cfg, experts4_kernel<GLU, GATHER>, a);
+  return cudaLaunchKernelEx(&l.cfg, experts4_kernel<GLU, GATHER, TILED>, a);
 }
 
 msk_status check_experts(const msk_fp4_experts* w) {
@@ -885,25 +929,37 @@ msk_status check_experts(const msk_fp4_experts* w) {
 struct WeightMaps {
   CUtensorMap codes, scales;
   const uint8_t *packed, *scale_codes;
-  int64_t experts, rows, cols, tiled;
+  int64_t experts, rows, cols, group;
 };
 static_assert(sizeof(WeightMaps) <= MSK_FP4_MAPS_BYTES && alignof(WeightMaps) <= 128, "msk.h");
 
-bool tiled_scales(int64_t cols) { return cols % kStageK == 0; }  // (a tiled copy's rows lie a multiple of 16 bytes apart)
+// A tiled copy's rows lie a multiple of 16 bytes apart, so scales' one, two or four rows
+// (of one expert) are one of a map, and a copy takes 32 bytes of each one's first, its
+// second ..: a stage's 16 from a multiple of 4 on.  Loaded by threads, which is left for
+// rows that are no such multiple, they hold the load unit for 256 clocks a stage and
+// matrix: 32768 rows of 8 experts, gate and up of 1024 x 3968, 161 us, by copies 136 (of 4096
+// columns 108); 16384 of 256, 2048 x 1088, 75 and 65.
+int scale_group(const msk_fp4_experts* w) {
+  const int group = w->cols % 256 == 0 ? 1 : w->cols % 128 == 0 ? 2 : 4;
+  return w->rows % group == 0 ? group : 0;
+}
 
 // Rows of codes in boxes of `box` x 128 bytes, of scales in boxes of `box` x 16.
 bool codes_map(CUtensorMap* m, const uint8_t* p, long long rows, long long cols, int box) {
   return matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, rows, cols / 2, cols / 2, box, kStageK / 2, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-bool scales_map(CUtensorMap* m, const uint8_t* p, long long rows, long long cols, int box) {
-  return matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, rows, cols / 16, cols / 16, box, kStageK / 16, CU_TENSOR_MAP_SWIZZLE_NONE);
+bool scales_map(CUtensorMap* m, const uint8_t* p, long long rows, long long cols, int box, int group) {
+  const long long bytes = cols / 16 * group;
+  return matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, rows / group, bytes, bytes, box / group, group > 1 ? 32 : kStageK / 16,
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 bool make_maps(const msk_fp4_experts* w, WeightMaps* m) {
   const long long rows = (long long)w->n_experts * w->rows;
   m->packed = w->packed, m->scale_codes = w->scales, m->experts = w->n_experts, m->rows = w->rows, m->cols = w->cols;
-  m->tiled = tiled_scales(w->cols);
-  return codes_map(&m->codes, w->packed, rows, w->cols, kM) && (!m->tiled || scales_map(&m->scales, w->scales, rows, w->cols, kM));
+  m->group = scale_group(w);
+  return codes_map(&m->codes, w->packed, rows, w->cols, kM) &&
+         (m->group == 0 || scales_map(&m->scales, w->scales, rows, w->cols, kM, (int)m->group));
 }
 
 // The weights' maps, the caller's or new ones.
@@ -917,7 +973,7 @@ msk_status weight_maps(const msk_fp4_experts* w, CUtensorMap* codes, CUtensorMap
     return MSK_ERR_INVALID_ARG;
   }
   *codes = m->codes;
-  if (m->tiled) *scales = m->scales;
+  if (m->group > 0) *scales = m->scales;
   return MSK_OK;
 }
 
@@ -995,18 +1051,23 @@ extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* sl
   const long long tiles = (long long)a.mblocks * ((n + a.nt - 1) / a.nt + std::min<int64_t>(n, a.E));  // at most
   if (tiles > (1ll << 31) - 1 - 65536) return MSK_ERR_SHAPE;
   const int mats = up != nullptr ? 2 : 1;
-  const int slot = mats * (kACodes + kSfABytes) + a.nt / 2 * (kStageK / 2) + (a.nt > 128 ? 2 : 1) * 512 * kSteps;
-  a.stages = std::min(kMaxStages, (kRing - (slots != nullptr ? kQuads : 0)) / slot);  // (4 at least)
-  a.tiled = tiled_scales(a.K);
+  a.w_group = scale_group(w);
+  const bool tiled = a.w_group == 1;
+  const int slot = mats * (kACodes + weight_scales_bytes(a.w_group)) + a.nt / 2 * (kStageK / 2) + (a.nt > 128 ? 2 : 1) * 512 * kSteps;
+  a.stages = std::min(kMaxStages, (kRing - (slots != nullptr && tiled ? kQuads : 0)) / slot);  // (4 at least)
   s = weight_maps(w, &a.w_map, &a.ws_map);
   if (s == MSK_OK && up != nullptr) s = weight_maps(up, &a.up_map, &a.us_map);
   if (s != MSK_OK) return s;
   if (slots == nullptr && ((a.nt >= 128 && !codes_map(&a.x_map, x->packed, x->rows, a.K, 64)) ||
                            !codes_map(&a.x16_map, x->packed, x->rows, a.K, 16) ||
-                           (a.tiled && !scales_map(&a.xs_map, x->scales, x->rows, a.K, a.nt))))
+                           (tiled && !scales_map(&a.xs_map, x->scales, x->rows, a.K, a.nt, 1))))
     return MSK_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = up != nullptr ? (slots != nullptr ? launch_products<true, true>(a, tiles, st) : launch_products<true, false>(a, tiles, st))
-                                      : (slots != nullptr ? launch_products<false, true>(a, tiles, st) : launch_products<false, false>(a, tiles, st));
+  const auto launch = [&](auto t) {
+    constexpr bool kTiled = decltype(t)::value;
+    if (up != nullptr) return slots != nullptr ? launch_products<true, true, kTiled>(a, tiles, st) : launch_products<true, false, kTiled>(a, tiles, st);
+    return slots != nullptr ? launch_products<false, true, kTiled>(a, tiles, st) : launch_products<false, false, kTiled>(a, tiles, st);
+  };
+  const cudaError_t e = tiled ? launch(std::true_type()) : launch(std::false_type());
   return e == cudaSuccess ? MSK_OK : MSK_ERR_CUDA;
 }

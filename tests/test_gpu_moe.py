@@ -302,6 +302,14 @@ def test_products_of_many_tiles(M, counts, rows, cols, glu, gather):
     run_products(M, counts, rows, cols, glu, gather)
 
 
+@pytest.mark.parametrize("rows", [256, 300, 302, 301, 4, 2])
+@pytest.mark.parametrize("cols", [64, 128, 1984, 2880, 4032])
+@pytest.mark.parametrize("glu,gather", [(False, False), (True, False), (False, True), (True, True)])
+def test_products_of_columns_that_end_inside_a_stage(M, rows, cols, glu, gather):
+    """Weights' scales by copies of two and four rows as one, and by loads; more stages than the ring has."""
+    run_products(M, [5, 0, 130, 261], rows, cols, glu, gather)
+
+
 @pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("glu", [False, True])
 def test_products_types_and_strides(M, out, glu):
