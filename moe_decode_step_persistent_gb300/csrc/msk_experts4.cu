@@ -152,7 +152,7 @@ constexpr int kM = 128;            // weight rows of a block (a pair's MMA has M
 constexpr int kStageK = 256;       // columns of a stage
 constexpr int kSteps = kStageK / 64;  // MMAs of a stage
 constexpr int kMaxN = 256;         // tokens of a tile at most (the MMA's N); half of it where a tile has gate and up
-constexpr int kStepN = 32;         // ... and what they are filled up to: each block has half of them, in boxes of 16
+constexpr int kStepN = 32;         // ... and what they are filled up to: each block has half of them
 constexpr int kMaxStages = 10;
 constexpr int kMaxE = 1024;
 constexpr int kScaleWarps = 4, kEpiWarps = 8;
@@ -180,9 +180,9 @@ static __device__ uint32_t g_error;  // nonzero once a wait has run out
 
 struct Experts4 {
   CUtensorMap w_map, up_map;     // [E rows][cols / 2] bytes, boxes of 128 x 128
-  CUtensorMap x_map, x16_map;    // [x_rows][cols / 2] bytes, boxes of 64 x 128, of 16 x 128
+  CUtensorMap x_map, x16_map, x8_map;  // [x_rows][cols / 2] bytes, boxes of 64 x 128, of 16 x 128, of 8 x 128
   CUtensorMap ws_map, us_map;    // scales: [E rows / w_group][w_group cols / 16] bytes, boxes of 128 rows
-  CUtensorMap xs_map;            // [x_rows][cols / 16], boxes of nt x 16
+  CUtensorMap xs_map, xs32_map, xs8_map;  // [x_rows][cols / 16], boxes of nt x 16, of 32 x 16, of 8 x 16
   const uint8_t *x_codes, *x_scales, *w_scales, *up_scales;
   const float *w_ts, *up_ts;
   const int32_t *offsets, *slots;
@@ -360,12 +360,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&a.w_map);
     if (GLU) prefetch_tensormap(&a.up_map);
-    if (!GATHER) prefetch_tensormap(a.nt >= 128 ? &a.x_map : &a.x16_map);
+    if (!GATHER) prefetch_tensormap(&a.x8_map);
     if (w_group > 0) {
       prefetch_tensormap(&a.ws_map);
       if (GLU) prefetch_tensormap(&a.us_map);
     }
-    if (!GATHER && TILED) prefetch_tensormap(&a.xs_map);
+    if (!GATHER && TILED) prefetch_tensormap(&a.xs8_map);
   }
   if (tid == 32) {
     abort = 0, never = 0;
@@ -502,7 +502,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
       ok = wait_tile(i);
       if (!ok) break;
       const Tile& t = tile_ring[i % kTiles];
-      const int n = t.n;
+      const int n = t.n, count = t.count;
+      // Tokens that each block copies.  Rows behind a tile's are others' tokens, which no
+      // one needs here, and where experts have few all pairs would read the same few lines: 512
+      // rows of 256 experts, 2048 x 1024, 62 us, in copies of no more than these 43.
+      const int few = (count + 7) & ~7, in_first = min(few, n / 2), copied = rank == 0 ? in_first : few - in_first;
+      const int with_scales = few <= 8 ? 8 : few <= 64 ? (few + 31) & ~31 : a.nt;  // (a copy more takes 40 clocks a stage)
       const int row = warp == 0 ? t.e * a.rows + t.m * 256 + rank * 128 : t.p0 + rank * (n / 2), p0 = t.p0, row_group = row / groups;
       for (int s = 0; s < kst; ++s) {
         ok = wait(bars.empty[st], ph);
@@ -515,8 +520,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
           const int xs = s * (kStageK / 16);
           if (warp == 1) {
             if (TILED) {
-              mbar_arrive_expect_tx(r, a.nt * (kStageK / 16));
-              tma_load_2d(dst + off_sfb, &a.xs_map, xs, p0, r);
+              mbar_arrive_expect_tx(r, with_scales * (kStageK / 16));
+              tma_load_2d(dst + off_sfb, few <= 8 ? &a.xs8_map : few <= 64 ? &a.xs32_map : &a.xs_map, xs, p0, r);
+              if (with_scales == 64) tma_load_2d(dst + off_sfb + 32 * (kStageK / 16), &a.xs32_map, xs, p0 + 32, r);
             }
           } else if (w_group > 0) {
             mbar_arrive_expect_tx(r, kMats * sfa);
@@ -527,11 +533,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
               if (GLU) tma_load_2d(to + sfa, &a.us_map, xu, row_group, r);
             }
           }
-          if (rank == 0) mbar_arrive_expect_tx(bar(bars.full[st]), warp == 0 ? 2 * kMats * kACodes : n * (kStageK / 2));
+          if (rank == 0) mbar_arrive_expect_tx(bar(bars.full[st]), warp == 0 ? 2 * kMats * kACodes : few * (kStageK / 2));
           if (warp == 1) {
             int j = 0;
-            for (; j + 64 <= n / 2; j += 64) pair_load_2d(dst + off_b + j * 128, &a.x_map, x, row + j, b);
-            for (; j < n / 2; j += 16) pair_load_2d(dst + off_b + j * 128, &a.x16_map, x, row + j, b);
+            for (; j + 64 <= copied; j += 64) pair_load_2d(dst + off_b + j * 128, &a.x_map, x, row + j, b);
+            for (; j + 16 <= copied; j += 16) pair_load_2d(dst + off_b + j * 128, &a.x16_map, x, row + j, b);
+            if (j < copied) pair_load_2d(dst + off_b + j * 128, &a.x8_map, x, row + j, b);
           } else {
             pair_load_2d(dst, &a.w_map, x, row, b);
             if (GLU) pair_load_2d(dst + kACodes, &a.up_map, x, row, b);
@@ -1044,23 +1051,29 @@ extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* sl
   a.n = (int)n, a.E = w->n_experts, a.rows = (int)w->rows, a.K = (int)w->cols, a.top_k = top_k, a.y_dtype = y_dtype;
   a.x_ts = x->tensor_scale;
   a.mblocks = (a.rows + 255) / 256;
-  // (128 tokens leave a deeper ring: 16384 rows of 256 experts, 2048 x 1024, 68.9 us, with
-  // 256 73.7; where experts have more, weights are loaded less often: 65536 rows 105, with 128 116)
-  const bool half = up != nullptr || slots != nullptr || n <= 128ll * w->n_experts;
-  a.nt = (int)std::min<int64_t>(half ? kMaxN / 2 : kMaxN, (n + kStepN - 1) / kStepN * kStepN);
-  const long long tiles = (long long)a.mblocks * ((n + a.nt - 1) / a.nt + std::min<int64_t>(n, a.E));  // at most
-  if (tiles > (1ll << 31) - 1 - 65536) return MSK_ERR_SHAPE;
-  const int mats = up != nullptr ? 2 : 1;
   a.w_group = scale_group(w);
   const bool tiled = a.w_group == 1;
+  const auto tiles_of = [&](int nt) { return a.mblocks * ((n + std::min<int64_t>(n, a.E) * (nt - 1)) / nt); };  // at most
+  // Tiles of 256 tokens load weights less often: 32768 rows of 256 experts, 2048 x 1024, 73 us,
+  // of 128 75, 65536 104 and 116; fewer rows no worse.  Of 128: where all tiles run at once (256 x
+  // 6144 x 4096 9.5 us, of 256 11.4), where threads load scales and experts have no more on
+  // average (16384 rows of 256, 2048 x 1088, 65.6 and 70), and where gate and up or gathered
+  // tokens' scales need the room.
+  const bool half = up != nullptr || slots != nullptr || tiles_of(kMaxN / 2) <= nsm / 2 || (!tiled && n <= 128ll * w->n_experts);
+  a.nt = (int)std::min<int64_t>(half ? kMaxN / 2 : kMaxN, (n + kStepN - 1) / kStepN * kStepN);
+  const long long tiles = tiles_of(a.nt);
+  if (tiles > (1ll << 31) - 1 - 65536) return MSK_ERR_SHAPE;
+  const int mats = up != nullptr ? 2 : 1;
   const int slot = mats * (kACodes + weight_scales_bytes(a.w_group)) + a.nt / 2 * (kStageK / 2) + (a.nt > 128 ? 2 : 1) * 512 * kSteps;
   a.stages = std::min(kMaxStages, (kRing - (slots != nullptr && tiled ? kQuads : 0)) / slot);  // (4 at least)
   s = weight_maps(w, &a.w_map, &a.ws_map);
   if (s == MSK_OK && up != nullptr) s = weight_maps(up, &a.up_map, &a.us_map);
   if (s != MSK_OK) return s;
   if (slots == nullptr && ((a.nt >= 128 && !codes_map(&a.x_map, x->packed, x->rows, a.K, 64)) ||
-                           !codes_map(&a.x16_map, x->packed, x->rows, a.K, 16) ||
-                           (tiled && !scales_map(&a.xs_map, x->scales, x->rows, a.K, a.nt, 1))))
+                           !codes_map(&a.x16_map, x->packed, x->rows, a.K, 16) || !codes_map(&a.x8_map, x->packed, x->rows, a.K, 8) ||
+                           (tiled && (!scales_map(&a.xs_map, x->scales, x->rows, a.K, a.nt, 1) ||
+                                      !scales_map(&a.xs32_map, x->scales, x->rows, a.K, 32, 1) ||
+                                      !scales_map(&a.xs8_map, x->scales, x->rows, a.K, 8, 1)))))
     return MSK_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const auto launch = [&](auto t) {
