@@ -1069,11 +1069,12 @@ extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* sl
   s = weight_maps(w, &a.w_map, &a.ws_map);
   if (s == MSK_OK && up != nullptr) s = weight_maps(up, &a.up_map, &a.us_map);
   if (s != MSK_OK) return s;
-  if (slots == nullptr && ((a.nt >= 128 && !codes_map(&a.x_map, x->packed, x->rows, a.K, 64)) ||
-                           !codes_map(&a.x16_map, x->packed, x->rows, a.K, 16) || !codes_map(&a.x8_map, x->packed, x->rows, a.K, 8) ||
-                           (tiled && (!scales_map(&a.xs_map, x->scales, x->rows, a.K, a.nt, 1) ||
-                                      !scales_map(&a.xs32_map, x->scales, x->rows, a.K, 32, 1) ||
-                                      !scales_map(&a.xs8_map, x->scales, x->rows, a.K, 8, 1)))))
+  // (a map takes the host 0.3 us: only those that some tile may take)
+  const auto codes_by = [&](CUtensorMap* m, int box, bool taken) { return !taken || codes_map(m, x->packed, x->rows, a.K, box); };
+  const auto scales_by = [&](CUtensorMap* m, int box, bool taken) { return !taken || scales_map(m, x->scales, x->rows, a.K, box, 1); };
+  if (slots == nullptr && (!codes_by(&a.x_map, 64, a.nt >= 128) || !codes_by(&a.x16_map, 16, n > 8) || !codes_by(&a.x8_map, 8, true) ||
+                           !scales_by(&a.xs_map, a.nt, tiled && a.nt > 64) || !scales_by(&a.xs32_map, 32, tiled && n > 8) ||
+                           !scales_by(&a.xs8_map, 8, tiled)))
     return MSK_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const auto launch = [&](auto t) {
