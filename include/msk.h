@@ -547,6 +547,13 @@ msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* slots, int32_
                            const int32_t* offsets, const msk_fp4_experts* w, const msk_fp4_experts* up, void* y,
                            int32_t y_dtype, int64_t y_stride, void* stream);
 
+/* Test hook (not needed in production), for the calls of msk_experts_fp4 that follow in
+ * this process: of tile number `tile` of each pair of blocks (0 its first; -1: of none)
+ * nobody is told that its sums are complete, and waits are bounded by wait_ns (up to 200
+ * ms; 0: these) and the time for each step.  Used to check that a signal which stays away
+ * ends in MSK_ERR_TIMEOUT from msk_ops_check; what such calls write is not to be used. */
+msk_status msk_debug_experts_fault(int32_t tile, uint64_t wait_ns);
+
 /* out[t] = sum over ranks r of gates[t][r] * y[places[t][r]], in order of rank, in
  * fp32, rounded once.
  *   y     : [y_rows][cols] of y_dtype, y_stride elements between rows;

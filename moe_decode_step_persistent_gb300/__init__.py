@@ -96,6 +96,7 @@ SYMBOLS = ["msk_create", "msk_load_layer", "msk_layer_step", "msk_decode_step", 
            "msk_attention_noalloc", "msk_kv4_write", "msk_kv4_read", "msk_attention_kv4_workspace",
            "msk_attention_kv4", "msk_linear_fp4", "msk_ops_check", "msk_token_logprobs",
            "msk_moe_route", "msk_moe_sort", "msk_quantize_fp4", "msk_dequantize_fp4", "msk_fp4_experts_maps", "msk_experts_fp4",
+           "msk_debug_experts_fault",
            "msk_moe_combine", "msk_get_info", "msk_status_string", "msk_destroy"]
 
 _lib = None
@@ -148,6 +149,7 @@ def load_library(path: str = LIB_PATH):
     L.msk_dequantize_fp4.argtypes = [vp, vp, f32, i64, i64, vp, i32, i64, vp]
     L.msk_fp4_experts_maps.argtypes = [experts, vp]
     L.msk_experts_fp4.argtypes = [fp4, vp, i32, i64, vp, experts, experts, vp, i32, i64, vp]
+    L.msk_debug_experts_fault.argtypes = [i32, u64]
     L.msk_moe_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i32, i64, vp, i32, i64, vp]
     L.msk_get_info.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(i64)]
     L.msk_status_string.argtypes = [i32]
@@ -688,6 +690,13 @@ def msk_experts_fp4(x, experts, offsets, up=None, slots=None, top_k=1, out_dtype
     _check(load_library().msk_experts_fp4(x_desc, slot_ptr, top_k, n, ptr, experts.desc, up_desc, out.data_ptr(),
                                           _DTYPES[out.dtype], step, st), "msk_experts_fp4")
     return out
+
+
+def msk_debug_experts_fault(tile=-1, wait_ns=0):
+    """For tests: later calls of msk_experts_fp4 never say that a pair of
+    blocks' tile number `tile` is complete, and wait for wait_ns at most; the
+    defaults put an end to both (see include/msk.h)."""
+    _check(load_library().msk_debug_experts_fault(_int32(tile, "tile"), int(wait_ns)), "msk_debug_experts_fault")
 
 
 def msk_moe_combine(y, places, gates=None, out_dtype=None, out=None, stream=None):

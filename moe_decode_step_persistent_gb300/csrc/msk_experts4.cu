@@ -191,6 +191,8 @@ struct Experts4 {
   int n, E, rows, K, top_k, y_dtype, nt, stages, mblocks;
   float x_ts;
   int w_group;  // weights' scales come by copies of so many rows as one (0: threads load them)
+  int withheld;       // tests: of this one of a pair's tiles nobody says that it is complete (-1: of none)
+  uint64_t wait_ns;   // bound of every wait, beside the time for each step
 };
 
 // A tile: the pair's 256 weight rows of an expert and up to nt of its tokens.
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
   const uint32_t tmem = tmem_base;
   const int mine = team < tiles_all ? (tiles_all - team + teams - 1) / teams : 0;
   const int kst = (a.K + kStageK - 1) / kStageK;  // stages of a tile
-  const uint64_t deadline = gtimer() + kOpsWaitNs + (uint64_t)mine * kst * kOpsStepNs;
+  const uint64_t deadline = gtimer() + a.wait_ns + (uint64_t)mine * kst * kOpsStepNs;
   const volatile int* ab = &abort;
   // Waits by whole warps.
   auto wait = [&](uint64_t& b, uint32_t parity) {
@@ -629,13 +631,13 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
           __syncwarp();
           if (++st == a.stages) st = 0, ph ^= 1;
         }
-        if (ok && el) pair_commit(bar(bars.accf[d]), 3);
+        if (ok && el && i != a.withheld) pair_commit(bar(bars.accf[d]), 3);
         __syncwarp();
       }
       // what is still in flight ends before the block does
       if (el) {
         pair_commit(bar(bars.done), 1);
-        mbar_wait(bar(bars.done), 0, gtimer() + kOpsWaitNs, &never);
+        if (!mbar_wait(bar(bars.done), 0, gtimer() + kOpsWaitNs, &never)) abort = 1;
       }
       __syncwarp();
     }
@@ -799,6 +801,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
       }
       if (ok && i < mine && s < kst) fetch(i, s);
     }
+    if (GATHER) cp_async_wait_all();  // (behind a wait that ran out)
   } else if (warp >= kEpiWarp0) {
     // --- epilogue -------------------------------------------------------------
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
@@ -882,6 +885,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     else run(__nv_bfloat16());
   }
   __syncwarp();
+  __syncthreads();  // (a wait may run out behind the end of the copies)
   if (tid == 0 && *ab) {
     atomicExch(&g_error, 1u);
     // copies end before the block does: a slot's newest may be a use ahead of what was waited for
@@ -984,6 +988,9 @@ msk_status weight_maps(const msk_fp4_experts* w, CUtensorMap* codes, CUtensorMap
   return MSK_OK;
 }
 
+std::atomic<int32_t> g_withheld{-1};
+std::atomic<uint64_t> g_wait_ns{kOpsWaitNs};
+
 }  // namespace
 
 cudaError_t experts4_error(uint32_t* e) {
@@ -1015,6 +1022,13 @@ extern "C" msk_status msk_fp4_experts_maps(const msk_fp4_experts* w, void* maps)
   if (w->packed == nullptr || w->scales == nullptr) return MSK_ERR_INVALID_ARG;
   if (!ops_aligned16(w->packed) || !ops_aligned16(w->scales) || (reinterpret_cast<uintptr_t>(maps) & 127)) return MSK_ERR_ALIGNMENT;
   return make_maps(w, static_cast<WeightMaps*>(maps)) ? MSK_OK : MSK_ERR_CUDA;
+}
+
+extern "C" msk_status msk_debug_experts_fault(int32_t tile, uint64_t wait_ns) {
+  if (tile < -1 || wait_ns > kOpsWaitNs) return MSK_ERR_INVALID_ARG;
+  g_withheld.store(tile, std::memory_order_relaxed);
+  g_wait_ns.store(wait_ns > 0 ? wait_ns : kOpsWaitNs, std::memory_order_relaxed);
+  return MSK_OK;
 }
 
 extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* slots, int32_t top_k, int64_t n,
@@ -1052,6 +1066,7 @@ extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* sl
   a.x_ts = x->tensor_scale;
   a.mblocks = (a.rows + 255) / 256;
   a.w_group = scale_group(w);
+  a.withheld = g_withheld.load(std::memory_order_relaxed), a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   const bool tiled = a.w_group == 1;
   const auto tiles_of = [&](int nt) { return a.mblocks * ((n + std::min<int64_t>(n, a.E) * (nt - 1)) / nt); };  // at most
   // Tiles of 256 tokens load weights less often: 32768 rows of 256 experts, 2048 x 1024, 73 us,

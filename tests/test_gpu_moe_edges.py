@@ -1,0 +1,56 @@
+"""The operators of a whole prompt's experts where test_gpu_moe.py does not go:
+signals that stay away, kernels for many elements, sizes and scales at the ends
+of their ranges.  Tolerances are those of test_gpu_moe.py."""
+
+import pytest
+import torch
+
+from tests.test_gpu_moe import M, gen, make_experts, no_wait_ran_out, random_fp4  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------------------
+# signals that stay away
+# ----------------------------------------------------------------------------
+
+
+def products_of(M, counts, rows, cols, glu, gather, top_k=2):
+    """A call without arguments, of fixed inputs."""
+    n = sum(counts)
+    w, _ = make_experts(M, 31, len(counts), rows, cols)
+    up = make_experts(M, 32, len(counts), rows, cols)[0] if glu else None
+    xr = (n + top_k - 1) // top_k if gather else n
+    c, s = random_fp4(33, xr, cols)
+    x = M.Fp4Weight(c.cuda(), s.cuda())
+    slots = torch.randperm(xr * top_k, generator=gen(34))[:n].int().cuda() if gather else None
+    off = torch.tensor([0] + counts).cumsum(0).int().cuda()
+    return lambda: M.msk_experts_fp4(x, w, off, up=up, slots=slots, top_k=top_k)
+
+
+@pytest.mark.parametrize("counts,rows,cols", [([40], 256, 256), ([5], 40, 64), ([100, 30], 300, 1344), ([256] * 40, 1030, 320)])
+@pytest.mark.parametrize("glu,gather", [(False, False), (True, False), (False, True), (True, True)])
+def test_a_signal_that_stays_away_is_reported(M, counts, rows, cols, glu, gather):
+    """Nobody says that a pair's first tile is complete: the warps that end tiles wait for it
+    in vain, long after the copies' warps have ended where the pair has no other tile.  The
+    check reports it, once, and the next call is sound."""
+    call = products_of(M, counts, rows, cols, glu, gather)
+    want = call()
+    M.msk_ops_check()
+    try:
+        M.msk_debug_experts_fault(0, 2_000_000)
+        call()
+    finally:
+        M.msk_debug_experts_fault()
+    with pytest.raises(M.MskError) as e:
+        M.msk_ops_check()
+    assert e.value.status == M.MSK_ERR_TIMEOUT
+    M.msk_ops_check()
+    assert torch.equal(call(), want)
+    # a tile that no pair has: nothing is missed within the short limit
+    try:
+        M.msk_debug_experts_fault(1 << 20, 50_000_000)
+        assert torch.equal(call(), want)
+    finally:
+        M.msk_debug_experts_fault()
+    M.msk_ops_check()
