@@ -831,6 +831,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
         for (int c = 0; c < nc; ++c) {
           const int c0 = 32 * (half + 2 * (d ? c : nc - 1 - c));
           float v[32], u[32];
+          __syncwarp();  // (lanes behind the last row store nothing and are here first)
           tmem_ld32(at + c0, v);
           if (GLU) tmem_ld32(at + n + c0, u);
           if (c == 0) {

@@ -5,7 +5,7 @@ of their ranges.  Tolerances are those of test_gpu_moe.py."""
 import pytest
 import torch
 
-from tests.test_gpu_moe import M, gen, make_experts, no_wait_ran_out, random_fp4  # noqa: F401
+from tests.test_gpu_moe import M, gen, make_experts, no_wait_ran_out, random_fp4, run_products  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,16 @@ def test_a_signal_that_stays_away_is_reported(M, counts, rows, cols, glu, gather
     finally:
         M.msk_debug_experts_fault()
     M.msk_ops_check()
+
+
+# ----------------------------------------------------------------------------
+# warps of which some lanes store nothing
+# ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("rows", [1, 17, 31, 33, 63, 250, 257, 290])
+@pytest.mark.parametrize("counts", [[256], [250, 3, 128], [255] * 12])
+@pytest.mark.parametrize("glu,gather", [(False, False), (True, True)])
+def test_products_whose_last_rows_are_part_of_a_warp(M, rows, counts, glu, gather):
+    """Lanes behind the last weight row go through all of a tile's chunks of 32 tokens beside those that store."""
+    run_products(M, counts, rows, 192, glu, gather, out="fp32", extra=1)
