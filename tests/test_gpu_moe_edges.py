@@ -2,10 +2,11 @@
 signals that stay away, kernels for many elements, sizes and scales at the ends
 of their ranges.  Tolerances are those of test_gpu_moe.py."""
 
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_moe import M, gen, make_experts, no_wait_ran_out, random_fp4, run_products  # noqa: F401
+from tests.test_gpu_moe import M, gen, make_experts, no_wait_ran_out, random_fp4, run_products, sort_ref_many  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,12 @@ def test_a_signal_that_stays_away_is_reported(M, counts, rows, cols, glu, gather
 def test_products_whose_last_rows_are_part_of_a_warp(M, rows, counts, glu, gather):
     """Lanes behind the last weight row go through all of a tile's chunks of 32 tokens beside those that store."""
     run_products(M, counts, rows, 192, glu, gather, out="fp32", extra=1)
+
+
+@pytest.mark.parametrize("E", [1, 31, 33, 1023])
+@pytest.mark.parametrize("n", [4095, 4097, 32769, 49153, 65537])
+def test_sort_of_experts_that_end_inside_a_warp(M, E, n):
+    """Of the block's threads as many as there are experts read the cluster's counts between its meetings."""
+    e = torch.randint(-1, E + 1, (n,), generator=gen(n + E), dtype=torch.int32)
+    for got, want in zip(M.msk_moe_sort(e.cuda(), E), sort_ref_many(e, E)):
+        assert np.array_equal(got.cpu().numpy(), want)
