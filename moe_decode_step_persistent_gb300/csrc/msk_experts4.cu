@@ -885,22 +885,28 @@ __global__ void __launch_bounds__(kProductThreads, 1) experts4_kernel(const __gr
     else if (a.y_dtype == MSK_FP16) run(__half());
     else run(__nv_bfloat16());
   }
-  __syncwarp();
-  __syncthreads();  // (a wait may run out behind the end of the copies)
-  if (tid == 0 && *ab) {
-    atomicExch(&g_error, 1u);
-    // copies end before the block does: a slot's newest may be a use ahead of what was waited for
-    for (uint32_t q = 0; q < 2; ++q)
-      for (int k = 0; k < a.stages; ++k) {
-        mbar_wait(bar(bars.full[k]), q, gtimer() + kOpsWaitNs / 100, &never);
-        mbar_wait(bar(bars.rfull[k]), q, gtimer() + kOpsWaitNs / 100, &never);
-      }
-  }
-  __syncwarp();
   tc_fence_before();
   cluster_sync();  // (no block leaves while the pair's MMAs, copies or arrivals may come to it)
   tc_fence_after();
-  if (warp == 3) pair_tmem_free(tmem, 512);
+  if (warp == 3) {
+    // Read here, where none of the block's waits can run out any more (a barrier of its threads in
+    // front of the pair's, for this alone, took 0.4 us of a product of one token, 7.5 us).
+    if (*ab) {
+      if (lane == 0) {
+        atomicExch(&g_error, 1u);
+        // copies end before the block does: a slot's newest may be a use ahead of what was waited for
+        // (those of the second block are counted by the first one, so that the second waits for as
+        // long as the limit is; where only the other block gave up, this one's have all been used)
+        for (uint32_t q = 0; q < 2; ++q)
+          for (int k = 0; k < a.stages; ++k) {
+            mbar_wait(bar(bars.full[k]), q, gtimer() + kOpsWaitNs / 100, &never);
+            mbar_wait(bar(bars.rfull[k]), q, gtimer() + kOpsWaitNs / 100, &never);
+          }
+      }
+      __syncwarp();
+    }
+    pair_tmem_free(tmem, 512);
+  }
 }
 
 // Clusters of two that run at a time, looked up once a device.
