@@ -271,16 +271,27 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4]) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
-// Two tensors' scales as a factor and 1 or, where the product might leave fp32's
-// range, as a significand with a half of the power of two and the other half, so that
-// no product with them leaves it unless the result does.
+// v = m 2^e, m's magnitude in [1, 2) (v finite and not 0; a subnormal number is made a
+// normal one first).
+__device__ __forceinline__ float significand(float v, int& e) {
+  e = -127;
+  if (fabsf(v) < 0x1p-126f) v *= 0x1p24f, e -= 24;
+  e += (__float_as_uint(v) >> 23) & 255;
+  return __uint_as_float((__float_as_uint(v) & 0x807FFFFFu) | 0x3F800000u);
+}
+
+// Two tensors' scales as a factor and 1 or, where the product leaves the range of
+// fp32's normal numbers, as a significand with a half of the power of two and the other
+// half, so that no product with them leaves it unless the result does (and the other way
+// round: a subnormal factor would have lost digits that the result has).
 __device__ __forceinline__ float2 scale_factors(float w, float x) {
-  const int ew = (__float_as_uint(w) >> 23) & 255, ex = (__float_as_uint(x) >> 23) & 255;
-  if (ew == 0 || ew == 255 || ex == 0 || ex == 255 || (ew + ex >= 128 && ew + ex <= 380)) return make_float2(w * x, 1.f);
-  const int e2 = max(-250, min(250, ew + ex - 254)), e1 = e2 / 2;
-  const float mw = __uint_as_float((__float_as_uint(w) & 0x807FFFFFu) | 0x3F800000u);
-  const float mx = __uint_as_float((__float_as_uint(x) & 0x807FFFFFu) | 0x3F800000u);
-  return make_float2(mw * mx * exp2i(e1), exp2i(e2 - e1));
+  const float p = w * x;
+  if (fabsf(p) >= 0x1p-126f && fabsf(p) <= 3e38f) return make_float2(p, 1.f);
+  if (w == 0.f || x == 0.f || !(fabsf(w) < INFINITY) || !(fabsf(x) < INFINITY)) return make_float2(p, 1.f);
+  int ew, ex;
+  const float m = significand(w, ew) * significand(x, ex);
+  const int e2 = max(-250, min(250, ew + ex)), e1 = e2 / 2;
+  return make_float2(m * exp2i(e1), exp2i(e2 - e1));
 }
 
 // `bytes` (0 or 16) of 16, zeros for the rest.

@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_moe import M, gen, make_experts, no_wait_ran_out, random_fp4, run_products, sort_ref_many  # noqa: F401
+from tests.test_gpu_moe import (M, gen, make_experts, no_wait_ran_out, products_ref, random_fp4, run_products,  # noqa: F401
+                                sort_ref_many, values64)
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,28 @@ def test_sort_of_experts_that_end_inside_a_warp(M, E, n):
     e = torch.randint(-1, E + 1, (n,), generator=gen(n + E), dtype=torch.int32)
     for got, want in zip(M.msk_moe_sort(e.cuda(), E), sort_ref_many(e, E)):
         assert np.array_equal(got.cpu().numpy(), want)
+
+
+# ----------------------------------------------------------------------------
+# tensors' scales at the ends of their range
+# ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("x_ts,w_ts", [(1e-40, 0.02), (0.02, 1e-40), (3e-45, 5e4), (1e-39, 1e-3), (-1e-41, 0.7), (1e-42, -2e-2)])
+def test_products_of_subnormal_tensor_scales(M, x_ts, w_ts):
+    """The product of the two scales is far below fp32's normal numbers and loses their digits, results are not:
+    block scales of 112 to 448 bring the sums to 1e5."""
+    counts, rows, cols = [5, 40], 70, 64
+    p, s = random_fp4(51, 2, rows, cols)
+    s = 0x7E - s % 16
+    t = torch.tensor([w_ts, w_ts * 0.7])
+    w = M.Fp4Experts(p.cuda(), s.cuda(), t.cuda())
+    wv = values64(p, s) * t.double().view(2, 1, 1)
+    c, xs = random_fp4(53, 45, cols)
+    xs = 0x7E - xs % 16
+    x = M.Fp4Weight(c.cuda(), xs.cuda(), x_ts)
+    off = torch.tensor([0, 5, 45], dtype=torch.int32, device="cuda")
+    y = M.msk_experts_fp4(x, w, off, out_dtype=torch.float32)
+    ref, err = products_ref(values64(c, xs, x_ts), wv, None, counts, torch.arange(45))
+    assert ref.abs().max() > 2.0 ** -126
+    assert ((y.cpu().double() - ref).abs() <= 2.0 ** -24 * ref.abs() + err + 2.0 ** -149).all()
