@@ -650,11 +650,12 @@ def msk_dequantize_fp4(w, dtype=torch.bfloat16, out=None, stream=None):
     return out
 
 
-def msk_experts_fp4(x, experts, offsets, up=None, slots=None, top_k=1, out_dtype=torch.bfloat16, out=None, stream=None):
+def msk_experts_fp4(x, experts, offsets, up=None, slots=None, top_k=None, out_dtype=torch.bfloat16, out=None, stream=None):
     """Products of the 4-bit rows x (an Fp4Weight) with their experts'
     matrices (Fp4Experts): places offsets[e] .. offsets[e + 1] - 1 are expert
     e's, and place p takes row p of x, or with `slots` (int32 [n], as from
-    msk_moe_sort) row slots[p] // top_k.  With `up` (a second Fp4Experts of
+    msk_moe_sort) row slots[p] // top_k (1 unless given; more slots than x has
+    rows need it said).  With `up` (a second Fp4Experts of
     the same size) the result is silu(x w^T) * (x up^T).  Returns
     [n][experts.rows] of out_dtype, or `out` (any row stride); rows of places
     behind the last expert's are not written."""
@@ -663,9 +664,12 @@ def msk_experts_fp4(x, experts, offsets, up=None, slots=None, top_k=1, out_dtype
     _need(x.cols == experts.cols and x.cols % 64 == 0, "x has the weights' columns, a multiple of 64")
     _need(up is None or (up.n_experts, up.rows, up.cols) == (experts.n_experts, experts.rows, experts.cols),
           "up: of the other weights' size")
-    _need(slots is None or (slots.dtype == torch.int32 and slots.dim() == 1 and slots.is_contiguous() and top_k >= 1),
-          "slots: contiguous int32 [n], with top_k")
-    top_k = _int32(top_k, "top_k")
+    _need(slots is None or (slots.dtype == torch.int32 and slots.dim() == 1 and slots.is_contiguous()),
+          "slots: contiguous int32 [n]")
+    # (rows behind x's last are taken as that one: a top_k that was forgotten would not be seen)
+    _need(slots is None or top_k is not None or slots.shape[0] <= x.rows, "slots: more than x has rows, say top_k")
+    top_k = 1 if top_k is None else _int32(top_k, "top_k")
+    _need(slots is None or top_k >= 1, "top_k: 1 or more")
     n = x.rows if slots is None else slots.shape[0]
     if out is None:
         _need(out_dtype in _DTYPES, "out_dtype: a floating type")

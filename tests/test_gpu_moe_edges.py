@@ -103,3 +103,22 @@ def test_products_of_subnormal_tensor_scales(M, x_ts, w_ts):
     ref, err = products_ref(values64(c, xs, x_ts), wv, None, counts, torch.arange(45))
     assert ref.abs().max() > 2.0 ** -126
     assert ((y.cpu().double() - ref).abs() <= 2.0 ** -24 * ref.abs() + err + 2.0 ** -149).all()
+
+
+# ----------------------------------------------------------------------------
+# slots and top_k
+# ----------------------------------------------------------------------------
+
+
+def test_slots_without_top_k(M):
+    """One expert a token: slots are tokens, with and without saying so; more slots than rows need it said."""
+    w, _ = make_experts(M, 61, 2, 40, 128)
+    c, s = random_fp4(62, 6, 128)
+    x, off = M.Fp4Weight(c.cuda(), s.cuda()), torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([3, 5, 0, 1, 2, 4], dtype=torch.int32, device="cuda")
+    assert torch.equal(M.msk_experts_fp4(x, w, off, slots=slots), M.msk_experts_fp4(x, w, off, slots=slots, top_k=1))
+    many = torch.tensor([4, 4, 0, 1, 4, 2, 5, 5], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="top_k"):
+        M.msk_experts_fp4(x, w, off, slots=many)
+    y = M.msk_experts_fp4(x, w, off, slots=many, top_k=1)
+    assert torch.equal(y[:6], M.msk_experts_fp4(x, w, off, slots=many[:6].contiguous()))
