@@ -6,8 +6,9 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_moe import (M, gen, make_experts, no_wait_ran_out, products_ref, random_fp4, run_products,  # noqa: F401
-                                sort_ref_many, values64)
+from oracle import formats as F
+from tests.test_gpu_moe import (DT, M, gen, half_step, make_experts, no_wait_ran_out, products_ref, randn,  # noqa: F401
+                                random_fp4, run_products, sort_ref_many, strided, tiny, values64)
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +123,81 @@ def test_slots_without_top_k(M):
         M.msk_experts_fp4(x, w, off, slots=many)
     y = M.msk_experts_fp4(x, w, off, slots=many, top_k=1)
     assert torch.equal(y[:6], M.msk_experts_fp4(x, w, off, slots=many[:6].contiguous()))
+
+
+# ----------------------------------------------------------------------------
+# kernels for many elements
+# ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("ydt", list(DT))
+@pytest.mark.parametrize("odt", list(DT))
+@pytest.mark.parametrize("tokens,k,cols,extra,offset", [
+    (2048, 3, 2048, 0, 0), (2047, 3, 2048, 0, 0),      # 2^22 outputs, and fewer: pieces of 32 bytes and of 16
+    (2050, 9, 2064, 16, 0), (2050, 9, 2064, 32, 16),   # padded rows, more ranks than are loaded at once
+    (2100, 2, 2048, 0, 8), (2100, 2, 2040, 4, 0),      # aligned to 16 bytes and not to 32: a y of 16-bit elements, rows of fp32
+    (20000, 5, 240, 0, 4)])                            # a y of 16-bit elements aligned to 8
+def test_combine_of_many_outputs(M, ydt, odt, tokens, k, cols, extra, offset):
+    g, n = torch.Generator("cuda").manual_seed(tokens + cols), tokens * k
+    wide = torch.full((n * (cols + extra) + offset + 64,), 7.0, dtype=DT[ydt], device="cuda")
+    y = wide[offset:offset + n * (cols + extra)].view(n, cols + extra)[:, :cols]
+    y.copy_(torch.randn(n, cols, generator=g, device="cuda"))
+    places = torch.randperm(n, generator=g, device="cuda").int().view(tokens, k)
+    drop = torch.rand(tokens, k, generator=g, device="cuda") < 0.1
+    y[places[drop].long()] = float("nan")              # (not read)
+    places[drop] = torch.tensor([-1, n, 2 ** 31 - 1, -2 ** 31], device="cuda")[torch.arange(int(drop.sum()), device="cuda") % 4].int()
+    places[5] = -1
+    gates = torch.rand(tokens, k, generator=g, device="cuda")
+    out = torch.full((tokens, cols + extra), 5.0, dtype=DT[odt], device="cuda")
+    M.msk_moe_combine(y, places, gates, out=out[:, :cols])
+    ref, mag = torch.zeros(tokens, cols, dtype=torch.float64, device="cuda"), torch.zeros(tokens, cols, dtype=torch.float64, device="cuda")
+    for r in range(k):
+        p = places[:, r].long()
+        ok = ((p >= 0) & (p < n)).unsqueeze(1)
+        term = torch.where(ok, y[p.clamp(0, n - 1)].double(), 0.0) * gates[:, r:r + 1].double()
+        ref += term
+        mag += term.abs()
+    bound = half_step(DT[odt]) * (ref.abs() + 2.0 ** -20 * mag) + k * 2.0 ** -23 * mag + tiny(DT[odt])
+    assert ((out[:, :cols].double() - ref).abs() <= bound).all()
+    assert (out[:, cols:] == 5.0).all() and (out[5, :cols] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,ts", [("bf16", 1.0), ("fp16", 0.37), ("fp32", 1.0)])
+def test_quantize_of_many_elements(M, dtype, ts):
+    """More blocks of 16 than run at once (8 x 256 an SM), the last pass part of one, bit for bit: contiguous rows, rows
+    apart by a multiple of 32 bytes, and by one of 16 only."""
+    rows, cols = 2701, 4112
+    x = randn(71, rows, cols)
+    x[:, ::97] *= 12.0
+    x[100:103] *= 1e-4
+    x = x.to(DT[dtype])
+    c, s, _ = F.q4((x.float() / torch.tensor(ts, dtype=torch.float32)).double().numpy())
+    c, s = torch.from_numpy(c), torch.from_numpy(s)
+    packed = c[..., 0::2] | (c[..., 1::2] << 4)
+    values, packed, s = values64(packed, s).float(), packed.cuda(), s.cuda()
+    assert rows * cols // 16 > 2 * 8 * 256 * torch.cuda.get_device_properties(0).multi_processor_count
+    for extra in (0, 16, 8):
+        w = M.msk_quantize_fp4(strided(x, extra), ts)
+        assert torch.equal(w.packed, packed) and torch.equal(w.scales, s)
+        back = torch.full((rows, cols + extra), 3.0, dtype=DT[dtype], device="cuda")
+        M.msk_dequantize_fp4(w, out=back[:, :cols])
+        # two fp32 products, the second one rounding, then the type's
+        assert torch.equal(back[:, :cols], (values * torch.tensor(ts, dtype=torch.float32)).to(DT[dtype]).cuda())
+        assert (back[:, cols:] == 3.0).all()
+
+
+@pytest.mark.parametrize("n,E", [(1 << 20, 256), (16_777_217, 1024), (50_000_003, 61)])
+def test_sort_of_many_slots(M, n, E):
+    """Runs of a warp far longer than what its threads hold; most slots are other clusters'."""
+    g = torch.Generator("cuda").manual_seed(n)
+    e = torch.randint(-1, E + 1, (n,), generator=g, dtype=torch.int32, device="cuda")
+    e[n // 3:n // 2] = 1                               # (a favourite)
+    offsets, slots, places = M.msk_moe_sort(e, E)
+    key = torch.where((e >= 0) & (e < E), e, E)
+    order = torch.sort(key, stable=True)
+    kept = int((key < E).sum())
+    assert torch.equal(offsets.long(), torch.searchsorted(order.values, torch.arange(E + 1, dtype=torch.int32, device="cuda")))
+    assert torch.equal(slots[:kept].long(), order.indices[:kept]) and (slots[kept:] == -1).all()
+    want = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    want[order.indices[:kept]] = torch.arange(kept, dtype=torch.int32, device="cuda")
+    assert torch.equal(places, want)
