@@ -463,7 +463,11 @@ msk_status msk_token_logprobs(const void* logits, int32_t dtype, int64_t rows, i
  * A token's slots are its experts by rank: slot = token * top_k + rank.  The
  * slots in sorted order are at places 0, 1, ...  The conventions are those of
  * the operators above: calls enqueue on `stream` and return, may be captured,
- * and keep nothing between calls; none takes a workspace. */
+ * and keep nothing between calls; none takes a workspace.
+ * Experts' weights are the caller's, row-major as msk_load_layer is given them.  The
+ * model's own copy is laid out for the step and serves the step alone: a program that
+ * verifies and sends prompts through the same experts keeps both, 9/16 of a byte for
+ * each weight once more (256 experts of 3 x 1024 x 2048: 0.9 GB a layer). */
 
 /* The step's router on any number of tokens: x = fp32(logits) + bias, the
  * top_k greatest, of equal ones the lowest index first, and their softmax.
@@ -516,7 +520,7 @@ typedef struct {
 } msk_fp4_experts;
 
 /* The copy engine's descriptors of the weights, which msk_experts_fp4 makes anew at
- * every call that is not given them (1.2 us each, two a matrix): into
+ * every call that is not given them (0.13 us each, two a matrix): into
  * MSK_FP4_MAPS_BYTES of HOST memory, 128-byte aligned, that the caller keeps with
  * the weights.  w->maps is not read.  They hold for these addresses and sizes: a
  * call with others in the struct beside them is MSK_ERR_INVALID_ARG. */
@@ -541,8 +545,10 @@ msk_status msk_fp4_experts_maps(const msk_fp4_experts* w, void* maps);
  *            they were.
  * One expert (offsets {0, n}) is a plain product.  cols a multiple of 64, 64 to
  * 131072; n_experts up to 1024, rows up to 2^24, n_experts * rows below 2^31 - 256;
- * n up to 2^30.  A NaN block scale makes its row's outputs NaN.  n == 0 or
- * rows == 0 does nothing.  Waits on the device are bounded: see msk_ops_check. */
+ * n up to 2^30.  A NaN block scale makes its row's outputs NaN.  silu is off by some
+ * 2^-21 of its value, and 0 for a gate below -87.3 (where it is under 2^-119 in
+ * magnitude).  Any tensor scales: results in fp32's range are not lost to products of
+ * scales out of it.  n == 0 or rows == 0 does nothing.  Waits on the device are bounded: see msk_ops_check. */
 msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* slots, int32_t top_k, int64_t n,
                            const int32_t* offsets, const msk_fp4_experts* w, const msk_fp4_experts* up, void* y,
                            int32_t y_dtype, int64_t y_stride, void* stream);

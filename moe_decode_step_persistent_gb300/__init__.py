@@ -583,7 +583,7 @@ def msk_token_logprobs(logits, tokens=None, top=0, temperature=1.0, stream=None)
 def msk_moe_route(logits, top_k, bias=None, stream=None):
     """Each token's top_k experts and their gates: (experts int32, gates
     fp32), both [tokens][top_k], from logits [tokens][n_experts] of any
-    floating type and row stride, with an fp32 bias [n_experts] added.  A
+    floating type and row stride (rows that do not overlap), with an fp32 bias [n_experts] added.  A
     barred expert has a logit of -inf; ranks that find none are -1, gate 0."""
     _need(logits.dim() == 2 and logits.dtype in _DTYPES and (logits.stride(1) == 1 or logits.shape[1] <= 1),
           "logits: [tokens][n_experts], contiguous rows")
@@ -705,7 +705,8 @@ def msk_debug_experts_fault(tile=-1, wait_ns=0):
 
 def msk_moe_combine(y, places, gates=None, out_dtype=None, out=None, stream=None):
     """out[t] = sum over ranks of gates[t][r] * y[places[t][r]] (gates None:
-    1), y [rows][cols] of any floating type and row stride, places int32 and
+    1), y [rows][cols] of any floating type and row stride (rows that do not
+    overlap), places int32 and
     gates fp32 [tokens][top_k]; a place outside y's rows is a dropped slot.
     Returns [tokens][cols] of out_dtype (y's unless given), or `out`."""
     _need(y.dim() == 2 and y.dtype in _DTYPES and (y.stride(1) == 1 or y.shape[1] <= 1), "y: [rows][cols], contiguous rows")

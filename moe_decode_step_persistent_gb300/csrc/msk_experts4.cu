@@ -300,8 +300,8 @@ __device__ __forceinline__ void cp_async16_some(uint32_t dst, const void* src, i
 }
 
 // silu(g) = g / (1 + e^-g) of two numbers, off by some 2^-21: 2^t for t = -g
-// log2(e), times a factor for what t's rounding and the constant's leave; results
-// below 2^-119 are 0.
+// log2(e), times a factor for what t's rounding and the constant's leave; 0 for
+// g below -87.3 (the reciprocal leaves fp32's normal numbers).
 __device__ __forceinline__ unsigned long long silu2(unsigned long long g) {
   const unsigned long long one = pair(1.f, 1.f), l = pair(-1.4426950409f, -1.4426950409f);
   float g0, g1, t0, t1, r0, r1;
@@ -332,8 +332,10 @@ __device__ __forceinline__ unsigned long long silu2(unsigned long long g) {
 // that neighbouring pairs share weights in L2; a pair takes every one that is a
 // multiple of the pairs on.
 //
-// 65536 rows of 256 experts, gate and up of 1024 x 2048: 150 us, 3.7 PFLOP/s, 5.0 TB/s;
-// 8192 x 8192 x 8192: 180 us, 6.1 PFLOP/s.  What bounds full tiles is what a stage takes
+// 65536 rows of 256 experts, gate and up of 1024 x 2048: 150 us, 3.7 PFLOP/s, 5.0 TB/s
+// (168 to 170 in a row of seconds, where the power limit holds the clock at 1.55 GHz);
+// 8192 x 8192 x 8192: 180 us, 6.1 PFLOP/s; 1 to 128 tokens with 4096 x 4096: 7.6 to 8.9 us,
+// 16 pairs of 76 and a chain of latencies.  What bounds full tiles is what a stage takes
 // of shared memory's 128 bytes a clock (copies in, the MMAs' reads, scales in, read,
 // put in order and read again: 94 KB, with gate and up 110 to 130), and, with weights
 // from DRAM, its latency behind four or five stages.
@@ -1102,7 +1104,7 @@ extern "C" msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* sl
   s = weight_maps(w, &a.w_map, &a.ws_map);
   if (s == MSK_OK && up != nullptr) s = weight_maps(up, &a.up_map, &a.us_map);
   if (s != MSK_OK) return s;
-  // (a map takes the host 0.3 us: only those that some tile may take)
+  // (a map takes the host 0.13 us: only those that some tile may take)
   const auto codes_by = [&](CUtensorMap* m, int box, bool taken) { return !taken || codes_map(m, x->packed, x->rows, a.K, box); };
   const auto scales_by = [&](CUtensorMap* m, int box, bool taken) { return !taken || scales_map(m, x->scales, x->rows, a.K, box, 1); };
   if (slots == nullptr && (!codes_by(&a.x_map, 64, a.nt >= 128) || !codes_by(&a.x16_map, 16, n > 8) || !codes_by(&a.x8_map, 8, true) ||

@@ -194,8 +194,9 @@ __device__ __forceinline__ uint32_t same_expert(int e, int bits) {
 // counts the slots of the others too, where the order in which counts are added
 // does not matter.  One launch, no workspace; the places do not depend on an order
 // of arrival.
-// 131072 slots of 256 experts: 9.4 us, bound by the SMs' issue of ballots and of single
-// stores; few slots: a chain of latencies, 3.5.
+// 131072 slots of 256 experts: 9.5 us (issue of the 64 SMs at work 44 %, then barriers, single
+// stores and the counting of others' slots), 2^20 slots 32.7, 2^24 438; few slots: a chain of
+// latencies, 3.1.
 constexpr int kHeld = 8;
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const Sort a) {
   extern __shared__ __align__(16) int32_t sort_smem[];
@@ -390,7 +391,8 @@ __device__ __forceinline__ void store_sums(void* out, long long at, const float 
 
 // A thread has B bytes of a token's columns (V elements; B = 0: one element, where
 // rows are not aligned), its ranks' rows all loaded before they are summed, eight at
-// a time.  Sums in fp32, by rank.
+// a time.  Sums in fp32, by rank.  8192 tokens x 8 x 2048 columns of 16 bits: 50 us, bound by
+// DRAM; of 2047, one element a thread, 176 (loads of two bytes and a position for each).
 template <int DT, int ODT, int B>
 __global__ void __launch_bounds__(256) combine_kernel(const Combine a) {
   constexpr int S = DT == MSK_FP32 ? 4 : 2, V = B ? B / S : 1, U = 8, W = B ? B / 4 : 1;
@@ -508,8 +510,9 @@ extern "C" msk_status msk_moe_sort(const int32_t* experts, int64_t n, int32_t n_
   Sort a{};
   a.experts = experts, a.offsets = offsets, a.slots = slots, a.places = places, a.n = n, a.E = n_experts;
   // (a block goes through 4096 slots, 4 steps a warp, in the time that a cluster's barriers take;
-  // with four clusters of 16 65536 slots take 8.0 us and 131072 9.4, with one 9.0 and 13.3, with
-  // two 8.7 and 11.4, with eight, which do not all run at once, 8.0 and 16.5)
+  // with four clusters of 16 65536 slots take 8.0 us, 131072 9.6, 2^20 32.7, 2^24 438, with one 9.1,
+  // 13.2, 77 and 1119, with two 8.7, 11.4, 50 and 703, with eight, which do not all run at once,
+  // 8.0, 16.5, 44 and 618)
   a.blocks = n <= 4096 ? 1 : n <= 8 * 4096 ? 8 : kSortCluster;
   const int clusters = a.blocks < kSortCluster ? 1 : (int)std::min<int64_t>(kSortClusters, (n + 16383) / 16384);
   const long long warps = (long long)a.blocks * clusters * kSortWarps;
