@@ -546,9 +546,10 @@ msk_status msk_fp4_experts_maps(const msk_fp4_experts* w, void* maps);
  * One expert (offsets {0, n}) is a plain product.  cols a multiple of 64, 64 to
  * 131072; n_experts up to 1024, rows up to 2^24, n_experts * rows below 2^31 - 256;
  * n up to 2^30.  A NaN block scale makes its row's outputs NaN.  silu is off by some
- * 2^-21 of its value, and 0 for a gate below -87.3 (where it is under 2^-119 in
+ * 2^-21 of its value, and 0 for a gate below some -87.3 (where it is under 2^-119 in
  * magnitude).  Any tensor scales: results in fp32's range are not lost to products of
- * scales out of it.  n == 0 or rows == 0 does nothing.  Waits on the device are bounded: see msk_ops_check. */
+ * scales out of it.  n == 0 or rows == 0 does nothing.  Waits on the device are
+ * bounded: see msk_ops_check. */
 msk_status msk_experts_fp4(const msk_nvfp4_desc* x, const int32_t* slots, int32_t top_k, int64_t n,
                            const int32_t* offsets, const msk_fp4_experts* w, const msk_fp4_experts* up, void* y,
                            int32_t y_dtype, int64_t y_stride, void* stream);

@@ -583,8 +583,8 @@ def msk_token_logprobs(logits, tokens=None, top=0, temperature=1.0, stream=None)
 def msk_moe_route(logits, top_k, bias=None, stream=None):
     """Each token's top_k experts and their gates: (experts int32, gates
     fp32), both [tokens][top_k], from logits [tokens][n_experts] of any
-    floating type and row stride (rows that do not overlap), with an fp32 bias [n_experts] added.  A
-    barred expert has a logit of -inf; ranks that find none are -1, gate 0."""
+    floating type and row stride (rows that do not overlap), with an fp32
+    bias [n_experts] added.  A barred expert has a logit of -inf; ranks that find none are -1, gate 0."""
     _need(logits.dim() == 2 and logits.dtype in _DTYPES and (logits.stride(1) == 1 or logits.shape[1] <= 1),
           "logits: [tokens][n_experts], contiguous rows")
     T, E = logits.shape

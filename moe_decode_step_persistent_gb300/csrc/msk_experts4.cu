@@ -301,7 +301,7 @@ __device__ __forceinline__ void cp_async16_some(uint32_t dst, const void* src, i
 
 // silu(g) = g / (1 + e^-g) of two numbers, off by some 2^-21: 2^t for t = -g
 // log2(e), times a factor for what t's rounding and the constant's leave; 0 for
-// g below -87.3 (the reciprocal leaves fp32's normal numbers).
+// g below some -87.3 (the reciprocal leaves fp32's normal numbers).
 __device__ __forceinline__ unsigned long long silu2(unsigned long long g) {
   const unsigned long long one = pair(1.f, 1.f), l = pair(-1.4426950409f, -1.4426950409f);
   float g0, g1, t0, t1, r0, r1;
